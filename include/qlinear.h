@@ -57,7 +57,13 @@ typedef enum {
 
 /* operation ids for ql_workspace_bytes */
 enum { QL_OP_INT8_W8A8 = 1, QL_OP_FP8_BLOCK = 2, QL_OP_MXFP4 = 3, QL_OP_MOE_MXFP4 = 4, QL_OP_BF16 = 5,
-       QL_OP_FP8_CHANNEL = 6 };
+       QL_OP_FP8_CHANNEL = 6, QL_OP_GATED_FFN = 7, QL_OP_GATED_FFN_BWD = 8 };
+
+/* scale formats of the 4-bit group-scaled weights */
+enum { QL_SCALE_BF16 = 0, QL_SCALE_FP16 = 1 };
+
+/* what gated_ffn keeps of g and u for gated_ffn_backward */
+enum { QL_SAVE_NONE = 0, QL_SAVE_BF16 = 1, QL_SAVE_INT8 = 2 };
 
 /* FP8 weight code formats of qlinear_fp8 */
 enum { QL_FP8_E4M3 = 0 /* e4m3fn: bias 7, no infinities, S.1111.111 is NaN */,
@@ -84,7 +90,12 @@ enum {
   QL_PATH_BF16_SKINNY = 7,     /* BF16 skinny GEMM (unquantised weights)                    */
   QL_PATH_FP8_CHANNEL_SKINNY = 8, /* FP8 skinny GEMM, per-channel / per-tensor fp32 scale    */
   QL_PATH_INT8_TCGEN05 = 9,      /* per-token INT8 quant + tcgen05 GEMM on exact f16 images  */
-  QL_PATH_MOE_MXFP4_TCGEN05 = 10 /* M > 16: routing + grouped tcgen05 GEMMs, 1x128 E4M3 act  */
+  QL_PATH_MOE_MXFP4_TCGEN05 = 10, /* M > 16: routing + grouped tcgen05 GEMMs, 1x128 E4M3 act  */
+  QL_PATH_INT4_SKINNY = 11,      /* 4-bit group-scaled skinny GEMM, bf16 activations         */
+  QL_PATH_GATED_FFN_INT4 = 12,   /* gated block on 4-bit weights, one skinny launch           */
+  QL_PATH_GATED_FFN_SKINNY = 13, /* gated block on bf16 weights, one skinny launch            */
+  QL_PATH_GATED_FFN_TCGEN05 = 14, /* gated block, one tcgen05 GEMM with the activation in its epilogue */
+  QL_PATH_GATED_FFN_BACKWARD = 15 /* gradients of g and u, then the dx and dW13 tcgen05 GEMMs */
 };
 
 /* device status flags (bitmask) */
@@ -99,7 +110,7 @@ QL_API int ql_version(void);
  * (split-K tickets, or the output cells of INT8 calls of up to 4 tokens), so one workspace can
  * serve calls of any op and shape in turn.  M, N, K as in the op; for
  * QL_OP_MOE_MXFP4: M tokens, N = H (hidden), K = I (expert intermediate), E experts and
- * topk routed experts per token.  Returns 0 for an unknown op or negative sizes.
+ * topk routed experts per token.  QL_OP_GATED_FFN, QL_OP_GATED_FFN_BWD: N = I, K = H.  Returns 0 for an unknown op or negative sizes.
  */
 QL_API size_t ql_workspace_bytes(int op, int64_t M, int64_t N, int64_t K, int E, int topk);
 
@@ -348,6 +359,82 @@ QL_API ql_status qlinear_int8_w8a8_noalloc(const uint16_t* x, int64_t M, int64_t
                                            const uint16_t* bias, uint16_t* y, int64_t ldy,
                                            int32_t* acc_out, int8_t* xq_out, float* xs_out,
                                            ql_stream_t stream, int* path_out);
+
+/*
+ * Linear layer on 4-bit integer weights with one scale (and zero point) per group of K
+ * elements of a row:
+ *   w[n,k] = (q[n,k] - z[n,k/group]) * s[n,k/group]
+ *   y[m,n] = bf16( sum_k x[m,k] * w[n,k] )  then, if bias, y = bf16(y + bias[n])
+ * q: codes 0..15 packed two per byte, element 2i in the LOW nibble of byte i, rows of
+ * ldw_bytes; s: bf16 (QL_SCALE_BF16) or fp16 (QL_SCALE_FP16) bits [N, lds], lds >=
+ * ceil(K/group); z: uint8 [N, ldz] holding 0..127, or NULL for 8 everywhere (symmetric codes);
+ * x: bf16 [M, ldx]; bias: nullable bf16 [N]; y: bf16 [M, ldy].  q - z is exact in bf16, its
+ * products with x are exact in fp32 and every group's fp32 sum is multiplied by its scale once:
+ * no weight is rounded.  Weights are streamed once per 32 tokens.
+ * Requires: 1 <= M <= 65535, K % 32 == 0 (the last group may be short), group a power of two
+ * >= 32 (a group >= K is one scale per row), ldx >= K, ldx % 8 == 0, ldw_bytes >= K/2,
+ * ldw_bytes % 16 == 0, 16-byte aligned x and w, 2-byte aligned scales, ldy >= N.
+ * Takes no workspace and waits on nothing inside the kernel.
+ */
+QL_API ql_status qlinear_int4(const uint16_t* x, int64_t M, int64_t K, int64_t ldx, const uint8_t* w, int64_t N,
+                              int64_t ldw_bytes, const uint16_t* w_scale, int scale_fmt, int64_t lds,
+                              const uint8_t* w_zero, int64_t ldz, int64_t group, const uint16_t* bias, uint16_t* y,
+                              int64_t ldy, ql_stream_t stream, int* path_out);
+
+/*
+ * Gated feed-forward block: both projections, the activation and the product in one launch.
+ *   g[m,i] = sum_k x[m,k] W13[i,k],  u[m,i] = sum_k x[m,k] W13[I+i,k]      (fp32)
+ *   h[m,i] = bf16( silu(alpha * min(g, limit)) * clamp(u, -limit, limit) )
+ * (moe_mxfp4_grouped's expert activation; limit = +infinity with alpha = 1 is silu(g) * u.)
+ * x: bf16 [M, ldx] (H used); w13: bf16 [2I, ldw], rows [0, I) gate and [I, 2I) up; h: bf16
+ * [M, ldh].
+ * save != QL_SAVE_NONE keeps g and u for gated_ffn_backward in ckpt, two halves per token, each
+ * of P = I rounded up to 128 columns: QL_SAVE_BF16: bf16 [M, 2, P]; QL_SAVE_INT8: int8
+ * [M, 2, P] and ckpt_scale fp32 [M, 2, P/128], per token and 128 columns
+ *   scale = max|v| / 127,  code = round_half_even(v / scale)  (scale 0 where max|v| < 2^-100;
+ * an infinity or a NaN in a group reads back as NaN throughout it).  Columns I..P are not
+ * written.  h does not depend on save.
+ * Paths: M <= 32 without a checkpoint: a skinny launch that streams the weights once; else one
+ *        tcgen05 GEMM whose epilogue applies the activation and writes h and the checkpoint.
+ * Requires: 1 <= M <= 2^22, H and I multiples of 8, at most 2^20, ldx >= H, ldw >= H, ldh >= I,
+ * leading dimensions multiples of 8, 16-byte aligned x, w13, h and ckpt; alpha finite, limit >=
+ * 0.  workspace: ql_workspace_bytes(QL_OP_GATED_FFN, M, I, H, 0, 0) bytes, zeroed once.
+ */
+QL_API ql_status gated_ffn(const uint16_t* x, int64_t M, int64_t H, int64_t ldx, const uint16_t* w13, int64_t I,
+                           int64_t ldw, float swiglu_alpha, float swiglu_limit, uint16_t* h, int64_t ldh, int save,
+                           void* ckpt, float* ckpt_scale, void* workspace, size_t workspace_bytes,
+                           ql_stream_t stream, int* path_out);
+
+/*
+ * The block's backward pass from the checkpoint of its forward (save QL_SAVE_BF16 or
+ * QL_SAVE_INT8; G and U are the values that the checkpoint stands for), with g' = min(G, limit)
+ * and u' = clamp(U, -limit, limit):
+ *   du = dh * silu(alpha g') where |U| <= limit, else 0
+ *   dg = dh * u' * alpha * silu'(alpha g') where G <= limit, else 0
+ *   dx = bf16( dg W13[0:I] + du W13[I:2I] ),  dw13 = bf16( [dg du]^T x )
+ * dg and du are rounded to bf16 (the tensor cores' operands), the sums are fp32.  dh: bf16
+ * [M, ld_dh]; x, w13 as in the forward; dx: bf16 [M, ld_dx] or NULL; dw13: bf16 [2I, ld_dw] or
+ * NULL (one of the two is required; x is not read without dw13, w13 not without dx).
+ * Deterministic: every output is summed in one order.
+ * Requires what gated_ffn requires, ld_dh >= I, ld_dx >= H, ld_dw >= H (multiples of 8) and
+ * 16-byte aligned dh, dx, dw13.  workspace: ql_workspace_bytes(QL_OP_GATED_FFN_BWD, M, I, H, 0, 0)
+ * bytes (it holds [dg du]), zeroed once.
+ */
+QL_API ql_status gated_ffn_backward(const uint16_t* dh, int64_t ld_dh, const uint16_t* x, int64_t M, int64_t H,
+                                    int64_t ldx, const uint16_t* w13, int64_t I, int64_t ldw, float swiglu_alpha,
+                                    float swiglu_limit, int save, const void* ckpt, const float* ckpt_scale,
+                                    uint16_t* dx, int64_t ld_dx, uint16_t* dw13, int64_t ld_dw, void* workspace,
+                                    size_t workspace_bytes, ql_stream_t stream, int* path_out);
+
+/*
+ * The gated block's form for few tokens on 4-bit weights: w13's 2I rows are stored, scaled and
+ * required as qlinear_int4's (K = H), h and the activation are as gated_ffn's.  g and u stay in
+ * fp32.  One launch per call, no workspace.
+ */
+QL_API ql_status gated_ffn_int4(const uint16_t* x, int64_t M, int64_t H, int64_t ldx, const uint8_t* w13, int64_t I,
+                                int64_t ldw_bytes, const uint16_t* w_scale, int scale_fmt, int64_t lds,
+                                const uint8_t* w_zero, int64_t ldz, int64_t group, float swiglu_alpha,
+                                float swiglu_limit, uint16_t* h, int64_t ldh, ql_stream_t stream, int* path_out);
 
 #ifdef __cplusplus
 }

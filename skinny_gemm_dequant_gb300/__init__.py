@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -24,6 +25,8 @@ __all__ = [
     "qlinear_fp8", "FP8_E4M3", "FP8_E5M2", "ACT_BF16", "ACT_E4M3_1X128", "PATHS",
     "token_amax", "qlinear_int8_w8a8_partial", "qlinear_int8_epilogue", "qlinear_fp8_block_partial",
     "qlinear_mxfp4_partial", "finish_f32",
+    "qlinear_int4", "gated_ffn_int4", "gated_ffn", "gated_ffn_backward", "FFNCheckpoint", "OP_GATED_FFN",
+    "OP_GATED_FFN_BWD",
 ]
 
 if not os.path.exists(_LIB_PATH):
@@ -79,12 +82,29 @@ lib.qlinear_mxfp4_partial.argtypes = [_vp, _i64, _i64, _i64, _vp, _i64, _i64, _v
 lib.ql_finish_f32.restype = _int
 lib.ql_finish_f32.argtypes = [_vp, _i64, _i64, _i64, _vp, _vp, _i64, _vp]
 
+lib.qlinear_int4.restype = _int
+lib.qlinear_int4.argtypes = [_vp, _i64, _i64, _i64, _vp, _i64, _i64, _vp, _int, _i64, _vp, _i64, _i64, _vp, _vp, _i64,
+                             _vp, _ip]
+lib.gated_ffn_int4.restype = _int
+lib.gated_ffn_int4.argtypes = [_vp, _i64, _i64, _i64, _vp, _i64, _i64, _vp, _int, _i64, _vp, _i64, _i64,
+                               ctypes.c_float, ctypes.c_float, _vp, _i64, _vp, _ip]
+lib.gated_ffn.restype = _int
+lib.gated_ffn.argtypes = [_vp, _i64, _i64, _i64, _vp, _i64, _i64, ctypes.c_float, ctypes.c_float, _vp, _i64, _int,
+                          _vp, _vp, _vp, _sz, _vp, _ip]
+lib.gated_ffn_backward.restype = _int
+lib.gated_ffn_backward.argtypes = [_vp, _i64, _vp, _i64, _i64, _i64, _vp, _i64, _i64, ctypes.c_float, ctypes.c_float,
+                                   _int, _vp, _vp, _vp, _i64, _vp, _i64, _vp, _sz, _vp, _ip]
+
 OP_INT8_W8A8, OP_FP8_BLOCK, OP_MXFP4, OP_MOE_MXFP4, OP_BF16, OP_FP8_CHANNEL = 1, 2, 3, 4, 5, 6
+OP_GATED_FFN, OP_GATED_FFN_BWD = 7, 8
 FP8_E4M3, FP8_E5M2 = 0, 1
+SCALE_BF16, SCALE_FP16 = 0, 1
+SAVE_NONE, SAVE_BF16, SAVE_INT8 = 0, 1, 2
 ACT_BF16, ACT_E4M3_1X128 = 0, 1
 PATHS = {0: "none", 1: "int8_skinny", 2: "fp8_skinny", 3: "fp8_tcgen05", 4: "mxfp4_skinny",
          5: "mxfp4_tcgen05", 6: "moe_mxfp4", 7: "bf16_skinny", 8: "fp8_channel_skinny",
-         9: "int8_tcgen05", 10: "moe_mxfp4_tcgen05"}
+         9: "int8_tcgen05", 10: "moe_mxfp4_tcgen05", 11: "int4_skinny", 12: "gated_ffn_int4",
+         13: "gated_ffn_skinny", 14: "gated_ffn_tcgen05", 15: "gated_ffn_backward"}
 
 
 class QLError(RuntimeError):
@@ -294,6 +314,160 @@ def moe_mxfp4_grouped(x, w13, s13, w2, s2, *, router_logits=None, topk_ids=None,
     if debug:
         return y, ids, wts, h, PATHS[path.value]
     return y
+
+
+# ------------------------------------------------------------------ 4-bit group-scaled weights
+def _int4_weights(x, w, w_scale, w_zero, group):
+    """Checks of packed codes [N, >=K/2], scales and zero points [N, >=ceil(K/group)] against x [M, K];
+    returns the scale format."""
+    K = x.shape[1]
+    if w.dtype != torch.uint8 or w.stride(1) != 1 or x.stride(1) != 1:
+        raise TypeError("w must be packed uint8 codes with unit inner stride; x must have unit inner stride")
+    if w_scale.dtype not in (torch.bfloat16, torch.float16) or w_scale.stride(1) != 1:
+        raise TypeError("w_scale must be bfloat16 or float16 with unit inner stride")
+    if group < 1:
+        raise ValueError("group must be positive")
+    groups = -(-K // group)
+    if w.shape[1] * 2 < K or w_scale.shape[0] != w.shape[0] or w_scale.shape[1] < groups:
+        raise ValueError("w must be [N, >=K/2] and w_scale [N, >=ceil(K/group)]")
+    if w_zero is not None:
+        if w_zero.dtype != torch.uint8 or w_zero.stride(1) != 1:
+            raise TypeError("w_zero must be uint8 with unit inner stride")
+        if w_zero.shape[0] != w.shape[0] or w_zero.shape[1] < groups:
+            raise ValueError("w_zero must be [N, >=ceil(K/group)]")
+    return SCALE_BF16 if w_scale.dtype == torch.bfloat16 else SCALE_FP16
+
+
+def _out(out, M, N, x, name="out"):
+    if out is None:
+        return torch.empty(M, N, dtype=torch.bfloat16, device=x.device)
+    if out.dtype != torch.bfloat16 or out.shape != (M, N) or out.stride(1) != 1:
+        raise TypeError(f"{name} must be bfloat16 [{M}, {N}] with unit inner stride")
+    return out
+
+
+def qlinear_int4(x, w, w_scale, w_zero=None, bias=None, *, group=128, debug=False, out=None, stream=None):
+    """y = x W^T (+ bias after the bf16 cast) on 4-bit weights w[n,k] = (q - zero) * scale per group
+    of K.  x: bf16 [M, K]; w: uint8 [N, >=K/2], element 2i in the low nibble of byte i; w_scale: bf16
+    or fp16 [N, >=ceil(K/group)]; w_zero: uint8 [N, >=ceil(K/group)] (values 0..127) or None: 8.
+    group: a power of two >= 32.  With debug=True returns (y, path)."""
+    _bf16(x, "x")
+    M, K = x.shape
+    N = w.shape[0]
+    fmt = _int4_weights(x, w, w_scale, w_zero, group)
+    if bias is not None and (bias.dtype != torch.bfloat16 or bias.shape != (N,) or not bias.is_contiguous()):
+        raise TypeError(f"bias must be bfloat16 [{N}]")
+    y = _out(out, M, N, x)
+    path = ctypes.c_int(0)
+    _check(lib.qlinear_int4(_ptr(x), M, K, x.stride(0), _ptr(w), N, w.stride(0), _ptr(w_scale), fmt,
+                            w_scale.stride(0), _ptr(w_zero), 0 if w_zero is None else w_zero.stride(0), group,
+                            _ptr(bias), _ptr(y), y.stride(0), _stream(stream), ctypes.byref(path)), "qlinear_int4")
+    if debug:
+        return y, PATHS[path.value]
+    return y
+
+
+def gated_ffn_int4(x, w13, w_scale, w_zero=None, *, group=128, swiglu_alpha=1.0, swiglu_limit=None, debug=False,
+                   out=None, stream=None):
+    """h = silu(alpha * min(g, limit)) * clamp(u, +-limit) with g, u = x W13^T on 4-bit weights (rows
+    [0, I) gate, [I, 2I) up), stored as qlinear_int4's, in one launch.  x: bf16 [M, H]; w13: uint8
+    [2I, >=H/2].  Returns bf16 [M, I]; with debug=True (h, path)."""
+    _bf16(x, "x")
+    M, H = x.shape
+    if w13.shape[0] % 2:
+        raise ValueError("w13 must have an even number of rows (gate, then up)")
+    I = w13.shape[0] // 2
+    fmt = _int4_weights(x, w13, w_scale, w_zero, group)
+    h = _out(out, M, I, x)
+    path = ctypes.c_int(0)
+    _check(lib.gated_ffn_int4(_ptr(x), M, H, x.stride(0), _ptr(w13), I, w13.stride(0), _ptr(w_scale), fmt,
+                              w_scale.stride(0), _ptr(w_zero), 0 if w_zero is None else w_zero.stride(0), group,
+                              float(swiglu_alpha), float("inf") if swiglu_limit is None else float(swiglu_limit),
+                              _ptr(h), h.stride(0), _stream(stream), ctypes.byref(path)), "gated_ffn_int4")
+    if debug:
+        return h, PATHS[path.value]
+    return h
+
+
+# ------------------------------------------------------------------ gated feed-forward block
+class FFNCheckpoint(NamedTuple):
+    """What gated_ffn keeps of g and u for gated_ffn_backward.  mode "bf16": data bf16 [M, 2, P];
+    mode "int8": data int8 codes [M, 2, P] and scale fp32 [M, 2, P/128], value = code * scale; P = I
+    rounded up to 128 (columns past I are not written)."""
+    mode: str
+    data: torch.Tensor
+    scale: torch.Tensor | None
+
+
+_SAVE = {None: SAVE_NONE, "bf16": SAVE_BF16, "int8": SAVE_INT8}
+
+
+def _ffn_weights(x, w13):
+    if w13.dtype != torch.bfloat16 or w13.stride(1) != 1 or x.stride(1) != 1:
+        raise TypeError("w13 must be bfloat16 with unit inner stride; x must have unit inner stride")
+    if w13.shape[0] % 2 or w13.shape[1] != x.shape[1]:
+        raise ValueError("w13 must be [2I, H] (gate rows, then up rows) for x [M, H]")
+
+
+def gated_ffn(x, w13, *, swiglu_alpha=1.0, swiglu_limit=None, save=None, debug=False, out=None, workspace=None,
+              stream=None):
+    """h = silu(alpha * min(g, limit)) * clamp(u, +-limit) with g, u = x W13^T, in one launch.  x: bf16
+    [M, H]; w13: bf16 [2I, H], rows [0, I) gate and [I, 2I) up; H and I multiples of 8.  save: None,
+    "bf16" or "int8" also returns an FFNCheckpoint of g and u: (h, checkpoint).  debug=True appends
+    the path."""
+    _bf16(x, "x")
+    _ffn_weights(x, w13)
+    if save not in _SAVE:
+        raise ValueError('save must be None, "bf16" or "int8"')
+    M, H = x.shape
+    I = w13.shape[0] // 2
+    h = _out(out, M, I, x)
+    saved = None
+    if save is not None:
+        P = -(-I // 128) * 128
+        saved = FFNCheckpoint(save, torch.empty(M, 2, P, dtype=torch.bfloat16 if save == "bf16" else torch.int8,
+                                                device=x.device),
+                              torch.empty(M, 2, P // 128, dtype=torch.float32, device=x.device)
+                              if save == "int8" else None)
+    ws = _ws(x.device, workspace_bytes(OP_GATED_FFN, M, I, H), stream, workspace)
+    path = ctypes.c_int(0)
+    _check(lib.gated_ffn(_ptr(x), M, H, x.stride(0), _ptr(w13), I, w13.stride(0), float(swiglu_alpha),
+                         float("inf") if swiglu_limit is None else float(swiglu_limit), _ptr(h), h.stride(0),
+                         _SAVE[save], _ptr(saved.data) if saved else None, _ptr(saved.scale) if saved else None,
+                         _ptr(ws), ws.numel(), _stream(stream), ctypes.byref(path)), "gated_ffn")
+    res = (h,) if saved is None else (h, saved)
+    if debug:
+        res += (PATHS[path.value],)
+    return res[0] if len(res) == 1 else res
+
+
+def gated_ffn_backward(dh, x, w13, saved, *, swiglu_alpha=1.0, swiglu_limit=None, need_dx=True, need_dw=True,
+                       out_dx=None, out_dw=None, workspace=None, stream=None):
+    """Gradients of gated_ffn from its checkpoint: (dx bf16 [M, H], dw13 bf16 [2I, H]) for dh bf16
+    [M, I]; an output that is not needed is None and costs nothing.  swiglu_alpha and swiglu_limit
+    as in the forward."""
+    _bf16(dh, "dh")
+    _bf16(x, "x")
+    _ffn_weights(x, w13)
+    M, H = x.shape
+    I = w13.shape[0] // 2
+    if dh.shape != (M, I) or dh.stride(1) != 1:
+        raise TypeError(f"dh must be [{M}, {I}] with unit inner stride")
+    P = -(-I // 128) * 128
+    if saved.mode not in ("bf16", "int8") or saved.data.shape != (M, 2, P) or not saved.data.is_contiguous():
+        raise ValueError("saved must be the FFNCheckpoint of this x and w13")
+    if saved.mode == "int8" and (saved.scale is None or saved.scale.shape != (M, 2, P // 128)):
+        raise ValueError("saved must be the FFNCheckpoint of this x and w13")
+    dx = _out(out_dx, M, H, x, "out_dx") if need_dx else None
+    dw = _out(out_dw, 2 * I, H, x, "out_dw") if need_dw else None
+    ws = _ws(x.device, workspace_bytes(OP_GATED_FFN_BWD, M, I, H), stream, workspace)
+    path = ctypes.c_int(0)
+    _check(lib.gated_ffn_backward(_ptr(dh), dh.stride(0), _ptr(x), M, H, x.stride(0), _ptr(w13), I, w13.stride(0),
+                                  float(swiglu_alpha), float("inf") if swiglu_limit is None else float(swiglu_limit),
+                                  _SAVE[saved.mode], _ptr(saved.data), _ptr(saved.scale), _ptr(dx),
+                                  0 if dx is None else dx.stride(0), _ptr(dw), 0 if dw is None else dw.stride(0),
+                                  _ptr(ws), ws.numel(), _stream(stream), ctypes.byref(path)), "gated_ffn_backward")
+    return dx, dw
 
 
 _u32 = ctypes.c_uint32

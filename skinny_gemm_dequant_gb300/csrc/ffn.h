@@ -1,0 +1,67 @@
+// Host-side declarations of the 4-bit group-scaled linear and the gated feed-forward block.
+#pragma once
+#include <cstdint>
+#include <cuda_runtime.h>
+
+namespace ql {
+
+// ------------------------------------------------------------------ skinny calls (kernels_ffn_skinny.cu)
+struct FfnSkinnyArgs {
+  const uint16_t* x;  // bf16 [M, ldx]
+  int64_t ldx;
+  int M, K;
+  const uint8_t* w;  // packed 4-bit codes or bf16, [rows, ldw_bytes]
+  int64_t ldw_bytes;
+  int N;  // outputs: weight rows of a plain linear, columns I of a gated block (its rows are 2I)
+  const uint16_t* scale;  // bf16 or fp16 bits [rows, lds] (4-bit weights only)
+  int64_t lds;
+  int scale_fp16;
+  const uint8_t* zero;  // [rows, ldz] or null: 8
+  int64_t ldz;
+  int group_shift;        // log2 of the group size
+  const uint16_t* bias;   // bf16 [N] or null (plain linear only)
+  uint16_t* y;            // bf16 [M, ldy]
+  int64_t ldy;
+  float alpha, limit;     // activation of a gated block
+};
+constexpr int64_t kFfnSkinnyTokens = 32;  // tokens one pass over the weights takes
+cudaError_t launch_ffn_skinny(bool int4, bool gated, const FfnSkinnyArgs& a, cudaStream_t st);
+
+// ------------------------------------------------------------------ tcgen05 path (ffn_tc.cu)
+namespace tc {
+struct FfnForward {
+  const uint16_t* x;    // bf16 [M, ldx]
+  const uint16_t* w13;  // bf16 [2I, ldw]
+  int64_t M, H, I, ldx, ldw;
+  uint16_t* h;  // bf16 [M, ldh]
+  int64_t ldh;
+  float alpha, limit;
+  int save;           // QL_SAVE_*
+  void* ckpt;         // [M, 2, I padded to 128] bf16 or int8
+  float* ckpt_scale;  // [M, 2, I padded / 128] (int8)
+  uint32_t* status;
+  uint32_t wait_limit;
+};
+cudaError_t launch_ffn_forward(const FfnForward& f, cudaStream_t st);
+
+struct FfnBackward {
+  const uint16_t* dh;  // bf16 [M, ld_dh]
+  const uint16_t* x;
+  const uint16_t* w13;
+  int64_t M, H, I, ld_dh, ldx, ldw;
+  int save;
+  const void* ckpt;
+  const float* ckpt_scale;
+  float alpha, limit;
+  uint16_t* dgu;   // workspace: bf16 [M, 2I]
+  uint16_t* dx;    // bf16 [M, ld_dx] or null
+  int64_t ld_dx;
+  uint16_t* dw13;  // bf16 [2I, ld_dw] or null
+  int64_t ld_dw;
+  uint32_t* status;
+  uint32_t wait_limit;
+};
+cudaError_t launch_ffn_backward(const FfnBackward& b, cudaStream_t st);
+}  // namespace tc
+
+}  // namespace ql
