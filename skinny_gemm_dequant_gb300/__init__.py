@@ -11,6 +11,7 @@ there is no fallback implementation.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from typing import NamedTuple
 
@@ -99,6 +100,7 @@ OP_INT8_W8A8, OP_FP8_BLOCK, OP_MXFP4, OP_MOE_MXFP4, OP_BF16, OP_FP8_CHANNEL = 1,
 OP_GATED_FFN, OP_GATED_FFN_BWD = 7, 8
 FP8_E4M3, FP8_E5M2 = 0, 1
 SCALE_BF16, SCALE_FP16 = 0, 1
+_SCALE_FORMATS = {torch.bfloat16: SCALE_BF16, torch.float16: SCALE_FP16}
 SAVE_NONE, SAVE_BF16, SAVE_INT8 = 0, 1, 2
 ACT_BF16, ACT_E4M3_1X128 = 0, 1
 PATHS = {0: "none", 1: "int8_skinny", 2: "fp8_skinny", 3: "fp8_tcgen05", 4: "mxfp4_skinny",
@@ -119,12 +121,14 @@ def _check(status: int, where: str):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream=None):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    # the current stream's handle without building a Stream object (2.9 us a call on the Arm host)
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream
 
 
 def workspace_bytes(op: int, M: int, N: int, K: int, E: int = 0, topk: int = 0) -> int:
@@ -317,31 +321,41 @@ def moe_mxfp4_grouped(x, w13, s13, w2, s2, *, router_logits=None, topk_ids=None,
 
 
 # ------------------------------------------------------------------ 4-bit group-scaled weights
-def _int4_weights(x, w, w_scale, w_zero, group):
-    """Checks of packed codes [N, >=K/2], scales and zero points [N, >=ceil(K/group)] against x [M, K];
-    returns the scale format."""
-    K = x.shape[1]
-    if w.dtype != torch.uint8 or w.stride(1) != 1 or x.stride(1) != 1:
+# These calls take microseconds on the GPU, so their Python is kept short: shapes and strides are
+# read once, and the dispatch marker is asked for only with debug=True.
+def _inf(limit):
+    return math.inf if limit is None else float(limit)
+
+
+def _int4_weights(K, sx, w, w_scale, w_zero, group):
+    """Checks packed codes [N, >=K/2] and scales and zero points [N, >=ceil(K/group)] against x
+    [M, K] with strides sx; returns (N, row strides of w, w_scale and w_zero, scale format)."""
+    (N, cols), (ldw, inner) = w.shape, w.stride()
+    if w.dtype is not torch.uint8 or inner != 1 or sx[1] != 1:
         raise TypeError("w must be packed uint8 codes with unit inner stride; x must have unit inner stride")
-    if w_scale.dtype not in (torch.bfloat16, torch.float16) or w_scale.stride(1) != 1:
+    fmt = _SCALE_FORMATS.get(w_scale.dtype)
+    (rows, scols), (lds, inner) = w_scale.shape, w_scale.stride()
+    if fmt is None or inner != 1:
         raise TypeError("w_scale must be bfloat16 or float16 with unit inner stride")
     if group < 1:
         raise ValueError("group must be positive")
     groups = -(-K // group)
-    if w.shape[1] * 2 < K or w_scale.shape[0] != w.shape[0] or w_scale.shape[1] < groups:
+    if cols * 2 < K or rows != N or scols < groups:
         raise ValueError("w must be [N, >=K/2] and w_scale [N, >=ceil(K/group)]")
+    ldz = 0
     if w_zero is not None:
-        if w_zero.dtype != torch.uint8 or w_zero.stride(1) != 1:
+        (rows, zcols), (ldz, inner) = w_zero.shape, w_zero.stride()
+        if w_zero.dtype is not torch.uint8 or inner != 1:
             raise TypeError("w_zero must be uint8 with unit inner stride")
-        if w_zero.shape[0] != w.shape[0] or w_zero.shape[1] < groups:
+        if rows != N or zcols < groups:
             raise ValueError("w_zero must be [N, >=ceil(K/group)]")
-    return SCALE_BF16 if w_scale.dtype == torch.bfloat16 else SCALE_FP16
+    return N, ldw, lds, ldz, fmt
 
 
 def _out(out, M, N, x, name="out"):
     if out is None:
-        return torch.empty(M, N, dtype=torch.bfloat16, device=x.device)
-    if out.dtype != torch.bfloat16 or out.shape != (M, N) or out.stride(1) != 1:
+        return torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+    if out.dtype is not torch.bfloat16 or out.shape != (M, N) or out.stride(1) != 1:
         raise TypeError(f"{name} must be bfloat16 [{M}, {N}] with unit inner stride")
     return out
 
@@ -352,19 +366,18 @@ def qlinear_int4(x, w, w_scale, w_zero=None, bias=None, *, group=128, debug=Fals
     or fp16 [N, >=ceil(K/group)]; w_zero: uint8 [N, >=ceil(K/group)] (values 0..127) or None: 8.
     group: a power of two >= 32.  With debug=True returns (y, path)."""
     _bf16(x, "x")
-    M, K = x.shape
-    N = w.shape[0]
-    fmt = _int4_weights(x, w, w_scale, w_zero, group)
-    if bias is not None and (bias.dtype != torch.bfloat16 or bias.shape != (N,) or not bias.is_contiguous()):
+    (M, K), sx = x.shape, x.stride()
+    N, ldw, lds, ldz, fmt = _int4_weights(K, sx, w, w_scale, w_zero, group)
+    if bias is not None and (bias.dtype is not torch.bfloat16 or bias.shape != (N,) or not bias.is_contiguous()):
         raise TypeError(f"bias must be bfloat16 [{N}]")
     y = _out(out, M, N, x)
-    path = ctypes.c_int(0)
-    _check(lib.qlinear_int4(_ptr(x), M, K, x.stride(0), _ptr(w), N, w.stride(0), _ptr(w_scale), fmt,
-                            w_scale.stride(0), _ptr(w_zero), 0 if w_zero is None else w_zero.stride(0), group,
-                            _ptr(bias), _ptr(y), y.stride(0), _stream(stream), ctypes.byref(path)), "qlinear_int4")
-    if debug:
-        return y, PATHS[path.value]
-    return y
+    path = ctypes.c_int(0) if debug else None
+    st = lib.qlinear_int4(x.data_ptr(), M, K, sx[0], w.data_ptr(), N, ldw, w_scale.data_ptr(), fmt, lds, _ptr(w_zero),
+                          ldz, group, _ptr(bias), y.data_ptr(), N if out is None else y.stride(0), _stream(stream),
+                          path)
+    if st:
+        raise QLError(st, "qlinear_int4")
+    return (y, PATHS[path.value]) if debug else y
 
 
 def gated_ffn_int4(x, w13, w_scale, w_zero=None, *, group=128, swiglu_alpha=1.0, swiglu_limit=None, debug=False,
@@ -373,20 +386,19 @@ def gated_ffn_int4(x, w13, w_scale, w_zero=None, *, group=128, swiglu_alpha=1.0,
     [0, I) gate, [I, 2I) up), stored as qlinear_int4's, in one launch.  x: bf16 [M, H]; w13: uint8
     [2I, >=H/2].  Returns bf16 [M, I]; with debug=True (h, path)."""
     _bf16(x, "x")
-    M, H = x.shape
-    if w13.shape[0] % 2:
+    (M, H), sx = x.shape, x.stride()
+    N, ldw, lds, ldz, fmt = _int4_weights(H, sx, w13, w_scale, w_zero, group)
+    if N & 1:
         raise ValueError("w13 must have an even number of rows (gate, then up)")
-    I = w13.shape[0] // 2
-    fmt = _int4_weights(x, w13, w_scale, w_zero, group)
+    I = N >> 1
     h = _out(out, M, I, x)
-    path = ctypes.c_int(0)
-    _check(lib.gated_ffn_int4(_ptr(x), M, H, x.stride(0), _ptr(w13), I, w13.stride(0), _ptr(w_scale), fmt,
-                              w_scale.stride(0), _ptr(w_zero), 0 if w_zero is None else w_zero.stride(0), group,
-                              float(swiglu_alpha), float("inf") if swiglu_limit is None else float(swiglu_limit),
-                              _ptr(h), h.stride(0), _stream(stream), ctypes.byref(path)), "gated_ffn_int4")
-    if debug:
-        return h, PATHS[path.value]
-    return h
+    path = ctypes.c_int(0) if debug else None
+    st = lib.gated_ffn_int4(x.data_ptr(), M, H, sx[0], w13.data_ptr(), I, ldw, w_scale.data_ptr(), fmt, lds,
+                            _ptr(w_zero), ldz, group, swiglu_alpha, _inf(swiglu_limit), h.data_ptr(),
+                            I if out is None else h.stride(0), _stream(stream), path)
+    if st:
+        raise QLError(st, "gated_ffn_int4")
+    return (h, PATHS[path.value]) if debug else h
 
 
 # ------------------------------------------------------------------ gated feed-forward block
@@ -399,14 +411,19 @@ class FFNCheckpoint(NamedTuple):
     scale: torch.Tensor | None
 
 
+_STATUS_BYTES = workspace_bytes(OP_GATED_FFN, 1, 8, 8)  # the same for every size
 _SAVE = {None: SAVE_NONE, "bf16": SAVE_BF16, "int8": SAVE_INT8}
 
 
 def _ffn_weights(x, w13):
-    if w13.dtype != torch.bfloat16 or w13.stride(1) != 1 or x.stride(1) != 1:
+    """Checks w13 [2I, H] against x [M, H]; returns (M, H, I, row strides of x and w13)."""
+    (M, H), (ldx, ix) = x.shape, x.stride()
+    (rows, cols), (ldw, iw) = w13.shape, w13.stride()
+    if w13.dtype is not torch.bfloat16 or iw != 1 or ix != 1:
         raise TypeError("w13 must be bfloat16 with unit inner stride; x must have unit inner stride")
-    if w13.shape[0] % 2 or w13.shape[1] != x.shape[1]:
+    if rows & 1 or cols != H:
         raise ValueError("w13 must be [2I, H] (gate rows, then up rows) for x [M, H]")
+    return M, H, rows >> 1, ldx, ldw
 
 
 def gated_ffn(x, w13, *, swiglu_alpha=1.0, swiglu_limit=None, save=None, debug=False, out=None, workspace=None,
@@ -416,25 +433,24 @@ def gated_ffn(x, w13, *, swiglu_alpha=1.0, swiglu_limit=None, save=None, debug=F
     "bf16" or "int8" also returns an FFNCheckpoint of g and u: (h, checkpoint).  debug=True appends
     the path."""
     _bf16(x, "x")
-    _ffn_weights(x, w13)
+    M, H, I, ldx, ldw = _ffn_weights(x, w13)
     if save not in _SAVE:
         raise ValueError('save must be None, "bf16" or "int8"')
-    M, H = x.shape
-    I = w13.shape[0] // 2
     h = _out(out, M, I, x)
-    saved = None
+    saved = data = scale = None
     if save is not None:
         P = -(-I // 128) * 128
-        saved = FFNCheckpoint(save, torch.empty(M, 2, P, dtype=torch.bfloat16 if save == "bf16" else torch.int8,
-                                                device=x.device),
-                              torch.empty(M, 2, P // 128, dtype=torch.float32, device=x.device)
-                              if save == "int8" else None)
-    ws = _ws(x.device, workspace_bytes(OP_GATED_FFN, M, I, H), stream, workspace)
-    path = ctypes.c_int(0)
-    _check(lib.gated_ffn(_ptr(x), M, H, x.stride(0), _ptr(w13), I, w13.stride(0), float(swiglu_alpha),
-                         float("inf") if swiglu_limit is None else float(swiglu_limit), _ptr(h), h.stride(0),
-                         _SAVE[save], _ptr(saved.data) if saved else None, _ptr(saved.scale) if saved else None,
-                         _ptr(ws), ws.numel(), _stream(stream), ctypes.byref(path)), "gated_ffn")
+        data = torch.empty((M, 2, P), dtype=torch.bfloat16 if save == "bf16" else torch.int8, device=x.device)
+        if save == "int8":
+            scale = torch.empty((M, 2, P // 128), dtype=torch.float32, device=x.device)
+        saved = FFNCheckpoint(save, data, scale)
+    ws = _ws(x.device, _STATUS_BYTES, stream, workspace)
+    path = ctypes.c_int(0) if debug else None
+    st = lib.gated_ffn(x.data_ptr(), M, H, ldx, w13.data_ptr(), I, ldw, swiglu_alpha, _inf(swiglu_limit), h.data_ptr(),
+                       I if out is None else h.stride(0), _SAVE[save], _ptr(data), _ptr(scale), ws.data_ptr(),
+                       ws.numel(), _stream(stream), path)
+    if st:
+        raise QLError(st, "gated_ffn")
     res = (h,) if saved is None else (h, saved)
     if debug:
         res += (PATHS[path.value],)
@@ -448,25 +464,26 @@ def gated_ffn_backward(dh, x, w13, saved, *, swiglu_alpha=1.0, swiglu_limit=None
     as in the forward."""
     _bf16(dh, "dh")
     _bf16(x, "x")
-    _ffn_weights(x, w13)
-    M, H = x.shape
-    I = w13.shape[0] // 2
+    M, H, I, ldx, ldw = _ffn_weights(x, w13)
     if dh.shape != (M, I) or dh.stride(1) != 1:
         raise TypeError(f"dh must be [{M}, {I}] with unit inner stride")
+    mode, data, scale = saved
     P = -(-I // 128) * 128
-    if saved.mode not in ("bf16", "int8") or saved.data.shape != (M, 2, P) or not saved.data.is_contiguous():
+    if (mode not in ("bf16", "int8") or data.shape != (M, 2, P) or not data.is_contiguous()
+            or data.dtype is not (torch.bfloat16 if mode == "bf16" else torch.int8)):
         raise ValueError("saved must be the FFNCheckpoint of this x and w13")
-    if saved.mode == "int8" and (saved.scale is None or saved.scale.shape != (M, 2, P // 128)):
+    if mode == "int8" and (scale is None or scale.shape != (M, 2, P // 128) or not scale.is_contiguous()
+                           or scale.dtype is not torch.float32):
         raise ValueError("saved must be the FFNCheckpoint of this x and w13")
     dx = _out(out_dx, M, H, x, "out_dx") if need_dx else None
     dw = _out(out_dw, 2 * I, H, x, "out_dw") if need_dw else None
     ws = _ws(x.device, workspace_bytes(OP_GATED_FFN_BWD, M, I, H), stream, workspace)
-    path = ctypes.c_int(0)
-    _check(lib.gated_ffn_backward(_ptr(dh), dh.stride(0), _ptr(x), M, H, x.stride(0), _ptr(w13), I, w13.stride(0),
-                                  float(swiglu_alpha), float("inf") if swiglu_limit is None else float(swiglu_limit),
-                                  _SAVE[saved.mode], _ptr(saved.data), _ptr(saved.scale), _ptr(dx),
-                                  0 if dx is None else dx.stride(0), _ptr(dw), 0 if dw is None else dw.stride(0),
-                                  _ptr(ws), ws.numel(), _stream(stream), ctypes.byref(path)), "gated_ffn_backward")
+    st = lib.gated_ffn_backward(dh.data_ptr(), dh.stride(0), x.data_ptr(), M, H, ldx, w13.data_ptr(), I, ldw,
+                                swiglu_alpha, _inf(swiglu_limit), _SAVE[mode], data.data_ptr(), _ptr(scale), _ptr(dx),
+                                0 if dx is None else dx.stride(0), _ptr(dw), 0 if dw is None else dw.stride(0),
+                                ws.data_ptr(), ws.numel(), _stream(stream), None)
+    if st:
+        raise QLError(st, "gated_ffn_backward")
     return dx, dw
 
 

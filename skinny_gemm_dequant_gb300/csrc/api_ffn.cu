@@ -82,7 +82,7 @@ ql_status qlinear_int4(const uint16_t* x, int64_t M, int64_t K, int64_t ldx, con
   FfnSkinnyArgs a = int4_args(x, M, K, ldx, w, ldw_bytes, w_scale, scale_fmt, lds, w_zero, ldz, group, y, ldy);
   a.N = (int)N;
   a.bias = bias;
-  const cudaError_t e = launch_ffn_skinny(true, false, a, (cudaStream_t)stream);
+  const cudaError_t e = launch_int4(false, a, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_status(e);
   if (path_out) *path_out = QL_PATH_INT4_SKINNY;
   return QL_OK;
@@ -102,7 +102,7 @@ ql_status gated_ffn_int4(const uint16_t* x, int64_t M, int64_t H, int64_t ldx, c
   a.N = (int)I;
   a.alpha = swiglu_alpha;
   a.limit = swiglu_limit;
-  const cudaError_t e = launch_ffn_skinny(true, true, a, (cudaStream_t)stream);
+  const cudaError_t e = launch_int4(true, a, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_status(e);
   if (path_out) *path_out = QL_PATH_GATED_FFN_INT4;
   return QL_OK;
@@ -136,7 +136,7 @@ ql_status gated_ffn(const uint16_t* x, int64_t M, int64_t H, int64_t ldx, const 
     a.ldy = ldh;
     a.alpha = swiglu_alpha;
     a.limit = swiglu_limit;
-    e = launch_ffn_skinny(false, true, a, st);
+    e = launch_ffn_skinny(a, st);
   } else {
     tc::FfnForward f = {};
     f.x = x;

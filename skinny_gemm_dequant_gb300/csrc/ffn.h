@@ -25,7 +25,8 @@ struct FfnSkinnyArgs {
   float alpha, limit;     // activation of a gated block
 };
 constexpr int64_t kFfnSkinnyTokens = 32;  // tokens one pass over the weights takes
-cudaError_t launch_ffn_skinny(bool int4, bool gated, const FfnSkinnyArgs& a, cudaStream_t st);
+cudaError_t launch_ffn_skinny(const FfnSkinnyArgs& a, cudaStream_t st);
+cudaError_t launch_int4(bool gated, const FfnSkinnyArgs& a, cudaStream_t st);  // kernels_int4.cu
 
 // ------------------------------------------------------------------ tcgen05 path (ffn_tc.cu)
 namespace tc {
