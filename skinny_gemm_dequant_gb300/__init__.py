@@ -11,6 +11,7 @@ there is no fallback implementation.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 from typing import NamedTuple
@@ -405,13 +406,13 @@ def gated_ffn_int4(x, w13, w_scale, w_zero=None, *, group=128, swiglu_alpha=1.0,
 class FFNCheckpoint(NamedTuple):
     """What gated_ffn keeps of g and u for gated_ffn_backward.  mode "bf16": data bf16 [M, 2, P];
     mode "int8": data int8 codes [M, 2, P] and scale fp32 [M, 2, P/128], value = code * scale; P = I
-    rounded up to 128 (columns past I are not written)."""
+    rounded up to 128 (columns past I are undefined)."""
     mode: str
     data: torch.Tensor
     scale: torch.Tensor | None
 
 
-_STATUS_BYTES = workspace_bytes(OP_GATED_FFN, 1, 8, 8)  # the same for every size
+_ffn_bytes = functools.lru_cache(maxsize=256)(workspace_bytes)
 _SAVE = {None: SAVE_NONE, "bf16": SAVE_BF16, "int8": SAVE_INT8}
 
 
@@ -444,7 +445,7 @@ def gated_ffn(x, w13, *, swiglu_alpha=1.0, swiglu_limit=None, save=None, debug=F
         if save == "int8":
             scale = torch.empty((M, 2, P // 128), dtype=torch.float32, device=x.device)
         saved = FFNCheckpoint(save, data, scale)
-    ws = _ws(x.device, _STATUS_BYTES, stream, workspace)
+    ws = _ws(x.device, _ffn_bytes(OP_GATED_FFN, M, I, H), stream, workspace)
     path = ctypes.c_int(0) if debug else None
     st = lib.gated_ffn(x.data_ptr(), M, H, ldx, w13.data_ptr(), I, ldw, swiglu_alpha, _inf(swiglu_limit), h.data_ptr(),
                        I if out is None else h.stride(0), _SAVE[save], _ptr(data), _ptr(scale), ws.data_ptr(),
@@ -477,7 +478,7 @@ def gated_ffn_backward(dh, x, w13, saved, *, swiglu_alpha=1.0, swiglu_limit=None
         raise ValueError("saved must be the FFNCheckpoint of this x and w13")
     dx = _out(out_dx, M, H, x, "out_dx") if need_dx else None
     dw = _out(out_dw, 2 * I, H, x, "out_dw") if need_dw else None
-    ws = _ws(x.device, workspace_bytes(OP_GATED_FFN_BWD, M, I, H), stream, workspace)
+    ws = _ws(x.device, _ffn_bytes(OP_GATED_FFN_BWD, M, I, H), stream, workspace)
     st = lib.gated_ffn_backward(dh.data_ptr(), dh.stride(0), x.data_ptr(), M, H, ldx, w13.data_ptr(), I, ldw,
                                 swiglu_alpha, _inf(swiglu_limit), _SAVE[mode], data.data_ptr(), _ptr(scale), _ptr(dx),
                                 0 if dx is None else dx.stride(0), _ptr(dw), 0 if dw is None else dw.stride(0),

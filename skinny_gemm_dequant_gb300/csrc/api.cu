@@ -4,6 +4,7 @@
 #include <cstdio>
 #include <cstring>
 
+#include "ffn.h"
 #include "gemm_i8_tcgen05.h"
 #include "gemm_tcgen05.h"
 #include "internal.h"
@@ -393,9 +394,9 @@ size_t ql_workspace_bytes(int op, int64_t M, int64_t N, int64_t K, int E, int to
     case QL_OP_FP8_CHANNEL:
       return dense2_layout(FMT_F8E4C, Mc, N, K, 128).total;  // E4M3 and E5M2 lay out alike
     case QL_OP_GATED_FFN:
-      return kRegionsOff;  // the status word
+      return kRegionsOff + tc::ffn_forward_slots(M, K, N);  // the status word, tickets; cut tiles' sums
     case QL_OP_GATED_FFN_BWD:
-      return kRegionsOff + al256((size_t)M * 2 * N * 2);  // [dg du]
+      return kRegionsOff + al256((size_t)M * 2 * N * 2) + tc::ffn_backward_slots(M, K, N);  // [dg du] first
     case QL_OP_MOE_MXFP4: {
       if (E <= 0 || topk <= 0) return 0;
       if (M > 16) return moe3_layout(M, N, K, E, topk).total;

@@ -11,6 +11,8 @@ using namespace ql;
 
 namespace {
 
+constexpr size_t kTicketOff = 256;  // the zero region of every workspace
+
 inline bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 inline bool al2(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 1) == 0; }
 inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -153,6 +155,8 @@ ql_status gated_ffn(const uint16_t* x, int64_t M, int64_t H, int64_t ldx, const 
     f.save = save;
     f.ckpt = ckpt;
     f.ckpt_scale = ckpt_scale;
+    f.slots = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + workspace_zero_bytes());
+    f.tickets = reinterpret_cast<unsigned*>(static_cast<uint8_t*>(workspace) + kTicketOff);
     f.status = static_cast<uint32_t*>(workspace);
     f.wait_limit = wait_limit();
     e = tc::launch_ffn_forward(f, st);
@@ -196,7 +200,10 @@ ql_status gated_ffn_backward(const uint16_t* dh, int64_t ld_dh, const uint16_t* 
   b.ckpt_scale = ckpt_scale;
   b.alpha = swiglu_alpha;
   b.limit = swiglu_limit;
-  b.dgu = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(workspace) + workspace_zero_bytes());
+  uint8_t* regions = static_cast<uint8_t*>(workspace) + workspace_zero_bytes();
+  b.dgu = reinterpret_cast<uint16_t*>(regions);
+  b.slots = reinterpret_cast<float*>(regions + ((size_t)M * 2 * I * 2 + 255) / 256 * 256);
+  b.tickets = reinterpret_cast<unsigned*>(static_cast<uint8_t*>(workspace) + kTicketOff);
   b.dx = dx;
   b.ld_dx = ld_dx;
   b.dw13 = dw13;

@@ -40,9 +40,13 @@ struct FfnForward {
   int save;           // QL_SAVE_*
   void* ckpt;         // [M, 2, I padded to 128] bf16 or int8
   float* ckpt_scale;  // [M, 2, I padded / 128] (int8)
+  float* slots;       // workspace: ffn_forward_slots bytes
+  unsigned* tickets;  // workspace: zero between calls
   uint32_t* status;
   uint32_t wait_limit;
 };
+size_t ffn_forward_slots(int64_t M, int64_t H, int64_t I);
+size_t ffn_backward_slots(int64_t M, int64_t H, int64_t I);
 cudaError_t launch_ffn_forward(const FfnForward& f, cudaStream_t st);
 
 struct FfnBackward {
@@ -59,6 +63,8 @@ struct FfnBackward {
   int64_t ld_dx;
   uint16_t* dw13;  // bf16 [2I, ld_dw] or null
   int64_t ld_dw;
+  float* slots;  // workspace: ffn_backward_slots bytes
+  unsigned* tickets;
   uint32_t* status;
   uint32_t wait_limit;
 };

@@ -49,14 +49,14 @@ __device__ __forceinline__ float ckpt_scale(float amax, float& inv) {
   inv = 127.0f / amax;
   return amax / 127.0f;
 }
-__device__ __forceinline__ uint2 ckpt_codes8(const float* v, float inv) {
-  uint32_t w[2] = {0u, 0u};
+__device__ __forceinline__ void ckpt_codes32(const float* v, float inv, uint32_t* w) {
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const int q = __float2int_rn(v[j] * inv);  // |v| inv <= 127 (1 + 2^-23): rounds to at most 127
-    w[j >> 2] |= ((uint32_t)q & 0xFFu) << (8 * (j & 3));
+    w[j] = 0u;
+#pragma unroll
+    for (int b = 0; b < 4; ++b)  // |v| inv <= 127 (1 + 2^-23): rounds to at most 127
+      w[j] |= ((uint32_t)__float2int_rn(v[4 * j + b] * inv) & 0xFFu) << (8 * b);
   }
-  return make_uint2(w[0], w[1]);
 }
 __device__ __forceinline__ void ckpt_values8(uint2 c, float scale, float* v) {
 #pragma unroll

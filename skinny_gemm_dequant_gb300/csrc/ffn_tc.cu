@@ -9,19 +9,28 @@
 //             with gc = min(g, L), uc = clamp(u, -L, L), silu'(t) = s(t) (1 + t (1 - s(t)))
 //
 // One GEMM kernel, C = A B^T with bf16 operands and fp32 sums in tensor memory, in three forms:
-//   FWD: A = x, B = W13 (both K-major); a tile is 256 tokens x 128 outputs, i.e. 128 gate and 128
-//        up columns, so that the activation and the product run in the epilogue and g, u never
-//        reach memory (but for the checkpoint)
-//   DX : A = [dg du] (K-major), B = W13^T (N-major: H is contiguous), a tile is 256 x 256
-//   DW : A = [dg du]^T (M-major), B = x^T (N-major), a tile is 256 x 256
+//   FWD: A = x, B = W13 (both K-major); a tile's columns are half gate, half up columns of the same
+//        outputs, so that the activation and the product run in the epilogue and g, u never reach
+//        memory (but for the checkpoint)
+//   DX : A = [dg du] (K-major), B = W13^T (N-major: H is contiguous)
+//   DW : A = [dg du]^T (M-major), B = x^T (N-major)
+// A tile is 256 rows by up to 256 columns.
 // A pair of CTAs on two SMs shares a tile (cta_group::2): each holds 128 rows of A, half of B's
-// 256 columns and 128 rows of the accumulator, so that an SM loads half of B.  The grid is one
+// columns and 128 rows of the accumulator, so that an SM loads half of B.  The grid is one
 // pair per two SMs; pairs take tiles in turn.  Roles in a CTA:
 //   warp 0: TMA producer;  warp 1: MMA issue (first CTA of the pair only);  warp 2: tensor memory;
-//   warps 4..7: epilogue, one row of the accumulator per thread.
+//   warps 4..11: epilogue, one row and half of the columns of the accumulator per thread.
 // Two accumulators of 256 columns take turns, so a tile's epilogue runs under the next tile's
-// MMAs.  Every wait is bounded; one that runs out raises QL_DEV_TIMEOUT in the status word and the
-// pair leaves its loops, waits for copies and MMAs in flight and frees its tensor memory.
+// MMAs.
+// Where whole tiles would leave most pairs idle in the last round, that round's tiles are cut along
+// K into equal parts, one per pair.  A pair that holds a part stores its fp32 sums in a slot of the
+// workspace and counts in on the tile's ticket; the CTA that completes the count adds the parts in
+// the order of K (the sum does not depend on who is last) and runs the epilogue on them.  Nobody
+// waits for another pair.  Equal shares of all tiles of the last two rounds, which would leave no
+// pair idle, were slower (4096 x 17408 x 5120 dx: 1009 us against 956 us uncut): the pairs then
+// stand at different k and no longer find each other's operands in L2.
+// Every wait is bounded; one that runs out raises QL_DEV_TIMEOUT in the status word and the pair
+// leaves its loops, waits for copies and MMAs in flight and frees its tensor memory.
 #include <cudaTypedefs.h>
 
 #include <atomic>
@@ -41,18 +50,25 @@ namespace {
 
 enum { FWD = 0, DX = 1, DW = 2 };
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 384;
+constexpr int kEpiThreads = 256;
 constexpr int kBlockK = 64;  // one 128-byte swizzled row of bf16
 constexpr int kStages = 6;
 constexpr uint32_t kHalfBytes = 128 * kBlockK * 2;  // one operand's half tile of a stage
 constexpr uint32_t kStageBytes = 2 * kHalfBytes;
+constexpr uint32_t kRowStage = 32 * 80;  // an epilogue warp's 32 rows on their way out
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kDrainLimit = 1u << 22;
 constexpr int kGroupM = 16;  // tile rows that run before the next tile column
 
 struct Params {
   int rows, cols, K;        // of C; FWD: cols = I (outputs)
+  int width;                // columns of a tile: 64, 96, ..., 256
   int tiles_m, tiles_n, nk;
+  int whole;                // tiles taken whole, pair after pair
+  int cut, parts;           // the tiles after them, each cut along K into so many parts
+  float* slots;             // [cut][parts][2 CTAs][64 groups of 4 columns][128 rows][4] sums
+  unsigned* tickets;        // [cut tiles][2 CTAs], zero between calls
   uint16_t* out;            // bf16 [rows, ld_out]
   int64_t ld_out;
   float alpha, limit;       // FWD
@@ -62,6 +78,30 @@ struct Params {
   float* ckpt_scale;
   uint32_t* status;
   uint32_t wait_limit;
+};
+constexpr int64_t kSlotFloats = 256 * 128;  // one CTA's sums of a part
+
+// what a pair works on, one item after the other: whole tiles, then a part of a cut one
+struct Walk {
+  int t, pair;
+  __device__ explicit Walk(int pair) : t(pair), pair(pair) {}
+  __device__ bool next(const Params& p, int pairs, int& tile, int& k0, int& k1) {
+    if (t < p.whole) {
+      tile = t;
+      k0 = 0;
+      k1 = p.nk;
+      t += pairs;
+      return true;
+    }
+    if (pair < 0 || pair >= p.cut * p.parts) return false;
+    // neighbouring pairs take the same k of neighbouring tiles
+    const int part = pair / p.cut;
+    tile = p.whole + pair - part * p.cut;
+    k0 = (int)((int64_t)part * p.nk / p.parts);
+    k1 = (int)((int64_t)(part + 1) * p.nk / p.parts);
+    pair = -1;
+    return true;
+  }
 };
 
 // ------------------------------------------------------------------ pair-of-CTAs PTX
@@ -130,11 +170,11 @@ __device__ __forceinline__ uint64_t desc_mn(uint32_t saddr) {
          (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
 
-// kind::f16, bf16 operands (format 1), fp32 accumulator, M = 256 over the pair, N = 256; bits 15
+// kind::f16, bf16 operands (format 1), fp32 accumulator, M = 256 over the pair, N = width; bits 15
 // and 16: A / B are MN-major
-constexpr uint32_t idesc_pair(bool a_mn, bool b_mn) {
+__device__ __forceinline__ uint32_t idesc_pair(bool a_mn, bool b_mn, int width) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
-         ((256u >> 3) << 17) | ((256u >> 4) << 24);
+         ((uint32_t)(width >> 3) << 17) | ((256u >> 4) << 24);
 }
 
 // tile index -> (m, n): blocks of kGroupM tile rows, the rows of a block first
@@ -145,11 +185,53 @@ __device__ __forceinline__ void tile_at(const Params& p, int t, int& m, int& n) 
   n = in / rows;
 }
 
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  uint32_t w;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
+  return w;
+}
 __device__ __forceinline__ void store8(uint16_t* p, const float* v) {
-  uint32_t w[4];
+  *reinterpret_cast<uint4*>(p) = make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
+}
+
+// One row of BYTES (32 or 64) per lane to global memory through shared memory, so that neighbouring
+// lanes write neighbouring 16 bytes: whole sectors instead of 16 bytes of 32 different rows.  dst:
+// the first lane's row; rows and bytes of a row that exist.  `stage`: 32 rows of BYTES + 16.
+template <int BYTES>
+__device__ __forceinline__ void store_rows(uint32_t stage, const uint32_t* w, uint8_t* dst, int64_t pitch, int rows,
+                                           int bytes) {
+  constexpr int LANES = BYTES / 16, STEP = 32 / LANES;  // lanes per row, rows per store
+  const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(v[2 * i + 1]), "f"(v[2 * i]));
-  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  for (int i = 0; i < LANES; ++i)
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(stage + lane * (BYTES + 16) + i * 16), "r"(w[4 * i]),
+                 "r"(w[4 * i + 1]), "r"(w[4 * i + 2]), "r"(w[4 * i + 3])
+                 : "memory");
+  __syncwarp();
+  const int piece = lane % LANES;
+#pragma unroll
+  for (int i = 0; i < LANES; ++i) {
+    const int r = i * STEP + lane / LANES;
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(stage + r * (BYTES + 16) + piece * 16)
+                 : "memory");
+    if (r < rows && piece * 16 < bytes) *reinterpret_cast<uint4*>(dst + r * pitch + piece * 16) = v;
+  }
+  __syncwarp();  // read before the next rows are put there
+}
+
+// true in every epilogue thread if `bad` is true in one
+__device__ __forceinline__ bool epilogue_any(bool bad) {
+  int r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, 1, %2, p;\n\t"
+      "selp.s32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((int)bad), "n"(kEpiThreads)
+      : "memory");
+  return r != 0;
 }
 
 template <int MODE>
@@ -160,14 +242,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t full[kStages], empty[kStages], tfull[2], tempty[2], done;
   __shared__ uint32_t s_tmem;
-  __shared__ int s_abort, s_issued;
+  __shared__ int s_abort, s_issued, s_last;
+  __shared__ float s_amax[2][2][128][2];  // FWD, int8: [tile parity][column half][row][g, u]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cta_rank();
   // the stages start at the same offset in both CTAs
   const uint32_t base = (smem_u32(smem_raw) + 1023) & ~1023u;
+  const int hw = p.width / 2;  // columns of B in each CTA; FWD: outputs of a tile
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-  const int tiles = p.tiles_m * p.tiles_n;
   const uint32_t lim = p.wait_limit;
   volatile int* abort = &s_abort;
 
@@ -178,7 +261,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tfull[b], 1);
-      mbar_init(&tempty[b], 8);  // four epilogue warps in each CTA
+      mbar_init(&tempty[b], 16);  // eight epilogue warps in each CTA
     }
     mbar_init(&done, 1);
     fence_mbar_init();
@@ -206,22 +289,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (warp == 0) {
     if (lane == 0) {
       // ---------------------------------------------------------- producer
+      // bytes of a stage in one CTA: B by N-major chunks of 64 columns is loaded whole
+      const uint32_t half_bytes = kHalfBytes + (B_MN ? (hw > 64 ? kHalfBytes : kHalfBytes / 2) : (uint32_t)hw * kBlockK * 2);
       int s = 0, issued = 0;
       uint32_t ph = 1;  // the first pass over the stages finds them empty
       bool ok = true;
-      for (int t = pair; t < tiles && ok; t += pairs) {
+      int t, k0, k1;
+      for (Walk w(pair); ok && w.next(p, pairs, t, k0, k1);) {
         int tm, tn;
         tile_at(p, t, tm, tn);
         const int ra = tm * 256 + (int)rank * 128;
-        const int rb = MODE == FWD ? tn * 128 + (int)rank * p.I : tn * 256 + (int)rank * 128;
-        for (int kt = 0; kt < p.nk; ++kt) {
+        const int rb = MODE == FWD ? tn * hw + (int)rank * p.I : tn * p.width + (int)rank * hw;
+        for (int kt = k0; kt < k1; ++kt) {
           if (!wait2(&empty[s], ph, lim, abort)) {
             fail();
             ok = false;
             break;
           }
           const uint32_t bar = in_cta(smem_u32(&full[s]), 0);
-          if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * kStageBytes);
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * half_bytes);
           const uint32_t sa = base + (uint32_t)s * kStageBytes, sb = sa + kHalfBytes;
           const int k = kt * kBlockK;
           if (A_MN) {
@@ -232,7 +318,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
           if (B_MN) {
             load_pair(sb, &tmB, rb, k, bar);
-            load_pair(sb + 8192, &tmB, rb + 64, k, bar);
+            if (hw > 64) load_pair(sb + 8192, &tmB, rb + 64, k, bar);
           } else {
             load_pair(sb, &tmB, k, rb, bar);
           }
@@ -258,22 +344,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {
       // ---------------------------------------------------------- MMA issue
-      constexpr uint32_t idesc = idesc_pair(A_MN, B_MN);
+      const uint32_t idesc = idesc_pair(A_MN, B_MN, p.width);
       constexpr uint64_t a_step = A_MN ? 2048 / 16 : 2, b_step = B_MN ? 2048 / 16 : 2;  // 16 k
       const uint64_t a0 = A_MN ? desc_mn(base) : smem_desc_sw128(base);
       const uint64_t b0 = B_MN ? desc_mn(base + kHalfBytes) : smem_desc_sw128(base + kHalfBytes);
       int s = 0, n = 0;
       uint32_t ph = 0;
       bool ok = true;
-      for (int t = pair; t < tiles && ok; t += pairs, ++n) {
+      int t, k0, k1;
+      for (Walk w(pair); ok && w.next(p, pairs, t, k0, k1); ++n) {
         const int buf = n & 1;
         if (!wait2(&tempty[buf], (uint32_t)((n >> 1) & 1) ^ 1, lim, abort)) {
           fail();
+          ok = false;
           break;
         }
         tc_fence_after();
         const uint32_t d = tmem + (uint32_t)buf * 256;
-        for (int kt = 0; kt < p.nk; ++kt) {
+        for (int kt = k0; kt < k1; ++kt) {
           if (!wait2(&full[s], ph, lim, abort)) {
             fail();
             ok = false;
@@ -283,7 +371,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const uint64_t off = (uint64_t)s * (kStageBytes >> 4);
 #pragma unroll
           for (int j = 0; j < kBlockK / 16; ++j)
-            mma_pair(d, a0 + off + j * a_step, b0 + off + j * b_step, idesc, (kt | j) != 0);
+            mma_pair(d, a0 + off + j * a_step, b0 + off + j * b_step, idesc, kt != k0 || j != 0);
           commit_pair(&empty[s]);
           if (++s == kStages) {
             s = 0;
@@ -296,103 +384,161 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
   } else if (warp >= 4) {
     // ------------------------------------------------------------ epilogue
-    const int q = warp & 3;
-    int n = 0;
-    for (int t = pair; t < tiles; t += pairs, ++n) {
+    const int q = warp & 3, half = (warp - 4) >> 2;  // tensor-memory lane quadrant, column half
+    const int r = 32 * q + lane;                     // row of this CTA's 128
+    const uint32_t stage = base + kStages * kStageBytes + (uint32_t)(warp - 4) * kRowStage;
+    int n = 0, t, k0, k1;
+    for (Walk w(pair); w.next(p, pairs, t, k0, k1); ++n) {
       int tm, tn;
       tile_at(p, t, tm, tn);
       const int buf = n & 1;
       int got = 0;
       if (lane == 0) got = wait2(&tfull[buf], (uint32_t)(n >> 1) & 1, lim, abort);
       got = __shfl_sync(0xffffffffu, got, 0);
-      if (!got) {
-        if (lane == 0) fail();
-        break;
-      }
+      if (!got && lane == 0) fail();
+      if (epilogue_any(!got)) break;  // all eight warps or none: they meet at barriers below
       tc_fence_after();
-      const int row = tm * 256 + (int)rank * 128 + 32 * q + lane;
+      const int row = tm * 256 + (int)rank * 128 + r;
+      const int row0 = row - lane, rows = min(32, p.rows - row0);  // this warp's rows that exist
       const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)buf * 256;
-      if constexpr (MODE == FWD) {
-        const int i0 = tn * 128;
-        float inv_g = 0.f, inv_u = 0.f;
-        const int64_t ipad = ckpt_pad(p.I);
-        if (p.save == QL_SAVE_INT8) {
-          // first pass over the accumulator: the largest |g| and |u| of the row's 128 columns
-          float ag = 0.f, au = 0.f;
-#pragma unroll 1
-          for (int c = 0; c < 128; c += 32) {
-            uint32_t rg[32], ru[32];
-            tmem_ld_x32(acc + c, rg);
-            tmem_ld_x32(acc + 128 + c, ru);
-            tmem_wait_ld();
+
+      // 32 columns of the tile's sums: from tensor memory, or the parts' sum from the workspace
+      auto slot_of = [&](int part) {
+        return p.slots + ((int64_t)((t - p.whole) * p.parts + part) * 2 + rank) * kSlotFloats + r * 4;
+      };
+      auto from_tmem = [&](int c, float (&v)[32]) {
+        uint32_t u[32];
+        tmem_ld_x32(acc + c, u);
+        tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (i0 + c + (i & ~7) < p.cols) {
-                ag = max_nan(ag, fabsf(__uint_as_float(rg[i])));
-                au = max_nan(au, fabsf(__uint_as_float(ru[i])));
-              }
-          }
-          if (row < p.rows) {
-            float* s = p.ckpt_scale + (int64_t)row * 2 * (ipad / 128) + tn;
-            s[0] = ckpt_scale(ag, inv_g);
-            s[ipad / 128] = ckpt_scale(au, inv_u);
+        for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(u[i]);
+      };
+      auto from_slots = [&](int c, float (&v)[32]) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = 0.f;
+#pragma unroll 2
+        for (int j = 0; j < p.parts; ++j) {
+          const float* src = slot_of(j) + (int64_t)c * 128;
+#pragma unroll
+          for (int i = 0; i < 32; i += 4) {
+            const float4 f = __ldcg(reinterpret_cast<const float4*>(src + i * 128));
+            v[i] += f.x;
+            v[i + 1] += f.y;
+            v[i + 2] += f.z;
+            v[i + 3] += f.w;
           }
         }
+      };
+      auto finish = [&](auto load) {
+        if constexpr (MODE == FWD) {
+          const int i0 = tn * hw, outs = min(hw, p.cols - i0);  // the tile's outputs
+          float inv_g = 0.f, inv_u = 0.f;
+          const int64_t ipad = ckpt_pad(p.I);
+          if (p.save == QL_SAVE_INT8) {
+            // first pass over the sums: the largest |g| and |u| of the row's 128 columns (a tile holds
+            // one group: its width is 256)
+            float ag = 0.f, au = 0.f;
 #pragma unroll 1
-        for (int c = 0; c < 128; c += 32) {
-          uint32_t rg[32], ru[32];
-          tmem_ld_x32(acc + c, rg);
-          tmem_ld_x32(acc + 128 + c, ru);
-          tmem_wait_ld();
-          if (row < p.rows) {
+            for (int c = 64 * half; c < 64 * half + 64; c += 32) {
+              float g[32], u[32];
+              load(c, g);
+              load(hw + c, u);
 #pragma unroll
-            for (int v = 0; v < 32; v += 8) {
-              const int i = i0 + c + v;
-              if (i < p.cols) {
-                float h[8], g[8], u[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                  g[j] = __uint_as_float(rg[v + j]);
-                  u[j] = __uint_as_float(ru[v + j]);
-                  h[j] = gated_act(g[j], u[j], p.alpha, p.limit);
+              for (int i = 0; i < 32; ++i)
+                if (c + (i & ~7) < outs) {
+                  ag = max_nan(ag, fabsf(g[i]));
+                  au = max_nan(au, fabsf(u[i]));
                 }
-                store8(p.out + (int64_t)row * p.ld_out + i, h);
-                if (p.save == QL_SAVE_BF16) {
-                  uint16_t* ck = reinterpret_cast<uint16_t*>(p.ckpt) + (int64_t)row * 2 * ipad + i;
-                  store8(ck, g);
-                  store8(ck + ipad, u);
-                } else if (p.save == QL_SAVE_INT8) {
-                  int8_t* ck = reinterpret_cast<int8_t*>(p.ckpt) + (int64_t)row * 2 * ipad + i;
-                  *reinterpret_cast<uint2*>(ck) = ckpt_codes8(g, inv_g);
-                  *reinterpret_cast<uint2*>(ck + ipad) = ckpt_codes8(u, inv_u);
-                }
-              }
+            }
+            s_amax[buf][half][r][0] = ag;
+            s_amax[buf][half][r][1] = au;
+            epilogue_any(false);
+            ag = max_nan(ag, s_amax[buf][half ^ 1][r][0]);
+            au = max_nan(au, s_amax[buf][half ^ 1][r][1]);
+            const float sg = ckpt_scale(ag, inv_g), su = ckpt_scale(au, inv_u);
+            if (row < p.rows && half == 0) {
+              float* s = p.ckpt_scale + (int64_t)row * 2 * (ipad / 128) + tn;
+              s[0] = sg;
+              s[ipad / 128] = su;
             }
           }
+#pragma unroll 1
+          for (int c = 64 * half; c < min(64 * half + 64, outs); c += 32) {
+            float g[32], u[32];
+            load(c, g);
+            load(hw + c, u);
+            const int left = outs - c;
+            if (p.save == QL_SAVE_INT8) {
+              uint8_t* ck = reinterpret_cast<uint8_t*>(p.ckpt) + (int64_t)row0 * 2 * ipad + i0 + c;
+              uint32_t w[8];
+              // (past the last output up to a whole 16 bytes: the padding of the row)
+              ckpt_codes32(g, inv_g, w);
+              store_rows<32>(stage, w, ck, 2 * ipad, rows, left);
+              ckpt_codes32(u, inv_u, w);
+              store_rows<32>(stage, w, ck + ipad, 2 * ipad, rows, left);
+            }
+            uint32_t w[16];
+            if (p.save == QL_SAVE_BF16) {
+              uint8_t* ck = reinterpret_cast<uint8_t*>(p.ckpt) + ((int64_t)row0 * 2 * ipad + i0 + c) * 2;
+#pragma unroll
+              for (int j = 0; j < 16; ++j) w[j] = pack2(g[2 * j], g[2 * j + 1]);
+              store_rows<64>(stage, w, ck, 4 * ipad, rows, left * 2);
+#pragma unroll
+              for (int j = 0; j < 16; ++j) w[j] = pack2(u[2 * j], u[2 * j + 1]);
+              store_rows<64>(stage, w, ck + 2 * ipad, 4 * ipad, rows, left * 2);
+            }
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              w[j] = pack2(gated_act(g[2 * j], u[2 * j], p.alpha, p.limit),
+                           gated_act(g[2 * j + 1], u[2 * j + 1], p.alpha, p.limit));
+            store_rows<64>(stage, w, reinterpret_cast<uint8_t*>(p.out + (int64_t)row0 * p.ld_out + i0 + c),
+                           p.ld_out * 2, rows, left * 2);
+          }
+        } else {
+          const int c0 = tn * p.width, cols = min(p.width, p.cols - c0);
+#pragma unroll 1
+          for (int c = 128 * half; c < min(128 * half + 128, cols); c += 32) {
+            float v[32];
+            load(c, v);
+            uint32_t w[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) w[j] = pack2(v[2 * j], v[2 * j + 1]);
+            store_rows<64>(stage, w, reinterpret_cast<uint8_t*>(p.out + (int64_t)row0 * p.ld_out + c0 + c),
+                           p.ld_out * 2, rows, (cols - c) * 2);
+          }
         }
+      };
+      auto release = [&]() {  // the accumulator has been read
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_remote(in_cta(smem_u32(&tempty[buf]), 0));
+      };
+
+      if (k1 - k0 == p.nk) {
+        finish(from_tmem);
+        release();
       } else {
-        const int c0 = tn * 256;
+        float* dst = slot_of(pair / p.cut);
 #pragma unroll 1
-        for (int c = 0; c < 256; c += 32) {
-          uint32_t r[32];
-          tmem_ld_x32(acc + c, r);
-          tmem_wait_ld();
-          if (row < p.rows) {
+        for (int c = 128 * half; c < min(128 * half + 128, p.width); c += 32) {
+          float v[32];
+          from_tmem(c, v);
 #pragma unroll
-            for (int v = 0; v < 32; v += 8) {
-              if (c0 + c + v < p.cols) {
-                float f[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) f[j] = __uint_as_float(r[v + j]);
-                store8(p.out + (int64_t)row * p.ld_out + c0 + c + v, f);
-              }
-            }
-          }
+          for (int i = 0; i < 32; i += 4)
+            __stcg(reinterpret_cast<float4*>(dst + (int64_t)(c + i) * 128), make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]));
+        }
+        release();
+        __threadfence();
+        epilogue_any(false);  // every warp's part is stored and fenced
+        unsigned* ticket = p.tickets + 2 * (t - p.whole) + rank;
+        if (threadIdx.x == 128) s_last = atomicAdd(ticket, 1u) == (unsigned)(p.parts - 1);
+        epilogue_any(false);
+        if (s_last) {
+          __threadfence();  // the other parts were fenced before their counts
+          finish(from_slots);
+          if (threadIdx.x == 128) *ticket = 0;  // every part has counted in: ready for the next call
         }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) arrive_remote(in_cta(smem_u32(&tempty[buf]), 0));
     }
   }
   tc_fence_before();
@@ -407,14 +553,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (rank == 0 && threadIdx.x == 0) {
       int other;
       asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(other) : "r"(in_cta(smem_u32(&s_issued), 1)) : "memory");
+      const uint32_t half_bytes = kHalfBytes + (B_MN ? (hw > 64 ? kHalfBytes : kHalfBytes / 2) : (uint32_t)hw * kBlockK * 2);
       const int mine = s_issued, last = mine > other ? mine : other;
       for (int i = last > kStages ? last - kStages : 0; i < last; ++i) {
         uint64_t* bar = &full[i % kStages];
         if (i >= mine)
-          mbar_arrive_expect_tx(bar, kStageBytes);
+          mbar_arrive_expect_tx(bar, half_bytes);
         else if (i >= other)
           asm volatile("mbarrier.complete_tx.relaxed.cluster.shared::cluster.b64 [%0], %1;" ::"r"(smem_u32(bar)),
-                       "r"(kStageBytes)
+                       "r"(half_bytes)
                        : "memory");
         wait2(bar, (uint32_t)(i / kStages) & 1, kDrainLimit, nullptr);
       }
@@ -427,35 +574,59 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 // ------------------------------------------------------------------ gradients of g and u
-// dgu[m, i] = dg, dgu[m, I + i] = du from dh and the checkpoint, eight columns per thread.  One
-// pass over memory: reads dh and the checkpoint, writes 4 bytes per output.
+// dgu[m, i] = dg, dgu[m, I + i] = du from dh and the checkpoint, eight columns of kGradRows rows
+// per thread (their loads go out together).  One pass over memory: reads dh and the checkpoint,
+// writes 4 bytes per output.
+constexpr int kGradRows = 4;
 template <bool INT8>
-__global__ void __launch_bounds__(256) gated_grad_kernel(const uint16_t* __restrict__ dh, int64_t ld_dh, int64_t M,
+__global__ void __launch_bounds__(128) gated_grad_kernel(const uint16_t* __restrict__ dh, int64_t ld_dh, int64_t M,
                                                          int I, const void* __restrict__ ckpt,
                                                          const float* __restrict__ scale, float alpha, float limit,
                                                          uint16_t* __restrict__ dgu) {
   const int64_t ipad = ckpt_pad(I);
-  const int i = (blockIdx.x * 256 + threadIdx.x) * 8;
+  const int i = (blockIdx.x * 128 + threadIdx.x) * 8;
   if (i >= I) return;
-  for (int64_t m = blockIdx.y; m < M; m += gridDim.y) {
-    const uint4 d = *reinterpret_cast<const uint4*>(dh + m * ld_dh + i);
-    float g[8], u[8];
-    if constexpr (INT8) {
-      const int8_t* ck = reinterpret_cast<const int8_t*>(ckpt) + m * 2 * ipad + i;
-      const float* s = scale + m * 2 * (ipad / 128) + (i >> 7);
-      ckpt_values8(*reinterpret_cast<const uint2*>(ck), s[0], g);
-      ckpt_values8(*reinterpret_cast<const uint2*>(ck + ipad), s[ipad / 128], u);
-    } else {
-      const uint16_t* ck = reinterpret_cast<const uint16_t*>(ckpt) + m * 2 * ipad + i;
-      bf16_values8(*reinterpret_cast<const uint4*>(ck), g);
-      bf16_values8(*reinterpret_cast<const uint4*>(ck + ipad), u);
-    }
-    float dv[8], dg[8], du[8];
-    bf16_values8(d, dv);
+  for (int64_t m0 = (int64_t)blockIdx.y * kGradRows; m0 < M; m0 += (int64_t)gridDim.y * kGradRows) {
+    uint4 d[kGradRows], kg[kGradRows], ku[kGradRows];
+    float sg[kGradRows], su[kGradRows];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) gated_grad(dv[j], g[j], u[j], alpha, limit, dg[j], du[j]);
-    store8(dgu + m * 2 * I + i, dg);
-    store8(dgu + m * 2 * I + I + i, du);
+    for (int r = 0; r < kGradRows; ++r) {
+      const int64_t m = min(m0 + r, M - 1);
+      d[r] = *reinterpret_cast<const uint4*>(dh + m * ld_dh + i);
+      if constexpr (INT8) {
+        const int8_t* ck = reinterpret_cast<const int8_t*>(ckpt) + m * 2 * ipad + i;
+        const uint2 a = *reinterpret_cast<const uint2*>(ck), b = *reinterpret_cast<const uint2*>(ck + ipad);
+        kg[r].x = a.x;
+        kg[r].y = a.y;
+        ku[r].x = b.x;
+        ku[r].y = b.y;
+        const float* s = scale + m * 2 * (ipad / 128) + (i >> 7);
+        sg[r] = s[0];
+        su[r] = s[ipad / 128];
+      } else {
+        const uint16_t* ck = reinterpret_cast<const uint16_t*>(ckpt) + m * 2 * ipad + i;
+        kg[r] = *reinterpret_cast<const uint4*>(ck);
+        ku[r] = *reinterpret_cast<const uint4*>(ck + ipad);
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < kGradRows; ++r) {
+      if (m0 + r >= M) break;
+      float g[8], u[8], dv[8], dg[8], du[8];
+      if constexpr (INT8) {
+        ckpt_values8(make_uint2(kg[r].x, kg[r].y), sg[r], g);
+        ckpt_values8(make_uint2(ku[r].x, ku[r].y), su[r], u);
+      } else {
+        bf16_values8(kg[r], g);
+        bf16_values8(ku[r], u);
+      }
+      bf16_values8(d[r], dv);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) gated_grad(dv[j], g[j], u[j], alpha, limit, dg[j], du[j]);
+      uint16_t* dst = dgu + (m0 + r) * 2 * I + i;
+      store8(dst, dg);
+      store8(dst + I, du);
+    }
   }
 }
 
@@ -488,28 +659,89 @@ bool bf16_map(CUtensorMap* m, const void* base, int64_t inner, int64_t outer, in
   return r == CUDA_SUCCESS;
 }
 
+// Tiles of a GEMM over the pairs: whole ones in turn, and the last round's cut along K where that is
+// shorter.  In steps of 64 K (0.38 us): a part takes nk / parts of them, storing it, and adding and
+// finishing all parts of a tile by one CTA about 6 + 5 * parts * width / 256.
+struct Cut {
+  int width, tiles_m, tiles_n, nk, whole, cut, parts;
+  int64_t cost;  // of the longest pair: steps of 64 K times (width + 64), see plan
+  size_t bytes() const { return (size_t)cut * parts * 2 * kSlotFloats * 4; }
+};
+constexpr int kPairs = kNumSMs / 2;
+Cut plan_width(int64_t rows, int64_t cols, int64_t K, int width, int outs) {
+  Cut c = {};
+  c.width = width;
+  c.tiles_m = (int)((rows + 255) / 256);
+  c.tiles_n = (int)((cols + outs - 1) / outs);
+  c.nk = (int)((K + kBlockK - 1) / kBlockK);
+  const int64_t tiles = (int64_t)c.tiles_m * c.tiles_n;
+  c.whole = (int)tiles;
+  const int rest = (int)(tiles % kPairs);
+  int64_t best = rest ? c.nk : 0;
+  for (int parts = 2; rest > 0 && parts * rest <= kPairs && parts <= c.nk; ++parts) {
+    const int64_t steps = (c.nk + parts - 1) / parts + 6 + 5 * parts * width / 256;
+    if (steps >= best) continue;
+    best = steps;
+    c.whole = (int)tiles - rest;
+    c.cut = rest;
+    c.parts = parts;
+  }
+  c.cost = (tiles / kPairs * c.nk + best) * (width + 64);
+  return c;
+}
+// Narrower tiles where they fill the rounds better (2048 x 2048 x 4096: 152 tiles of 224 columns in
+// two rounds against 128 of 256) or, with few tiles, put more SMs to work.  They load as much of A
+// for fewer columns: a step is taken as width + 64, and 4 % at least has to come of it.
+Cut plan(int64_t rows, int64_t cols, int64_t K, bool fwd, bool narrow) {
+  Cut c = plan_width(rows, cols, K, 256, fwd ? 128 : 256);
+  for (int width = 224; narrow && width >= 64; width -= 32) {
+    const Cut d = plan_width(rows, cols, K, width, fwd ? width / 2 : width);
+    if (d.cost * 25 < c.cost * 24) c = d;
+  }
+  return c;
+}
+// an int8 checkpoint's groups of 128 columns are whole tiles
+Cut plan_fwd(int64_t M, int64_t H, int64_t I, bool int8) { return plan(M, I, H, true, !int8); }
+Cut plan_dx(int64_t M, int64_t H, int64_t I) { return plan(M, H, 2 * I, false, true); }
+Cut plan_dw(int64_t M, int64_t H, int64_t I) { return plan(2 * I, H, M, false, true); }
+
 template <int MODE>
-cudaError_t run(const CUtensorMap& ta, const CUtensorMap& tb, Params& p, cudaStream_t st) {
-  p.tiles_m = (p.rows + 255) / 256;
-  p.tiles_n = MODE == FWD ? (p.cols + 127) / 128 : (p.cols + 255) / 256;
-  p.nk = (p.K + kBlockK - 1) / kBlockK;
+cudaError_t run(const CUtensorMap& ta, const CUtensorMap& tb, Params& p, const Cut& c, cudaStream_t st) {
+  p.width = c.width;
+  p.tiles_m = c.tiles_m;
+  p.tiles_n = c.tiles_n;
+  p.nk = c.nk;
+  p.whole = c.whole;
+  p.cut = c.cut;
+  p.parts = c.parts;
   static std::atomic<int> attr{0};
   if (!attr.load()) {
     const cudaError_t e = raise_smem_limit(ffn_gemm_kernel<MODE>);
     if (e != cudaSuccess) return e;
     attr.store(1);
   }
-  const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
-  const int pairs = (int)(tiles < kNumSMs / 2 ? tiles : kNumSMs / 2);
-  ffn_gemm_kernel<MODE><<<2 * pairs, kThreads, 1024 + kStages * kStageBytes, st>>>(ta, tb, p);
+  const int busy = c.whole > c.cut * c.parts ? c.whole : c.cut * c.parts;
+  const int pairs = busy < kPairs ? busy : kPairs;
+  ffn_gemm_kernel<MODE><<<2 * pairs, kThreads, 1024 + kStages * kStageBytes + 8 * kRowStage, st>>>(ta, tb, p);
   return cudaGetLastError();
 }
 
 }  // namespace
 
+size_t ffn_forward_slots(int64_t M, int64_t H, int64_t I) {
+  const size_t a = plan_fwd(M, H, I, false).bytes(), b = plan_fwd(M, H, I, true).bytes();
+  return a > b ? a : b;
+}
+size_t ffn_backward_slots(int64_t M, int64_t H, int64_t I) {
+  const size_t a = plan_dx(M, H, I).bytes(), b = plan_dw(M, H, I).bytes();
+  return a > b ? a : b;  // one GEMM after the other
+}
+
 cudaError_t launch_ffn_forward(const FfnForward& f, cudaStream_t st) {
   CUtensorMap ta, tb;
-  if (!bf16_map(&ta, f.x, f.H, f.M, f.ldx, 128) || !bf16_map(&tb, f.w13, f.H, 2 * f.I, f.ldw, 128))
+  const Cut c = plan_fwd(f.M, f.H, f.I, f.save == QL_SAVE_INT8);
+  if (!bf16_map(&ta, f.x, f.H, f.M, f.ldx, 128) ||
+      !bf16_map(&tb, f.w13, f.H, 2 * f.I, f.ldw, (uint32_t)(c.width / 2)))
     return cudaErrorInvalidValue;
   Params p = {};
   p.rows = (int)f.M;
@@ -525,16 +757,19 @@ cudaError_t launch_ffn_forward(const FfnForward& f, cudaStream_t st) {
   p.ckpt_scale = f.ckpt_scale;
   p.status = f.status;
   p.wait_limit = f.wait_limit;
-  return run<FWD>(ta, tb, p, st);
+  p.slots = f.slots;
+  p.tickets = f.tickets;
+  return run<FWD>(ta, tb, p, c, st);
 }
 
 cudaError_t launch_ffn_backward(const FfnBackward& b, cudaStream_t st) {
-  const dim3 grid((unsigned)((b.I + 2047) / 2048), (unsigned)(b.M < 32768 ? b.M : 32768));
+  const int64_t gy = (b.M + kGradRows - 1) / kGradRows;
+  const dim3 grid((unsigned)((b.I + 1023) / 1024), (unsigned)(gy < 32768 ? gy : 32768));
   if (b.save == QL_SAVE_INT8)
-    gated_grad_kernel<true><<<grid, 256, 0, st>>>(b.dh, b.ld_dh, b.M, (int)b.I, b.ckpt, b.ckpt_scale, b.alpha, b.limit,
+    gated_grad_kernel<true><<<grid, 128, 0, st>>>(b.dh, b.ld_dh, b.M, (int)b.I, b.ckpt, b.ckpt_scale, b.alpha, b.limit,
                                                   b.dgu);
   else
-    gated_grad_kernel<false><<<grid, 256, 0, st>>>(b.dh, b.ld_dh, b.M, (int)b.I, b.ckpt, nullptr, b.alpha, b.limit,
+    gated_grad_kernel<false><<<grid, 128, 0, st>>>(b.dh, b.ld_dh, b.M, (int)b.I, b.ckpt, nullptr, b.alpha, b.limit,
                                                    b.dgu);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
@@ -542,6 +777,8 @@ cudaError_t launch_ffn_backward(const FfnBackward& b, cudaStream_t st) {
   Params p = {};
   p.status = b.status;
   p.wait_limit = b.wait_limit;
+  p.slots = b.slots;
+  p.tickets = b.tickets;
   if (b.dx) {
     if (!bf16_map(&ta, b.dgu, 2 * b.I, b.M, 2 * b.I, 128) || !bf16_map(&tb, b.w13, b.H, 2 * b.I, b.ldw, 64))
       return cudaErrorInvalidValue;
@@ -550,7 +787,7 @@ cudaError_t launch_ffn_backward(const FfnBackward& b, cudaStream_t st) {
     p.K = (int)(2 * b.I);
     p.out = b.dx;
     p.ld_out = b.ld_dx;
-    e = run<DX>(ta, tb, p, st);
+    e = run<DX>(ta, tb, p, plan_dx(b.M, b.H, b.I), st);
     if (e != cudaSuccess) return e;
   }
   if (b.dw13) {
@@ -561,7 +798,7 @@ cudaError_t launch_ffn_backward(const FfnBackward& b, cudaStream_t st) {
     p.K = (int)b.M;
     p.out = b.dw13;
     p.ld_out = b.ld_dw;
-    e = run<DW>(ta, tb, p, st);
+    e = run<DW>(ta, tb, p, plan_dw(b.M, b.H, b.I), st);
   }
   return e;
 }

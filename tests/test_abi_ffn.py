@@ -75,6 +75,6 @@ def test_workspace_of_the_gated_block(lib):
     f = lib.ql_workspace_bytes
     f.restype = SZ
     f.argtypes = [C, I64, I64, I64, C, C]
-    assert f(7, 4096, 17408, 5120, 0, 0) == f(7, 1, 8, 8, 0, 0) >= 256 + (1 << 20)
+    assert f(7, 4096, 17408, 5120, 0, 0) >= f(7, 1, 8, 8, 0, 0) >= 256 + (1 << 20)
     assert f(8, 4096, 17408, 5120, 0, 0) >= 256 + (1 << 20) + 4096 * 2 * 17408 * 2
     assert f(8, -1, 8, 8, 0, 0) == 0

@@ -120,6 +120,23 @@ def test_checkpoint_and_backward(ql, M, H, I, save):
     check_backward(dx, dw, dh, x, w, *kept(saved, I))
 
 
+# tiles cut along K over pairs of CTAs: all of them (few tiles), the last ones after whole rounds, in
+# the forward (with either checkpoint), dx (K = 2I) and dw (K = tokens)
+@pytest.mark.parametrize("save", ["bf16", "int8"])
+@pytest.mark.parametrize("M,H,I", [(300, 2048, 1024), (2000, 512, 520), (300, 512, 4096), (4096, 1600, 1400)])
+def test_cut_tiles(ql, M, H, I, save):
+    x, w, dh = make(M, H, I, seed=M + 2)
+    h, saved = ql.gated_ffn(x, w, save=save)
+    check_h(h, *forward_reference(x, w, I), H)
+    dx, dw = ql.gated_ffn_backward(dh, x, w, saved)
+    check_backward(dx, dw, dh, x, w, *kept(saved, I))
+    for _ in range(3):  # the order of a sum does not depend on who finishes last
+        h2, saved2 = ql.gated_ffn(x, w, save=save)
+        dx2, dw2 = ql.gated_ffn_backward(dh, x, w, saved2)
+        assert torch.equal(h2, h) and torch.equal(saved2.data[:, :, :I], saved.data[:, :, :I])
+        assert torch.equal(dx2, dx) and torch.equal(dw2, dw)
+
+
 @pytest.mark.parametrize("alpha,limit", [(1.0, 0.8), (1.7, 1.5), (-1.0, None), (1.0, 0.0)])
 @pytest.mark.parametrize("M", [9, 65])
 def test_activation_parameters(ql, M, alpha, limit):
@@ -305,6 +322,7 @@ def test_timeout_is_reported_and_recoverable(ql):
     finally:
         ql.set_wait_limit(1 << 20)
     assert seen and st != 0
+    ws.buf.zero_()  # tickets may be left mid-count: the workspace is initialised again
     h, s = ql.gated_ffn(x, w, save="bf16", workspace=ws)
     dx, dw = ql.gated_ffn_backward(dh, x, w, s, workspace=ws)
     torch.cuda.synchronize()
