@@ -393,7 +393,7 @@ QL_API ql_status qlinear_int4(const uint16_t* x, int64_t M, int64_t K, int64_t l
  * [M, 2, P] and ckpt_scale fp32 [M, 2, P/128], per token and 128 columns
  *   scale = max|v| / 127,  code = round_half_even(v / scale)  (scale 0 where max|v| < 2^-100;
  * an infinity or a NaN in a group reads back as NaN throughout it).  Columns I..P are
- * undefined.  h does not depend on save.
+ * undefined.
  * Paths: M <= 32 without a checkpoint: a skinny launch that streams the weights once; else one
  *        tcgen05 GEMM whose epilogue applies the activation and writes h and the checkpoint.
  * Requires: 1 <= M <= 2^22, H and I multiples of 8, at most 2^20, ldx >= H, ldw >= H, ldh >= I,

@@ -36,6 +36,7 @@
 #include <atomic>
 #include <cstdio>
 #include <mutex>
+#include <utility>
 
 #include "common.cuh"
 #include "ffn.h"
@@ -234,10 +235,10 @@ __device__ __forceinline__ bool epilogue_any(bool bad) {
   return r != 0;
 }
 
+// one GEMM on `pairs` pairs of CTAs, of which this is number `pair`
 template <int MODE>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    ffn_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                    const __grid_constant__ Params p) {
+__device__ __forceinline__ void gemm(const CUtensorMap& tmA, const CUtensorMap& tmB, const Params& p, int pair,
+                                     int pairs) {
   constexpr bool A_MN = MODE == DW, B_MN = MODE != FWD;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t full[kStages], empty[kStages], tfull[2], tempty[2], done;
@@ -250,7 +251,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   // the stages start at the same offset in both CTAs
   const uint32_t base = (smem_u32(smem_raw) + 1023) & ~1023u;
   const int hw = p.width / 2;  // columns of B in each CTA; FWD: outputs of a tile
-  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   const uint32_t lim = p.wait_limit;
   volatile int* abort = &s_abort;
 
@@ -279,6 +279,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   __syncthreads();
   cluster_sync_all();
   tc_fence_after();
+  // up to here nothing of the launch before is read or written: this part runs while it ends
+  pdl_wait();
+  pdl_launch_dependents();
   const uint32_t tmem = s_tmem;
   auto fail = [&]() {
     atomicOr(p.status, (uint32_t)QL_DEV_TIMEOUT);
@@ -573,6 +576,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
 }
 
+template <int MODE>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    ffn_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                    const __grid_constant__ Params p) {
+  gemm<MODE>(tmA, tmB, p, blockIdx.x >> 1, gridDim.x >> 1);
+}
+// dx and dW13 side by side: the first dx_pairs pairs take dx
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    ffn_gemms_kernel(const __grid_constant__ CUtensorMap dxA, const __grid_constant__ CUtensorMap dxB,
+                     const __grid_constant__ CUtensorMap dwA, const __grid_constant__ CUtensorMap dwB,
+                     const __grid_constant__ Params dx, const __grid_constant__ Params dw, int dx_pairs) {
+  const int pair = blockIdx.x >> 1;
+  if (pair < dx_pairs)
+    gemm<DX>(dxA, dxB, dx, pair, dx_pairs);
+  else
+    gemm<DW>(dwA, dwB, dw, pair - dx_pairs, (gridDim.x >> 1) - dx_pairs);
+}
+
 // ------------------------------------------------------------------ gradients of g and u
 // dgu[m, i] = dg, dgu[m, I + i] = du from dh and the checkpoint, eight columns of kGradRows rows
 // per thread (their loads go out together).  One pass over memory: reads dh and the checkpoint,
@@ -583,6 +604,8 @@ __global__ void __launch_bounds__(128) gated_grad_kernel(const uint16_t* __restr
                                                          int I, const void* __restrict__ ckpt,
                                                          const float* __restrict__ scale, float alpha, float limit,
                                                          uint16_t* __restrict__ dgu) {
+  pdl_launch_dependents();
+  pdl_wait();
   const int64_t ipad = ckpt_pad(I);
   const int i = (blockIdx.x * 128 + threadIdx.x) * 8;
   if (i >= I) return;
@@ -668,7 +691,7 @@ struct Cut {
   size_t bytes() const { return (size_t)cut * parts * 2 * kSlotFloats * 4; }
 };
 constexpr int kPairs = kNumSMs / 2;
-Cut plan_width(int64_t rows, int64_t cols, int64_t K, int width, int outs) {
+Cut plan_width(int64_t rows, int64_t cols, int64_t K, int width, int outs, int pairs) {
   Cut c = {};
   c.width = width;
   c.tiles_m = (int)((rows + 255) / 256);
@@ -676,9 +699,9 @@ Cut plan_width(int64_t rows, int64_t cols, int64_t K, int width, int outs) {
   c.nk = (int)((K + kBlockK - 1) / kBlockK);
   const int64_t tiles = (int64_t)c.tiles_m * c.tiles_n;
   c.whole = (int)tiles;
-  const int rest = (int)(tiles % kPairs);
+  const int rest = (int)(tiles % pairs);
   int64_t best = rest ? c.nk : 0;
-  for (int parts = 2; rest > 0 && parts * rest <= kPairs && parts <= c.nk; ++parts) {
+  for (int parts = 2; rest > 0 && parts * rest <= pairs && parts <= c.nk && parts <= 8; ++parts) {
     const int64_t steps = (c.nk + parts - 1) / parts + 6 + 5 * parts * width / 256;
     if (steps >= best) continue;
     best = steps;
@@ -686,27 +709,54 @@ Cut plan_width(int64_t rows, int64_t cols, int64_t K, int width, int outs) {
     c.cut = rest;
     c.parts = parts;
   }
-  c.cost = (tiles / kPairs * c.nk + best) * (width + 64);
+  c.cost = (tiles / pairs * c.nk + best) * (width + 64);
   return c;
 }
 // Narrower tiles where they fill the rounds better (2048 x 2048 x 4096: 152 tiles of 224 columns in
 // two rounds against 128 of 256) or, with few tiles, put more SMs to work.  They load as much of A
 // for fewer columns: a step is taken as width + 64, and 4 % at least has to come of it.
-Cut plan(int64_t rows, int64_t cols, int64_t K, bool fwd, bool narrow) {
-  Cut c = plan_width(rows, cols, K, 256, fwd ? 128 : 256);
+Cut plan(int64_t rows, int64_t cols, int64_t K, bool fwd, bool narrow, int pairs = kPairs) {
+  Cut c = plan_width(rows, cols, K, 256, fwd ? 128 : 256, pairs);
   for (int width = 224; narrow && width >= 64; width -= 32) {
-    const Cut d = plan_width(rows, cols, K, width, fwd ? width / 2 : width);
+    const Cut d = plan_width(rows, cols, K, width, fwd ? width / 2 : width, pairs);
     if (d.cost * 25 < c.cost * 24) c = d;
   }
   return c;
 }
 // an int8 checkpoint's groups of 128 columns are whole tiles
 Cut plan_fwd(int64_t M, int64_t H, int64_t I, bool int8) { return plan(M, I, H, true, !int8); }
-Cut plan_dx(int64_t M, int64_t H, int64_t I) { return plan(M, H, 2 * I, false, true); }
-Cut plan_dw(int64_t M, int64_t H, int64_t I) { return plan(2 * I, H, M, false, true); }
+Cut plan_dx(int64_t M, int64_t H, int64_t I, int pairs = kPairs) { return plan(M, H, 2 * I, false, true, pairs); }
+Cut plan_dw(int64_t M, int64_t H, int64_t I, int pairs = kPairs) { return plan(2 * I, H, M, false, true, pairs); }
 
-template <int MODE>
-cudaError_t run(const CUtensorMap& ta, const CUtensorMap& tb, Params& p, const Cut& c, cudaStream_t st) {
+// Both gradients in one launch, the pairs shared between them by their work, where neither fills
+// the pairs for long: short GEMMs leave them idle at their ends, and a launch is saved.  Past a few
+// rounds the two would only take L2 from each other.
+struct Both {
+  int dx_pairs;  // 0: one GEMM after the other
+  Cut dx, dw;
+};
+Both plan_both(int64_t M, int64_t H, int64_t I) {
+  Both b = {0, plan_dx(M, H, I), plan_dw(M, H, I)};
+  const int64_t w0 = (int64_t)b.dx.tiles_m * b.dx.tiles_n * b.dx.nk * b.dx.width;
+  const int64_t w1 = (int64_t)b.dw.tiles_m * b.dw.tiles_n * b.dw.nk * b.dw.width;
+  if (w0 + w1 > (int64_t)8 * kPairs * 64 * 256) return b;  // eight rounds of 64 steps
+  int64_t best = b.dx.cost + b.dw.cost + 8 * 320;  // a launch and a pipeline's start: about 8 steps
+  const int share = (int)(w0 * kPairs / (w0 + w1));
+  for (int d = -6; d <= 14; d += 4) {
+    const int n = share + d;
+    if (n < 1 || n >= kPairs) continue;
+    const Cut x = plan_dx(M, H, I, n), w = plan_dw(M, H, I, kPairs - n);
+    const int64_t cost = x.cost > w.cost ? x.cost : w.cost;
+    if (cost >= best) continue;
+    best = cost;
+    b.dx_pairs = n;
+    b.dx = x;
+    b.dw = w;
+  }
+  return b;
+}
+
+void take(Params& p, const Cut& c) {
   p.width = c.width;
   p.tiles_m = c.tiles_m;
   p.tiles_n = c.tiles_n;
@@ -714,6 +764,27 @@ cudaError_t run(const CUtensorMap& ta, const CUtensorMap& tb, Params& p, const C
   p.whole = c.whole;
   p.cut = c.cut;
   p.parts = c.parts;
+}
+
+template <class... P, class... A>
+cudaError_t launch_pdl(void (*kfn)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, A&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kfn, std::forward<A>(args)...);
+}
+constexpr size_t kSmem = 1024 + kStages * kStageBytes + 8 * kRowStage;
+
+template <int MODE>
+cudaError_t run(const CUtensorMap& ta, const CUtensorMap& tb, Params& p, const Cut& c, cudaStream_t st) {
+  take(p, c);
   static std::atomic<int> attr{0};
   if (!attr.load()) {
     const cudaError_t e = raise_smem_limit(ffn_gemm_kernel<MODE>);
@@ -721,9 +792,7 @@ cudaError_t run(const CUtensorMap& ta, const CUtensorMap& tb, Params& p, const C
     attr.store(1);
   }
   const int busy = c.whole > c.cut * c.parts ? c.whole : c.cut * c.parts;
-  const int pairs = busy < kPairs ? busy : kPairs;
-  ffn_gemm_kernel<MODE><<<2 * pairs, kThreads, 1024 + kStages * kStageBytes + 8 * kRowStage, st>>>(ta, tb, p);
-  return cudaGetLastError();
+  return launch_pdl(ffn_gemm_kernel<MODE>, dim3(2 * (busy < kPairs ? busy : kPairs)), kThreads, kSmem, st, ta, tb, p);
 }
 
 }  // namespace
@@ -733,8 +802,11 @@ size_t ffn_forward_slots(int64_t M, int64_t H, int64_t I) {
   return a > b ? a : b;
 }
 size_t ffn_backward_slots(int64_t M, int64_t H, int64_t I) {
+  // dx and dW13 alone, one after the other, or together
   const size_t a = plan_dx(M, H, I).bytes(), b = plan_dw(M, H, I).bytes();
-  return a > b ? a : b;  // one GEMM after the other
+  const Both both = plan_both(M, H, I);
+  const size_t c = both.dx_pairs ? both.dx.bytes() + both.dw.bytes() : 0;
+  return a > b ? (a > c ? a : c) : (b > c ? b : c);
 }
 
 cudaError_t launch_ffn_forward(const FfnForward& f, cudaStream_t st) {
@@ -765,42 +837,52 @@ cudaError_t launch_ffn_forward(const FfnForward& f, cudaStream_t st) {
 cudaError_t launch_ffn_backward(const FfnBackward& b, cudaStream_t st) {
   const int64_t gy = (b.M + kGradRows - 1) / kGradRows;
   const dim3 grid((unsigned)((b.I + 1023) / 1024), (unsigned)(gy < 32768 ? gy : 32768));
-  if (b.save == QL_SAVE_INT8)
-    gated_grad_kernel<true><<<grid, 128, 0, st>>>(b.dh, b.ld_dh, b.M, (int)b.I, b.ckpt, b.ckpt_scale, b.alpha, b.limit,
-                                                  b.dgu);
-  else
-    gated_grad_kernel<false><<<grid, 128, 0, st>>>(b.dh, b.ld_dh, b.M, (int)b.I, b.ckpt, nullptr, b.alpha, b.limit,
-                                                   b.dgu);
-  cudaError_t e = cudaGetLastError();
+  const float* scale = b.save == QL_SAVE_INT8 ? b.ckpt_scale : nullptr;
+  cudaError_t e = launch_pdl(b.save == QL_SAVE_INT8 ? gated_grad_kernel<true> : gated_grad_kernel<false>, grid, 128, 0,
+                             st, b.dh, b.ld_dh, b.M, (int)b.I, b.ckpt, scale, b.alpha, b.limit, b.dgu);
   if (e != cudaSuccess) return e;
-  CUtensorMap ta, tb;
-  Params p = {};
-  p.status = b.status;
-  p.wait_limit = b.wait_limit;
-  p.slots = b.slots;
-  p.tickets = b.tickets;
+  CUtensorMap xa, xb, wa, wb;
+  Params x = {}, w = {};
+  x.status = w.status = b.status;
+  x.wait_limit = w.wait_limit = b.wait_limit;
+  x.slots = w.slots = b.slots;
+  x.tickets = w.tickets = b.tickets;
   if (b.dx) {
-    if (!bf16_map(&ta, b.dgu, 2 * b.I, b.M, 2 * b.I, 128) || !bf16_map(&tb, b.w13, b.H, 2 * b.I, b.ldw, 64))
+    if (!bf16_map(&xa, b.dgu, 2 * b.I, b.M, 2 * b.I, 128) || !bf16_map(&xb, b.w13, b.H, 2 * b.I, b.ldw, 64))
       return cudaErrorInvalidValue;
-    p.rows = (int)b.M;
-    p.cols = (int)b.H;
-    p.K = (int)(2 * b.I);
-    p.out = b.dx;
-    p.ld_out = b.ld_dx;
-    e = run<DX>(ta, tb, p, plan_dx(b.M, b.H, b.I), st);
-    if (e != cudaSuccess) return e;
+    x.rows = (int)b.M;
+    x.cols = (int)b.H;
+    x.K = (int)(2 * b.I);
+    x.out = b.dx;
+    x.ld_out = b.ld_dx;
   }
   if (b.dw13) {
-    if (!bf16_map(&ta, b.dgu, 2 * b.I, b.M, 2 * b.I, 64) || !bf16_map(&tb, b.x, b.H, b.M, b.ldx, 64))
+    if (!bf16_map(&wa, b.dgu, 2 * b.I, b.M, 2 * b.I, 64) || !bf16_map(&wb, b.x, b.H, b.M, b.ldx, 64))
       return cudaErrorInvalidValue;
-    p.rows = (int)(2 * b.I);
-    p.cols = (int)b.H;
-    p.K = (int)b.M;
-    p.out = b.dw13;
-    p.ld_out = b.ld_dw;
-    e = run<DW>(ta, tb, p, plan_dw(b.M, b.H, b.I), st);
+    w.rows = (int)(2 * b.I);
+    w.cols = (int)b.H;
+    w.K = (int)b.M;
+    w.out = b.dw13;
+    w.ld_out = b.ld_dw;
   }
-  return e;
+  if (!b.dw13) return run<DX>(xa, xb, x, plan_dx(b.M, b.H, b.I), st);
+  if (!b.dx) return run<DW>(wa, wb, w, plan_dw(b.M, b.H, b.I), st);
+  const Both both = plan_both(b.M, b.H, b.I);
+  if (!both.dx_pairs) {
+    e = run<DX>(xa, xb, x, both.dx, st);
+    return e != cudaSuccess ? e : run<DW>(wa, wb, w, both.dw, st);
+  }
+  take(x, both.dx);
+  take(w, both.dw);
+  w.slots += both.dx.bytes() / sizeof(float);
+  w.tickets += 2 * kPairs;
+  static std::atomic<int> attr{0};
+  if (!attr.load()) {
+    e = raise_smem_limit(ffn_gemms_kernel);
+    if (e != cudaSuccess) return e;
+    attr.store(1);
+  }
+  return launch_pdl(ffn_gemms_kernel, dim3(2 * kPairs), kThreads, kSmem, st, xa, xb, wa, wb, x, w, both.dx_pairs);
 }
 
 }  // namespace tc
