@@ -24,6 +24,7 @@ constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kDepth = 4;        // blocks in a warp's ring
 constexpr int kBlockK = 32;      // k per block
+constexpr int kPrefetch = 2;  // blocks
 constexpr int kOut = 16;         // outputs of a CTA
 constexpr uint32_t kBlock = 4 * 512;  // a warp's bytes per block: 32 rows of 64
 
@@ -40,6 +41,7 @@ __device__ __forceinline__ uint4 lds16(uint32_t a) {
   asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
   return v;
 }
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -95,6 +97,13 @@ __global__ void __launch_bounds__(kThreads) ffn_skinny_kernel(const __grid_const
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
+  // Before the wait for the launch before, nothing is read or written but L2 is asked for the first
+  // blocks' rows (a prefetch only moves them there): a row per lane
+  if (n0 + lane % kOut < a.N) {
+    const uint8_t* row = a.w + ((lane >= kOut ? (int64_t)a.N : 0) + n0 + lane % kOut) * a.ldw_bytes;
+    for (int d = 0, b = b0; d < kPrefetch && b < nblk; ++d, b += bstep) prefetch_l2(row + (int64_t)b * 64);
+  }
+  pdl_wait();
 #pragma unroll
   for (int d = 0; d < kDepth - 1; ++d) fetch(d);
 
@@ -133,6 +142,7 @@ __global__ void __launch_bounds__(kThreads) ffn_skinny_kernel(const __grid_const
       }
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
+  pdl_launch_dependents();  // the next launch may take the places that become free
 
   // every warp leaves its sums in its own part of the ring (its copies have landed and are read).
   // Accumulator i of lane (g, t): row g + 8 (i >> 1), token 2t + (i & 1)
@@ -198,13 +208,15 @@ cudaError_t launch(const FfnSkinnyArgs& a, cudaStream_t st) {
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = kWarps * kDepth * kBlock;
   cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = 1;
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = (unsigned)ks;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = 1;
+  at[1].val.clusterDim.y = 1;
+  at[1].val.clusterDim.z = (unsigned)ks;
   cfg.attrs = at;
-  cfg.numAttrs = ks > 1 ? 1 : 0;
+  cfg.numAttrs = ks > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kfn, a);
 }
 

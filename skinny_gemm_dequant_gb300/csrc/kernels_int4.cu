@@ -40,6 +40,7 @@ constexpr int kBlockK = 128;
 // costs more than the loads it saves (5120 x 17408: 1 token 18.1 us staged, 23.1 not; 4 tokens 23.6
 // and 23.6; 8 tokens 34.9 and 25.4)
 constexpr int kStagedTokens = 4;
+constexpr int kPrefetch = 2;  // steps
 
 struct Plan {
   int rw_log2;  // warps of a CTA on different rows; the others split K
@@ -106,6 +107,7 @@ __device__ __forceinline__ uint32_t lds4(uint32_t a) {
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
   return v;
 }
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -171,6 +173,16 @@ __global__ void __launch_bounds__(W * 32) int4_kernel(const __grid_constant__ Ff
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
+  // Before the wait for the launch before, nothing is read or written but L2 is asked for the first
+  // steps' rows (a prefetch only moves them there): a row per lane
+  {
+    const int o = GATED ? lane % OUT : lane;
+    if (o < valid) {
+      const uint8_t* row = a.w + ((GATED && lane >= OUT ? (int64_t)a.N : 0) + n0 + o) * a.ldw_bytes;
+      for (int d = 0, b = c0 + wk * SB; d < kPrefetch && b < c1; ++d, b += kw * SB) prefetch_l2(row + (int64_t)b * 64);
+    }
+  }
+  pdl_wait();
   // activations of a chunk, one row of 16-byte pieces per token.  All CTAs read the same few lines
   // of L2, which serves a line's requests one after the other: whole lines are asked for (with
   // neighbouring lanes 64 bytes apart this took 5 us more at 1 x 17408 x 5120).  Piece 4 t + j of a
@@ -365,6 +377,9 @@ __global__ void __launch_bounds__(W * 32) int4_kernel(const __grid_constant__ Ff
     }
   }
 
+  // the next launch may take the places that become free (asked for earlier, its CTAs took places
+  // unevenly while this launch ran: 16 x 10240 x 5120 21.0 against 18.9 us)
+  pdl_launch_dependents();
   auto store = [&](float v, float u, int m, int n) {
     uint16_t yb;
     if constexpr (GATED) {
@@ -466,13 +481,15 @@ cudaError_t launch(const FfnSkinnyArgs& a, int rw_log2, cudaStream_t st) {
   cfg.blockDim = dim3(W * 32, 1, 1);
   cfg.dynamicSmemBytes = (size_t)W * kDepth * MT * 16 * SEG + p.x_bytes;
   cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = 1;
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = (unsigned)ks;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = 1;
+  at[1].val.clusterDim.y = 1;
+  at[1].val.clusterDim.z = (unsigned)ks;
   cfg.attrs = at;
-  cfg.numAttrs = ks > 1 ? 1 : 0;
+  cfg.numAttrs = ks > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kfn, a, p);
 }
 
