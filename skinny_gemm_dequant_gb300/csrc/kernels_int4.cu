@@ -452,7 +452,10 @@ cudaError_t launch(const FfnSkinnyArgs& a, int rw_log2, cudaStream_t st) {
   auto* kfn = int4_kernel<GATED, MT, NT, FINE, ZP, XS, SEG, kDepth, W>;
   static std::atomic<int> attr{0};
   if (!attr.load()) {
-    const cudaError_t e = raise_smem_limit(kfn);
+    cudaError_t e = raise_smem_limit(kfn);
+    // activations read block by block live in L1: half of it (gated 8 x 17408 x 5120: 27.9 us, with
+    // all of it shared memory 29.9; staged activations want the shared memory: 22.2 against 25.6)
+    if (e == cudaSuccess && !XS) e = cudaFuncSetAttribute(kfn, cudaFuncAttributePreferredSharedMemoryCarveout, 50);
     if (e != cudaSuccess) return e;
     attr.store(1);
   }
@@ -461,10 +464,10 @@ cudaError_t launch(const FfnSkinnyArgs& a, int rw_log2, cudaStream_t st) {
   p.rw_log2 = rw_log2;
   const int out = (GATED ? MT * 8 : MT * 16) << rw_log2, kw = W >> rw_log2;
   const int64_t tiles = (int64_t)((a.N + out - 1) / out) * ((a.M + NT * 8 - 1) / (NT * 8));
-  // K over a cluster's CTAs while eight warps per SM are missing and every warp keeps four blocks or more
-  // (5120 x 17408, 1 token: 2 CTAs 18.1 us, 1: 26.8, 4: 19.4; 1024 x 8192: 8 CTAs 4.8 us, 1: 9.8)
+  // K over a cluster's CTAs while eight warps per SM are missing and every warp keeps four blocks or
+  // more (1 x 5120 x 17408: 2 CTAs 18.1 us, 1: 26.8, 4: 19.4; 16 x 4096 x 4096: 2: 10.6, 4: 15.4)
   int ks = 1;
-  while (ks < 8 && tiles * ks * W < 8 * kNumSMs && nblk >= kw * ks * 4) ks *= 2;
+  while (ks < 8 && tiles * ks * W < 8 * kNumSMs && nblk >= kw * ks * 8) ks *= 2;
   if constexpr (XS) {
     // the activations of the CTA's share of K, or of as many blocks of it as 32 KB hold
     constexpr int xb = (int)x_block(FINE);
