@@ -367,7 +367,8 @@ QL_API ql_status qlinear_int8_w8a8_noalloc(const uint16_t* x, int64_t M, int64_t
  *   y[m,n] = bf16( sum_k x[m,k] * w[n,k] )  then, if bias, y = bf16(y + bias[n])
  * q: codes 0..15 packed two per byte, element 2i in the LOW nibble of byte i, rows of
  * ldw_bytes; s: bf16 (QL_SCALE_BF16) or fp16 (QL_SCALE_FP16) bits [N, lds], lds >=
- * ceil(K/group); z: uint8 [N, ldz] holding 0..127, or NULL for 8 everywhere (symmetric codes);
+ * ceil(K/group), |s| < 2^122; z: uint8 [N, ldz] holding 0..127, or NULL for 8 everywhere (symmetric
+ * codes);
  * x: bf16 [M, ldx]; bias: nullable bf16 [N]; y: bf16 [M, ldy].  q - z is exact in bf16, its
  * products with x are exact in fp32 and every group's fp32 sum is multiplied by its scale once:
  * no weight is rounded.  Weights are streamed once per 32 tokens.
@@ -398,7 +399,8 @@ QL_API ql_status qlinear_int4(const uint16_t* x, int64_t M, int64_t K, int64_t l
  *        tcgen05 GEMM whose epilogue applies the activation and writes h and the checkpoint.
  * Requires: 1 <= M <= 2^22, H and I multiples of 8, at most 2^20, ldx >= H, ldw >= H, ldh >= I,
  * leading dimensions multiples of 8, 16-byte aligned x, w13, h and ckpt; alpha finite, limit >=
- * 0.  workspace: ql_workspace_bytes(QL_OP_GATED_FFN, M, I, H, 0, 0) bytes, zeroed once.
+ * 0.  workspace: ql_workspace_bytes(QL_OP_GATED_FFN, M, I, H, 0, 0) bytes, zeroed once, and again
+ * after a call that raised QL_DEV_TIMEOUT (its tickets may be left mid-count).
  */
 QL_API ql_status gated_ffn(const uint16_t* x, int64_t M, int64_t H, int64_t ldx, const uint16_t* w13, int64_t I,
                            int64_t ldw, float swiglu_alpha, float swiglu_limit, uint16_t* h, int64_t ldh, int save,

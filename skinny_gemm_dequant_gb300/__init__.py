@@ -353,9 +353,18 @@ def _int4_weights(K, sx, w, w_scale, w_zero, group):
     return N, ldw, lds, ldz, fmt
 
 
-def _out(out, M, N, x, name="out"):
+def _empty(shape, dtype, x, stream):
+    # an output belongs to the stream that writes it: memory of the current stream's pool may still
+    # be in use there
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=x.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=x.device)
+
+
+def _out(out, M, N, x, stream, name="out"):
     if out is None:
-        return torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+        return _empty((M, N), torch.bfloat16, x, stream)
     if out.dtype is not torch.bfloat16 or out.shape != (M, N) or out.stride(1) != 1:
         raise TypeError(f"{name} must be bfloat16 [{M}, {N}] with unit inner stride")
     return out
@@ -371,7 +380,7 @@ def qlinear_int4(x, w, w_scale, w_zero=None, bias=None, *, group=128, debug=Fals
     N, ldw, lds, ldz, fmt = _int4_weights(K, sx, w, w_scale, w_zero, group)
     if bias is not None and (bias.dtype is not torch.bfloat16 or bias.shape != (N,) or not bias.is_contiguous()):
         raise TypeError(f"bias must be bfloat16 [{N}]")
-    y = _out(out, M, N, x)
+    y = _out(out, M, N, x, stream)
     path = ctypes.c_int(0) if debug else None
     st = lib.qlinear_int4(x.data_ptr(), M, K, sx[0], w.data_ptr(), N, ldw, w_scale.data_ptr(), fmt, lds, _ptr(w_zero),
                           ldz, group, _ptr(bias), y.data_ptr(), N if out is None else y.stride(0), _stream(stream),
@@ -392,7 +401,7 @@ def gated_ffn_int4(x, w13, w_scale, w_zero=None, *, group=128, swiglu_alpha=1.0,
     if N & 1:
         raise ValueError("w13 must have an even number of rows (gate, then up)")
     I = N >> 1
-    h = _out(out, M, I, x)
+    h = _out(out, M, I, x, stream)
     path = ctypes.c_int(0) if debug else None
     st = lib.gated_ffn_int4(x.data_ptr(), M, H, sx[0], w13.data_ptr(), I, ldw, w_scale.data_ptr(), fmt, lds,
                             _ptr(w_zero), ldz, group, swiglu_alpha, _inf(swiglu_limit), h.data_ptr(),
@@ -413,6 +422,24 @@ class FFNCheckpoint(NamedTuple):
 
 
 _ffn_bytes = functools.lru_cache(maxsize=256)(workspace_bytes)
+_ffn_workspaces: dict = {}
+
+
+def _ffn_ws(device, op, M, I, H, stream, workspace):
+    """The caller's workspace, or one per device and stream (the current stream's handle if none is
+    given): calls on different streams do not share one.  Allocated from its stream's own pool."""
+    nbytes = _ffn_bytes(op, M, I, H)
+    if workspace is None:
+        key = (device.index, _stream(stream))
+        workspace = _ffn_workspaces.get(key)
+        if workspace is None:
+            workspace = _ffn_workspaces.setdefault(key, Workspace(device))
+    if stream is None or (workspace.buf is not None and workspace.buf.numel() >= nbytes):
+        return workspace.get(nbytes, stream)
+    with torch.cuda.stream(stream):
+        return workspace.get(nbytes, stream)
+
+
 _SAVE = {None: SAVE_NONE, "bf16": SAVE_BF16, "int8": SAVE_INT8}
 
 
@@ -437,15 +464,15 @@ def gated_ffn(x, w13, *, swiglu_alpha=1.0, swiglu_limit=None, save=None, debug=F
     M, H, I, ldx, ldw = _ffn_weights(x, w13)
     if save not in _SAVE:
         raise ValueError('save must be None, "bf16" or "int8"')
-    h = _out(out, M, I, x)
+    h = _out(out, M, I, x, stream)
     saved = data = scale = None
     if save is not None:
         P = -(-I // 128) * 128
-        data = torch.empty((M, 2, P), dtype=torch.bfloat16 if save == "bf16" else torch.int8, device=x.device)
+        data = _empty((M, 2, P), torch.bfloat16 if save == "bf16" else torch.int8, x, stream)
         if save == "int8":
-            scale = torch.empty((M, 2, P // 128), dtype=torch.float32, device=x.device)
+            scale = _empty((M, 2, P // 128), torch.float32, x, stream)
         saved = FFNCheckpoint(save, data, scale)
-    ws = _ws(x.device, _ffn_bytes(OP_GATED_FFN, M, I, H), stream, workspace)
+    ws = _ffn_ws(x.device, OP_GATED_FFN, M, I, H, stream, workspace)
     path = ctypes.c_int(0) if debug else None
     st = lib.gated_ffn(x.data_ptr(), M, H, ldx, w13.data_ptr(), I, ldw, swiglu_alpha, _inf(swiglu_limit), h.data_ptr(),
                        I if out is None else h.stride(0), _SAVE[save], _ptr(data), _ptr(scale), ws.data_ptr(),
@@ -476,9 +503,9 @@ def gated_ffn_backward(dh, x, w13, saved, *, swiglu_alpha=1.0, swiglu_limit=None
     if mode == "int8" and (scale is None or scale.shape != (M, 2, P // 128) or not scale.is_contiguous()
                            or scale.dtype is not torch.float32):
         raise ValueError("saved must be the FFNCheckpoint of this x and w13")
-    dx = _out(out_dx, M, H, x, "out_dx") if need_dx else None
-    dw = _out(out_dw, 2 * I, H, x, "out_dw") if need_dw else None
-    ws = _ws(x.device, _ffn_bytes(OP_GATED_FFN_BWD, M, I, H), stream, workspace)
+    dx = _out(out_dx, M, H, x, stream, "out_dx") if need_dx else None
+    dw = _out(out_dw, 2 * I, H, x, stream, "out_dw") if need_dw else None
+    ws = _ffn_ws(x.device, OP_GATED_FFN_BWD, M, I, H, stream, workspace)
     st = lib.gated_ffn_backward(dh.data_ptr(), dh.stride(0), x.data_ptr(), M, H, ldx, w13.data_ptr(), I, ldw,
                                 swiglu_alpha, _inf(swiglu_limit), _SAVE[mode], data.data_ptr(), _ptr(scale), _ptr(dx),
                                 0 if dx is None else dx.stride(0), _ptr(dw), 0 if dw is None else dw.stride(0),

@@ -394,8 +394,10 @@ size_t ql_workspace_bytes(int op, int64_t M, int64_t N, int64_t K, int E, int to
     case QL_OP_FP8_CHANNEL:
       return dense2_layout(FMT_F8E4C, Mc, N, K, 128).total;  // E4M3 and E5M2 lay out alike
     case QL_OP_GATED_FFN:
-      return kRegionsOff + tc::ffn_forward_slots(M, K, N);  // the status word, tickets; cut tiles' sums
     case QL_OP_GATED_FFN_BWD:
+      if (M < 1 || N < 1 || K < 1 || M > (1 << 22) || N > (1 << 20) || K > (1 << 20)) return kRegionsOff;  // refused
+      if (op == QL_OP_GATED_FFN)
+        return kRegionsOff + tc::ffn_forward_slots(M, K, N);  // the status word, tickets; cut tiles' sums
       return kRegionsOff + al256((size_t)M * 2 * N * 2) + tc::ffn_backward_slots(M, K, N);  // [dg du] first
     case QL_OP_MOE_MXFP4: {
       if (E <= 0 || topk <= 0) return 0;

@@ -252,6 +252,8 @@ __device__ __forceinline__ void gemm(const CUtensorMap& tmA, const CUtensorMap& 
   const uint32_t base = (smem_u32(smem_raw) + 1023) & ~1023u;
   const int hw = p.width / 2;  // columns of B in each CTA; FWD: outputs of a tile
   const uint32_t lim = p.wait_limit;
+  // the epilogue waits for a whole tile's K, the others for a step of it
+  const uint32_t lim_tile = (uint32_t)min((uint64_t)lim * (1 + p.nk / 512), (uint64_t)0xFFFFFFFEu);
   volatile int* abort = &s_abort;
 
   if (threadIdx.x == 0) {
@@ -396,7 +398,7 @@ __device__ __forceinline__ void gemm(const CUtensorMap& tmA, const CUtensorMap& 
       tile_at(p, t, tm, tn);
       const int buf = n & 1;
       int got = 0;
-      if (lane == 0) got = wait2(&tfull[buf], (uint32_t)(n >> 1) & 1, lim, abort);
+      if (lane == 0) got = wait2(&tfull[buf], (uint32_t)(n >> 1) & 1, lim_tile, abort);
       got = __shfl_sync(0xffffffffu, got, 0);
       if (!got && lane == 0) fail();
       if (epilogue_any(!got)) break;  // all eight warps or none: they meet at barriers below
@@ -739,7 +741,7 @@ Both plan_both(int64_t M, int64_t H, int64_t I) {
   Both b = {0, plan_dx(M, H, I), plan_dw(M, H, I)};
   const int64_t w0 = (int64_t)b.dx.tiles_m * b.dx.tiles_n * b.dx.nk * b.dx.width;
   const int64_t w1 = (int64_t)b.dw.tiles_m * b.dw.tiles_n * b.dw.nk * b.dw.width;
-  if (w0 + w1 > (int64_t)8 * kPairs * 64 * 256) return b;  // eight rounds of 64 steps
+  if (w0 + w1 < 1 || w0 + w1 > (int64_t)8 * kPairs * 64 * 256) return b;  // eight rounds of 64 steps
   int64_t best = b.dx.cost + b.dw.cost + 8 * 320;  // a launch and a pipeline's start: about 8 steps
   const int share = (int)(w0 * kPairs / (w0 + w1));
   for (int d = -6; d <= 14; d += 4) {

@@ -78,3 +78,6 @@ def test_workspace_of_the_gated_block(lib):
     assert f(7, 4096, 17408, 5120, 0, 0) >= f(7, 1, 8, 8, 0, 0) >= 256 + (1 << 20)
     assert f(8, 4096, 17408, 5120, 0, 0) >= 256 + (1 << 20) + 4096 * 2 * 17408 * 2
     assert f(8, -1, 8, 8, 0, 0) == 0
+    for op in (7, 8):  # sizes that the calls refuse: an answer all the same
+        for M, N, K in ((0, 8, 8), (8, 0, 8), (8, 8, 0), (0, 0, 0), (1 << 40, 8, 8), (8, 1 << 40, 1 << 40)):
+            assert f(op, M, N, K, 0, 0) >= 256 + (1 << 20)

@@ -276,6 +276,31 @@ def test_other_stream_and_graph(ql):
     assert torch.equal(hg, h0) and torch.equal(dxg, dx0) and torch.equal(dwg, dw0)
 
 
+def test_streams_do_not_share_a_workspace(ql):
+    """Backward passes on two streams, with the default workspaces, at the same time."""
+    sets = [make(300, 512, 264, seed=20 + i) for i in range(2)]
+    want = []
+    for x, w, dh in sets:
+        _, s = ql.gated_ffn(x, w, save="int8")
+        want.append(ql.gated_ffn_backward(dh, x, w, s))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    for explicit in (False, True):
+        got = [None, None]
+        for _ in range(10):
+            for i, ((x, w, dh), st) in enumerate(zip(sets, streams)):
+                if explicit:
+                    _, s = ql.gated_ffn(x, w, save="int8", stream=st)
+                    got[i] = ql.gated_ffn_backward(dh, x, w, s, stream=st)
+                else:
+                    with torch.cuda.stream(st):
+                        _, s = ql.gated_ffn(x, w, save="int8")
+                        got[i] = ql.gated_ffn_backward(dh, x, w, s)
+        torch.cuda.synchronize()
+        for (dx, dw), (rdx, rdw) in zip(got, want):
+            assert torch.equal(dx, rdx) and torch.equal(dw, rdw)
+
+
 def test_python_refusals(ql):
     x, w, dh = make(40, 64, 72)
     _, saved = ql.gated_ffn(x, w, save="int8")

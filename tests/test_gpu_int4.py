@@ -55,6 +55,37 @@ def test_int4_matches_the_definition(ql, M, N, K, group):
     check(y, *reference(x, w, s, z, K, group), K)
 
 
+def sampled(N, n=60):
+    return np.unique(np.concatenate([[0, 1, N // 2, N - 2, N - 1], np.random.default_rng(N).integers(0, N, n)]))
+
+
+# K shares over clusters of CTAs, activations staged in several pieces (up to 4 tokens) and read
+# block by block (more), rows for two CTAs per SM and more: every token, sampled rows
+@pytest.mark.parametrize("group,zeros", [(32, False), (64, True), (128, True), (512, False)])
+@pytest.mark.parametrize("M,N,K", [(1, 5000, 17408), (3, 5000, 17408), (4, 5000, 17376), (4, 96, 17408), (8, 640, 8224),
+                                   (16, 640, 8224), (24, 330, 4128), (2, 19500, 3232), (4, 19500, 3232)])
+def test_int4_large_sampled(ql, M, N, K, group, zeros):
+    x, w, s, z = make(M, N, K, group, zeros, torch.bfloat16, seed=N + M)
+    y = ql.qlinear_int4(x, w, s, z, group=group)
+    rows = torch.from_numpy(sampled(N)).cuda()
+    ref, absum = reference(x, w[rows], s[rows], None if z is None else z[rows], K, group)
+    check(y[:, rows].contiguous(), ref, absum, K)
+
+
+@pytest.mark.parametrize("group,zeros", [(64, True), (128, False)])
+@pytest.mark.parametrize("M,I,H", [(1, 9750, 3232), (4, 9750, 3232), (3, 1030, 8224), (12, 1030, 8224)])
+def test_gated_int4_large_sampled(ql, M, I, H, group, zeros):
+    x, w, s, z = make(M, 2 * I, H, group, zeros, torch.float16, seed=I + M)
+    h = ql.gated_ffn_int4(x, w, s, z, group=group)
+    o = sampled(I)
+    rows = torch.from_numpy(np.concatenate([o, I + o])).cuda()
+    gu, absum = reference(x, w[rows], s[rows], None if z is None else z[rows], H, group)
+    n = len(o)
+    g, u, G, U = gu[:, :n], gu[:, n:], absum[:, :n], absum[:, n:]
+    got = F.bf16_to_f64(bits_of(h[:, torch.from_numpy(o).cuda()].contiguous()))
+    assert np.all(np.abs(got - O.gated(g, u)) <= h_tol(g, u, G, U, H, 1.0, np.inf))
+
+
 @pytest.mark.parametrize("group", [32, 128])
 def test_int4_strides_bias_and_guard_columns(ql, group):
     M, N, K = 5, 70, 352
