@@ -261,6 +261,22 @@ __global__ void __launch_bounds__(W * 32) int4_kernel(const __grid_constant__ Ff
     x_from[nt] = a.x + (int64_t)(m0 + m) * a.ldx + (FINE ? t * 8 : t * 32);
   }
   const uint32_t negz8 = 0xBE00BE00u;  // bf16x2 of -8 / 64
+  // activations that are not staged.  Up to 8 tokens they are read a block ahead (8 x 5120 x 17408:
+  // 22.8 to 21.6 us); more would take the registers of a CTA (16 tokens: 30.1 to 44.8 us)
+  static_assert(XS || SB == 1, "one block per step");
+  uint4 x_next[XS ? 1 : NT][4];
+  auto x_load = [&](int b) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int k = b * kBlockK + j * (FINE ? 32 : 8);
+        x_next[nt][j] = make_uint4(0u, 0u, 0u, 0u);
+        if (b < c1 && k + (FINE ? t * 8 : t * 32) < a.K)
+          x_next[nt][j] = *reinterpret_cast<const uint4*>(x_from[nt] + k);
+      }
+  };
+  if constexpr (!XS && NT == 1) x_load(c0 + wk);
   uint32_t slot = 0;
   for (int q0 = c0; q0 < c1; q0 += XS ? p.chunk : c1 - c0) {
     const int q1 = XS ? min(q0 + p.chunk, c1) : c1;
@@ -277,18 +293,14 @@ __global__ void __launch_bounds__(W * 32) int4_kernel(const __grid_constant__ Ff
     }
 
     for (int b0 = q0 + wk * SB; b0 < q1; b0 += kw * SB) {
-      uint4 xr[XS ? 1 : SB][XS ? 1 : NT][4];  // before the wait for the weights: the latencies overlap
+      uint4 xr[XS ? 1 : NT][4];
       if constexpr (!XS) {
+        if constexpr (NT > 1) x_load(b0);  // before the wait for the weights: the latencies overlap
 #pragma unroll
-        for (int sb = 0; sb < SB; ++sb)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int k = (b0 + sb) * kBlockK + j * (FINE ? 32 : 8);
-              xr[sb][nt][j] = make_uint4(0u, 0u, 0u, 0u);
-              if (k + (FINE ? t * 8 : t * 32) < a.K) xr[sb][nt][j] = *reinterpret_cast<const uint4*>(x_from[nt] + k);
-            }
+          for (int j = 0; j < 4; ++j) xr[nt][j] = x_next[nt][j];
+        if constexpr (NT == 1) x_load(b0 + kw);
       }
       asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 2) : "memory");
       __syncwarp();  // every lane's copies of this step have landed, and the step before is read
@@ -349,7 +361,7 @@ __global__ void __launch_bounds__(W * 32) int4_kernel(const __grid_constant__ Ff
           uint4 bx[NT];
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
-            bx[nt] = XS ? lds16(xa[nt] + j * (FINE ? 64 : 16)) : pair_up(xr[XS ? 0 : sb][XS ? 0 : nt][j]);
+            bx[nt] = XS ? lds16(xa[nt] + j * (FINE ? 64 : 16)) : pair_up(xr[XS ? 0 : nt][j]);
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
             uint32_t q0v[4], q1v[4];
