@@ -223,6 +223,17 @@ __device__ __forceinline__ void store_rows(uint32_t stage, const uint32_t* w, ui
   __syncwarp();  // read before the next rows are put there
 }
 
+__device__ __forceinline__ void tmem_st_x32(uint32_t taddr, const float (&v)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]),
+      "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15]), "f"(v[16]), "f"(v[17]), "f"(v[18]),
+      "f"(v[19]), "f"(v[20]), "f"(v[21]), "f"(v[22]), "f"(v[23]), "f"(v[24]), "f"(v[25]), "f"(v[26]), "f"(v[27]),
+      "f"(v[28]), "f"(v[29]), "f"(v[30]), "f"(v[31])
+      : "memory");
+}
+
 // true in every epilogue thread if `bad` is true in one
 __device__ __forceinline__ bool epilogue_any(bool bad) {
   int r;
@@ -407,34 +418,18 @@ __device__ __forceinline__ void gemm(const CUtensorMap& tmA, const CUtensorMap& 
       const int row0 = row - lane, rows = min(32, p.rows - row0);  // this warp's rows that exist
       const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)buf * 256;
 
-      // 32 columns of the tile's sums: from tensor memory, or the parts' sum from the workspace
+      // a part's sums of this thread's row
       auto slot_of = [&](int part) {
         return p.slots + ((int64_t)((t - p.whole) * p.parts + part) * 2 + rank) * kSlotFloats + r * 4;
       };
-      auto from_tmem = [&](int c, float (&v)[32]) {
+      auto load = [&](int c, float (&v)[32]) {  // 32 columns of the tile's sums
         uint32_t u[32];
         tmem_ld_x32(acc + c, u);
         tmem_wait_ld();
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(u[i]);
       };
-      auto from_slots = [&](int c, float (&v)[32]) {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = 0.f;
-#pragma unroll 2
-        for (int j = 0; j < p.parts; ++j) {
-          const float* src = slot_of(j) + (int64_t)c * 128;
-#pragma unroll
-          for (int i = 0; i < 32; i += 4) {
-            const float4 f = __ldcg(reinterpret_cast<const float4*>(src + i * 128));
-            v[i] += f.x;
-            v[i + 1] += f.y;
-            v[i + 2] += f.z;
-            v[i + 3] += f.w;
-          }
-        }
-      };
-      auto finish = [&](auto load) {
+      auto finish = [&]() {
         if constexpr (MODE == FWD) {
           const int i0 = tn * hw, outs = min(hw, p.cols - i0);  // the tile's outputs
           float inv_g = 0.f, inv_u = 0.f;
@@ -520,19 +515,18 @@ __device__ __forceinline__ void gemm(const CUtensorMap& tmA, const CUtensorMap& 
       };
 
       if (k1 - k0 == p.nk) {
-        finish(from_tmem);
-        release();
+        finish();
       } else {
         float* dst = slot_of(pair / p.cut);
 #pragma unroll 1
         for (int c = 128 * half; c < min(128 * half + 128, p.width); c += 32) {
           float v[32];
-          from_tmem(c, v);
+          load(c, v);
+          if (row >= p.rows) continue;
 #pragma unroll
           for (int i = 0; i < 32; i += 4)
             __stcg(reinterpret_cast<float4*>(dst + (int64_t)(c + i) * 128), make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]));
         }
-        release();
         __threadfence();
         epilogue_any(false);  // every warp's part is stored and fenced
         unsigned* ticket = p.tickets + 2 * (t - p.whole) + rank;
@@ -540,10 +534,45 @@ __device__ __forceinline__ void gemm(const CUtensorMap& tmA, const CUtensorMap& 
         epilogue_any(false);
         if (s_last) {
           __threadfence();  // the other parts were fenced before their counts
-          finish(from_slots);
           if (threadIdx.x == 128) *ticket = 0;  // every part has counted in: ready for the next call
+          // the parts in the order of K, this CTA's own where it stands in it, back to tensor memory
+          const int mine = pair / p.cut;
+#pragma unroll 1
+          for (int c = 128 * half; c < min(128 * half + 128, p.width); c += 32) {
+            float v[32], own[32];
+            load(c, own);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = 0.f;
+#pragma unroll 1
+            for (int j = 0; j < p.parts; ++j) {
+              if (j == mine) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] += own[i];
+                continue;
+              }
+              const float* src = slot_of(j) + (int64_t)c * 128;
+              float4 f[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                f[i] = row < p.rows ? __ldcg(reinterpret_cast<const float4*>(src + i * 512)) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                v[4 * i] += f[i].x;
+                v[4 * i + 1] += f[i].y;
+                v[4 * i + 2] += f[i].z;
+                v[4 * i + 3] += f[i].w;
+              }
+            }
+            tmem_st_x32(acc + c, v);
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          epilogue_any(false);  // a row's other half of the columns is another warp's
+          tc_fence_after();
+          finish();
         }
       }
+      release();
     }
   }
   tc_fence_before();
@@ -693,6 +722,7 @@ struct Cut {
   size_t bytes() const { return (size_t)cut * parts * 2 * kSlotFloats * 4; }
 };
 constexpr int kPairs = kNumSMs / 2;
+constexpr int kTileSteps = 9;  // writing a tile out takes about as long as nine steps (3.4 us)
 Cut plan_width(int64_t rows, int64_t cols, int64_t K, int width, int outs, int pairs) {
   Cut c = {};
   c.width = width;
@@ -702,7 +732,8 @@ Cut plan_width(int64_t rows, int64_t cols, int64_t K, int width, int outs, int p
   const int64_t tiles = (int64_t)c.tiles_m * c.tiles_n;
   c.whole = (int)tiles;
   const int rest = (int)(tiles % pairs);
-  int64_t best = rest ? c.nk : 0;
+  const int whole_steps = c.nk > kTileSteps ? c.nk : kTileSteps;
+  int64_t best = rest ? whole_steps : 0;
   for (int parts = 2; rest > 0 && parts * rest <= pairs && parts <= c.nk && parts <= 8; ++parts) {
     const int64_t steps = (c.nk + parts - 1) / parts + 6 + 5 * parts * width / 256;
     if (steps >= best) continue;
@@ -711,7 +742,7 @@ Cut plan_width(int64_t rows, int64_t cols, int64_t K, int width, int outs, int p
     c.cut = rest;
     c.parts = parts;
   }
-  c.cost = (tiles / pairs * c.nk + best) * (width + 64);
+  c.cost = (tiles / pairs * whole_steps + best) * (width + 64);
   return c;
 }
 // Narrower tiles where they fill the rounds better (2048 x 2048 x 4096: 152 tiles of 224 columns in
@@ -739,8 +770,10 @@ struct Both {
 };
 Both plan_both(int64_t M, int64_t H, int64_t I) {
   Both b = {0, plan_dx(M, H, I), plan_dw(M, H, I)};
-  const int64_t w0 = (int64_t)b.dx.tiles_m * b.dx.tiles_n * b.dx.nk * b.dx.width;
-  const int64_t w1 = (int64_t)b.dw.tiles_m * b.dw.tiles_n * b.dw.nk * b.dw.width;
+  auto work = [](const Cut& c) {
+    return (int64_t)c.tiles_m * c.tiles_n * (c.nk > kTileSteps ? c.nk : kTileSteps) * c.width;
+  };
+  const int64_t w0 = work(b.dx), w1 = work(b.dw);
   if (w0 + w1 < 1 || w0 + w1 > (int64_t)8 * kPairs * 64 * 256) return b;  // eight rounds of 64 steps
   int64_t best = b.dx.cost + b.dw.cost + 8 * 320;  // a launch and a pipeline's start: about 8 steps
   const int share = (int)(w0 * kPairs / (w0 + w1));
