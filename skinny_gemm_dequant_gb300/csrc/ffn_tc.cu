@@ -29,6 +29,12 @@
 // waits for another pair.  Equal shares of all tiles of the last two rounds, which would leave no
 // pair idle, were slower (4096 x 17408 x 5120 dx: 1009 us against 956 us uncut): the pairs then
 // stand at different k and no longer find each other's operands in L2.
+// What bounds it: the tensor cores under the power cap in long calls (4096 tokens, 17408 x 5120:
+// forward 0.83 ms, dx 0.82 ms, dW13 0.81 ms, 1.76 to 1.81 PFLOP/s each alone; 1.69 PFLOP/s over a
+// step); the rounds' rest in middling ones (2048 x 2048 x 4096: 1.3 PFLOP/s); in short ones about
+// 7 us of fixed cost (launch, set-up, the first loads, the epilogue of the one tile) and the parts'
+// way through L2; the weights' HBM traffic for few tokens (64 x 17408 x 5120 forward 66 us, 5.4
+// TB/s) and the writing of dW13 (2.9 of 4.0 TB/s that a plain fill of memory reaches).
 // Every wait is bounded; one that runs out raises QL_DEV_TIMEOUT in the status word and the pair
 // leaves its loops, waits for copies and MMAs in flight and frees its tensor memory.
 #include <cudaTypedefs.h>
@@ -628,7 +634,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // ------------------------------------------------------------------ gradients of g and u
 // dgu[m, i] = dg, dgu[m, I + i] = du from dh and the checkpoint, eight columns of kGradRows rows
 // per thread (their loads go out together).  One pass over memory: reads dh and the checkpoint,
-// writes 4 bytes per output.
+// writes 4 bytes per output.  Bound by HBM: 4096 x 17408, int8 checkpoint, 570 MB in 104 us, 5.5
+// TB/s (126 us with one row per thread).
 constexpr int kGradRows = 4;
 template <bool INT8>
 __global__ void __launch_bounds__(128) gated_grad_kernel(const uint16_t* __restrict__ dh, int64_t ld_dh, int64_t M,

@@ -15,13 +15,14 @@
 // as long as both operands agree, so the codes stay in the order in which a word's nibbles come out
 // in pairs, and the activations are put in that order (pair_up).
 //
-// What bounds it: a block of 16 rows takes about 110 warp instructions, half of them on the ALU,
-// which takes one every two cycles: 4.5 us of 45 MB of weights at full rate, next to 6.6 us of HBM.
-// Measured on one GB300: 1 x 17408 x 5120 gated 23.6 us (3.9 TB/s), 1 x 5120 x 17408 18.1 us
-// (2.6 TB/s), 16 x 10240 x 5120 with groups of 32 19.7 us.  Two row tiles a warp against one: two
-// independent MMA chains, and the activations are read once for both (gated 28.2 to 23.6 us).
-// Scales read a step ahead and shared by shuffles: 2-byte loads per lane and block, waited for in
-// the block that reads them, took 11 us of 35.
+// What bounds it: a block of 16 rows takes about 130 warp instructions, half of them on the ALU,
+// which takes one every two cycles, from four or so warps per scheduler that each run a dependent
+// chain: with the loads taken out, 1 x 17408 x 5120 (gated) still takes 17.4 us; with the
+// arithmetic taken out 18.1 us; both together 22.7 us (4.1 TB/s; HBM alone 13.7).  1 x 5120 x 17408
+// 17.4 us (2.7 TB/s), 16 x 10240 x 5120 with groups of 32 18.0 us, of which the activations' loads
+// are 6.  Two row tiles a warp against one: two independent MMA chains, and the activations are
+// read once for both (28.2 to 23.6 us).  Scales a step ahead, shared by shuffles: 2-byte loads
+// waited for in the block that uses them took 11 us of 35.
 #include <cuda_fp16.h>
 
 #include <atomic>
