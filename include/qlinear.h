@@ -374,7 +374,7 @@ QL_API ql_status qlinear_int8_w8a8_noalloc(const uint16_t* x, int64_t M, int64_t
  * no weight is rounded.  Weights are streamed once per 32 tokens.
  * Requires: 1 <= M <= 65535, K % 32 == 0 (the last group may be short), group a power of two
  * >= 32 (a group >= K is one scale per row), ldx >= K, ldx % 8 == 0, ldw_bytes >= K/2,
- * ldw_bytes % 16 == 0, 16-byte aligned x and w, 2-byte aligned scales, ldy >= N.
+ * ldw_bytes % 16 == 0, 16-byte aligned x and w, 2-byte aligned scales, bias and y, ldy >= N.
  * Takes no workspace and waits on nothing inside the kernel.
  */
 QL_API ql_status qlinear_int4(const uint16_t* x, int64_t M, int64_t K, int64_t ldx, const uint8_t* w, int64_t N,
@@ -398,8 +398,8 @@ QL_API ql_status qlinear_int4(const uint16_t* x, int64_t M, int64_t K, int64_t l
  * Paths: M <= 32 without a checkpoint: a skinny launch that streams the weights once; else one
  *        tcgen05 GEMM whose epilogue applies the activation and writes h and the checkpoint.
  * Requires: 1 <= M <= 2^22, H and I multiples of 8, at most 2^20, ldx >= H, ldw >= H, ldh >= I,
- * leading dimensions multiples of 8, 16-byte aligned x, w13, h and ckpt; alpha finite, limit >=
- * 0.  workspace: ql_workspace_bytes(QL_OP_GATED_FFN, M, I, H, 0, 0) bytes, zeroed once, and again
+ * leading dimensions multiples of 8, 16-byte aligned x, w13, h and ckpt, 4-byte aligned ckpt_scale;
+ * alpha finite, limit >= 0.  workspace: ql_workspace_bytes(QL_OP_GATED_FFN, M, I, H, 0, 0) bytes, zeroed once, and again
  * after a call that raised QL_DEV_TIMEOUT (its tickets may be left mid-count).
  */
 QL_API ql_status gated_ffn(const uint16_t* x, int64_t M, int64_t H, int64_t ldx, const uint16_t* w13, int64_t I,

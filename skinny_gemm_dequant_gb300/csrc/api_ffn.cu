@@ -14,6 +14,7 @@ namespace {
 constexpr size_t kTicketOff = 256;  // the zero region of every workspace
 
 inline bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+inline bool al4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
 inline bool al2(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 1) == 0; }
 inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -36,7 +37,7 @@ ql_status int4_check(const uint16_t* x, int64_t M, int64_t K, int64_t ldx, const
   if (lds < cdiv(K, group) || (zero && ldz < cdiv(K, group))) return QL_ERR_INVALID_ARG;
   if (M > 65535 || rows > (1 << 30) || K > (1 << 28)) return QL_ERR_UNSUPPORTED;
   if (K % 32 != 0 || group < 32 || (group & (group - 1)) != 0 || group > (1 << 28)) return QL_ERR_UNSUPPORTED;
-  if (!al16(x) || !al16(w) || !al2(scale) || ldx % 8 != 0 || ldw_bytes % 16 != 0) return QL_ERR_ALIGNMENT;
+  if (!al16(x) || !al16(w) || !al2(scale) || !al2(y) || ldx % 8 != 0 || ldw_bytes % 16 != 0) return QL_ERR_ALIGNMENT;
   return QL_OK;
 }
 
@@ -81,6 +82,7 @@ ql_status qlinear_int4(const uint16_t* x, int64_t M, int64_t K, int64_t ldx, con
   if (path_out) *path_out = QL_PATH_NONE;
   const ql_status s = int4_check(x, M, K, ldx, w, N, N, ldw_bytes, w_scale, scale_fmt, lds, w_zero, ldz, group, y, ldy);
   if (s != QL_OK) return s;
+  if (!al2(bias)) return QL_ERR_ALIGNMENT;
   FfnSkinnyArgs a = int4_args(x, M, K, ldx, w, ldw_bytes, w_scale, scale_fmt, lds, w_zero, ldz, group, y, ldy);
   a.N = (int)N;
   a.bias = bias;
@@ -120,7 +122,7 @@ ql_status gated_ffn(const uint16_t* x, int64_t M, int64_t H, int64_t ldx, const 
   if (save == QL_SAVE_INT8 && !ckpt_scale) return QL_ERR_INVALID_ARG;
   const ql_status s = ffn_check(M, H, I, ldx, ldw, swiglu_alpha, swiglu_limit);
   if (s != QL_OK) return s;
-  if (!al16(x) || !al16(w13) || !al16(h) || !al16(ckpt) || ldh % 8 != 0) return QL_ERR_ALIGNMENT;
+  if (!al16(x) || !al16(w13) || !al16(h) || !al16(ckpt) || !al4(ckpt_scale) || ldh % 8 != 0) return QL_ERR_ALIGNMENT;
   if (!workspace || workspace_bytes < ql_workspace_bytes(QL_OP_GATED_FFN, M, I, H, 0, 0)) return QL_ERR_WORKSPACE;
   if (!al16(workspace)) return QL_ERR_ALIGNMENT;
   cudaStream_t st = (cudaStream_t)stream;
@@ -180,7 +182,7 @@ ql_status gated_ffn_backward(const uint16_t* dh, int64_t ld_dh, const uint16_t* 
   const ql_status s = ffn_check(M, H, I, dw13 ? ldx : (H + 7) / 8 * 8, dx ? ldw : (H + 7) / 8 * 8, swiglu_alpha,
                                 swiglu_limit);
   if (s != QL_OK) return s;
-  if (!al16(dh) || !al16(ckpt) || ld_dh % 8 != 0) return QL_ERR_ALIGNMENT;
+  if (!al16(dh) || !al16(ckpt) || !al4(ckpt_scale) || ld_dh % 8 != 0) return QL_ERR_ALIGNMENT;
   if (dx && (!al16(w13) || !al16(dx) || ld_dx % 8 != 0)) return QL_ERR_ALIGNMENT;
   if (dw13 && (!al16(x) || !al16(dw13) || ld_dw % 8 != 0)) return QL_ERR_ALIGNMENT;
   if (!workspace || workspace_bytes < ql_workspace_bytes(QL_OP_GATED_FFN_BWD, M, I, H, 0, 0)) return QL_ERR_WORKSPACE;

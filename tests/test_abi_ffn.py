@@ -56,7 +56,10 @@ CASES = ([("qlinear_int4", *c) for c in INT4] + [("gated_ffn_int4", *c) for c in
              (dict(dh=None), INVALID), (dict(dx=None, dw=None), INVALID), (dict(x=None), INVALID),
              (dict(w=None), INVALID), (dict(save=0), INVALID), (dict(ld_dh=56), INVALID), (dict(ld_dx=56), INVALID),
              (dict(ld_dw=56), INVALID), (dict(ld_dh=68), ALIGNMENT), (dict(ld_dx=68), ALIGNMENT),
-             (dict(ld_dw=68), ALIGNMENT), (dict(dh=8), ALIGNMENT), (dict(dx=8), ALIGNMENT), (dict(dw=8), ALIGNMENT)]])
+             (dict(ld_dw=68), ALIGNMENT), (dict(dh=8), ALIGNMENT), (dict(dx=8), ALIGNMENT), (dict(dw=8), ALIGNMENT)]]
+         + [("qlinear_int4", dict(y=17), ALIGNMENT), ("qlinear_int4", dict(bias=17), ALIGNMENT),
+            ("gated_ffn_int4", dict(y=17), ALIGNMENT), ("gated_ffn", dict(scale=18), ALIGNMENT),
+            ("gated_ffn_backward", dict(scale=18), ALIGNMENT)])
 
 
 @pytest.mark.parametrize("name,change,want", CASES, ids=[f"{n}-{'-'.join(f'{k}={v}' for k, v in c.items())}"
