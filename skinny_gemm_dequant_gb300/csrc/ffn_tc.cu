@@ -528,10 +528,12 @@ __device__ __forceinline__ void gemm(const CUtensorMap& tmA, const CUtensorMap& 
         for (int c = 128 * half; c < min(128 * half + 128, p.width); c += 32) {
           float v[32];
           load(c, v);
-          if (row >= p.rows) continue;
+          if (row < p.rows) {
 #pragma unroll
-          for (int i = 0; i < 32; i += 4)
-            __stcg(reinterpret_cast<float4*>(dst + (int64_t)(c + i) * 128), make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]));
+            for (int i = 0; i < 32; i += 4)
+              __stcg(reinterpret_cast<float4*>(dst + (int64_t)(c + i) * 128), make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]));
+          }
+          __syncwarp();  // the next read of tensor memory is the whole warp's
         }
         __threadfence();
         epilogue_any(false);  // every warp's part is stored and fenced
