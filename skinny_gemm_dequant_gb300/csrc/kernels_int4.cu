@@ -13,16 +13,17 @@
 // an output) and walks K in blocks of 128, 64 bytes of every row, through a ring of its own that it
 // fills with cp.async: warps need no barrier between them.  Which k an MMA slot stands for is free
 // as long as both operands agree, so the codes stay in the order in which a word's nibbles come out
-// in pairs, and the activations are put in that order (pair_up).
+// in pairs, and the activations are put in that order (pair_up).  The activations travel in the same
+// ring as the weights that meet them; one token of many rows is staged for a whole CTA instead.
 //
-// What bounds it: a block of 16 rows takes about 130 warp instructions, half of them on the ALU,
-// which takes one every two cycles, from four or so warps per scheduler that each run a dependent
+// What bounds it: a block of 16 rows takes about 150 warp instructions, half of them on the ALU,
+// which takes one every two cycles, from two to six warps per scheduler that each run a dependent
 // chain: with the loads taken out, 1 x 17408 x 5120 (gated) still takes 17.4 us; with the
-// arithmetic taken out 18.1 us; both together 22.7 us (4.1 TB/s; HBM alone 13.7).  1 x 5120 x 17408
-// 17.4 us (2.7 TB/s), 16 x 10240 x 5120 with groups of 32 18.0 us, of which the activations' loads
-// are 6.  Two row tiles a warp against one: two independent MMA chains, and the activations are
-// read once for both (28.2 to 23.6 us).  Scales a step ahead, shared by shuffles: 2-byte loads
-// waited for in the block that uses them took 11 us of 35.
+// arithmetic taken out 18.1 us; both together 22.5 us (4.2 TB/s; HBM alone 13.7).  1 x 5120 x 17408
+// 17.3 us (2.7 TB/s), 8 tokens 19.3; 16 x 10240 x 5120 with groups of 32 15.3 us.  Two row tiles a
+// warp against one: two independent MMA chains, and the activations are read once for both (28.2
+// to 23.6 us).  Scales a step ahead, shared by shuffles: 2-byte loads waited for in the block that
+// uses them took 11 us of 35.
 #include <cuda_fp16.h>
 
 #include <atomic>
@@ -37,19 +38,14 @@ namespace ql {
 namespace {
 
 constexpr int kBlockK = 128;
-// calls of up to this many tokens stage their activations in shared memory; with more the staging
-// costs more than the loads it saves (5120 x 17408: 1 token 18.1 us staged, 23.1 not; 4 tokens 23.6
-// and 23.6; 8 tokens 34.9 and 25.4)
-constexpr int kStagedTokens = 4;
 constexpr int kPrefetch = 2;  // steps
 
 struct Plan {
   int rw_log2;  // warps of a CTA on different rows; the others split K
-  int chunk;    // blocks of K whose activations are staged at a time
-  int x_pitch;  // bytes of a token's activations in shared memory
-  int x_bytes;  // of all tokens'
+  int chunk;    // staged activations: blocks of K at a time
+  int x_bytes;  // of them
 };
-// bytes of a token's block there
+// bytes of a block of staged activations
 __host__ __device__ constexpr uint32_t x_block(bool fine) { return fine ? 256 : 320; }
 
 // bf16 bit patterns below 256 are linear, pattern p has the value p 2^-133 (subnormals, then the
@@ -121,7 +117,8 @@ __device__ __forceinline__ float ld_cta(uint32_t saddr, uint32_t rank) {
 }
 
 // MT: 16-row tiles of a warp; NT: 8-token tiles; FINE: groups shorter than 128; ZP: zero points
-// given; SEG: bytes of a row that a step copies; kDepth: steps in a warp's ring; W: warps.
+// given; XS: one token, staged for the CTA, else the activations travel in the warps' rings;
+// SEG: bytes of a row that a step copies; kDepth: steps in a ring; W: warps.
 // gridDim.z CTAs (a cluster) take contiguous shares of K.
 template <bool GATED, int MT, int NT, bool FINE, bool ZP, bool XS, int SEG, int kDepth, int W>
 __global__ void __launch_bounds__(W * 32) int4_kernel(const __grid_constant__ FfnSkinnyArgs a, const Plan p) {
@@ -129,7 +126,9 @@ __global__ void __launch_bounds__(W * 32) int4_kernel(const __grid_constant__ Ff
   constexpr int TT = NT * 8, RT = MT * 16, OUT = GATED ? RT / 2 : RT, PITCH = TT + 1;
   constexpr int SB = SEG / 64;                   // blocks per step
   constexpr int LPR = SEG / 16, RPI = 32 / LPR;  // lanes per row, rows per copy instruction
-  constexpr uint32_t kStep = RT * SEG;           // a warp's bytes per step
+  constexpr uint32_t kX = RT * SEG;                   // weight bytes of a warp's step
+  constexpr uint32_t kStep = kX + (XS ? 0 : TT * 256);  // all of its bytes
+  static_assert(XS || SB == 1, "activations: one block per step");
   constexpr uint32_t XB = x_block(FINE);
   extern __shared__ __align__(128) uint8_t smem[];
   uint8_t* ring = smem + p.x_bytes;
@@ -153,6 +152,13 @@ __global__ void __launch_bounds__(W * 32) int4_kernel(const __grid_constant__ Ff
   const uint8_t* wp = a.w + (int64_t)(n0 + cr) * a.ldw_bytes + (int64_t)(c0 + wk * SB) * 64 + cc * 16;
   const int64_t rstep = (int64_t)RPI * a.ldw_bytes;
   const int64_t to_up = ((int64_t)a.N - OUT) * a.ldw_bytes;
+  // activations in the ring: a row of 16 pieces per token, lane = (row of two, piece).  Piece c of
+  // token m lies in slot c ^ h, FINE: h = 4 (m % 2), else h = c / 8 + 2 (m % 2): four lanes of a token
+  // and four of the next then meet every bank once.  Read where they are used, the loads took 6 of 18
+  // us at 16 x 10240 x 5120 (15.0 so; 8 x 5120 x 17408 21.6 to 19.2 us, 32 tokens 60 to 42 us)
+  const int xc = lane & 15, xm = lane >> 4;
+  const uint16_t* xq = a.x + (int64_t)(m0 + xm) * a.ldx + (int64_t)(c0 + wk * SB) * kBlockK + xc * 8;
+  const uint32_t x_dst = kX + (uint32_t)(xm * 256 + (xc ^ (FINE ? xm * 4 : (xc >> 3) + xm * 2)) * 16);
   int bf = c0 + wk * SB;  // first block of the next step to copy
   auto fetch = [&](uint32_t slot) {
     if (bf < c1) {
@@ -169,6 +175,16 @@ __global__ void __launch_bounds__(W * 32) int4_kernel(const __grid_constant__ Ff
         cp16((dst ^ flip) + i * RPI * SEG, src, in && (GATED && i * RPI >= OUT ? r - OUT : r) < valid);
         src += rstep;
       }
+      if constexpr (!XS) {
+        const uint16_t* xs = xq;
+        const bool in = bf * kBlockK + xc * 8 < a.K;
+#pragma unroll
+        for (int i = 0; i < TT / 2; ++i) {
+          cp16(mine + slot * kStep + x_dst + i * 512, xs, in && i * 2 + xm < toks);
+          xs += 2 * a.ldx;
+        }
+        xq += kw * kBlockK;
+      }
       wp += kw * SEG;
       bf += kw * SB;
     }
@@ -184,27 +200,23 @@ __global__ void __launch_bounds__(W * 32) int4_kernel(const __grid_constant__ Ff
     }
   }
   pdl_wait();
-  // activations of a chunk, one row of 16-byte pieces per token.  All CTAs read the same few lines
-  // of L2, which serves a line's requests one after the other: whole lines are asked for (with
-  // neighbouring lanes 64 bytes apart this took 5 us more at 1 x 17408 x 5120).  Piece 4 t + j of a
-  // block lies at 80 t + 16 j and the rows an odd multiple of 64 bytes apart, so that the four lanes
-  // of a token and the next token's four meet every bank once; FINE lanes read neighbouring pieces.
-  // Every thread then puts its own pieces in the order of the codes
+  // staged activations of a chunk.  All CTAs read the same few lines of L2, which serves a line's
+  // requests one after the other: whole lines are asked for (with neighbouring lanes 64 bytes apart
+  // this took 5 us more at 1 x 17408 x 5120).  Piece 4 t + j of a block lies at 80 t + 16 j, so that
+  // the four lanes meet every bank once; FINE lanes read neighbouring pieces.  Every thread then puts
+  // its own pieces in the order of the codes
   auto x_slot = [](int i) { return (uint32_t)(FINE ? i * 16 : (i >> 4) * XB + ((i >> 2) & 3) * 80 + (i & 3) * 16); };
   auto x_copy = [&](int q0, int q1) {
-    for (int m = 0; m < toks; ++m) {
-      const uint16_t* src = a.x + (int64_t)(m0 + m) * a.ldx + (int64_t)q0 * kBlockK;
-      for (int i = threadIdx.x; i < (q1 - q0) * 16; i += kThreads)
-        cp16(smem_addr(smem) + m * p.x_pitch + x_slot(i), src + i * 8, q0 * kBlockK + i * 8 < a.K);
-    }
+    const uint16_t* src = a.x + (int64_t)m0 * a.ldx + (int64_t)q0 * kBlockK;
+    for (int i = threadIdx.x; i < (q1 - q0) * 16; i += kThreads)
+      cp16(smem_addr(smem) + x_slot(i), src + i * 8, q0 * kBlockK + i * 8 < a.K);
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
   auto x_order = [&](int q0, int q1) {
-    for (int m = 0; m < toks; ++m)
-      for (int i = threadIdx.x; i < (q1 - q0) * 16; i += kThreads) {
-        uint4* at = reinterpret_cast<uint4*>(smem + m * p.x_pitch + x_slot(i));
-        *at = pair_up(*at);
-      }
+    for (int i = threadIdx.x; i < (q1 - q0) * 16; i += kThreads) {
+      uint4* at = reinterpret_cast<uint4*>(smem + x_slot(i));
+      *at = pair_up(*at);
+    }
   };
   if constexpr (XS) x_copy(c0, min(c0 + p.chunk, c1));
 #pragma unroll 1
@@ -237,7 +249,8 @@ __global__ void __launch_bounds__(W * 32) int4_kernel(const __grid_constant__ Ff
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          s_next[i][mt][h] = sp[mt][h][gi];
+          // (FINE: a group past the end has no scale, its sum of zeros stays zero)
+          s_next[i][mt][h] = FINE && k >= a.K ? (uint16_t)0 : sp[mt][h][gi];
           if (ZP) z_next[i][mt][h] = zp[mt][h][gi];
         }
     }
@@ -252,32 +265,11 @@ __global__ void __launch_bounds__(W * 32) int4_kernel(const __grid_constant__ Ff
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[mt][nt][i] = 0.f;
 
-  // this lane's token's pieces: of the chunk's first block in shared memory, or in global memory
-  uint32_t x_at[NT];
-  const uint16_t* x_from[NT];
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const int m = min(nt * 8 + g, toks - 1);
-    x_at[nt] = smem_addr(smem) + m * p.x_pitch + (FINE ? t * 16 : t * 80);
-    x_from[nt] = a.x + (int64_t)(m0 + m) * a.ldx + (FINE ? t * 8 : t * 32);
-  }
+  // this lane's pieces of its token: staged (every lane of a row of the MMA reads the one token), or
+  // in a ring's slot
+  const uint32_t x_at = smem_addr(smem) + (uint32_t)(FINE ? t * 16 : t * 80);
+  const uint32_t x_src = (uint32_t)((FINE ? t ^ (g & 1) << 2 : t * 4 ^ (t >> 1 | (g & 1) << 1)) * 16);
   const uint32_t negz8 = 0xBE00BE00u;  // bf16x2 of -8 / 64
-  // activations that are not staged.  Up to 8 tokens they are read a block ahead (8 x 5120 x 17408:
-  // 22.8 to 21.6 us); more would take the registers of a CTA (16 tokens: 30.1 to 44.8 us)
-  static_assert(XS || SB == 1, "one block per step");
-  uint4 x_next[XS ? 1 : NT][4];
-  auto x_load = [&](int b) {
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int k = b * kBlockK + j * (FINE ? 32 : 8);
-        x_next[nt][j] = make_uint4(0u, 0u, 0u, 0u);
-        if (b < c1 && k + (FINE ? t * 8 : t * 32) < a.K)
-          x_next[nt][j] = *reinterpret_cast<const uint4*>(x_from[nt] + k);
-      }
-  };
-  if constexpr (!XS && NT == 1) x_load(c0 + wk);
   uint32_t slot = 0;
   for (int q0 = c0; q0 < c1; q0 += XS ? p.chunk : c1 - c0) {
     const int q1 = XS ? min(q0 + p.chunk, c1) : c1;
@@ -294,19 +286,11 @@ __global__ void __launch_bounds__(W * 32) int4_kernel(const __grid_constant__ Ff
     }
 
     for (int b0 = q0 + wk * SB; b0 < q1; b0 += kw * SB) {
-      uint4 xr[XS ? 1 : NT][4];
-      if constexpr (!XS) {
-        if constexpr (NT > 1) x_load(b0);  // before the wait for the weights: the latencies overlap
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) xr[nt][j] = x_next[nt][j];
-        if constexpr (NT == 1) x_load(b0 + kw);
-      }
       asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 2) : "memory");
       __syncwarp();  // every lane's copies of this step have landed, and the step before is read
       fetch(slot == 0 ? kDepth - 1 : slot - 1);
       const uint32_t from = mine + slot * kStep + (uint32_t)(g * SEG);
+      const uint32_t x_from = mine + slot * kStep + kX + (uint32_t)(g * 256);
       if (++slot == kDepth) slot = 0;
       // 64 x scale and the zero point in one word: a bf16 or fp16 scale leaves the low 13 bits of
       // its fp32 image free
@@ -341,9 +325,7 @@ __global__ void __launch_bounds__(W * 32) int4_kernel(const __grid_constant__ Ff
               wv[mt][h][3] = v.w;
             }
           }
-        uint32_t xa[NT];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) xa[nt] = x_at[nt] + (uint32_t)(b0 + sb - q0) * XB;
+        const uint32_t x_block0 = x_at + (uint32_t)(b0 + sb - q0) * XB;
         uint32_t negz[MT][2];
         float sc[MT][2], part[MT][NT][4];
 #pragma unroll
@@ -362,7 +344,8 @@ __global__ void __launch_bounds__(W * 32) int4_kernel(const __grid_constant__ Ff
           uint4 bx[NT];
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
-            bx[nt] = XS ? lds16(xa[nt] + j * (FINE ? 64 : 16)) : pair_up(xr[XS ? 0 : nt][j]);
+            bx[nt] = XS ? lds16(x_block0 + j * (FINE ? 64 : 16))
+                        : pair_up(lds16(x_from + nt * 2048 + (x_src ^ (uint32_t)(j * (FINE ? 64 : 16)))));
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
             uint32_t q0v[4], q1v[4];
@@ -465,10 +448,7 @@ cudaError_t launch(const FfnSkinnyArgs& a, int rw_log2, cudaStream_t st) {
   auto* kfn = int4_kernel<GATED, MT, NT, FINE, ZP, XS, SEG, kDepth, W>;
   static std::atomic<int> attr{0};
   if (!attr.load()) {
-    cudaError_t e = raise_smem_limit(kfn);
-    // activations read block by block live in L1: half of it (gated 8 x 17408 x 5120: 27.9 us, with
-    // all of it shared memory 29.9; staged activations want the shared memory: 22.2 against 25.6)
-    if (e == cudaSuccess && !XS) e = cudaFuncSetAttribute(kfn, cudaFuncAttributePreferredSharedMemoryCarveout, 50);
+    const cudaError_t e = raise_smem_limit(kfn);
     if (e != cudaSuccess) return e;
     attr.store(1);
   }
@@ -484,18 +464,16 @@ cudaError_t launch(const FfnSkinnyArgs& a, int rw_log2, cudaStream_t st) {
   if constexpr (XS) {
     // the activations of the CTA's share of K, or of as many blocks of it as 32 KB hold
     constexpr int xb = (int)x_block(FINE);
-    const int step = SEG / 64 * kw, toks = a.M < NT * 8 ? a.M : NT * 8;
+    const int step = SEG / 64 * kw;
     const int share = ((nblk + ks - 1) / ks + step - 1) / step * step;
-    p.chunk = 32 * 1024 / (xb * toks) / step * step;
-    if (p.chunk < step) p.chunk = step;
+    p.chunk = 32 * 1024 / xb / step * step;
     if (p.chunk > share) p.chunk = share;
-    p.x_pitch = p.chunk * xb + (p.chunk * xb / 64 % 2 ? 0 : 64);
-    p.x_bytes = (p.x_pitch * toks + 127) & ~127;
+    p.x_bytes = (p.chunk * xb + 127) & ~127;
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((a.N + out - 1) / out), (unsigned)((a.M + NT * 8 - 1) / (NT * 8)), (unsigned)ks);
   cfg.blockDim = dim3(W * 32, 1, 1);
-  cfg.dynamicSmemBytes = (size_t)W * kDepth * MT * 16 * SEG + p.x_bytes;
+  cfg.dynamicSmemBytes = (size_t)W * kDepth * (MT * 16 * SEG + (XS ? 0 : NT * 8 * 256)) + p.x_bytes;
   cfg.stream = st;
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -511,16 +489,31 @@ cudaError_t launch(const FfnSkinnyArgs& a, int rw_log2, cudaStream_t st) {
 
 template <bool GATED, bool FINE, bool ZP>
 cudaError_t launch_nt(const FfnSkinnyArgs& a, cudaStream_t st) {
-  if (a.M <= kStagedTokens) {
-    // many rows: eight warps on four row groups share the staged activations (1 x 17408 x 5120
-    // gated: 23.6 us against 28 us with four warps on one row group); few rows: all on K
-    const int64_t tiles = (a.N + (GATED ? 15 : 31)) / (GATED ? 16 : 32);
-    if (tiles >= 4 * kNumSMs) return launch<GATED, 1, FINE, ZP, true, 128, 3, 8>(a, 2, st);
-    return launch<GATED, 1, FINE, ZP, true, 128, 3, 4>(a, 0, st);
+  // row tiles of a warp; up to one per SM, more warps share a tile's K in place of more CTAs
+  const int64_t tiles = (a.N + (GATED ? 15 : 31)) / (GATED ? 16 : 32);
+  const bool few = tiles <= kNumSMs;
+  // One token of many rows is staged: 1 x 5120 x 17408 17.4 us, in the rings 19.3 (2 tokens 23.7 and
+  // 19.3).  From four tiles per SM on, eight warps on four row groups share it (1 x 17408 x 5120 gated:
+  // 22.5 us against 27.0 with four warps on one row group)
+  if (a.M == 1 && tiles >= 4 * kNumSMs) return launch<GATED, 1, FINE, ZP, true, 128, 3, 8>(a, 2, st);
+  if (a.M == 1 && !few) return launch<GATED, 1, FINE, ZP, true, 128, 3, 4>(a, 0, st);
+  // 6 x 4096 x 4096: 16 warps 4.9 us, 8: 5.3, 4: 6.2; 6 x 5120 x 17408: 24.2, 21.9, 19.1; 16 warps want
+  // two blocks each (6 x 512 x 1024: 2.3 us, 8 warps 2.2)
+  if (a.M <= 8) {
+    if (few && a.K > 31 * kBlockK) return launch<GATED, 1, FINE, ZP, false, 64, 3, 16>(a, 0, st);
+    if (few) return launch<GATED, 1, FINE, ZP, false, 64, 3, 8>(a, 0, st);
+    return launch<GATED, 1, FINE, ZP, false, 64, 3, 4>(a, 0, st);
   }
-  if (a.M <= 8) return launch<GATED, 1, FINE, ZP, false, 64, 4, 4>(a, 0, st);
-  if (a.M <= 16) return launch<GATED, 2, FINE, ZP, false, 64, 4, 4>(a, 0, st);
-  return launch<GATED, 4, FINE, ZP, false, 64, 4, 4>(a, 0, st);
+  // 13 x 2048 x 4096 gated: 8 warps 6.1 us, 4: 7.8; 16 x 10240 x 5120 16.6 and 15.1 us
+  if (a.M <= 16) {
+    if (few) return launch<GATED, 2, FINE, ZP, false, 64, 3, 8>(a, 0, st);
+    return launch<GATED, 2, FINE, ZP, false, 64, 2, 4>(a, 0, st);
+  }
+  // 25 x 2048 x 4096 gated: 8 warps 8.7 us, 4: 10.4; 32 x 10240 x 5120: 4 warps 27.5 us, 2: 33.3; 24 x
+  // 17408 x 5120 gated: 57.8 and 53.5 us (registers and shared memory leave room for 8 and 10 warps)
+  if (few) return launch<GATED, 4, FINE, ZP, false, 64, 2, 8>(a, 0, st);
+  if (tiles >= 4 * kNumSMs) return launch<GATED, 4, FINE, ZP, false, 64, 2, 2>(a, 0, st);
+  return launch<GATED, 4, FINE, ZP, false, 64, 2, 4>(a, 0, st);
 }
 
 template <bool GATED>

@@ -59,8 +59,8 @@ def sampled(N, n=60):
     return np.unique(np.concatenate([[0, 1, N // 2, N - 2, N - 1], np.random.default_rng(N).integers(0, N, n)]))
 
 
-# K shares over clusters of CTAs, activations staged in several pieces (up to 4 tokens) and read
-# block by block (more), rows for two CTAs per SM and more: every token, sampled rows
+# K shares over clusters of CTAs, one token's activations staged in several pieces, more tokens' in
+# the rings, rows for two CTAs per SM and more: every token, sampled rows
 @pytest.mark.parametrize("group,zeros", [(32, False), (64, True), (128, True), (512, False)])
 @pytest.mark.parametrize("M,N,K", [(1, 5000, 17408), (3, 5000, 17408), (4, 5000, 17376), (4, 96, 17408), (8, 640, 8224),
                                    (16, 640, 8224), (24, 330, 4128), (2, 19500, 3232), (4, 19500, 3232)])
@@ -70,6 +70,32 @@ def test_int4_large_sampled(ql, M, N, K, group, zeros):
     rows = torch.from_numpy(sampled(N)).cuda()
     ref, absum = reference(x, w[rows], s[rows], None if z is None else z[rows], K, group)
     check(y[:, rows].contiguous(), ref, absum, K)
+
+
+# each number of warps, tokens and rows that the launch chooses between: up to a row tile per SM (4864
+# rows), from four per SM on (19456), K of fewer blocks than warps and of more
+@pytest.mark.parametrize("group,zeros", [(32, True), (128, False)])
+@pytest.mark.parametrize("M", [1, 2, 8, 9, 16, 17, 32])
+@pytest.mark.parametrize("N,K", [(4864, 4000), (4865, 4000), (19457, 672), (200, 17408), (100, 3968)])
+def test_int4_every_variant_sampled(ql, M, N, K, group, zeros):
+    x, w, s, z = make(M, N, K, group, zeros, torch.bfloat16, seed=N + K + M)
+    y = ql.qlinear_int4(x, w, s, z, group=group)
+    rows = torch.from_numpy(sampled(N, 24)).cuda()
+    ref, absum = reference(x, w[rows], s[rows], None if z is None else z[rows], K, group)
+    check(y[:, rows].contiguous(), ref, absum, K)
+
+
+def test_int4_infinite_scale_of_a_short_last_block(ql):
+    """K ends inside a block of 128: the groups after its end do not exist, whatever the last one's
+    scale is; a row with an infinite scale is infinite where its group's sum is not zero."""
+    M, N, K, group = 2, 20, 160, 32
+    x, w, s, z = make(M, N, K, group, True, torch.bfloat16, seed=5)
+    s[3, 4] = float("inf")
+    y = ql.qlinear_int4(x, w, s, z, group=group)
+    wd = O.int4_dequant(w.cpu().numpy(), np.ones((N, 5)), z.cpu().numpy(), K, group)
+    last = (x.double().cpu().numpy()[:, 128:] * wd[3, 128:]).sum(1)
+    assert np.all(last != 0)
+    assert np.array_equal(y[:, 3].double().cpu().numpy(), np.sign(last) * np.inf)
 
 
 @pytest.mark.parametrize("group,zeros", [(64, True), (128, False)])
