@@ -3,13 +3,15 @@
 //
 // bf16 products are exact in fp32 and the warp MMA sums them in fp32; g and u stay there until the
 // activation.  The weights are the MMA's A operand (16 rows), the tokens its N = 8 columns.  A CTA
-// owns 16 outputs: 16 gate rows and the matching 16 up rows; its eight warps take K in turn, 32 at
-// a time (64 bytes of every row), and their sums meet in shared memory.  Which k an MMA slot stands
-// for is free as long as both operands agree: a lane's 16-byte piece of a row is four slots.  Every
-// lane copies its own pieces (cp.async) to its own slots of a ring, so a warp needs no barrier.
+// owns 16 outputs: 16 gate rows and the matching 16 up rows; its warps take K in turn, 32 at a time
+// (64 bytes of every row), and their sums meet in shared memory.  Which k an MMA slot stands for is
+// free as long as both operands agree: a lane's 16-byte piece of a row is four slots.  Every lane
+// copies its own pieces, of weights and activations, to its own slots of a ring (cp.async), so a
+// warp needs no barrier.  (Activations read where they are used, or a block ahead into registers:
+// 13 x 17408 x 5120 62.9 us, so 60.8; 1 x 2056 x 4096 8.5 and 7.3.)
 //
-// Bound by HBM for large weights: 1 token x 17408 x 5120 (356 MB) 55.6 us, 6.4 TB/s, 0.94 of the
-// measured copy rate; 13 x 2056 x 4096 (34 MB) 9.3 us, where launch, first loads and the joining of
+// Bound by HBM for large weights: 1 token x 17408 x 5120 (356 MB) 54.2 us, 6.6 TB/s, 0.97 of the
+// measured copy rate; 13 x 2056 x 4096 (34 MB) 8.3 us, where launch, first loads and the joining of
 // the K shares are half of it.
 #include <atomic>
 
@@ -22,13 +24,10 @@ namespace ql {
 
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
-constexpr int kDepth = 4;        // blocks in a warp's ring
 constexpr int kBlockK = 32;      // k per block
 constexpr int kPrefetch = 2;  // blocks
 constexpr int kOut = 16;         // outputs of a CTA
-constexpr uint32_t kBlock = 4 * 512;  // a warp's bytes per block: 32 rows of 64
+constexpr uint32_t kWBlock = 4 * 512;  // a warp's weight bytes per block: 32 rows of 64
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
@@ -55,10 +54,11 @@ __device__ __forceinline__ float ld_cta(uint32_t saddr, uint32_t rank) {
   return v;
 }
 
-// NT: 8-token tiles.  gridDim.z CTAs (a cluster) split K further.
-template <int NT>
-__global__ void __launch_bounds__(kThreads) ffn_skinny_kernel(const __grid_constant__ FfnSkinnyArgs a) {
-  constexpr int TT = NT * 8, PITCH = TT + 1;
+// NT: 8-token tiles; kDepth: blocks in a warp's ring.  gridDim.z CTAs (a cluster) split K further.
+template <int NT, int kDepth, int kWarps>
+__global__ void __launch_bounds__(kWarps * 32) ffn_skinny_kernel(const __grid_constant__ FfnSkinnyArgs a) {
+  constexpr int TT = NT * 8, PITCH = TT + 1, kThreads = kWarps * 32;
+  constexpr uint32_t kBlock = kWBlock + NT * 512;  // and the activations'
   extern __shared__ __align__(16) uint8_t ring[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(kThreads) ffn_skinny_kernel(const __grid_const
   const uint32_t mine = smem_addr(ring) + (uint32_t)warp * (kDepth * kBlock) + (uint32_t)lane * 16;
 
   // this lane's rows, [gate, up][half of the 16]; rows past the end read the last row, tokens past
-  // the end the last token: neither is stored
+  // the end are zeros: neither is stored
   const uint8_t* wp[2][2];
 #pragma unroll
   for (int up = 0; up < 2; ++up)
@@ -82,7 +82,7 @@ __global__ void __launch_bounds__(kThreads) ffn_skinny_kernel(const __grid_const
   const uint16_t* xp[NT];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
-    xp[nt] = a.x + (int64_t)(m0 + min(nt * 8 + g, toks - 1)) * a.ldx + (int64_t)b0 * kBlockK + t * 8;
+    xp[nt] = a.x + (int64_t)(m0 + nt * 8 + g) * a.ldx + (int64_t)b0 * kBlockK + t * 8;
 
   int bf = b0;  // the next block to fetch
   auto fetch = [&](uint32_t slot) {
@@ -95,6 +95,11 @@ __global__ void __launch_bounds__(kThreads) ffn_skinny_kernel(const __grid_const
           cp16(mine + slot * kBlock + (up * 2 + h) * 512, wp[up][h], take);
           wp[up][h] += bstep * 64;
         }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        cp16(mine + slot * kBlock + kWBlock + nt * 512, xp[nt], take && nt * 8 + g < toks);
+        xp[nt] += bstep * kBlockK;
+      }
       bf += bstep;
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -117,31 +122,17 @@ __global__ void __launch_bounds__(kThreads) ffn_skinny_kernel(const __grid_const
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[up][nt][i] = 0.f;
 
-  // activations; more than 8 tokens' a block ahead (13 x 2056 x 4096: 10.4 to 9.4 us, 16 x 17408 x
-  // 5120: 68.1 to 63.3 us; 8 tokens 58.3 to 60.0 us)
-  uint4 x_next[NT];
-  auto x_load = [&](int b) {
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      x_next[nt] = make_uint4(0u, 0u, 0u, 0u);
-      if (b < nblk && b * kBlockK + t * 8 < a.K) x_next[nt] = *reinterpret_cast<const uint4*>(xp[nt]);
-      xp[nt] += bstep * kBlockK;
-    }
-  };
-  if constexpr (NT > 1) x_load(b0);
   uint32_t slot = 0;
   for (int b = b0; b < nblk; b += bstep) {
-    if constexpr (NT == 1) x_load(b);  // before the wait for the weights: the latencies overlap
-    uint4 xv[NT];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) xv[nt] = x_next[nt];
-    if constexpr (NT > 1) x_load(b + bstep);
     asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 2) : "memory");
     uint4 wv[2][2];
 #pragma unroll
     for (int up = 0; up < 2; ++up)
 #pragma unroll
       for (int h = 0; h < 2; ++h) wv[up][h] = lds16(mine + slot * kBlock + (up * 2 + h) * 512);
+    uint4 xv[NT];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) xv[nt] = lds16(mine + slot * kBlock + kWBlock + nt * 512);
     // the slot of the block before this one is free: its pieces are in registers
     fetch(slot == 0 ? kDepth - 1 : slot - 1);
     if (++slot == kDepth) slot = 0;
@@ -200,30 +191,25 @@ __global__ void __launch_bounds__(kThreads) ffn_skinny_kernel(const __grid_const
   if (ks > 1) cluster_sync_all();  // the others may still read this CTA's sums
 }
 
-template <int NT>
+template <int NT, int kDepth, int kWarps>
 cudaError_t launch(const FfnSkinnyArgs& a, cudaStream_t st) {
-  auto* kfn = ffn_skinny_kernel<NT>;
+  auto* kfn = ffn_skinny_kernel<NT, kDepth, kWarps>;
   static std::atomic<int> attr{0};
   if (!attr.load()) {
-    cudaError_t e = raise_smem_limit(kfn);
-    // the activations live in L1, so not all of it goes to the rings: 8 x 17408 x 5120 57.1 us with
-    // half, 60.6 with none of it left; 16 tokens 66.9 us with a fifth, 69.7 with half (registers keep
-    // the CTAs few); 32 tokens 74.0 and 95.3 us; 1 token 55.3 and 54.5 us
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(kfn, cudaFuncAttributePreferredSharedMemoryCarveout, NT == 2 ? 80 : 50);
+    const cudaError_t e = raise_smem_limit(kfn);
     if (e != cudaSuccess) return e;
     attr.store(1);
   }
   const dim3 grid((unsigned)((a.N + kOut - 1) / kOut), (unsigned)((a.M + NT * 8 - 1) / (NT * 8)));
-  // K over a cluster's CTAs while there are fewer than three CTAs per two SMs and every warp keeps
-  // four blocks or more (13 x 2056 x 4096: 2 CTAs 10.9 us, 1: 15.8, 4: 14.9)
+  // K over a cluster's CTAs while there are fewer than twelve warps per SM and every warp keeps four
+  // blocks or more (13 x 2056 x 4096, 8 warps: 2 CTAs 9.1 us, 1: 9.7, 4: 13.0)
   const int nblk = (a.K + kBlockK - 1) / kBlockK;
   int ks = 1;
-  while (ks < 8 && (int64_t)grid.x * grid.y * ks < 3 * kNumSMs / 2 && nblk >= kWarps * ks * 8) ks *= 2;
+  while (ks < 8 && (int64_t)grid.x * grid.y * ks * kWarps < 12 * kNumSMs && nblk >= kWarps * ks * 8) ks *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid.x, grid.y, (unsigned)ks);
-  cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = kWarps * kDepth * kBlock;
+  cfg.blockDim = dim3(kWarps * 32, 1, 1);
+  cfg.dynamicSmemBytes = kWarps * kDepth * (kWBlock + NT * 512);
   cfg.stream = st;
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -240,9 +226,14 @@ cudaError_t launch(const FfnSkinnyArgs& a, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_ffn_skinny(const FfnSkinnyArgs& a, cudaStream_t st) {
-  if (a.M <= 8) return launch<1>(a, st);
-  if (a.M <= 16) return launch<2>(a, st);
-  return launch<4>(a, st);
+  // up to a CTA per SM, 16 warps share its K: 13 x 2056 x 4096 8.3 us, with 8 warps and a cluster of two
+  // 9.1 (32 tokens 10.1 and 11.6); at 13 x 4096 x 2048 (256 CTAs) 10.1 and 8.2.  They want four
+  // blocks each (1 x 520 x 1024: 2.5 us, 8 warps 2.3).  32 tokens: three blocks in the ring let two
+  // CTAs on an SM (73 us against 82 with four at 17408 x 5120)
+  const bool few = (a.N + kOut - 1) / kOut <= kNumSMs && a.K > 63 * kBlockK;
+  if (a.M <= 8) return few ? launch<1, 3, 16>(a, st) : launch<1, 4, 8>(a, st);
+  if (a.M <= 16) return few ? launch<2, 3, 16>(a, st) : launch<2, 4, 8>(a, st);
+  return few ? launch<4, 3, 16>(a, st) : launch<4, 3, 8>(a, st);
 }
 
 }  // namespace ql

@@ -92,6 +92,18 @@ def test_forward(ql, M, H, I):
     check_h(h, *forward_reference(x, w, I), H)
 
 
+# each number of warps and CTAs that a few tokens' launch chooses between: up to a CTA of 16 outputs
+# per SM (2432) and more, K of few blocks and of many
+@pytest.mark.parametrize("M", [1, 7, 9, 16, 17, 32])
+@pytest.mark.parametrize("H,I", [(2016, 2432), (2024, 2432), (2024, 2440), (8200, 80), (520, 5000)])
+def test_few_tokens_every_variant_sampled(ql, M, H, I):
+    x, w, _ = make(M, H, I, seed=H + I + M)
+    h = ql.gated_ffn(x, w)
+    o = np.unique(np.concatenate([[0, 1, I // 2, I - 1], np.random.default_rng(I).integers(0, I, 40)]))
+    rows = torch.from_numpy(np.concatenate([o, I + o])).cuda()
+    check_h(h[:, torch.from_numpy(o).cuda()], *forward_reference(x, w[rows], len(o)), H)
+
+
 @pytest.mark.parametrize("save", ["bf16", "int8"])
 @pytest.mark.parametrize("M,H,I", SHAPES)
 def test_checkpoint_and_backward(ql, M, H, I, save):
