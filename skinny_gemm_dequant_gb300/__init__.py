@@ -332,12 +332,12 @@ def _int4_weights(K, sx, w, w_scale, w_zero, group):
     """Checks packed codes [N, >=K/2] and scales and zero points [N, >=ceil(K/group)] against x
     [M, K] with strides sx; returns (N, row strides of w, w_scale and w_zero, scale format)."""
     (N, cols), (ldw, inner) = w.shape, w.stride()
-    if w.dtype is not torch.uint8 or inner != 1 or sx[1] != 1:
-        raise TypeError("w must be packed uint8 codes with unit inner stride; x must have unit inner stride")
+    if w.dtype is not torch.uint8 or not w.is_cuda or inner != 1 or sx[1] != 1:
+        raise TypeError("w must be packed uint8 CUDA codes with unit inner stride; x must have unit inner stride")
     fmt = _SCALE_FORMATS.get(w_scale.dtype)
     (rows, scols), (lds, inner) = w_scale.shape, w_scale.stride()
-    if fmt is None or inner != 1:
-        raise TypeError("w_scale must be bfloat16 or float16 with unit inner stride")
+    if fmt is None or not w_scale.is_cuda or inner != 1:
+        raise TypeError("w_scale must be a bfloat16 or float16 CUDA tensor with unit inner stride")
     if group < 1:
         raise ValueError("group must be positive")
     groups = -(-K // group)
@@ -346,8 +346,8 @@ def _int4_weights(K, sx, w, w_scale, w_zero, group):
     ldz = 0
     if w_zero is not None:
         (rows, zcols), (ldz, inner) = w_zero.shape, w_zero.stride()
-        if w_zero.dtype is not torch.uint8 or inner != 1:
-            raise TypeError("w_zero must be uint8 with unit inner stride")
+        if w_zero.dtype is not torch.uint8 or not w_zero.is_cuda or inner != 1:
+            raise TypeError("w_zero must be a uint8 CUDA tensor with unit inner stride")
         if rows != N or zcols < groups:
             raise ValueError("w_zero must be [N, >=ceil(K/group)]")
     return N, ldw, lds, ldz, fmt
@@ -365,8 +365,8 @@ def _empty(shape, dtype, x, stream):
 def _out(out, M, N, x, stream, name="out"):
     if out is None:
         return _empty((M, N), torch.bfloat16, x, stream)
-    if out.dtype is not torch.bfloat16 or out.shape != (M, N) or out.stride(1) != 1:
-        raise TypeError(f"{name} must be bfloat16 [{M}, {N}] with unit inner stride")
+    if out.dtype is not torch.bfloat16 or not out.is_cuda or out.shape != (M, N) or out.stride(1) != 1:
+        raise TypeError(f"{name} must be a bfloat16 CUDA tensor [{M}, {N}] with unit inner stride")
     return out
 
 
@@ -378,8 +378,9 @@ def qlinear_int4(x, w, w_scale, w_zero=None, bias=None, *, group=128, debug=Fals
     _bf16(x, "x")
     (M, K), sx = x.shape, x.stride()
     N, ldw, lds, ldz, fmt = _int4_weights(K, sx, w, w_scale, w_zero, group)
-    if bias is not None and (bias.dtype is not torch.bfloat16 or bias.shape != (N,) or not bias.is_contiguous()):
-        raise TypeError(f"bias must be bfloat16 [{N}]")
+    if bias is not None and (bias.dtype is not torch.bfloat16 or not bias.is_cuda or bias.shape != (N,)
+                             or not bias.is_contiguous()):
+        raise TypeError(f"bias must be a bfloat16 CUDA tensor [{N}]")
     y = _out(out, M, N, x, stream)
     path = ctypes.c_int(0) if debug else None
     st = lib.qlinear_int4(x.data_ptr(), M, K, sx[0], w.data_ptr(), N, ldw, w_scale.data_ptr(), fmt, lds, _ptr(w_zero),
@@ -447,8 +448,8 @@ def _ffn_weights(x, w13):
     """Checks w13 [2I, H] against x [M, H]; returns (M, H, I, row strides of x and w13)."""
     (M, H), (ldx, ix) = x.shape, x.stride()
     (rows, cols), (ldw, iw) = w13.shape, w13.stride()
-    if w13.dtype is not torch.bfloat16 or iw != 1 or ix != 1:
-        raise TypeError("w13 must be bfloat16 with unit inner stride; x must have unit inner stride")
+    if w13.dtype is not torch.bfloat16 or not w13.is_cuda or iw != 1 or ix != 1:
+        raise TypeError("w13 must be a bfloat16 CUDA tensor with unit inner stride; x must have unit inner stride")
     if rows & 1 or cols != H:
         raise ValueError("w13 must be [2I, H] (gate rows, then up rows) for x [M, H]")
     return M, H, rows >> 1, ldx, ldw
@@ -497,10 +498,10 @@ def gated_ffn_backward(dh, x, w13, saved, *, swiglu_alpha=1.0, swiglu_limit=None
         raise TypeError(f"dh must be [{M}, {I}] with unit inner stride")
     mode, data, scale = saved
     P = -(-I // 128) * 128
-    if (mode not in ("bf16", "int8") or data.shape != (M, 2, P) or not data.is_contiguous()
+    if (mode not in ("bf16", "int8") or not data.is_cuda or data.shape != (M, 2, P) or not data.is_contiguous()
             or data.dtype is not (torch.bfloat16 if mode == "bf16" else torch.int8)):
         raise ValueError("saved must be the FFNCheckpoint of this x and w13")
-    if mode == "int8" and (scale is None or scale.shape != (M, 2, P // 128) or not scale.is_contiguous()
+    if mode == "int8" and (scale is None or not scale.is_cuda or scale.shape != (M, 2, P // 128) or not scale.is_contiguous()
                            or scale.dtype is not torch.float32):
         raise ValueError("saved must be the FFNCheckpoint of this x and w13")
     dx = _out(out_dx, M, H, x, stream, "out_dx") if need_dx else None

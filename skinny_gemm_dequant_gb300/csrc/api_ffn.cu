@@ -127,7 +127,8 @@ ql_status gated_ffn(const uint16_t* x, int64_t M, int64_t H, int64_t ldx, const 
   if (!al16(workspace)) return QL_ERR_ALIGNMENT;
   cudaStream_t st = (cudaStream_t)stream;
   cudaError_t e;
-  if (M <= kFfnSkinnyTokens && save == QL_SAVE_NONE) {
+  const bool few = save == QL_SAVE_NONE && ffn_few_tokens(M, I);
+  if (few) {
     FfnSkinnyArgs a = {};
     a.x = x;
     a.ldx = ldx;
@@ -164,8 +165,7 @@ ql_status gated_ffn(const uint16_t* x, int64_t M, int64_t H, int64_t ldx, const 
     e = tc::launch_ffn_forward(f, st);
   }
   if (e != cudaSuccess) return cuda_status(e);
-  if (path_out)
-    *path_out = M <= kFfnSkinnyTokens && save == QL_SAVE_NONE ? QL_PATH_GATED_FFN_SKINNY : QL_PATH_GATED_FFN_TCGEN05;
+  if (path_out) *path_out = few ? QL_PATH_GATED_FFN_SKINNY : QL_PATH_GATED_FFN_TCGEN05;
   return QL_OK;
 }
 

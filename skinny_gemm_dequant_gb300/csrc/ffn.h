@@ -3,6 +3,8 @@
 #include <cstdint>
 #include <cuda_runtime.h>
 
+#include "internal.h"
+
 namespace ql {
 
 // ------------------------------------------------------------------ skinny calls (kernels_ffn_skinny.cu)
@@ -25,6 +27,12 @@ struct FfnSkinnyArgs {
   float alpha, limit;     // activation of a gated block
 };
 constexpr int64_t kFfnSkinnyTokens = 32;  // tokens one pass over the weights takes
+// A forward without a checkpoint: the few-token kernel for one pass over the weights, and for more
+// while its CTAs (32 tokens, 16 outputs) are two per SM at most (64 x 2056 x 4096: 14.3 us, tcgen05
+// 20.7; 96 tokens 25.0 and 20.7; 128 x 1024 x 1024 6.4 and 9.7; 40 x 4096 x 2048 16.7 and 16.0)
+inline bool ffn_few_tokens(int64_t M, int64_t I) {
+  return M <= kFfnSkinnyTokens || (M + 31) / 32 * ((I + 15) / 16) <= 2 * kNumSMs;
+}
 cudaError_t launch_ffn_skinny(const FfnSkinnyArgs& a, cudaStream_t st);
 cudaError_t launch_int4(bool gated, const FfnSkinnyArgs& a, cudaStream_t st);  // kernels_int4.cu
 

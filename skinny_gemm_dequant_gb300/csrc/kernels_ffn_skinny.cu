@@ -201,11 +201,12 @@ cudaError_t launch(const FfnSkinnyArgs& a, cudaStream_t st) {
     attr.store(1);
   }
   const dim3 grid((unsigned)((a.N + kOut - 1) / kOut), (unsigned)((a.M + NT * 8 - 1) / (NT * 8)));
-  // K over a cluster's CTAs while there are fewer than twelve warps per SM and every warp keeps four
-  // blocks or more (13 x 2056 x 4096, 8 warps: 2 CTAs 9.1 us, 1: 9.7, 4: 13.0)
+  // K over a cluster's CTAs while all of them find a place at once (16 warps per SM; 96 x 1024 x 2048 in
+  // two waves 14.9 us, unsplit 8.6) and every warp keeps four blocks or more (13 x 2056 x 4096, 8 warps:
+  // 2 CTAs 9.1 us, 1: 9.7, 4: 13.0)
   const int nblk = (a.K + kBlockK - 1) / kBlockK;
   int ks = 1;
-  while (ks < 8 && (int64_t)grid.x * grid.y * ks * kWarps < 12 * kNumSMs && nblk >= kWarps * ks * 8) ks *= 2;
+  while (ks < 8 && (int64_t)grid.x * grid.y * ks * kWarps <= 8 * kNumSMs && nblk >= kWarps * ks * 8) ks *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid.x, grid.y, (unsigned)ks);
   cfg.blockDim = dim3(kWarps * 32, 1, 1);
@@ -230,7 +231,7 @@ cudaError_t launch_ffn_skinny(const FfnSkinnyArgs& a, cudaStream_t st) {
   // 9.1 (32 tokens 10.1 and 11.6); at 13 x 4096 x 2048 (256 CTAs) 10.1 and 8.2.  They want four
   // blocks each (1 x 520 x 1024: 2.5 us, 8 warps 2.3).  32 tokens: three blocks in the ring let two
   // CTAs on an SM (73 us against 82 with four at 17408 x 5120)
-  const bool few = (a.N + kOut - 1) / kOut <= kNumSMs && a.K > 63 * kBlockK;
+  const bool few = (int64_t)((a.N + kOut - 1) / kOut) * ((a.M + 31) / 32) <= kNumSMs && a.K > 63 * kBlockK;
   if (a.M <= 8) return few ? launch<1, 3, 16>(a, st) : launch<1, 4, 8>(a, st);
   if (a.M <= 16) return few ? launch<2, 3, 16>(a, st) : launch<2, 4, 8>(a, st);
   return few ? launch<4, 3, 16>(a, st) : launch<4, 3, 8>(a, st);

@@ -489,8 +489,9 @@ cudaError_t launch(const FfnSkinnyArgs& a, int rw_log2, cudaStream_t st) {
 
 template <bool GATED, bool FINE, bool ZP>
 cudaError_t launch_nt(const FfnSkinnyArgs& a, cudaStream_t st) {
-  // row tiles of a warp; up to one per SM, more warps share a tile's K in place of more CTAs
-  const int64_t tiles = (a.N + (GATED ? 15 : 31)) / (GATED ? 16 : 32);
+  // row tiles of a warp, for 32 tokens; up to one per SM, more warps share a tile's K in place of more
+  // CTAs
+  const int64_t tiles = (int64_t)((a.N + (GATED ? 15 : 31)) / (GATED ? 16 : 32)) * ((a.M + 31) / 32);
   const bool few = tiles <= kNumSMs;
   // One token of many rows is staged: 1 x 5120 x 17408 17.4 us, in the rings 19.3 (2 tokens 23.7 and
   // 19.3).  From four tiles per SM on, eight warps on four row groups share it (1 x 17408 x 5120 gated:

@@ -84,11 +84,13 @@ SHAPES = [(1, 8, 8), (1, 512, 264), (3, 72, 40), (13, 264, 72), (32, 1024, 136),
           (128, 320, 200), (129, 8, 256), (256, 512, 128), (257, 1000, 520), (700, 264, 1032)]
 
 
-@pytest.mark.parametrize("M,H,I", SHAPES)
+@pytest.mark.parametrize("M,H,I", SHAPES + [(33, 72, 2432), (33, 72, 2440), (40, 2056, 2448), (300, 328, 488),
+                                         (1000, 136, 152), (2400, 64, 72), (257, 320, 1000)])
 def test_forward(ql, M, H, I):
     x, w, _ = make(M, H, I, seed=M)
     h, path = ql.gated_ffn(x, w, debug=True)
-    assert path == ("gated_ffn_skinny" if M <= 32 else "gated_ffn_tcgen05")
+    few = M <= 32 or -(-M // 32) * -(-I // 16) <= 304
+    assert path == ("gated_ffn_skinny" if few else "gated_ffn_tcgen05")
     check_h(h, *forward_reference(x, w, I), H)
 
 
@@ -168,9 +170,9 @@ def test_activation_parameters(ql, M, alpha, limit):
 def test_strides_and_guard_columns(ql):
     M, H, I = 70, 136, 72
     x, w, dh = make(M, H, I, seed=7, pad=2)
-    for m in (4, M):  # skinny, tcgen05
+    for m, save in ((4, None), (M, None), (M, "bf16")):  # the few-token kernel, twice; tcgen05
         wide = torch.full((m, I + 24), 7.0, dtype=torch.bfloat16, device="cuda")
-        ql.gated_ffn(x[:m], w, out=wide[:, 8:8 + I])
+        ql.gated_ffn(x[:m], w, out=wide[:, 8:8 + I], save=save)
         check_h(wide[:, 8:8 + I], *forward_reference(x[:m], w, I), H)
         assert torch.all(wide[:, :8] == 7.0) and torch.all(wide[:, 8 + I:] == 7.0)
     _, saved = ql.gated_ffn(x, w, save="int8")
@@ -320,6 +322,14 @@ def test_python_refusals(ql):
         ql.gated_ffn(x.float(), w)
     with pytest.raises(TypeError):
         ql.gated_ffn(x, w.float())
+    with pytest.raises(TypeError):
+        ql.gated_ffn(x, w.cpu())
+    with pytest.raises(TypeError):
+        ql.gated_ffn_backward(dh, x, w.cpu(), saved)
+    with pytest.raises(ValueError):
+        ql.gated_ffn_backward(dh, x, w, saved._replace(data=saved.data.cpu()))
+    with pytest.raises(ValueError):
+        ql.gated_ffn_backward(dh, x, w, saved._replace(scale=saved.scale.cpu()))
     with pytest.raises(TypeError):
         ql.gated_ffn(x, w, out=torch.empty(40, 80, dtype=torch.bfloat16, device="cuda"))
     with pytest.raises(TypeError):

@@ -181,7 +181,9 @@ def test_int4_other_stream_and_graph(ql):
 def test_int4_python_refusals(ql):
     x, w, s, z = make(2, 32, 256, 128)
     for bad in (dict(w=w.to(torch.int8)), dict(w_scale=s.float()), dict(w_zero=z.int()), dict(x=x.float()),
-                dict(bias=torch.zeros(32, device="cuda"))):
+                dict(bias=torch.zeros(32, device="cuda")), dict(w=w.cpu()), dict(w_scale=s.cpu()),
+                dict(w_zero=z.cpu()), dict(bias=torch.zeros(32, dtype=torch.bfloat16)),
+                dict(out=torch.empty(2, 32, dtype=torch.bfloat16))):
         with pytest.raises(TypeError):
             ql.qlinear_int4(**{**dict(x=x, w=w, w_scale=s, w_zero=z), **bad})
     for bad in (dict(w=w[:, :64]), dict(w_scale=s[:, :1]), dict(w_zero=z[:, :1]), dict(w_scale=s[:16]), dict(group=0)):
