@@ -145,6 +145,16 @@ __device__ __forceinline__ bool wait2(uint64_t* bar, uint32_t parity, uint32_t l
     if (n >= limit || (abort && *abort)) return false;
   }
 }
+// one lane of a whole warp, the same one every time
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+// the whole warp waits; one answer for all lanes
+__device__ __forceinline__ bool wait2_warp(uint64_t* bar, uint32_t parity, uint32_t limit, volatile int* abort) {
+  return __all_sync(0xffffffffu, wait2(bar, parity, limit, abort));
+}
 // the box goes to this CTA's shared memory, its bytes to the barrier at cluster address `bar`
 __device__ __forceinline__ void load_pair(uint32_t smem_dst, const CUtensorMap* m, int x, int y, uint32_t bar) {
   asm volatile(
@@ -308,26 +318,31 @@ __device__ __forceinline__ void gemm(const CUtensorMap& tmA, const CUtensorMap& 
     st_remote(in_cta(smem_u32(&s_abort), rank ^ 1), 1);
   };
 
+  // The producer and the MMA issuer run as whole warps of which one lane issues: addresses and
+  // descriptors then live in uniform registers.  With one lane alone in the loop every operand was
+  // moved there anew, and a step of 64 K took 0.35 us whatever was loaded or multiplied in it (2048 x
+  // 2048 x 4096 forward 49 us; so 0.28 and 40)
   if (warp == 0) {
-    if (lane == 0) {
-      // ---------------------------------------------------------- producer
-      // bytes of a stage in one CTA: B by N-major chunks of 64 columns is loaded whole
-      const uint32_t half_bytes = kHalfBytes + (B_MN ? (hw > 64 ? kHalfBytes : kHalfBytes / 2) : (uint32_t)hw * kBlockK * 2);
-      int s = 0, issued = 0;
-      uint32_t ph = 1;  // the first pass over the stages finds them empty
-      bool ok = true;
-      int t, k0, k1;
-      for (Walk w(pair); ok && w.next(p, pairs, t, k0, k1);) {
-        int tm, tn;
-        tile_at(p, t, tm, tn);
-        const int ra = tm * 256 + (int)rank * 128;
-        const int rb = MODE == FWD ? tn * hw + (int)rank * p.I : tn * p.width + (int)rank * hw;
-        for (int kt = k0; kt < k1; ++kt) {
-          if (!wait2(&empty[s], ph, lim, abort)) {
-            fail();
-            ok = false;
-            break;
-          }
+    // ------------------------------------------------------------ producer
+    const bool leader = elect_one();
+    // bytes of a stage in one CTA: B by N-major chunks of 64 columns is loaded whole
+    const uint32_t half_bytes = kHalfBytes + (B_MN ? (hw > 64 ? kHalfBytes : kHalfBytes / 2) : (uint32_t)hw * kBlockK * 2);
+    int s = 0, issued = 0;
+    uint32_t ph = 1;  // the first pass over the stages finds them empty
+    bool ok = true;
+    int t, k0, k1;
+    for (Walk w(pair); ok && w.next(p, pairs, t, k0, k1);) {
+      int tm, tn;
+      tile_at(p, t, tm, tn);
+      const int ra = tm * 256 + (int)rank * 128;
+      const int rb = MODE == FWD ? tn * hw + (int)rank * p.I : tn * p.width + (int)rank * hw;
+      for (int kt = k0; kt < k1; ++kt) {
+        if (!wait2_warp(&empty[s], ph, lim, abort)) {
+          if (leader) fail();
+          ok = false;
+          break;
+        }
+        if (leader) {
           const uint32_t bar = in_cta(smem_u32(&full[s]), 0);
           if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * half_bytes);
           const uint32_t sa = base + (uint32_t)s * kStageBytes, sb = sa + kHalfBytes;
@@ -344,28 +359,30 @@ __device__ __forceinline__ void gemm(const CUtensorMap& tmA, const CUtensorMap& 
           } else {
             load_pair(sb, &tmB, k, rb, bar);
           }
-          ++issued;
-          if (++s == kStages) {
-            s = 0;
-            ph ^= 1;
-          }
         }
-      }
-      // the last stages' releases, multicast by the other CTA, land before this CTA may leave
-      for (int i = 0; i < kStages && ok; ++i) {
-        ok = wait2(&empty[s], ph, lim, abort);
-        if (!ok) fail();
+        __syncwarp();
+        ++issued;
         if (++s == kStages) {
           s = 0;
           ph ^= 1;
         }
       }
-      if (ok && !wait2(&done, 0, lim, abort)) fail();
-      s_issued = issued;
     }
+    // the last stages' releases, multicast by the other CTA, land before this CTA may leave
+    for (int i = 0; i < kStages && ok; ++i) {
+      ok = wait2_warp(&empty[s], ph, lim, abort);
+      if (!ok && leader) fail();
+      if (++s == kStages) {
+        s = 0;
+        ph ^= 1;
+      }
+    }
+    if (ok && !wait2_warp(&done, 0, lim, abort) && leader) fail();
+    if (leader) s_issued = issued;
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
       // ---------------------------------------------------------- MMA issue
+      const bool leader = elect_one();
       const uint32_t idesc = idesc_pair(A_MN, B_MN, p.width);
       constexpr uint64_t a_step = A_MN ? 2048 / 16 : 2, b_step = B_MN ? 2048 / 16 : 2;  // 16 k
       const uint64_t a0 = A_MN ? desc_mn(base) : smem_desc_sw128(base);
@@ -376,33 +393,37 @@ __device__ __forceinline__ void gemm(const CUtensorMap& tmA, const CUtensorMap& 
       int t, k0, k1;
       for (Walk w(pair); ok && w.next(p, pairs, t, k0, k1); ++n) {
         const int buf = n & 1;
-        if (!wait2(&tempty[buf], (uint32_t)((n >> 1) & 1) ^ 1, lim, abort)) {
-          fail();
+        if (!wait2_warp(&tempty[buf], (uint32_t)((n >> 1) & 1) ^ 1, lim, abort)) {
+          if (leader) fail();
           ok = false;
           break;
         }
         tc_fence_after();
         const uint32_t d = tmem + (uint32_t)buf * 256;
         for (int kt = k0; kt < k1; ++kt) {
-          if (!wait2(&full[s], ph, lim, abort)) {
-            fail();
+          if (!wait2_warp(&full[s], ph, lim, abort)) {
+            if (leader) fail();
             ok = false;
             break;
           }
           tc_fence_after();
           const uint64_t off = (uint64_t)s * (kStageBytes >> 4);
+          if (leader) {
 #pragma unroll
-          for (int j = 0; j < kBlockK / 16; ++j)
-            mma_pair(d, a0 + off + j * a_step, b0 + off + j * b_step, idesc, kt != k0 || j != 0);
-          commit_pair(&empty[s]);
+            for (int j = 0; j < kBlockK / 16; ++j)
+              mma_pair(d, a0 + off + j * a_step, b0 + off + j * b_step, idesc, kt != k0 || j != 0);
+            commit_pair(&empty[s]);
+          }
+          __syncwarp();
           if (++s == kStages) {
             s = 0;
             ph ^= 1;
           }
         }
-        if (ok) commit_pair(&tfull[buf]);
+        if (ok && leader) commit_pair(&tfull[buf]);
+        __syncwarp();
       }
-      commit_pair(&done);
+      if (leader) commit_pair(&done);
     }
   } else if (warp >= 4) {
     // ------------------------------------------------------------ epilogue
