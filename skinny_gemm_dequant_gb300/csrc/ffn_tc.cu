@@ -29,12 +29,11 @@
 // waits for another pair.  Equal shares of all tiles of the last two rounds, which would leave no
 // pair idle, were slower (4096 x 17408 x 5120 dx: 1009 us against 956 us uncut): the pairs then
 // stand at different k and no longer find each other's operands in L2.
-// What bounds it: the tensor cores under the power cap in long calls (4096 tokens, 17408 x 5120:
-// forward 0.83 ms, dx 0.82 ms, dW13 0.81 ms, 1.76 to 1.81 PFLOP/s each alone; 1.69 PFLOP/s over a
-// step); the rounds' rest in middling ones (2048 x 2048 x 4096: 1.3 PFLOP/s); in short ones about
-// 7 us of fixed cost (launch, set-up, the first loads, the epilogue of the one tile) and the parts'
-// way through L2; the weights' HBM traffic for few tokens (64 x 17408 x 5120 forward 66 us, 5.4
-// TB/s) and the writing of dW13 (2.9 of 4.0 TB/s that a plain fill of memory reaches).
+// What bounds it: the tensor cores in long calls (4096 tokens, 17408 x 5120: a step 2.38 ms, 1.84
+// PFLOP/s); in middling ones (2048 x 2048 x 4096: a step 131 us, 1.57 PFLOP/s) a step of 64 K takes
+// 0.27 us, 0.23 of them the products', and each launch's first loads and last writing about 7 us; in
+// short ones those 7 us and the parts' way through L2; the weights' HBM traffic for few tokens (64 x
+// 17408 x 5120 forward 65 us, 5.5 TB/s) and the writing of dW13.
 // Every wait is bounded; one that runs out raises QL_DEV_TIMEOUT in the status word and the pair
 // leaves its loops, waits for copies and MMAs in flight and frees its tensor memory.
 #include <cudaTypedefs.h>
@@ -744,44 +743,49 @@ bool bf16_map(CUtensorMap* m, const void* base, int64_t inner, int64_t outer, in
 }
 
 // Tiles of a GEMM over the pairs: whole ones in turn, and the last round's cut along K where that is
-// shorter.  In steps of 64 K (0.38 us): a part takes nk / parts of them, storing it, and adding and
-// finishing all parts of a tile by one CTA about 6 + 5 * parts * width / 256.
+// shorter.  Times in ns, as measured at 2048 x 2048 x 4096: a step of 64 K takes 216 for 64 columns,
+// 227 for 128, 247 for 192, 281 for 256 (its waits and issues more than its products); from a tile's
+// last product to the end of its writing 1.7 us for 64 and 3.4 for 256, 2.5 and 5.4 with the activation
 struct Cut {
   int width, tiles_m, tiles_n, nk, whole, cut, parts;
-  int64_t cost;  // of the longest pair: steps of 64 K times (width + 64), see plan
+  int64_t cost;  // of the longest pair
   size_t bytes() const { return (size_t)cut * parts * 2 * kSlotFloats * 4; }
 };
 constexpr int kPairs = kNumSMs / 2;
-constexpr int kTileSteps = 9;  // writing a tile out takes about as long as nine steps (3.4 us)
-Cut plan_width(int64_t rows, int64_t cols, int64_t K, int width, int outs, int pairs) {
+int64_t step_ns(int width) { return 190 + width / 3; }
+int64_t write_ns(int width, bool fwd) { return fwd ? 1600 + 15 * width : 1100 + 9 * width; }
+Cut plan_width(int64_t rows, int64_t cols, int64_t K, int width, bool fwd, int pairs) {
+  const int outs = fwd ? width / 2 : width;
   Cut c = {};
   c.width = width;
   c.tiles_m = (int)((rows + 255) / 256);
   c.tiles_n = (int)((cols + outs - 1) / outs);
   c.nk = (int)((K + kBlockK - 1) / kBlockK);
-  const int64_t tiles = (int64_t)c.tiles_m * c.tiles_n;
+  const int64_t tiles = (int64_t)c.tiles_m * c.tiles_n, step = step_ns(width);
   c.whole = (int)tiles;
   const int rest = (int)(tiles % pairs);
-  const int whole_steps = c.nk > kTileSteps ? c.nk : kTileSteps;
-  int64_t best = rest ? whole_steps : 0;
+  const int64_t write = write_ns(width, fwd);  // runs under the next tile's products; the last one's does not
+  const int64_t whole = c.nk * step > write ? c.nk * step : write;
+  int64_t best = (rest ? whole : 0) + write;
   for (int parts = 2; rest > 0 && parts * rest <= pairs && parts <= c.nk && parts <= 8; ++parts) {
-    const int64_t steps = (c.nk + parts - 1) / parts + 6 + 5 * parts * width / 256;
-    if (steps >= best) continue;
-    best = steps;
+    // the longest part, storing it, adding and finishing all parts of a tile by one CTA
+    const int64_t ns = (c.nk + parts - 1) / parts * step + write + 3500 + 8 * parts * width;
+    if (ns >= best) continue;
+    best = ns;
     c.whole = (int)tiles - rest;
     c.cut = rest;
     c.parts = parts;
   }
-  c.cost = (tiles / pairs * whole_steps + best) * (width + 64);
+  c.cost = tiles / pairs * whole + best;
   return c;
 }
 // Narrower tiles where they fill the rounds better (2048 x 2048 x 4096: 152 tiles of 224 columns in
-// two rounds against 128 of 256) or, with few tiles, put more SMs to work.  They load as much of A
-// for fewer columns: a step is taken as width + 64, and 4 % at least has to come of it.
+// two rounds against 128 of 256) or, with few tiles, put more SMs to work; 4 % at least has to come
+// of it
 Cut plan(int64_t rows, int64_t cols, int64_t K, bool fwd, bool narrow, int pairs = kPairs) {
-  Cut c = plan_width(rows, cols, K, 256, fwd ? 128 : 256, pairs);
+  Cut c = plan_width(rows, cols, K, 256, fwd, pairs);
   for (int width = 224; narrow && width >= 64; width -= 32) {
-    const Cut d = plan_width(rows, cols, K, width, fwd ? width / 2 : width, pairs);
+    const Cut d = plan_width(rows, cols, K, width, fwd, pairs);
     if (d.cost * 25 < c.cost * 24) c = d;
   }
   return c;
@@ -801,11 +805,12 @@ struct Both {
 Both plan_both(int64_t M, int64_t H, int64_t I) {
   Both b = {0, plan_dx(M, H, I), plan_dw(M, H, I)};
   auto work = [](const Cut& c) {
-    return (int64_t)c.tiles_m * c.tiles_n * (c.nk > kTileSteps ? c.nk : kTileSteps) * c.width;
+    const int64_t k = c.nk * step_ns(c.width), write = write_ns(c.width, false);
+    return (int64_t)c.tiles_m * c.tiles_n * (k > write ? k : write);
   };
   const int64_t w0 = work(b.dx), w1 = work(b.dw);
-  if (w0 + w1 < 1 || w0 + w1 > (int64_t)8 * kPairs * 64 * 256) return b;  // eight rounds of 64 steps
-  int64_t best = b.dx.cost + b.dw.cost + 8 * 320;  // a launch and a pipeline's start: about 8 steps
+  if (w0 + w1 < 1 || w0 + w1 > (int64_t)12 * kPairs * 64 * 275) return b;  // twelve rounds of 64 steps
+  int64_t best = b.dx.cost + b.dw.cost + 3000;  // a launch and a pipeline's start
   const int share = (int)(w0 * kPairs / (w0 + w1));
   for (int d = -6; d <= 14; d += 4) {
     const int n = share + d;
