@@ -395,9 +395,9 @@ QL_API ql_status qlinear_int4(const uint16_t* x, int64_t M, int64_t K, int64_t l
  *   scale = max|v| / 127,  code = round_half_even(v / scale)  (scale 0 where max|v| < 2^-100;
  * an infinity or a NaN in a group reads back as NaN throughout it).  Columns I..P are
  * undefined.
- * Paths: without a checkpoint, M <= 32, or more where ceil(M/32) ceil(I/16) is twice the number of
- *        SMs at most: a skinny launch that streams the weights once per 32 tokens; else one tcgen05
- *        GEMM whose epilogue applies the activation and writes h and the checkpoint.
+ * Paths: without a checkpoint, M <= 16, or more where ceil(M/32) ceil(I/16) is at most four times
+ *        (M <= 32) or twice the number of SMs: a skinny launch that streams the weights once per 32
+ *        tokens; else one tcgen05 GEMM whose epilogue applies the activation and writes h and the checkpoint.
  * Requires: 1 <= M <= 2^22, H and I multiples of 8, at most 2^20, ldx >= H, ldw >= H, ldh >= I,
  * leading dimensions multiples of 8, 16-byte aligned x, w13, h and ckpt, 4-byte aligned ckpt_scale;
  * alpha finite, limit >= 0.  workspace: ql_workspace_bytes(QL_OP_GATED_FFN, M, I, H, 0, 0) bytes, zeroed once, and again

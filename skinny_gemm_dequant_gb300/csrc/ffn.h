@@ -26,12 +26,12 @@ struct FfnSkinnyArgs {
   int64_t ldy;
   float alpha, limit;     // activation of a gated block
 };
-constexpr int64_t kFfnSkinnyTokens = 32;  // tokens one pass over the weights takes
-// A forward without a checkpoint: the few-token kernel for one pass over the weights, and for more
-// while its CTAs (32 tokens, 16 outputs) are two per SM at most (64 x 2056 x 4096: 14.3 us, tcgen05
-// 20.7; 96 tokens 25.0 and 20.7; 128 x 1024 x 1024 6.4 and 9.7; 40 x 4096 x 2048 16.7 and 16.0)
+// A forward without a checkpoint goes to the few-token kernel up to 16 tokens (17408 x 5120: 60 us,
+// tcgen05 64), and with more while its CTAs (32 tokens, 16 outputs) are few: four per SM for one pass
+// over the weights (32 x 8192 x 2048 18.0 us, tcgen05 17.8; 32 x 17408 x 5120 73 and 64), two for more
+// (64 x 2056 x 4096 14.3 and 17.5; 64 x 520 x 1024 3.9 and 7.2; 40 x 4096 x 2048 16.7 and 13.0)
 inline bool ffn_few_tokens(int64_t M, int64_t I) {
-  return M <= kFfnSkinnyTokens || (M + 31) / 32 * ((I + 15) / 16) <= 2 * kNumSMs;
+  return M <= 16 || (M + 31) / 32 * ((I + 15) / 16) <= (M <= 32 ? 4 : 2) * kNumSMs;
 }
 cudaError_t launch_ffn_skinny(const FfnSkinnyArgs& a, cudaStream_t st);
 cudaError_t launch_int4(bool gated, const FfnSkinnyArgs& a, cudaStream_t st);  // kernels_int4.cu

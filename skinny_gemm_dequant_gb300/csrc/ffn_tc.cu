@@ -801,9 +801,11 @@ Cut plan_dw(int64_t M, int64_t H, int64_t I, int pairs = kPairs) { return plan(2
 struct Both {
   int dx_pairs;  // 0: one GEMM after the other
   Cut dx, dw;
+  size_t slots;  // bytes: dx and dW13 alone, one after the other, or together
 };
-Both plan_both(int64_t M, int64_t H, int64_t I) {
-  Both b = {0, plan_dx(M, H, I), plan_dw(M, H, I)};
+Both make_both(int64_t M, int64_t H, int64_t I) {
+  Both b = {0, plan_dx(M, H, I), plan_dw(M, H, I), 0};
+  b.slots = b.dx.bytes() > b.dw.bytes() ? b.dx.bytes() : b.dw.bytes();
   auto work = [](const Cut& c) {
     const int64_t k = c.nk * step_ns(c.width), write = write_ns(c.width, false);
     return (int64_t)c.tiles_m * c.tiles_n * (k > write ? k : write);
@@ -822,6 +824,21 @@ Both plan_both(int64_t M, int64_t H, int64_t I) {
     b.dx_pairs = n;
     b.dx = x;
     b.dw = w;
+  }
+  if (b.dx_pairs && b.dx.bytes() + b.dw.bytes() > b.slots) b.slots = b.dx.bytes() + b.dw.bytes();
+  return b;
+}
+
+// the plan of a thread's last sizes: a call asks for it twice (workspace, launch), a training loop
+// again every step, and it takes 1 us on the host
+const Both& plan_both(int64_t M, int64_t H, int64_t I) {
+  thread_local int64_t at[3] = {-1, -1, -1};
+  thread_local Both b;
+  if (at[0] != M || at[1] != H || at[2] != I) {
+    b = make_both(M, H, I);
+    at[0] = M;
+    at[1] = H;
+    at[2] = I;
   }
   return b;
 }
@@ -872,11 +889,7 @@ size_t ffn_forward_slots(int64_t M, int64_t H, int64_t I) {
   return a > b ? a : b;
 }
 size_t ffn_backward_slots(int64_t M, int64_t H, int64_t I) {
-  // dx and dW13 alone, one after the other, or together
-  const size_t a = plan_dx(M, H, I).bytes(), b = plan_dw(M, H, I).bytes();
-  const Both both = plan_both(M, H, I);
-  const size_t c = both.dx_pairs ? both.dx.bytes() + both.dw.bytes() : 0;
-  return a > b ? (a > c ? a : c) : (b > c ? b : c);
+  return plan_both(M, H, I).slots;
 }
 
 cudaError_t launch_ffn_forward(const FfnForward& f, cudaStream_t st) {
@@ -937,7 +950,7 @@ cudaError_t launch_ffn_backward(const FfnBackward& b, cudaStream_t st) {
   }
   if (!b.dw13) return run<DX>(xa, xb, x, plan_dx(b.M, b.H, b.I), st);
   if (!b.dx) return run<DW>(wa, wb, w, plan_dw(b.M, b.H, b.I), st);
-  const Both both = plan_both(b.M, b.H, b.I);
+  const Both& both = plan_both(b.M, b.H, b.I);
   if (!both.dx_pairs) {
     e = run<DX>(xa, xb, x, both.dx, st);
     return e != cudaSuccess ? e : run<DW>(wa, wb, w, both.dw, st);

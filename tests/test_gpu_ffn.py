@@ -84,12 +84,12 @@ SHAPES = [(1, 8, 8), (1, 512, 264), (3, 72, 40), (13, 264, 72), (32, 1024, 136),
           (128, 320, 200), (129, 8, 256), (256, 512, 128), (257, 1000, 520), (700, 264, 1032)]
 
 
-@pytest.mark.parametrize("M,H,I", SHAPES + [(33, 72, 2432), (33, 72, 2440), (40, 2056, 2448), (300, 328, 488),
+@pytest.mark.parametrize("M,H,I", SHAPES + [(16, 40, 9736), (17, 40, 9736), (32, 40, 9728), (33, 72, 2432), (33, 72, 2440), (40, 2056, 2448), (300, 328, 488),
                                          (1000, 136, 152), (2400, 64, 72), (257, 320, 1000)])
 def test_forward(ql, M, H, I):
     x, w, _ = make(M, H, I, seed=M)
     h, path = ql.gated_ffn(x, w, debug=True)
-    few = M <= 32 or -(-M // 32) * -(-I // 16) <= 304
+    few = M <= 16 or -(-M // 32) * -(-I // 16) <= (608 if M <= 32 else 304)
     assert path == ("gated_ffn_skinny" if few else "gated_ffn_tcgen05")
     check_h(h, *forward_reference(x, w, I), H)
 
