@@ -430,6 +430,18 @@ QL_API ql_status gated_ffn_backward(const uint16_t* dh, int64_t ld_dh, const uin
                                     size_t workspace_bytes, ql_stream_t stream, int* path_out);
 
 /*
+ * How the block's GEMMs are laid out for these sizes (no launch): what the tests of the split paths
+ * check their shapes by.  gemm: QL_FFN_GEMM_FORWARD (mode: QL_SAVE_*), _DX or _DW (mode: 1 if the
+ * call computes both gradients, 0 if this one alone).  out receives
+ *   [0] pairs of CTAs that share the GEMM (0: the few-token kernel, and the rest 0)
+ *   [1] columns of a tile   [2] tiles taken whole
+ *   [3] tiles after them that are cut along the summed dimension, [4] each into so many parts
+ *   [5] launches that the call's GEMMs take (both gradients: 1 side by side, 2 one after the other)
+ */
+enum { QL_FFN_GEMM_FORWARD = 0, QL_FFN_GEMM_DX = 1, QL_FFN_GEMM_DW = 2 };
+QL_API ql_status ql_gated_ffn_plan(int gemm, int64_t M, int64_t I, int64_t H, int mode, int32_t* out);
+
+/*
  * The gated block's form for few tokens on 4-bit weights: w13's 2I rows are stored, scaled and
  * required as qlinear_int4's (K = H), h and the activation are as gated_ffn's.  g and u stay in
  * fp32.  One launch per call, no workspace.

@@ -28,7 +28,7 @@ __all__ = [
     "token_amax", "qlinear_int8_w8a8_partial", "qlinear_int8_epilogue", "qlinear_fp8_block_partial",
     "qlinear_mxfp4_partial", "finish_f32",
     "qlinear_int4", "gated_ffn_int4", "gated_ffn", "gated_ffn_backward", "FFNCheckpoint", "OP_GATED_FFN",
-    "OP_GATED_FFN_BWD",
+    "OP_GATED_FFN_BWD", "gated_ffn_plan", "FFNPlan",
 ]
 
 if not os.path.exists(_LIB_PATH):
@@ -96,6 +96,9 @@ lib.gated_ffn.argtypes = [_vp, _i64, _i64, _i64, _vp, _i64, _i64, ctypes.c_float
 lib.gated_ffn_backward.restype = _int
 lib.gated_ffn_backward.argtypes = [_vp, _i64, _vp, _i64, _i64, _i64, _vp, _i64, _i64, ctypes.c_float, ctypes.c_float,
                                    _int, _vp, _vp, _vp, _i64, _vp, _i64, _vp, _sz, _vp, _ip]
+
+lib.ql_gated_ffn_plan.restype = _int
+lib.ql_gated_ffn_plan.argtypes = [_int, _i64, _i64, _i64, _int, ctypes.POINTER(ctypes.c_int32)]
 
 OP_INT8_W8A8, OP_FP8_BLOCK, OP_MXFP4, OP_MOE_MXFP4, OP_BF16, OP_FP8_CHANNEL = 1, 2, 3, 4, 5, 6
 OP_GATED_FFN, OP_GATED_FFN_BWD = 7, 8
@@ -516,7 +519,25 @@ def gated_ffn_backward(dh, x, w13, saved, *, swiglu_alpha=1.0, swiglu_limit=None
     return dx, dw
 
 
-_u32 = ctypes.c_uint32
+class FFNPlan(NamedTuple):
+    """How one GEMM of the gated block is laid out: pairs of CTAs (0: the few-token kernel), columns of
+    a tile, tiles taken whole, tiles cut along the summed dimension and parts of each, and the
+    launches of the call's GEMMs."""
+    pairs: int
+    width: int
+    whole: int
+    cut: int
+    parts: int
+    launches: int
+
+
+def gated_ffn_plan(gemm, M, I, H, *, save=None, both=True) -> FFNPlan:
+    """gemm: "forward" (with save as in gated_ffn), "dx" or "dw" (both: the call computes the other
+    gradient too).  Nothing is launched."""
+    out = (ctypes.c_int32 * 6)()
+    which = {"forward": 0, "dx": 1, "dw": 2}[gemm]
+    _check(lib.ql_gated_ffn_plan(which, M, I, H, int(both) if which else _SAVE[save], out), "ql_gated_ffn_plan")
+    return FFNPlan(*out)
 
 
 # ------------------------------------------------------------------ sharded layers

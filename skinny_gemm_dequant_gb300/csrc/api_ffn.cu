@@ -218,4 +218,19 @@ ql_status gated_ffn_backward(const uint16_t* dh, int64_t ld_dh, const uint16_t* 
   return QL_OK;
 }
 
+ql_status ql_gated_ffn_plan(int gemm, int64_t M, int64_t I, int64_t H, int mode, int32_t* out) {
+  if (!out || gemm < QL_FFN_GEMM_FORWARD || gemm > QL_FFN_GEMM_DW) return QL_ERR_INVALID_ARG;
+  if (gemm == QL_FFN_GEMM_FORWARD ? mode < QL_SAVE_NONE || mode > QL_SAVE_INT8 : mode != 0 && mode != 1)
+    return QL_ERR_INVALID_ARG;
+  const ql_status s = ffn_check(M, H, I, (H + 7) / 8 * 8, (H + 7) / 8 * 8, 1.f, 1.f);
+  if (s != QL_OK) return s;
+  for (int i = 0; i < 6; ++i) out[i] = 0;
+  if (gemm == QL_FFN_GEMM_FORWARD && mode == QL_SAVE_NONE && ffn_few_tokens(M, I)) {
+    out[5] = 1;
+    return QL_OK;
+  }
+  tc::ffn_plan(gemm, M, H, I, mode, out);
+  return QL_OK;
+}
+
 }  // extern "C"

@@ -77,6 +77,9 @@ struct FfnBackward {
   uint32_t wait_limit;
 };
 cudaError_t launch_ffn_backward(const FfnBackward& b, cudaStream_t st);
+
+// ql_gated_ffn_plan's answer for gemm (QL_FFN_GEMM_*), mode as there
+void ffn_plan(int gemm, int64_t M, int64_t H, int64_t I, int mode, int32_t* out);
 }  // namespace tc
 
 }  // namespace ql

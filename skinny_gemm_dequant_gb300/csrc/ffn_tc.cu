@@ -892,6 +892,29 @@ size_t ffn_backward_slots(int64_t M, int64_t H, int64_t I) {
   return plan_both(M, H, I).slots;
 }
 
+void ffn_plan(int gemm, int64_t M, int64_t H, int64_t I, int mode, int32_t* out) {
+  Cut c;
+  int pairs = kPairs, launches = 1;
+  if (gemm == QL_FFN_GEMM_FORWARD) {
+    c = plan_fwd(M, H, I, mode == QL_SAVE_INT8);
+  } else if (!mode) {
+    c = gemm == QL_FFN_GEMM_DX ? plan_dx(M, H, I) : plan_dw(M, H, I);
+  } else {
+    const Both& b = plan_both(M, H, I);
+    c = gemm == QL_FFN_GEMM_DX ? b.dx : b.dw;
+    if (!b.dx_pairs)
+      launches = 2;
+    else
+      pairs = gemm == QL_FFN_GEMM_DX ? b.dx_pairs : kPairs - b.dx_pairs;
+  }
+  out[0] = pairs;
+  out[1] = c.width;
+  out[2] = c.whole;
+  out[3] = c.cut;
+  out[4] = c.parts;
+  out[5] = launches;
+}
+
 cudaError_t launch_ffn_forward(const FfnForward& f, cudaStream_t st) {
   CUtensorMap ta, tb;
   const Cut c = plan_fwd(f.M, f.H, f.I, f.save == QL_SAVE_INT8);
