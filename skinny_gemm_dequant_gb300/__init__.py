@@ -146,6 +146,7 @@ class Workspace:
     def __init__(self, device=None):
         self.device = torch.device(device if device is not None else "cuda")
         self.buf = None
+        self._recorded = []  # buffers that graphs hold the addresses of: not freed by a larger call
 
     def get(self, nbytes: int, stream=None) -> torch.Tensor:
         if self.buf is None or self.buf.numel() < nbytes:
@@ -427,17 +428,37 @@ class FFNCheckpoint(NamedTuple):
 
 _ffn_bytes = functools.lru_cache(maxsize=256)(workspace_bytes)
 _ffn_workspaces: dict = {}
+_ZERO_BYTES = 256 + (1 << 20)  # of a workspace's start: the status word and what is zero between calls
 
 
-def _ffn_ws(device, op, M, I, H, stream, workspace):
+def _capturing(stream):
+    if stream is None:
+        return torch.cuda.is_current_stream_capturing()
+    with torch.cuda.stream(stream):
+        return torch.cuda.is_current_stream_capturing()
+
+
+def _ffn_ws(x, op, M, I, H, stream, workspace, cut):
     """The caller's workspace, or one per device and stream (the current stream's handle if none is
-    given): calls on different streams do not share one.  Allocated from its stream's own pool."""
+    given), allocated from its stream's own pool.  While the stream is captured, a workspace that is
+    large enough already, kept from then on for the graph's sake, or else memory of the graph's own:
+    one that is kept for later calls would be zeroed by that graph alone and shared with every graph
+    that is captured on the same stream.  cut() says whether the call counts on zeroed tickets."""
     nbytes = _ffn_bytes(op, M, I, H)
+    if _capturing(stream):
+        if workspace is not None and workspace.buf is not None and workspace.buf.numel() >= nbytes:
+            if not any(b is workspace.buf for b in workspace._recorded):
+                workspace._recorded.append(workspace.buf)
+            return workspace.buf
+        buf = _empty((nbytes,), torch.uint8, x, stream)
+        if cut():
+            _check(lib.ql_workspace_init(_ptr(buf), _ZERO_BYTES, _stream(stream)), "ql_workspace_init")
+        return buf
     if workspace is None:
-        key = (device.index, _stream(stream))
+        key = (x.device.index, _stream(stream))
         workspace = _ffn_workspaces.get(key)
         if workspace is None:
-            workspace = _ffn_workspaces.setdefault(key, Workspace(device))
+            workspace = _ffn_workspaces.setdefault(key, Workspace(x.device))
     if stream is None or (workspace.buf is not None and workspace.buf.numel() >= nbytes):
         return workspace.get(nbytes, stream)
     with torch.cuda.stream(stream):
@@ -463,7 +484,9 @@ def gated_ffn(x, w13, *, swiglu_alpha=1.0, swiglu_limit=None, save=None, debug=F
     """h = silu(alpha * min(g, limit)) * clamp(u, +-limit) with g, u = x W13^T, in one launch.  x: bf16
     [M, H]; w13: bf16 [2I, H], rows [0, I) gate and [I, 2I) up; H and I multiples of 8.  save: None,
     "bf16" or "int8" also returns an FFNCheckpoint of g and u: (h, checkpoint).  debug=True appends
-    the path."""
+    the path.  Without a workspace one is kept per device and stream; a captured call takes memory of
+    its graph's own, and zeroes its tickets in the graph where it uses any (none with a workspace that
+    is large enough when the capture starts)."""
     _bf16(x, "x")
     M, H, I, ldx, ldw = _ffn_weights(x, w13)
     if save not in _SAVE:
@@ -476,7 +499,8 @@ def gated_ffn(x, w13, *, swiglu_alpha=1.0, swiglu_limit=None, save=None, debug=F
         if save == "int8":
             scale = _empty((M, 2, P // 128), torch.float32, x, stream)
         saved = FFNCheckpoint(save, data, scale)
-    ws = _ffn_ws(x.device, OP_GATED_FFN, M, I, H, stream, workspace)
+    ws = _ffn_ws(x, OP_GATED_FFN, M, I, H, stream, workspace,
+                 lambda: gated_ffn_plan("forward", M, I, H, save=save).cut)
     path = ctypes.c_int(0) if debug else None
     st = lib.gated_ffn(x.data_ptr(), M, H, ldx, w13.data_ptr(), I, ldw, swiglu_alpha, _inf(swiglu_limit), h.data_ptr(),
                        I if out is None else h.stride(0), _SAVE[save], _ptr(data), _ptr(scale), ws.data_ptr(),
@@ -509,7 +533,9 @@ def gated_ffn_backward(dh, x, w13, saved, *, swiglu_alpha=1.0, swiglu_limit=None
         raise ValueError("saved must be the FFNCheckpoint of this x and w13")
     dx = _out(out_dx, M, H, x, stream, "out_dx") if need_dx else None
     dw = _out(out_dw, 2 * I, H, x, stream, "out_dw") if need_dw else None
-    ws = _ffn_ws(x.device, OP_GATED_FFN_BWD, M, I, H, stream, workspace)
+    ws = _ffn_ws(x, OP_GATED_FFN_BWD, M, I, H, stream, workspace, lambda: (
+        (need_dx and gated_ffn_plan("dx", M, I, H, both=need_dw).cut)
+        or (need_dw and gated_ffn_plan("dw", M, I, H, both=need_dx).cut)))
     st = lib.gated_ffn_backward(dh.data_ptr(), dh.stride(0), x.data_ptr(), M, H, ldx, w13.data_ptr(), I, ldw,
                                 swiglu_alpha, _inf(swiglu_limit), _SAVE[mode], data.data_ptr(), _ptr(scale), _ptr(dx),
                                 0 if dx is None else dx.stride(0), _ptr(dw), 0 if dw is None else dw.stride(0),
