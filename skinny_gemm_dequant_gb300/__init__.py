@@ -14,6 +14,7 @@ import ctypes
 import functools
 import math
 import os
+import threading
 from typing import NamedTuple
 
 import torch
@@ -146,6 +147,7 @@ class Workspace:
     def __init__(self, device=None):
         self.device = torch.device(device if device is not None else "cuda")
         self.buf = None
+        self.lock = threading.Lock()  # held from the choice of the buffer to a gated block call's last launch
         self._recorded = []  # buffers that graphs hold the addresses of: not freed by a larger call
 
     def get(self, nbytes: int, stream=None) -> torch.Tensor:
@@ -438,31 +440,56 @@ def _capturing(stream):
         return torch.cuda.is_current_stream_capturing()
 
 
-def _ffn_ws(x, op, M, I, H, stream, workspace, cut):
-    """The caller's workspace, or one per device and stream (the current stream's handle if none is
-    given), allocated from its stream's own pool.  While the stream is captured, a workspace that is
-    large enough already, kept from then on for the graph's sake, or else memory of the graph's own:
-    one that is kept for later calls would be zeroed by that graph alone and shared with every graph
-    that is captured on the same stream.  cut() says whether the call counts on zeroed tickets."""
-    nbytes = _ffn_bytes(op, M, I, H)
-    if _capturing(stream):
-        if workspace is not None and workspace.buf is not None and workspace.buf.numel() >= nbytes:
-            if not any(b is workspace.buf for b in workspace._recorded):
-                workspace._recorded.append(workspace.buf)
-            return workspace.buf
-        buf = _empty((nbytes,), torch.uint8, x, stream)
-        if cut():
-            _check(lib.ql_workspace_init(_ptr(buf), _ZERO_BYTES, _stream(stream)), "ql_workspace_init")
-        return buf
-    if workspace is None:
-        key = (x.device.index, _stream(stream))
-        workspace = _ffn_workspaces.get(key)
-        if workspace is None:
-            workspace = _ffn_workspaces.setdefault(key, Workspace(x.device))
-    if stream is None or (workspace.buf is not None and workspace.buf.numel() >= nbytes):
-        return workspace.get(nbytes, stream)
-    with torch.cuda.stream(stream):
-        return workspace.get(nbytes, stream)
+class _FFNScratch:
+    """A gated block call's workspace, locked while its launches are put on the stream:
+
+        with _FFNScratch(...) as ws:  # the buffer
+
+    The caller's Workspace, or one per device and stream (the current stream's handle if none is
+    given), allocated from its stream's own pool.  A backward pass is two or three launches that hand
+    [dg du] on in the workspace, and ctypes lets other threads run meanwhile: without the lock a
+    thread's launches on the same stream could come between another's.
+
+    While the stream is captured: a given Workspace that is large enough already, kept from then on
+    for the graph's sake, or else memory of the graph's own: one that is kept for later calls would be
+    zeroed by that graph alone and shared with every graph that is captured on the same stream.
+    cut() says whether the call counts on zeroed tickets."""
+
+    __slots__ = ("ws", "nbytes", "stream", "recorded")
+
+    def __init__(self, x, op, M, I, H, stream, workspace, cut):
+        self.nbytes, self.stream, self.recorded = _ffn_bytes(op, M, I, H), stream, _capturing(stream)
+        if self.recorded:
+            if workspace is None or workspace.buf is None or workspace.buf.numel() < self.nbytes:
+                workspace = Workspace(x.device)
+                workspace.buf = _empty((self.nbytes,), torch.uint8, x, stream)
+                if cut():
+                    _check(lib.ql_workspace_init(_ptr(workspace.buf), _ZERO_BYTES, _stream(stream)), "ql_workspace_init")
+        elif workspace is None:
+            key = (x.device.index, _stream(stream))
+            workspace = _ffn_workspaces.get(key)
+            if workspace is None:
+                workspace = _ffn_workspaces.setdefault(key, Workspace(x.device))
+        self.ws = workspace
+
+    def __enter__(self):
+        ws = self.ws
+        ws.lock.acquire()
+        try:
+            if self.stream is None or (ws.buf is not None and ws.buf.numel() >= self.nbytes):
+                buf = ws.get(self.nbytes, self.stream)
+            else:
+                with torch.cuda.stream(self.stream):
+                    buf = ws.get(self.nbytes, self.stream)
+            if self.recorded and not any(b is buf for b in ws._recorded):
+                ws._recorded.append(buf)
+            return buf
+        except BaseException:
+            ws.lock.release()
+            raise
+
+    def __exit__(self, *exc):
+        self.ws.lock.release()
 
 
 _SAVE = {None: SAVE_NONE, "bf16": SAVE_BF16, "int8": SAVE_INT8}
@@ -499,12 +526,12 @@ def gated_ffn(x, w13, *, swiglu_alpha=1.0, swiglu_limit=None, save=None, debug=F
         if save == "int8":
             scale = _empty((M, 2, P // 128), torch.float32, x, stream)
         saved = FFNCheckpoint(save, data, scale)
-    ws = _ffn_ws(x, OP_GATED_FFN, M, I, H, stream, workspace,
-                 lambda: gated_ffn_plan("forward", M, I, H, save=save).cut)
     path = ctypes.c_int(0) if debug else None
-    st = lib.gated_ffn(x.data_ptr(), M, H, ldx, w13.data_ptr(), I, ldw, swiglu_alpha, _inf(swiglu_limit), h.data_ptr(),
-                       I if out is None else h.stride(0), _SAVE[save], _ptr(data), _ptr(scale), ws.data_ptr(),
-                       ws.numel(), _stream(stream), path)
+    with _FFNScratch(x, OP_GATED_FFN, M, I, H, stream, workspace,
+                     lambda: gated_ffn_plan("forward", M, I, H, save=save).cut) as ws:
+        st = lib.gated_ffn(x.data_ptr(), M, H, ldx, w13.data_ptr(), I, ldw, swiglu_alpha, _inf(swiglu_limit),
+                           h.data_ptr(), I if out is None else h.stride(0), _SAVE[save], _ptr(data), _ptr(scale),
+                           ws.data_ptr(), ws.numel(), _stream(stream), path)
     if st:
         raise QLError(st, "gated_ffn")
     res = (h,) if saved is None else (h, saved)
@@ -533,13 +560,13 @@ def gated_ffn_backward(dh, x, w13, saved, *, swiglu_alpha=1.0, swiglu_limit=None
         raise ValueError("saved must be the FFNCheckpoint of this x and w13")
     dx = _out(out_dx, M, H, x, stream, "out_dx") if need_dx else None
     dw = _out(out_dw, 2 * I, H, x, stream, "out_dw") if need_dw else None
-    ws = _ffn_ws(x, OP_GATED_FFN_BWD, M, I, H, stream, workspace, lambda: (
-        (need_dx and gated_ffn_plan("dx", M, I, H, both=need_dw).cut)
-        or (need_dw and gated_ffn_plan("dw", M, I, H, both=need_dx).cut)))
-    st = lib.gated_ffn_backward(dh.data_ptr(), dh.stride(0), x.data_ptr(), M, H, ldx, w13.data_ptr(), I, ldw,
-                                swiglu_alpha, _inf(swiglu_limit), _SAVE[mode], data.data_ptr(), _ptr(scale), _ptr(dx),
-                                0 if dx is None else dx.stride(0), _ptr(dw), 0 if dw is None else dw.stride(0),
-                                ws.data_ptr(), ws.numel(), _stream(stream), None)
+    with _FFNScratch(x, OP_GATED_FFN_BWD, M, I, H, stream, workspace, lambda: (
+            (need_dx and gated_ffn_plan("dx", M, I, H, both=need_dw).cut)
+            or (need_dw and gated_ffn_plan("dw", M, I, H, both=need_dx).cut))) as ws:
+        st = lib.gated_ffn_backward(dh.data_ptr(), dh.stride(0), x.data_ptr(), M, H, ldx, w13.data_ptr(), I, ldw,
+                                    swiglu_alpha, _inf(swiglu_limit), _SAVE[mode], data.data_ptr(), _ptr(scale), _ptr(dx),
+                                    0 if dx is None else dx.stride(0), _ptr(dw), 0 if dw is None else dw.stride(0),
+                                    ws.data_ptr(), ws.numel(), _stream(stream), None)
     if st:
         raise QLError(st, "gated_ffn_backward")
     return dx, dw
