@@ -401,7 +401,8 @@ QL_API ql_status qlinear_int4(const uint16_t* x, int64_t M, int64_t K, int64_t l
  * Requires: 1 <= M <= 2^22, H and I multiples of 8, at most 2^20, ldx >= H, ldw >= H, ldh >= I,
  * leading dimensions multiples of 8, 16-byte aligned x, w13, h and ckpt, 4-byte aligned ckpt_scale;
  * alpha finite, limit >= 0.  workspace: ql_workspace_bytes(QL_OP_GATED_FFN, M, I, H, 0, 0) bytes,
- * zeroed once, and again after a call that raised QL_DEV_TIMEOUT (its tickets may be left mid-count).
+ * zeroed once.  Outputs of a call that raised QL_DEV_TIMEOUT in its status word are incomplete; the
+ * next call needs nothing.
  */
 QL_API ql_status gated_ffn(const uint16_t* x, int64_t M, int64_t H, int64_t ldx, const uint16_t* w13, int64_t I,
                            int64_t ldw, float swiglu_alpha, float swiglu_limit, uint16_t* h, int64_t ldh, int save,

@@ -168,7 +168,14 @@ def _ws(device, nbytes, stream, workspace):
     return workspace.get(nbytes, stream)
 
 
-def read_device_status(ws: torch.Tensor, clear: bool = True, stream=None):
+def read_device_status(ws: torch.Tensor | None = None, clear: bool = True, stream=None):
+    """(status, flags) of a workspace's status word: of ws, or, without one, of all default workspaces
+    on the current device together, whose work is waited for."""
+    if ws is None:
+        torch.cuda.synchronize()
+        bufs = [w.buf for w in (*_default_ws.values(), *_ffn_workspaces.values()) if w.buf is not None]
+        both = [read_device_status(b, clear, stream) for b in bufs if b.device.index == torch.cuda.current_device()]
+        return max((st for st, _ in both), default=0), functools.reduce(int.__or__, (f for _, f in both), 0)
     flags = _u32(0)
     st = lib.ql_read_device_status(_ptr(ws), _stream(stream), int(clear), ctypes.byref(flags))
     return st, int(flags.value)

@@ -35,7 +35,8 @@
 // short ones those 7 us and the parts' way through L2; the weights' HBM traffic for few tokens (64 x
 // 17408 x 5120 forward 65 us, 5.5 TB/s) and the writing of dW13.
 // Every wait is bounded; one that runs out raises QL_DEV_TIMEOUT in the status word and the pair
-// leaves its loops, waits for copies and MMAs in flight and frees its tensor memory.
+// leaves its loops, waits for copies and MMAs in flight and frees its tensor memory.  Its part of a cut
+// tile counts in as missing, so that the next call finds the tickets as it needs them.
 #include <cudaTypedefs.h>
 
 #include <atomic>
@@ -85,6 +86,7 @@ struct Params {
   uint32_t* status;
   uint32_t wait_limit;
 };
+constexpr unsigned kMissing = 1u << 16;  // of a ticket: a part that was not computed
 constexpr int64_t kSlotFloats = 256 * 128;  // one CTA's sums of a part
 
 // what a pair works on, one item after the other: whole tiles, then a part of a cut one
@@ -429,6 +431,16 @@ __device__ __forceinline__ void gemm(const CUtensorMap& tmA, const CUtensorMap& 
     const int q = warp & 3, half = (warp - 4) >> 2;  // tensor-memory lane quadrant, column half
     const int r = 32 * q + lane;                     // row of this CTA's 128
     const uint32_t stage = base + kStages * kStageBytes + (uint32_t)(warp - 4) * kRowStage;
+    // counts a part of cut tile `c` in; true for the last one if every part is there.  That one leaves
+    // the ticket at zero for the next call
+    auto count_in = [&](int c, unsigned add) {
+      unsigned* ticket = p.tickets + 2 * c + rank;
+      const unsigned before = atomicAdd(ticket, add);
+      if ((before & (kMissing - 1)) != (unsigned)(p.parts - 1)) return false;
+      *ticket = 0;
+      return before < kMissing;
+    };
+    bool counted = pair >= p.cut * p.parts;  // no part is this pair's
     int n = 0, t, k0, k1;
     for (Walk w(pair); w.next(p, pairs, t, k0, k1); ++n) {
       int tm, tn;
@@ -557,12 +569,11 @@ __device__ __forceinline__ void gemm(const CUtensorMap& tmA, const CUtensorMap& 
         }
         __threadfence();
         epilogue_any(false);  // every warp's part is stored and fenced
-        unsigned* ticket = p.tickets + 2 * (t - p.whole) + rank;
-        if (threadIdx.x == 128) s_last = atomicAdd(ticket, 1u) == (unsigned)(p.parts - 1);
+        if (threadIdx.x == 128) s_last = count_in(t - p.whole, 1u);
+        counted = true;
         epilogue_any(false);
         if (s_last) {
           __threadfence();  // the other parts were fenced before their counts
-          if (threadIdx.x == 128) *ticket = 0;  // every part has counted in: ready for the next call
           // the parts in the order of K, this CTA's own where it stands in it, back to tensor memory
           const int mine = pair / p.cut;
 #pragma unroll 1
@@ -602,6 +613,9 @@ __device__ __forceinline__ void gemm(const CUtensorMap& tmA, const CUtensorMap& 
       }
       release();
     }
+    // a pair that gave up counts its part in as missing, and its tile is not finished: the tickets are
+    // zero after every launch, whatever ran out
+    if (!counted && threadIdx.x == 128) count_in(pair % p.cut, 1u + kMissing);
   }
   tc_fence_before();
   __syncthreads();
