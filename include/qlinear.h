@@ -367,7 +367,7 @@ QL_API ql_status qlinear_int8_w8a8_noalloc(const uint16_t* x, int64_t M, int64_t
  *   y[m,n] = bf16( sum_k x[m,k] * w[n,k] )  then, if bias, y = bf16(y + bias[n])
  * q: codes 0..15 packed two per byte, element 2i in the LOW nibble of byte i, rows of
  * ldw_bytes; s: bf16 (QL_SCALE_BF16) or fp16 (QL_SCALE_FP16) bits [N, lds], lds >=
- * ceil(K/group), |s| < 2^122; z: uint8 [N, ldz] holding 0..127, or NULL for 8 everywhere (symmetric
+ * ceil(K/group), |s| < 2^122; z: uint8 [N, ldz], or NULL for 8 everywhere (symmetric
  * codes);
  * x: bf16 [M, ldx]; bias: nullable bf16 [N]; y: bf16 [M, ldy].  q - z is exact in bf16, its
  * products with x are exact in fp32 and every group's fp32 sum is multiplied by its scale once:

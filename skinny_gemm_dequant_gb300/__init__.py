@@ -386,7 +386,7 @@ def _out(out, M, N, x, stream, name="out"):
 def qlinear_int4(x, w, w_scale, w_zero=None, bias=None, *, group=128, debug=False, out=None, stream=None):
     """y = x W^T (+ bias after the bf16 cast) on 4-bit weights w[n,k] = (q - zero) * scale per group
     of K.  x: bf16 [M, K]; w: uint8 [N, >=K/2], element 2i in the low nibble of byte i; w_scale: bf16
-    or fp16 [N, >=ceil(K/group)]; w_zero: uint8 [N, >=ceil(K/group)] (values 0..127) or None: 8.
+    or fp16 [N, >=ceil(K/group)]; w_zero: uint8 [N, >=ceil(K/group)] or None: 8.
     group: a power of two >= 32.  With debug=True returns (y, path)."""
     _bf16(x, "x")
     (M, K), sx = x.shape, x.stride()

@@ -1,7 +1,7 @@
 // Linear layers on 4-bit integer weights with group scales, for few tokens: y = x W^T, and the gated
 // block h = silu(a min(g, L)) clamp(u, -L, L) on such weights, streaming them once per 32 tokens.
 //
-//   w[n,k] = (q[n,k] - z[n,k/G]) * s[n,k/G],   q in 0..15, z in 0..127 (8 without zero points)
+//   w[n,k] = (q[n,k] - z[n,k/G]) * s[n,k/G],   q in 0..15, z in 0..255 (8 without zero points)
 //   y[m,n] = bf16( sum_groups s * sum_{k in group} x[m,k] (q - z) )      (+ bias after the cast)
 //
 // q - z is exact in bf16 and a bf16 product is exact in fp32, so the warp MMA (bf16 operands, fp32
@@ -302,7 +302,7 @@ __global__ void __launch_bounds__(W * 32) int4_kernel(const __grid_constant__ Ff
 #pragma unroll
           for (int h = 0; h < 2; ++h)
             sz[i][mt][h] = __float_as_uint(scale_to_f32(s_next[i][mt][h], a.scale_fp16) * 64.f) |
-                           (ZP ? z_next[i][mt][h] & 127u : 0u);
+                           (ZP ? z_next[i][mt][h] : 0u);
       if (b0 + kw * SB < c1) scales(b0 + kw * SB);
 #pragma unroll
       for (int sb = 0; sb < SB; ++sb) {
@@ -337,8 +337,8 @@ __global__ void __launch_bounds__(W * 32) int4_kernel(const __grid_constant__ Ff
               for (int h = 0; h < 2; ++h) {
                 const uint32_t v = FINE ? __shfl_sync(0xffffffffu, sz[FINE ? sb : 0][mt][h], j, 4)
                                         : __shfl_sync(0xffffffffu, sz[FINE ? 0 : sb / 4][mt][h], sb & 3, 4);
-                sc[mt][h] = __uint_as_float(ZP ? v & ~127u : v);
-                negz[mt][h] = ZP ? fma_bf16x2((v & 127u) * 0x10001u, kNegMul, 0u) : negz8;
+                sc[mt][h] = __uint_as_float(ZP ? v & ~255u : v);
+                negz[mt][h] = ZP ? fma_bf16x2((v & 255u) * 0x10001u, kNegMul, 0u) : negz8;
               }
           }
           uint4 bx[NT];
