@@ -4,10 +4,11 @@ dW13, with both gradients in one launch and in two that share the workspace.  Th
 to be cut by the library's own plan.
 
 Tolerances.  One by one as in test_gpu_ffn.py.  Of the whole output, ||got - exact|| / ||exact||:
-  h         rounded once to bf16 (half an ulp: 2^-9 relative), 2^-17 for the activation and 2^-19 for
-            fp32 sums: under 1.1 * 2^-9
-  dx, dW13  that, and dg, du rounded to bf16 before the sums: 2^-9 of every term, whose signs are
-            random: under 2^-8 in all
+  h         rounded once to bf16: errors spread evenly over +-2^-8 of a number's power of two, 0.8 to
+            0.9 * 2^-9 of the norm over numbers of all leading digits; 2^-17 for the activation and
+            2^-19 for fp32 sums: under 1.1 * 2^-9
+  dx, dW13  that, and dg, du rounded to bf16 before the sums: as much again of terms whose errors are
+            independent, a square root of two in all: under 2^-8
 A step of 64 lost from one tile's sum is off by 0.0068 of the norm or more at the sizes here."""
 import numpy as np
 import pytest
