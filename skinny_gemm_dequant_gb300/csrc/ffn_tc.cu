@@ -39,7 +39,6 @@
 // tile counts in as missing, so that the next call finds the tickets as it needs them.
 #include <cudaTypedefs.h>
 
-#include <atomic>
 #include <cstdio>
 #include <mutex>
 #include <utility>
@@ -886,12 +885,8 @@ constexpr size_t kSmem = 1024 + kStages * kStageBytes + 8 * kRowStage;
 template <int MODE>
 cudaError_t run(const CUtensorMap& ta, const CUtensorMap& tb, Params& p, const Cut& c, cudaStream_t st) {
   take(p, c);
-  static std::atomic<int> attr{0};
-  if (!attr.load()) {
-    const cudaError_t e = raise_smem_limit(ffn_gemm_kernel<MODE>);
-    if (e != cudaSuccess) return e;
-    attr.store(1);
-  }
+  static OncePerDevice once;
+  if (const cudaError_t e = raise_smem_limit(ffn_gemm_kernel<MODE>, once); e != cudaSuccess) return e;
   const int busy = c.whole > c.cut * c.parts ? c.whole : c.cut * c.parts;
   return launch_pdl(ffn_gemm_kernel<MODE>, dim3(2 * (busy < kPairs ? busy : kPairs)), kThreads, kSmem, st, ta, tb, p);
 }
@@ -996,12 +991,9 @@ cudaError_t launch_ffn_backward(const FfnBackward& b, cudaStream_t st) {
   take(w, both.dw);
   w.slots += both.dx.bytes() / sizeof(float);
   w.tickets += 2 * kPairs;
-  static std::atomic<int> attr{0};
-  if (!attr.load()) {
-    e = raise_smem_limit(ffn_gemms_kernel);
-    if (e != cudaSuccess) return e;
-    attr.store(1);
-  }
+  static OncePerDevice once;
+  e = raise_smem_limit(ffn_gemms_kernel, once);
+  if (e != cudaSuccess) return e;
   return launch_pdl(ffn_gemms_kernel, dim3(2 * kPairs), kThreads, kSmem, st, xa, xb, wa, wb, x, w, both.dx_pairs);
 }
 

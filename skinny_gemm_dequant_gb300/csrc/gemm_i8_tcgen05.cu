@@ -28,7 +28,6 @@
 // freed before the CTA exits.
 #include <cudaTypedefs.h>
 
-#include <atomic>
 #include <cstdio>
 #include <mutex>
 
@@ -573,13 +572,10 @@ cudaError_t launch_i8_gemm(const I8GemmArgs& g, cudaStream_t st) {
     p.tma_y = 1;
 
   const size_t smem = 1024 + (size_t)S * stage + (size_t)(3 * S + 5) * 8;
-  static std::atomic<int> attr{0};
-  if (!attr.load()) {
-    e = raise_smem_limit(i8_gemm_kernel<false>);
-    if (e == cudaSuccess) e = raise_smem_limit(i8_gemm_kernel<true>);
-    if (e != cudaSuccess) return e;
-    attr.store(1);
-  }
+  static OncePerDevice once[2];
+  e = raise_smem_limit(i8_gemm_kernel<false>, once[0]);
+  if (e == cudaSuccess) e = raise_smem_limit(i8_gemm_kernel<true>, once[1]);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((g.N + 127) / 128), (unsigned)((g.M + p.tt - 1) / p.tt), (unsigned)p.ks);
   cfg.blockDim = dim3(kI8Threads, 1, 1);

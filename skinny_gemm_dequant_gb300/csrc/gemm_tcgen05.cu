@@ -20,7 +20,6 @@
 #include <cudaTypedefs.h>
 
 #include <cstdio>
-#include <atomic>
 #include <mutex>
 
 #include "gemm_tcgen05.h"
@@ -571,12 +570,8 @@ cudaError_t launch_gemm(const GemmArgs& g, cudaStream_t st) {
   }
 
   const size_t smem = 1024 + (size_t)S * stage + (size_t)(3 * S + 2) * 8 + extra;
-  static std::atomic<int> attr_set{0};
-  if (!attr_set.load()) {
-    cudaError_t e = raise_smem_limit(tc_gemm_kernel);
-    if (e != cudaSuccess) return e;
-    attr_set.store(1);
-  }
+  static OncePerDevice once;
+  if (const cudaError_t e = raise_smem_limit(tc_gemm_kernel, once); e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   const unsigned gy = g.grouped ? (unsigned)g.tiles_max : (unsigned)((g.M + p.tt - 1) / p.tt);
   cfg.gridDim = dim3((unsigned)((g.N + kBlockN - 1) / kBlockN), gy, 1);

@@ -4,6 +4,7 @@
 #include <cstdint>
 #include <cuda_runtime.h>
 
+#include "per_device.h"
 #include "skinny.cuh"
 
 namespace ql {
@@ -109,13 +110,12 @@ cudaError_t launch_finish_f32(const float* y32, int M, int N, int64_t ld32, cons
                               int64_t ldy, cudaStream_t st);
 
 // Raise a kernel's dynamic shared-memory limit to the device's opt-in maximum minus its static
-// shared memory.  Done once per kernel, before any launch, so calls made during CUDA-graph
-// capture only enqueue work.
+// shared memory.  Done once per kernel and device (`once` is the kernel's), before any launch, so
+// calls made during CUDA-graph capture only enqueue work.
 template <class F>
-cudaError_t raise_smem_limit(F* kfn) {
-  int dev = 0, optin = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
+cudaError_t raise_smem_limit(F* kfn, int dev) {
+  int optin = 0;
+  cudaError_t e = cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
   cudaFuncAttributes fa;
   if (e == cudaSuccess) e = cudaFuncGetAttributes(&fa, kfn);
   if (e == cudaSuccess)
@@ -123,6 +123,12 @@ cudaError_t raise_smem_limit(F* kfn) {
   // prefer the largest shared-memory carveout, so kernels sized for several CTAs per SM get them
   if (e == cudaSuccess) e = cudaFuncSetAttribute(kfn, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
   return e;
+}
+template <class F>
+cudaError_t raise_smem_limit(F* kfn, OncePerDevice& once) {
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  return e != cudaSuccess ? e : once.run(dev, cudaSuccess, [&] { return raise_smem_limit(kfn, dev); });
 }
 
 }  // namespace ql

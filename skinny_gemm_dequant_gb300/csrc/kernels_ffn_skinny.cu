@@ -13,7 +13,6 @@
 // Bound by HBM for large weights: 1 token x 17408 x 5120 (356 MB) 54.2 us, 6.6 TB/s, 0.97 of the
 // measured copy rate; 13 x 2056 x 4096 (34 MB) 8.3 us, where launch, first loads and the joining of
 // the K shares are half of it.
-#include <atomic>
 
 #include "common.cuh"
 #include "ffn.h"
@@ -194,12 +193,8 @@ __global__ void __launch_bounds__(kWarps * 32) ffn_skinny_kernel(const __grid_co
 template <int NT, int kDepth, int kWarps>
 cudaError_t launch(const FfnSkinnyArgs& a, cudaStream_t st) {
   auto* kfn = ffn_skinny_kernel<NT, kDepth, kWarps>;
-  static std::atomic<int> attr{0};
-  if (!attr.load()) {
-    const cudaError_t e = raise_smem_limit(kfn);
-    if (e != cudaSuccess) return e;
-    attr.store(1);
-  }
+  static OncePerDevice once;
+  if (const cudaError_t e = raise_smem_limit(kfn, once); e != cudaSuccess) return e;
   const dim3 grid((unsigned)((a.N + kOut - 1) / kOut), (unsigned)((a.M + NT * 8 - 1) / (NT * 8)));
   // K over a cluster's CTAs while all of them find a place at once (16 warps per SM; 96 x 1024 x 2048 in
   // two waves 14.9 us, unsplit 8.6) and every warp keeps four blocks or more (13 x 2056 x 4096, 8 warps:

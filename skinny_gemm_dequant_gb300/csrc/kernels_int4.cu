@@ -26,7 +26,6 @@
 // uses them took 11 us of 35.
 #include <cuda_fp16.h>
 
-#include <atomic>
 
 #include "common.cuh"
 #include "ffn.h"
@@ -446,12 +445,8 @@ template <bool GATED, int NT, bool FINE, bool ZP, bool XS, int SEG, int kDepth, 
 cudaError_t launch(const FfnSkinnyArgs& a, int rw_log2, cudaStream_t st) {
   constexpr int MT = 2;
   auto* kfn = int4_kernel<GATED, MT, NT, FINE, ZP, XS, SEG, kDepth, W>;
-  static std::atomic<int> attr{0};
-  if (!attr.load()) {
-    const cudaError_t e = raise_smem_limit(kfn);
-    if (e != cudaSuccess) return e;
-    attr.store(1);
-  }
+  static OncePerDevice once;
+  if (const cudaError_t e = raise_smem_limit(kfn, once); e != cudaSuccess) return e;
   const int nblk = (a.K + kBlockK - 1) / kBlockK;
   Plan p = {};
   p.rw_log2 = rw_log2;

@@ -1,5 +1,4 @@
 // Instantiations and launch of the skinny weight-streaming GEMM (see skinny.cuh).
-#include <atomic>
 
 #include "internal.h"
 
@@ -41,12 +40,8 @@ static cudaError_t launch_one(const SkinnyArgs& a, dim3 grid, cudaStream_t st, b
   const size_t smem = skinny_smem_bytes<FMT, MT>(a.kc);
   // raise the dynamic shared-memory limit once (to the largest size seen), so that calls made
   // during CUDA-graph capture only enqueue the launch
-  static std::atomic<int> attr_set{0};
-  if (!attr_set.load()) {
-    cudaError_t err = raise_smem_limit(kfn);
-    if (err != cudaSuccess) return err;
-    attr_set.store(1);
-  }
+  static OncePerDevice once;
+  if (const cudaError_t e = raise_smem_limit(kfn, once); e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(SK_THREADS, 1, 1);

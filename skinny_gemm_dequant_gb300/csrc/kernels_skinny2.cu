@@ -150,12 +150,8 @@ static cudaError_t launch2(const Skinny2Plan& p, Skinny2Args a, const uint8_t* w
     if (!mapnd(&tx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, a.x16, 4, d, st, b)) return cudaErrorInvalidValue;
   }
   auto kfn = skinny2_kernel<FMT, MT, KIND>;
-  static std::atomic<int> attr{0};
-  if (!attr.load()) {
-    cudaError_t e = raise_smem_limit(kfn);
-    if (e != cudaSuccess) return e;
-    attr.store(1);
-  }
+  static OncePerDevice once;
+  if (const cudaError_t e = raise_smem_limit(kfn, once); e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)p.grid, 1, 1);
   cfg.blockDim = dim3(S2_THREADS, 1, 1);
