@@ -37,10 +37,10 @@ namespace ql {
 namespace {
 
 constexpr int kBlockK = 128;
+constexpr int kRowTiles = 2;  // of 16 rows, a warp
 constexpr int kPrefetch = 2;  // steps
 
 struct Plan {
-  int rw_log2;  // warps of a CTA on different rows; the others split K
   int chunk;    // staged activations: blocks of K at a time
   int x_bytes;  // of them
 };
@@ -115,13 +115,17 @@ __device__ __forceinline__ float ld_cta(uint32_t saddr, uint32_t rank) {
   return v;
 }
 
-// MT: 16-row tiles of a warp; NT: 8-token tiles; FINE: groups shorter than 128; ZP: zero points
-// given; XS: one token, staged for the CTA, else the activations travel in the warps' rings;
-// SEG: bytes of a row that a step copies; kDepth: steps in a ring; W: warps.
+// NT: 8-token tiles; FINE: groups shorter than 128; ZP: zero points given; XS: one token, staged for
+// the CTA, else the activations travel in the warps' rings; SEG: bytes of a row that a step copies;
+// kDepth: steps in a ring; W: warps, on RW row groups; the warps of a row group, two at least, split K.
 // gridDim.z CTAs (a cluster) take contiguous shares of K.
-template <bool GATED, int MT, int NT, bool FINE, bool ZP, bool XS, int SEG, int kDepth, int W>
-__global__ void __launch_bounds__(W * 32) int4_kernel(const __grid_constant__ FfnSkinnyArgs a, const Plan p) {
-  constexpr int kThreads = W * 32;
+// Up to 8 tokens the compiler is told that 16 warps share an SM, 128 registers a thread: left alone it
+// used 72 to 127 and ran 2 to 7 % longer (gated 1 x 10240 x 5120 21.7 us, so 20.5; int4 2 x 5120 x
+// 17408, groups of 64, 19.2 and 18.6); with more tokens the same bound costs 10 to 57 %.
+template <bool GATED, int NT, bool FINE, bool ZP, bool XS, int SEG, int kDepth, int W, int RW>
+__global__ void __launch_bounds__(W * 32, NT > 1 ? 0 : 16 / W)
+    int4_kernel(const __grid_constant__ FfnSkinnyArgs a, const Plan p) {
+  constexpr int kThreads = W * 32, MT = kRowTiles;
   constexpr int TT = NT * 8, RT = MT * 16, OUT = GATED ? RT / 2 : RT, PITCH = TT + 1;
   constexpr int SB = SEG / 64;                   // blocks per step
   constexpr int LPR = SEG / 16, RPI = 32 / LPR;  // lanes per row, rows per copy instruction
@@ -133,9 +137,11 @@ __global__ void __launch_bounds__(W * 32) int4_kernel(const __grid_constant__ Ff
   uint8_t* ring = smem + p.x_bytes;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
-  const int rw = 1 << p.rw_log2, wr = warp & (rw - 1), wk = warp >> p.rw_log2, kw = W >> p.rw_log2;
+  constexpr int KW = W / RW;
+  static_assert(KW > 1 && KW * RW == W, "the sums meet in shared memory");
+  const int wr = warp % RW, wk = warp / RW;
   const int m0 = blockIdx.y * TT, toks = min(TT, a.M - m0);
-  const int n_cta = (int)blockIdx.x * rw * OUT, n0 = n_cta + wr * OUT;
+  const int n_cta = (int)blockIdx.x * RW * OUT, n0 = n_cta + wr * OUT;
   const int ks = gridDim.z, kz = blockIdx.z;
   const int nblk = (a.K + kBlockK - 1) / kBlockK;
   const int c0 = nblk / ks * kz + min(kz, nblk % ks), c1 = c0 + nblk / ks + (kz < nblk % ks);
@@ -182,10 +188,10 @@ __global__ void __launch_bounds__(W * 32) int4_kernel(const __grid_constant__ Ff
           cp16(mine + slot * kStep + x_dst + i * 512, xs, in && i * 2 + xm < toks);
           xs += 2 * a.ldx;
         }
-        xq += kw * kBlockK;
+        xq += KW * kBlockK;
       }
-      wp += kw * SEG;
-      bf += kw * SB;
+      wp += KW * SEG;
+      bf += KW * SB;
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
@@ -195,7 +201,7 @@ __global__ void __launch_bounds__(W * 32) int4_kernel(const __grid_constant__ Ff
     const int o = GATED ? lane % OUT : lane;
     if (o < valid) {
       const uint8_t* row = a.w + ((GATED && lane >= OUT ? (int64_t)a.N : 0) + n0 + o) * a.ldw_bytes;
-      for (int d = 0, b = c0 + wk * SB; d < kPrefetch && b < c1; ++d, b += kw * SB) prefetch_l2(row + (int64_t)b * 64);
+      for (int d = 0, b = c0 + wk * SB; d < kPrefetch && b < c1; ++d, b += KW * SB) prefetch_l2(row + (int64_t)b * 64);
     }
   }
   pdl_wait();
@@ -284,7 +290,7 @@ __global__ void __launch_bounds__(W * 32) int4_kernel(const __grid_constant__ Ff
       __syncthreads();
     }
 
-    for (int b0 = q0 + wk * SB; b0 < q1; b0 += kw * SB) {
+    for (int b0 = q0 + wk * SB; b0 < q1; b0 += KW * SB) {
       asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 2) : "memory");
       __syncwarp();  // every lane's copies of this step have landed, and the step before is read
       fetch(slot == 0 ? kDepth - 1 : slot - 1);
@@ -302,7 +308,7 @@ __global__ void __launch_bounds__(W * 32) int4_kernel(const __grid_constant__ Ff
           for (int h = 0; h < 2; ++h)
             sz[i][mt][h] = __float_as_uint(scale_to_f32(s_next[i][mt][h], a.scale_fp16) * 64.f) |
                            (ZP ? z_next[i][mt][h] : 0u);
-      if (b0 + kw * SB < c1) scales(b0 + kw * SB);
+      if (b0 + KW * SB < c1) scales(b0 + KW * SB);
 #pragma unroll
       for (int sb = 0; sb < SB; ++sb) {
         if (sb > 0 && b0 + sb >= q1) break;
@@ -337,7 +343,7 @@ __global__ void __launch_bounds__(W * 32) int4_kernel(const __grid_constant__ Ff
                 const uint32_t v = FINE ? __shfl_sync(0xffffffffu, sz[FINE ? sb : 0][mt][h], j, 4)
                                         : __shfl_sync(0xffffffffu, sz[FINE ? 0 : sb / 4][mt][h], sb & 3, 4);
                 sc[mt][h] = __uint_as_float(ZP ? v & ~255u : v);
-                negz[mt][h] = ZP ? fma_bf16x2((v & 255u) * 0x10001u, kNegMul, 0u) : negz8;
+                negz[mt][h] = ZP ? fma_bf16x2(__byte_perm(v, 0u, 0x4040), kNegMul, 0u) : negz8;
               }
           }
           uint4 bx[NT];
@@ -385,20 +391,8 @@ __global__ void __launch_bounds__(W * 32) int4_kernel(const __grid_constant__ Ff
     }
     a.y[(int64_t)(m0 + m) * a.ldy + n] = yb;
   };
-  // accumulator i of lane (g, t): row g + 8 (i >> 1), token 2t + (i & 1)
-  if (kw * ks == 1) {
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int i = 0; i < (GATED ? 2 : 4); ++i) {
-          const int n = n0 + (GATED ? mt * 8 : mt * 16 + 8 * (i >> 1)) + g, m = nt * 8 + 2 * t + (i & 1);
-          if (n < a.N && m < toks) store(acc[mt][nt][i], acc[mt][nt][i | 2], m, n);
-        }
-    return;
-  }
-  // every warp leaves its sums in its own part of the ring (its copies have landed and are read)
+  // every warp leaves its sums in its own part of the ring (its copies have landed and are read).
+  // Accumulator i of lane (g, t): row g + 8 (i >> 1), token 2t + (i & 1)
   static_assert(RT * PITCH * 4 <= kDepth * kStep, "a warp's sums fit its part of the ring");
   asm volatile("cp.async.wait_group 0;" ::: "memory");
   __syncwarp();
@@ -411,12 +405,12 @@ __global__ void __launch_bounds__(W * 32) int4_kernel(const __grid_constant__ Ff
       for (int i = 0; i < 4; ++i)
         sums(warp)[(mt * 16 + g + 8 * (i >> 1)) * PITCH + nt * 8 + 2 * t + (i & 1)] = acc[mt][nt][i];
   __syncthreads();
-  if (kw > 1 && ks > 1) {
+  if (ks > 1) {
     // the K shares of this CTA into the first one's place: each value has one reader and writer
-    for (int e = threadIdx.x; e < rw * RT * toks; e += kThreads) {
-      const int r = e % RT, w = e / RT & (rw - 1), m = e / RT >> p.rw_log2;
+    for (int e = threadIdx.x; e < RW * RT * toks; e += kThreads) {
+      const int r = e % RT, w = e / RT % RW, m = e / (RT * RW);
       float v = 0.f;
-      for (int i = 0; i < kw; ++i) v += sums(w + i * rw)[r * PITCH + m];
+      for (int i = 0; i < KW; ++i) v += sums(w + i * RW)[r * PITCH + m];
       sums(w)[r * PITCH + m] = v;
     }
     __syncthreads();
@@ -425,32 +419,29 @@ __global__ void __launch_bounds__(W * 32) int4_kernel(const __grid_constant__ Ff
   auto total = [&](int w, int r, int m) {
     float v = 0.f;
     if (ks == 1) {
-      for (int i = 0; i < kw; ++i) v += sums(w + i * rw)[r * PITCH + m];
+      for (int i = 0; i < KW; ++i) v += sums(w + i * RW)[r * PITCH + m];
     } else {
       for (int z = 0; z < ks; ++z) v += ld_cta(smem_addr(sums(w) + r * PITCH + m), (uint32_t)z);
     }
     return v;
   };
   // the CTAs of a cluster share the outputs
-  for (int e = kz * kThreads + threadIdx.x; e < rw * OUT * toks; e += ks * kThreads) {
-    const int o = e & (rw * OUT - 1), m = e / OUT >> p.rw_log2, w = o / OUT, oo = o % OUT;
+  for (int e = kz * kThreads + threadIdx.x; e < RW * OUT * toks; e += ks * kThreads) {
+    const int o = e % (RW * OUT), m = e / (RW * OUT), w = o / OUT, oo = o % OUT;
     const int r = GATED ? (oo >> 3) * 16 + (oo & 7) : oo;
     if (n_cta + o < a.N) store(total(w, r, m), GATED ? total(w, r + 8, m) : 0.f, m, n_cta + o);
   }
   if (ks > 1) cluster_sync_all();  // the others may still read this CTA's sums
 }
 
-// W warps on 1 << rw_log2 row groups; the warps of a row group split K
-template <bool GATED, int NT, bool FINE, bool ZP, bool XS, int SEG, int kDepth, int W>
-cudaError_t launch(const FfnSkinnyArgs& a, int rw_log2, cudaStream_t st) {
-  constexpr int MT = 2;
-  auto* kfn = int4_kernel<GATED, MT, NT, FINE, ZP, XS, SEG, kDepth, W>;
+template <bool GATED, int NT, bool FINE, bool ZP, bool XS, int SEG, int kDepth, int W, int RW>
+cudaError_t launch(const FfnSkinnyArgs& a, cudaStream_t st) {
+  constexpr int MT = kRowTiles, out = (GATED ? MT * 8 : MT * 16) * RW, kw = W / RW;
+  auto* kfn = int4_kernel<GATED, NT, FINE, ZP, XS, SEG, kDepth, W, RW>;
   static OncePerDevice once;
   if (const cudaError_t e = raise_smem_limit(kfn, once); e != cudaSuccess) return e;
   const int nblk = (a.K + kBlockK - 1) / kBlockK;
   Plan p = {};
-  p.rw_log2 = rw_log2;
-  const int out = (GATED ? MT * 8 : MT * 16) << rw_log2, kw = W >> rw_log2;
   const int64_t tiles = (int64_t)((a.N + out - 1) / out) * ((a.M + NT * 8 - 1) / (NT * 8));
   // K over a cluster's CTAs while eight warps per SM are missing and every warp keeps four blocks or
   // more (1 x 5120 x 17408: 2 CTAs 18.1 us, 1: 26.8, 4: 19.4; 16 x 4096 x 4096: 2: 10.6, 4: 15.4)
@@ -491,25 +482,25 @@ cudaError_t launch_nt(const FfnSkinnyArgs& a, cudaStream_t st) {
   // One token of many rows is staged: 1 x 5120 x 17408 17.4 us, in the rings 19.3 (2 tokens 23.7 and
   // 19.3).  From four tiles per SM on, eight warps on four row groups share it (1 x 17408 x 5120 gated:
   // 22.5 us against 27.0 with four warps on one row group)
-  if (a.M == 1 && tiles >= 4 * kNumSMs) return launch<GATED, 1, FINE, ZP, true, 128, 3, 8>(a, 2, st);
-  if (a.M == 1 && !few) return launch<GATED, 1, FINE, ZP, true, 128, 3, 4>(a, 0, st);
+  if (a.M == 1 && tiles >= 4 * kNumSMs) return launch<GATED, 1, FINE, ZP, true, 128, 3, 8, 4>(a, st);
+  if (a.M == 1 && !few) return launch<GATED, 1, FINE, ZP, true, 128, 3, 4, 1>(a, st);
   // 6 x 4096 x 4096: 16 warps 4.9 us, 8: 5.3, 4: 6.2; 6 x 5120 x 17408: 24.2, 21.9, 19.1; 16 warps want
   // two blocks each (6 x 512 x 1024: 2.3 us, 8 warps 2.2)
   if (a.M <= 8) {
-    if (few && a.K > 31 * kBlockK) return launch<GATED, 1, FINE, ZP, false, 64, 3, 16>(a, 0, st);
-    if (few) return launch<GATED, 1, FINE, ZP, false, 64, 3, 8>(a, 0, st);
-    return launch<GATED, 1, FINE, ZP, false, 64, 3, 4>(a, 0, st);
+    if (few && a.K > 31 * kBlockK) return launch<GATED, 1, FINE, ZP, false, 64, 3, 16, 1>(a, st);
+    if (few) return launch<GATED, 1, FINE, ZP, false, 64, 3, 8, 1>(a, st);
+    return launch<GATED, 1, FINE, ZP, false, 64, 3, 4, 1>(a, st);
   }
   // 13 x 2048 x 4096 gated: 8 warps 6.1 us, 4: 7.8; 16 x 10240 x 5120 16.6 and 15.1 us
   if (a.M <= 16) {
-    if (few) return launch<GATED, 2, FINE, ZP, false, 64, 3, 8>(a, 0, st);
-    return launch<GATED, 2, FINE, ZP, false, 64, 2, 4>(a, 0, st);
+    if (few) return launch<GATED, 2, FINE, ZP, false, 64, 3, 8, 1>(a, st);
+    return launch<GATED, 2, FINE, ZP, false, 64, 2, 4, 1>(a, st);
   }
   // 25 x 2048 x 4096 gated: 8 warps 8.7 us, 4: 10.4; 32 x 10240 x 5120: 4 warps 27.5 us, 2: 33.3; 24 x
   // 17408 x 5120 gated: 57.8 and 53.5 us (registers and shared memory leave room for 8 and 10 warps)
-  if (few) return launch<GATED, 4, FINE, ZP, false, 64, 2, 8>(a, 0, st);
-  if (tiles >= 4 * kNumSMs) return launch<GATED, 4, FINE, ZP, false, 64, 2, 2>(a, 0, st);
-  return launch<GATED, 4, FINE, ZP, false, 64, 2, 4>(a, 0, st);
+  if (few) return launch<GATED, 4, FINE, ZP, false, 64, 2, 8, 1>(a, st);
+  if (tiles >= 4 * kNumSMs) return launch<GATED, 4, FINE, ZP, false, 64, 2, 2, 1>(a, st);
+  return launch<GATED, 4, FINE, ZP, false, 64, 2, 4, 1>(a, st);
 }
 
 template <bool GATED>
