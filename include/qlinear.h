@@ -117,6 +117,9 @@ QL_API size_t ql_workspace_bytes(int op, int64_t M, int64_t N, int64_t K, int E,
 /* Zero `bytes` of workspace on `stream` (cudaMemsetAsync).  Call once after allocating. */
 QL_API ql_status ql_workspace_init(void* workspace, size_t bytes, ql_stream_t stream);
 
+/* Which CUDA graph capture `stream` takes part in (the capture's id; 0: none). */
+QL_API uint64_t ql_capture_id(ql_stream_t stream);
+
 /*
  * Read (and, if clear != 0, reset) the device status word of `workspace`; synchronises
  * `stream`.  *flags_out receives the QL_DEV_* bits.  Returns QL_ERR_TIMEOUT if the timeout

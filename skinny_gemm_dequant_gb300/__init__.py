@@ -49,6 +49,8 @@ lib.ql_workspace_init.restype = _int
 lib.ql_workspace_init.argtypes = [_vp, _sz, _vp]
 lib.ql_read_device_status.restype = _int
 lib.ql_read_device_status.argtypes = [_vp, _vp, _int, ctypes.POINTER(_u32)]
+lib.ql_capture_id.restype = ctypes.c_uint64
+lib.ql_capture_id.argtypes = [_vp]
 lib.ql_set_wait_limit.restype = None
 lib.ql_set_wait_limit.argtypes = [_u32]
 lib.qlinear_int8_w8a8.restype = _int
@@ -437,14 +439,16 @@ class FFNCheckpoint(NamedTuple):
 
 _ffn_bytes = functools.lru_cache(maxsize=256)(workspace_bytes)
 _ffn_workspaces: dict = {}
+_ffn_captures: dict = {}  # of graphs being captured: (device, stream) -> _Captured
 _ZERO_BYTES = 256 + (1 << 20)  # of a workspace's start: the status word and what is zero between calls
 
 
-def _capturing(stream):
-    if stream is None:
-        return torch.cuda.is_current_stream_capturing()
-    with torch.cuda.stream(stream):
-        return torch.cuda.is_current_stream_capturing()
+class _Captured:
+    """The workspace of a graph's calls on one stream: memory of the graph's pool, zeroed once in the
+    graph, before the first call that counts on it."""
+
+    def __init__(self, capture, ws):
+        self.capture, self.ws, self.zeroed = capture, ws, False
 
 
 class _FFNScratch:
@@ -458,26 +462,39 @@ class _FFNScratch:
     thread's launches on the same stream could come between another's.
 
     While the stream is captured: a given Workspace that is large enough already, kept from then on
-    for the graph's sake, or else memory of the graph's own: one that is kept for later calls would be
-    zeroed by that graph alone and shared with every graph that is captured on the same stream.
-    cut() says whether the call counts on zeroed tickets."""
+    for the graph's sake, or else memory of the graph's own, one piece for all of its calls on the
+    stream: a Workspace that later calls use too would be zeroed by that graph alone and shared with
+    every graph that is captured on the same stream.  cut() says whether the call counts on zeroed
+    tickets."""
 
     __slots__ = ("ws", "nbytes", "stream", "recorded")
 
     def __init__(self, x, op, M, I, H, stream, workspace, cut):
-        self.nbytes, self.stream, self.recorded = _ffn_bytes(op, M, I, H), stream, _capturing(stream)
+        self.nbytes, self.stream = _ffn_bytes(op, M, I, H), stream
+        key = (x.device.index, _stream(stream))
+        self.recorded = lib.ql_capture_id(key[1])
         if self.recorded:
             if workspace is None or workspace.buf is None or workspace.buf.numel() < self.nbytes:
-                workspace = Workspace(x.device)
-                workspace.buf = _empty((self.nbytes,), torch.uint8, x, stream)
-                if cut():
-                    _check(lib.ql_workspace_init(_ptr(workspace.buf), _ZERO_BYTES, _stream(stream)), "ql_workspace_init")
-        elif workspace is None:
-            key = (x.device.index, _stream(stream))
-            workspace = _ffn_workspaces.get(key)
+                workspace = self.of_graph(key, x, cut)
+        else:
+            if _ffn_captures:
+                _ffn_captures.clear()  # their graphs' pools keep the memory; one that goes on takes another piece
             if workspace is None:
-                workspace = _ffn_workspaces.setdefault(key, Workspace(x.device))
+                workspace = _ffn_workspaces.get(key)
+                if workspace is None:
+                    workspace = _ffn_workspaces.setdefault(key, Workspace(x.device))
         self.ws = workspace
+
+    def of_graph(self, key, x, cut):
+        mine = _ffn_captures.get(key)
+        if mine is None or mine.capture != self.recorded or mine.ws.buf.numel() < self.nbytes:
+            mine = _Captured(self.recorded, Workspace(x.device))
+            mine.ws.buf = _empty((self.nbytes,), torch.uint8, x, self.stream)
+            _ffn_captures[key] = mine
+        if not mine.zeroed and cut():
+            _check(lib.ql_workspace_init(_ptr(mine.ws.buf), _ZERO_BYTES, key[1]), "ql_workspace_init")
+            mine.zeroed = True
+        return mine.ws
 
     def __enter__(self):
         ws = self.ws
@@ -518,9 +535,8 @@ def gated_ffn(x, w13, *, swiglu_alpha=1.0, swiglu_limit=None, save=None, debug=F
     """h = silu(alpha * min(g, limit)) * clamp(u, +-limit) with g, u = x W13^T, in one launch.  x: bf16
     [M, H]; w13: bf16 [2I, H], rows [0, I) gate and [I, 2I) up; H and I multiples of 8.  save: None,
     "bf16" or "int8" also returns an FFNCheckpoint of g and u: (h, checkpoint).  debug=True appends
-    the path.  Without a workspace one is kept per device and stream; a captured call takes memory of
-    its graph's own, and zeroes its tickets in the graph where it uses any (none with a workspace that
-    is large enough when the capture starts)."""
+    the path.  Without a workspace one is kept per device and stream; captured calls share a piece of
+    their graph's own memory per stream."""
     _bf16(x, "x")
     M, H, I, ldx, ldw = _ffn_weights(x, w13)
     if save not in _SAVE:

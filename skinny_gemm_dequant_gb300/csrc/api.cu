@@ -414,6 +414,16 @@ ql_status ql_workspace_init(void* workspace, size_t bytes, ql_stream_t stream) {
   return cuda_status(cudaMemsetAsync(workspace, 0, bytes, (cudaStream_t)stream));
 }
 
+uint64_t ql_capture_id(ql_stream_t stream) {
+  cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+  unsigned long long id = 0;
+  if (cudaStreamGetCaptureInfo((cudaStream_t)stream, &status, &id) != cudaSuccess) {
+    cudaGetLastError();  // the launch that follows meets the error and tells it
+    return 0;
+  }
+  return status == cudaStreamCaptureStatusActive ? id : 0;
+}
+
 ql_status ql_read_device_status(void* workspace, ql_stream_t stream, int clear, uint32_t* flags_out) {
   if (!workspace) return QL_ERR_WORKSPACE;
   uint32_t flags = 0;

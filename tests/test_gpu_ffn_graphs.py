@@ -134,3 +134,51 @@ def test_one_gradient_and_few_tokens_captured(ql, cases):
     g.replay()
     torch.cuda.synchronize()
     assert same(out, (dx, h))
+
+
+def test_many_calls_in_one_graph_share_its_workspace(ql, cases):
+    """Sizes that grow and shrink, replayed twice: the second replay finds what the first left."""
+    sets, want = cases
+    order = [0, 1, 0, 3, 2, 1]
+    g, out = capture(lambda: [step(ql, sets[i]) for i in order])
+    for _ in range(2):
+        g.replay()
+    torch.cuda.synchronize()
+    for got, i in zip(out, order):
+        assert same(got, want[i])
+
+
+def test_eager_calls_while_another_stream_is_captured(ql, cases):
+    sets, want = cases
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        step(ql, sets[1])
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, capture_error_mode="relaxed"):
+        first = step(ql, sets[1])
+        with torch.cuda.stream(side):
+            eager = step(ql, sets[1])
+        second = step(ql, sets[3])
+    step(ql, sets[0])
+    assert not ql._ffn_captures
+    g.replay()
+    torch.cuda.synchronize()
+    assert same(first, want[1]) and same(second, want[3]) and same(eager, want[1])
+
+
+def test_branches_of_a_graph_do_not_share(ql, cases):
+    """Calls on two streams of one capture run side by side when it is replayed."""
+    sets, want = cases
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=main):
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            b = [step(ql, sets[3]) for _ in range(4)]
+        a = [step(ql, sets[1]) for _ in range(4)]
+        main.wait_stream(side)
+    for _ in range(5):
+        g.replay()
+    torch.cuda.synchronize()
+    assert all(same(t, want[1]) for t in a) and all(same(t, want[3]) for t in b)
