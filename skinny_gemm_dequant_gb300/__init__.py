@@ -536,7 +536,8 @@ def gated_ffn(x, w13, *, swiglu_alpha=1.0, swiglu_limit=None, save=None, debug=F
     [M, H]; w13: bf16 [2I, H], rows [0, I) gate and [I, 2I) up; H and I multiples of 8.  save: None,
     "bf16" or "int8" also returns an FFNCheckpoint of g and u: (h, checkpoint).  debug=True appends
     the path.  Without a workspace one is kept per device and stream; captured calls share a piece of
-    their graph's own memory per stream."""
+    their graph's own memory per stream.  As with every call here, autograd records nothing: the
+    gradients are gated_ffn_backward's."""
     _bf16(x, "x")
     M, H, I, ldx, ldw = _ffn_weights(x, w13)
     if save not in _SAVE:
@@ -567,8 +568,16 @@ def gated_ffn_backward(dh, x, w13, saved, *, swiglu_alpha=1.0, swiglu_limit=None
                        out_dx=None, out_dw=None, workspace=None, stream=None):
     """Gradients of gated_ffn from its checkpoint: (dx bf16 [M, H], dw13 bf16 [2I, H]) for dh bf16
     [M, I]; an output that is not needed is None and costs nothing.  swiglu_alpha and swiglu_limit
-    as in the forward."""
+    as in the forward.  x is read for dw13 only and w13 for dx only: the other may be None
+    (I is dh's width then)."""
     _bf16(dh, "dh")
+    if (x is None and (need_dw or w13 is None)) or (w13 is None and need_dx):
+        raise TypeError("x is needed for dw13, w13 for dx")
+    # a row of the other operand stands in for the one that is not given: its shape is used, it is not read
+    if x is None:
+        x = w13[:1].expand(dh.shape[0], -1)
+    if w13 is None:
+        w13 = x[:1].expand(2 * dh.shape[1], -1)
     _bf16(x, "x")
     M, H, I, ldx, ldw = _ffn_weights(x, w13)
     if dh.shape != (M, I) or dh.stride(1) != 1:
