@@ -19,8 +19,8 @@
 // What bounds it: a block of 16 rows takes about 150 warp instructions, half of them on the ALU,
 // which takes one every two cycles, from two to six warps per scheduler that each run a dependent
 // chain: with the loads taken out, 1 x 17408 x 5120 (gated) still takes 17.4 us; with the
-// arithmetic taken out 18.1 us; both together 22.5 us (4.2 TB/s; HBM alone 13.7).  1 x 5120 x 17408
-// 17.3 us (2.7 TB/s), 8 tokens 19.3; 16 x 10240 x 5120 with groups of 32 15.3 us.  Two row tiles a
+// arithmetic taken out 18.1 us; both together 22.2 us (4.2 TB/s; HBM alone 13.7).  1 x 5120 x 17408
+// 17.2 us (2.7 TB/s), 8 tokens 18.9; 16 x 10240 x 5120 with groups of 32 15.4 us.  Two row tiles a
 // warp against one: two independent MMA chains, and the activations are read once for both (28.2
 // to 23.6 us).  Scales a step ahead, shared by shuffles: 2-byte loads waited for in the block that
 // uses them took 11 us of 35.
@@ -43,6 +43,7 @@ constexpr int kPrefetch = 2;  // steps
 struct Plan {
   int chunk;    // staged activations: blocks of K at a time
   int x_bytes;  // of them
+  int kw;       // warps of a row group
 };
 // bytes of a block of staged activations
 __host__ __device__ constexpr uint32_t x_block(bool fine) { return fine ? 256 : 320; }
@@ -123,7 +124,7 @@ __device__ __forceinline__ float ld_cta(uint32_t saddr, uint32_t rank) {
 // used 72 to 127 and ran 2 to 7 % longer (gated 1 x 10240 x 5120 21.7 us, so 20.5; int4 2 x 5120 x
 // 17408, groups of 64, 19.2 and 18.6); with more tokens the same bound costs 10 to 57 %.
 template <bool GATED, int NT, bool FINE, bool ZP, bool XS, int SEG, int kDepth, int W, int RW>
-__global__ void __launch_bounds__(W * 32, NT > 1 ? 0 : 16 / W)
+__global__ void __launch_bounds__(W * 32, NT > 1 || (XS && FINE && ZP) ? 0 : 16 / W)
     int4_kernel(const __grid_constant__ FfnSkinnyArgs a, const Plan p) {
   constexpr int kThreads = W * 32, MT = kRowTiles;
   constexpr int TT = NT * 8, RT = MT * 16, OUT = GATED ? RT / 2 : RT, PITCH = TT + 1;
@@ -140,6 +141,9 @@ __global__ void __launch_bounds__(W * 32, NT > 1 ? 0 : 16 / W)
   constexpr int KW = W / RW;
   static_assert(KW > 1 && KW * RW == W, "the sums meet in shared memory");
   const int wr = warp % RW, wk = warp / RW;
+  // (one staged token, groups shorter than 128, zero points: with the warps' stride known and the
+  // register bound above the compiler's order of the loop took 1 x 16000 x 17408 64.7 us, so 51.0)
+  const int kw = XS && FINE && ZP ? p.kw : KW;
   const int m0 = blockIdx.y * TT, toks = min(TT, a.M - m0);
   const int n_cta = (int)blockIdx.x * RW * OUT, n0 = n_cta + wr * OUT;
   const int ks = gridDim.z, kz = blockIdx.z;
@@ -188,10 +192,10 @@ __global__ void __launch_bounds__(W * 32, NT > 1 ? 0 : 16 / W)
           cp16(mine + slot * kStep + x_dst + i * 512, xs, in && i * 2 + xm < toks);
           xs += 2 * a.ldx;
         }
-        xq += KW * kBlockK;
+        xq += kw * kBlockK;
       }
-      wp += KW * SEG;
-      bf += KW * SB;
+      wp += kw * SEG;
+      bf += kw * SB;
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
@@ -201,7 +205,7 @@ __global__ void __launch_bounds__(W * 32, NT > 1 ? 0 : 16 / W)
     const int o = GATED ? lane % OUT : lane;
     if (o < valid) {
       const uint8_t* row = a.w + ((GATED && lane >= OUT ? (int64_t)a.N : 0) + n0 + o) * a.ldw_bytes;
-      for (int d = 0, b = c0 + wk * SB; d < kPrefetch && b < c1; ++d, b += KW * SB) prefetch_l2(row + (int64_t)b * 64);
+      for (int d = 0, b = c0 + wk * SB; d < kPrefetch && b < c1; ++d, b += kw * SB) prefetch_l2(row + (int64_t)b * 64);
     }
   }
   pdl_wait();
@@ -290,7 +294,7 @@ __global__ void __launch_bounds__(W * 32, NT > 1 ? 0 : 16 / W)
       __syncthreads();
     }
 
-    for (int b0 = q0 + wk * SB; b0 < q1; b0 += KW * SB) {
+    for (int b0 = q0 + wk * SB; b0 < q1; b0 += kw * SB) {
       asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 2) : "memory");
       __syncwarp();  // every lane's copies of this step have landed, and the step before is read
       fetch(slot == 0 ? kDepth - 1 : slot - 1);
@@ -308,7 +312,7 @@ __global__ void __launch_bounds__(W * 32, NT > 1 ? 0 : 16 / W)
           for (int h = 0; h < 2; ++h)
             sz[i][mt][h] = __float_as_uint(scale_to_f32(s_next[i][mt][h], a.scale_fp16) * 64.f) |
                            (ZP ? z_next[i][mt][h] : 0u);
-      if (b0 + KW * SB < c1) scales(b0 + KW * SB);
+      if (b0 + kw * SB < c1) scales(b0 + kw * SB);
 #pragma unroll
       for (int sb = 0; sb < SB; ++sb) {
         if (sb > 0 && b0 + sb >= q1) break;
@@ -442,9 +446,10 @@ cudaError_t launch(const FfnSkinnyArgs& a, cudaStream_t st) {
   if (const cudaError_t e = raise_smem_limit(kfn, once); e != cudaSuccess) return e;
   const int nblk = (a.K + kBlockK - 1) / kBlockK;
   Plan p = {};
+  p.kw = kw;
   const int64_t tiles = (int64_t)((a.N + out - 1) / out) * ((a.M + NT * 8 - 1) / (NT * 8));
   // K over a cluster's CTAs while eight warps per SM are missing and every warp keeps four blocks or
-  // more (1 x 5120 x 17408: 2 CTAs 18.1 us, 1: 26.8, 4: 19.4; 16 x 4096 x 4096: 2: 10.6, 4: 15.4)
+  // more (1 x 5120 x 17408: 2 CTAs 17.1 us, 1: 20.7, 4: 19.7; 16 x 4096 x 4096: 1: 5.6, 2: 10.2, 4: 17.8)
   int ks = 1;
   while (ks < 8 && tiles * ks * W < 8 * kNumSMs && nblk >= kw * ks * 8) ks *= 2;
   if constexpr (XS) {
@@ -479,25 +484,25 @@ cudaError_t launch_nt(const FfnSkinnyArgs& a, cudaStream_t st) {
   // CTAs
   const int64_t tiles = (int64_t)((a.N + (GATED ? 15 : 31)) / (GATED ? 16 : 32)) * ((a.M + 31) / 32);
   const bool few = tiles <= kNumSMs;
-  // One token of many rows is staged: 1 x 5120 x 17408 17.4 us, in the rings 19.3 (2 tokens 23.7 and
-  // 19.3).  From four tiles per SM on, eight warps on four row groups share it (1 x 17408 x 5120 gated:
-  // 22.5 us against 27.0 with four warps on one row group)
+  // One token of many rows is staged: 1 x 5120 x 17408 17.1 us, in the rings 18.9.  From four tiles
+  // per SM on, eight warps on four row groups share it (1 x 17408 x 5120 gated: 22.2 us against 25.8
+  // with four warps on one row group; 1 x 14336 x 5120, 448 tiles: 13.2 and 12.8)
   if (a.M == 1 && tiles >= 4 * kNumSMs) return launch<GATED, 1, FINE, ZP, true, 128, 3, 8, 4>(a, st);
   if (a.M == 1 && !few) return launch<GATED, 1, FINE, ZP, true, 128, 3, 4, 1>(a, st);
-  // 6 x 4096 x 4096: 16 warps 4.9 us, 8: 5.3, 4: 6.2; 6 x 5120 x 17408: 24.2, 21.9, 19.1; 16 warps want
-  // two blocks each (6 x 512 x 1024: 2.3 us, 8 warps 2.2)
+  // 6 x 4096 x 4096: 16 warps 4.7 us, 8: 5.1, 4: 5.8; 6 x 5120 x 17408: 22.0, 20.2, 17.9; 16 warps want
+  // two blocks each (6 x 512 x 1024, half of them idle: 2.0 us, 8 warps 2.0)
   if (a.M <= 8) {
     if (few && a.K > 31 * kBlockK) return launch<GATED, 1, FINE, ZP, false, 64, 3, 16, 1>(a, st);
     if (few) return launch<GATED, 1, FINE, ZP, false, 64, 3, 8, 1>(a, st);
     return launch<GATED, 1, FINE, ZP, false, 64, 3, 4, 1>(a, st);
   }
-  // 13 x 2048 x 4096 gated: 8 warps 6.1 us, 4: 7.8; 16 x 10240 x 5120 16.6 and 15.1 us
+  // 13 x 2048 x 4096 gated: 8 warps 5.5 us, 4: 6.9; 16 x 10240 x 5120, groups of 32: 20.5 and 15.4
   if (a.M <= 16) {
     if (few) return launch<GATED, 2, FINE, ZP, false, 64, 3, 8, 1>(a, st);
     return launch<GATED, 2, FINE, ZP, false, 64, 2, 4, 1>(a, st);
   }
-  // 25 x 2048 x 4096 gated: 8 warps 8.7 us, 4: 10.4; 32 x 10240 x 5120: 4 warps 27.5 us, 2: 33.3; 24 x
-  // 17408 x 5120 gated: 57.8 and 53.5 us (registers and shared memory leave room for 8 and 10 warps)
+  // 25 x 2048 x 4096 gated: 8 warps 8.1 us, 4: 9.2; 32 x 10240 x 5120: 4 warps 22.7 us, 2: 23.3; 24 x
+  // 17408 x 5120 gated: 53.4 and 50.7 (registers and shared memory leave room for 8 and 10 warps)
   if (few) return launch<GATED, 4, FINE, ZP, false, 64, 2, 8, 1>(a, st);
   if (tiles >= 4 * kNumSMs) return launch<GATED, 4, FINE, ZP, false, 64, 2, 2, 1>(a, st);
   return launch<GATED, 4, FINE, ZP, false, 64, 2, 4, 1>(a, st);

@@ -6,7 +6,7 @@ and every output has to be the rounded sum bit for bit.
 One token's activations are staged for a CTA 32 KB at a time (96 blocks of 128 k; 128 with groups
 shorter than 128) where its share of K is longer: 9760 rows and K = 17408 are 305 row tiles, enough
 that K is not shared by a cluster, so a CTA stages 136 blocks in two pieces, the second of 40 or of 8
-blocks; 19500 rows go to the form with four row groups."""
+blocks; 19457 rows and more go to the form with four row groups."""
 import pytest
 import torch
 
@@ -67,7 +67,7 @@ def test_long_sums(ql, M, N, K, group, zeros, dtype):
 
 
 @pytest.mark.parametrize("group,zeros,dtype", FORMS)
-@pytest.mark.parametrize("N,K", [(9760, 17408), (9761, 17312), (9760, 12320), (19500, 17408), (19457, 25632), (19500, 16416)])
+@pytest.mark.parametrize("N,K", [(9760, 17408), (9761, 17312), (9760, 12320), (14592, 17408), (14593, 17376), (19500, 17408), (19457, 25632), (19500, 16416)])
 def test_one_token_staged_in_pieces(ql, N, K, group, zeros, dtype):
     check(ql, 1, N, K, group, zeros, dtype)
 
