@@ -395,8 +395,9 @@ QL_API ql_status qlinear_int4(const uint16_t* x, int64_t M, int64_t K, int64_t l
  * save != QL_SAVE_NONE keeps g and u for gated_ffn_backward in ckpt, two halves per token, each
  * of P = I rounded up to 128 columns: QL_SAVE_BF16: bf16 [M, 2, P]; QL_SAVE_INT8: int8
  * [M, 2, P] and ckpt_scale fp32 [M, 2, P/128], per token and 128 columns
- *   scale = max|v| / 127,  code = round_half_even(v / scale)  (scale 0 where max|v| < 2^-100;
- * an infinity or a NaN in a group reads back as NaN throughout it).  Columns I..P are
+ *   scale = max|v| / 127,  code = round_half_even(v * (127 / max|v|)), all in fp32: within 2^-16 of a
+ * tie it may be the other neighbour of v / scale  (scale 0 where max|v| < 2^-100; an infinity or a
+ * NaN in a group reads back as NaN throughout it).  Columns I..P are
  * undefined.
  * Paths: without a checkpoint, M <= 16, or more where ceil(M/32) ceil(I/16) is at most four times
  *        (M <= 32) or twice the number of SMs: a skinny launch that streams the weights once per 32
@@ -419,10 +420,12 @@ QL_API ql_status gated_ffn(const uint16_t* x, int64_t M, int64_t H, int64_t ldx,
  *   du = dh * silu(alpha g') where |U| <= limit, else 0
  *   dg = dh * u' * alpha * silu'(alpha g') where G <= limit, else 0
  *   dx = bf16( dg W13[0:I] + du W13[I:2I] ),  dw13 = bf16( [dg du]^T x )
- * dg and du are rounded to bf16 (the tensor cores' operands), the sums are fp32.  dh: bf16
+ * dg and du are rounded to bf16 (the tensor cores' operands: dx and dw13 are then 0.0024 of their
+ * norm from exact, 0.0017 of it the outputs' own rounding), the sums are fp32.  dh: bf16
  * [M, ld_dh]; x, w13 as in the forward; dx: bf16 [M, ld_dx] or NULL; dw13: bf16 [2I, ld_dw] or
  * NULL (one of the two is required; x is not read without dw13, w13 not without dx).
- * Deterministic: every output is summed in one order.
+ * Deterministic: the same sizes and the same set of outputs are summed in the same order, whatever
+ * runs when.  A gradient alone may be summed in another order than together with the other one.
  * Requires what gated_ffn requires, ld_dh >= I, ld_dx >= H, ld_dw >= H (multiples of 8) and
  * 16-byte aligned dh, dx, dw13.  workspace: ql_workspace_bytes(QL_OP_GATED_FFN_BWD, M, I, H, 0, 0)
  * bytes (it holds [dg du]), zeroed once.

@@ -38,7 +38,8 @@ __device__ __forceinline__ void gated_grad(float dh, float g, float u, float alp
 }
 
 // ------------------------------------------------------------------ 8-bit checkpoint
-// scale = amax / 127, codes rint(v * 127 / amax).  Groups whose amax is under 2^-100 are kept as
+// scale = amax / 127, codes rint(v * (127 / amax)): one division a group, and the product is within
+// 2^-16 of v / scale, so that only a value that near to a tie gets the other of its two codes.  Groups whose amax is under 2^-100 are kept as
 // zeros (127 / amax would overflow); an infinity or a NaN makes the scale a NaN, so that every value
 // of the group reads back as one.
 __device__ __forceinline__ float ckpt_scale(float amax, float& inv) {
