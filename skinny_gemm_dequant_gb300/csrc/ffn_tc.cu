@@ -30,10 +30,11 @@
 // pair idle, were slower (4096 x 17408 x 5120 dx: 1009 us against 956 us uncut): the pairs then
 // stand at different k and no longer find each other's operands in L2.
 // What bounds it: the tensor cores in long calls (4096 tokens, 17408 x 5120: a step 2.38 ms, 1.84
-// PFLOP/s, in a burst; 2.6 to 2.7 ms, 1.6 to 1.7, one after the other under the power cap); in middling ones (2048 x 2048 x 4096: a step 131 us, 1.57 PFLOP/s) a step of 64 K takes
-// 0.27 us, 0.23 of them the products', and each launch's first loads and last writing about 7 us; in
-// short ones those 7 us and the parts' way through L2; the weights' HBM traffic for few tokens (64 x
-// 17408 x 5120 forward 65 us, 5.5 TB/s) and the writing of dW13.
+// PFLOP/s, in a burst; 2.6 to 2.7 ms, 1.6 to 1.7, one after the other under the power cap); in
+// middling ones (2048 x 2048 x 4096: a step 127 to 130 us, 1.6 PFLOP/s) a step of 64 K takes 0.27 us,
+// 0.23 of them the products', and each launch's first loads and last writing about 7 us; in short
+// ones those 7 us and the parts' way through L2; the weights' HBM traffic for few tokens (64 x 17408 x
+// 5120 forward 65 us, 5.5 TB/s) and the writing of dW13.
 // Every wait is bounded; one that runs out raises QL_DEV_TIMEOUT in the status word and the pair
 // leaves its loops, waits for copies and MMAs in flight and frees its tensor memory.  Its part of a cut
 // tile counts in as missing, so that the next call finds the tickets as it needs them.
@@ -670,9 +671,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // dgu[m, i] = dg, dgu[m, I + i] = du from dh and the checkpoint, eight columns of kGradRows rows
 // per thread (their loads go out together).  dg and du leave in bf16: the tensor cores multiply bf16
 // with bf16, and a second pair of terms for the rest would double both GEMMs.  It moves dx and dW13
-// from 0.0017 to 0.0024 of their norm from exact.  One pass over memory: reads dh and the
-// checkpoint, writes 4 bytes per output.  Bound by HBM: 4096 x 17408, int8 checkpoint, 570 MB in 104 us, 5.5
-// TB/s (126 us with one row per thread).
+// from 0.0017 to 0.0024 of their norm from exact.  One pass over memory: reads dh and the checkpoint,
+// writes 4 bytes per output.  Bound by HBM: 4096 x 17408, int8 checkpoint, 570 MB in 104 us, 5.5 TB/s
+// (126 us with one row per thread).
 constexpr int kGradRows = 4;
 template <bool INT8>
 __global__ void __launch_bounds__(128) gated_grad_kernel(const uint16_t* __restrict__ dh, int64_t ld_dh, int64_t M,
