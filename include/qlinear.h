@@ -57,13 +57,17 @@ typedef enum {
 
 /* operation ids for ql_workspace_bytes */
 enum { QL_OP_INT8_W8A8 = 1, QL_OP_FP8_BLOCK = 2, QL_OP_MXFP4 = 3, QL_OP_MOE_MXFP4 = 4, QL_OP_BF16 = 5,
-       QL_OP_FP8_CHANNEL = 6, QL_OP_GATED_FFN = 7, QL_OP_GATED_FFN_BWD = 8 };
+       QL_OP_FP8_CHANNEL = 6, QL_OP_GATED_FFN = 7, QL_OP_GATED_FFN_BWD = 8, QL_OP_INT8_CODES = 9,
+       QL_OP_MOE_FEW = 10 };
 
 /* scale formats of the 4-bit group-scaled weights */
 enum { QL_SCALE_BF16 = 0, QL_SCALE_FP16 = 1 };
 
 /* what gated_ffn keeps of g and u for gated_ffn_backward */
 enum { QL_SAVE_NONE = 0, QL_SAVE_BF16 = 1, QL_SAVE_INT8 = 2 };
+
+/* output types of qlinear_int8 */
+enum { QL_OUT_BF16 = 0, QL_OUT_FP16 = 1, QL_OUT_FP32 = 2 };
 
 /* FP8 weight code formats of qlinear_fp8 */
 enum { QL_FP8_E4M3 = 0 /* e4m3fn: bias 7, no infinities, S.1111.111 is NaN */,
@@ -95,7 +99,11 @@ enum {
   QL_PATH_GATED_FFN_INT4 = 12,   /* gated block on 4-bit weights, one skinny launch           */
   QL_PATH_GATED_FFN_SKINNY = 13, /* gated block on bf16 weights, one skinny launch            */
   QL_PATH_GATED_FFN_TCGEN05 = 14, /* gated block, one tcgen05 GEMM with the activation in its epilogue */
-  QL_PATH_GATED_FFN_BACKWARD = 15 /* gradients of g and u, then the dx and dW13 tcgen05 GEMMs */
+  QL_PATH_GATED_FFN_BACKWARD = 15, /* gradients of g and u, then the dx and dW13 tcgen05 GEMMs */
+  QL_PATH_INT8_CODES_SKINNY = 16,  /* given 8-bit codes, weight-streaming kernel                */
+  QL_PATH_MOE_BF16 = 18,           /* routing + gate, up and activation; down and the weighted  */
+  QL_PATH_MOE_INT8 = 19,           /* sum: two weight-streaming launches                        */
+  QL_PATH_MOE_INT4 = 20
 };
 
 /* device status flags (bitmask) */
@@ -457,6 +465,79 @@ QL_API ql_status gated_ffn_int4(const uint16_t* x, int64_t M, int64_t H, int64_t
                                 int64_t ldw_bytes, const uint16_t* w_scale, int scale_fmt, int64_t lds,
                                 const uint8_t* w_zero, int64_t ldz, int64_t group, float swiglu_alpha,
                                 float swiglu_limit, uint16_t* h, int64_t ldh, ql_stream_t stream, int* path_out);
+
+/*
+ * 8-bit codes of tokens, by the rule of qlinear_int8_w8a8, for projections that share them:
+ *   scale[m] = max_k |x[m,k]| / 127,  codes[m,k] = clamp(round_half_even(x[m,k] / scale[m]), -127, 127)
+ * (IEEE fp32 divisions; an all-zero token has scale 0 and codes 0.)  x: bf16 [M, ldx]; codes: int8
+ * [M, K] dense; scale: fp32 [M].
+ * Requires 1 <= M <= 2^22, K >= 8, K % 8 == 0, K <= 2^20, ldx >= K, ldx % 8 == 0, 16-byte aligned x
+ * and codes.
+ */
+QL_API ql_status quantize_int8(const uint16_t* x, int64_t M, int64_t K, int64_t ldx, int8_t* codes, float* scale,
+                               ql_stream_t stream);
+
+/*
+ * Linear layer on 8-bit codes on both sides, their scales given:
+ *   acc[m,n] = sum_k x_q[m,k] * w[n,k]  (exact int32),  y[m,n] = out((acc * x_scale[m]) * w_scale[n])
+ * then, if bias, y = out(y + bias[n]).  With quantize_int8's codes and scales and QL_OUT_BF16 it is
+ * qlinear_int8_w8a8's y bit for bit.  x_q: int8 [M, ldx]; x_scale: fp32 [M]; w: int8 [N, ldw], both of
+ * any value, -128 too; w_scale: fp32 [N] or [1] (w_scale_len); bias: nullable bf16 [N]; y: [M, ldy] of
+ * out_type QL_OUT_*.
+ * One launch that streams the weights once per 16 tokens.
+ * Requires 1 <= M <= 2^22, 1 <= N <= 2^24, ceil(M/16) ceil(N/32) ceil(K/128) <= 2^30, K >= 16, K % 16 == 0, K <= 131056 (|acc| < 2^31), ldx >= K,
+ * ldw >= K, both multiples of 16, 16-byte aligned x_q and w, 4-byte aligned scales, y aligned to its
+ * type, ldy >= N.  workspace: ql_workspace_bytes(QL_OP_INT8_CODES, M, N, K, 0, 0) bytes, zeroed once.
+ */
+QL_API ql_status qlinear_int8(const int8_t* x_q, int64_t M, int64_t K, int64_t ldx, const float* x_scale,
+                              const int8_t* w, int64_t N, int64_t ldw, const float* w_scale, int64_t w_scale_len,
+                              const uint16_t* bias, int out_type, void* y, int64_t ldy, void* workspace,
+                              size_t workspace_bytes, ql_stream_t stream, int* path_out);
+
+/*
+ * Mixture-of-experts layers for a few tokens on bf16, 8-bit and 4-bit weights: moe_mxfp4_grouped's
+ * layer (routing, gate and up, activation, down, weighted sum; the same routing arguments, activation
+ * and debug outputs) in two launches that stream every chosen expert's weights once per 8 of its
+ * tokens.
+ * Expert ids outside [0, E) are padding: the pair is left out, and a token without any expert gets
+ * zeros (topk_ids_out reports -1).
+ *   h = bf16( silu(alpha * min(g, limit)) * clamp(u, -limit, limit) ),  y = bf16( sum_j weight_j W2[e_j] h_j )
+ *   moe_bf16: w13 bf16 [E, 2I, H], w2 bf16 [E, H, I]; fp32 sums.
+ *   moe_int8: w13 int8 [E, 2I, H] and s13 fp32 [E, 2I], w2 int8 [E, H, I] and s2 fp32 [E, H] (dense);
+ *     x is quantised per token and h per pair: scale = max|v| / 127, code = v (127 / max|v|) rounded
+ *     half to even in fp32 (within 2^-13 of a tie it may be the other neighbour); exact int32 sums.
+ *     A row with an infinity or a NaN gives NaN throughout.
+ *   moe_int4: w13 packed codes [E, 2I, ldw13], w2 [E, H, ldw2] with scales and zero points stored as
+ *     qlinear_int4's: s13 [E, 2I, lds13], s2 [E, H, lds2], z13, z2 likewise (each NULL: 8).  No weight
+ *     is rounded; x and h stay bf16.
+ * Experts, rows and scale rows are ld / stride elements apart (packed codes: bytes): w_estride13 is the distance
+ * of two experts of w13, and so on.  x: bf16 [M, ldx]; y: bf16 [M, ldy].
+ * Requires 1 <= M <= 64, 1 <= topk <= min(E, 16), E <= 1024, H and I at most 32768 and multiples of 8
+ * (bf16), 16 (int8), 32 (int4); 16-byte aligned x and weights, their rows and experts whole 16 bytes
+ * apart; 4-byte aligned fp32 scales.  int4: one group for w13 and w2, a power of two >= 32.
+ * workspace: ql_workspace_bytes(QL_OP_MOE_FEW, M, H, I, E, topk) bytes, zeroed once.
+ */
+QL_API ql_status moe_bf16(const uint16_t* x, int64_t M, int64_t H, int64_t ldx, const uint16_t* router_logits,
+                          const int32_t* topk_ids_in, const float* topk_w_in, int E, int topk, int renormalize,
+                          const uint16_t* w13, int64_t ldw13, int64_t w_estride13, const uint16_t* w2, int64_t ldw2,
+                          int64_t w_estride2, int64_t I, float swiglu_alpha, float swiglu_limit,
+                          int32_t* topk_ids_out, float* topk_w_out, uint16_t* h_out, uint16_t* y, int64_t ldy,
+                          void* workspace, size_t workspace_bytes, ql_stream_t stream, int* path_out);
+QL_API ql_status moe_int8(const uint16_t* x, int64_t M, int64_t H, int64_t ldx, const uint16_t* router_logits,
+                          const int32_t* topk_ids_in, const float* topk_w_in, int E, int topk, int renormalize,
+                          const int8_t* w13, int64_t ldw13, int64_t w_estride13, const float* s13, const int8_t* w2,
+                          int64_t ldw2, int64_t w_estride2, const float* s2, int64_t I, float swiglu_alpha,
+                          float swiglu_limit, int32_t* topk_ids_out, float* topk_w_out, uint16_t* h_out, uint16_t* y,
+                          int64_t ldy, void* workspace, size_t workspace_bytes, ql_stream_t stream, int* path_out);
+QL_API ql_status moe_int4(const uint16_t* x, int64_t M, int64_t H, int64_t ldx, const uint16_t* router_logits,
+                          const int32_t* topk_ids_in, const float* topk_w_in, int E, int topk, int renormalize,
+                          const uint8_t* w13, int64_t ldw13, int64_t w_estride13, const uint16_t* s13, int64_t lds13,
+                          int64_t s_estride13, const uint8_t* z13, int64_t ldz13, int64_t z_estride13,
+                          const uint8_t* w2, int64_t ldw2, int64_t w_estride2, const uint16_t* s2, int64_t lds2,
+                          int64_t s_estride2, const uint8_t* z2, int64_t ldz2, int64_t z_estride2, int scale_fmt,
+                          int64_t group, int64_t I, float swiglu_alpha, float swiglu_limit, int32_t* topk_ids_out,
+                          float* topk_w_out, uint16_t* h_out, uint16_t* y, int64_t ldy, void* workspace,
+                          size_t workspace_bytes, ql_stream_t stream, int* path_out);
 
 #ifdef __cplusplus
 }

@@ -30,6 +30,7 @@ __all__ = [
     "qlinear_mxfp4_partial", "finish_f32",
     "qlinear_int4", "gated_ffn_int4", "gated_ffn", "gated_ffn_backward", "FFNCheckpoint", "OP_GATED_FFN",
     "OP_GATED_FFN_BWD", "gated_ffn_plan", "FFNPlan",
+    "quantize_int8", "qlinear_int8", "moe_bf16", "moe_int8", "moe_int4", "OP_INT8_CODES", "OP_MOE_FEW",
 ]
 
 if not os.path.exists(_LIB_PATH):
@@ -103,8 +104,22 @@ lib.gated_ffn_backward.argtypes = [_vp, _i64, _vp, _i64, _i64, _i64, _vp, _i64, 
 lib.ql_gated_ffn_plan.restype = _int
 lib.ql_gated_ffn_plan.argtypes = [_int, _i64, _i64, _i64, _int, ctypes.POINTER(ctypes.c_int32)]
 
+lib.quantize_int8.restype = _int
+lib.quantize_int8.argtypes = [_vp, _i64, _i64, _i64, _vp, _vp, _vp]
+lib.qlinear_int8.restype = _int
+lib.qlinear_int8.argtypes = [_vp, _i64, _i64, _i64, _vp, _vp, _i64, _i64, _vp, _i64, _vp, _int, _vp, _i64, _vp, _sz,
+                             _vp, _ip]
+_MOE_HEAD = [_vp, _i64, _i64, _i64, _vp, _vp, _vp, _int, _int, _int]
+_MOE_TAIL = [_i64, ctypes.c_float, ctypes.c_float, _vp, _vp, _vp, _vp, _i64, _vp, _sz, _vp, _ip]
+lib.moe_bf16.restype = _int
+lib.moe_bf16.argtypes = _MOE_HEAD + 2 * [_vp, _i64, _i64] + _MOE_TAIL
+lib.moe_int8.restype = _int
+lib.moe_int8.argtypes = _MOE_HEAD + 2 * [_vp, _i64, _i64, _vp] + _MOE_TAIL
+lib.moe_int4.restype = _int
+lib.moe_int4.argtypes = _MOE_HEAD + 6 * [_vp, _i64, _i64] + [_int, _i64] + _MOE_TAIL
+
 OP_INT8_W8A8, OP_FP8_BLOCK, OP_MXFP4, OP_MOE_MXFP4, OP_BF16, OP_FP8_CHANNEL = 1, 2, 3, 4, 5, 6
-OP_GATED_FFN, OP_GATED_FFN_BWD = 7, 8
+OP_GATED_FFN, OP_GATED_FFN_BWD, OP_INT8_CODES, OP_MOE_FEW = 7, 8, 9, 10
 FP8_E4M3, FP8_E5M2 = 0, 1
 SCALE_BF16, SCALE_FP16 = 0, 1
 _SCALE_FORMATS = {torch.bfloat16: SCALE_BF16, torch.float16: SCALE_FP16}
@@ -113,7 +128,8 @@ ACT_BF16, ACT_E4M3_1X128 = 0, 1
 PATHS = {0: "none", 1: "int8_skinny", 2: "fp8_skinny", 3: "fp8_tcgen05", 4: "mxfp4_skinny",
          5: "mxfp4_tcgen05", 6: "moe_mxfp4", 7: "bf16_skinny", 8: "fp8_channel_skinny",
          9: "int8_tcgen05", 10: "moe_mxfp4_tcgen05", 11: "int4_skinny", 12: "gated_ffn_int4",
-         13: "gated_ffn_skinny", 14: "gated_ffn_tcgen05", 15: "gated_ffn_backward"}
+         13: "gated_ffn_skinny", 14: "gated_ffn_tcgen05", 15: "gated_ffn_backward",
+         16: "int8_codes_skinny", 18: "moe_bf16", 19: "moe_int8", 20: "moe_int4"}
 
 
 class QLError(RuntimeError):
@@ -451,14 +467,15 @@ class _Captured:
         self.capture, self.ws, self.zeroed = capture, ws, False
 
 
-class _FFNScratch:
-    """A gated block call's workspace, locked while its launches are put on the stream:
+class _Scratch:
+    """The workspace of a call of the gated block, of an 8-bit-code linear or of a few-token
+    mixture-of-experts layer, locked while its launches are put on the stream:
 
-        with _FFNScratch(...) as ws:  # the buffer
+        with _Scratch(...) as ws:  # the buffer
 
     The caller's Workspace, or one per device and stream (the current stream's handle if none is
     given), allocated from its stream's own pool.  A backward pass is two or three launches that hand
-    [dg du] on in the workspace, and ctypes lets other threads run meanwhile: without the lock a
+    [dg du] on in the workspace, a mixture-of-experts layer two that hand h on, and ctypes lets other threads run meanwhile: without the lock a
     thread's launches on the same stream could come between another's.
 
     While the stream is captured: a given Workspace that is large enough already, kept from then on
@@ -469,8 +486,8 @@ class _FFNScratch:
 
     __slots__ = ("ws", "nbytes", "stream", "recorded")
 
-    def __init__(self, x, op, M, I, H, stream, workspace, cut):
-        self.nbytes, self.stream = _ffn_bytes(op, M, I, H), stream
+    def __init__(self, x, nbytes, stream, workspace, cut):
+        self.nbytes, self.stream = nbytes, stream
         key = (x.device.index, _stream(stream))
         self.recorded = lib.ql_capture_id(key[1])
         if self.recorded:
@@ -551,8 +568,8 @@ def gated_ffn(x, w13, *, swiglu_alpha=1.0, swiglu_limit=None, save=None, debug=F
             scale = _empty((M, 2, P // 128), torch.float32, x, stream)
         saved = FFNCheckpoint(save, data, scale)
     path = ctypes.c_int(0) if debug else None
-    with _FFNScratch(x, OP_GATED_FFN, M, I, H, stream, workspace,
-                     lambda: gated_ffn_plan("forward", M, I, H, save=save).cut) as ws:
+    with _Scratch(x, _ffn_bytes(OP_GATED_FFN, M, I, H), stream, workspace,
+                  lambda: gated_ffn_plan("forward", M, I, H, save=save).cut) as ws:
         st = lib.gated_ffn(x.data_ptr(), M, H, ldx, w13.data_ptr(), I, ldw, swiglu_alpha, _inf(swiglu_limit),
                            h.data_ptr(), I if out is None else h.stride(0), _SAVE[save], _ptr(data), _ptr(scale),
                            ws.data_ptr(), ws.numel(), _stream(stream), path)
@@ -592,7 +609,7 @@ def gated_ffn_backward(dh, x, w13, saved, *, swiglu_alpha=1.0, swiglu_limit=None
         raise ValueError("saved must be the FFNCheckpoint of this x and w13")
     dx = _out(out_dx, M, H, x, stream, "out_dx") if need_dx else None
     dw = _out(out_dw, 2 * I, H, x, stream, "out_dw") if need_dw else None
-    with _FFNScratch(x, OP_GATED_FFN_BWD, M, I, H, stream, workspace, lambda: (
+    with _Scratch(x, _ffn_bytes(OP_GATED_FFN_BWD, M, I, H), stream, workspace, lambda: (
             (need_dx and gated_ffn_plan("dx", M, I, H, both=need_dw).cut)
             or (need_dw and gated_ffn_plan("dw", M, I, H, both=need_dx).cut))) as ws:
         st = lib.gated_ffn_backward(dh.data_ptr(), dh.stride(0), x.data_ptr(), M, H, ldx, w13.data_ptr(), I, ldw,
@@ -623,6 +640,192 @@ def gated_ffn_plan(gemm, M, I, H, *, save=None, both=True) -> FFNPlan:
     which = {"forward": 0, "dx": 1, "dw": 2}[gemm]
     _check(lib.ql_gated_ffn_plan(which, M, I, H, int(both) if which else _SAVE[save], out), "ql_gated_ffn_plan")
     return FFNPlan(*out)
+
+
+# ------------------------------------------------------------------ 8-bit codes on both sides
+_OUT_TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+def _always():
+    return True
+
+
+def _codes(t, name):
+    if t.dtype is not torch.int8 or not t.is_cuda or t.dim() != 2 or t.stride(1) != 1:
+        raise TypeError(f"{name} must be a 2-d int8 CUDA tensor with unit inner stride")
+    return t
+
+
+def _vector(t, name, n, dtype):
+    if t.dtype is not dtype or not t.is_cuda or t.numel() != n or not t.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous {str(dtype)[6:]} CUDA tensor of {n}")
+    return t
+
+
+def _on(x, **others):
+    """Refuses tensors that are not on x's device, and x on another device than the current one."""
+    if x.device.index != torch.cuda.current_device():
+        raise ValueError("the tensors must be on the current device")
+    for name, t in others.items():
+        if t is not None and t.device != x.device:
+            raise ValueError(f"{name} must be on {x.device}, as x is")
+
+
+def quantize_int8(x, *, out=None, out_scale=None, stream=None):
+    """(codes int8 [M, K], scale fp32 [M]) of x bf16 [M, K], K a multiple of 8, by qlinear_int8_w8a8's
+    rule: scale = max|x| / 127 of the row, codes = x / scale rounded half to even.  For projections
+    that share their input: qlinear_int8 takes both."""
+    _bf16(x, "x")
+    (M, K), (ldx, inner) = x.shape, x.stride()
+    if inner != 1:
+        raise TypeError("x must have unit inner stride")
+    _on(x, out=out, out_scale=out_scale)
+    if out is None:
+        out = _empty((M, K), torch.int8, x, stream)
+    elif _codes(out, "out").shape != (M, K) or not out.is_contiguous():
+        raise TypeError(f"out must be a contiguous int8 CUDA tensor [{M}, {K}]")
+    out_scale = _empty((M,), torch.float32, x, stream) if out_scale is None else _vector(out_scale, "out_scale", M, torch.float32)
+    if M:
+        _check(lib.quantize_int8(x.data_ptr(), M, K, max(ldx, K) if M == 1 else ldx, out.data_ptr(), out_scale.data_ptr(), _stream(stream)), "quantize_int8")
+    return out, out_scale
+
+
+def qlinear_int8(x_q, x_scale, w, w_scale, bias=None, *, out_dtype=torch.bfloat16, debug=False, out=None,
+                 workspace=None, stream=None):
+    """y = (acc * x_scale) * w_scale (+ bias after the cast), acc = x_q w^T exact in int32.  x_q: int8
+    [M, K], K a multiple of 16; x_scale: fp32 [M] (quantize_int8 gives both); w: int8 [N, K]; w_scale:
+    fp32 [N] or [1]; bias: bf16 [N]; out_dtype: bfloat16, float16 or float32.  Without a workspace one
+    is kept per device and stream; captured calls share a piece of their graph's own memory per stream.
+    With debug=True returns (y, path)."""
+    _codes(x_q, "x_q")
+    _codes(w, "w")
+    (M, K), (N, Kw) = x_q.shape, w.shape
+    if Kw != K:
+        raise ValueError(f"w must be [N, {K}] for x_q [{M}, {K}]")
+    _on(x_q, x_scale=x_scale, w=w, w_scale=w_scale, bias=bias, out=out)
+    _vector(x_scale, "x_scale", M, torch.float32)
+    _vector(w_scale, "w_scale", 1 if w_scale.numel() == 1 else N, torch.float32)
+    if bias is not None:
+        _vector(bias, "bias", N, torch.bfloat16)
+    if out is not None:
+        out_dtype = out.dtype
+    fmt = _OUT_TYPES.get(out_dtype)
+    if fmt is None:
+        raise TypeError("the output must be bfloat16, float16 or float32")
+    if out is None:
+        out = _empty((M, N), out_dtype, x_q, stream)
+    elif out.shape != (M, N) or out.stride(1) != 1:
+        raise TypeError(f"out must be [{M}, {N}] with unit inner stride")
+    path = ctypes.c_int(0) if debug else None
+    with _Scratch(x_q, _ffn_bytes(OP_INT8_CODES, M, N, K), stream, workspace, _always) as ws:
+        st = lib.qlinear_int8(x_q.data_ptr(), M, K, x_q.stride(0), x_scale.data_ptr(), w.data_ptr(), N, w.stride(0),
+                              w_scale.data_ptr(), w_scale.numel(), _ptr(bias), fmt, out.data_ptr(), out.stride(0),
+                              ws.data_ptr(), ws.numel(), _stream(stream), path)
+    if st:
+        raise QLError(st, "qlinear_int8")
+    return (out, PATHS[path.value]) if debug else out
+
+
+# ------------------------------------------------------------------ mixture of experts, few tokens
+def _experts(w, name, E, rows, cols, dtype):
+    """Checks a projection's weights [E, rows, >= cols]; returns (address, row stride, expert stride)."""
+    if w.dtype is not dtype or not w.is_cuda or w.dim() != 3 or w.stride(2) != 1:
+        raise TypeError(f"{name} must be a 3-d {str(dtype)[6:]} CUDA tensor with unit inner stride")
+    if w.shape[0] != E or w.shape[1] != rows or w.shape[2] < cols:
+        raise ValueError(f"{name} must be [{E}, {rows}, {cols}]")
+    return w.data_ptr(), w.stride(1), w.stride(0)
+
+
+def _moe(name, x, w13, w2, mats, *, router_logits, topk_ids, topk_weights, topk, renormalize, swiglu_alpha,
+         swiglu_limit, debug, out, workspace, stream):
+    """mats(E, I, H): the weights' arguments of the C call, checked."""
+    _bf16(x, "x")
+    M, H = x.shape
+    if x.stride(1) != 1 or w13.dim() != 3 or w2.dim() != 3:
+        raise TypeError("x must have unit inner stride; w13 and w2 must be [E, rows, columns]")
+    E, rows, _ = w13.shape
+    if rows & 1:
+        raise ValueError("w13 must have an even number of rows (gate, then up)")
+    I = rows >> 1
+    _on(x, w13=w13, w2=w2, router_logits=router_logits, topk_ids=topk_ids, topk_weights=topk_weights, out=out)
+    if (router_logits is None) == (topk_ids is None):
+        raise ValueError("either router_logits or topk_ids and topk_weights must be given")
+    if topk_ids is not None:
+        if topk_ids.dim() != 2 or topk_ids.shape[0] != M or topk_weights is None:
+            raise ValueError(f"topk_ids and topk_weights must be [{M}, topk]")
+        topk = topk_ids.shape[1]
+        _vector(topk_ids, "topk_ids", M * topk, torch.int32)
+        if _vector(topk_weights, "topk_weights", M * topk, torch.float32).shape != topk_ids.shape:
+            raise ValueError(f"topk_weights must be [{M}, {topk}]")
+    elif _vector(router_logits, "router_logits", M * E, torch.bfloat16).shape != (M, E):
+        raise ValueError(f"router_logits must be [{M}, {E}]")
+    args = mats(E, I, H)
+    y = _out(out, M, H, x, stream)
+    ids = wts = h = None
+    if debug:
+        ids = _empty((M, topk), torch.int32, x, stream)
+        wts = _empty((M, topk), torch.float32, x, stream)
+        h = _empty((M * topk, I), torch.bfloat16, x, stream)
+    path = ctypes.c_int(0) if debug else None
+    with _Scratch(x, _ffn_bytes(OP_MOE_FEW, M, H, I, E, topk), stream, workspace, _always) as ws:
+        st = getattr(lib, name)(x.data_ptr(), M, H, x.stride(0), _ptr(router_logits), _ptr(topk_ids), _ptr(topk_weights),
+                                E, topk, int(renormalize), *args, I, swiglu_alpha, _inf(swiglu_limit), _ptr(ids),
+                                _ptr(wts), _ptr(h), y.data_ptr(), y.stride(0), ws.data_ptr(), ws.numel(),
+                                _stream(stream), path)
+    if st:
+        raise QLError(st, name)
+    return (y, ids, wts, h, PATHS[path.value]) if debug else y
+
+
+def moe_bf16(x, w13, w2, *, router_logits=None, topk_ids=None, topk_weights=None, topk=8, renormalize=False,
+             swiglu_alpha=1.0, swiglu_limit=None, debug=False, out=None, workspace=None, stream=None):
+    """Mixture-of-experts layer for 1 to 64 tokens on bf16 weights, in two launches.  x: bf16 [M, H];
+    w13: bf16 [E, 2I, H] (gate rows, then up rows), w2: bf16 [E, H, I]; H and I multiples of 8.  Routing,
+    activation and debug=True's (y, ids, weights, h, path) are moe_mxfp4_grouped's; an id outside
+    [0, E) is padding, and a token without an expert gets zeros.  Workspaces as qlinear_int8's."""
+    def mats(E, I, H):
+        return (*_experts(w13, "w13", E, 2 * I, H, torch.bfloat16), *_experts(w2, "w2", E, H, I, torch.bfloat16))
+    return _moe("moe_bf16", x, w13, w2, mats, router_logits=router_logits, topk_ids=topk_ids,
+                topk_weights=topk_weights, topk=topk, renormalize=renormalize, swiglu_alpha=swiglu_alpha,
+                swiglu_limit=swiglu_limit, debug=debug, out=out, workspace=workspace, stream=stream)
+
+
+def moe_int8(x, w13, s13, w2, s2, *, router_logits=None, topk_ids=None, topk_weights=None, topk=8, renormalize=False,
+             swiglu_alpha=1.0, swiglu_limit=None, debug=False, out=None, workspace=None, stream=None):
+    """moe_bf16's layer on 8-bit codes: w13 int8 [E, 2I, H] with s13 fp32 [E, 2I], w2 int8 [E, H, I]
+    with s2 fp32 [E, H]; H and I multiples of 16.  x is quantised per token and h per (token, expert)
+    inside, scale = max|v| / 127; the sums are exact."""
+    def mats(E, I, H):
+        _on(x, s13=s13, s2=s2)
+        return (*_experts(w13, "w13", E, 2 * I, H, torch.int8), _vector(s13, "s13", E * 2 * I, torch.float32).data_ptr(),
+                *_experts(w2, "w2", E, H, I, torch.int8), _vector(s2, "s2", E * H, torch.float32).data_ptr())
+    return _moe("moe_int8", x, w13, w2, mats, router_logits=router_logits, topk_ids=topk_ids,
+                topk_weights=topk_weights, topk=topk, renormalize=renormalize, swiglu_alpha=swiglu_alpha,
+                swiglu_limit=swiglu_limit, debug=debug, out=out, workspace=workspace, stream=stream)
+
+
+def moe_int4(x, w13, s13, w2, s2, z13=None, z2=None, *, group=128, router_logits=None, topk_ids=None,
+             topk_weights=None, topk=8, renormalize=False, swiglu_alpha=1.0, swiglu_limit=None, debug=False, out=None,
+             workspace=None, stream=None):
+    """moe_bf16's layer on 4-bit weights stored as qlinear_int4's: w13 uint8 [E, 2I, >=H/2], w2 uint8
+    [E, H, >=I/2], scales bf16 or fp16 [E, rows, >=ceil(columns/group)], zero points uint8 of the same
+    shape or None: 8; H and I multiples of 32, group a power of two >= 32."""
+    def mats(E, I, H):
+        _on(x, s13=s13, s2=s2, z13=z13, z2=z2)
+        fmt = _SCALE_FORMATS.get(s13.dtype)
+        if fmt is None or s2.dtype is not s13.dtype:
+            raise TypeError("s13 and s2 must both be bfloat16 or both float16")
+        if group < 1:
+            raise ValueError("group must be positive")
+        args = ()
+        for n, w, s, z, rows, k in (("13", w13, s13, z13, 2 * I, H), ("2", w2, s2, z2, H, I)):
+            groups = -(-k // group)
+            args += (*_experts(w, "w" + n, E, rows, -(-k // 2), torch.uint8), *_experts(s, "s" + n, E, rows, groups, s.dtype))
+            args += (None, 0, 0) if z is None else _experts(z, "z" + n, E, rows, groups, torch.uint8)
+        return (*args, fmt, group)
+    return _moe("moe_int4", x, w13, w2, mats, router_logits=router_logits, topk_ids=topk_ids,
+                topk_weights=topk_weights, topk=topk, renormalize=renormalize, swiglu_alpha=swiglu_alpha,
+                swiglu_limit=swiglu_limit, debug=debug, out=out, workspace=workspace, stream=stream)
 
 
 # ------------------------------------------------------------------ sharded layers

@@ -8,6 +8,7 @@
 #include "gemm_i8_tcgen05.h"
 #include "gemm_tcgen05.h"
 #include "internal.h"
+#include "stream.h"
 #include "skinny2.cuh"
 
 using namespace ql;
@@ -399,6 +400,9 @@ size_t ql_workspace_bytes(int op, int64_t M, int64_t N, int64_t K, int E, int to
       if (op == QL_OP_GATED_FFN)
         return kRegionsOff + tc::ffn_forward_slots(M, K, N);  // the status word, tickets; cut tiles' sums
       return kRegionsOff + al256((size_t)M * 2 * N * 2) + tc::ffn_backward_slots(M, K, N);  // [dg du] first
+    case QL_OP_INT8_CODES:
+    case QL_OP_MOE_FEW:
+      return stream_workspace_bytes(op, M, N, K, E, topk);
     case QL_OP_MOE_MXFP4: {
       if (E <= 0 || topk <= 0) return 0;
       if (M > 16) return moe3_layout(M, N, K, E, topk).total;

@@ -1,0 +1,830 @@
+// Weight-streaming kernels for few tokens: the two launches of a mixture-of-experts layer (bf16,
+// 8-bit and 4-bit weights) and the linear on 8-bit codes.
+//
+//   GATE_UP  g = W13[e][0:I] x_m, u = W13[e][I:2I] x_m for every routed pair (m, j) with expert e,
+//            h = bf16( silu(a min(g, L)) clamp(u, -L, L) )
+//   DOWN     y_m = bf16( sum_j w_(m,j) W2[e] h_(m,j) )
+//   LINEAR   y = (acc x_s) w_s, acc = sum_k x_q w_q  (+ bias after the cast)
+//
+// 8-bit weights: tokens (GATE_UP) and h (DOWN) are quantised here, scale = max|v| / 127 over the
+// row, code = v (127 / max|v|) rounded half to even; products of codes are exact in fp32, sums
+// below 2^24 too, and every 1024 k they move to int32: sums are exact.  4-bit weights: q - z is
+// exact in bf16, a group's fp32 sum is multiplied by its scale once.
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+#include "ffn_act.cuh"
+#include "route.cuh"
+#include "stream.h"
+
+namespace ql {
+
+namespace {
+
+constexpr int R = kStreamRows;
+constexpr int kPitch = 36;  // of a column of sums: lanes (g, t) write 8 t + g, all banks once
+constexpr int kBuffers = 2;
+
+__host__ __device__ constexpr int compute_warps(int fmt) { return fmt == STREAM_INT4 ? 12 : 8; }
+__host__ __device__ constexpr int unit_k(int fmt) { return fmt == STREAM_BF16 ? 64 : 128; }
+__host__ __device__ constexpr int row_bytes(int fmt) { return fmt == STREAM_INT4 ? 64 : 128; }
+__host__ __device__ constexpr int token_bytes(int fmt, int mode) {
+  return fmt == STREAM_BF16 || mode == STREAM_LINEAR ? 128 : 256;
+}
+
+// what a call's shared memory is cut into
+struct Layout {
+  int xt;     // token rows of a stage
+  int stage;  // bytes
+  int depth;  // stages of a warp's ring
+  int sums, lists;  // offsets
+  int total;
+};
+
+struct Entry {  // one pass over an expert's weights
+  int expert, first, count;  // its pairs: sorted[first, first + count)
+};
+
+__device__ __forceinline__ uint32_t smem_addr(const void* p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+// 16 bytes to shared memory; zeros, and no access to src, where `take` is false
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool take) {
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(take ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds4(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+template <int ID0, int THREADS>
+__device__ __forceinline__ void bar_sync(int b) {
+  asm volatile("bar.sync %0, %1;" ::"r"(ID0 + b), "n"(THREADS) : "memory");
+}
+template <int ID0, int THREADS>
+__device__ __forceinline__ void bar_arrive(int b) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(ID0 + b), "n"(THREADS) : "memory");
+}
+// all but the newest `left` copy groups have landed
+__device__ __forceinline__ void cp_wait(int left) {
+  switch (left) {
+    case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
+    case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+    case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+    case 3: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+    case 4: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
+    default: asm volatile("cp.async.wait_group 5;" ::: "memory"); break;
+  }
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+// bf16 patterns below 256 are linear (pattern p stands for p 2^-133), so a nibble in place is a
+// number: one multiply-add gives (q - z) / 64, exactly
+__device__ __forceinline__ void codes_to_bf16(uint32_t w, uint32_t negz, uint32_t (&o)[4]) {
+  const uint32_t v = w >> 8;
+  o[0] = fma_bf16x2(w & 0x000F000Fu, 0x7F007F00u, negz);
+  o[1] = fma_bf16x2(w & 0x00F000F0u, 0x7D007D00u, negz);
+  o[2] = fma_bf16x2(v & 0x000F000Fu, 0x7F007F00u, negz);
+  o[3] = fma_bf16x2(v & 0x00F000F0u, 0x7D007D00u, negz);
+}
+// eight activations in the order in which a word's codes come out: (0,4) (1,5) (2,6) (3,7)
+__device__ __forceinline__ uint4 pair_up(uint4 x) {
+  return make_uint4(__byte_perm(x.x, x.z, 0x5410), __byte_perm(x.x, x.z, 0x7632), __byte_perm(x.y, x.w, 0x5410),
+                    __byte_perm(x.y, x.w, 0x7632));
+}
+// two bf16 values as whole f16 numbers: v inv + 1536 rounded to a whole number by the conversion
+// (f16 has steps of 1 there), less 1536
+__device__ __forceinline__ uint32_t quant2(uint32_t w, float inv) {
+  const float lo = fmaf(__uint_as_float(w << 16), inv, 1536.f);
+  const float hi = fmaf(__uint_as_float(w & 0xFFFF0000u), inv, 1536.f);
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(pack_f16x2(lo, hi)), "r"(0x66006600u));
+  return r;
+}
+
+// position of a warp in its CTA's units
+struct Walk {
+  int u, item, kb, a, tile;
+  __device__ void set(int u_, int nblk, int entries) {
+    u = u_;
+    item = u / nblk;
+    kb = u - item * nblk;
+    tile = item / entries;
+    a = item - tile * entries;
+  }
+  __device__ void next(int step, int nblk, int entries) {
+    u += step;
+    kb += step;
+    while (kb >= nblk) {
+      kb -= nblk;
+      ++item;
+      if (++a == entries) {
+        a = 0;
+        ++tile;
+      }
+    }
+  }
+};
+
+template <int FMT, int MODE, int NT, bool FINE, bool ZP>
+__global__ void __launch_bounds__((compute_warps(FMT) + 1) * 32, 1)
+    stream_kernel(const __grid_constant__ StreamArgs p, const __grid_constant__ Layout lay) {
+  constexpr int W = compute_warps(FMT), THREADS = (W + 1) * 32;
+  constexpr int TT = NT * 8, KU = unit_k(FMT), WB = row_bytes(FMT), XB = token_bytes(FMT, MODE);
+  constexpr bool GU = MODE == STREAM_GATE_UP, DN = MODE == STREAM_DOWN, LIN = MODE == STREAM_LINEAR;
+  constexpr bool I8 = FMT == STREAM_INT8, I4 = FMT == STREAM_INT4;
+  constexpr int kFull = 1, kEmpty = 1 + kBuffers;  // named barriers
+  using Sum = typename std::conditional<I8, int, float>::type;
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int P = LIN ? 0 : p.M * p.topk;
+
+  // lists: entries, sorted pairs, weights by pair, (INT8) factor and scale by row of x, experts' counts
+  Entry* entries = reinterpret_cast<Entry*>(smem + lay.lists);
+  int* sorted = reinterpret_cast<int*>(entries + P);
+  float* s_wt = reinterpret_cast<float*>(sorted + P);
+  float* s_inv = s_wt + P;
+  float* s_xs = s_inv + P;
+  int* s_id = reinterpret_cast<int*>(s_xs + P);
+  int* s_cnt = s_id + P;
+  float* s_y = reinterpret_cast<float*>(s_cnt + (LIN ? 0 : p.E));  // DOWN: [M][32]
+  __shared__ int s_entries;
+
+  if (!DN) {
+    pdl_wait();
+    pdl_launch_dependents();
+  }
+  int ne;
+  if constexpr (LIN) {
+    ne = (p.M + TT - 1) / TT;
+  } else {
+    // ---------------------------------------------------------------- routing and dispatch
+    // (DOWN runs this before its wait: the launch before, GATE_UP, has waited for what wrote the
+    // logits.)
+    for (int e = threadIdx.x; e < p.E; e += THREADS) s_cnt[e] = 0;
+    for (int m = warp; m < p.M; m += W + 1) {
+      int id = -1;
+      float wt = 0.f;
+      if (p.logits) {
+        route_token_warp(p.logits + (int64_t)m * p.E, p.E, p.topk, p.renorm != 0, id, wt);
+      } else if (lane < p.topk) {
+        id = p.ids[m * p.topk + lane];
+        wt = p.wts[m * p.topk + lane];
+        if (id < 0 || id >= p.E) id = -1;  // padding: not dispatched
+      }
+      if (lane < p.topk) {
+        s_id[m * p.topk + lane] = id;
+        s_wt[m * p.topk + lane] = wt;
+        if (GU && blockIdx.x == 0) {
+          if (p.ids_out) p.ids_out[m * p.topk + lane] = id;
+          if (p.wts_out) p.wts_out[m * p.topk + lane] = wt;
+        }
+      }
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < P; i += THREADS)
+      if (s_id[i] >= 0) atomicAdd(&s_cnt[s_id[i]], 1);
+    __syncthreads();
+    if (warp == 0) {
+      // counts to first positions, and the passes of up to TT pairs of every expert in use
+      int pos = 0, n = 0;
+      for (int e0 = 0; e0 < p.E; e0 += 32) {
+        const int e = e0 + lane, c = e < p.E ? s_cnt[e] : 0, k = (c + TT - 1) / TT;
+        int ci = c, ki = k;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int a = __shfl_up_sync(0xffffffffu, ci, o), b = __shfl_up_sync(0xffffffffu, ki, o);
+          if (lane >= o) {
+            ci += a;
+            ki += b;
+          }
+        }
+        if (e < p.E) s_cnt[e] = pos + ci - c;
+        for (int i = 0; i < k; ++i) entries[n + ki - k + i] = {e, pos + ci - c + i * TT, min(TT, c - i * TT)};
+        pos += __shfl_sync(0xffffffffu, ci, 31);
+        n += __shfl_sync(0xffffffffu, ki, 31);
+      }
+      __syncwarp();
+      for (int i0 = 0; i0 < P; i0 += 32) {
+        const int i = i0 + lane, e = i < P ? s_id[i] : -1;
+        const unsigned same = __match_any_sync(0xffffffffu, e);
+        const int rank = __popc(same & ((1u << lane) - 1));
+        if (e >= 0) sorted[s_cnt[e] + rank] = i;
+        __syncwarp();
+        if (e >= 0 && rank == 0) s_cnt[e] += __popc(same);
+        __syncwarp();
+      }
+      if (lane == 0) s_entries = n;
+    }
+    if (GU && I8) {
+      for (int m = warp; m < p.M; m += W + 1) {
+        const uint4* row = reinterpret_cast<const uint4*>(p.x + m * p.ldx);
+        float top = 0.f;
+        for (int i = lane; i < p.K / 8; i += 32) {
+          const uint4 v = row[i];
+          const uint32_t q[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            top = max_nan(max_nan(top, fabsf(__uint_as_float(q[j] << 16))), fabsf(__uint_as_float(q[j] & 0xFFFF0000u)));
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+        if (lane == 0) {
+          s_xs[m] = __fdiv_rn(top, 127.f);
+          s_inv[m] = top == 0.f ? 0.f : __fdiv_rn(127.f, top);
+        }
+      }
+    }
+    __syncthreads();
+    ne = s_entries;
+  }
+
+  // ------------------------------------------------------------------ this CTA's units
+  const int nblk = (p.K + KU - 1) / KU;
+  const int tiles = (p.N + (GU ? 15 : 31)) / (GU ? 16 : 32);
+  const int whole = (DN ? ne : 1) * nblk;  // units whose sums meet before the epilogue
+  const int total = tiles * ne * nblk;
+  // equal shares; a short item stays in one CTA, which is cheaper than joining its parts
+  int share = (total + gridDim.x - 1) / gridDim.x;
+  if (share < whole && whole <= 2 * W) share = whole;
+  const int u0 = min(total, (int)blockIdx.x * share), u1 = min(total, u0 + share);
+
+  auto entry = [&](int a) {
+    if constexpr (LIN) return Entry{0, a * TT, min(TT, p.M - a * TT)};
+    return entries[a];
+  };
+  if (total == 0) {  // nothing was dispatched
+    if (DN) {
+      pdl_wait();
+      for (int i = blockIdx.x * THREADS + threadIdx.x; i < p.M * p.N; i += gridDim.x * THREADS)
+        reinterpret_cast<uint16_t*>(p.y)[(int64_t)(i / p.N) * p.ldy + i % p.N] = 0;
+    }
+    return;
+  }
+
+  if (warp < W) {
+    // ---------------------------------------------------------------- streaming and products
+    const int g = lane >> 2, t = lane & 3;
+    const uint32_t ring = smem_addr(smem) + (uint32_t)(warp * lay.depth * lay.stage);
+    constexpr int LPR = WB / 16, RPI = 32 / LPR;   // lanes per weight row, rows per copy
+    constexpr int LPT = XB / 16, TPI = 32 / LPT;   // lanes per token row, tokens per copy
+    constexpr int XCOPIES = TT / TPI;
+    const int cr = lane / LPR, cc = lane % LPR, tr = lane / LPT, tc = lane % LPT;
+    auto swz = [](int r) { return (((r & 1) << 2) | ((r >> 1) & 3)) & (LPR - 1); };
+    // slot of piece c of token m: the lanes of a read meet every bank once
+    auto xswz = [](int c, int m) {
+      if (XB == 128) return c ^ ((m & 1) << 2);
+      if (I8) return c ^ (m & 1);
+      return c ^ (FINE ? (m & 1) << 2 : (c >> 3) + ((m & 1) << 1));
+    };
+
+    Walk f;  // the next unit to copy
+    f.set(u0 + warp, nblk, ne);
+    int f_item = -1, f_valid = 0, f_toks = 0;
+    const uint8_t* f_w = nullptr;
+    int64_t f_x[XCOPIES];
+    auto target = [&]() {  // addresses of the item that f is in
+      if (f.item == f_item) return;
+      f_item = f.item;
+      const Entry en = entry(f.a);
+      const int n0 = f.tile * (GU ? 16 : 32);
+      f_valid = p.N - n0;
+      f_toks = en.count;
+      f_w = p.w + en.expert * p.w_estride + (int64_t)(n0 + cr) * p.ldw + cc * 16;
+#pragma unroll
+      for (int i = 0; i < XCOPIES; ++i) {
+        const int r = min(i * TPI + tr, en.count - 1);
+        int row = en.first + r;
+        if constexpr (!LIN) row = GU ? sorted[row] / p.topk : sorted[row];
+        f_x[i] = row * p.ldx + tc * 16;
+      }
+    };
+    const int64_t wstep = (int64_t)RPI * p.ldw, to_up = ((int64_t)p.N - 16) * p.ldw;
+    auto fetch_w = [&](uint32_t at) {
+      const bool in = f.kb * WB + cc * 16 < (I4 ? p.K / 2 : I8 ? p.K : p.K * 2);
+      const uint8_t* src = f_w + (int64_t)f.kb * WB;
+#pragma unroll
+      for (int i = 0; i < R / RPI; ++i) {
+        const int r = i * RPI + cr;
+        if (GU && i * RPI == 16) src += to_up;
+        cp16(at + r * WB + ((cc ^ swz(r)) * 16), src, in && (GU && i * RPI >= 16 ? r - 16 : r) < f_valid);
+        src += wstep;
+      }
+    };
+    auto fetch_x = [&](uint32_t at) {
+      const int kb = f.kb * XB + tc * 16;  // byte in the row
+      const bool in = kb < (LIN ? p.K : p.K * 2);
+#pragma unroll
+      for (int i = 0; i < XCOPIES; ++i) {
+        const int m = i * TPI + tr;
+        if (i * TPI < f_toks && m < lay.xt) cp16(at + R * WB + m * XB + xswz(tc, m) * 16, p.x + f_x[i] + f.kb * XB, in);
+      }
+    };
+
+    // scales of a unit: lane = row of the tile
+    constexpr int NS = I4 ? (FINE ? 4 : 1) : 1;
+    uint32_t sz_next[NS];
+    const uint16_t* sp = nullptr;
+    const uint8_t* zp = nullptr;
+    int s_item = -1;
+    auto scales = [&](const Walk& w) {
+      if constexpr (I4) {
+        if (w.item != s_item) {
+          s_item = w.item;
+          const int e = entry(w.a).expert, n0 = w.tile * (GU ? 16 : 32);
+          const int64_t row = GU ? (int64_t)(lane >= 16 ? p.N : 0) + min(n0 + (lane & 15), p.N - 1) : min(n0 + lane, p.N - 1);
+          sp = reinterpret_cast<const uint16_t*>(p.scale) + e * p.s_estride + row * p.lds;
+          if (ZP) zp = p.zero + e * p.z_estride + row * p.ldz;
+        }
+#pragma unroll
+        for (int j = 0; j < NS; ++j) {
+          const int k = w.kb * KU + j * 32;
+          const bool in = k < p.K;
+          const int gi = (in ? k : 0) >> p.group_shift;
+          // a scale leaves the low bits of its fp32 image free for the zero point
+          sz_next[j] = in ? (uint32_t)sp[gi] << 16 | (ZP ? zp[gi] : 0u) : 0u;
+        }
+      }
+    };
+
+    Sum acc[2][NT][4];
+    float part[2][NT][4];  // INT8: sums of the last units, exact; BF16: all sums
+    int folded = 0;
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          acc[mt][nt][i] = 0;
+          part[mt][nt][i] = 0.f;
+        }
+    auto fold = [&]() {
+      if constexpr (!I4) {
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if constexpr (I8)
+                acc[mt][nt][i] += __float2int_rn(part[mt][nt][i]);
+              else
+                acc[mt][nt][i] = part[mt][nt][i];
+              part[mt][nt][i] = 0.f;
+            }
+        folded = 0;
+      }
+    };
+
+    // weights do not depend on the launch before (DOWN); activations do
+    const int pre = lay.depth - 1;
+    {
+      Walk first = f;
+      for (int d = 0; d < pre; ++d) {
+        if (f.u < u1) {
+          target();
+          fetch_w(ring + d * lay.stage);
+        }
+        f.next(W, nblk, ne);
+      }
+      if (DN) {
+        pdl_wait();
+        pdl_launch_dependents();
+        if (I8) {
+          for (int i = threadIdx.x; i < P; i += W * 32) {
+            const float top = __uint_as_float(__ldcg(p.amax + i));
+            s_xs[i] = __fdiv_rn(top, 127.f);
+            s_inv[i] = top == 0.f ? 0.f : __fdiv_rn(127.f, top);
+          }
+        }
+      }
+      f = first;
+      for (int d = 0; d < pre; ++d) {
+        if (f.u < u1) {
+          target();
+          fetch_x(ring + d * lay.stage);
+        }
+        cp_commit();
+        f.next(W, nblk, ne);
+      }
+    }
+    if (DN && I8) {
+      __syncthreads();
+      // every CTA has read the maxima once all have counted in: they are zero for the next call
+      if (threadIdx.x == 0) {
+        __threadfence();
+        s_entries = atomicAdd(p.tickets + gridDim.x, 1u) == gridDim.x - 1;
+      }
+      __syncthreads();
+      if (s_entries) {
+        for (int i = threadIdx.x; i < P; i += W * 32) p.amax[i] = 0u;
+        if (threadIdx.x == 0) p.tickets[gridDim.x] = 0u;
+      }
+    }
+
+    Walk c, n;  // the unit to compute, and the one after it
+    c.set(u0 + warp, nblk, ne);
+    n = c;
+    const int item0 = u0 / nblk, item1 = u1 > u0 ? (u1 - 1) / nblk : item0 - 1;
+    int done = item0, c_item = -1;
+    bool mine = false;  // a unit of item `done` has been added
+    float inv[NT] = {};
+    uint32_t slot = 0;
+    const int cap_t = lay.xt - 1;
+    if (c.u < u1) scales(c);
+    for (;;) {
+      const int to = c.u < u1 ? c.item : item1 + 1;
+      for (; done < to; ++done) {
+        // leave the sums of item `done` to the last warp
+        const int b = (done - item0) % kBuffers;
+        if (done - item0 >= kBuffers) bar_sync<kEmpty, THREADS>(b);
+        if (mine) {
+          fold();
+          Sum* s = reinterpret_cast<Sum*>(smem + lay.sums) + (b * W + warp) * (TT * kPitch);
+#pragma unroll
+          for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                s[(nt * 8 + 2 * t + (i & 1)) * kPitch + mt * 16 + g + 8 * (i >> 1)] = acc[mt][nt][i];
+                acc[mt][nt][i] = 0;
+              }
+          mine = false;
+        }
+        bar_arrive<kFull, THREADS>(b);
+      }
+      if (c.u >= u1) break;
+      mine = true;
+      if (I8 && !LIN && c.item != c_item) {
+        c_item = c.item;
+        const Entry en = entry(c.a);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const int row = sorted[en.first + min(nt * 8 + g, en.count - 1)];
+          inv[nt] = s_inv[GU ? row / p.topk : row];
+        }
+      }
+      cp_wait(pre - 1);
+      __syncwarp();  // every lane's copies of this unit have landed, and the unit before is read
+      {
+        const uint32_t at = ring + (slot == 0 ? pre : slot - 1) * lay.stage;
+        if (f.u < u1) {
+          target();
+          fetch_w(at);
+          fetch_x(at);
+        }
+        cp_commit();
+        f.next(W, nblk, ne);
+      }
+      const uint32_t wat = ring + slot * lay.stage + g * WB, xat = ring + slot * lay.stage + R * WB;
+      if (++slot == (uint32_t)lay.depth) slot = 0;
+      uint32_t sz[NS];
+#pragma unroll
+      for (int j = 0; j < NS; ++j) sz[j] = sz_next[j];
+      n.next(W, nblk, ne);
+      if (n.u < u1) scales(n);
+
+      if constexpr (I4) {
+        uint32_t wv[2][2][4];
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t at = wat + (mt * 16 + h * 8) * WB;
+            if constexpr (FINE) {
+              // word t of every 32-k piece, so that an MMA stays inside one group
+#pragma unroll
+              for (int j = 0; j < 4; ++j) wv[mt][h][j] = lds4(at + (j ^ swz(g)) * 16 + t * 4);
+            } else {
+              const uint4 v = lds16(at + (t ^ swz(g)) * 16);
+              wv[mt][h][0] = v.x;
+              wv[mt][h][1] = v.y;
+              wv[mt][h][2] = v.z;
+              wv[mt][h][3] = v.w;
+            }
+          }
+        uint32_t negz[2][2];
+        float sc[2][2], grp[2][NT][4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (j == 0 || FINE) {
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const uint32_t v = __shfl_sync(0xffffffffu, sz[FINE ? j : 0], mt * 16 + h * 8 + g);
+                sc[mt][h] = 64.f * (p.scale_fp16 ? __half2float(__ushort_as_half(v >> 16)) : __uint_as_float(v & 0xFFFF0000u));
+                // -z / 64 from z's pattern: z 2^-133 times -2^127
+                negz[mt][h] = ZP ? fma_bf16x2(__byte_perm(v, 0u, 0x4040), 0xFF00FF00u, 0u) : 0xBE00BE00u;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) grp[mt][nt][2 * h] = grp[mt][nt][2 * h + 1] = 0.f;
+              }
+          }
+          uint4 bx[NT];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const int m = min(nt * 8 + g, cap_t);
+            bx[nt] = pair_up(lds16(xat + m * XB + xswz(FINE ? j * 4 + t : t * 4 + j, m) * 16));
+          }
+#pragma unroll
+          for (int mt = 0; mt < 2; ++mt) {
+            uint32_t q0[4], q1[4];
+            codes_to_bf16(wv[mt][0][j], negz[mt][0], q0);
+            codes_to_bf16(wv[mt][1][j], negz[mt][1], q1);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              mma_bf16_16816(grp[mt][nt], q0[0], q1[0], q0[1], q1[1], bx[nt].x, bx[nt].y);
+              mma_bf16_16816(grp[mt][nt], q0[2], q1[2], q0[3], q1[3], bx[nt].z, bx[nt].w);
+            }
+          }
+          if (FINE || j == 3) {
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[mt][nt][i] = fmaf(sc[mt][i >> 1], grp[mt][nt][i], acc[mt][nt][i]);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          uint4 wv[2][2];
+#pragma unroll
+          for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) wv[mt][h] = lds16(wat + (mt * 16 + h * 8) * WB + ((4 * j + t) ^ swz(g)) * 16);
+          if constexpr (I8) {
+            uint32_t b[NT][8];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              const int m = min(nt * 8 + g, cap_t);
+              if constexpr (LIN) {
+                const uint4 v = lds16(xat + m * XB + xswz(4 * j + t, m) * 16);
+                s8x4_to_f16x2x2(v.x, b[nt][0], b[nt][1]);
+                s8x4_to_f16x2x2(v.y, b[nt][2], b[nt][3]);
+                s8x4_to_f16x2x2(v.z, b[nt][4], b[nt][5]);
+                s8x4_to_f16x2x2(v.w, b[nt][6], b[nt][7]);
+              } else {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  const uint4 v = lds16(xat + m * XB + xswz(8 * j + 2 * t + i, m) * 16);
+                  b[nt][4 * i] = quant2(v.x, inv[nt]);
+                  b[nt][4 * i + 1] = quant2(v.y, inv[nt]);
+                  b[nt][4 * i + 2] = quant2(v.z, inv[nt]);
+                  b[nt][4 * i + 3] = quant2(v.w, inv[nt]);
+                }
+              }
+            }
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt) {
+              const uint32_t lo[4] = {wv[mt][0].x, wv[mt][0].y, wv[mt][0].z, wv[mt][0].w};
+              const uint32_t hi[4] = {wv[mt][1].x, wv[mt][1].y, wv[mt][1].z, wv[mt][1].w};
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                uint32_t a0, a1, a2, a3;
+                s8x4_to_f16x2x2(lo[i], a0, a2);
+                s8x4_to_f16x2x2(hi[i], a1, a3);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) mma_f16_16816(part[mt][nt], a0, a1, a2, a3, b[nt][2 * i], b[nt][2 * i + 1]);
+              }
+            }
+          } else {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              const int m = min(nt * 8 + g, cap_t);
+              const uint4 v = lds16(xat + m * XB + xswz(4 * j + t, m) * 16);
+#pragma unroll
+              for (int mt = 0; mt < 2; ++mt) {
+                mma_bf16_16816(part[mt][nt], wv[mt][0].x, wv[mt][1].x, wv[mt][0].y, wv[mt][1].y, v.x, v.y);
+                mma_bf16_16816(part[mt][nt], wv[mt][0].z, wv[mt][1].z, wv[mt][0].w, wv[mt][1].w, v.z, v.w);
+              }
+            }
+          }
+        }
+        if (I8 && ++folded == 8) fold();  // 1024 k: sums of at most 2^24
+      }
+      c = n;
+    }
+  } else {
+    // ---------------------------------------------------------------- sums and results: lane = row
+    if (DN) {
+      pdl_wait();
+      if (I8) {
+        __syncthreads();
+        __syncthreads();
+      }
+    }
+    const int slot_floats = (DN ? p.M : TT) * 32;
+    // 0: the part of an item that began in an earlier CTA, 1: of one that ends in a later CTA
+    auto slot_of = [&](int cta, int tail) { return p.slots + ((int64_t)cta * 2 + tail) * slot_floats + lane; };
+    // counts a part of the item of units [a, b) in; true for the last one, which finds all parts stored
+    auto last_part = [&](int a, int b) {
+      const int c0 = a / share, c1 = (b - 1) / share;
+      __threadfence();
+      __syncwarp();
+      unsigned before = 0;
+      if (lane == 0) {
+        before = atomicAdd(p.tickets + c0, 1u);
+        if (before == (unsigned)(c1 - c0)) p.tickets[c0] = 0u;
+      }
+      before = __shfl_sync(0xffffffffu, before, 0);
+      __threadfence();
+      return before == (unsigned)(c1 - c0);
+    };
+    const int item0 = u0 / nblk, item1 = u1 > u0 ? (u1 - 1) / nblk : item0 - 1;
+    Walk c;
+    c.set(item0 * nblk, nblk, ne);
+    if (DN)
+      for (int m = 0; m < p.M; ++m) s_y[m * 32 + lane] = 0.f;
+    for (int it = item0; it <= item1; ++it) {
+      const Entry en = entry(c.a);
+      const int b = (it - item0) % kBuffers;
+      bar_sync<kFull, THREADS>(b);
+      Sum v[TT];
+#pragma unroll
+      for (int i = 0; i < TT; ++i) v[i] = 0;
+      {
+        const int a = max(u0, it * nblk), units = min(u1, (it + 1) * nblk) - a;
+        int w = (a - u0) % W;
+        const Sum* s = reinterpret_cast<const Sum*>(smem + lay.sums) + b * W * (TT * kPitch) + lane;
+        for (int i = 0; i < min(units, W); ++i) {
+#pragma unroll
+          for (int k = 0; k < TT; ++k)
+            if (k < en.count) v[k] += s[w * (TT * kPitch) + k * kPitch];
+          if (++w == W) w = 0;
+        }
+      }
+      if (it + kBuffers <= item1) bar_arrive<kEmpty, THREADS>(b);
+
+      bool ready = true;
+      if (!DN && (it * nblk < u0 || (it + 1) * nblk > u1)) {
+        // the item is shared with other CTAs: the last of them adds the parts in the order of K
+        float* mine = slot_of(blockIdx.x, it * nblk >= u0);
+#pragma unroll
+        for (int k = 0; k < TT; ++k)
+          if (k < en.count) __stcg(reinterpret_cast<Sum*>(mine) + k * 32, v[k]);
+        ready = last_part(it * nblk, (it + 1) * nblk);
+        if (ready) {
+          const int c0 = it * nblk / share, c1 = ((it + 1) * nblk - 1) / share;
+#pragma unroll
+          for (int i = 0; i < TT; ++i) v[i] = 0;
+          for (int q = c0; q <= c1; ++q) {
+            const Sum* s = reinterpret_cast<const Sum*>(slot_of(q, q == c0));
+#pragma unroll
+            for (int k = 0; k < TT; ++k)
+              if (k < en.count) v[k] += __ldcg(s + k * 32);
+          }
+        }
+      }
+      if (GU && ready) {
+        const int i = c.tile * 16 + (lane & 15);
+        const bool in = i < p.N;
+        const float ws = I8 && in ? reinterpret_cast<const float*>(p.scale)[en.expert * p.s_estride + (lane >= 16 ? p.N : 0) + i] : 1.f;
+#pragma unroll
+        for (int k = 0; k < TT; ++k)
+          if (k < en.count) {
+            const int pair = sorted[en.first + k];
+            float f = (float)v[k];
+            if (I8) f = f * s_xs[pair / p.topk] * ws;
+            const float u = __shfl_down_sync(0xffffffffu, f, 16);
+            const uint16_t hb = f32_to_bf16_rn(gated_act(f, u, p.alpha, p.limit));
+            const bool store = lane < 16 && in;
+            if (store) p.h[pair * p.ldh + i] = hb;
+            if (I8) {
+              const unsigned top = __reduce_max_sync(0xffffffffu, store ? (unsigned)(hb & 0x7FFF) << 16 : 0u);
+              if (lane == 0) atomicMax(p.amax + pair, top);
+            }
+          }
+      }
+      if (LIN && ready) {
+        const int n = c.tile * 32 + lane;
+        if (n < p.N) {
+          const float ws = reinterpret_cast<const float*>(p.scale)[p.lds ? n : 0];
+          const float bias = p.bias ? bf16_bits_to_f32(p.bias[n]) : 0.f;
+#pragma unroll
+          for (int k = 0; k < TT; ++k)
+            if (k < en.count) {
+              const int m = en.first + k;
+              const float f = __fmul_rn(__fmul_rn((float)v[k], p.x_scale[m]), ws);
+              const int64_t at = (int64_t)m * p.ldy + n;
+              if (p.out_type == QL_OUT_FP32) {
+                reinterpret_cast<float*>(p.y)[at] = p.bias ? f + bias : f;
+              } else if (p.out_type == QL_OUT_FP16) {
+                __half o = __float2half_rn(f);
+                if (p.bias) o = __float2half_rn(__half2float(o) + bias);
+                reinterpret_cast<__half*>(p.y)[at] = o;
+              } else {
+                uint16_t o = f32_to_bf16_rn(f);
+                if (p.bias) o = f32_to_bf16_rn(bf16_bits_to_f32(o) + bias);
+                reinterpret_cast<uint16_t*>(p.y)[at] = o;
+              }
+            }
+        }
+      }
+      if (DN) {
+        const int n = c.tile * 32 + lane;
+        const float ws = I8 && n < p.N ? reinterpret_cast<const float*>(p.scale)[en.expert * p.s_estride + n] : 1.f;
+#pragma unroll
+        for (int k = 0; k < TT; ++k)
+          if (k < en.count) {
+            const int pair = sorted[en.first + k];
+            float f = (float)v[k];
+            if (I8) f = f * s_xs[pair] * ws;
+            s_y[pair / p.topk * 32 + lane] += s_wt[pair] * f;
+          }
+        if (it == item1 || c.a == ne - 1) {
+          // the end of this CTA's part of the tile
+          const int a = c.tile * whole, b1 = a + whole;
+          bool write = true, parts = a < u0 || b1 > u1;
+          if (parts) {
+            float* mine = slot_of(blockIdx.x, a >= u0);
+            for (int m = 0; m < p.M; ++m) __stcg(mine + m * 32, s_y[m * 32 + lane]);
+            write = last_part(a, b1);
+          }
+          const int c0 = a / share, c1 = (b1 - 1) / share;
+          for (int m = 0; m < p.M; ++m) {
+            float y = s_y[m * 32 + lane];
+            s_y[m * 32 + lane] = 0.f;
+            if (!write) continue;
+            if (parts) {
+              y = 0.f;
+              for (int q = c0; q <= c1; ++q) y += __ldcg(slot_of(q, q == c0) + m * 32);
+            }
+            if (n < p.N) reinterpret_cast<uint16_t*>(p.y)[(int64_t)m * p.ldy + n] = f32_to_bf16_rn(y);
+          }
+        }
+      }
+      c.next(nblk, nblk, ne);
+    }
+  }
+}
+
+template <int FMT, int MODE, int NT, bool FINE, bool ZP>
+cudaError_t launch(const StreamArgs& a, cudaStream_t st) {
+  constexpr int W = compute_warps(FMT), TT = NT * 8;
+  auto* kfn = stream_kernel<FMT, MODE, NT, FINE, ZP>;
+  static OncePerDevice once;
+  if (const cudaError_t e = raise_smem_limit(kfn, once); e != cudaSuccess) return e;
+  const int P = MODE == STREAM_LINEAR ? 0 : a.M * a.topk;
+  Layout l = {};
+  l.xt = a.M < TT ? a.M : TT;
+  l.stage = R * row_bytes(FMT) + l.xt * token_bytes(FMT, MODE);
+  const int lists = P * (int)(sizeof(Entry) + 5 * 4) + (P ? a.E * 4 : 0) + (MODE == STREAM_DOWN ? a.M * 128 : 0);
+  const int sums = kBuffers * W * TT * kPitch * 4;
+  l.depth = (227 * 1024 - 256 - lists - sums) / (W * l.stage);
+  if (l.depth > 6) l.depth = 6;
+  l.sums = W * l.depth * l.stage;
+  l.lists = l.sums + sums;
+  l.total = l.lists + lists;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kNumSMs, 1, 1);
+  cfg.blockDim = dim3((W + 1) * 32, 1, 1);
+  cfg.dynamicSmemBytes = (size_t)l.total;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kfn, a, l);
+}
+
+template <int MODE>
+cudaError_t launch_moe(int fmt, const StreamArgs& a, cudaStream_t st) {
+  if (fmt == STREAM_BF16) return launch<STREAM_BF16, MODE, 1, false, false>(a, st);
+  if (fmt == STREAM_INT8) return launch<STREAM_INT8, MODE, 1, false, false>(a, st);
+  if (a.group_shift < 7)
+    return a.zero ? launch<STREAM_INT4, MODE, 1, true, true>(a, st) : launch<STREAM_INT4, MODE, 1, true, false>(a, st);
+  return a.zero ? launch<STREAM_INT4, MODE, 1, false, true>(a, st) : launch<STREAM_INT4, MODE, 1, false, false>(a, st);
+}
+
+}  // namespace
+
+size_t stream_slot_bytes(int64_t M) {
+  const int64_t columns = M < kStreamMaxTokens ? kStreamMaxTokens : M;
+  return (size_t)kNumSMs * 2 * columns * 32 * 4;
+}
+
+cudaError_t launch_stream(int fmt, int mode, const StreamArgs& a, cudaStream_t st) {
+  if (mode == STREAM_GATE_UP) return launch_moe<STREAM_GATE_UP>(fmt, a, st);
+  if (mode == STREAM_DOWN) return launch_moe<STREAM_DOWN>(fmt, a, st);
+  if (a.M <= 8) return launch<STREAM_INT8, STREAM_LINEAR, 1, false, false>(a, st);
+  return launch<STREAM_INT8, STREAM_LINEAR, 2, false, false>(a, st);
+}
+
+}  // namespace ql

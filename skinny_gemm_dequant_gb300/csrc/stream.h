@@ -1,0 +1,58 @@
+// Host-side declarations of the weight-streaming kernels for few tokens (kernels_stream.cu): the
+// mixture-of-experts layers on bf16, 8-bit and 4-bit weights and the linear on 8-bit codes.
+#pragma once
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "internal.h"
+
+namespace ql {
+
+enum { STREAM_BF16 = 0, STREAM_INT8 = 1, STREAM_INT4 = 2 };
+enum { STREAM_GATE_UP = 0, STREAM_DOWN = 1, STREAM_LINEAR = 2 };
+
+constexpr int kStreamRows = 32;       // weight rows of a tile
+constexpr int kMoeMaxTokens = 64;     // of a mixture-of-experts call
+constexpr int kMoeMaxTopk = 16;
+constexpr int kStreamMaxTokens = 32;  // of a linear call
+
+struct StreamArgs {
+  const uint8_t* x;  // activations: bf16 rows (tokens; DOWN: h by pair), LINEAR: 8-bit codes
+  int64_t ldx;       // bytes
+  int K;             // summed elements
+  const uint8_t* w;
+  int64_t ldw, w_estride;  // bytes
+  int N;                   // outputs: GATE_UP: I (2I rows of W13), DOWN: H, LINEAR: N
+  const void* scale;       // INT4: bf16 / fp16 bits [rows, lds]; INT8: fp32 [rows]
+  int64_t lds, s_estride;  // elements
+  int scale_fp16;
+  const uint8_t* zero;     // INT4: [rows, ldz] or null: 8
+  int64_t ldz, z_estride;
+  int group_shift;
+  // routing (GATE_UP, DOWN)
+  const uint16_t* logits;  // bf16 [M, E] or null
+  const int32_t* ids;      // [M, topk] and fp32 weights, where logits are null
+  const float* wts;
+  int M, E, topk, renorm;
+  int32_t* ids_out;  // nullable
+  float* wts_out;
+  float alpha, limit;
+  uint16_t* h;  // GATE_UP writes bf16 [M topk, ldh]
+  int64_t ldh;
+  unsigned* amax;     // INT8: [M topk] bits of max|h|, zero between calls
+  unsigned* tickets;  // zero between calls
+  float* slots;       // sums of tiles that CTAs share
+  // DOWN, LINEAR
+  void* y;
+  int64_t ldy;
+  int out_type;          // LINEAR: QL_OUT_*
+  const uint16_t* bias;  // LINEAR
+  const float* x_scale;  // LINEAR: [M]
+};
+
+cudaError_t launch_stream(int fmt, int mode, const StreamArgs& a, cudaStream_t st);
+size_t stream_slot_bytes(int64_t M);
+// of QL_OP_INT8_CODES and QL_OP_MOE_FEW (api_stream.cu)
+size_t stream_workspace_bytes(int op, int64_t M, int64_t N, int64_t K, int E, int topk);
+
+}  // namespace ql

@@ -1,0 +1,102 @@
+"""Linear on given 8-bit codes, and the codes: exact against integers.
+
+acc is exact; (float)acc, the product with x_scale and the one with w_scale are each rounded to fp32,
+then the result to its type: compared bit for bit with the same three roundings in numpy."""
+import numpy as np
+import pytest
+import torch
+
+from _util import bits_of, gpu_lib
+from oracle import moe_few_oracle as MO
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def ql():
+    return gpu_lib()
+
+
+def make(M, N, K, seed=0, pad_x=0, pad_w=0, lo=-128):
+    g = np.random.default_rng(seed)
+    xq = g.integers(lo, 128, (M, K + 16 * pad_x), dtype=np.int8)
+    w = g.integers(lo, 128, (N, K + 16 * pad_w), dtype=np.int8)
+    return xq, (g.random(M) * 0.05).astype(np.float32), w, (g.random(N) * 0.01).astype(np.float32)
+
+
+def want(acc, xs, ws, dtype, bias=None):
+    f = torch.from_numpy(acc.astype(np.float32) * xs[:, None] * ws)  # fp32 all along
+    y = f.to(dtype)
+    return y if bias is None else (y.float() + bias.float()).to(dtype)
+
+
+def call(ql, xq, xs, w, ws, K, **kw):
+    return ql.qlinear_int8(torch.from_numpy(xq).cuda()[:, :K], torch.from_numpy(xs).cuda(),
+                           torch.from_numpy(w).cuda()[:, :K], torch.from_numpy(ws).cuda(), **kw)
+
+
+SIZES = [(1, 512, 1024), (1, 1, 16), (2, 33, 48), (3, 5120, 272), (8, 100, 2080), (9, 31, 1040), (16, 257, 528),
+         (17, 64, 2048), (32, 130, 1600)]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("M,N,K", SIZES)
+def test_exact(ql, M, N, K, dtype):
+    xq, xs, w, ws = make(M, N, K, seed=M + N, pad_x=M % 3, pad_w=N % 2)
+    acc = MO.linear_codes(xq[:, :K], xs, w[:, :K], ws)[0]
+    bias = torch.randn(N, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16) if M % 2 else None
+    y, path = call(ql, xq, xs, w, ws, K, bias=None if bias is None else bias.cuda(), out_dtype=dtype, debug=True)
+    assert path == "int8_codes_skinny"
+    assert torch.equal(y.cpu(), want(acc, xs, ws, dtype, bias))
+    one = call(ql, xq, xs, w, ws[:1], K, out_dtype=dtype)
+    assert torch.equal(one.cpu(), want(acc, xs, np.repeat(ws[:1], N), dtype))
+
+
+def test_sums_of_one_sign_are_exact(ql):
+    """Codes of -128 over a long K: every partial sum is a power of two, the last one 2^14 K."""
+    for M, K in ((2, 17408), (24, 131056)):
+        xq, w = np.full((M, K), -128, np.int8), np.full((40, K), -128, np.int8)
+        w[1] = 127
+        xq[1, ::2] = 1
+        one = np.ones(max(M, 40), np.float32)
+        y = call(ql, xq, one[:M], w, one[:40], K, out_dtype=torch.float32)
+        acc = MO.linear_codes(xq, one[:M], w, one[:40])[0]
+        assert np.array_equal(y.cpu().numpy(), acc.astype(np.float32))
+
+
+@pytest.mark.parametrize("M", [1, 7, 32])
+def test_output_rows_beyond_the_call_stay(ql, M):
+    xq, xs, w, ws = make(M, 45, 160, seed=3)
+    wide = torch.full((M + 2, 64), 5.0, dtype=torch.bfloat16, device="cuda")
+    y = call(ql, xq, xs, w, ws, 160, out=wide[1:M + 1, 8:53])
+    acc = MO.linear_codes(xq, xs, w, ws)[0]
+    assert torch.equal(y.cpu(), want(acc, xs, ws, torch.bfloat16))
+    wide[1:M + 1, 8:53] = 5.0
+    assert (wide == 5.0).all()
+
+
+@pytest.mark.parametrize("M,K", [(1, 8), (3, 5120), (40, 264)])
+def test_quantize(ql, M, K):
+    g = torch.Generator().manual_seed(K)
+    x = torch.randn(M, K + 8, generator=g).to(torch.bfloat16)
+    x[0, :] = 0
+    x[-1, 0] = 31.75  # ties: quarters of 31.75 / 127
+    x[-1, 1:8] = torch.tensor([0.125, 0.375, -0.625, 31.625, -31.75, 1.125, -0.125])
+    q, s = ql.quantize_int8(x.cuda()[:, :K])
+    v = x[:, :K].float().numpy()
+    scale = np.abs(v).max(axis=1) / np.float32(127)
+    assert np.array_equal(s.cpu().numpy(), scale)
+    with np.errstate(invalid="ignore", divide="ignore"):
+        codes = np.where(scale[:, None] > 0, np.rint(v / scale[:, None]), 0).astype(np.int8)
+    assert np.array_equal(q.cpu().numpy(), codes)
+
+
+@pytest.mark.parametrize("M", [1, 5, 16, 30])
+def test_same_as_the_linear_that_quantises_itself(ql, M):
+    g = torch.Generator().manual_seed(M)
+    x = torch.randn(M, 1280, generator=g).to(torch.bfloat16).cuda()
+    w = torch.randint(-127, 128, (300, 1280), generator=g, dtype=torch.int8).cuda()
+    ws = (torch.rand(300, generator=g) * 0.01).cuda()
+    bias = torch.randn(300, generator=g).to(torch.bfloat16).cuda()
+    codes, scale = ql.quantize_int8(x)
+    assert torch.equal(ql.qlinear_int8(codes, scale, w, ws, bias), ql.qlinear_int8_w8a8(x, w, ws, bias))
