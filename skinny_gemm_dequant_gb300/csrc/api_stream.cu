@@ -88,7 +88,8 @@ StreamArgs moe_args(const Moe& a) {
   s.tickets = at<unsigned>(a.ws, kTicketOff);
   s.amax = at<unsigned>(a.ws, kAmaxOff);
   s.slots = at<float>(a.ws, workspace_zero_bytes());
-  s.h = at<uint16_t>(a.ws, workspace_zero_bytes() + al256(stream_slot_bytes(a.M)));
+  s.weights = at<float>(a.ws, workspace_zero_bytes() + al256(stream_slot_bytes(a.M)));
+  s.h = reinterpret_cast<uint16_t*>(s.weights + kMoeMaxTokens * kMoeMaxTopk);
   s.ldh = cdiv(a.I, 8) * 8;
   return s;
 }
@@ -137,7 +138,8 @@ size_t stream_workspace_bytes(int op, int64_t M, int64_t N, int64_t K, int E, in
   if (op == QL_OP_INT8_CODES) return workspace_zero_bytes() + stream_slot_bytes(1);
   if (E <= 0 || topk <= 0) return 0;
   if (M > kMoeMaxTokens || topk > kMoeMaxTopk || K > 32768) return workspace_zero_bytes();  // refused
-  return workspace_zero_bytes() + al256(stream_slot_bytes(M)) + (size_t)M * topk * cdiv(K, 8) * 8 * 2;
+  return workspace_zero_bytes() + al256(stream_slot_bytes(M)) +
+         kMoeMaxTokens * kMoeMaxTopk * 4 + (size_t)M * topk * cdiv(K, 8) * 8 * 2;
 }
 }  // namespace ql
 

@@ -24,6 +24,7 @@ namespace {
 constexpr int R = kStreamRows;
 constexpr int kPitch = 36;  // of a column of sums: lanes (g, t) write 8 t + g, all banks once
 constexpr int kBuffers = 2;
+constexpr int kNone = 0x7FFFFFFF;  // the expert of a pair that is left out
 
 __host__ __device__ constexpr int compute_warps(int fmt) { return fmt == STREAM_INT4 ? 12 : 8; }
 __host__ __device__ constexpr int unit_k(int fmt) { return fmt == STREAM_BF16 ? 64 : 128; }
@@ -63,7 +64,6 @@ __device__ __forceinline__ uint32_t lds4(uint32_t a) {
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
   return v;
 }
-__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 template <int ID0, int THREADS>
 __device__ __forceinline__ void bar_sync(int b) {
   asm volatile("bar.sync %0, %1;" ::"r"(ID0 + b), "n"(THREADS) : "memory");
@@ -151,15 +151,15 @@ __global__ void __launch_bounds__((compute_warps(FMT) + 1) * 32, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int P = LIN ? 0 : p.M * p.topk;
 
-  // lists: entries, sorted pairs, weights by pair, (INT8) factor and scale by row of x, experts' counts
+  // lists: entries, sorted pairs, weights and ids by pair, (INT8) factor and scale by row of x
   Entry* entries = reinterpret_cast<Entry*>(smem + lay.lists);
-  int* sorted = reinterpret_cast<int*>(entries + P);
+  Entry* heads = entries + P;
+  int* sorted = reinterpret_cast<int*>(heads + P);
   float* s_wt = reinterpret_cast<float*>(sorted + P);
-  float* s_inv = s_wt + P;
+  int* s_id = reinterpret_cast<int*>(s_wt + P);
+  float* s_inv = reinterpret_cast<float*>(s_id + P);
   float* s_xs = s_inv + P;
-  int* s_id = reinterpret_cast<int*>(s_xs + P);
-  int* s_cnt = s_id + P;
-  float* s_y = reinterpret_cast<float*>(s_cnt + (LIN ? 0 : p.E));  // DOWN: [M][32]
+  float* s_y = s_xs + P;  // DOWN: [M][32]
   __shared__ int s_entries;
 
   if (!DN) {
@@ -171,67 +171,25 @@ __global__ void __launch_bounds__((compute_warps(FMT) + 1) * 32, 1)
     ne = (p.M + TT - 1) / TT;
   } else {
     // ---------------------------------------------------------------- routing and dispatch
-    // (DOWN runs this before its wait: the launch before, GATE_UP, has waited for what wrote the
-    // logits.)
-    for (int e = threadIdx.x; e < p.E; e += THREADS) s_cnt[e] = 0;
+    // Every CTA chooses for itself.  DOWN does so before its wait: the launch before, GATE_UP, has
+    // waited for what wrote the logits.  The weights are computed later, by one CTA for each token.
+#pragma unroll 1
     for (int m = warp; m < p.M; m += W + 1) {
       int id = -1;
-      float wt = 0.f;
-      if (p.logits) {
-        route_token_warp(p.logits + (int64_t)m * p.E, p.E, p.topk, p.renorm != 0, id, wt);
-      } else if (lane < p.topk) {
+      float wt;
+      if (p.logits)
+        route_token_warp<false>(p.logits + (int64_t)m * p.E, p.E, p.topk, false, id, wt);
+      else if (lane < p.topk)
         id = p.ids[m * p.topk + lane];
-        wt = p.wts[m * p.topk + lane];
-        if (id < 0 || id >= p.E) id = -1;  // padding: not dispatched
-      }
-      if (lane < p.topk) {
-        s_id[m * p.topk + lane] = id;
-        s_wt[m * p.topk + lane] = wt;
-        if (GU && blockIdx.x == 0) {
-          if (p.ids_out) p.ids_out[m * p.topk + lane] = id;
-          if (p.wts_out) p.wts_out[m * p.topk + lane] = wt;
-        }
-      }
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < P; i += THREADS)
-      if (s_id[i] >= 0) atomicAdd(&s_cnt[s_id[i]], 1);
-    __syncthreads();
-    if (warp == 0) {
-      // counts to first positions, and the passes of up to TT pairs of every expert in use
-      int pos = 0, n = 0;
-      for (int e0 = 0; e0 < p.E; e0 += 32) {
-        const int e = e0 + lane, c = e < p.E ? s_cnt[e] : 0, k = (c + TT - 1) / TT;
-        int ci = c, ki = k;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int a = __shfl_up_sync(0xffffffffu, ci, o), b = __shfl_up_sync(0xffffffffu, ki, o);
-          if (lane >= o) {
-            ci += a;
-            ki += b;
-          }
-        }
-        if (e < p.E) s_cnt[e] = pos + ci - c;
-        for (int i = 0; i < k; ++i) entries[n + ki - k + i] = {e, pos + ci - c + i * TT, min(TT, c - i * TT)};
-        pos += __shfl_sync(0xffffffffu, ci, 31);
-        n += __shfl_sync(0xffffffffu, ki, 31);
-      }
-      __syncwarp();
-      for (int i0 = 0; i0 < P; i0 += 32) {
-        const int i = i0 + lane, e = i < P ? s_id[i] : -1;
-        const unsigned same = __match_any_sync(0xffffffffu, e);
-        const int rank = __popc(same & ((1u << lane) - 1));
-        if (e >= 0) sorted[s_cnt[e] + rank] = i;
-        __syncwarp();
-        if (e >= 0 && rank == 0) s_cnt[e] += __popc(same);
-        __syncwarp();
-      }
-      if (lane == 0) s_entries = n;
+      if (id < 0 || id >= p.E) id = kNone;  // padding: not dispatched
+      if (lane < p.topk) s_id[m * p.topk + lane] = id;
     }
     if (GU && I8) {
-      for (int m = warp; m < p.M; m += W + 1) {
+#pragma unroll 1
+      for (int m = W - warp; m < p.M; m += W + 1) {  // (from the last warp on: the first ones route)
         const uint4* row = reinterpret_cast<const uint4*>(p.x + m * p.ldx);
         float top = 0.f;
+#pragma unroll 4
         for (int i = lane; i < p.K / 8; i += 32) {
           const uint4 v = row[i];
           const uint32_t q[4] = {v.x, v.y, v.z, v.w};
@@ -246,6 +204,36 @@ __global__ void __launch_bounds__((compute_warps(FMT) + 1) * 32, 1)
           s_inv[m] = top == 0.f ? 0.f : __fdiv_rn(127.f, top);
         }
       }
+    }
+    __syncthreads();
+    // a pair's place is the number of pairs before it by (expert, pair); every TT pairs of an expert
+    // begin a pass over its weights
+#pragma unroll 1
+    for (int i = threadIdx.x; i < P; i += THREADS) {
+      const int e = s_id[i];
+      int before = 0, rank = 0, all = 0;
+#pragma unroll 4
+      for (int j = 0; j < P; ++j) {
+        const int o = s_id[j];
+        before += o < e;
+        all += o == e;
+        rank += o == e && j < i;
+      }
+      sorted[before + rank] = i;
+      const bool head = e != kNone && rank % TT == 0;
+      heads[before + rank] = {e, before + rank, head ? min(TT, all - rank) : 0};
+    }
+    __syncthreads();
+    if (warp == 0) {
+      int n = 0;
+#pragma unroll 1
+      for (int i0 = 0; i0 < P; i0 += 32) {
+        const bool head = i0 + lane < P && heads[i0 + lane].count > 0;
+        const unsigned all = __ballot_sync(0xffffffffu, head);
+        if (head) entries[n + __popc(all & ((1u << lane) - 1))] = heads[i0 + lane];
+        n += __popc(all);
+      }
+      if (lane == 0) s_entries = n;
     }
     __syncthreads();
     ne = s_entries;
@@ -265,6 +253,22 @@ __global__ void __launch_bounds__((compute_warps(FMT) + 1) * 32, 1)
     if constexpr (LIN) return Entry{0, a * TT, min(TT, p.M - a * TT)};
     return entries[a];
   };
+  if (GU && warp == W && blockIdx.x < p.M) {
+    // the weights of a token, for the next launch
+    const int m = blockIdx.x;
+    int id = 0;
+    float wt = 0.f;
+    if (p.logits)
+      route_token_warp(p.logits + (int64_t)m * p.E, p.E, p.topk, p.renorm != 0, id, wt);
+    else if (lane < p.topk)
+      wt = p.wts[m * p.topk + lane];
+    if (lane < p.topk) {
+      const int i = m * p.topk + lane;
+      p.weights[i] = wt;
+      if (p.wts_out) p.wts_out[i] = wt;
+      if (p.ids_out) p.ids_out[i] = s_id[i] == kNone ? -1 : s_id[i];
+    }
+  }
   if (total == 0) {  // nothing was dispatched
     if (DN) {
       pdl_wait();
@@ -335,7 +339,8 @@ __global__ void __launch_bounds__((compute_warps(FMT) + 1) * 32, 1)
 
     // scales of a unit: lane = row of the tile
     constexpr int NS = I4 ? (FINE ? 4 : 1) : 1;
-    uint32_t sz_next[NS];
+    uint16_t s_next[NS];  // as loaded: turning them into numbers here would wait for them
+    uint8_t z_next[NS];
     const uint16_t* sp = nullptr;
     const uint8_t* zp = nullptr;
     int s_item = -1;
@@ -351,10 +356,9 @@ __global__ void __launch_bounds__((compute_warps(FMT) + 1) * 32, 1)
 #pragma unroll
         for (int j = 0; j < NS; ++j) {
           const int k = w.kb * KU + j * 32;
-          const bool in = k < p.K;
-          const int gi = (in ? k : 0) >> p.group_shift;
-          // a scale leaves the low bits of its fp32 image free for the zero point
-          sz_next[j] = in ? (uint32_t)sp[gi] << 16 | (ZP ? zp[gi] : 0u) : 0u;
+          const int gi = min(k, p.K - 1) >> p.group_shift;  // past the end: any finite sum of zeros
+          s_next[j] = k < p.K ? sp[gi] : (uint16_t)0;
+          if (ZP) z_next[j] = zp[gi];
         }
       }
     };
@@ -389,51 +393,34 @@ __global__ void __launch_bounds__((compute_warps(FMT) + 1) * 32, 1)
       }
     };
 
-    // weights do not depend on the launch before (DOWN); activations do
+    // DOWN: weights do not depend on the launch before, activations (h) do.  So the first steps of the
+    // loop below only copy: weights, then, after the wait, what meets them
     const int pre = lay.depth - 1;
-    {
-      Walk first = f;
-      for (int d = 0; d < pre; ++d) {
-        if (f.u < u1) {
-          target();
-          fetch_w(ring + d * lay.stage);
+    int warm = DN ? 2 * pre : pre;
+    const Walk first = f;
+    auto after_wait = [&]() {
+      pdl_wait();
+      pdl_launch_dependents();
+      if constexpr (I8) {
+#pragma unroll 1
+        for (int i = threadIdx.x; i < P; i += W * 32) {
+          const float top = __uint_as_float(__ldcg(p.amax + i));
+          s_xs[i] = __fdiv_rn(top, 127.f);
+          s_inv[i] = top == 0.f ? 0.f : __fdiv_rn(127.f, top);
         }
-        f.next(W, nblk, ne);
-      }
-      if (DN) {
-        pdl_wait();
-        pdl_launch_dependents();
-        if (I8) {
-          for (int i = threadIdx.x; i < P; i += W * 32) {
-            const float top = __uint_as_float(__ldcg(p.amax + i));
-            s_xs[i] = __fdiv_rn(top, 127.f);
-            s_inv[i] = top == 0.f ? 0.f : __fdiv_rn(127.f, top);
-          }
+        __syncthreads();
+        // every CTA has read the maxima once all have counted in: they are zero for the next call
+        if (threadIdx.x == 0) {
+          __threadfence();
+          s_entries = atomicAdd(p.tickets + gridDim.x, 1u) == gridDim.x - 1;
+        }
+        __syncthreads();
+        if (s_entries) {
+          for (int i = threadIdx.x; i < P; i += W * 32) p.amax[i] = 0u;
+          if (threadIdx.x == 0) p.tickets[gridDim.x] = 0u;
         }
       }
-      f = first;
-      for (int d = 0; d < pre; ++d) {
-        if (f.u < u1) {
-          target();
-          fetch_x(ring + d * lay.stage);
-        }
-        cp_commit();
-        f.next(W, nblk, ne);
-      }
-    }
-    if (DN && I8) {
-      __syncthreads();
-      // every CTA has read the maxima once all have counted in: they are zero for the next call
-      if (threadIdx.x == 0) {
-        __threadfence();
-        s_entries = atomicAdd(p.tickets + gridDim.x, 1u) == gridDim.x - 1;
-      }
-      __syncthreads();
-      if (s_entries) {
-        for (int i = threadIdx.x; i < P; i += W * 32) p.amax[i] = 0u;
-        if (threadIdx.x == 0) p.tickets[gridDim.x] = 0u;
-      }
-    }
+    };
 
     Walk c, n;  // the unit to compute, and the one after it
     c.set(u0 + warp, nblk, ne);
@@ -445,56 +432,68 @@ __global__ void __launch_bounds__((compute_warps(FMT) + 1) * 32, 1)
     uint32_t slot = 0;
     const int cap_t = lay.xt - 1;
     if (c.u < u1) scales(c);
+    uint32_t to_slot = 0;
+#pragma unroll 1
     for (;;) {
-      const int to = c.u < u1 ? c.item : item1 + 1;
-      for (; done < to; ++done) {
-        // leave the sums of item `done` to the last warp
-        const int b = (done - item0) % kBuffers;
-        if (done - item0 >= kBuffers) bar_sync<kEmpty, THREADS>(b);
-        if (mine) {
-          fold();
-          Sum* s = reinterpret_cast<Sum*>(smem + lay.sums) + (b * W + warp) * (TT * kPitch);
+      if (warm == 0) {
+        const int to = c.u < u1 ? c.item : item1 + 1;
+#pragma unroll 1
+        for (; done < to; ++done) {
+          // leave the sums of item `done` to the last warp
+          const int b = (done - item0) % kBuffers;
+          if (done - item0 >= kBuffers) bar_sync<kEmpty, THREADS>(b);
+          if (mine) {
+            fold();
+            Sum* s = reinterpret_cast<Sum*>(smem + lay.sums) + (b * W + warp) * (TT * kPitch);
 #pragma unroll
-          for (int mt = 0; mt < 2; ++mt)
+            for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+              for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                s[(nt * 8 + 2 * t + (i & 1)) * kPitch + mt * 16 + g + 8 * (i >> 1)] = acc[mt][nt][i];
-                acc[mt][nt][i] = 0;
-              }
-          mine = false;
+                for (int i = 0; i < 4; ++i) {
+                  s[(nt * 8 + 2 * t + (i & 1)) * kPitch + mt * 16 + g + 8 * (i >> 1)] = acc[mt][nt][i];
+                  acc[mt][nt][i] = 0;
+                }
+            mine = false;
+          }
+          bar_arrive<kFull, THREADS>(b);
         }
-        bar_arrive<kFull, THREADS>(b);
+        if (c.u >= u1) break;
+        mine = true;
+        if (I8 && !LIN && c.item != c_item) {
+          c_item = c.item;
+          const Entry en = entry(c.a);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const int row = sorted[en.first + min(nt * 8 + g, en.count - 1)];
+            inv[nt] = s_inv[GU ? row / p.topk : row];
+          }
+        }
+        cp_wait(pre - 1);
+        __syncwarp();  // every lane's copies of this unit have landed, and the unit before is read
+      } else if (DN && warm == pre) {
+        after_wait();
+        f = first;
+        to_slot = 0;
       }
-      if (c.u >= u1) break;
-      mine = true;
-      if (I8 && !LIN && c.item != c_item) {
-        c_item = c.item;
-        const Entry en = entry(c.a);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const int row = sorted[en.first + min(nt * 8 + g, en.count - 1)];
-          inv[nt] = s_inv[GU ? row / p.topk : row];
-        }
+      if (f.u < u1) {
+        target();
+        const uint32_t at = ring + to_slot * lay.stage;
+        if (!DN || warm == 0 || warm > pre) fetch_w(at);
+        if (!DN || warm <= pre) fetch_x(at);
       }
-      cp_wait(pre - 1);
-      __syncwarp();  // every lane's copies of this unit have landed, and the unit before is read
-      {
-        const uint32_t at = ring + (slot == 0 ? pre : slot - 1) * lay.stage;
-        if (f.u < u1) {
-          target();
-          fetch_w(at);
-          fetch_x(at);
-        }
-        cp_commit();
-        f.next(W, nblk, ne);
+      if (!DN || warm <= pre) cp_commit();
+      if (++to_slot == (uint32_t)lay.depth) to_slot = 0;
+      f.next(W, nblk, ne);
+      if (warm > 0) {
+        --warm;
+        continue;
       }
       const uint32_t wat = ring + slot * lay.stage + g * WB, xat = ring + slot * lay.stage + R * WB;
       if (++slot == (uint32_t)lay.depth) slot = 0;
-      uint32_t sz[NS];
+      uint32_t sz[NS];  // a scale leaves the low bits of its fp32 image free for the zero point
 #pragma unroll
-      for (int j = 0; j < NS; ++j) sz[j] = sz_next[j];
+      for (int j = 0; j < NS; ++j) sz[j] = I4 ? (uint32_t)s_next[j] << 16 | (ZP ? z_next[j] : 0u) : 0u;
       n.next(W, nblk, ne);
       if (n.u < u1) scales(n);
 
@@ -624,6 +623,8 @@ __global__ void __launch_bounds__((compute_warps(FMT) + 1) * 32, 1)
     // ---------------------------------------------------------------- sums and results: lane = row
     if (DN) {
       pdl_wait();
+      for (int i = lane; i < P; i += 32) s_wt[i] = p.weights[i];
+      __syncwarp();
       if (I8) {
         __syncthreads();
         __syncthreads();
@@ -655,103 +656,86 @@ __global__ void __launch_bounds__((compute_warps(FMT) + 1) * 32, 1)
       const Entry en = entry(c.a);
       const int b = (it - item0) % kBuffers;
       bar_sync<kFull, THREADS>(b);
-      Sum v[TT];
-#pragma unroll
-      for (int i = 0; i < TT; ++i) v[i] = 0;
-      {
-        const int a = max(u0, it * nblk), units = min(u1, (it + 1) * nblk) - a;
-        int w = (a - u0) % W;
-        const Sum* s = reinterpret_cast<const Sum*>(smem + lay.sums) + b * W * (TT * kPitch) + lane;
-        for (int i = 0; i < min(units, W); ++i) {
-#pragma unroll
-          for (int k = 0; k < TT; ++k)
-            if (k < en.count) v[k] += s[w * (TT * kPitch) + k * kPitch];
+      const int ua = max(u0, it * nblk), units = min(min(u1, (it + 1) * nblk) - ua, W), w0 = (ua - u0) % W;
+      const Sum* sums = reinterpret_cast<const Sum*>(smem + lay.sums) + b * W * (TT * kPitch) + lane;
+      auto own = [&](int k) {  // the sum of this CTA's warps
+        Sum v = 0;
+        int w = w0;
+#pragma unroll 4
+        for (int i = 0; i < units; ++i) {
+          v += sums[w * (TT * kPitch) + k * kPitch];
           if (++w == W) w = 0;
         }
-      }
-      if (it + kBuffers <= item1) bar_arrive<kEmpty, THREADS>(b);
-
+        return v;
+      };
+      // an item that is shared with other CTAs: the last of them adds the parts in the order of K
+      const bool parts = !DN && (it * nblk < u0 || (it + 1) * nblk > u1);
       bool ready = true;
-      if (!DN && (it * nblk < u0 || (it + 1) * nblk > u1)) {
-        // the item is shared with other CTAs: the last of them adds the parts in the order of K
+      if (parts) {
         float* mine = slot_of(blockIdx.x, it * nblk >= u0);
-#pragma unroll
-        for (int k = 0; k < TT; ++k)
-          if (k < en.count) __stcg(reinterpret_cast<Sum*>(mine) + k * 32, v[k]);
+#pragma unroll 1
+        for (int k = 0; k < en.count; ++k) __stcg(reinterpret_cast<Sum*>(mine) + k * 32, own(k));
         ready = last_part(it * nblk, (it + 1) * nblk);
-        if (ready) {
+      }
+      const int rows = GU ? 16 : 32, r = GU ? lane & 15 : lane, n = c.tile * rows + r;
+      const bool in = n < p.N;
+      float ws = 1.f, bias = 0.f;
+      if (I8 && in)
+        ws = reinterpret_cast<const float*>(p.scale)[LIN ? (p.lds ? n : 0)
+                                                         : en.expert * p.s_estride + (GU && lane >= 16 ? p.N : 0) + n];
+      if (LIN && in && p.bias) bias = bf16_bits_to_f32(p.bias[n]);
+#pragma unroll 1
+      for (int k = 0; k < en.count && ready; ++k) {
+        Sum v = 0;
+        if (parts) {
           const int c0 = it * nblk / share, c1 = ((it + 1) * nblk - 1) / share;
-#pragma unroll
-          for (int i = 0; i < TT; ++i) v[i] = 0;
-          for (int q = c0; q <= c1; ++q) {
-            const Sum* s = reinterpret_cast<const Sum*>(slot_of(q, q == c0));
-#pragma unroll
-            for (int k = 0; k < TT; ++k)
-              if (k < en.count) v[k] += __ldcg(s + k * 32);
+#pragma unroll 2
+          for (int q = c0; q <= c1; ++q) v += __ldcg(reinterpret_cast<const Sum*>(slot_of(q, q == c0)) + k * 32);
+        } else {
+          v = own(k);
+        }
+        float f = (float)v;
+        if constexpr (GU) {
+          const int pair = sorted[en.first + k];
+          if (I8) f = f * s_xs[pair / p.topk] * ws;
+          const float u = __shfl_down_sync(0xffffffffu, f, 16);
+          const uint16_t hb = f32_to_bf16_rn(gated_act(f, u, p.alpha, p.limit));
+          const bool store = lane < 16 && in;
+          if (store) p.h[pair * p.ldh + n] = hb;
+          if (I8) {
+            const unsigned top = __reduce_max_sync(0xffffffffu, store ? (unsigned)(hb & 0x7FFF) << 16 : 0u);
+            if (lane == 0) atomicMax(p.amax + pair, top);
+          }
+        } else if constexpr (DN) {
+          const int pair = sorted[en.first + k];
+          if (I8) f = f * s_xs[pair] * ws;
+          s_y[pair / p.topk * 32 + lane] += s_wt[pair] * f;
+        } else if (in) {
+          const int m = en.first + k;
+          f = __fmul_rn(__fmul_rn(f, p.x_scale[m]), ws);
+          const int64_t at = (int64_t)m * p.ldy + n;
+          if (p.out_type == QL_OUT_FP32) {
+            reinterpret_cast<float*>(p.y)[at] = p.bias ? f + bias : f;
+          } else if (p.out_type == QL_OUT_FP16) {
+            __half o = __float2half_rn(f);
+            if (p.bias) o = __float2half_rn(__half2float(o) + bias);
+            reinterpret_cast<__half*>(p.y)[at] = o;
+          } else {
+            uint16_t o = f32_to_bf16_rn(f);
+            if (p.bias) o = f32_to_bf16_rn(bf16_bits_to_f32(o) + bias);
+            reinterpret_cast<uint16_t*>(p.y)[at] = o;
           }
         }
       }
-      if (GU && ready) {
-        const int i = c.tile * 16 + (lane & 15);
-        const bool in = i < p.N;
-        const float ws = I8 && in ? reinterpret_cast<const float*>(p.scale)[en.expert * p.s_estride + (lane >= 16 ? p.N : 0) + i] : 1.f;
-#pragma unroll
-        for (int k = 0; k < TT; ++k)
-          if (k < en.count) {
-            const int pair = sorted[en.first + k];
-            float f = (float)v[k];
-            if (I8) f = f * s_xs[pair / p.topk] * ws;
-            const float u = __shfl_down_sync(0xffffffffu, f, 16);
-            const uint16_t hb = f32_to_bf16_rn(gated_act(f, u, p.alpha, p.limit));
-            const bool store = lane < 16 && in;
-            if (store) p.h[pair * p.ldh + i] = hb;
-            if (I8) {
-              const unsigned top = __reduce_max_sync(0xffffffffu, store ? (unsigned)(hb & 0x7FFF) << 16 : 0u);
-              if (lane == 0) atomicMax(p.amax + pair, top);
-            }
-          }
-      }
-      if (LIN && ready) {
-        const int n = c.tile * 32 + lane;
-        if (n < p.N) {
-          const float ws = reinterpret_cast<const float*>(p.scale)[p.lds ? n : 0];
-          const float bias = p.bias ? bf16_bits_to_f32(p.bias[n]) : 0.f;
-#pragma unroll
-          for (int k = 0; k < TT; ++k)
-            if (k < en.count) {
-              const int m = en.first + k;
-              const float f = __fmul_rn(__fmul_rn((float)v[k], p.x_scale[m]), ws);
-              const int64_t at = (int64_t)m * p.ldy + n;
-              if (p.out_type == QL_OUT_FP32) {
-                reinterpret_cast<float*>(p.y)[at] = p.bias ? f + bias : f;
-              } else if (p.out_type == QL_OUT_FP16) {
-                __half o = __float2half_rn(f);
-                if (p.bias) o = __float2half_rn(__half2float(o) + bias);
-                reinterpret_cast<__half*>(p.y)[at] = o;
-              } else {
-                uint16_t o = f32_to_bf16_rn(f);
-                if (p.bias) o = f32_to_bf16_rn(bf16_bits_to_f32(o) + bias);
-                reinterpret_cast<uint16_t*>(p.y)[at] = o;
-              }
-            }
-        }
-      }
+      __syncwarp();
+      if (it + kBuffers <= item1) bar_arrive<kEmpty, THREADS>(b);
       if (DN) {
-        const int n = c.tile * 32 + lane;
-        const float ws = I8 && n < p.N ? reinterpret_cast<const float*>(p.scale)[en.expert * p.s_estride + n] : 1.f;
-#pragma unroll
-        for (int k = 0; k < TT; ++k)
-          if (k < en.count) {
-            const int pair = sorted[en.first + k];
-            float f = (float)v[k];
-            if (I8) f = f * s_xs[pair] * ws;
-            s_y[pair / p.topk * 32 + lane] += s_wt[pair] * f;
-          }
         if (it == item1 || c.a == ne - 1) {
           // the end of this CTA's part of the tile
           const int a = c.tile * whole, b1 = a + whole;
-          bool write = true, parts = a < u0 || b1 > u1;
-          if (parts) {
+          bool write = true;
+          const bool shared = a < u0 || b1 > u1;
+          if (shared) {
             float* mine = slot_of(blockIdx.x, a >= u0);
             for (int m = 0; m < p.M; ++m) __stcg(mine + m * 32, s_y[m * 32 + lane]);
             write = last_part(a, b1);
@@ -761,7 +745,7 @@ __global__ void __launch_bounds__((compute_warps(FMT) + 1) * 32, 1)
             float y = s_y[m * 32 + lane];
             s_y[m * 32 + lane] = 0.f;
             if (!write) continue;
-            if (parts) {
+            if (shared) {
               y = 0.f;
               for (int q = c0; q <= c1; ++q) y += __ldcg(slot_of(q, q == c0) + m * 32);
             }
@@ -784,7 +768,7 @@ cudaError_t launch(const StreamArgs& a, cudaStream_t st) {
   Layout l = {};
   l.xt = a.M < TT ? a.M : TT;
   l.stage = R * row_bytes(FMT) + l.xt * token_bytes(FMT, MODE);
-  const int lists = P * (int)(sizeof(Entry) + 5 * 4) + (P ? a.E * 4 : 0) + (MODE == STREAM_DOWN ? a.M * 128 : 0);
+  const int lists = P * (int)(2 * sizeof(Entry) + 5 * 4) + (MODE == STREAM_DOWN ? a.M * 128 : 0);
   const int sums = kBuffers * W * TT * kPitch * 4;
   l.depth = (227 * 1024 - 256 - lists - sums) / (W * l.stage);
   if (l.depth > 6) l.depth = 6;

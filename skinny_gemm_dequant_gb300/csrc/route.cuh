@@ -76,8 +76,8 @@ __device__ __forceinline__ float bf16_from_order(uint32_t o) {
 // experts of exp(l_e - max).  The topk largest logits are chosen in decreasing order, equal
 // logits to the lower expert id; the weight of a chosen expert is its p, or with renorm
 // p / (sum of the chosen p) = its exp / (sum of the chosen exps).  Lane k < topk receives the
-// k-th choice in id and w; other lanes keep theirs.
-template <int J>
+// k-th choice in id and w; other lanes keep theirs.  kWeights false: the choice alone, w is not set.
+template <int J, bool kWeights = true>
 __device__ __forceinline__ void route_token_warp_j(const uint16_t* __restrict__ row, int E, int topk, bool renorm,
                                                    int& id, float& w) {
   const int lane = threadIdx.x & 31;
@@ -88,14 +88,17 @@ __device__ __forceinline__ void route_token_warp_j(const uint16_t* __restrict__ 
     key[j] = e < E ? (bf16_order(row[e]) << 16) | (0xFFFFu - (uint32_t)e) : 0u;
   }
   uint32_t best = 0u;
-#pragma unroll
-  for (int j = 0; j < J; ++j) best = max(best, key[j]);
-  const float mx = bf16_from_order(__reduce_max_sync(0xffffffffu, best) >> 16);
+  float mx = 0.f;
   FloatPair sum = {0.f, 0.f};
+  if constexpr (kWeights) {
 #pragma unroll
-  for (int j = 0; j < J; ++j)
-    if (key[j]) sum = pair_add(sum, expf(bf16_from_order(key[j] >> 16) - mx));
-  sum = warp_pair_sum(sum);
+    for (int j = 0; j < J; ++j) best = max(best, key[j]);
+    mx = bf16_from_order(__reduce_max_sync(0xffffffffu, best) >> 16);
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+      if (key[j]) sum = pair_add(sum, expf(bf16_from_order(key[j] >> 16) - mx));
+    sum = warp_pair_sum(sum);
+  }
   uint32_t mine = 0u;
   for (int k = 0; k < topk; ++k) {
     best = 0u;
@@ -107,24 +110,25 @@ __device__ __forceinline__ void route_token_warp_j(const uint16_t* __restrict__ 
       if (key[j] == win) key[j] = 0u;  // keys are distinct: only the owner's entry matches
     if (lane == k) mine = win;
   }
-  const float x = lane < topk ? expf(bf16_from_order(mine >> 16) - mx) : 0.f;
-  const FloatPair chosen = renorm ? warp_pair_sum(FloatPair{x, 0.f}) : sum;
-  if (lane < topk) {
-    id = (int)(0xFFFFu - (mine & 0xFFFFu));
-    w = pair_div(x, chosen);
+  if (lane < topk) id = (int)(0xFFFFu - (mine & 0xFFFFu));
+  if constexpr (kWeights) {
+    const float x = lane < topk ? expf(bf16_from_order(mine >> 16) - mx) : 0.f;
+    const FloatPair chosen = renorm ? warp_pair_sum(FloatPair{x, 0.f}) : sum;
+    if (lane < topk) w = pair_div(x, chosen);
   }
 }
 
+template <bool kWeights = true>
 __device__ __forceinline__ void route_token_warp(const uint16_t* __restrict__ row, int E, int topk, bool renorm,
                                                  int& id, float& w) {
   if (E <= 128)
-    route_token_warp_j<4>(row, E, topk, renorm, id, w);
+    route_token_warp_j<4, kWeights>(row, E, topk, renorm, id, w);
   else if (E <= 256)
-    route_token_warp_j<8>(row, E, topk, renorm, id, w);
+    route_token_warp_j<8, kWeights>(row, E, topk, renorm, id, w);
   else if (E <= 512)
-    route_token_warp_j<16>(row, E, topk, renorm, id, w);
+    route_token_warp_j<16, kWeights>(row, E, topk, renorm, id, w);
   else
-    route_token_warp_j<32>(row, E, topk, renorm, id, w);
+    route_token_warp_j<32, kWeights>(row, E, topk, renorm, id, w);
 }
 
 }  // namespace ql

@@ -39,6 +39,7 @@ struct StreamArgs {
   float alpha, limit;
   uint16_t* h;  // GATE_UP writes bf16 [M topk, ldh]
   int64_t ldh;
+  float* weights;     // GATE_UP writes [M topk], DOWN reads
   unsigned* amax;     // INT8: [M topk] bits of max|h|, zero between calls
   unsigned* tickets;  // zero between calls
   float* slots;       // sums of tiles that CTAs share
