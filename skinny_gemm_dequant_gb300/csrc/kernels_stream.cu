@@ -22,11 +22,11 @@ namespace ql {
 namespace {
 
 constexpr int R = kStreamRows;
-constexpr int kPitch = 36;  // of a column of sums: lanes (g, t) write 8 t + g, all banks once
-constexpr int kBuffers = 2;
+constexpr int MT = R / 16;
+constexpr int kPitch = R + 4;  // of a column of sums: lanes (g, t) write 8 t + g, all banks once
 constexpr int kNone = 0x7FFFFFFF;  // the expert of a pair that is left out
 
-__host__ __device__ constexpr int compute_warps(int fmt) { return fmt == STREAM_INT4 ? 12 : 8; }
+__host__ __device__ constexpr int compute_warps(int fmt) { return fmt == STREAM_INT4 ? 11 : 8; }
 __host__ __device__ constexpr int unit_k(int fmt) { return fmt == STREAM_BF16 ? 64 : 128; }
 __host__ __device__ constexpr int row_bytes(int fmt) { return fmt == STREAM_INT4 ? 64 : 128; }
 __host__ __device__ constexpr int token_bytes(int fmt, int mode) {
@@ -43,7 +43,8 @@ struct Layout {
 };
 
 struct Entry {  // one pass over an expert's weights
-  int expert, first, count;  // its pairs: sorted[first, first + count)
+  uint16_t expert, first;
+  int count;  // its pairs: s_pair[first, first + count)
 };
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) {
@@ -64,13 +65,13 @@ __device__ __forceinline__ uint32_t lds4(uint32_t a) {
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
   return v;
 }
-template <int ID0, int THREADS>
-__device__ __forceinline__ void bar_sync(int b) {
-  asm volatile("bar.sync %0, %1;" ::"r"(ID0 + b), "n"(THREADS) : "memory");
+template <int ID, int THREADS>
+__device__ __forceinline__ void bar_sync() {
+  asm volatile("bar.sync %0, %1;" ::"n"(ID), "n"(THREADS) : "memory");
 }
-template <int ID0, int THREADS>
-__device__ __forceinline__ void bar_arrive(int b) {
-  asm volatile("bar.arrive %0, %1;" ::"r"(ID0 + b), "n"(THREADS) : "memory");
+template <int ID, int THREADS>
+__device__ __forceinline__ void bar_arrive() {
+  asm volatile("bar.arrive %0, %1;" ::"n"(ID), "n"(THREADS) : "memory");
 }
 // all but the newest `left` copy groups have landed
 __device__ __forceinline__ void cp_wait(int left) {
@@ -145,21 +146,24 @@ __global__ void __launch_bounds__((compute_warps(FMT) + 1) * 32, 1)
   constexpr int TT = NT * 8, KU = unit_k(FMT), WB = row_bytes(FMT), XB = token_bytes(FMT, MODE);
   constexpr bool GU = MODE == STREAM_GATE_UP, DN = MODE == STREAM_DOWN, LIN = MODE == STREAM_LINEAR;
   constexpr bool I8 = FMT == STREAM_INT8, I4 = FMT == STREAM_INT4;
-  constexpr int kFull = 1, kEmpty = 1 + kBuffers;  // named barriers
+  constexpr int kFull = 1, kEmpty = 2;  // named barriers: sums written, sums read
+  constexpr int OUT = GU ? R / 2 : R;   // outputs of a tile: half gate rows, half up rows
   using Sum = typename std::conditional<I8, int, float>::type;
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int P = LIN ? 0 : p.M * p.topk;
 
-  // lists: entries, sorted pairs, weights and ids by pair, (INT8) factor and scale by row of x
+  // lists: entries, ids and weights by pair, (INT8) factor and scale by row of x, sorted pairs
+  Entry* heads = reinterpret_cast<Entry*>(smem);  // of passes, by place; read before the rings are filled
   Entry* entries = reinterpret_cast<Entry*>(smem + lay.lists);
-  Entry* heads = entries + P;
-  int* sorted = reinterpret_cast<int*>(heads + P);
-  float* s_wt = reinterpret_cast<float*>(sorted + P);
-  int* s_id = reinterpret_cast<int*>(s_wt + P);
-  float* s_inv = reinterpret_cast<float*>(s_id + P);
-  float* s_xs = s_inv + P;
-  float* s_y = s_xs + P;  // DOWN: [M][32]
+  int* s_id = reinterpret_cast<int*>(entries + P);
+  float* s_wt = reinterpret_cast<float*>(s_id + P);
+  float* s_inv = s_wt + (DN ? P : 0);
+  float* s_xs = s_inv + (I8 ? P : 0);
+  float* s_y = s_xs + (I8 ? P : 0);                                   // DOWN: [M][R]
+  uint16_t* s_pair = reinterpret_cast<uint16_t*>(s_y + (DN ? p.M * R : 0));  // sorted by expert
+  uint16_t* s_tok = s_pair + P;                                       // their tokens
+  const uint16_t* s_row = GU ? s_tok : s_pair;                        // their rows of x
   __shared__ int s_entries;
 
   if (!DN) {
@@ -219,9 +223,10 @@ __global__ void __launch_bounds__((compute_warps(FMT) + 1) * 32, 1)
         all += o == e;
         rank += o == e && j < i;
       }
-      sorted[before + rank] = i;
+      s_pair[before + rank] = (uint16_t)i;
+      s_tok[before + rank] = (uint16_t)(i / p.topk);
       const bool head = e != kNone && rank % TT == 0;
-      heads[before + rank] = {e, before + rank, head ? min(TT, all - rank) : 0};
+      heads[before + rank] = {(uint16_t)e, (uint16_t)(before + rank), head ? min(TT, all - rank) : 0};
     }
     __syncthreads();
     if (warp == 0) {
@@ -241,7 +246,7 @@ __global__ void __launch_bounds__((compute_warps(FMT) + 1) * 32, 1)
 
   // ------------------------------------------------------------------ this CTA's units
   const int nblk = (p.K + KU - 1) / KU;
-  const int tiles = (p.N + (GU ? 15 : 31)) / (GU ? 16 : 32);
+  const int tiles = (p.N + OUT - 1) / OUT;
   const int whole = (DN ? ne : 1) * nblk;  // units whose sums meet before the epilogue
   const int total = tiles * ne * nblk;
   // equal shares; a short item stays in one CTA, which is cheaper than joining its parts
@@ -250,8 +255,16 @@ __global__ void __launch_bounds__((compute_warps(FMT) + 1) * 32, 1)
   const int u0 = min(total, (int)blockIdx.x * share), u1 = min(total, u0 + share);
 
   auto entry = [&](int a) {
-    if constexpr (LIN) return Entry{0, a * TT, min(TT, p.M - a * TT)};
-    return entries[a];
+    struct {
+      int expert, first, count;
+    } en = {0, a * TT, p.M - a * TT};
+    if constexpr (LIN) {
+      en.count = min(TT, en.count);
+    } else {
+      const Entry q = entries[a];
+      en = {q.expert, q.first, q.count};
+    }
+    return en;
   };
   if (GU && warp == W && blockIdx.x < p.M) {
     // the weights of a token, for the next launch
@@ -286,7 +299,10 @@ __global__ void __launch_bounds__((compute_warps(FMT) + 1) * 32, 1)
     constexpr int LPT = XB / 16, TPI = 32 / LPT;   // lanes per token row, tokens per copy
     constexpr int XCOPIES = TT / TPI;
     const int cr = lane / LPR, cc = lane % LPR, tr = lane / LPT, tc = lane % LPT;
+    // piece c of row r lies in slot c ^ f(r): four pieces of two rows (LDS.128) or a word of a piece
+    // of eight rows meet every bank once
     auto swz = [](int r) { return (((r & 1) << 2) | ((r >> 1) & 3)) & (LPR - 1); };
+    const uint32_t w_dst = (uint32_t)(cr * WB + ((cc ^ swz(cr)) * 16));
     // slot of piece c of token m: the lanes of a read meet every bank once
     auto xswz = [](int c, int m) {
       if (XB == 128) return c ^ ((m & 1) << 2);
@@ -298,76 +314,82 @@ __global__ void __launch_bounds__((compute_warps(FMT) + 1) * 32, 1)
     f.set(u0 + warp, nblk, ne);
     int f_item = -1, f_valid = 0, f_toks = 0;
     const uint8_t* f_w = nullptr;
-    int64_t f_x[XCOPIES];
+    const uint8_t* f_x[XCOPIES];
     auto target = [&]() {  // addresses of the item that f is in
       if (f.item == f_item) return;
       f_item = f.item;
-      const Entry en = entry(f.a);
-      const int n0 = f.tile * (GU ? 16 : 32);
-      f_valid = p.N - n0;
+      const auto en = entry(f.a);
+      const int n0 = f.tile * OUT;
+      f_valid = p.N - n0 - cr;
       f_toks = en.count;
       f_w = p.w + en.expert * p.w_estride + (int64_t)(n0 + cr) * p.ldw + cc * 16;
 #pragma unroll
       for (int i = 0; i < XCOPIES; ++i) {
-        const int r = min(i * TPI + tr, en.count - 1);
-        int row = en.first + r;
-        if constexpr (!LIN) row = GU ? sorted[row] / p.topk : sorted[row];
-        f_x[i] = row * p.ldx + tc * 16;
+        if (i * TPI >= en.count) break;
+        const int r = en.first + min(i * TPI + tr, en.count - 1);
+        f_x[i] = p.x + (LIN ? r : s_row[r]) * p.ldx + tc * 16;
       }
     };
-    const int64_t wstep = (int64_t)RPI * p.ldw, to_up = ((int64_t)p.N - 16) * p.ldw;
+    const int64_t wstep = (int64_t)RPI * p.ldw, to_up = ((int64_t)p.N - OUT) * p.ldw;
     auto fetch_w = [&](uint32_t at) {
       const bool in = f.kb * WB + cc * 16 < (I4 ? p.K / 2 : I8 ? p.K : p.K * 2);
+      const int valid = in ? f_valid : -R;
       const uint8_t* src = f_w + (int64_t)f.kb * WB;
 #pragma unroll
       for (int i = 0; i < R / RPI; ++i) {
-        const int r = i * RPI + cr;
-        if (GU && i * RPI == 16) src += to_up;
-        cp16(at + r * WB + ((cc ^ swz(r)) * 16), src, in && (GU && i * RPI >= 16 ? r - 16 : r) < f_valid);
+        if (GU && i * RPI == OUT) src += to_up;
+        // (rows 4 apart: f differs in bit 1)
+        cp16((at + w_dst + i * RPI * WB) ^ (RPI == 4 && (i & 1) ? 32u : 0u), src, i * RPI % OUT < valid);
         src += wstep;
       }
     };
     auto fetch_x = [&](uint32_t at) {
-      const int kb = f.kb * XB + tc * 16;  // byte in the row
-      const bool in = kb < (LIN ? p.K : p.K * 2);
+      const bool in = f.kb * XB + tc * 16 < (LIN ? p.K : p.K * 2);
 #pragma unroll
       for (int i = 0; i < XCOPIES; ++i) {
+        if (i * TPI >= f_toks) break;
         const int m = i * TPI + tr;
-        if (i * TPI < f_toks && m < lay.xt) cp16(at + R * WB + m * XB + xswz(tc, m) * 16, p.x + f_x[i] + f.kb * XB, in);
+        if (m < lay.xt) cp16(at + R * WB + m * XB + xswz(tc, m) * 16, f_x[i] + f.kb * XB, in);
       }
     };
 
-    // scales of a unit: lane = row of the tile
+    // scales of a unit: a lane reads those of rows lane and lane + 32 of the tile
     constexpr int NS = I4 ? (FINE ? 4 : 1) : 1;
-    uint16_t s_next[NS];  // as loaded: turning them into numbers here would wait for them
-    uint8_t z_next[NS];
-    const uint16_t* sp = nullptr;
-    const uint8_t* zp = nullptr;
+    uint16_t s_next[2][NS];  // as loaded: turning them into numbers here would wait for them
+    uint8_t z_next[2][NS];
+    const uint16_t* sp[2];
+    const uint8_t* zp[2];
     int s_item = -1;
     auto scales = [&](const Walk& w) {
       if constexpr (I4) {
         if (w.item != s_item) {
           s_item = w.item;
-          const int e = entry(w.a).expert, n0 = w.tile * (GU ? 16 : 32);
-          const int64_t row = GU ? (int64_t)(lane >= 16 ? p.N : 0) + min(n0 + (lane & 15), p.N - 1) : min(n0 + lane, p.N - 1);
-          sp = reinterpret_cast<const uint16_t*>(p.scale) + e * p.s_estride + row * p.lds;
-          if (ZP) zp = p.zero + e * p.z_estride + row * p.ldz;
+          const int e = entry(w.a).expert, n0 = w.tile * OUT + lane;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int64_t row = GU ? (int64_t)(h ? p.N : 0) + min(n0, p.N - 1) : min(n0 + 32 * h, p.N - 1);
+            sp[h] = reinterpret_cast<const uint16_t*>(p.scale) + e * p.s_estride + row * p.lds;
+            if (ZP) zp[h] = p.zero + e * p.z_estride + row * p.ldz;
+          }
         }
 #pragma unroll
         for (int j = 0; j < NS; ++j) {
           const int k = w.kb * KU + j * 32;
           const int gi = min(k, p.K - 1) >> p.group_shift;  // past the end: any finite sum of zeros
-          s_next[j] = k < p.K ? sp[gi] : (uint16_t)0;
-          if (ZP) z_next[j] = zp[gi];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            s_next[h][j] = k < p.K ? sp[h][gi] : (uint16_t)0;
+            if (ZP) z_next[h][j] = zp[h][gi];
+          }
         }
       }
     };
 
-    Sum acc[2][NT][4];
-    float part[2][NT][4];  // INT8: sums of the last units, exact; BF16: all sums
+    Sum acc[MT][NT][4];
+    float part[MT][NT][4];  // INT8: sums of the last units, exact; BF16: all sums
     int folded = 0;
 #pragma unroll
-    for (int mt = 0; mt < 2; ++mt)
+    for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -378,7 +400,7 @@ __global__ void __launch_bounds__((compute_warps(FMT) + 1) * 32, 1)
     auto fold = [&]() {
       if constexpr (!I4) {
 #pragma unroll
-        for (int mt = 0; mt < 2; ++mt)
+        for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -440,13 +462,12 @@ __global__ void __launch_bounds__((compute_warps(FMT) + 1) * 32, 1)
 #pragma unroll 1
         for (; done < to; ++done) {
           // leave the sums of item `done` to the last warp
-          const int b = (done - item0) % kBuffers;
-          if (done - item0 >= kBuffers) bar_sync<kEmpty, THREADS>(b);
+          if (done > item0) bar_sync<kEmpty, THREADS>();
           if (mine) {
             fold();
-            Sum* s = reinterpret_cast<Sum*>(smem + lay.sums) + (b * W + warp) * (TT * kPitch);
+            Sum* s = reinterpret_cast<Sum*>(smem + lay.sums) + warp * (TT * kPitch);
 #pragma unroll
-            for (int mt = 0; mt < 2; ++mt)
+            for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -456,17 +477,16 @@ __global__ void __launch_bounds__((compute_warps(FMT) + 1) * 32, 1)
                 }
             mine = false;
           }
-          bar_arrive<kFull, THREADS>(b);
+          bar_arrive<kFull, THREADS>();
         }
         if (c.u >= u1) break;
         mine = true;
         if (I8 && !LIN && c.item != c_item) {
           c_item = c.item;
-          const Entry en = entry(c.a);
+          const auto en = entry(c.a);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            const int row = sorted[en.first + min(nt * 8 + g, en.count - 1)];
-            inv[nt] = s_inv[GU ? row / p.topk : row];
+            inv[nt] = s_inv[s_row[en.first + min(nt * 8 + g, en.count - 1)]];
           }
         }
         cp_wait(pre - 1);
@@ -491,16 +511,18 @@ __global__ void __launch_bounds__((compute_warps(FMT) + 1) * 32, 1)
       }
       const uint32_t wat = ring + slot * lay.stage + g * WB, xat = ring + slot * lay.stage + R * WB;
       if (++slot == (uint32_t)lay.depth) slot = 0;
-      uint32_t sz[NS];  // a scale leaves the low bits of its fp32 image free for the zero point
+      uint32_t sz[2][NS];  // a scale leaves the low bits of its fp32 image free for the zero point
 #pragma unroll
-      for (int j = 0; j < NS; ++j) sz[j] = I4 ? (uint32_t)s_next[j] << 16 | (ZP ? z_next[j] : 0u) : 0u;
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int j = 0; j < NS; ++j) sz[h][j] = I4 ? (uint32_t)s_next[h][j] << 16 | (ZP ? z_next[h][j] : 0u) : 0u;
       n.next(W, nblk, ne);
       if (n.u < u1) scales(n);
 
       if constexpr (I4) {
-        uint32_t wv[2][2][4];
+        uint32_t wv[MT][2][4];
 #pragma unroll
-        for (int mt = 0; mt < 2; ++mt)
+        for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const uint32_t at = wat + (mt * 16 + h * 8) * WB;
@@ -516,16 +538,16 @@ __global__ void __launch_bounds__((compute_warps(FMT) + 1) * 32, 1)
               wv[mt][h][3] = v.w;
             }
           }
-        uint32_t negz[2][2];
-        float sc[2][2], grp[2][NT][4];
+        uint32_t negz[MT][2];
+        float sc[MT][2], grp[MT][NT][4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           if (j == 0 || FINE) {
 #pragma unroll
-            for (int mt = 0; mt < 2; ++mt)
+            for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
-                const uint32_t v = __shfl_sync(0xffffffffu, sz[FINE ? j : 0], mt * 16 + h * 8 + g);
+                const uint32_t v = __shfl_sync(0xffffffffu, sz[mt / 2][FINE ? j : 0], mt % 2 * 16 + h * 8 + g);
                 sc[mt][h] = 64.f * (p.scale_fp16 ? __half2float(__ushort_as_half(v >> 16)) : __uint_as_float(v & 0xFFFF0000u));
                 // -z / 64 from z's pattern: z 2^-133 times -2^127
                 negz[mt][h] = ZP ? fma_bf16x2(__byte_perm(v, 0u, 0x4040), 0xFF00FF00u, 0u) : 0xBE00BE00u;
@@ -540,7 +562,7 @@ __global__ void __launch_bounds__((compute_warps(FMT) + 1) * 32, 1)
             bx[nt] = pair_up(lds16(xat + m * XB + xswz(FINE ? j * 4 + t : t * 4 + j, m) * 16));
           }
 #pragma unroll
-          for (int mt = 0; mt < 2; ++mt) {
+          for (int mt = 0; mt < MT; ++mt) {
             uint32_t q0[4], q1[4];
             codes_to_bf16(wv[mt][0][j], negz[mt][0], q0);
             codes_to_bf16(wv[mt][1][j], negz[mt][1], q1);
@@ -552,7 +574,7 @@ __global__ void __launch_bounds__((compute_warps(FMT) + 1) * 32, 1)
           }
           if (FINE || j == 3) {
 #pragma unroll
-            for (int mt = 0; mt < 2; ++mt)
+            for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -562,9 +584,9 @@ __global__ void __launch_bounds__((compute_warps(FMT) + 1) * 32, 1)
       } else {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          uint4 wv[2][2];
+          uint4 wv[MT][2];
 #pragma unroll
-          for (int mt = 0; mt < 2; ++mt)
+          for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
             for (int h = 0; h < 2; ++h) wv[mt][h] = lds16(wat + (mt * 16 + h * 8) * WB + ((4 * j + t) ^ swz(g)) * 16);
           if constexpr (I8) {
@@ -590,7 +612,7 @@ __global__ void __launch_bounds__((compute_warps(FMT) + 1) * 32, 1)
               }
             }
 #pragma unroll
-            for (int mt = 0; mt < 2; ++mt) {
+            for (int mt = 0; mt < MT; ++mt) {
               const uint32_t lo[4] = {wv[mt][0].x, wv[mt][0].y, wv[mt][0].z, wv[mt][0].w};
               const uint32_t hi[4] = {wv[mt][1].x, wv[mt][1].y, wv[mt][1].z, wv[mt][1].w};
 #pragma unroll
@@ -608,7 +630,7 @@ __global__ void __launch_bounds__((compute_warps(FMT) + 1) * 32, 1)
               const int m = min(nt * 8 + g, cap_t);
               const uint4 v = lds16(xat + m * XB + xswz(4 * j + t, m) * 16);
 #pragma unroll
-              for (int mt = 0; mt < 2; ++mt) {
+              for (int mt = 0; mt < MT; ++mt) {
                 mma_bf16_16816(part[mt][nt], wv[mt][0].x, wv[mt][1].x, wv[mt][0].y, wv[mt][1].y, v.x, v.y);
                 mma_bf16_16816(part[mt][nt], wv[mt][0].z, wv[mt][1].z, wv[mt][0].w, wv[mt][1].w, v.z, v.w);
               }
@@ -620,7 +642,7 @@ __global__ void __launch_bounds__((compute_warps(FMT) + 1) * 32, 1)
       c = n;
     }
   } else {
-    // ---------------------------------------------------------------- sums and results: lane = row
+    // ---------------------------------------------------------------- sums and results: rows lane, lane + 32
     if (DN) {
       pdl_wait();
       for (int i = lane; i < P; i += 32) s_wt[i] = p.weights[i];
@@ -630,7 +652,7 @@ __global__ void __launch_bounds__((compute_warps(FMT) + 1) * 32, 1)
         __syncthreads();
       }
     }
-    const int slot_floats = (DN ? p.M : TT) * 32;
+    const int slot_floats = (DN ? p.M : TT) * R;
     // 0: the part of an item that began in an earlier CTA, 1: of one that ends in a later CTA
     auto slot_of = [&](int cta, int tail) { return p.slots + ((int64_t)cta * 2 + tail) * slot_floats + lane; };
     // counts a part of the item of units [a, b) in; true for the last one, which finds all parts stored
@@ -651,106 +673,137 @@ __global__ void __launch_bounds__((compute_warps(FMT) + 1) * 32, 1)
     Walk c;
     c.set(item0 * nblk, nblk, ne);
     if (DN)
-      for (int m = 0; m < p.M; ++m) s_y[m * 32 + lane] = 0.f;
+      for (int i = lane; i < p.M * R; i += 32) s_y[i] = 0.f;
+#pragma unroll 1
     for (int it = item0; it <= item1; ++it) {
-      const Entry en = entry(c.a);
-      const int b = (it - item0) % kBuffers;
-      bar_sync<kFull, THREADS>(b);
+      const auto en = entry(c.a);
+      bar_sync<kFull, THREADS>();
       const int ua = max(u0, it * nblk), units = min(min(u1, (it + 1) * nblk) - ua, W), w0 = (ua - u0) % W;
-      const Sum* sums = reinterpret_cast<const Sum*>(smem + lay.sums) + b * W * (TT * kPitch) + lane;
-      auto own = [&](int k) {  // the sum of this CTA's warps
-        Sum v = 0;
+      const Sum* sums = reinterpret_cast<const Sum*>(smem + lay.sums) + lane;
+      auto own = [&](int k, Sum (&v)[2]) {  // the sums of this CTA's warps
+        v[0] = v[1] = 0;
         int w = w0;
 #pragma unroll 4
         for (int i = 0; i < units; ++i) {
-          v += sums[w * (TT * kPitch) + k * kPitch];
+          const Sum* s = sums + (w * TT + k) * kPitch;
+          v[0] += s[0];
+          v[1] += s[32];
           if (++w == W) w = 0;
         }
-        return v;
       };
       // an item that is shared with other CTAs: the last of them adds the parts in the order of K
       const bool parts = !DN && (it * nblk < u0 || (it + 1) * nblk > u1);
       bool ready = true;
       if (parts) {
-        float* mine = slot_of(blockIdx.x, it * nblk >= u0);
+        Sum* mine = reinterpret_cast<Sum*>(slot_of(blockIdx.x, it * nblk >= u0));
 #pragma unroll 1
-        for (int k = 0; k < en.count; ++k) __stcg(reinterpret_cast<Sum*>(mine) + k * 32, own(k));
+        for (int k = 0; k < en.count; ++k) {
+          Sum v[2];
+          own(k, v);
+          __stcg(mine + k * R, v[0]);
+          __stcg(mine + k * R + 32, v[1]);
+        }
         ready = last_part(it * nblk, (it + 1) * nblk);
       }
-      const int rows = GU ? 16 : 32, r = GU ? lane & 15 : lane, n = c.tile * rows + r;
-      const bool in = n < p.N;
-      float ws = 1.f, bias = 0.f;
-      if (I8 && in)
-        ws = reinterpret_cast<const float*>(p.scale)[LIN ? (p.lds ? n : 0)
-                                                         : en.expert * p.s_estride + (GU && lane >= 16 ? p.N : 0) + n];
-      if (LIN && in && p.bias) bias = bf16_bits_to_f32(p.bias[n]);
+      const int n = c.tile * OUT + lane;
+      float ws[2] = {1.f, 1.f}, bias[2] = {};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int row = GU ? n : n + 32 * h;
+        if (row < p.N) {
+          if (I8)
+            ws[h] = reinterpret_cast<const float*>(p.scale)[LIN ? (p.lds ? row : 0)
+                                                                : en.expert * p.s_estride + (GU && h ? p.N : 0) + row];
+          if (LIN && p.bias) bias[h] = bf16_bits_to_f32(p.bias[row]);
+        }
+      }
 #pragma unroll 1
       for (int k = 0; k < en.count && ready; ++k) {
-        Sum v = 0;
+        Sum v[2];
         if (parts) {
           const int c0 = it * nblk / share, c1 = ((it + 1) * nblk - 1) / share;
+          v[0] = v[1] = 0;
 #pragma unroll 2
-          for (int q = c0; q <= c1; ++q) v += __ldcg(reinterpret_cast<const Sum*>(slot_of(q, q == c0)) + k * 32);
+          for (int q = c0; q <= c1; ++q) {
+            const Sum* s = reinterpret_cast<const Sum*>(slot_of(q, q == c0)) + k * R;
+            v[0] += __ldcg(s);
+            v[1] += __ldcg(s + 32);
+          }
         } else {
-          v = own(k);
+          own(k, v);
         }
-        float f = (float)v;
+        float f[2] = {(float)v[0], (float)v[1]};
         if constexpr (GU) {
-          const int pair = sorted[en.first + k];
-          if (I8) f = f * s_xs[pair / p.topk] * ws;
-          const float u = __shfl_down_sync(0xffffffffu, f, 16);
-          const uint16_t hb = f32_to_bf16_rn(gated_act(f, u, p.alpha, p.limit));
-          const bool store = lane < 16 && in;
-          if (store) p.h[pair * p.ldh + n] = hb;
+          const int pair = s_pair[en.first + k];
+          if constexpr (I8) {
+            const float xs = s_xs[s_tok[en.first + k]];
+            f[0] = f[0] * xs * ws[0];
+            f[1] = f[1] * xs * ws[1];
+          }
+          const uint16_t hb = f32_to_bf16_rn(gated_act(f[0], f[1], p.alpha, p.limit));
+          if (n < p.N) p.h[pair * p.ldh + n] = hb;
           if (I8) {
-            const unsigned top = __reduce_max_sync(0xffffffffu, store ? (unsigned)(hb & 0x7FFF) << 16 : 0u);
+            const unsigned top = __reduce_max_sync(0xffffffffu, n < p.N ? (unsigned)(hb & 0x7FFF) << 16 : 0u);
             if (lane == 0) atomicMax(p.amax + pair, top);
           }
         } else if constexpr (DN) {
-          const int pair = sorted[en.first + k];
-          if (I8) f = f * s_xs[pair] * ws;
-          s_y[pair / p.topk * 32 + lane] += s_wt[pair] * f;
-        } else if (in) {
+          const int pair = s_pair[en.first + k];
+          const float wt = s_wt[pair];
+          float* y = s_y + s_tok[en.first + k] * R + lane;
+          if constexpr (I8) {
+            const float xs = s_xs[pair];
+            f[0] = f[0] * xs * ws[0];
+            f[1] = f[1] * xs * ws[1];
+          }
+          y[0] += wt * f[0];
+          y[32] += wt * f[1];
+        } else {
           const int m = en.first + k;
-          f = __fmul_rn(__fmul_rn(f, p.x_scale[m]), ws);
-          const int64_t at = (int64_t)m * p.ldy + n;
-          if (p.out_type == QL_OUT_FP32) {
-            reinterpret_cast<float*>(p.y)[at] = p.bias ? f + bias : f;
-          } else if (p.out_type == QL_OUT_FP16) {
-            __half o = __float2half_rn(f);
-            if (p.bias) o = __float2half_rn(__half2float(o) + bias);
-            reinterpret_cast<__half*>(p.y)[at] = o;
-          } else {
-            uint16_t o = f32_to_bf16_rn(f);
-            if (p.bias) o = f32_to_bf16_rn(bf16_bits_to_f32(o) + bias);
-            reinterpret_cast<uint16_t*>(p.y)[at] = o;
+          const float xs = p.x_scale[m];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (n + 32 * h >= p.N) continue;
+            const float o32 = __fmul_rn(__fmul_rn(f[h], xs), ws[h]);
+            const int64_t at = (int64_t)m * p.ldy + n + 32 * h;
+            if (p.out_type == QL_OUT_FP32) {
+              reinterpret_cast<float*>(p.y)[at] = p.bias ? o32 + bias[h] : o32;
+            } else if (p.out_type == QL_OUT_FP16) {
+              __half o = __float2half_rn(o32);
+              if (p.bias) o = __float2half_rn(__half2float(o) + bias[h]);
+              reinterpret_cast<__half*>(p.y)[at] = o;
+            } else {
+              uint16_t o = f32_to_bf16_rn(o32);
+              if (p.bias) o = f32_to_bf16_rn(bf16_bits_to_f32(o) + bias[h]);
+              reinterpret_cast<uint16_t*>(p.y)[at] = o;
+            }
           }
         }
       }
       __syncwarp();
-      if (it + kBuffers <= item1) bar_arrive<kEmpty, THREADS>(b);
-      if (DN) {
-        if (it == item1 || c.a == ne - 1) {
-          // the end of this CTA's part of the tile
-          const int a = c.tile * whole, b1 = a + whole;
-          bool write = true;
-          const bool shared = a < u0 || b1 > u1;
+      if (it < item1) bar_arrive<kEmpty, THREADS>();
+      if (DN && (it == item1 || c.a == ne - 1)) {
+        // the end of this CTA's part of the tile
+        const int a = c.tile * whole, b = a + whole;
+        const bool shared = a < u0 || b > u1;
+        bool write = true;
+        if (shared) {
+          float* mine = slot_of(blockIdx.x, a >= u0);
+          for (int i = 0; i < p.M * 2; ++i) __stcg(mine + i * 32, s_y[i * 32 + lane]);
+          write = last_part(a, b);
+        }
+        const int c0 = a / share, c1 = (b - 1) / share;
+#pragma unroll 1
+        for (int i = 0; i < p.M * 2; ++i) {
+          float y = s_y[i * 32 + lane];
+          s_y[i * 32 + lane] = 0.f;
+          if (!write) continue;
           if (shared) {
-            float* mine = slot_of(blockIdx.x, a >= u0);
-            for (int m = 0; m < p.M; ++m) __stcg(mine + m * 32, s_y[m * 32 + lane]);
-            write = last_part(a, b1);
+            y = 0.f;
+#pragma unroll 2
+            for (int q = c0; q <= c1; ++q) y += __ldcg(slot_of(q, q == c0) + i * 32);
           }
-          const int c0 = a / share, c1 = (b1 - 1) / share;
-          for (int m = 0; m < p.M; ++m) {
-            float y = s_y[m * 32 + lane];
-            s_y[m * 32 + lane] = 0.f;
-            if (!write) continue;
-            if (shared) {
-              y = 0.f;
-              for (int q = c0; q <= c1; ++q) y += __ldcg(slot_of(q, q == c0) + m * 32);
-            }
-            if (n < p.N) reinterpret_cast<uint16_t*>(p.y)[(int64_t)m * p.ldy + n] = f32_to_bf16_rn(y);
-          }
+          const int row = n + (i & 1) * 32;
+          if (row < p.N) reinterpret_cast<uint16_t*>(p.y)[(int64_t)(i >> 1) * p.ldy + row] = f32_to_bf16_rn(y);
         }
       }
       c.next(nblk, nblk, ne);
@@ -768,10 +821,12 @@ cudaError_t launch(const StreamArgs& a, cudaStream_t st) {
   Layout l = {};
   l.xt = a.M < TT ? a.M : TT;
   l.stage = R * row_bytes(FMT) + l.xt * token_bytes(FMT, MODE);
-  const int lists = P * (int)(2 * sizeof(Entry) + 5 * 4) + (MODE == STREAM_DOWN ? a.M * 128 : 0);
-  const int sums = kBuffers * W * TT * kPitch * 4;
+  const int lists = P * (int)(sizeof(Entry) + 4 + 2 * 2 + (MODE == STREAM_DOWN ? 4 : 0) + (FMT == STREAM_INT8 ? 8 : 0)) +
+                    (MODE == STREAM_DOWN ? a.M * R * 4 : 0);
+  const int sums = W * TT * kPitch * 4;
   l.depth = (227 * 1024 - 256 - lists - sums) / (W * l.stage);
   if (l.depth > 6) l.depth = 6;
+  if (l.depth < 2) return cudaErrorInvalidConfiguration;  // (2 with 64 tokens and 16 experts each)
   l.sums = W * l.depth * l.stage;
   l.lists = l.sums + sums;
   l.total = l.lists + lists;
@@ -801,7 +856,7 @@ cudaError_t launch_moe(int fmt, const StreamArgs& a, cudaStream_t st) {
 
 size_t stream_slot_bytes(int64_t M) {
   const int64_t columns = M < kStreamMaxTokens ? kStreamMaxTokens : M;
-  return (size_t)kNumSMs * 2 * columns * 32 * 4;
+  return (size_t)kNumSMs * 2 * columns * R * 4;
 }
 
 cudaError_t launch_stream(int fmt, int mode, const StreamArgs& a, cudaStream_t st) {

@@ -11,7 +11,7 @@ namespace ql {
 enum { STREAM_BF16 = 0, STREAM_INT8 = 1, STREAM_INT4 = 2 };
 enum { STREAM_GATE_UP = 0, STREAM_DOWN = 1, STREAM_LINEAR = 2 };
 
-constexpr int kStreamRows = 32;       // weight rows of a tile
+constexpr int kStreamRows = 64;       // weight rows of a tile
 constexpr int kMoeMaxTokens = 64;     // of a mixture-of-experts call
 constexpr int kMoeMaxTopk = 16;
 constexpr int kStreamMaxTokens = 32;  // of a linear call
