@@ -24,22 +24,20 @@ namespace {
 constexpr int R = kStreamRows;
 constexpr int MT = R / 16;
 constexpr int kPitch = R + 4;  // of a column of sums: lanes (g, t) write 8 t + g, all banks once
+constexpr int kBuffers = 4;  // of sums, at most
 constexpr int kNone = 0x7FFFFFFF;  // the expert of a pair that is left out
 
-__host__ __device__ constexpr int compute_warps(int fmt) { return fmt == STREAM_INT4 ? 11 : 8; }
+__host__ __device__ constexpr int compute_warps(int fmt, int nt) { return fmt == STREAM_INT4 ? 11 : nt > 1 ? 6 : 8; }
 __host__ __device__ constexpr int unit_k(int fmt) { return fmt == STREAM_BF16 ? 64 : 128; }
 __host__ __device__ constexpr int row_bytes(int fmt) { return fmt == STREAM_INT4 ? 64 : 128; }
 __host__ __device__ constexpr int token_bytes(int fmt, int mode) {
   return fmt == STREAM_BF16 || mode == STREAM_LINEAR ? 128 : 256;
 }
 
-// what a call's shared memory is cut into
+// shared memory: lists, buffers of the warps' sums, the warps' rings.  Both of the latter are cut when
+// the largest number of tokens that meet an expert's weights is known: most often it is 1 or 2 of 8
 struct Layout {
-  int xt;     // token rows of a stage
-  int stage;  // bytes
-  int depth;  // stages of a warp's ring
-  int sums, lists;  // offsets
-  int total;
+  int lists, total;  // bytes
 };
 
 struct Entry {  // one pass over an expert's weights
@@ -65,13 +63,13 @@ __device__ __forceinline__ uint32_t lds4(uint32_t a) {
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
   return v;
 }
-template <int ID, int THREADS>
-__device__ __forceinline__ void bar_sync() {
-  asm volatile("bar.sync %0, %1;" ::"n"(ID), "n"(THREADS) : "memory");
+template <int ID0, int THREADS>
+__device__ __forceinline__ void bar_sync(int b) {
+  asm volatile("bar.sync %0, %1;" ::"r"(ID0 + b), "n"(THREADS) : "memory");
 }
-template <int ID, int THREADS>
-__device__ __forceinline__ void bar_arrive() {
-  asm volatile("bar.arrive %0, %1;" ::"n"(ID), "n"(THREADS) : "memory");
+template <int ID0, int THREADS>
+__device__ __forceinline__ void bar_arrive(int b) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(ID0 + b), "n"(THREADS) : "memory");
 }
 // all but the newest `left` copy groups have landed
 __device__ __forceinline__ void cp_wait(int left) {
@@ -140,39 +138,40 @@ struct Walk {
 };
 
 template <int FMT, int MODE, int NT, bool FINE, bool ZP>
-__global__ void __launch_bounds__((compute_warps(FMT) + 1) * 32, 1)
+__global__ void __launch_bounds__((compute_warps(FMT, NT) + 1) * 32, 1)
     stream_kernel(const __grid_constant__ StreamArgs p, const __grid_constant__ Layout lay) {
-  constexpr int W = compute_warps(FMT), THREADS = (W + 1) * 32;
+  constexpr int W = compute_warps(FMT, NT), THREADS = (W + 1) * 32;
   constexpr int TT = NT * 8, KU = unit_k(FMT), WB = row_bytes(FMT), XB = token_bytes(FMT, MODE);
   constexpr bool GU = MODE == STREAM_GATE_UP, DN = MODE == STREAM_DOWN, LIN = MODE == STREAM_LINEAR;
   constexpr bool I8 = FMT == STREAM_INT8, I4 = FMT == STREAM_INT4;
-  constexpr int kFull = 1, kEmpty = 2;  // named barriers: sums written, sums read
+  constexpr int kFull = 1, kEmpty = 1 + kBuffers;  // named barriers: a buffer of sums is written, is read
   constexpr int OUT = GU ? R / 2 : R;   // outputs of a tile: half gate rows, half up rows
   using Sum = typename std::conditional<I8, int, float>::type;
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int P = LIN ? 0 : p.M * p.topk;
 
-  // lists: entries, ids and weights by pair, (INT8) factor and scale by row of x, sorted pairs
-  Entry* heads = reinterpret_cast<Entry*>(smem);  // of passes, by place; read before the rings are filled
-  Entry* entries = reinterpret_cast<Entry*>(smem + lay.lists);
+  // lists: results of the tile, entries, ids and weights by pair, (INT8) factor and scale by row of x, sorted pairs
+  float* s_y = reinterpret_cast<float*>(smem);  // DOWN: [M][R]
+  Entry* entries = reinterpret_cast<Entry*>(s_y + (DN ? p.M * R : 0));
+  Entry* heads = reinterpret_cast<Entry*>(smem + lay.lists);  // of passes, by place; read before the rings are filled
   int* s_id = reinterpret_cast<int*>(entries + P);
   float* s_wt = reinterpret_cast<float*>(s_id + P);
   float* s_inv = s_wt + (DN ? P : 0);
   float* s_xs = s_inv + (I8 ? P : 0);
-  float* s_y = s_xs + (I8 ? P : 0);                                   // DOWN: [M][R]
-  uint16_t* s_pair = reinterpret_cast<uint16_t*>(s_y + (DN ? p.M * R : 0));  // sorted by expert
-  uint16_t* s_tok = s_pair + P;                                       // their tokens
-  const uint16_t* s_row = GU ? s_tok : s_pair;                        // their rows of x
-  __shared__ int s_entries;
+  uint16_t* s_pair = reinterpret_cast<uint16_t*>(s_xs + (I8 ? P : 0));  // sorted by expert
+  uint16_t* s_tok = s_pair + P;                                         // their tokens
+  const uint16_t* s_row = GU ? s_tok : s_pair;                          // their rows of x
+  __shared__ int s_entries, s_most;
 
   if (!DN) {
     pdl_wait();
     pdl_launch_dependents();
   }
-  int ne;
+  int ne, xt;  // entries, most tokens of one
   if constexpr (LIN) {
     ne = (p.M + TT - 1) / TT;
+    xt = min(p.M, TT);
   } else {
     // ---------------------------------------------------------------- routing and dispatch
     // Every CTA chooses for itself.  DOWN does so before its wait: the launch before, GATE_UP, has
@@ -230,19 +229,29 @@ __global__ void __launch_bounds__((compute_warps(FMT) + 1) * 32, 1)
     }
     __syncthreads();
     if (warp == 0) {
-      int n = 0;
+      int n = 0, most = 1;
 #pragma unroll 1
       for (int i0 = 0; i0 < P; i0 += 32) {
-        const bool head = i0 + lane < P && heads[i0 + lane].count > 0;
+        const int count = i0 + lane < P ? heads[i0 + lane].count : 0;
+        const bool head = count > 0;
+        most = max(most, count);
         const unsigned all = __ballot_sync(0xffffffffu, head);
         if (head) entries[n + __popc(all & ((1u << lane) - 1))] = heads[i0 + lane];
         n += __popc(all);
       }
-      if (lane == 0) s_entries = n;
+      most = __reduce_max_sync(0xffffffffu, most);
+      if (lane == 0) {
+        s_entries = n;
+        s_most = most;
+      }
     }
     __syncthreads();
     ne = s_entries;
+    xt = s_most;
   }
+  const int buffer = W * xt * kPitch * 4, buffers = max(1, min(kBuffers, 24 * 1024 / buffer));
+  const int rings = (lay.lists + buffers * buffer + 127) & ~127, stage = R * WB + xt * XB;
+  const int depth = min(6, (lay.total - rings) / (W * stage));  // of a warp's ring; 2 at least, as the host made sure
 
   // ------------------------------------------------------------------ this CTA's units
   const int nblk = (p.K + KU - 1) / KU;
@@ -294,7 +303,7 @@ __global__ void __launch_bounds__((compute_warps(FMT) + 1) * 32, 1)
   if (warp < W) {
     // ---------------------------------------------------------------- streaming and products
     const int g = lane >> 2, t = lane & 3;
-    const uint32_t ring = smem_addr(smem) + (uint32_t)(warp * lay.depth * lay.stage);
+    const uint32_t ring = smem_addr(smem) + (uint32_t)(rings + warp * depth * stage);
     constexpr int LPR = WB / 16, RPI = 32 / LPR;   // lanes per weight row, rows per copy
     constexpr int LPT = XB / 16, TPI = 32 / LPT;   // lanes per token row, tokens per copy
     constexpr int XCOPIES = TT / TPI;
@@ -349,7 +358,7 @@ __global__ void __launch_bounds__((compute_warps(FMT) + 1) * 32, 1)
       for (int i = 0; i < XCOPIES; ++i) {
         if (i * TPI >= f_toks) break;
         const int m = i * TPI + tr;
-        if (m < lay.xt) cp16(at + R * WB + m * XB + xswz(tc, m) * 16, f_x[i] + f.kb * XB, in);
+        if (m < xt) cp16(at + R * WB + m * XB + xswz(tc, m) * 16, f_x[i] + f.kb * XB, in);
       }
     };
 
@@ -417,7 +426,7 @@ __global__ void __launch_bounds__((compute_warps(FMT) + 1) * 32, 1)
 
     // DOWN: weights do not depend on the launch before, activations (h) do.  So the first steps of the
     // loop below only copy: weights, then, after the wait, what meets them
-    const int pre = lay.depth - 1;
+    const int pre = depth - 1;
     int warm = DN ? 2 * pre : pre;
     const Walk first = f;
     auto after_wait = [&]() {
@@ -452,7 +461,7 @@ __global__ void __launch_bounds__((compute_warps(FMT) + 1) * 32, 1)
     bool mine = false;  // a unit of item `done` has been added
     float inv[NT] = {};
     uint32_t slot = 0;
-    const int cap_t = lay.xt - 1;
+    const int cap_t = xt - 1;
     if (c.u < u1) scales(c);
     uint32_t to_slot = 0;
 #pragma unroll 1
@@ -462,22 +471,24 @@ __global__ void __launch_bounds__((compute_warps(FMT) + 1) * 32, 1)
 #pragma unroll 1
         for (; done < to; ++done) {
           // leave the sums of item `done` to the last warp
-          if (done > item0) bar_sync<kEmpty, THREADS>();
+          const int b = (done - item0) % buffers;
+          if (done - item0 >= buffers) bar_sync<kEmpty, THREADS>(b);
           if (mine) {
             fold();
-            Sum* s = reinterpret_cast<Sum*>(smem + lay.sums) + warp * (TT * kPitch);
+            Sum* s = reinterpret_cast<Sum*>(smem + lay.lists + b * buffer) + warp * xt * kPitch;
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                  s[(nt * 8 + 2 * t + (i & 1)) * kPitch + mt * 16 + g + 8 * (i >> 1)] = acc[mt][nt][i];
+                  if (nt * 8 + 2 * t + (i & 1) < xt)
+                    s[(nt * 8 + 2 * t + (i & 1)) * kPitch + mt * 16 + g + 8 * (i >> 1)] = acc[mt][nt][i];
                   acc[mt][nt][i] = 0;
                 }
             mine = false;
           }
-          bar_arrive<kFull, THREADS>();
+          bar_arrive<kFull, THREADS>(b);
         }
         if (c.u >= u1) break;
         mine = true;
@@ -498,19 +509,19 @@ __global__ void __launch_bounds__((compute_warps(FMT) + 1) * 32, 1)
       }
       if (f.u < u1) {
         target();
-        const uint32_t at = ring + to_slot * lay.stage;
+        const uint32_t at = ring + to_slot * stage;
         if (!DN || warm == 0 || warm > pre) fetch_w(at);
         if (!DN || warm <= pre) fetch_x(at);
       }
       if (!DN || warm <= pre) cp_commit();
-      if (++to_slot == (uint32_t)lay.depth) to_slot = 0;
+      if (++to_slot == (uint32_t)depth) to_slot = 0;
       f.next(W, nblk, ne);
       if (warm > 0) {
         --warm;
         continue;
       }
-      const uint32_t wat = ring + slot * lay.stage + g * WB, xat = ring + slot * lay.stage + R * WB;
-      if (++slot == (uint32_t)lay.depth) slot = 0;
+      const uint32_t wat = ring + slot * stage + g * WB, xat = ring + slot * stage + R * WB;
+      if (++slot == (uint32_t)depth) slot = 0;
       uint32_t sz[2][NS];  // a scale leaves the low bits of its fp32 image free for the zero point
 #pragma unroll
       for (int h = 0; h < 2; ++h)
@@ -654,7 +665,7 @@ __global__ void __launch_bounds__((compute_warps(FMT) + 1) * 32, 1)
     }
     const int slot_floats = (DN ? p.M : TT) * R;
     // 0: the part of an item that began in an earlier CTA, 1: of one that ends in a later CTA
-    auto slot_of = [&](int cta, int tail) { return p.slots + ((int64_t)cta * 2 + tail) * slot_floats + lane; };
+    auto slot_of = [&](int cta, int tail) { return p.slots + ((int64_t)cta * 2 + tail) * slot_floats; };
     // counts a part of the item of units [a, b) in; true for the last one, which finds all parts stored
     auto last_part = [&](int a, int b) {
       const int c0 = a / share, c1 = (b - 1) / share;
@@ -677,15 +688,16 @@ __global__ void __launch_bounds__((compute_warps(FMT) + 1) * 32, 1)
 #pragma unroll 1
     for (int it = item0; it <= item1; ++it) {
       const auto en = entry(c.a);
-      bar_sync<kFull, THREADS>();
+      const int b = (it - item0) % buffers;
+      bar_sync<kFull, THREADS>(b);
       const int ua = max(u0, it * nblk), units = min(min(u1, (it + 1) * nblk) - ua, W), w0 = (ua - u0) % W;
-      const Sum* sums = reinterpret_cast<const Sum*>(smem + lay.sums) + lane;
+      const Sum* sums = reinterpret_cast<const Sum*>(smem + lay.lists + b * buffer) + lane;
       auto own = [&](int k, Sum (&v)[2]) {  // the sums of this CTA's warps
         v[0] = v[1] = 0;
         int w = w0;
 #pragma unroll 4
         for (int i = 0; i < units; ++i) {
-          const Sum* s = sums + (w * TT + k) * kPitch;
+          const Sum* s = sums + (w * xt + k) * kPitch;
           v[0] += s[0];
           v[1] += s[32];
           if (++w == W) w = 0;
@@ -695,7 +707,7 @@ __global__ void __launch_bounds__((compute_warps(FMT) + 1) * 32, 1)
       const bool parts = !DN && (it * nblk < u0 || (it + 1) * nblk > u1);
       bool ready = true;
       if (parts) {
-        Sum* mine = reinterpret_cast<Sum*>(slot_of(blockIdx.x, it * nblk >= u0));
+        Sum* mine = reinterpret_cast<Sum*>(slot_of(blockIdx.x, it * nblk >= u0)) + lane;
 #pragma unroll 1
         for (int k = 0; k < en.count; ++k) {
           Sum v[2];
@@ -723,9 +735,9 @@ __global__ void __launch_bounds__((compute_warps(FMT) + 1) * 32, 1)
         if (parts) {
           const int c0 = it * nblk / share, c1 = ((it + 1) * nblk - 1) / share;
           v[0] = v[1] = 0;
-#pragma unroll 2
+#pragma unroll 4
           for (int q = c0; q <= c1; ++q) {
-            const Sum* s = reinterpret_cast<const Sum*>(slot_of(q, q == c0)) + k * R;
+            const Sum* s = reinterpret_cast<const Sum*>(slot_of(q, q == c0)) + k * R + lane;
             v[0] += __ldcg(s);
             v[1] += __ldcg(s + 32);
           }
@@ -780,31 +792,45 @@ __global__ void __launch_bounds__((compute_warps(FMT) + 1) * 32, 1)
         }
       }
       __syncwarp();
-      if (it < item1) bar_arrive<kEmpty, THREADS>();
+      if (it + buffers <= item1) bar_arrive<kEmpty, THREADS>(b);
       if (DN && (it == item1 || c.a == ne - 1)) {
         // the end of this CTA's part of the tile
-        const int a = c.tile * whole, b = a + whole;
-        const bool shared = a < u0 || b > u1;
+        const int a = c.tile * whole, z = a + whole;
+        const bool shared = a < u0 || z > u1;
+        const int c0 = a / share, c1 = (z - 1) / share;
+        float4* y4 = reinterpret_cast<float4*>(s_y);
         bool write = true;
         if (shared) {
-          float* mine = slot_of(blockIdx.x, a >= u0);
-          for (int i = 0; i < p.M * 2; ++i) __stcg(mine + i * 32, s_y[i * 32 + lane]);
-          write = last_part(a, b);
+          float4* mine = reinterpret_cast<float4*>(slot_of(blockIdx.x, a >= u0));
+          __syncwarp();
+          for (int i = lane; i < p.M * (R / 4); i += 32) __stcg(mine + i, y4[i]);
+          write = last_part(a, z);
         }
-        const int c0 = a / share, c1 = (b - 1) / share;
+        if (write) {
+          // four rows of a token a lane; the parts' loads go out together
 #pragma unroll 1
-        for (int i = 0; i < p.M * 2; ++i) {
-          float y = s_y[i * 32 + lane];
-          s_y[i * 32 + lane] = 0.f;
-          if (!write) continue;
-          if (shared) {
-            y = 0.f;
-#pragma unroll 2
-            for (int q = c0; q <= c1; ++q) y += __ldcg(slot_of(q, q == c0) + i * 32);
+          for (int i = lane; i < p.M * (R / 4); i += 32) {
+            float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (shared) {
+#pragma unroll 4
+              for (int q = c0; q <= c1; ++q) {
+                const float4 v = __ldcg(reinterpret_cast<const float4*>(slot_of(q, q == c0)) + i);
+                y = make_float4(y.x + v.x, y.y + v.y, y.z + v.z, y.w + v.w);
+              }
+            } else {
+              y = y4[i];
+            }
+            const int row = c.tile * R + i % (R / 4) * 4;
+            uint16_t* dst = reinterpret_cast<uint16_t*>(p.y) + (int64_t)(i / (R / 4)) * p.ldy + row;
+            const float v[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (row + j < p.N) dst[j] = f32_to_bf16_rn(v[j]);
           }
-          const int row = n + (i & 1) * 32;
-          if (row < p.N) reinterpret_cast<uint16_t*>(p.y)[(int64_t)(i >> 1) * p.ldy + row] = f32_to_bf16_rn(y);
         }
+        __syncwarp();
+        for (int i = lane; i < p.M * (R / 4); i += 32) y4[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        __syncwarp();
       }
       c.next(nblk, nblk, ne);
     }
@@ -813,23 +839,19 @@ __global__ void __launch_bounds__((compute_warps(FMT) + 1) * 32, 1)
 
 template <int FMT, int MODE, int NT, bool FINE, bool ZP>
 cudaError_t launch(const StreamArgs& a, cudaStream_t st) {
-  constexpr int W = compute_warps(FMT), TT = NT * 8;
+  constexpr int W = compute_warps(FMT, NT), TT = NT * 8;
   auto* kfn = stream_kernel<FMT, MODE, NT, FINE, ZP>;
   static OncePerDevice once;
   if (const cudaError_t e = raise_smem_limit(kfn, once); e != cudaSuccess) return e;
   const int P = MODE == STREAM_LINEAR ? 0 : a.M * a.topk;
   Layout l = {};
-  l.xt = a.M < TT ? a.M : TT;
-  l.stage = R * row_bytes(FMT) + l.xt * token_bytes(FMT, MODE);
-  const int lists = P * (int)(sizeof(Entry) + 4 + 2 * 2 + (MODE == STREAM_DOWN ? 4 : 0) + (FMT == STREAM_INT8 ? 8 : 0)) +
-                    (MODE == STREAM_DOWN ? a.M * R * 4 : 0);
-  const int sums = W * TT * kPitch * 4;
-  l.depth = (227 * 1024 - 256 - lists - sums) / (W * l.stage);
-  if (l.depth > 6) l.depth = 6;
-  if (l.depth < 2) return cudaErrorInvalidConfiguration;  // (2 with 64 tokens and 16 experts each)
-  l.sums = W * l.depth * l.stage;
-  l.lists = l.sums + sums;
-  l.total = l.lists + lists;
+  l.lists = P * (int)(sizeof(Entry) + 4 + 2 * 2 + (MODE == STREAM_DOWN ? 4 : 0) + (FMT == STREAM_INT8 ? 8 : 0)) +
+            (MODE == STREAM_DOWN ? a.M * R * 4 : 0);
+  l.lists = (l.lists + 127) & ~127;
+  l.total = 227 * 1024 - 1024;
+  // two stages with the most tokens an entry can have (64 tokens, 16 experts each: 2.05)
+  if ((l.total - l.lists - W * TT * kPitch * 4 - 128) / (W * (R * row_bytes(FMT) + TT * token_bytes(FMT, MODE))) < 2)
+    return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(kNumSMs, 1, 1);
   cfg.blockDim = dim3((W + 1) * 32, 1, 1);
