@@ -1,0 +1,1012 @@
+// The two launches of a mixture-of-experts layer for up to 16 tokens (bf16, 8-bit and 4-bit weights).
+//
+//   GATE_UP  g = W13[e][0:I] x_m, u = W13[e][I:2I] x_m for every routed pair (m, j) with expert e,
+//            h = bf16( silu(a min(g, L)) clamp(u, -L, L) )
+//   DOWN     y_m = bf16( sum_j w_(m,j) W2[e] h_(m,j) )
+//
+// 8-bit weights: tokens (GATE_UP) and h (DOWN) are quantised here, scale = max|v| / 127 over the
+// row, code = v (127 / max|v|) rounded half to even; products of codes are exact in fp32, sums of
+// 1024 k too.  4-bit weights: no weight is rounded, a group's fp32 sum is multiplied by its scale once.
+//
+// Both kernels are persistent, one CTA per SM, and stream every chosen expert's weights once through
+// rings of the warps' own (cp.async), the weights as the warp MMA's A operand and tokens as its columns.
+// GATE_UP: all tokens stay in shared memory as MMA operands; a warp takes 8 gate rows and the 8 up rows
+// of the same outputs over the whole K, so that nothing is joined and h is made in its registers.
+// DOWN: tokens are the columns whatever expert they meet, so a warp adds experts one after the other
+// into the same registers: w_(m,j) is applied where the expert changes.  The units of a 64-row tile
+// are all its experts' K in a row; they are cut evenly over the warps of all CTAs.
+#include "common.cuh"
+#include "ffn_act.cuh"
+#include "route.cuh"
+#include "stream.h"
+#include "stream_dev.cuh"
+
+namespace ql {
+
+namespace {
+
+constexpr int kGuWarps = 16;
+constexpr int R = kStreamRows;
+constexpr int kPitch = R + 4;  // of a column of sums: lanes (g, t) write 8 t + g, all banks once
+constexpr int kSmem = 226 * 1024;
+constexpr int kMaxX = 96 * 1024;  // shared memory for the tokens of GATE_UP
+
+__host__ __device__ constexpr int dn_warps(int fmt) { return fmt == STREAM_INT4 ? 12 : 8; }
+__host__ __device__ constexpr int gu_k(int fmt) { return fmt == STREAM_INT4 ? 256 : fmt == STREAM_INT8 ? 128 : 64; }
+
+// Routing and dispatch, by every CTA for itself: pairs sorted by (expert, how often the token had it
+// before), entries of up to `most` pairs.  Scratch: P keys.
+struct Lists {
+  Entry* entries;
+  int* ids;        // by pair
+  uint16_t *pair, *tok;  // sorted
+  Entry* heads;    // scratch
+  int* keys;       // scratch
+};
+
+template <int WARPS>
+__device__ __forceinline__ void route(const StreamArgs& p, const Lists& l) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll 1
+  for (int m = warp; m < p.M; m += WARPS) {
+    int id = -1;
+    float wt;
+    if (p.logits)
+      route_token_warp<false>(p.logits + (int64_t)m * p.E, p.E, p.topk, false, id, wt);
+    else if (lane < p.topk)
+      id = p.ids[m * p.topk + lane];
+    if (id < 0 || id >= p.E) id = kNone;  // padding: not dispatched
+    if (lane < p.topk) l.ids[m * p.topk + lane] = id;
+  }
+}
+
+// after a barrier; ends with one.  Returns the number of entries, and the most pairs of one
+template <int WARPS>
+__device__ __forceinline__ int dispatch(const StreamArgs& p, const Lists& l, int per_entry, int& most_out) {
+  __shared__ int s_entries, s_most;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, P = p.M * p.topk;
+#pragma unroll 1
+  for (int i = threadIdx.x; i < P; i += WARPS * 32) {
+    int repeats = 0;
+    if (!p.logits)
+      for (int j = i - i % p.topk; j < i; ++j) repeats += l.ids[j] == l.ids[i];
+    l.keys[i] = l.ids[i] == kNone ? kNone : l.ids[i] * kMoeMaxTopk + repeats;
+  }
+  __syncthreads();
+#pragma unroll 1
+  for (int i = threadIdx.x; i < P; i += WARPS * 32) {
+    const int key = l.keys[i];
+    int before = 0, rank = 0, all = 0;
+#pragma unroll 4
+    for (int j = 0; j < P; ++j) {
+      const int o = l.keys[j];
+      before += o < key;
+      all += o == key;
+      rank += o == key && j < i;
+    }
+    l.pair[before + rank] = (uint16_t)i;
+    l.tok[before + rank] = (uint16_t)(i / p.topk);
+    const bool head = key != kNone && rank % per_entry == 0;
+    l.heads[before + rank] = {(uint16_t)l.ids[i], (uint16_t)(before + rank), head ? min(per_entry, all - rank) : 0};
+  }
+  __syncthreads();
+  if (warp == 0) {
+    int n = 0, most = 1;
+#pragma unroll 1
+    for (int i0 = 0; i0 < P; i0 += 32) {
+      const int count = i0 + lane < P ? l.heads[i0 + lane].count : 0;
+      const unsigned all = __ballot_sync(0xffffffffu, count > 0);
+      most = max(most, count);
+      if (count > 0) l.entries[n + __popc(all & ((1u << lane) - 1))] = l.heads[i0 + lane];
+      n += __popc(all);
+    }
+    most = __reduce_max_sync(0xffffffffu, most);
+    if (lane == 0) {
+      s_entries = n;
+      s_most = most;
+    }
+  }
+  __syncthreads();
+  most_out = s_most;
+  return s_entries;
+}
+
+// slot of 16-byte piece c of row m of MMA operands of BYTES a row, for the reads below
+template <int FMT, bool FINE>
+__device__ __forceinline__ int xslot(int c, int m) {
+  if (FMT == STREAM_BF16) return c ^ ((m & 1) << 2);
+  if (FMT == STREAM_INT8) return c ^ (m & 1);
+  return c ^ (FINE ? (m & 1) << 2 : (c >> 3) + ((m & 1) << 1));
+}
+__device__ __forceinline__ int wslot(int c, int r) { return c ^ (((r & 1) << 2) | ((r >> 1) & 3)); }
+
+// x of a 4-bit product: nibbles stay where they are in their half words, as bf16 numbers q 2^-133 (low
+// nibble) and q 2^-129, so activations carry 2^64 and 2^60 and a sum is 2^-69 of the true one
+constexpr uint32_t kLowScale = 0x5F805F80u, kHighScale = 0x5D805D80u;  // bf16x2 of 2^64, 2^60
+constexpr float kDown69 = 1.6940658945086007e-21f;                       // 2^-69
+constexpr float kUp69 = 590295810358705651712.f;                         // 2^69
+
+// ------------------------------------------------------------------ GATE_UP
+template <int FMT, bool FINE, bool ZP>
+__global__ void __launch_bounds__(kGuWarps * 32, 1)
+    gate_up_kernel(const __grid_constant__ StreamArgs p, int x_bytes, int lists, int depth) {
+  constexpr bool I8 = FMT == STREAM_INT8, I4 = FMT == STREAM_INT4;
+  constexpr int KS = gu_k(FMT), XB = FMT == STREAM_BF16 ? 128 : 256;  // k of a stage; bytes of a token's x block
+  constexpr int XK = FMT == STREAM_BF16 ? 64 : 128, SB = KS / XK;     // k of an x block; blocks of a stage
+  constexpr int kStage = 16 * 128;
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int P = p.M * p.topk;
+  const int nstage = (p.K + KS - 1) / KS, nxb = nstage * SB;  // x is zero past K
+
+  // shared memory: x blocks [nxb][M], 4-bit: sums of x [nxb or 4 nxb][M], lists, rings
+  uint8_t* ring_base = smem + x_bytes + lists;
+  float* s_sum = reinterpret_cast<float*>(smem + (size_t)nxb * p.M * XB);
+  Lists l;
+  l.entries = reinterpret_cast<Entry*>(smem + x_bytes);
+  l.ids = reinterpret_cast<int*>(l.entries + P);
+  float* s_xs = reinterpret_cast<float*>(l.ids + P);
+  l.pair = reinterpret_cast<uint16_t*>(s_xs + 16);
+  l.tok = l.pair + P;
+  l.heads = reinterpret_cast<Entry*>(ring_base);  // the rings are filled later
+  l.keys = reinterpret_cast<int*>(l.heads + P);
+  __shared__ unsigned s_top[16];
+
+  if (I8 && threadIdx.x < 16) s_top[threadIdx.x] = 0u;
+  pdl_wait();
+  pdl_launch_dependents();
+  if (I8) __syncthreads();
+
+  // the first warps route; the others take x meanwhile, 16 bytes a thread
+  const int routing = min(p.M, kGuWarps / 2), vecs = nxb * (XK / 8);
+  auto stage_x = [&](int first, int step) {
+    // pieces of a token are neighbours: 16 lanes hold a block of 128 k
+#pragma unroll 1
+    for (int i = first; i - lane < vecs * p.M; i += step) {
+      const bool on = i < vecs * p.M;  // (whole groups of 16 lanes)
+      const int m = on ? i / vecs : 0, v = i - m * vecs, b = v / (XK / 8), c = v % (XK / 8);
+      uint4 x = make_uint4(0u, 0u, 0u, 0u);
+      if (on && v * 8 < p.K) x = *reinterpret_cast<const uint4*>(p.x + m * p.ldx + v * 16);
+      if constexpr (I8) {
+        const float top = __uint_as_float(s_top[m]), inv = top == 0.f ? 0.f : __fdiv_rn(127.f, top);
+        x = make_uint4(quant2(x.x, inv), quant2(x.y, inv), quant2(x.z, inv), quant2(x.w, inv));
+      }
+      if constexpr (I4) {
+        const uint32_t q[4] = {x.x, x.y, x.z, x.w};
+        float s = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s += __uint_as_float(q[j] << 16) + __uint_as_float(q[j] & 0xFFFF0000u);
+        s += __shfl_xor_sync(0xffffffffu, s, 1);
+        s += __shfl_xor_sync(0xffffffffu, s, 2);
+        if constexpr (FINE) {
+          if (on && (c & 3) == 0) s_sum[(b * 4 + (c >> 2)) * p.M + m] = s * kDown69;
+        } else {
+          s += __shfl_xor_sync(0xffffffffu, s, 4);
+          s += __shfl_xor_sync(0xffffffffu, s, 8);
+          if (on && c == 0) s_sum[b * p.M + m] = s * kDown69;
+        }
+        x = pair_up(x);
+        x = make_uint4(mul_bf16x2(x.x, kLowScale), mul_bf16x2(x.y, kHighScale), mul_bf16x2(x.z, kLowScale),
+                       mul_bf16x2(x.w, kHighScale));
+      }
+      if (on) *reinterpret_cast<uint4*>(smem + (size_t)(b * p.M + m) * XB + xslot<FMT, FINE>(c, m) * 16) = x;
+    }
+  };
+  if (warp < routing) {
+    route<kGuWarps / 2>(p, l);
+  } else if constexpr (I8) {
+#pragma unroll 1
+    for (int m = 0; m < p.M; ++m) {
+      float top = 0.f;
+#pragma unroll 2
+      for (int i = threadIdx.x - routing * 32; i < p.K / 8; i += (kGuWarps - routing) * 32) {
+        const uint4 v = *reinterpret_cast<const uint4*>(p.x + m * p.ldx + i * 16);
+        const uint32_t q[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          top = max_nan(max_nan(top, fabsf(__uint_as_float(q[j] << 16))), fabsf(__uint_as_float(q[j] & 0xFFFF0000u)));
+      }
+      // as whole numbers: a NaN is above all
+      const unsigned most = __reduce_max_sync(0xffffffffu, __float_as_uint(top) & 0x7FFFFFFFu);
+      if (lane == 0) atomicMax(&s_top[m], most);
+    }
+  } else {
+    stage_x(threadIdx.x - routing * 32, (kGuWarps - routing) * 32);
+  }
+  __syncthreads();
+  if (I8) {
+    stage_x(threadIdx.x, kGuWarps * 32);
+    if (threadIdx.x < p.M) s_xs[threadIdx.x] = __fdiv_rn(__uint_as_float(s_top[threadIdx.x]), 127.f);
+  }
+  int most;
+  const int ne = dispatch<kGuWarps>(p, l, 8, most);
+
+  const int otiles = p.N / 8, total = ne * otiles;
+  const int step = (int)gridDim.x * kGuWarps;
+  const uint32_t ring = smem_addr(ring_base) + (uint32_t)(warp * depth * kStage);
+
+  // a lane copies 16-byte piece cc of rows cr and cr + 4, gate and up
+  const int cr = lane >> 3, cc = lane & 7;
+  const uint32_t dst0 = (uint32_t)(cr * 128 + wslot(cc, cr) * 16), dst1 = (uint32_t)((cr + 4) * 128 + wslot(cc, cr + 4) * 16);
+  const int64_t up = (int64_t)p.N * p.ldw, four = 4 * p.ldw;
+  const int kbytes = I4 ? p.K / 2 : I8 ? p.K : p.K * 2;
+  int f_tile = (int)blockIdx.x + warp * (int)gridDim.x, f_left = 0, f_at = 0;
+  const uint8_t* f_w = nullptr;
+  auto fetch = [&](uint32_t at) {
+    if (f_left == 0 && f_tile < total) {
+      const int a = f_tile / otiles, o = f_tile - a * otiles;
+      f_w = p.w + l.entries[a].expert * p.w_estride + (int64_t)(o * 8 + cr) * p.ldw + cc * 16;
+      f_left = nstage;
+      f_at = cc * 16;
+      f_tile += step;
+    }
+    if (f_left > 0) {
+      const bool in = f_at < kbytes;
+      cp16(at + dst0, f_w, in);
+      cp16(at + dst1, f_w + four, in);
+      cp16(at + 1024 + dst0, f_w + up, in);
+      cp16(at + 1024 + dst1, f_w + up + four, in);
+      f_w += 128;
+      f_at += 128;
+      --f_left;
+    }
+    cp_commit();
+  };
+#pragma unroll 1
+  for (int d = 0; d < depth - 1; ++d) fetch(ring + d * kStage);
+
+  if (blockIdx.x < p.M && warp == kGuWarps - 1) {
+    // the weights of a token, for the next launch (its warp's copies are under way)
+    const int m = blockIdx.x;
+    int id = 0;
+    float wt = 0.f;
+    if (p.logits)
+      route_token_warp(p.logits + (int64_t)m * p.E, p.E, p.topk, p.renorm != 0, id, wt);
+    else if (lane < p.topk)
+      wt = p.wts[m * p.topk + lane];
+    if (lane < p.topk) {
+      const int i = m * p.topk + lane;
+      p.weights[i] = wt;
+      if (p.wts_out) p.wts_out[i] = wt;
+      if (p.ids_out) p.ids_out[i] = l.ids[i] == kNone ? -1 : l.ids[i];
+    }
+  }
+
+  uint32_t slot = 0, to_slot = depth - 1;
+#pragma unroll 1
+  for (int tile = (int)blockIdx.x + warp * (int)gridDim.x; tile < total; tile += step) {
+    const int a = tile / otiles, o = tile - a * otiles;
+    const Entry en = l.entries[a];
+    const int xg = l.tok[en.first + min(g, en.count - 1)];  // the token of this lane's B column
+    const uint32_t xat = smem_addr(smem) + (uint32_t)(xg * XB);
+    // scales: 4-bit: lane (g, t) those of gate (t < 2) or up row g, of block t % 2 of a stage
+    constexpr int NS = FINE ? 4 : 1;
+    uint16_t s_next[NS];
+    uint8_t z_next[NS];
+    const uint16_t* sp = nullptr;
+    const uint8_t* zp = nullptr;
+    float ws[2] = {1.f, 1.f};
+    auto scales = [&](int s) {
+      if constexpr (I4) {
+#pragma unroll
+        for (int j = 0; j < NS; ++j) {
+          const int k = s * KS + (t & 1) * 128 + j * 32;
+          const int gi = min(k, p.K - 1) >> p.group_shift;
+          s_next[j] = k < p.K ? sp[gi] : (uint16_t)0;  // past the end: sums of zeros
+          if (ZP) z_next[j] = zp[gi];
+        }
+      }
+    };
+    {
+      const int64_t row = o * 8 + g + (I4 && t >= 2 ? (int64_t)p.N : 0);
+      if constexpr (I4) {
+        sp = reinterpret_cast<const uint16_t*>(p.scale) + en.expert * p.s_estride + row * p.lds;
+        if (ZP) zp = p.zero + en.expert * p.z_estride + row * p.ldz;
+        scales(0);
+      }
+      if constexpr (I8) {
+        const float* s = reinterpret_cast<const float*>(p.scale) + en.expert * p.s_estride + row;
+        ws[0] = s[0];
+        ws[1] = s[p.N];
+      }
+    }
+    // token columns 2t, 2t + 1 of the sums
+    const int c0 = l.tok[en.first + min(2 * t, en.count - 1)], c1 = l.tok[en.first + min(2 * t + 1, en.count - 1)];
+    float acc[4] = {};
+    int whole[4] = {};
+#pragma unroll 1
+    for (int s = 0; s < nstage; ++s) {
+      cp_wait(depth - 2);
+      __syncwarp();  // every lane's copies of this stage have landed, and the stage before is read
+      fetch(ring + to_slot * kStage);
+      if (++to_slot == (uint32_t)depth) to_slot = 0;
+      const uint32_t wat = ring + slot * kStage + g * 128;
+      if (++slot == (uint32_t)depth) slot = 0;
+      uint32_t sz[NS];
+      if constexpr (I4) {
+#pragma unroll
+        for (int j = 0; j < NS; ++j) sz[j] = (uint32_t)s_next[j] << 16 | (ZP ? z_next[j] : 0u);
+        if (s + 1 < nstage) scales(s + 1);
+      }
+#pragma unroll
+      for (int sb = 0; sb < SB; ++sb) {
+        const uint32_t xb = xat + (uint32_t)((s * SB + sb) * p.M * XB);
+        if constexpr (I4) {
+          uint32_t wv[2][4];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if constexpr (FINE) {
+              // word t of every 32-k piece, so that an MMA stays inside one group
+#pragma unroll
+              for (int j = 0; j < 4; ++j) wv[h][j] = lds4(wat + h * 1024 + wslot(4 * sb + j, g) * 16 + t * 4);
+            } else {
+              const uint4 v = lds16(wat + h * 1024 + wslot(4 * sb + t, g) * 16);
+              wv[h][0] = v.x;
+              wv[h][1] = v.y;
+              wv[h][2] = v.z;
+              wv[h][3] = v.w;
+            }
+          }
+          float grp[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint4 bx = lds16(xb + xslot<FMT, FINE>(FINE ? 4 * j + t : 4 * t + j, xg) * 16);
+            const uint32_t w0 = wv[0][j], w1 = wv[1][j], v0 = w0 >> 8, v1 = w1 >> 8;
+            if (j == 0 || FINE)
+              mma_first(grp, w0 & 0x000F000Fu, w1 & 0x000F000Fu, w0 & 0x00F000F0u, w1 & 0x00F000F0u, bx.x, bx.y);
+            else
+              mma_bf16_16816(grp, w0 & 0x000F000Fu, w1 & 0x000F000Fu, w0 & 0x00F000F0u, w1 & 0x00F000F0u, bx.x, bx.y);
+            mma_bf16_16816(grp, v0 & 0x000F000Fu, v1 & 0x000F000Fu, v0 & 0x00F000F0u, v1 & 0x00F000F0u, bx.z, bx.w);
+            if (FINE || j == 3) {
+              const float* sx = s_sum + (FINE ? (s * SB + sb) * 4 + j : s * SB + sb) * p.M;
+              const float x0 = sx[c0], x1 = sx[c1];
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const uint32_t v = __shfl_sync(0xffffffffu, sz[FINE ? j : 0], g * 4 + h * 2 + sb);
+                const float sc = p.scale_fp16 ? __half2float(__ushort_as_half(v >> 16)) : __uint_as_float(v & 0xFFFF0000u);
+                // the zero point as a number: 2^23 + z, less 2^23
+                const float z = ZP ? __uint_as_float(0x4B000000u | (v & 255u)) - 8388608.f : 8.f;
+                acc[2 * h] = fmaf(sc, fmaf(-z, x0, grp[2 * h]), acc[2 * h]);
+                acc[2 * h + 1] = fmaf(sc, fmaf(-z, x1, grp[2 * h + 1]), acc[2 * h + 1]);
+              }
+            }
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const uint4 w0 = lds16(wat + wslot(4 * j + t, g) * 16), w1 = lds16(wat + 1024 + wslot(4 * j + t, g) * 16);
+            if constexpr (I8) {
+              const uint32_t lo[4] = {w0.x, w0.y, w0.z, w0.w}, hi[4] = {w1.x, w1.y, w1.z, w1.w};
+              const uint4 xa = lds16(xb + xslot<FMT, FINE>(8 * j + 2 * t, xg) * 16);
+              const uint4 xc = lds16(xb + xslot<FMT, FINE>(8 * j + 2 * t + 1, xg) * 16);
+              const uint32_t b[8] = {xa.x, xa.y, xa.z, xa.w, xc.x, xc.y, xc.z, xc.w};
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                uint32_t a0, a1, a2, a3;
+                s8x4_to_f16x2x2(lo[i], a0, a2);
+                s8x4_to_f16x2x2(hi[i], a1, a3);
+                mma_f16_16816(acc, a0, a1, a2, a3, b[2 * i], b[2 * i + 1]);
+              }
+            } else {
+              const uint4 x = lds16(xb + xslot<FMT, FINE>(4 * j + t, xg) * 16);
+              mma_bf16_16816(acc, w0.x, w1.x, w0.y, w1.y, x.x, x.y);
+              mma_bf16_16816(acc, w0.z, w1.z, w0.w, w1.w, x.z, x.w);
+            }
+          }
+        }
+      }
+      if (I8 && ((s & 7) == 7 || s == nstage - 1)) {  // 1024 k: sums of at most 2^24
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          whole[i] += __float2int_rn(acc[i]);
+          acc[i] = 0.f;
+        }
+      }
+    }
+    // a lane holds gate (0, 1) and up (2, 3) of output g for columns 2t, 2t + 1
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const bool in = 2 * t + i < en.count;
+      float gv = acc[i], uv = acc[2 + i];
+      if constexpr (I8) {
+        const float xs = s_xs[i ? c1 : c0];
+        gv = (float)whole[i] * xs * ws[0];
+        uv = (float)whole[2 + i] * xs * ws[1];
+      }
+      if constexpr (I4) {
+        gv *= kUp69;
+        uv *= kUp69;
+      }
+      const uint16_t hb = f32_to_bf16_rn(gated_act(gv, uv, p.alpha, p.limit));
+      const int pair = l.pair[en.first + min(2 * t + i, en.count - 1)];
+      if (in) p.h[pair * p.ldh + o * 8 + g] = hb;
+      if constexpr (I8) {
+        unsigned top = (unsigned)(hb & 0x7FFF) << 16;
+#pragma unroll
+        for (int q = 4; q < 32; q <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, q));
+        if (in && g == 0) atomicMax(p.amax + pair, top);
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------ DOWN
+// NT: token columns / 8
+template <int FMT, int NT, bool FINE, bool ZP>
+__global__ void __launch_bounds__(dn_warps(FMT) * 32, 1)
+    down_kernel(const __grid_constant__ StreamArgs p, int lists) {
+  constexpr bool I8 = FMT == STREAM_INT8, I4 = FMT == STREAM_INT4;
+  constexpr int W = dn_warps(FMT), THREADS = W * 32, MT = R / 16;
+  constexpr int KU = FMT == STREAM_BF16 ? 64 : 128, WB = I4 ? 64 : 128, XB = FMT == STREAM_BF16 ? 128 : 256;
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int P = p.M * p.topk;
+
+  // shared memory: sums that a warp leaves of the tile it begins in [W][M][kPitch], lists, rings
+  float* s_head = reinterpret_cast<float*>(smem);
+  Lists l;
+  l.entries = reinterpret_cast<Entry*>(s_head + W * p.M * kPitch);
+  l.ids = reinterpret_cast<int*>(l.entries + P);
+  float* s_wt = reinterpret_cast<float*>(l.ids + P);  // by pair; 8-bit: times the scale of h
+  float* s_inv = s_wt + P;
+  l.pair = reinterpret_cast<uint16_t*>(s_inv + P);
+  l.tok = l.pair + P;
+  uint8_t* rings = smem + lists;
+  l.heads = reinterpret_cast<Entry*>(rings);
+  l.keys = reinterpret_cast<int*>(l.heads + P);
+  __shared__ int s_last;
+
+  // this runs before the wait: the launch before, GATE_UP, has waited for what wrote the logits
+  route<W>(p, l);
+  __syncthreads();
+  int xt;
+  const int ne = dispatch<W>(p, l, 16, xt);
+
+  const int nblk = (p.K + KU - 1) / KU, tiles = (p.N + R - 1) / R, whole = ne * nblk, total = tiles * whole;
+  if (total == 0) {  // nothing was dispatched
+    pdl_wait();
+    for (int i = blockIdx.x * THREADS + threadIdx.x; i < p.M * p.N; i += gridDim.x * THREADS)
+      reinterpret_cast<uint16_t*>(p.y)[(int64_t)(i / p.N) * p.ldy + i % p.N] = 0;
+    return;
+  }
+  // equal shares; a short tile stays in one CTA, which is cheaper than joining its parts
+  int share = (total + gridDim.x - 1) / gridDim.x;
+  if (share < whole && whole <= 2 * W) share = whole;
+  const int u0 = min(total, (int)blockIdx.x * share), u1 = min(total, u0 + share);
+  auto bound = [&](int w) { return u0 + (u1 - u0) * w / W; };  // (at most 2^26 units a CTA)
+  const int v0 = bound(warp), v1 = bound(warp + 1);
+  const int stage = R * WB + xt * XB, depth = min(6, (kSmem - lists) / (W * stage));
+  const uint32_t ring = smem_addr(rings) + (uint32_t)(warp * depth * stage);
+
+  constexpr int LPR = WB / 16, RPI = 32 / LPR;  // lanes per weight row, rows per copy
+  constexpr int LPT = XB / 16, TPI = 32 / LPT;  // lanes per token row, tokens per copy
+  const int cr = lane / LPR, cc = lane % LPR, tr = lane / LPT, tc = lane % LPT;
+  auto swz = [](int c, int r) { return c ^ ((((r & 1) << 2) | ((r >> 1) & 3)) & (LPR - 1)); };
+  const uint32_t w_dst = (uint32_t)(cr * WB + swz(cc, cr) * 16);
+
+  struct At {  // a unit: its number, block of K, entry, tile
+    int u, kb, a, tile;
+  };
+  auto set = [&](int u) {
+    At w;
+    w.u = u;
+    w.tile = u / whole;
+    const int r = u - w.tile * whole;
+    w.a = r / nblk;
+    w.kb = r - w.a * nblk;
+    return w;
+  };
+  auto next = [&](At& w) {
+    ++w.u;
+    if (++w.kb == nblk) {
+      w.kb = 0;
+      if (++w.a == ne) {
+        w.a = 0;
+        ++w.tile;
+      }
+    }
+  };
+
+  At f = set(v0);
+  bool f_new = true;
+  int f_valid = 0, f_toks = 0, f_first = 0;
+  const uint8_t* f_w = nullptr;
+  const int64_t wstep = (int64_t)RPI * p.ldw;
+  auto target = [&]() {
+    const Entry en = l.entries[f.a];
+    f_valid = p.N - f.tile * R - cr;
+    f_toks = en.count;
+    f_first = en.first;
+    f_w = p.w + en.expert * p.w_estride + (int64_t)(f.tile * R + cr) * p.ldw + cc * 16;
+  };
+  auto fetch_w = [&](uint32_t at) {
+    const int k = f.kb * WB + cc * 16;
+    const int valid = k < (I4 ? p.K / 2 : I8 ? p.K : p.K * 2) ? f_valid : -R;
+    const uint8_t* src = f_w + (int64_t)f.kb * WB;
+#pragma unroll
+    for (int i = 0; i < R / RPI; ++i) {
+      // (rows 4 apart: the slot differs in bit 1)
+      cp16((at + w_dst + i * RPI * WB) ^ (RPI == 4 && (i & 1) ? 32u : 0u), src, i * RPI < valid);
+      src += wstep;
+    }
+  };
+  auto fetch_x = [&](uint32_t at) {
+    const int k = f.kb * XB + tc * 16;
+#pragma unroll 1
+    for (int m = tr; m < f_toks; m += TPI)
+      cp16(at + R * WB + m * XB + xslot<FMT, FINE>(tc, m) * 16, p.x + l.pair[f_first + m] * p.ldx + k, k < p.K * 2);
+  };
+
+  // scales of a unit (4-bit) or of an entry (8-bit): a lane reads those of rows lane and lane + 32
+  constexpr int NS = FINE ? 4 : 1;
+  uint16_t s_next[2][NS];
+  uint8_t z_next[2][NS];
+  const uint16_t* sp[2] = {};
+  const uint8_t* zp[2] = {};
+  auto scale_rows = [&](const At& w) {
+    if constexpr (I4) {
+      const int e = l.entries[w.a].expert;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int64_t row = min(w.tile * R + lane + 32 * h, p.N - 1);
+        sp[h] = reinterpret_cast<const uint16_t*>(p.scale) + e * p.s_estride + row * p.lds;
+        if (ZP) zp[h] = p.zero + e * p.z_estride + row * p.ldz;
+      }
+    }
+  };
+  auto scales = [&](int kb) {
+    if constexpr (I4) {
+#pragma unroll
+      for (int j = 0; j < NS; ++j) {
+        const int k = kb * KU + j * 32;
+        const int gi = min(k, p.K - 1) >> p.group_shift;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          s_next[h][j] = k < p.K ? sp[h][gi] : (uint16_t)0;  // past the end: sums of zeros
+          if (ZP) z_next[h][j] = zp[h][gi];
+        }
+      }
+    }
+  };
+
+  float y[MT][NT][4], part[MT][NT][4];
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) y[mt][nt][i] = part[mt][nt][i] = 0.f;
+
+  // The first steps only copy: weights, which do not depend on the launch before, then, after the wait,
+  // the rows of h that meet them
+  const int pre = depth - 1;
+  {
+    const At first = f;
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass) {
+      if (pass) {
+        pdl_wait();
+        pdl_launch_dependents();
+      }
+      f = first;
+#pragma unroll 1
+      for (int d = 0; d < pre; ++d) {
+        if (f.u < v1) {
+          target();
+          if (pass)
+            fetch_x(ring + d * stage);
+          else
+            fetch_w(ring + d * stage);
+        }
+        if (pass) cp_commit();
+        next(f);
+      }
+    }
+    f_new = true;
+  }
+#pragma unroll 1
+  for (int i = threadIdx.x; i < P; i += THREADS) {
+    float wt = p.weights[i];
+    if constexpr (I8) {
+      const float top = __uint_as_float(__ldcg(p.amax + i));
+      wt *= __fdiv_rn(top, 127.f);
+      s_inv[i] = top == 0.f ? 0.f : __fdiv_rn(127.f, top);
+    }
+    s_wt[i] = wt;
+  }
+  __syncthreads();
+  if constexpr (I8) {
+    // every CTA has read the maxima once all have counted in: they are zero for the next call
+    if (threadIdx.x == 0) {
+      __threadfence();
+      s_last = atomicAdd(p.tickets + gridDim.x, 1u) == gridDim.x - 1;
+    }
+    __syncthreads();
+    if (s_last) {
+      for (int i = threadIdx.x; i < P; i += THREADS) p.amax[i] = 0u;
+      if (threadIdx.x == 0) p.tickets[gridDim.x] = 0u;
+    }
+  }
+
+  At c = set(v0);
+  int first_u = v0;  // of the tile's units that this warp has added
+  uint32_t slot = 0, to_slot = pre;
+  // what the entry's tokens are to this lane: its B columns' rows of x and factors; its sums' weights
+  int row[NT];
+  float inv[NT], wc[NT][2];
+  bool here[NT][2], any[NT];
+  float ws[2] = {1.f, 1.f};
+  auto enter = [&]() {
+    const Entry en = l.entries[c.a];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      row[nt] = 0;
+      here[nt][0] = here[nt][1] = any[nt] = false;
+      wc[nt][0] = wc[nt][1] = inv[nt] = 0.f;
+    }
+#pragma unroll 1
+    for (int i = 0; i < en.count; ++i) {
+      const int m = l.tok[en.first + i], pair = l.pair[en.first + i];
+      const float wt = s_wt[pair];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        if (m == nt * 8 + g) {
+          row[nt] = i;
+          if (I8) inv[nt] = s_inv[pair];
+        }
+        any[nt] = any[nt] || (m >> 3) == nt;
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+          if (m == nt * 8 + 2 * t + q) {
+            here[nt][q] = true;
+            wc[nt][q] = wt;
+          }
+      }
+    }
+    if constexpr (I8) {
+      const float* s = reinterpret_cast<const float*>(p.scale) + en.expert * p.s_estride + c.tile * R + lane;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) ws[h] = c.tile * R + lane + 32 * h < p.N ? s[32 * h] : 0.f;
+    }
+  };
+  // an entry's sums, times the token's weight, into the tile's
+  auto fold = [&]() {
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float s = I8 ? __shfl_sync(0xffffffffu, ws[mt / 2], mt % 2 * 16 + h * 8 + g) : I4 ? 64.f : 1.f;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            float& d = part[mt][nt][2 * h + q];
+            if (here[nt][q]) y[mt][nt][2 * h + q] = fmaf(wc[nt][q], s * d, y[mt][nt][2 * h + q]);
+            d = 0.f;
+          }
+      }
+  };
+  auto leave = [&](float* to) {  // [M][kPitch]
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int m = nt * 8 + 2 * t + (i & 1);
+          if (m < p.M) to[m * kPitch + mt * 16 + g + 8 * (i >> 1)] = y[mt][nt][i];
+          y[mt][nt][i] = 0.f;
+        }
+  };
+  // the end of this warp's part [first_u, end) of a tile
+  auto finish = [&](int tile, int end) {
+    if (first_u > tile * whole) {
+      leave(s_head + warp * p.M * kPitch);
+    } else if (end == (tile + 1) * whole) {  // all of it
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int m = nt * 8 + 2 * t + (i & 1), n = tile * R + mt * 16 + g + 8 * (i >> 1);
+            if (m < p.M && n < p.N)
+              reinterpret_cast<uint16_t*>(p.y)[(int64_t)m * p.ldy + n] = f32_to_bf16_rn(y[mt][nt][i]);
+            y[mt][nt][i] = 0.f;
+          }
+    } else {  // the last of this warp's units: its ring is free
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+      __syncwarp();
+      leave(reinterpret_cast<float*>(rings + (size_t)warp * depth * stage));
+    }
+  };
+
+  int folded = 0;
+  if (c.u < v1) {
+    enter();
+    scale_rows(c);
+    scales(c.kb);
+  }
+#pragma unroll 1
+  while (c.u < v1) {
+    cp_wait(pre - 1);
+    __syncwarp();  // every lane's copies of this unit have landed, and the unit before is read
+    if (f.u < v1) {
+      if (f_new || f.kb == 0) target();
+      f_new = false;
+      fetch_w(ring + to_slot * stage);
+      fetch_x(ring + to_slot * stage);
+    }
+    cp_commit();
+    next(f);
+    if (++to_slot == (uint32_t)depth) to_slot = 0;
+    const uint32_t wat = ring + slot * stage + g * WB, xat = ring + slot * stage + R * WB;
+    if (++slot == (uint32_t)depth) slot = 0;
+    uint32_t sz[2][NS];  // a scale leaves the low bits of its fp32 image free for the zero point
+    At n = c;
+    next(n);
+    if constexpr (I4) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int j = 0; j < NS; ++j) sz[h][j] = (uint32_t)s_next[h][j] << 16 | (ZP ? z_next[h][j] : 0u);
+      if (n.u < v1) {
+        if (n.kb == 0) scale_rows(n);
+        scales(n.kb);
+      }
+    }
+
+    if constexpr (I4) {
+      uint4 bx[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+        if (NT == 1 || any[nt]) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            bx[nt][j] = pair_up(lds16(xat + row[nt] * XB + xslot<FMT, FINE>(FINE ? j * 4 + t : t * 4 + j, row[nt]) * 16));
+        }
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        // rows g, g + 8 of the row tile
+        uint32_t wv[2][4], negz[2];
+        float sc[2], grp[NT][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t at = wat + (mt * 16 + h * 8) * WB;
+          if constexpr (FINE) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) wv[h][j] = lds4(at + swz(j, g) * 16 + t * 4);
+          } else {
+            const uint4 v = lds16(at + swz(t, g) * 16);
+            wv[h][0] = v.x;
+            wv[h][1] = v.y;
+            wv[h][2] = v.z;
+            wv[h][3] = v.w;
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (j == 0 || FINE) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t v = __shfl_sync(0xffffffffu, sz[mt / 2][FINE ? j : 0], mt % 2 * 16 + h * 8 + g);
+              sc[h] = p.scale_fp16 ? __half2float(__ushort_as_half(v >> 16)) : __uint_as_float(v & 0xFFFF0000u);
+              // -z / 64 from z's pattern: z 2^-133 times -2^127
+              negz[h] = ZP ? fma_bf16x2(__byte_perm(v, 0u, 0x4040), 0xFF00FF00u, 0u) : 0xBE00BE00u;
+            }
+          }
+          uint32_t q0[4], q1[4];
+          codes_to_bf16(wv[0][j], negz[0], q0);
+          codes_to_bf16(wv[1][j], negz[1], q1);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            if (NT == 1 || any[nt]) {
+              if (j == 0 || FINE)
+                mma_first(grp[nt], q0[0], q1[0], q0[1], q1[1], bx[nt][j].x, bx[nt][j].y);
+              else
+                mma_bf16_16816(grp[nt], q0[0], q1[0], q0[1], q1[1], bx[nt][j].x, bx[nt][j].y);
+              mma_bf16_16816(grp[nt], q0[2], q1[2], q0[3], q1[3], bx[nt][j].z, bx[nt][j].w);
+              if (FINE || j == 3) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) part[mt][nt][i] = fmaf(sc[i >> 1], grp[nt][i], part[mt][nt][i]);
+              }
+            }
+        }
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        uint32_t b[NT][8];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          if (NT == 1 || any[nt]) {
+            if constexpr (I8) {
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const uint4 v = lds16(xat + row[nt] * XB + xslot<FMT, FINE>(8 * j + 2 * t + i, row[nt]) * 16);
+                b[nt][4 * i] = quant2(v.x, inv[nt]);
+                b[nt][4 * i + 1] = quant2(v.y, inv[nt]);
+                b[nt][4 * i + 2] = quant2(v.z, inv[nt]);
+                b[nt][4 * i + 3] = quant2(v.w, inv[nt]);
+              }
+            } else {
+              const uint4 v = lds16(xat + row[nt] * XB + xslot<FMT, FINE>(4 * j + t, row[nt]) * 16);
+              b[nt][0] = v.x;
+              b[nt][1] = v.y;
+              b[nt][2] = v.z;
+              b[nt][3] = v.w;
+            }
+          }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          const uint4 w0 = lds16(wat + (mt * 16) * WB + swz(4 * j + t, g) * 16);
+          const uint4 w1 = lds16(wat + (mt * 16 + 8) * WB + swz(4 * j + t, g) * 16);
+          if constexpr (I8) {
+            const uint32_t lo[4] = {w0.x, w0.y, w0.z, w0.w}, hi[4] = {w1.x, w1.y, w1.z, w1.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t a0, a1, a2, a3;
+              s8x4_to_f16x2x2(lo[i], a0, a2);
+              s8x4_to_f16x2x2(hi[i], a1, a3);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                if (NT == 1 || any[nt]) mma_f16_16816(part[mt][nt], a0, a1, a2, a3, b[nt][2 * i], b[nt][2 * i + 1]);
+            }
+          } else {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              if (NT == 1 || any[nt]) {
+                mma_bf16_16816(part[mt][nt], w0.x, w1.x, w0.y, w1.y, b[nt][0], b[nt][1]);
+                mma_bf16_16816(part[mt][nt], w0.z, w1.z, w0.w, w1.w, b[nt][2], b[nt][3]);
+              }
+          }
+        }
+      }
+    }
+    const bool last = n.u == v1;
+    if (last || n.kb == 0 || (I8 && ++folded == 8)) {  // 8-bit: at most 1024 k, sums of at most 2^24
+      fold();
+      folded = 0;
+      if (last || (n.kb == 0 && n.a == 0)) {
+        finish(c.tile, n.u);
+        first_u = n.u;
+      }
+      c = n;
+      if (!last && n.kb == 0) enter();
+    }
+    c = n;
+  }
+  __syncthreads();
+
+  // ---------------------------------------------------------------- tiles that warps or CTAs share
+  const int slot_floats = p.M * R;
+  // 0: the part of a tile that began in an earlier CTA, 1: of one that ends in a later CTA
+  auto slot_of = [&](int cta, int tail) { return p.slots + ((int64_t)cta * 2 + tail) * slot_floats; };
+  if (u0 >= u1) return;
+#pragma unroll 1
+  for (int tile = u0 / whole; tile <= (u1 - 1) / whole; ++tile) {
+    const int s = tile * whole, e = s + whole, a = max(s, u0), b = min(e, u1);
+    // the warps that hold parts of it
+    int lo = 0, hi = W - 1;
+    while (bound(lo + 1) <= a) ++lo;
+    while (bound(hi) >= b) --hi;
+    if (lo == hi && a == s && b == e) continue;  // written
+    const bool shared = a > s || b < e;
+    const int c0 = s / share, c1 = (e - 1) / share;
+    float* mine = slot_of(blockIdx.x, a == s);
+    auto put = [&](int i, float v) {
+      const int n = tile * R + i % R;
+      if (n < p.N) reinterpret_cast<uint16_t*>(p.y)[(int64_t)(i / R) * p.ldy + n] = f32_to_bf16_rn(v);
+    };
+#pragma unroll 1
+    for (int i = threadIdx.x; i < p.M * R; i += THREADS) {
+      float v = 0.f;
+#pragma unroll 1
+      for (int w = lo; w <= hi; ++w) {
+        if (bound(w) == bound(w + 1)) continue;
+        const float* from = bound(w) > s ? s_head + w * p.M * kPitch
+                                         : reinterpret_cast<const float*>(rings + (size_t)w * depth * stage);
+        v += from[i / R * kPitch + i % R];
+      }
+      if (shared)
+        __stcg(mine + i, v);
+      else
+        put(i, v);
+    }
+    if (!shared) continue;
+    // the last of the CTAs that share it adds the parts in the order of K
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      s_last = atomicAdd(p.tickets + c0, 1u) == (unsigned)(c1 - c0);
+      if (s_last) p.tickets[c0] = 0u;
+    }
+    __syncthreads();
+    if (s_last) {
+      __threadfence();
+#pragma unroll 1
+      for (int i = threadIdx.x; i < p.M * R; i += THREADS) {
+        float v = 0.f;
+#pragma unroll 4
+        for (int q = c0; q <= c1; ++q) v += __ldcg(slot_of(q, q == c0) + i);
+        put(i, v);
+      }
+    }
+    __syncthreads();  // s_last is read
+  }
+}
+
+template <int FMT, bool FINE, bool ZP>
+cudaError_t launch_gu(const StreamArgs& a, int x_bytes, cudaStream_t st) {
+  auto* kfn = gate_up_kernel<FMT, FINE, ZP>;
+  static OncePerDevice once;
+  if (const cudaError_t e = raise_smem_limit(kfn, once); e != cudaSuccess) return e;
+  const int P = a.M * a.topk;
+  const int lists = (P * (int)(sizeof(Entry) + 4 + 4) + 64 + 127) & ~127;
+  int depth = (kSmem - x_bytes - lists) / (kGuWarps * 2048);
+  if (depth > 6) depth = 6;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kNumSMs, 1, 1);
+  cfg.blockDim = dim3(kGuWarps * 32, 1, 1);
+  cfg.dynamicSmemBytes = (size_t)(x_bytes + lists + depth * kGuWarps * 2048);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kfn, a, x_bytes, lists, depth);
+}
+
+template <int FMT, int NT, bool FINE, bool ZP>
+cudaError_t launch_dn(const StreamArgs& a, cudaStream_t st) {
+  auto* kfn = down_kernel<FMT, NT, FINE, ZP>;
+  static OncePerDevice once;
+  if (const cudaError_t e = raise_smem_limit(kfn, once); e != cudaSuccess) return e;
+  const int P = a.M * a.topk;
+  const int lists = (dn_warps(FMT) * a.M * kPitch * 4 + P * (int)(sizeof(Entry) + 3 * 4 + 4) + 127) & ~127;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kNumSMs, 1, 1);
+  cfg.blockDim = dim3(dn_warps(FMT) * 32, 1, 1);
+  cfg.dynamicSmemBytes = (size_t)kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kfn, a, lists);
+}
+
+// bytes of GATE_UP's tokens in shared memory
+int64_t gu_x_bytes(int fmt, const StreamArgs& a) {
+  const int64_t ks = gu_k(fmt), stages = (a.K + ks - 1) / ks;
+  int64_t b = stages * ks * 2 * a.M;
+  if (fmt == STREAM_INT4) b += stages * 2 * (a.group_shift < 7 ? 4 : 1) * a.M * 4;
+  return (b + 127) & ~int64_t(127);
+}
+
+}  // namespace
+
+bool moe_few_takes(int fmt, int mode, const StreamArgs& a) {
+  if (a.M > 8) return false;
+  if (mode == STREAM_GATE_UP) return gu_x_bytes(fmt, a) <= kMaxX;
+  return true;
+}
+
+cudaError_t launch_moe_few(int fmt, int mode, const StreamArgs& a, cudaStream_t st) {
+  const bool fine = a.group_shift < 7;
+  if (mode == STREAM_GATE_UP) {
+    const int x = (int)gu_x_bytes(fmt, a);
+    if (fmt == STREAM_BF16) return launch_gu<STREAM_BF16, false, false>(a, x, st);
+    if (fmt == STREAM_INT8) return launch_gu<STREAM_INT8, false, false>(a, x, st);
+    if (fine) return a.zero ? launch_gu<STREAM_INT4, true, true>(a, x, st) : launch_gu<STREAM_INT4, true, false>(a, x, st);
+    return a.zero ? launch_gu<STREAM_INT4, false, true>(a, x, st) : launch_gu<STREAM_INT4, false, false>(a, x, st);
+  }
+  if (fmt == STREAM_BF16) return launch_dn<STREAM_BF16, 1, false, false>(a, st);
+  if (fmt == STREAM_INT8) return launch_dn<STREAM_INT8, 1, false, false>(a, st);
+  if (fine) return a.zero ? launch_dn<STREAM_INT4, 1, true, true>(a, st) : launch_dn<STREAM_INT4, 1, true, false>(a, st);
+  return a.zero ? launch_dn<STREAM_INT4, 1, false, true>(a, st) : launch_dn<STREAM_INT4, 1, false, false>(a, st);
+}
+
+}  // namespace ql

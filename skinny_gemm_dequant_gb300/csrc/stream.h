@@ -52,6 +52,9 @@ struct StreamArgs {
 };
 
 cudaError_t launch_stream(int fmt, int mode, const StreamArgs& a, cudaStream_t st);
+// the launches for up to 8 tokens (kernels_moe_few.cu), where they take the call
+bool moe_few_takes(int fmt, int mode, const StreamArgs& a);
+cudaError_t launch_moe_few(int fmt, int mode, const StreamArgs& a, cudaStream_t st);
 size_t stream_slot_bytes(int64_t M);
 // of QL_OP_INT8_CODES and QL_OP_MOE_FEW (api_stream.cu)
 size_t stream_workspace_bytes(int op, int64_t M, int64_t N, int64_t K, int E, int topk);

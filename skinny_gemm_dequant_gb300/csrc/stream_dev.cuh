@@ -1,0 +1,89 @@
+// Device helpers of the weight-streaming kernels (kernels_stream.cu, kernels_moe_few.cu): copies into a
+// warp's ring, weights and activations to MMA operands.
+#pragma once
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+
+namespace ql {
+
+constexpr int kNone = 0x7FFFFFFF;  // the expert of a pair that is left out
+
+struct Entry {  // one pass over an expert's weights
+  uint16_t expert, first;
+  int count;  // its pairs: s_pair[first, first + count)
+};
+
+__device__ __forceinline__ uint32_t smem_addr(const void* p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+// 16 bytes to shared memory; zeros, and no access to src, where `take` is false
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool take) {
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(take ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds4(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+// all but the newest `left` copy groups have landed
+__device__ __forceinline__ void cp_wait(int left) {
+  switch (left) {
+    case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
+    case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+    case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+    case 3: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+    case 4: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
+    default: asm volatile("cp.async.wait_group 5;" ::: "memory"); break;
+  }
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+// bf16 patterns below 256 are linear (pattern p stands for p 2^-133), so a nibble in place is a
+// number: one multiply-add gives (q - z) / 64, exactly
+__device__ __forceinline__ void codes_to_bf16(uint32_t w, uint32_t negz, uint32_t (&o)[4]) {
+  const uint32_t v = w >> 8;
+  o[0] = fma_bf16x2(w & 0x000F000Fu, 0x7F007F00u, negz);
+  o[1] = fma_bf16x2(w & 0x00F000F0u, 0x7D007D00u, negz);
+  o[2] = fma_bf16x2(v & 0x000F000Fu, 0x7F007F00u, negz);
+  o[3] = fma_bf16x2(v & 0x00F000F0u, 0x7D007D00u, negz);
+}
+// eight activations in the order in which a word's codes come out: (0,4) (1,5) (2,6) (3,7)
+__device__ __forceinline__ uint4 pair_up(uint4 x) {
+  return make_uint4(__byte_perm(x.x, x.z, 0x5410), __byte_perm(x.x, x.z, 0x7632), __byte_perm(x.y, x.w, 0x5410),
+                    __byte_perm(x.y, x.w, 0x7632));
+}
+// two bf16 values as whole f16 numbers: v inv + 1536 rounded to a whole number by the conversion
+// (f16 has steps of 1 there), less 1536
+__device__ __forceinline__ uint32_t quant2(uint32_t w, float inv) {
+  const float lo = fmaf(__uint_as_float(w << 16), inv, 1536.f);
+  const float hi = fmaf(__uint_as_float(w & 0xFFFF0000u), inv, 1536.f);
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(pack_f16x2(lo, hi)), "r"(0x66006600u));
+  return r;
+}
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// the first MMA of a group's sum: no accumulator to clear
+__device__ __forceinline__ void mma_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                          uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+}  // namespace ql
