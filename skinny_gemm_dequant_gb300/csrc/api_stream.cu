@@ -13,6 +13,7 @@ namespace {
 
 constexpr size_t kTicketOff = 256;          // the zero region of every workspace: tickets,
 constexpr size_t kAmaxOff = 256 + 4096;     // then the rows' maxima of moe_int8
+static_assert(kMoeMaxTokens * kMoeMaxTopk * 4 <= kMoeHandedBytes, "weights");
 static_assert((kNumSMs + 1) * 4 <= 4096 && kMoeMaxTokens * kMoeMaxTopk * 4 <= (1 << 20) - 4096, "zero region");
 
 template <int N>
@@ -88,8 +89,8 @@ StreamArgs moe_args(const Moe& a) {
   s.tickets = at<unsigned>(a.ws, kTicketOff);
   s.amax = at<unsigned>(a.ws, kAmaxOff);
   s.slots = at<float>(a.ws, workspace_zero_bytes());
-  s.weights = at<float>(a.ws, workspace_zero_bytes() + al256(stream_slot_bytes(a.M)));
-  s.h = reinterpret_cast<uint16_t*>(s.weights + kMoeMaxTokens * kMoeMaxTopk);
+  s.handed = at<uint8_t>(a.ws, workspace_zero_bytes() + al256(stream_slot_bytes(a.M)));
+  s.h = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(s.handed) + kMoeHandedBytes);
   s.ldh = cdiv(a.I, 8) * 8;
   return s;
 }
@@ -115,9 +116,10 @@ ql_status moe_run(int fmt, const Moe& a, const Matrix& w13, const Matrix& w2, St
   dn.N = (int)a.H;
   dn.y = a.y;
   dn.ldy = a.ldy;
-  cudaError_t e = launch_stream(fmt, STREAM_GATE_UP, gu, st);
+  const bool few = moe_few_takes(fmt, gu);
+  cudaError_t e = few ? launch_moe_few(fmt, STREAM_GATE_UP, gu, st) : launch_stream(fmt, STREAM_GATE_UP, gu, st);
   if (e != cudaSuccess) return cuda_status(e);
-  e = launch_stream(fmt, STREAM_DOWN, dn, st);
+  e = few ? launch_moe_few(fmt, STREAM_DOWN, dn, st) : launch_stream(fmt, STREAM_DOWN, dn, st);
   if (e != cudaSuccess) {
     // the maxima that GATE_UP left are not taken back: what is zero between calls is made so
     cudaMemsetAsync(gu.amax, 0, (size_t)a.M * a.topk * 4, st);
@@ -139,7 +141,7 @@ size_t stream_workspace_bytes(int op, int64_t M, int64_t N, int64_t K, int E, in
   if (E <= 0 || topk <= 0) return 0;
   if (M > kMoeMaxTokens || topk > kMoeMaxTopk || K > 32768) return workspace_zero_bytes();  // refused
   return workspace_zero_bytes() + al256(stream_slot_bytes(M)) +
-         kMoeMaxTokens * kMoeMaxTopk * 4 + (size_t)M * topk * cdiv(K, 8) * 8 * 2;
+         kMoeHandedBytes + (size_t)M * topk * cdiv(K, 8) * 8 * 2;
 }
 }  // namespace ql
 

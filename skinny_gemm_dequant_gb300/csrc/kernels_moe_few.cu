@@ -26,10 +26,12 @@ namespace ql {
 namespace {
 
 constexpr int kGuWarps = 16;
+constexpr int kMaxTokens = 8, kMaxPairs = kMaxTokens * kMoeMaxTopk;
 constexpr int R = kStreamRows;
 constexpr int kPitch = R + 4;  // of a column of sums: lanes (g, t) write 8 t + g, all banks once
 constexpr int kSmem = 226 * 1024;
-constexpr int kMaxX = 96 * 1024;  // shared memory for the tokens of GATE_UP
+constexpr int kStage = 16 * 128, kDepth = 4;  // a ring of GATE_UP: bytes of a stage, stages
+constexpr int kMaxX = kSmem - kGuWarps * kDepth * kStage - 4096;  // for the tokens of GATE_UP; the lists take 2.5 KB
 
 __host__ __device__ constexpr int dn_warps(int fmt) { return fmt == STREAM_INT4 ? 12 : 8; }
 __host__ __device__ constexpr int gu_k(int fmt) { return fmt == STREAM_INT4 ? 256 : fmt == STREAM_INT8 ? 128 : 64; }
@@ -42,6 +44,14 @@ struct Lists {
   uint16_t *pair, *tok;  // sorted
   Entry* heads;    // scratch
   int* keys;       // scratch
+};
+
+// what GATE_UP hands to DOWN beside h: the lists and the weights
+struct Handed {
+  int entries, most, pad[2];
+  Entry entry[kMaxPairs];
+  uint16_t pair[kMaxPairs], tok[kMaxPairs];
+  float weight[kMaxPairs];  // by pair
 };
 
 template <int WARPS>
@@ -58,6 +68,27 @@ __device__ __forceinline__ void route(const StreamArgs& p, const Lists& l) {
     if (id < 0 || id >= p.E) id = kNone;  // padding: not dispatched
     if (lane < p.topk) l.ids[m * p.topk + lane] = id;
   }
+}
+
+// One token, by one warp: an entry for each pair.  Returns their number.
+__device__ __forceinline__ int route_one(const StreamArgs& p, const Lists& l) {
+  const int lane = threadIdx.x & 31;
+  int id = -1;
+  float wt;
+  if (p.logits)
+    route_token_warp<false>(p.logits, p.E, p.topk, false, id, wt);
+  else if (lane < p.topk)
+    id = p.ids[lane];
+  const bool on = lane < p.topk && id >= 0 && id < p.E;
+  const unsigned all = __ballot_sync(0xffffffffu, on);
+  if (lane < p.topk) l.ids[lane] = on ? id : kNone;
+  if (on) {
+    const int n = __popc(all & ((1u << lane) - 1));
+    l.entries[n] = {(uint16_t)id, (uint16_t)n, 1};
+    l.pair[n] = (uint16_t)lane;
+    l.tok[n] = 0;
+  }
+  return __popc(all);
 }
 
 // after a barrier; ends with one.  Returns the number of entries, and the most pairs of one
@@ -129,11 +160,10 @@ constexpr float kUp69 = 590295810358705651712.f;                         // 2^69
 // ------------------------------------------------------------------ GATE_UP
 template <int FMT, bool FINE, bool ZP>
 __global__ void __launch_bounds__(kGuWarps * 32, 1)
-    gate_up_kernel(const __grid_constant__ StreamArgs p, int x_bytes, int lists, int depth) {
+    gate_up_kernel(const __grid_constant__ StreamArgs p, int x_bytes, int lists) {
   constexpr bool I8 = FMT == STREAM_INT8, I4 = FMT == STREAM_INT4;
   constexpr int KS = gu_k(FMT), XB = FMT == STREAM_BF16 ? 128 : 256;  // k of a stage; bytes of a token's x block
   constexpr int XK = FMT == STREAM_BF16 ? 64 : 128, SB = KS / XK;     // k of an x block; blocks of a stage
-  constexpr int kStage = 16 * 128;
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int P = p.M * p.topk;
@@ -151,6 +181,7 @@ __global__ void __launch_bounds__(kGuWarps * 32, 1)
   l.heads = reinterpret_cast<Entry*>(ring_base);  // the rings are filled later
   l.keys = reinterpret_cast<int*>(l.heads + P);
   __shared__ unsigned s_top[16];
+  __shared__ int s_one;
 
   if (I8 && threadIdx.x < 16) s_top[threadIdx.x] = 0u;
   pdl_wait();
@@ -192,14 +223,12 @@ __global__ void __launch_bounds__(kGuWarps * 32, 1)
       if (on) *reinterpret_cast<uint4*>(smem + (size_t)(b * p.M + m) * XB + xslot<FMT, FINE>(c, m) * 16) = x;
     }
   };
-  if (warp < routing) {
-    route<kGuWarps / 2>(p, l);
-  } else if constexpr (I8) {
+  auto top_x = [&](int first, int step) {
 #pragma unroll 1
     for (int m = 0; m < p.M; ++m) {
       float top = 0.f;
 #pragma unroll 2
-      for (int i = threadIdx.x - routing * 32; i < p.K / 8; i += (kGuWarps - routing) * 32) {
+      for (int i = first; i < p.K / 8; i += step) {
         const uint4 v = *reinterpret_cast<const uint4*>(p.x + m * p.ldx + i * 16);
         const uint32_t q[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -210,54 +239,75 @@ __global__ void __launch_bounds__(kGuWarps * 32, 1)
       const unsigned most = __reduce_max_sync(0xffffffffu, __float_as_uint(top) & 0x7FFFFFFFu);
       if (lane == 0) atomicMax(&s_top[m], most);
     }
+  };
+  int ne, most = 1;
+  if (warp < routing) {
+    if (p.M == 1)
+      s_one = route_one(p, l);
+    else
+      route<kGuWarps / 2>(p, l);
+  } else if constexpr (I8) {
+    top_x(threadIdx.x - routing * 32, (kGuWarps - routing) * 32);
   } else {
     stage_x(threadIdx.x - routing * 32, (kGuWarps - routing) * 32);
   }
   __syncthreads();
-  if (I8) {
-    stage_x(threadIdx.x, kGuWarps * 32);
-    if (threadIdx.x < p.M) s_xs[threadIdx.x] = __fdiv_rn(__uint_as_float(s_top[threadIdx.x]), 127.f);
-  }
-  int most;
-  const int ne = dispatch<kGuWarps>(p, l, 8, most);
+  ne = p.M == 1 ? s_one : dispatch<kGuWarps>(p, l, kMaxTokens, most);
 
   const int otiles = p.N / 8, total = ne * otiles;
   const int step = (int)gridDim.x * kGuWarps;
-  const uint32_t ring = smem_addr(ring_base) + (uint32_t)(warp * depth * kStage);
+  const uint32_t ring = smem_addr(ring_base) + (uint32_t)(warp * kDepth * kStage);
 
   // a lane copies 16-byte piece cc of rows cr and cr + 4, gate and up
   const int cr = lane >> 3, cc = lane & 7;
   const uint32_t dst0 = (uint32_t)(cr * 128 + wslot(cc, cr) * 16), dst1 = (uint32_t)((cr + 4) * 128 + wslot(cc, cr + 4) * 16);
   const int64_t up = (int64_t)p.N * p.ldw, four = 4 * p.ldw;
   const int kbytes = I4 ? p.K / 2 : I8 ? p.K : p.K * 2;
-  int f_tile = (int)blockIdx.x + warp * (int)gridDim.x, f_left = 0, f_at = 0;
-  const uint8_t* f_w = nullptr;
+  int f_tile = (int)blockIdx.x + warp * (int)gridDim.x, f_left = 0;  // bytes of a row to copy
+  const uint8_t *f_gate = nullptr, *f_up = nullptr;
   auto fetch = [&](uint32_t at) {
-    if (f_left == 0 && f_tile < total) {
+    if (f_left <= 0 && f_tile < total) {
       const int a = f_tile / otiles, o = f_tile - a * otiles;
-      f_w = p.w + l.entries[a].expert * p.w_estride + (int64_t)(o * 8 + cr) * p.ldw + cc * 16;
-      f_left = nstage;
-      f_at = cc * 16;
+      f_gate = p.w + l.entries[a].expert * p.w_estride + (int64_t)(o * 8 + cr) * p.ldw + cc * 16;
+      f_up = f_gate + up;
+      f_left = kbytes;
       f_tile += step;
     }
     if (f_left > 0) {
-      const bool in = f_at < kbytes;
-      cp16(at + dst0, f_w, in);
-      cp16(at + dst1, f_w + four, in);
-      cp16(at + 1024 + dst0, f_w + up, in);
-      cp16(at + 1024 + dst1, f_w + up + four, in);
-      f_w += 128;
-      f_at += 128;
-      --f_left;
+      const bool in = cc * 16 < f_left;
+      cp16(at + dst0, f_gate, in);
+      cp16(at + dst1, f_gate + four, in);
+      cp16(at + 1024 + dst0, f_up, in);
+      cp16(at + 1024 + dst1, f_up + four, in);
+      f_gate += 128;
+      f_up += 128;
+      f_left -= 128;
     }
     cp_commit();
   };
 #pragma unroll 1
-  for (int d = 0; d < depth - 1; ++d) fetch(ring + d * kStage);
+  for (int d = 0; d < kDepth - 1; ++d) fetch(ring + d * kStage);
 
-  if (blockIdx.x < p.M && warp == kGuWarps - 1) {
-    // the weights of a token, for the next launch (its warp's copies are under way)
-    const int m = blockIdx.x;
+  if constexpr (I8) {  // (the weights are on their way)
+    stage_x(threadIdx.x, kGuWarps * 32);
+    if (threadIdx.x < p.M) s_xs[threadIdx.x] = __fdiv_rn(__uint_as_float(s_top[threadIdx.x]), 127.f);
+    __syncthreads();
+  }
+  Handed& to_down = *reinterpret_cast<Handed*>(p.handed);
+  if (blockIdx.x == gridDim.x - 1 && warp == kGuWarps - 2) {
+    if (lane == 0) {
+      to_down.entries = ne;
+      to_down.most = most;
+    }
+    for (int i = lane; i < P; i += 32) {
+      if (i < ne) to_down.entry[i] = l.entries[i];
+      to_down.pair[i] = l.pair[i];
+      to_down.tok[i] = l.tok[i];
+    }
+  }
+  if (gridDim.x - 1 - blockIdx.x < p.M && warp == kGuWarps - 1) {
+    // the weights of a token, for the next launch: by the warps that have the fewest tiles
+    const int m = gridDim.x - 1 - blockIdx.x;
     int id = 0;
     float wt = 0.f;
     if (p.logits)
@@ -266,19 +316,20 @@ __global__ void __launch_bounds__(kGuWarps * 32, 1)
       wt = p.wts[m * p.topk + lane];
     if (lane < p.topk) {
       const int i = m * p.topk + lane;
-      p.weights[i] = wt;
+      to_down.weight[i] = wt;
       if (p.wts_out) p.wts_out[i] = wt;
       if (p.ids_out) p.ids_out[i] = l.ids[i] == kNone ? -1 : l.ids[i];
     }
   }
 
-  uint32_t slot = 0, to_slot = depth - 1;
+  uint32_t slot = 0;  // byte offset of the stage in the ring
+  const uint32_t w0_at = ring + (uint32_t)(g * 128 + wslot(t, g) * 16), w1_at = w0_at ^ 64u;  // pieces t, 4 + t
 #pragma unroll 1
   for (int tile = (int)blockIdx.x + warp * (int)gridDim.x; tile < total; tile += step) {
     const int a = tile / otiles, o = tile - a * otiles;
     const Entry en = l.entries[a];
     const int xg = l.tok[en.first + min(g, en.count - 1)];  // the token of this lane's B column
-    const uint32_t xat = smem_addr(smem) + (uint32_t)(xg * XB);
+    uint32_t xb = smem_addr(smem) + (uint32_t)(xg * XB);  // its row of the x block
     // scales: 4-bit: lane (g, t) those of gate (t < 2) or up row g, of block t % 2 of a stage
     constexpr int NS = FINE ? 4 : 1;
     uint16_t s_next[NS];
@@ -316,12 +367,12 @@ __global__ void __launch_bounds__(kGuWarps * 32, 1)
     int whole[4] = {};
 #pragma unroll 1
     for (int s = 0; s < nstage; ++s) {
-      cp_wait(depth - 2);
+      asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 2) : "memory");
       __syncwarp();  // every lane's copies of this stage have landed, and the stage before is read
-      fetch(ring + to_slot * kStage);
-      if (++to_slot == (uint32_t)depth) to_slot = 0;
-      const uint32_t wat = ring + slot * kStage + g * 128;
-      if (++slot == (uint32_t)depth) slot = 0;
+      fetch(ring + ((slot - kStage) & (kDepth * kStage - 1)));
+      const uint32_t wa[2] = {w0_at + slot, w1_at + slot};
+      const uint32_t wf = ring + slot + g * 128 + t * 4, wx = wslot(0, g) * 16;  // FINE: word t of piece c at c * 16 ^ wx
+      slot = (slot + kStage) & (kDepth * kStage - 1);
       uint32_t sz[NS];
       if constexpr (I4) {
 #pragma unroll
@@ -330,7 +381,6 @@ __global__ void __launch_bounds__(kGuWarps * 32, 1)
       }
 #pragma unroll
       for (int sb = 0; sb < SB; ++sb) {
-        const uint32_t xb = xat + (uint32_t)((s * SB + sb) * p.M * XB);
         if constexpr (I4) {
           uint32_t wv[2][4];
 #pragma unroll
@@ -338,9 +388,9 @@ __global__ void __launch_bounds__(kGuWarps * 32, 1)
             if constexpr (FINE) {
               // word t of every 32-k piece, so that an MMA stays inside one group
 #pragma unroll
-              for (int j = 0; j < 4; ++j) wv[h][j] = lds4(wat + h * 1024 + wslot(4 * sb + j, g) * 16 + t * 4);
+              for (int j = 0; j < 4; ++j) wv[h][j] = lds4(wf + h * 1024 + ((4 * sb + j) * 16 ^ wx));
             } else {
-              const uint4 v = lds16(wat + h * 1024 + wslot(4 * sb + t, g) * 16);
+              const uint4 v = lds16(wa[sb] + h * 1024);
               wv[h][0] = v.x;
               wv[h][1] = v.y;
               wv[h][2] = v.z;
@@ -374,7 +424,7 @@ __global__ void __launch_bounds__(kGuWarps * 32, 1)
         } else {
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const uint4 w0 = lds16(wat + wslot(4 * j + t, g) * 16), w1 = lds16(wat + 1024 + wslot(4 * j + t, g) * 16);
+            const uint4 w0 = lds16(wa[j]), w1 = lds16(wa[j] + 1024);
             if constexpr (I8) {
               const uint32_t lo[4] = {w0.x, w0.y, w0.z, w0.w}, hi[4] = {w1.x, w1.y, w1.z, w1.w};
               const uint4 xa = lds16(xb + xslot<FMT, FINE>(8 * j + 2 * t, xg) * 16);
@@ -394,6 +444,7 @@ __global__ void __launch_bounds__(kGuWarps * 32, 1)
             }
           }
         }
+        xb += (uint32_t)(p.M * XB);
       }
       if (I8 && ((s & 7) == 7 || s == nstage - 1)) {  // 1024 k: sums of at most 2^24
 #pragma unroll
@@ -452,19 +503,28 @@ __global__ void __launch_bounds__(dn_warps(FMT) * 32, 1)
   l.pair = reinterpret_cast<uint16_t*>(s_inv + P);
   l.tok = l.pair + P;
   uint8_t* rings = smem + lists;
-  l.heads = reinterpret_cast<Entry*>(rings);
-  l.keys = reinterpret_cast<int*>(l.heads + P);
-  __shared__ int s_last;
+  __shared__ int s_last[3];
 
-  // this runs before the wait: the launch before, GATE_UP, has waited for what wrote the logits
-  route<W>(p, l);
+  pdl_wait();
+  pdl_launch_dependents();
+  const Handed& from_gu = *reinterpret_cast<const Handed*>(p.handed);
+  const int ne = from_gu.entries, xt = from_gu.most;
+#pragma unroll 1
+  for (int i = threadIdx.x; i < P; i += THREADS) {
+    if (i < ne) l.entries[i] = from_gu.entry[i];
+    l.pair[i] = from_gu.pair[i];
+    l.tok[i] = from_gu.tok[i];
+    float wt = from_gu.weight[i];
+    if constexpr (I8) {
+      const float top = __uint_as_float(p.amax[i]);
+      wt *= __fdiv_rn(top, 127.f);
+      s_inv[i] = top == 0.f ? 0.f : __fdiv_rn(127.f, top);
+    }
+    s_wt[i] = wt;
+  }
   __syncthreads();
-  int xt;
-  const int ne = dispatch<W>(p, l, 16, xt);
-
   const int nblk = (p.K + KU - 1) / KU, tiles = (p.N + R - 1) / R, whole = ne * nblk, total = tiles * whole;
   if (total == 0) {  // nothing was dispatched
-    pdl_wait();
     for (int i = blockIdx.x * THREADS + threadIdx.x; i < p.M * p.N; i += gridDim.x * THREADS)
       reinterpret_cast<uint16_t*>(p.y)[(int64_t)(i / p.N) * p.ldy + i % p.N] = 0;
     return;
@@ -508,7 +568,6 @@ __global__ void __launch_bounds__(dn_warps(FMT) * 32, 1)
   };
 
   At f = set(v0);
-  bool f_new = true;
   int f_valid = 0, f_toks = 0, f_first = 0;
   const uint8_t* f_w = nullptr;
   const int64_t wstep = (int64_t)RPI * p.ldw;
@@ -577,55 +636,16 @@ __global__ void __launch_bounds__(dn_warps(FMT) * 32, 1)
 #pragma unroll
       for (int i = 0; i < 4; ++i) y[mt][nt][i] = part[mt][nt][i] = 0.f;
 
-  // The first steps only copy: weights, which do not depend on the launch before, then, after the wait,
-  // the rows of h that meet them
   const int pre = depth - 1;
-  {
-    const At first = f;
 #pragma unroll 1
-    for (int pass = 0; pass < 2; ++pass) {
-      if (pass) {
-        pdl_wait();
-        pdl_launch_dependents();
-      }
-      f = first;
-#pragma unroll 1
-      for (int d = 0; d < pre; ++d) {
-        if (f.u < v1) {
-          target();
-          if (pass)
-            fetch_x(ring + d * stage);
-          else
-            fetch_w(ring + d * stage);
-        }
-        if (pass) cp_commit();
-        next(f);
-      }
+  for (int d = 0; d < pre; ++d) {
+    if (f.u < v1) {
+      if (d == 0 || f.kb == 0) target();
+      fetch_x(ring + d * stage);
+      fetch_w(ring + d * stage);
     }
-    f_new = true;
-  }
-#pragma unroll 1
-  for (int i = threadIdx.x; i < P; i += THREADS) {
-    float wt = p.weights[i];
-    if constexpr (I8) {
-      const float top = __uint_as_float(__ldcg(p.amax + i));
-      wt *= __fdiv_rn(top, 127.f);
-      s_inv[i] = top == 0.f ? 0.f : __fdiv_rn(127.f, top);
-    }
-    s_wt[i] = wt;
-  }
-  __syncthreads();
-  if constexpr (I8) {
-    // every CTA has read the maxima once all have counted in: they are zero for the next call
-    if (threadIdx.x == 0) {
-      __threadfence();
-      s_last = atomicAdd(p.tickets + gridDim.x, 1u) == gridDim.x - 1;
-    }
-    __syncthreads();
-    if (s_last) {
-      for (int i = threadIdx.x; i < P; i += THREADS) p.amax[i] = 0u;
-      if (threadIdx.x == 0) p.tickets[gridDim.x] = 0u;
-    }
+    cp_commit();
+    next(f);
   }
 
   At c = set(v0);
@@ -732,10 +752,9 @@ __global__ void __launch_bounds__(dn_warps(FMT) * 32, 1)
     cp_wait(pre - 1);
     __syncwarp();  // every lane's copies of this unit have landed, and the unit before is read
     if (f.u < v1) {
-      if (f_new || f.kb == 0) target();
-      f_new = false;
-      fetch_w(ring + to_slot * stage);
+      if (f.kb == 0) target();
       fetch_x(ring + to_slot * stage);
+      fetch_w(ring + to_slot * stage);
     }
     cp_commit();
     next(f);
@@ -882,22 +901,19 @@ __global__ void __launch_bounds__(dn_warps(FMT) * 32, 1)
   const int slot_floats = p.M * R;
   // 0: the part of a tile that began in an earlier CTA, 1: of one that ends in a later CTA
   auto slot_of = [&](int cta, int tail) { return p.slots + ((int64_t)cta * 2 + tail) * slot_floats; };
-  if (u0 >= u1) return;
+  auto put = [&](int tile, int i, float v) {
+    const int n = tile * R + i % R;
+    if (n < p.N) reinterpret_cast<uint16_t*>(p.y)[(int64_t)(i / R) * p.ldy + n] = f32_to_bf16_rn(v);
+  };
+  const int tile0 = u0 / whole, tile1 = u1 > u0 ? (u1 - 1) / whole : tile0 - 1;
 #pragma unroll 1
-  for (int tile = u0 / whole; tile <= (u1 - 1) / whole; ++tile) {
+  for (int tile = tile0; tile <= tile1; ++tile) {
     const int s = tile * whole, e = s + whole, a = max(s, u0), b = min(e, u1);
     // the warps that hold parts of it
     int lo = 0, hi = W - 1;
     while (bound(lo + 1) <= a) ++lo;
     while (bound(hi) >= b) --hi;
     if (lo == hi && a == s && b == e) continue;  // written
-    const bool shared = a > s || b < e;
-    const int c0 = s / share, c1 = (e - 1) / share;
-    float* mine = slot_of(blockIdx.x, a == s);
-    auto put = [&](int i, float v) {
-      const int n = tile * R + i % R;
-      if (n < p.N) reinterpret_cast<uint16_t*>(p.y)[(int64_t)(i / R) * p.ldy + n] = f32_to_bf16_rn(v);
-    };
 #pragma unroll 1
     for (int i = threadIdx.x; i < p.M * R; i += THREADS) {
       float v = 0.f;
@@ -908,31 +924,49 @@ __global__ void __launch_bounds__(dn_warps(FMT) * 32, 1)
                                          : reinterpret_cast<const float*>(rings + (size_t)w * depth * stage);
         v += from[i / R * kPitch + i % R];
       }
-      if (shared)
-        __stcg(mine + i, v);
+      if (a > s || b < e)
+        __stcg(slot_of(blockIdx.x, a == s) + i, v);
       else
-        put(i, v);
+        put(tile, i, v);
     }
-    if (!shared) continue;
-    // the last of the CTAs that share it adds the parts in the order of K
-    __threadfence();
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      s_last = atomicAdd(p.tickets + c0, 1u) == (unsigned)(c1 - c0);
-      if (s_last) p.tickets[c0] = 0u;
+  }
+  // At most two tiles, the first and the last, have parts in other CTAs: the last CTA of each adds the
+  // parts in the order of K
+  const bool cut0 = tile0 <= tile1 && (tile0 * whole < u0 || (tile0 + 1) * whole > u1);
+  const bool cut1 = tile1 > tile0 && (tile1 + 1) * whole > u1;
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x < 64 && (threadIdx.x & 31) == 0) {
+    const int which = threadIdx.x >> 5, tile = which ? tile1 : tile0;
+    bool last = false;
+    if (which ? cut1 : cut0) {
+      const int c0 = tile * whole / share, c1 = ((tile + 1) * whole - 1) / share;
+      last = atomicAdd(p.tickets + c0, 1u) == (unsigned)(c1 - c0);
+      if (last) p.tickets[c0] = 0u;
     }
-    __syncthreads();
-    if (s_last) {
-      __threadfence();
+    s_last[which] = last;
+  }
+  if (I8 && threadIdx.x == 64) {
+    // every CTA has read h's maxima before its first product: the last one here leaves them zero
+    s_last[2] = atomicAdd(p.tickets + gridDim.x, 1u) == gridDim.x - 1;
+  }
+  __syncthreads();
+  if (I8 && s_last[2]) {
+    for (int i = threadIdx.x; i < P; i += THREADS) p.amax[i] = 0u;
+    if (threadIdx.x == 0) p.tickets[gridDim.x] = 0u;
+  }
 #pragma unroll 1
-      for (int i = threadIdx.x; i < p.M * R; i += THREADS) {
-        float v = 0.f;
+  for (int which = 0; which < 2; ++which) {
+    if (!s_last[which]) continue;
+    __threadfence();
+    const int tile = which ? tile1 : tile0, c0 = tile * whole / share, c1 = ((tile + 1) * whole - 1) / share;
+#pragma unroll 1
+    for (int i = threadIdx.x; i < p.M * R; i += THREADS) {
+      float v = 0.f;
 #pragma unroll 4
-        for (int q = c0; q <= c1; ++q) v += __ldcg(slot_of(q, q == c0) + i);
-        put(i, v);
-      }
+      for (int q = c0; q <= c1; ++q) v += __ldcg(slot_of(q, q == c0) + i);
+      put(tile, i, v);
     }
-    __syncthreads();  // s_last is read
   }
 }
 
@@ -943,19 +977,17 @@ cudaError_t launch_gu(const StreamArgs& a, int x_bytes, cudaStream_t st) {
   if (const cudaError_t e = raise_smem_limit(kfn, once); e != cudaSuccess) return e;
   const int P = a.M * a.topk;
   const int lists = (P * (int)(sizeof(Entry) + 4 + 4) + 64 + 127) & ~127;
-  int depth = (kSmem - x_bytes - lists) / (kGuWarps * 2048);
-  if (depth > 6) depth = 6;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(kNumSMs, 1, 1);
   cfg.blockDim = dim3(kGuWarps * 32, 1, 1);
-  cfg.dynamicSmemBytes = (size_t)(x_bytes + lists + depth * kGuWarps * 2048);
+  cfg.dynamicSmemBytes = (size_t)(x_bytes + lists + kGuWarps * kDepth * kStage);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kfn, a, x_bytes, lists, depth);
+  return cudaLaunchKernelEx(&cfg, kfn, a, x_bytes, lists);
 }
 
 template <int FMT, int NT, bool FINE, bool ZP>
@@ -988,10 +1020,10 @@ int64_t gu_x_bytes(int fmt, const StreamArgs& a) {
 
 }  // namespace
 
-bool moe_few_takes(int fmt, int mode, const StreamArgs& a) {
-  if (a.M > 8) return false;
-  if (mode == STREAM_GATE_UP) return gu_x_bytes(fmt, a) <= kMaxX;
-  return true;
+static_assert(sizeof(Handed) <= kMoeHandedBytes, "workspace");
+
+bool moe_few_takes(int fmt, const StreamArgs& gate_up) {
+  return gate_up.M <= kMaxTokens && gu_x_bytes(fmt, gate_up) <= kMaxX;
 }
 
 cudaError_t launch_moe_few(int fmt, int mode, const StreamArgs& a, cudaStream_t st) {

@@ -221,7 +221,7 @@ __global__ void __launch_bounds__((compute_warps(FMT, NT) + 1) * 32, 1)
       wt = p.wts[m * p.topk + lane];
     if (lane < p.topk) {
       const int i = m * p.topk + lane;
-      p.weights[i] = wt;
+      reinterpret_cast<float*>(p.handed)[i] = wt;
       if (p.wts_out) p.wts_out[i] = wt;
       if (p.ids_out) p.ids_out[i] = s_id[i] == kNone ? -1 : s_id[i];
     }
@@ -591,7 +591,7 @@ __global__ void __launch_bounds__((compute_warps(FMT, NT) + 1) * 32, 1)
     // ---------------------------------------------------------------- sums and results: rows lane, lane + 32
     if (DN) {
       pdl_wait();
-      for (int i = lane; i < P; i += 32) s_wt[i] = p.weights[i];
+      for (int i = lane; i < P; i += 32) s_wt[i] = reinterpret_cast<const float*>(p.handed)[i];
       __syncwarp();
       if (I8) {
         __syncthreads();
@@ -817,7 +817,6 @@ size_t stream_slot_bytes(int64_t M) {
 }
 
 cudaError_t launch_stream(int fmt, int mode, const StreamArgs& a, cudaStream_t st) {
-  if (mode != STREAM_LINEAR && moe_few_takes(fmt, mode, a)) return launch_moe_few(fmt, mode, a, st);
   if (mode == STREAM_GATE_UP) return launch_moe<STREAM_GATE_UP>(fmt, a, st);
   if (mode == STREAM_DOWN) return launch_moe<STREAM_DOWN>(fmt, a, st);
   if (a.M <= 8) return launch<STREAM_INT8, STREAM_LINEAR, 1, false, false>(a, st);
