@@ -101,6 +101,7 @@ enum {
   QL_PATH_GATED_FFN_TCGEN05 = 14, /* gated block, one tcgen05 GEMM with the activation in its epilogue */
   QL_PATH_GATED_FFN_BACKWARD = 15, /* gradients of g and u, then the dx and dW13 tcgen05 GEMMs */
   QL_PATH_INT8_CODES_SKINNY = 16,  /* given 8-bit codes, weight-streaming kernel                */
+  QL_PATH_INT8_CODES_TCGEN05 = 17, /* given 8-bit codes, tcgen05 GEMM on pairs of SMs           */
   QL_PATH_MOE_BF16 = 18,           /* routing + gate, up and activation; down and the weighted  */
   QL_PATH_MOE_INT8 = 19,           /* sum: two weight-streaming launches                        */
   QL_PATH_MOE_INT4 = 20
@@ -484,8 +485,10 @@ QL_API ql_status quantize_int8(const uint16_t* x, int64_t M, int64_t K, int64_t 
  * qlinear_int8_w8a8's y bit for bit.  x_q: int8 [M, ldx]; x_scale: fp32 [M]; w: int8 [N, ldw], both of
  * any value, -128 too; w_scale: fp32 [N] or [1] (w_scale_len); bias: nullable bf16 [N]; y: [M, ldy] of
  * out_type QL_OUT_*.
- * One launch that streams the weights once per 16 tokens.
- * Requires 1 <= M <= 2^22, 1 <= N <= 2^24, ceil(M/16) ceil(N/32) ceil(K/128) <= 2^30, K >= 16, K % 16 == 0, K <= 131056 (|acc| < 2^31), ldx >= K,
+ * Paths: M <= 16: one launch that streams the weights once; else a launch that widens the tokens'
+ *        codes to f16 and one tcgen05 GEMM that widens the weights on the way (sm_103a has no integer
+ *        tcgen05 MMA; fp32 sums are exact below 2^24 and move to int32 every 1024 k).
+ * Requires 1 <= M <= 2^22, 1 <= N <= 2^24, K >= 16, K % 16 == 0, K <= 131056 (|acc| < 2^31), ldx >= K,
  * ldw >= K, both multiples of 16, 16-byte aligned x_q and w, 4-byte aligned scales, y aligned to its
  * type, ldy >= N.  workspace: ql_workspace_bytes(QL_OP_INT8_CODES, M, N, K, 0, 0) bytes, zeroed once.
  */

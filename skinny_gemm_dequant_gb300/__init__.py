@@ -129,7 +129,7 @@ PATHS = {0: "none", 1: "int8_skinny", 2: "fp8_skinny", 3: "fp8_tcgen05", 4: "mxf
          5: "mxfp4_tcgen05", 6: "moe_mxfp4", 7: "bf16_skinny", 8: "fp8_channel_skinny",
          9: "int8_tcgen05", 10: "moe_mxfp4_tcgen05", 11: "int4_skinny", 12: "gated_ffn_int4",
          13: "gated_ffn_skinny", 14: "gated_ffn_tcgen05", 15: "gated_ffn_backward",
-         16: "int8_codes_skinny", 18: "moe_bf16", 19: "moe_int8", 20: "moe_int4"}
+         16: "int8_codes_skinny", 17: "int8_codes_tcgen05", 18: "moe_bf16", 19: "moe_int8", 20: "moe_int4"}
 
 
 class QLError(RuntimeError):

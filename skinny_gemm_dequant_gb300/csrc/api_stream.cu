@@ -4,6 +4,7 @@
 #include <cstdio>
 
 #include "../../include/qlinear.h"
+#include "gemm_codes.h"
 #include "internal.h"
 #include "stream.h"
 
@@ -137,7 +138,10 @@ ql_status moe_run(int fmt, const Moe& a, const Matrix& w13, const Matrix& w2, St
 
 namespace ql {
 size_t stream_workspace_bytes(int op, int64_t M, int64_t N, int64_t K, int E, int topk) {
-  if (op == QL_OP_INT8_CODES) return workspace_zero_bytes() + stream_slot_bytes(1);
+  if (op == QL_OP_INT8_CODES) {
+    if (M > (1 << 22) || N > (1 << 24) || K > 131056 || M < 1 || N < 1 || K < 1) return workspace_zero_bytes();  // refused
+    return workspace_zero_bytes() + (M > kStreamMaxTokens ? tc::codes_gemm_bytes(M, N, K) : stream_slot_bytes(1));
+  }
   if (E <= 0 || topk <= 0) return 0;
   if (M > kMoeMaxTokens || topk > kMoeMaxTopk || K > 32768) return workspace_zero_bytes();  // refused
   return workspace_zero_bytes() + al256(stream_slot_bytes(M)) +
@@ -171,7 +175,31 @@ ql_status qlinear_int8(const int8_t* x_q, int64_t M, int64_t K, int64_t ldx, con
     return QL_ERR_ALIGNMENT;
   if (!workspace || workspace_bytes < ql_workspace_bytes(QL_OP_INT8_CODES, M, N, K, 0, 0)) return QL_ERR_WORKSPACE;
   if (!aligned<16>(workspace)) return QL_ERR_ALIGNMENT;
-  if (cdiv(M, 16) * cdiv(N, kStreamRows) * cdiv(K, 128) > (int64_t(1) << 30)) return QL_ERR_UNSUPPORTED;
+  if (M > kStreamMaxTokens) {
+    tc::CodesGemm g = {};
+    g.x = x_q;
+    g.M = M;
+    g.K = K;
+    g.ldx = ldx;
+    g.w = w;
+    g.N = N;
+    g.ldw = ldw;
+    g.x_scale = x_scale;
+    g.w_scale = w_scale;
+    g.w_scale_len = (int)w_scale_len;
+    g.bias = bias;
+    g.y = y;
+    g.ldy = ldy;
+    g.out_type = out_type;
+    g.scratch = at<uint8_t>(workspace, workspace_zero_bytes());
+    g.tickets = at<unsigned>(workspace, kTicketOff);
+    g.status = at<uint32_t>(workspace, 0);
+    g.wait_limit = wait_limit();
+    const cudaError_t e = tc::launch_codes_gemm(g, (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_status(e);
+    if (path_out) *path_out = QL_PATH_INT8_CODES_TCGEN05;
+    return QL_OK;
+  }
   StreamArgs s = {};
   s.x = reinterpret_cast<const uint8_t*>(x_q);
   s.ldx = ldx;

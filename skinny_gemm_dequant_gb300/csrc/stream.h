@@ -15,7 +15,7 @@ constexpr int kStreamRows = 64;       // weight rows of a tile
 constexpr int kMoeMaxTokens = 64;     // of a mixture-of-experts call
 constexpr int kMoeMaxTopk = 16;
 constexpr int kMoeHandedBytes = 4096;
-constexpr int kStreamMaxTokens = 32;  // of a linear call
+constexpr int kStreamMaxTokens = 16;  // of a linear call
 
 struct StreamArgs {
   const uint8_t* x;  // activations: bf16 rows (tokens; DOWN: h by pair), LINEAR: 8-bit codes

@@ -36,7 +36,8 @@ def call(ql, xq, xs, w, ws, K, **kw):
 
 
 SIZES = [(1, 512, 1024), (1, 1, 16), (2, 33, 48), (3, 5120, 272), (8, 100, 2080), (9, 31, 1040), (16, 257, 528),
-         (17, 64, 2048), (32, 130, 1600)]
+         (17, 64, 2048), (32, 130, 1600), (33, 513, 144), (100, 256, 1024), (192, 300, 2064), (193, 1000, 5136),
+         (400, 2056, 400), (1000, 777, 1040)]
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
@@ -46,7 +47,7 @@ def test_exact(ql, M, N, K, dtype):
     acc = MO.linear_codes(xq[:, :K], xs, w[:, :K], ws)[0]
     bias = torch.randn(N, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16) if M % 2 else None
     y, path = call(ql, xq, xs, w, ws, K, bias=None if bias is None else bias.cuda(), out_dtype=dtype, debug=True)
-    assert path == "int8_codes_skinny"
+    assert path == ("int8_codes_skinny" if M <= 16 else "int8_codes_tcgen05")
     assert torch.equal(y.cpu(), want(acc, xs, ws, dtype, bias))
     one = call(ql, xq, xs, w, ws[:1], K, out_dtype=dtype)
     assert torch.equal(one.cpu(), want(acc, xs, np.repeat(ws[:1], N), dtype))
@@ -64,7 +65,7 @@ def test_sums_of_one_sign_are_exact(ql):
         assert np.array_equal(y.cpu().numpy(), acc.astype(np.float32))
 
 
-@pytest.mark.parametrize("M", [1, 7, 32])
+@pytest.mark.parametrize("M", [1, 7, 16, 32, 200])
 def test_output_rows_beyond_the_call_stay(ql, M):
     xq, xs, w, ws = make(M, 45, 160, seed=3)
     wide = torch.full((M + 2, 64), 5.0, dtype=torch.bfloat16, device="cuda")
@@ -91,7 +92,7 @@ def test_quantize(ql, M, K):
     assert np.array_equal(q.cpu().numpy(), codes)
 
 
-@pytest.mark.parametrize("M", [1, 5, 16, 30])
+@pytest.mark.parametrize("M", [1, 5, 16, 30, 260])
 def test_same_as_the_linear_that_quantises_itself(ql, M):
     g = torch.Generator().manual_seed(M)
     x = torch.randn(M, 1280, generator=g).to(torch.bfloat16).cuda()
