@@ -14,7 +14,7 @@
 //   warp 0: TMA producer;  warp 1: MMA issue (first CTA of the pair only);  warp 2: tensor memory;
 //   warps 4..11: accumulators to int32 registers (a row and half of the columns per thread), results;
 //   warps 12..19: weights to f16 (a row and half of a stage's 128 k per thread).
-// Two accumulators take turns every 1024 k, two A buffers every 128 k: 2 * 192 + 2 * 64 columns.
+// Two accumulators take turns every 1024 k, six A buffers every 64 k: 2 * 160 + 6 * 32 columns.
 // Pairs take whole tiles in turn.  What is left over, less than one tile each, is cut into equal
 // stretches of 128-k stages; a pair leaves the sums of its part of a tile in a slot of the workspace and
 // counts in on the tile's ticket, and the one that completes the count adds the parts (whole numbers:
@@ -43,17 +43,18 @@ constexpr int kThreads = 640;
 constexpr int kPairs = kNumSMs / 2;
 constexpr int kStageK = 128;
 constexpr int kGroup = 8;  // stages of an accumulator: 1024 k
-constexpr int kMaxWidth = 192;
+constexpr int kMaxWidth = 160;
 constexpr int kStages = 5;
 constexpr uint32_t kWBytes = 128 * kStageK;                     // 8-bit weights of a stage
 constexpr uint32_t kXTile = kMaxWidth / 2 * 128;                // f16 tokens of 64 k
 constexpr uint32_t kStageBytes = kWBytes + 2 * kXTile;
-constexpr uint32_t kAccCols = 192, kACol = 2 * kAccCols, kACols = 64;
 constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kAccCols = kMaxWidth, kACol = 2 * kAccCols, kACols = 32;
+constexpr int kABufs = (kTmemCols - kACol) / kACols / 2 * 2;  // of 64 k: even ones hold a stage's first half
 constexpr uint32_t kDrainLimit = 1u << 22;
 constexpr int kBlockRows = 16;  // tile rows that run before the next tile column
 constexpr unsigned kMissing = 1u << 16;  // of a ticket: a part that was not computed
-static_assert(kACol + 2 * kACols <= kTmemCols, "tensor memory");
+static_assert(kABufs >= 4, "tensor memory");
 // registers a thread of the five warpgroups; the launch gives each 96 (640 threads share 65536)
 constexpr int kRegsIssue = 48, kRegsSums = 152, kRegsWiden = 64;
 static_assert(kRegsIssue + 2 * kRegsSums + 2 * kRegsWiden <= 5 * 96, "register split");
@@ -127,6 +128,15 @@ __device__ __forceinline__ void tmem_st_u32x32(uint32_t taddr, const uint32_t (&
       "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
       : "memory");
 }
+// What these order is tensor memory, written and read: tcgen05 fences on both sides of the barrier do
+// that.  No other memory is handed over, so neither side pays for a cluster-wide release or acquire
+// (with them a stage of 128 k took 1.15 us, whatever was left out of it).
+__device__ __forceinline__ void arrive_tmem(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, uint32_t limit, volatile int* abort) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, limit, abort));
+}
 // a barrier of the eight warps that hold the results; true if `bad` is true in one of their threads
 __device__ __forceinline__ bool results_any(bool bad) {
   int r;
@@ -145,7 +155,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   // full_w: 8-bit weights of a stage (this CTA's); full_x: both CTAs' tokens (first CTA's);
   // conv: A buffer written by both CTAs (first CTA's); afree: its products have finished
-  __shared__ uint64_t full_w[kStages], full_x[kStages], empty[kStages], conv[2], afree[2], dfull[2], dempty[2], done;
+  __shared__ uint64_t full_w[kStages], full_x[kStages], empty[kStages], conv[kABufs], afree[kABufs], dfull[2], dempty[2], done;
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort, s_issued, s_last;
   __shared__ float s_xs[kMaxWidth];
@@ -167,9 +177,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(&full_x[s], 1);
       mbar_init(&empty[s], 1);
     }
-    for (int b = 0; b < 2; ++b) {
-      mbar_init(&conv[b], 16);    // eight converter warps in each CTA
+    for (int b = 0; b < kABufs; ++b) {
+      mbar_init(&conv[b], 8);  // four converter warps in each CTA
       mbar_init(&afree[b], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
       mbar_init(&dfull[b], 1);
       mbar_init(&dempty[b], 16);  // eight result warps in each CTA
     }
@@ -212,7 +224,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tile_at(p, t, tn, tm);
         const int rw = tn * 256 + (int)rank * 128, rx = tm * p.width + (int)rank * hw;
         for (int kt = k0; kt < k1; ++kt) {
-          if (!wait2_warp(&empty[s], ph, lim, abort)) {
+          if (!wait_warp(&empty[s], ph, lim, abort)) {
             if (leader) fail();
             ok = false;
             break;
@@ -259,27 +271,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int kt = k0; kt < k1; ++kt) {
           const bool first = (kt - k0) % kGroup == 0, last = (kt - k0) % kGroup == kGroup - 1 || kt == k1 - 1;
           const int buf = g & 1;
-          if ((first && !wait2_warp(&dempty[buf], (uint32_t)((g >> 1) & 1) ^ 1, lim, abort)) ||
-              !wait2_warp(&full_x[s], ph, lim, abort) || !wait2_warp(&conv[a], aph, lim, abort)) {
+          if ((first && !wait_warp(&dempty[buf], (uint32_t)((g >> 1) & 1) ^ 1, lim, abort)) ||
+              !wait_warp(&full_x[s], ph, lim, abort)) {
             if (leader) fail();
             ok = false;
             break;
           }
-          tc_fence_after();
-          if (leader) {
-            const uint32_t d = tmem + (uint32_t)buf * kAccCols, at = tmem + kACol + (uint32_t)a * kACols;
-            const uint64_t x = x0 + (uint64_t)s * (kStageBytes >> 4);
+          const uint32_t d = tmem + (uint32_t)buf * kAccCols;
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              mma_pair_ta(d, at + j * 8, x + (j >> 2) * (kXTile >> 4) + (j & 3) * 2, idesc, !first || j != 0);
-            commit_pair(&afree[a]);
+          for (int h = 0; h < 2; ++h) {
+            if (!ok || !wait_warp(&conv[a + h], aph, lim, abort)) {
+              if (leader && ok) fail();
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            if (leader) {
+              const uint32_t at = tmem + kACol + (uint32_t)(a + h) * kACols;
+              const uint64_t x = x0 + (uint64_t)s * (kStageBytes >> 4) + h * (kXTile >> 4);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) mma_pair_ta(d, at + j * 8, x + j * 2, idesc, !first || h != 0 || j != 0);
+              commit_pair(&afree[a + h]);
+            }
+            __syncwarp();
+          }
+          if (!ok) break;
+          if (leader) {
             commit_pair(&empty[s]);
             if (last) commit_pair(&dfull[buf]);
           }
           __syncwarp();
           if (last) ++g;
-          a ^= 1;
-          if (a == 0) aph ^= 1;
+          a += 2;
+          if (a == kABufs) {
+            a = 0;
+            aph ^= 1;
+          }
           if (++s == kStages) {
             s = 0;
             ph ^= 1;
@@ -317,7 +344,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (int k = k0; k < k1 && ok; k += kGroup, ++g) {
         const int buf = g & 1;
         int got = 0;
-        if (lane == 0) got = wait2(&dfull[buf], (uint32_t)(g >> 1) & 1, lim_group, abort);
+        if (lane == 0) got = mbar_wait(&dfull[buf], (uint32_t)(g >> 1) & 1, lim_group, abort);
         got = __shfl_sync(0xffffffffu, got, 0);
         if (!got && lane == 0) fail();
         if (!got) {
@@ -336,7 +363,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive_remote(in_cta(smem_u32(&dempty[buf]), 0));
+        if (lane == 0) arrive_tmem(in_cta(smem_u32(&dempty[buf]), 0));
       }
       if (results_any(!ok)) {  // all eight warps or none: they meet at barriers below
         ok = false;
@@ -412,15 +439,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int q = warp & 3, half = (warp - 12) >> 2;  // lane quadrant; 64 k of a stage's 128
     const int r = 32 * q + lane;
     const uint32_t row = base + (uint32_t)(r * 128);
-    const uint32_t to = tmem + ((uint32_t)(32 * q) << 16) + kACol + (uint32_t)(half * 32);
-    const uint32_t arrive[2] = {in_cta(smem_u32(&conv[0]), 0), in_cta(smem_u32(&conv[1]), 0)};
-    int s = 0, a = 0;
-    uint32_t ph = 0, aph = 1;  // the first two buffers are free
+    const uint32_t to = tmem + ((uint32_t)(32 * q) << 16) + kACol;
+    const uint32_t arrive = in_cta(smem_u32(&conv[0]), 0);
+    int s = 0, a = half;
+    uint32_t ph = 0, aph = 1;  // the buffers are free at first
     bool ok = true;
     int t, k0, k1;
     for (Walk w(p, pair); ok && w.next(p, t, k0, k1);)
       for (int kt = k0; kt < k1; ++kt) {
-        if (!wait2_warp(&full_w[s], ph, lim, abort)) {
+        if (!wait_warp(&full_w[s], ph, lim, abort)) {
           if (lane == 0) fail();
           ok = false;
           break;
@@ -436,7 +463,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 4; ++i) s8x4_to_f16x2x2(b[i], v[8 * j + 2 * i], v[8 * j + 2 * i + 1]);
         }
-        if (!wait2_warp(&afree[a], aph, lim, abort)) {
+        if (!wait_warp(&afree[a], aph, lim, abort)) {
           if (lane == 0) fail();
           ok = false;
           break;
@@ -446,9 +473,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive_remote(arrive[a]);
-        a ^= 1;
-        if (a == 0) aph ^= 1;
+        if (lane == 0) arrive_tmem(arrive + (uint32_t)a * 8);
+        a += 2;
+        if (a >= kABufs) {
+          a = half;
+          aph ^= 1;
+        }
         if (++s == kStages) {
           s = 0;
           ph ^= 1;
