@@ -445,45 +445,50 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint32_t ph = 0, aph = 1;  // the buffers are free at first
     bool ok = true;
     int t, k0, k1;
-    for (Walk w(p, pair); ok && w.next(p, t, k0, k1);)
-      for (int kt = k0; kt < k1; ++kt) {
-        if (!wait_warp(&full_w[s], ph, lim, abort)) {
-          if (lane == 0) fail();
-          ok = false;
-          break;
-        }
-        const uint32_t from = row + (uint32_t)s * kStageBytes;
-        uint32_t v[32];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          uint32_t b[4];
-          asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                       : "=r"(b[0]), "=r"(b[1]), "=r"(b[2]), "=r"(b[3])
-                       : "r"(from + (uint32_t)(((half * 4 + j) ^ (r & 7)) * 16)));
-#pragma unroll
-          for (int i = 0; i < 4; ++i) s8x4_to_f16x2x2(b[i], v[8 * j + 2 * i], v[8 * j + 2 * i + 1]);
-        }
-        if (!wait_warp(&afree[a], aph, lim, abort)) {
-          if (lane == 0) fail();
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        tmem_st_u32x32(to + (uint32_t)a * kACols, v);
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) arrive_tmem(arrive + (uint32_t)a * 8);
-        a += 2;
-        if (a >= kABufs) {
-          a = half;
-          aph ^= 1;
-        }
-        if (++s == kStages) {
-          s = 0;
-          ph ^= 1;
-        }
+    // the loads of a stage go out before the stage before is waited for in tensor memory
+    int n = 0;  // stages of all items
+    for (Walk w(p, pair); w.next(p, t, k0, k1);) n += k1 - k0;
+    uint32_t b[16];
+    auto load = [&]() {
+      if (!wait_warp(&full_w[s], ph, lim, abort)) {
+        if (lane == 0) fail();
+        ok = false;
+        return;
       }
+      const uint32_t from = row + (uint32_t)s * kStageBytes;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(b[4 * j]), "=r"(b[4 * j + 1]), "=r"(b[4 * j + 2]), "=r"(b[4 * j + 3])
+                     : "r"(from + (uint32_t)(((half * 4 + j) ^ (r & 7)) * 16)));
+      if (++s == kStages) {
+        s = 0;
+        ph ^= 1;
+      }
+    };
+    if (n > 0) load();
+#pragma unroll 1
+    for (int i = 0; i < n && ok; ++i) {
+      uint32_t v[32];
+#pragma unroll
+      for (int j = 0; j < 16; ++j) s8x4_to_f16x2x2(b[j], v[2 * j], v[2 * j + 1]);
+      if (!wait_warp(&afree[a], aph, lim, abort)) {
+        if (lane == 0) fail();
+        break;
+      }
+      tc_fence_after();
+      tmem_st_u32x32(to + (uint32_t)a * kACols, v);
+      if (i + 1 < n) load();
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) arrive_tmem(arrive + (uint32_t)a * 8);
+      a += 2;
+      if (a >= kABufs) {
+        a = half;
+        aph ^= 1;
+      }
+    }
   }
   tc_fence_before();
   __syncthreads();
