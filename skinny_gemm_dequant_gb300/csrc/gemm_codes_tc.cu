@@ -11,10 +11,11 @@
 // The weights stay 8-bit up to the SM: converter warps widen them into tensor memory, which holds the
 // products' A operand, so their f16 form costs shared memory no bandwidth.  Tokens are widened once,
 // by a launch before (their f16 form is read by every row of tiles).  Roles in a CTA:
-//   warp 0: TMA producer;  warp 1: MMA issue (first CTA of the pair only);  warp 2: tensor memory;
+//   warp 0: TMA producer;  warp 1: MMA issue, warp 3: tokens' arrival (both in the first CTA of the pair
+//   only);  warp 2: tensor memory;
 //   warps 4..11: accumulators to int32 registers (a row and half of the columns per thread), results;
 //   warps 12..19: weights to f16 (a row and half of a stage's 128 k per thread).
-// Two accumulators take turns every 1024 k, six A buffers every 64 k: 2 * 160 + 6 * 32 columns.
+// Two accumulators take turns every 1024 k, three A buffers every 128 k: 2 * 160 + 3 * 64 columns.
 // Pairs take whole tiles in turn.  What is left over, less than one tile each, is cut into equal
 // stretches of 128-k stages; a pair leaves the sums of its part of a tile in a slot of the workspace and
 // counts in on the tile's ticket, and the one that completes the count adds the parts (whole numbers:
@@ -49,12 +50,12 @@ constexpr uint32_t kWBytes = 128 * kStageK;                     // 8-bit weights
 constexpr uint32_t kXTile = kMaxWidth / 2 * 128;                // f16 tokens of 64 k
 constexpr uint32_t kStageBytes = kWBytes + 2 * kXTile;
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kAccCols = kMaxWidth, kACol = 2 * kAccCols, kACols = 32;
-constexpr int kABufs = (kTmemCols - kACol) / kACols / 2 * 2;  // of 64 k: even ones hold a stage's first half
+constexpr uint32_t kAccCols = kMaxWidth, kACol = 2 * kAccCols, kACols = 64;
+constexpr int kABufs = (kTmemCols - kACol) / kACols;  // a stage's weights each
 constexpr uint32_t kDrainLimit = 1u << 22;
 constexpr int kBlockRows = 16;  // tile rows that run before the next tile column
 constexpr unsigned kMissing = 1u << 16;  // of a ticket: a part that was not computed
-static_assert(kABufs >= 4, "tensor memory");
+static_assert(kABufs == 3 && kABufs < kStages, "tensor memory");
 // registers a thread of the five warpgroups; the launch gives each 96 (640 threads share 65536)
 constexpr int kRegsIssue = 48, kRegsSums = 152, kRegsWiden = 64;
 static_assert(kRegsIssue + 2 * kRegsSums + 2 * kRegsWiden <= 5 * 96, "register split");
@@ -137,6 +138,16 @@ __device__ __forceinline__ void arrive_tmem(uint32_t cluster_addr) {
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, uint32_t limit, volatile int* abort) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, limit, abort));
 }
+// asked early and used later: the answer takes about 250 cycles, the phase complete or not
+__device__ __forceinline__ uint32_t ask(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok;
+}
 // a barrier of the eight warps that hold the results; true if `bad` is true in one of their threads
 __device__ __forceinline__ bool results_any(bool bad) {
   int r;
@@ -153,9 +164,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     codes_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                       const __grid_constant__ Params p) {
   extern __shared__ uint8_t smem_raw[];
-  // full_w: 8-bit weights of a stage (this CTA's); full_x: both CTAs' tokens (first CTA's);
-  // conv: A buffer written by both CTAs (first CTA's); afree: its products have finished
-  __shared__ uint64_t full_w[kStages], full_x[kStages], empty[kStages], conv[kABufs], afree[kABufs], dfull[2], dempty[2], done;
+  // full_w: 8-bit weights of a stage (this CTA's); full_x: both CTAs' tokens (first CTA's); ready: both
+  // CTAs have widened a stage's weights, and its tokens are there (first CTA's); empty: its products
+  // have finished, the stage and its A buffer are free
+  __shared__ uint64_t full_w[kStages], full_x[kStages], empty[kStages], ready[kABufs], dfull[2], dempty[2], done;
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort, s_issued, s_last;
   __shared__ float s_xs[kMaxWidth];
@@ -177,10 +189,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(&full_x[s], 1);
       mbar_init(&empty[s], 1);
     }
-    for (int b = 0; b < kABufs; ++b) {
-      mbar_init(&conv[b], 8);  // four converter warps in each CTA
-      mbar_init(&afree[b], 1);
-    }
+    for (int b = 0; b < kABufs; ++b) mbar_init(&ready[b], 17);  // eight converter warps in each CTA, the first CTA's warp 3
     for (int b = 0; b < 2; ++b) {
       mbar_init(&dfull[b], 1);
       mbar_init(&dempty[b], 16);  // eight result warps in each CTA
@@ -264,56 +273,62 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const uint32_t idesc = (1u << 4) | ((uint32_t)(p.width >> 3) << 17) | ((256u >> 4) << 24);
       const uint64_t x0 = smem_desc_sw128(base + kWBytes);
       int s = 0, a = 0, g = 0;  // stage, A buffer, groups so far
-      uint32_t ph = 0, aph = 0;
+      uint32_t aph = 0;
       bool ok = true;
       int t, k0, k1;
       for (Walk w(p, pair); ok && w.next(p, t, k0, k1);) {
         for (int kt = k0; kt < k1; ++kt) {
           const bool first = (kt - k0) % kGroup == 0, last = (kt - k0) % kGroup == kGroup - 1 || kt == k1 - 1;
           const int buf = g & 1;
+          // (a wait costs this warp 0.1 us, waited for or not: one for each 128 k, and one commit)
           if ((first && !wait_warp(&dempty[buf], (uint32_t)((g >> 1) & 1) ^ 1, lim, abort)) ||
-              !wait_warp(&full_x[s], ph, lim, abort)) {
+              !wait_warp(&ready[a], aph, lim, abort)) {
             if (leader) fail();
             ok = false;
             break;
           }
-          const uint32_t d = tmem + (uint32_t)buf * kAccCols;
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if (!ok || !wait_warp(&conv[a + h], aph, lim, abort)) {
-              if (leader && ok) fail();
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            if (leader) {
-              const uint32_t at = tmem + kACol + (uint32_t)(a + h) * kACols;
-              const uint64_t x = x0 + (uint64_t)s * (kStageBytes >> 4) + h * (kXTile >> 4);
-#pragma unroll
-              for (int j = 0; j < 4; ++j) mma_pair_ta(d, at + j * 8, x + j * 2, idesc, !first || h != 0 || j != 0);
-              commit_pair(&afree[a + h]);
-            }
-            __syncwarp();
-          }
-          if (!ok) break;
+          tc_fence_after();
           if (leader) {
+            const uint32_t d = tmem + (uint32_t)buf * kAccCols, at = tmem + kACol + (uint32_t)a * kACols;
+            const uint64_t x = x0 + (uint64_t)s * (kStageBytes >> 4);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              mma_pair_ta(d, at + j * 8, x + (j >> 2) * (kXTile >> 4) + (j & 3) * 2, idesc, !first || j != 0);
             commit_pair(&empty[s]);
             if (last) commit_pair(&dfull[buf]);
           }
           __syncwarp();
           if (last) ++g;
-          a += 2;
-          if (a == kABufs) {
+          if (++a == kABufs) {
             a = 0;
             aph ^= 1;
           }
-          if (++s == kStages) {
-            s = 0;
-            ph ^= 1;
-          }
+          if (++s == kStages) s = 0;
         }
       }
       if (leader) commit_pair(&done);
+    } else if (warp == 3 && rank == 0) {
+      // ---------------------------------------------------------- a stage's tokens are there
+      int s = 0, a = 0, n = 0;
+      uint32_t ph = 0, aph = 1;
+      int t, k0, k1;
+      for (Walk w(p, pair); w.next(p, t, k0, k1);) n += k1 - k0;
+      for (int i = 0; i < n; ++i) {
+        // (the buffer's count for the stage before it is complete)
+        if (!wait_warp(&ready[a], aph, lim, abort) || !wait_warp(&full_x[s], ph, lim, abort)) {
+          if (lane == 0) fail();
+          break;
+        }
+        if (lane == 0) mbar_arrive(&ready[a]);
+        if (++a == kABufs) {
+          a = 0;
+          aph ^= 1;
+        }
+        if (++s == kStages) {
+          s = 0;
+          ph ^= 1;
+        }
+      }
     }
   } else if (warp < 12) {
     // ------------------------------------------------------------ int32 sums, results
@@ -439,18 +454,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int q = warp & 3, half = (warp - 12) >> 2;  // lane quadrant; 64 k of a stage's 128
     const int r = 32 * q + lane;
     const uint32_t row = base + (uint32_t)(r * 128);
-    const uint32_t to = tmem + ((uint32_t)(32 * q) << 16) + kACol;
-    const uint32_t arrive = in_cta(smem_u32(&conv[0]), 0);
-    int s = 0, a = half;
-    uint32_t ph = 0, aph = 1;  // the buffers are free at first
+    const uint32_t to = tmem + ((uint32_t)(32 * q) << 16) + kACol + (uint32_t)(half * 32);
+    const uint32_t arrive = in_cta(smem_u32(&ready[0]), 0);
+    int s = 0, a = 0, old = 0;  // old: the stage whose A buffer comes next
+    uint32_t ph = 0, oph = 0;
     bool ok = true;
     int t, k0, k1;
-    // the loads of a stage go out before the stage before is waited for in tensor memory
     int n = 0;  // stages of all items
     for (Walk w(p, pair); w.next(p, t, k0, k1);) n += k1 - k0;
     uint32_t b[16];
-    auto load = [&]() {
-      if (!wait_warp(&full_w[s], ph, lim, abort)) {
+    auto load = [&](uint32_t there) {
+      if (!__all_sync(0xffffffffu, there) && !wait_warp(&full_w[s], ph, lim, abort)) {
         if (lane == 0) fail();
         ok = false;
         return;
@@ -466,28 +480,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         ph ^= 1;
       }
     };
-    if (n > 0) load();
+    if (n > 0) load(0);
 #pragma unroll 1
     for (int i = 0; i < n && ok; ++i) {
+      const uint32_t is_free = ask(&empty[old], oph), there = ask(&full_w[s], ph);
       uint32_t v[32];
 #pragma unroll
       for (int j = 0; j < 16; ++j) s8x4_to_f16x2x2(b[j], v[2 * j], v[2 * j + 1]);
-      if (!wait_warp(&afree[a], aph, lim, abort)) {
-        if (lane == 0) fail();
-        break;
+      if (i >= kABufs) {
+        if (!__all_sync(0xffffffffu, is_free) && !wait_warp(&empty[old], oph, lim, abort)) {
+          if (lane == 0) fail();
+          break;
+        }
+        if (++old == kStages) {
+          old = 0;
+          oph ^= 1;
+        }
       }
       tc_fence_after();
       tmem_st_u32x32(to + (uint32_t)a * kACols, v);
-      if (i + 1 < n) load();
+      if (i + 1 < n) load(there);
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) arrive_tmem(arrive + (uint32_t)a * 8);
-      a += 2;
-      if (a >= kABufs) {
-        a = half;
-        aph ^= 1;
-      }
+      if (++a == kABufs) a = 0;
     }
   }
   tc_fence_before();
