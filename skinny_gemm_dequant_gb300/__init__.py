@@ -643,6 +643,7 @@ def gated_ffn_plan(gemm, M, I, H, *, save=None, both=True) -> FFNPlan:
 
 
 # ------------------------------------------------------------------ 8-bit codes on both sides
+# A few microseconds on the GPU: each tensor's shape, strides and device are read once.
 _OUT_TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
 
@@ -650,43 +651,48 @@ def _always():
     return True
 
 
-def _codes(t, name):
-    if t.dtype is not torch.int8 or not t.is_cuda or t.dim() != 2 or t.stride(1) != 1:
-        raise TypeError(f"{name} must be a 2-d int8 CUDA tensor with unit inner stride")
-    return t
+def _device(x, name="x"):
+    """x's device, the current one: launches go there."""
+    dev = x.get_device()
+    if dev < 0 or dev != torch._C._cuda_getDevice():
+        raise ValueError(f"{name} must be on the current CUDA device")
+    return dev
 
 
-def _vector(t, name, n, dtype):
-    if t.dtype is not dtype or not t.is_cuda or t.numel() != n or not t.is_contiguous():
-        raise TypeError(f"{name} must be a contiguous {str(dtype)[6:]} CUDA tensor of {n}")
-    return t
+def _codes(t, name, dev):
+    """(shape, strides) of an int8 matrix."""
+    shape, stride = t.shape, t.stride()
+    if t.dtype is not torch.int8 or t.get_device() != dev or len(shape) != 2 or stride[1] != 1:
+        raise TypeError(f"{name} must be a 2-d int8 tensor with unit inner stride on cuda:{dev}")
+    return shape, stride
 
 
-def _on(x, **others):
-    """Refuses tensors that are not on x's device, and x on another device than the current one."""
-    if x.device.index != torch.cuda.current_device():
-        raise ValueError("the tensors must be on the current device")
-    for name, t in others.items():
-        if t is not None and t.device != x.device:
-            raise ValueError(f"{name} must be on {x.device}, as x is")
+def _dense(t, name, shape, dtype, dev):
+    """The address of a contiguous tensor of that shape."""
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous {str(dtype)[6:]} tensor {list(shape)} on cuda:{dev}")
+    return t.data_ptr()
 
 
 def quantize_int8(x, *, out=None, out_scale=None, stream=None):
     """(codes int8 [M, K], scale fp32 [M]) of x bf16 [M, K], K a multiple of 8, by qlinear_int8_w8a8's
     rule: scale = max|x| / 127 of the row, codes = x / scale rounded half to even.  For projections
     that share their input: qlinear_int8 takes both."""
+    dev = _device(x)
     _bf16(x, "x")
     (M, K), (ldx, inner) = x.shape, x.stride()
     if inner != 1:
         raise TypeError("x must have unit inner stride")
-    _on(x, out=out, out_scale=out_scale)
     if out is None:
         out = _empty((M, K), torch.int8, x, stream)
-    elif _codes(out, "out").shape != (M, K) or not out.is_contiguous():
-        raise TypeError(f"out must be a contiguous int8 CUDA tensor [{M}, {K}]")
-    out_scale = _empty((M,), torch.float32, x, stream) if out_scale is None else _vector(out_scale, "out_scale", M, torch.float32)
-    if M:
-        _check(lib.quantize_int8(x.data_ptr(), M, K, max(ldx, K) if M == 1 else ldx, out.data_ptr(), out_scale.data_ptr(), _stream(stream)), "quantize_int8")
+    else:
+        _dense(out, "out", (M, K), torch.int8, dev)
+    if out_scale is None:
+        out_scale = _empty((M,), torch.float32, x, stream)
+    else:
+        _dense(out_scale, "out_scale", (M,), torch.float32, dev)
+    _check(lib.quantize_int8(x.data_ptr(), M, K, ldx, out.data_ptr(), out_scale.data_ptr(), _stream(stream)),
+           "quantize_int8")
     return out, out_scale
 
 
@@ -697,83 +703,86 @@ def qlinear_int8(x_q, x_scale, w, w_scale, bias=None, *, out_dtype=torch.bfloat1
     fp32 [N] or [1]; bias: bf16 [N]; out_dtype: bfloat16, float16 or float32.  Without a workspace one
     is kept per device and stream; captured calls share a piece of their graph's own memory per stream.
     With debug=True returns (y, path)."""
-    _codes(x_q, "x_q")
-    _codes(w, "w")
-    (M, K), (N, Kw) = x_q.shape, w.shape
+    dev = _device(x_q, "x_q")
+    (M, K), sx = _codes(x_q, "x_q", dev)
+    (N, Kw), sw = _codes(w, "w", dev)
     if Kw != K:
         raise ValueError(f"w must be [N, {K}] for x_q [{M}, {K}]")
-    _on(x_q, x_scale=x_scale, w=w, w_scale=w_scale, bias=bias, out=out)
-    _vector(x_scale, "x_scale", M, torch.float32)
-    _vector(w_scale, "w_scale", 1 if w_scale.numel() == 1 else N, torch.float32)
-    if bias is not None:
-        _vector(bias, "bias", N, torch.bfloat16)
-    if out is not None:
-        out_dtype = out.dtype
+    xs = _dense(x_scale, "x_scale", (M,), torch.float32, dev)
+    channels = w_scale.numel()
+    ws = _dense(w_scale, "w_scale", (1 if channels == 1 else N,), torch.float32, dev)
+    bias = None if bias is None else _dense(bias, "bias", (N,), torch.bfloat16, dev)
+    if out is None:
+        out = _empty((M, N), out_dtype, x_q, stream)
+        ldy = N
+    else:
+        out_dtype, ldy = out.dtype, out.stride(0)
+        if out.get_device() != dev or out.shape != (M, N) or out.stride(1) != 1:
+            raise TypeError(f"out must be [{M}, {N}] with unit inner stride on cuda:{dev}")
     fmt = _OUT_TYPES.get(out_dtype)
     if fmt is None:
         raise TypeError("the output must be bfloat16, float16 or float32")
-    if out is None:
-        out = _empty((M, N), out_dtype, x_q, stream)
-    elif out.shape != (M, N) or out.stride(1) != 1:
-        raise TypeError(f"out must be [{M}, {N}] with unit inner stride")
     path = ctypes.c_int(0) if debug else None
-    with _Scratch(x_q, _ffn_bytes(OP_INT8_CODES, M, N, K), stream, workspace, _always) as ws:
-        st = lib.qlinear_int8(x_q.data_ptr(), M, K, x_q.stride(0), x_scale.data_ptr(), w.data_ptr(), N, w.stride(0),
-                              w_scale.data_ptr(), w_scale.numel(), _ptr(bias), fmt, out.data_ptr(), out.stride(0),
-                              ws.data_ptr(), ws.numel(), _stream(stream), path)
+    with _Scratch(x_q, _ffn_bytes(OP_INT8_CODES, M, N, K), stream, workspace, _always) as buf:
+        st = lib.qlinear_int8(x_q.data_ptr(), M, K, sx[0], xs, w.data_ptr(), N, sw[0], ws, channels, bias, fmt,
+                              out.data_ptr(), ldy, buf.data_ptr(), buf.numel(), _stream(stream), path)
     if st:
         raise QLError(st, "qlinear_int8")
     return (out, PATHS[path.value]) if debug else out
 
 
 # ------------------------------------------------------------------ mixture of experts, few tokens
-def _experts(w, name, E, rows, cols, dtype):
-    """Checks a projection's weights [E, rows, >= cols]; returns (address, row stride, expert stride)."""
-    if w.dtype is not dtype or not w.is_cuda or w.dim() != 3 or w.stride(2) != 1:
-        raise TypeError(f"{name} must be a 3-d {str(dtype)[6:]} CUDA tensor with unit inner stride")
-    if w.shape[0] != E or w.shape[1] != rows or w.shape[2] < cols:
+def _experts(w, name, E, rows, cols, dtype, dev):
+    """(address, row stride, expert stride) of [E, rows, >= cols] weights, scales or zero points."""
+    shape, stride = w.shape, w.stride()
+    if w.dtype is not dtype or w.get_device() != dev or len(shape) != 3 or stride[2] != 1:
+        raise TypeError(f"{name} must be a 3-d {str(dtype)[6:]} tensor with unit inner stride on cuda:{dev}")
+    if shape[0] != E or shape[1] != rows or shape[2] < cols:
         raise ValueError(f"{name} must be [{E}, {rows}, {cols}]")
-    return w.data_ptr(), w.stride(1), w.stride(0)
+    return w.data_ptr(), stride[1], stride[0]
 
 
-def _moe(name, x, w13, w2, mats, *, router_logits, topk_ids, topk_weights, topk, renormalize, swiglu_alpha,
-         swiglu_limit, debug, out, workspace, stream):
-    """mats(E, I, H): the weights' arguments of the C call, checked."""
+def _moe(call, x, w13, mats, router_logits, topk_ids, topk_weights, topk, renormalize, swiglu_alpha, swiglu_limit, debug,
+         out, workspace, stream):
+    """mats(E, I, H, device): the weights' arguments of the C call, checked."""
+    dev = _device(x)
     _bf16(x, "x")
-    M, H = x.shape
-    if x.stride(1) != 1 or w13.dim() != 3 or w2.dim() != 3:
-        raise TypeError("x must have unit inner stride; w13 and w2 must be [E, rows, columns]")
-    E, rows, _ = w13.shape
+    (M, H), sx, (E, rows, _) = x.shape, x.stride(), w13.shape
+    if sx[1] != 1:
+        raise TypeError("x must have unit inner stride")
     if rows & 1:
         raise ValueError("w13 must have an even number of rows (gate, then up)")
     I = rows >> 1
-    _on(x, w13=w13, w2=w2, router_logits=router_logits, topk_ids=topk_ids, topk_weights=topk_weights, out=out)
-    if (router_logits is None) == (topk_ids is None):
-        raise ValueError("either router_logits or topk_ids and topk_weights must be given")
-    if topk_ids is not None:
-        if topk_ids.dim() != 2 or topk_ids.shape[0] != M or topk_weights is None:
-            raise ValueError(f"topk_ids and topk_weights must be [{M}, topk]")
-        topk = topk_ids.shape[1]
-        _vector(topk_ids, "topk_ids", M * topk, torch.int32)
-        if _vector(topk_weights, "topk_weights", M * topk, torch.float32).shape != topk_ids.shape:
-            raise ValueError(f"topk_weights must be [{M}, {topk}]")
-    elif _vector(router_logits, "router_logits", M * E, torch.bfloat16).shape != (M, E):
-        raise ValueError(f"router_logits must be [{M}, {E}]")
-    args = mats(E, I, H)
-    y = _out(out, M, H, x, stream)
-    ids = wts = h = None
+    logits = ids_in = w_in = None
+    if topk_ids is None:
+        if router_logits is None:
+            raise ValueError("either router_logits or topk_ids and topk_weights must be given")
+        logits = _dense(router_logits, "router_logits", (M, E), torch.bfloat16, dev)
+    else:
+        if router_logits is not None or topk_weights is None:
+            raise ValueError("either router_logits or topk_ids and topk_weights must be given")
+        topk = topk_ids.shape[-1]
+        ids_in = _dense(topk_ids, "topk_ids", (M, topk), torch.int32, dev)
+        w_in = _dense(topk_weights, "topk_weights", (M, topk), torch.float32, dev)
+    args = mats(E, I, H, dev)
+    if out is None:
+        y, ldy = _empty((M, H), torch.bfloat16, x, stream), H
+    else:
+        y, ldy = _out(out, M, H, x, stream), out.stride(0)
+        if out.get_device() != dev:
+            raise TypeError(f"out must be on cuda:{dev}")
+    ids = wts = h = path = None
     if debug:
         ids = _empty((M, topk), torch.int32, x, stream)
         wts = _empty((M, topk), torch.float32, x, stream)
         h = _empty((M * topk, I), torch.bfloat16, x, stream)
-    path = ctypes.c_int(0) if debug else None
-    with _Scratch(x, _ffn_bytes(OP_MOE_FEW, M, H, I, E, topk), stream, workspace, _always) as ws:
-        st = getattr(lib, name)(x.data_ptr(), M, H, x.stride(0), _ptr(router_logits), _ptr(topk_ids), _ptr(topk_weights),
-                                E, topk, int(renormalize), *args, I, swiglu_alpha, _inf(swiglu_limit), _ptr(ids),
-                                _ptr(wts), _ptr(h), y.data_ptr(), y.stride(0), ws.data_ptr(), ws.numel(),
-                                _stream(stream), path)
+        path = ctypes.c_int(0)
+    with _Scratch(x, _ffn_bytes(OP_MOE_FEW, M, H, I, E, topk), stream, workspace, _always) as buf:
+        st = call(x.data_ptr(), M, H, sx[0], logits, ids_in, w_in, E, topk, renormalize, *args, I, swiglu_alpha,
+                  _inf(swiglu_limit), _ptr(ids), _ptr(wts), _ptr(h), y.data_ptr(), ldy, buf.data_ptr(), buf.numel(),
+                  _stream(stream), path)
     if st:
-        raise QLError(st, name)
+        raise QLError(st, call.__name__)
     return (y, ids, wts, h, PATHS[path.value]) if debug else y
 
 
@@ -783,11 +792,10 @@ def moe_bf16(x, w13, w2, *, router_logits=None, topk_ids=None, topk_weights=None
     w13: bf16 [E, 2I, H] (gate rows, then up rows), w2: bf16 [E, H, I]; H and I multiples of 8.  Routing,
     activation and debug=True's (y, ids, weights, h, path) are moe_mxfp4_grouped's; an id outside
     [0, E) is padding, and a token without an expert gets zeros.  Workspaces as qlinear_int8's."""
-    def mats(E, I, H):
-        return (*_experts(w13, "w13", E, 2 * I, H, torch.bfloat16), *_experts(w2, "w2", E, H, I, torch.bfloat16))
-    return _moe("moe_bf16", x, w13, w2, mats, router_logits=router_logits, topk_ids=topk_ids,
-                topk_weights=topk_weights, topk=topk, renormalize=renormalize, swiglu_alpha=swiglu_alpha,
-                swiglu_limit=swiglu_limit, debug=debug, out=out, workspace=workspace, stream=stream)
+    def mats(E, I, H, dev):
+        return (*_experts(w13, "w13", E, 2 * I, H, torch.bfloat16, dev), *_experts(w2, "w2", E, H, I, torch.bfloat16, dev))
+    return _moe(lib.moe_bf16, x, w13, mats, router_logits, topk_ids, topk_weights, topk, renormalize, swiglu_alpha,
+                swiglu_limit, debug, out, workspace, stream)
 
 
 def moe_int8(x, w13, s13, w2, s2, *, router_logits=None, topk_ids=None, topk_weights=None, topk=8, renormalize=False,
@@ -795,13 +803,14 @@ def moe_int8(x, w13, s13, w2, s2, *, router_logits=None, topk_ids=None, topk_wei
     """moe_bf16's layer on 8-bit codes: w13 int8 [E, 2I, H] with s13 fp32 [E, 2I], w2 int8 [E, H, I]
     with s2 fp32 [E, H]; H and I multiples of 16.  x is quantised per token and h per (token, expert)
     inside, scale = max|v| / 127; the sums are exact."""
-    def mats(E, I, H):
-        _on(x, s13=s13, s2=s2)
-        return (*_experts(w13, "w13", E, 2 * I, H, torch.int8), _vector(s13, "s13", E * 2 * I, torch.float32).data_ptr(),
-                *_experts(w2, "w2", E, H, I, torch.int8), _vector(s2, "s2", E * H, torch.float32).data_ptr())
-    return _moe("moe_int8", x, w13, w2, mats, router_logits=router_logits, topk_ids=topk_ids,
-                topk_weights=topk_weights, topk=topk, renormalize=renormalize, swiglu_alpha=swiglu_alpha,
-                swiglu_limit=swiglu_limit, debug=debug, out=out, workspace=workspace, stream=stream)
+    def mats(E, I, H, dev):
+        return (*_experts(w13, "w13", E, 2 * I, H, torch.int8, dev), _dense(s13, "s13", (E, 2 * I), torch.float32, dev),
+                *_experts(w2, "w2", E, H, I, torch.int8, dev), _dense(s2, "s2", (E, H), torch.float32, dev))
+    return _moe(lib.moe_int8, x, w13, mats, router_logits, topk_ids, topk_weights, topk, renormalize, swiglu_alpha,
+                swiglu_limit, debug, out, workspace, stream)
+
+
+_NO_ZEROS = (None, 0, 0)
 
 
 def moe_int4(x, w13, s13, w2, s2, z13=None, z2=None, *, group=128, router_logits=None, topk_ids=None,
@@ -809,23 +818,22 @@ def moe_int4(x, w13, s13, w2, s2, z13=None, z2=None, *, group=128, router_logits
              workspace=None, stream=None):
     """moe_bf16's layer on 4-bit weights stored as qlinear_int4's: w13 uint8 [E, 2I, >=H/2], w2 uint8
     [E, H, >=I/2], scales bf16 or fp16 [E, rows, >=ceil(columns/group)], zero points uint8 of the same
-    shape or None: 8; H and I multiples of 32, group a power of two >= 32."""
-    def mats(E, I, H):
-        _on(x, s13=s13, s2=s2, z13=z13, z2=z2)
-        fmt = _SCALE_FORMATS.get(s13.dtype)
-        if fmt is None or s2.dtype is not s13.dtype:
+    shape or None: 8; H and I multiples of 32, group a power of two >= 32.  Values of x or h of 2^63 and more
+    count as infinite."""
+    def mats(E, I, H, dev):
+        scale, u8 = s13.dtype, torch.uint8
+        fmt = _SCALE_FORMATS.get(scale)
+        if fmt is None:
             raise TypeError("s13 and s2 must both be bfloat16 or both float16")
         if group < 1:
             raise ValueError("group must be positive")
-        args = ()
-        for n, w, s, z, rows, k in (("13", w13, s13, z13, 2 * I, H), ("2", w2, s2, z2, H, I)):
-            groups = -(-k // group)
-            args += (*_experts(w, "w" + n, E, rows, -(-k // 2), torch.uint8), *_experts(s, "s" + n, E, rows, groups, s.dtype))
-            args += (None, 0, 0) if z is None else _experts(z, "z" + n, E, rows, groups, torch.uint8)
-        return (*args, fmt, group)
-    return _moe("moe_int4", x, w13, w2, mats, router_logits=router_logits, topk_ids=topk_ids,
-                topk_weights=topk_weights, topk=topk, renormalize=renormalize, swiglu_alpha=swiglu_alpha,
-                swiglu_limit=swiglu_limit, debug=debug, out=out, workspace=workspace, stream=stream)
+        g13, g2 = -(-H // group), -(-I // group)
+        return (*_experts(w13, "w13", E, 2 * I, (H + 1) >> 1, u8, dev), *_experts(s13, "s13", E, 2 * I, g13, scale, dev),
+                *(_NO_ZEROS if z13 is None else _experts(z13, "z13", E, 2 * I, g13, u8, dev)),
+                *_experts(w2, "w2", E, H, (I + 1) >> 1, u8, dev), *_experts(s2, "s2", E, H, g2, scale, dev),
+                *(_NO_ZEROS if z2 is None else _experts(z2, "z2", E, H, g2, u8, dev)), fmt, group)
+    return _moe(lib.moe_int4, x, w13, mats, router_logits, topk_ids, topk_weights, topk, renormalize, swiglu_alpha,
+                swiglu_limit, debug, out, workspace, stream)
 
 
 # ------------------------------------------------------------------ sharded layers

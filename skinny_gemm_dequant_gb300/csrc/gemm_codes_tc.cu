@@ -374,7 +374,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             tmem_ld_x32(at + (uint32_t)buf * kAccCols + c, v);
             tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) acc[c + i] += __float2int_rn(__uint_as_float(v[i]));
+            for (int i = 0; i < 32; ++i)
+              if (c + i < kMaxWidth / 2) acc[c + i] += __float2int_rn(__uint_as_float(v[i]));
           }
         tc_fence_before();
         __syncwarp();

@@ -26,12 +26,13 @@ namespace ql {
 namespace {
 
 constexpr int kGuWarps = 16;
-constexpr int kMaxTokens = 8, kMaxPairs = kMaxTokens * kMoeMaxTopk;
+constexpr int kMaxTokens = 16, kMaxPairs = kMaxTokens * kMoeMaxTopk;
+constexpr int kPerEntry = 8;  // pairs: one token tile of GATE_UP
 constexpr int R = kStreamRows;
 constexpr int kPitch = R + 4;  // of a column of sums: lanes (g, t) write 8 t + g, all banks once
 constexpr int kSmem = 226 * 1024;
 constexpr int kStage = 16 * 128, kDepth = 4;  // a ring of GATE_UP: bytes of a stage, stages
-constexpr int kMaxX = kSmem - kGuWarps * kDepth * kStage - 4096;  // for the tokens of GATE_UP; the lists take 2.5 KB
+constexpr int kMaxX = kSmem - kGuWarps * kDepth * kStage - 4352;  // for the tokens of GATE_UP; the lists take 4 KB
 
 __host__ __device__ constexpr int dn_warps(int fmt) { return fmt == STREAM_INT4 ? 12 : 8; }
 __host__ __device__ constexpr int gu_k(int fmt) { return fmt == STREAM_INT4 ? 256 : fmt == STREAM_INT8 ? 128 : 64; }
@@ -252,7 +253,7 @@ __global__ void __launch_bounds__(kGuWarps * 32, 1)
     stage_x(threadIdx.x - routing * 32, (kGuWarps - routing) * 32);
   }
   __syncthreads();
-  ne = p.M == 1 ? s_one : dispatch<kGuWarps>(p, l, kMaxTokens, most);
+  ne = p.M == 1 ? s_one : dispatch<kGuWarps>(p, l, kPerEntry, most);
 
   const int otiles = p.N / 8, total = ne * otiles;
   const int step = (int)gridDim.x * kGuWarps;
@@ -1010,6 +1011,15 @@ cudaError_t launch_dn(const StreamArgs& a, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, kfn, a, lists);
 }
 
+template <int NT>
+cudaError_t launch_dn_nt(int fmt, const StreamArgs& a, cudaStream_t st) {
+  if (fmt == STREAM_BF16) return launch_dn<STREAM_BF16, NT, false, false>(a, st);
+  if (fmt == STREAM_INT8) return launch_dn<STREAM_INT8, NT, false, false>(a, st);
+  if (a.group_shift < 7)
+    return a.zero ? launch_dn<STREAM_INT4, NT, true, true>(a, st) : launch_dn<STREAM_INT4, NT, true, false>(a, st);
+  return a.zero ? launch_dn<STREAM_INT4, NT, false, true>(a, st) : launch_dn<STREAM_INT4, NT, false, false>(a, st);
+}
+
 // bytes of GATE_UP's tokens in shared memory
 int64_t gu_x_bytes(int fmt, const StreamArgs& a) {
   const int64_t ks = gu_k(fmt), stages = (a.K + ks - 1) / ks;
@@ -1035,10 +1045,7 @@ cudaError_t launch_moe_few(int fmt, int mode, const StreamArgs& a, cudaStream_t 
     if (fine) return a.zero ? launch_gu<STREAM_INT4, true, true>(a, x, st) : launch_gu<STREAM_INT4, true, false>(a, x, st);
     return a.zero ? launch_gu<STREAM_INT4, false, true>(a, x, st) : launch_gu<STREAM_INT4, false, false>(a, x, st);
   }
-  if (fmt == STREAM_BF16) return launch_dn<STREAM_BF16, 1, false, false>(a, st);
-  if (fmt == STREAM_INT8) return launch_dn<STREAM_INT8, 1, false, false>(a, st);
-  if (fine) return a.zero ? launch_dn<STREAM_INT4, 1, true, true>(a, st) : launch_dn<STREAM_INT4, 1, true, false>(a, st);
-  return a.zero ? launch_dn<STREAM_INT4, 1, false, true>(a, st) : launch_dn<STREAM_INT4, 1, false, false>(a, st);
+  return a.M <= 8 ? launch_dn_nt<1>(fmt, a, st) : launch_dn_nt<2>(fmt, a, st);
 }
 
 }  // namespace ql

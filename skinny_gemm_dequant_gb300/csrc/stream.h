@@ -14,7 +14,7 @@ enum { STREAM_GATE_UP = 0, STREAM_DOWN = 1, STREAM_LINEAR = 2 };
 constexpr int kStreamRows = 64;       // weight rows of a tile
 constexpr int kMoeMaxTokens = 64;     // of a mixture-of-experts call
 constexpr int kMoeMaxTopk = 16;
-constexpr int kMoeHandedBytes = 4096;
+constexpr int kMoeHandedBytes = 8192;
 constexpr int kStreamMaxTokens = 16;  // of a linear call
 
 struct StreamArgs {
@@ -40,7 +40,7 @@ struct StreamArgs {
   float alpha, limit;
   uint16_t* h;  // GATE_UP writes bf16 [M topk, ldh]
   int64_t ldh;
-  void* handed;       // kMoeHandedBytes that GATE_UP writes for DOWN: weights by pair, up to 8 tokens lists too
+  void* handed;       // kMoeHandedBytes that GATE_UP writes for DOWN: weights by pair, up to 16 tokens lists too
   unsigned* amax;     // INT8: [M topk] bits of max|h|, zero between calls
   unsigned* tickets;  // zero between calls
   float* slots;       // sums of tiles that CTAs share
@@ -53,7 +53,7 @@ struct StreamArgs {
 };
 
 cudaError_t launch_stream(int fmt, int mode, const StreamArgs& a, cudaStream_t st);
-// the launches for up to 8 tokens (kernels_moe_few.cu), where they take a call's GATE_UP
+// the launches for up to 16 tokens (kernels_moe_few.cu), where they take a call's GATE_UP
 bool moe_few_takes(int fmt, const StreamArgs& gate_up);
 cudaError_t launch_moe_few(int fmt, int mode, const StreamArgs& a, cudaStream_t st);
 size_t stream_slot_bytes(int64_t M);
