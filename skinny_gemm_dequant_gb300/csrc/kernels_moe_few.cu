@@ -182,46 +182,63 @@ __global__ void __launch_bounds__(kGuWarps * 32, 1)
   l.heads = reinterpret_cast<Entry*>(ring_base);  // the rings are filled later
   l.keys = reinterpret_cast<int*>(l.heads + P);
   __shared__ unsigned s_top[16];
-  __shared__ int s_one;
+  __shared__ int s_one, s_next;
 
   if (I8 && threadIdx.x < 16) s_top[threadIdx.x] = 0u;
+  if (threadIdx.x == 0) s_next = 0;
+  __syncthreads();
   pdl_wait();
   pdl_launch_dependents();
-  if (I8) __syncthreads();
 
-  // the first warps route; the others take x meanwhile, 16 bytes a thread
+  // the first warps route, the others take x meanwhile
   const int routing = min(p.M, kGuWarps / 2), vecs = nxb * (XK / 8);
-  auto stage_x = [&](int first, int step) {
-    // pieces of a token are neighbours: 16 lanes hold a block of 128 k
+  const int chunks = (vecs * p.M + 63) / 64;
+  auto stage_x = [&]() {
+    // a warp takes the next 64 pieces, so that those that route join in later; pieces of a token are
+    // neighbours, 16 lanes hold a block of 128 k
 #pragma unroll 1
-    for (int i = first; i - lane < vecs * p.M; i += step) {
-      const bool on = i < vecs * p.M;  // (whole groups of 16 lanes)
-      const int m = on ? i / vecs : 0, v = i - m * vecs, b = v / (XK / 8), c = v % (XK / 8);
-      uint4 x = make_uint4(0u, 0u, 0u, 0u);
-      if (on && v * 8 < p.K) x = *reinterpret_cast<const uint4*>(p.x + m * p.ldx + v * 16);
-      if constexpr (I8) {
-        const float top = __uint_as_float(s_top[m]), inv = top == 0.f ? 0.f : __fdiv_rn(127.f, top);
-        x = make_uint4(quant2(x.x, inv), quant2(x.y, inv), quant2(x.z, inv), quant2(x.w, inv));
-      }
-      if constexpr (I4) {
-        const uint32_t q[4] = {x.x, x.y, x.z, x.w};
-        float s = 0.f;
+    for (;;) {
+      int next = 0;
+      if (lane == 0) next = atomicAdd(&s_next, 1);
+      next = __shfl_sync(0xffffffffu, next, 0);
+      if (next >= chunks) break;
+      uint4 x2[2];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s += __uint_as_float(q[j] << 16) + __uint_as_float(q[j] & 0xFFFF0000u);
-        s += __shfl_xor_sync(0xffffffffu, s, 1);
-        s += __shfl_xor_sync(0xffffffffu, s, 2);
-        if constexpr (FINE) {
-          if (on && (c & 3) == 0) s_sum[(b * 4 + (c >> 2)) * p.M + m] = s * kDown69;
-        } else {
-          s += __shfl_xor_sync(0xffffffffu, s, 4);
-          s += __shfl_xor_sync(0xffffffffu, s, 8);
-          if (on && c == 0) s_sum[b * p.M + m] = s * kDown69;
-        }
-        x = pair_up(x);
-        x = make_uint4(mul_bf16x2(x.x, kLowScale), mul_bf16x2(x.y, kHighScale), mul_bf16x2(x.z, kLowScale),
-                       mul_bf16x2(x.w, kHighScale));
+      for (int q = 0; q < 2; ++q) {
+        const int i = next * 64 + q * 32 + lane, m = i / vecs, v = i - m * vecs;
+        x2[q] = make_uint4(0u, 0u, 0u, 0u);
+        if (m < p.M && v * 8 < p.K) x2[q] = *reinterpret_cast<const uint4*>(p.x + m * p.ldx + v * 16);
       }
-      if (on) *reinterpret_cast<uint4*>(smem + (size_t)(b * p.M + m) * XB + xslot<FMT, FINE>(c, m) * 16) = x;
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const int i = next * 64 + q * 32 + lane;
+        const bool on = i < vecs * p.M;  // (whole groups of 16 lanes)
+        const int m = on ? i / vecs : 0, v = i - m * vecs, b = v / (XK / 8), c = v % (XK / 8);
+        uint4 x = x2[q];
+        if constexpr (I8) {
+          const float top = __uint_as_float(s_top[m]), inv = top == 0.f ? 0.f : __fdiv_rn(127.f, top);
+          x = make_uint4(quant2(x.x, inv), quant2(x.y, inv), quant2(x.z, inv), quant2(x.w, inv));
+        }
+        if constexpr (I4) {
+          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+          float s = 0.f;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) s += __uint_as_float(w[j] << 16) + __uint_as_float(w[j] & 0xFFFF0000u);
+          s += __shfl_xor_sync(0xffffffffu, s, 1);
+          s += __shfl_xor_sync(0xffffffffu, s, 2);
+          if constexpr (FINE) {
+            if (on && (c & 3) == 0) s_sum[(b * 4 + (c >> 2)) * p.M + m] = s * kDown69;
+          } else {
+            s += __shfl_xor_sync(0xffffffffu, s, 4);
+            s += __shfl_xor_sync(0xffffffffu, s, 8);
+            if (on && c == 0) s_sum[b * p.M + m] = s * kDown69;
+          }
+          x = pair_up(x);
+          x = make_uint4(mul_bf16x2(x.x, kLowScale), mul_bf16x2(x.y, kHighScale), mul_bf16x2(x.z, kLowScale),
+                         mul_bf16x2(x.w, kHighScale));
+        }
+        if (on) *reinterpret_cast<uint4*>(smem + (size_t)(b * p.M + m) * XB + xslot<FMT, FINE>(c, m) * 16) = x;
+      }
     }
   };
   auto top_x = [&](int first, int step) {
@@ -249,9 +266,8 @@ __global__ void __launch_bounds__(kGuWarps * 32, 1)
       route<kGuWarps / 2>(p, l);
   } else if constexpr (I8) {
     top_x(threadIdx.x - routing * 32, (kGuWarps - routing) * 32);
-  } else {
-    stage_x(threadIdx.x - routing * 32, (kGuWarps - routing) * 32);
   }
+  if constexpr (!I8) stage_x();
   __syncthreads();
   ne = p.M == 1 ? s_one : dispatch<kGuWarps>(p, l, kPerEntry, most);
 
@@ -290,7 +306,7 @@ __global__ void __launch_bounds__(kGuWarps * 32, 1)
   for (int d = 0; d < kDepth - 1; ++d) fetch(ring + d * kStage);
 
   if constexpr (I8) {  // (the weights are on their way)
-    stage_x(threadIdx.x, kGuWarps * 32);
+    stage_x();
     if (threadIdx.x < p.M) s_xs[threadIdx.x] = __fdiv_rn(__uint_as_float(s_top[threadIdx.x]), 127.f);
     __syncthreads();
   }
@@ -374,10 +390,14 @@ __global__ void __launch_bounds__(kGuWarps * 32, 1)
       const uint32_t wa[2] = {w0_at + slot, w1_at + slot};
       const uint32_t wf = ring + slot + g * 128 + t * 4, wx = wslot(0, g) * 16;  // FINE: word t of piece c at c * 16 ^ wx
       slot = (slot + kStage) & (kDepth * kStage - 1);
-      uint32_t sz[NS];
+      float sc[NS], sz[NS];  // scale, scale times zero point: of this lane's row and block
       if constexpr (I4) {
 #pragma unroll
-        for (int j = 0; j < NS; ++j) sz[j] = (uint32_t)s_next[j] << 16 | (ZP ? z_next[j] : 0u);
+        for (int j = 0; j < NS; ++j) {
+          sc[j] = p.scale_fp16 ? __half2float(__ushort_as_half(s_next[j])) : bf16_bits_to_f32(s_next[j]);
+          // the zero point as a number: 2^23 + z, less 2^23
+          sz[j] = -sc[j] * (ZP ? __uint_as_float(0x4B000000u | z_next[j]) - 8388608.f : 8.f);
+        }
         if (s + 1 < nstage) scales(s + 1);
       }
 #pragma unroll
@@ -413,12 +433,10 @@ __global__ void __launch_bounds__(kGuWarps * 32, 1)
               const float x0 = sx[c0], x1 = sx[c1];
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
-                const uint32_t v = __shfl_sync(0xffffffffu, sz[FINE ? j : 0], g * 4 + h * 2 + sb);
-                const float sc = p.scale_fp16 ? __half2float(__ushort_as_half(v >> 16)) : __uint_as_float(v & 0xFFFF0000u);
-                // the zero point as a number: 2^23 + z, less 2^23
-                const float z = ZP ? __uint_as_float(0x4B000000u | (v & 255u)) - 8388608.f : 8.f;
-                acc[2 * h] = fmaf(sc, fmaf(-z, x0, grp[2 * h]), acc[2 * h]);
-                acc[2 * h + 1] = fmaf(sc, fmaf(-z, x1, grp[2 * h + 1]), acc[2 * h + 1]);
+                const float f = __shfl_sync(0xffffffffu, sc[FINE ? j : 0], g * 4 + h * 2 + sb);
+                const float z = ZP ? __shfl_sync(0xffffffffu, sz[FINE ? j : 0], g * 4 + h * 2 + sb) : -8.f * f;
+                acc[2 * h] = fmaf(z, x0, fmaf(f, grp[2 * h], acc[2 * h]));
+                acc[2 * h + 1] = fmaf(z, x1, fmaf(f, grp[2 * h + 1], acc[2 * h + 1]));
               }
             }
           }
@@ -762,14 +780,19 @@ __global__ void __launch_bounds__(dn_warps(FMT) * 32, 1)
     if (++to_slot == (uint32_t)depth) to_slot = 0;
     const uint32_t wat = ring + slot * stage + g * WB, xat = ring + slot * stage + R * WB;
     if (++slot == (uint32_t)depth) slot = 0;
-    uint32_t sz[2][NS];  // a scale leaves the low bits of its fp32 image free for the zero point
+    float scl[2][NS];  // scale and zero point (as bf16x2 of -z / 64) of this lane's rows
+    uint32_t nzl[2][NS];
     At n = c;
     next(n);
     if constexpr (I4) {
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int j = 0; j < NS; ++j) sz[h][j] = (uint32_t)s_next[h][j] << 16 | (ZP ? z_next[h][j] : 0u);
+        for (int j = 0; j < NS; ++j) {
+          scl[h][j] = p.scale_fp16 ? __half2float(__ushort_as_half(s_next[h][j])) : bf16_bits_to_f32(s_next[h][j]);
+          // z's pattern stands for z 2^-133, times -2^127
+          if (ZP) nzl[h][j] = fma_bf16x2(z_next[h][j] * 0x10001u, 0xFF00FF00u, 0u);
+        }
       if (n.u < v1) {
         if (n.kb == 0) scale_rows(n);
         scales(n.kb);
@@ -809,10 +832,8 @@ __global__ void __launch_bounds__(dn_warps(FMT) * 32, 1)
           if (j == 0 || FINE) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const uint32_t v = __shfl_sync(0xffffffffu, sz[mt / 2][FINE ? j : 0], mt % 2 * 16 + h * 8 + g);
-              sc[h] = p.scale_fp16 ? __half2float(__ushort_as_half(v >> 16)) : __uint_as_float(v & 0xFFFF0000u);
-              // -z / 64 from z's pattern: z 2^-133 times -2^127
-              negz[h] = ZP ? fma_bf16x2(__byte_perm(v, 0u, 0x4040), 0xFF00FF00u, 0u) : 0xBE00BE00u;
+              sc[h] = __shfl_sync(0xffffffffu, scl[mt / 2][FINE ? j : 0], mt % 2 * 16 + h * 8 + g);
+              negz[h] = ZP ? __shfl_sync(0xffffffffu, nzl[mt / 2][FINE ? j : 0], mt % 2 * 16 + h * 8 + g) : 0xBE00BE00u;
             }
           }
           uint32_t q0[4], q1[4];
@@ -956,18 +977,17 @@ __global__ void __launch_bounds__(dn_warps(FMT) * 32, 1)
     for (int i = threadIdx.x; i < P; i += THREADS) p.amax[i] = 0u;
     if (threadIdx.x == 0) p.tickets[gridDim.x] = 0u;
   }
+  if (!s_last[0] && !s_last[1]) return;
+  __threadfence();  // the other parts were fenced before their counts
 #pragma unroll 1
-  for (int which = 0; which < 2; ++which) {
+  for (int i = threadIdx.x; i < 2 * p.M * R; i += THREADS) {
+    const int which = i >= p.M * R, at = i - which * p.M * R;
     if (!s_last[which]) continue;
-    __threadfence();
     const int tile = which ? tile1 : tile0, c0 = tile * whole / share, c1 = ((tile + 1) * whole - 1) / share;
-#pragma unroll 1
-    for (int i = threadIdx.x; i < p.M * R; i += THREADS) {
-      float v = 0.f;
+    float v = 0.f;
 #pragma unroll 4
-      for (int q = c0; q <= c1; ++q) v += __ldcg(slot_of(q, q == c0) + i);
-      put(tile, i, v);
-    }
+    for (int q = c0; q <= c1; ++q) v += __ldcg(slot_of(q, q == c0) + at);
+    put(tile, at, v);
   }
 }
 
