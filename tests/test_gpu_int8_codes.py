@@ -37,7 +37,7 @@ def call(ql, xq, xs, w, ws, K, **kw):
 
 SIZES = [(1, 512, 1024), (1, 1, 16), (2, 33, 48), (3, 5120, 272), (8, 100, 2080), (9, 31, 1040), (16, 257, 528),
          (17, 64, 2048), (32, 130, 1600), (33, 513, 144), (100, 256, 1024), (192, 300, 2064), (193, 1000, 5136),
-         (400, 2056, 400), (1000, 777, 1040)]
+         (400, 2056, 400), (1000, 777, 1040), (200, 17408, 272), (161, 40, 8192)]
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
@@ -101,3 +101,68 @@ def test_same_as_the_linear_that_quantises_itself(ql, M):
     bias = torch.randn(300, generator=g).to(torch.bfloat16).cuda()
     codes, scale = ql.quantize_int8(x)
     assert torch.equal(ql.qlinear_int8(codes, scale, w, ws, bias), ql.qlinear_int8_w8a8(x, w, ws, bias))
+
+
+GEMM = [(20, 300, 8192), (161, 5000, 1040), (400, 700, 4112)]  # tiles of the rest alone; whole tiles too
+
+
+@pytest.mark.parametrize("M,N,K", GEMM)
+def test_nothing_is_left_behind_by_waits_that_run_out(ql, M, N, K):
+    """A wait limit of a few polls lets roles of the GEMM give up; the pair waits for its copies in flight
+    and leaves, and the next call finds the workspace as it needs it."""
+    xq, xs, w, ws = make(M, N, K, seed=6)
+    args = [torch.from_numpy(a).cuda() for a in (xq, xs, w, ws)]
+    space = ql.Workspace("cuda")
+    whole = ql.qlinear_int8(*args, workspace=space)
+    assert torch.equal(whole.cpu(), want(MO.linear_codes(xq, xs, w, ws)[0], xs, ws, torch.bfloat16))
+    seen = 0
+    for limit in (0, 0, 0, 1, 2, 4, 8, 16, 32, 64, 128):
+        ql.set_wait_limit(limit)
+        try:
+            ql.qlinear_int8(*args, workspace=space)
+        finally:
+            ql.set_wait_limit(1 << 20)
+        seen += ql.read_device_status(space.buf, clear=True)[1] & 1
+        assert not space.buf[256:256 + (1 << 20)].any()
+        assert torch.equal(ql.qlinear_int8(*args, workspace=space), whole)
+        assert ql.read_device_status(space.buf) == (0, 0)
+    assert seen
+
+
+@pytest.mark.parametrize("M", [1, 12, 40, 300])
+def test_graphs_and_streams(ql, M):
+    sets = [[torch.from_numpy(a).cuda() for a in make(M, 600, 2064, seed=s)] for s in (1, 2)]
+    alone = [ql.qlinear_int8(*a) for a in sets]
+    graphs = []
+    for a in sets:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs = [ql.qlinear_int8(*a), ql.qlinear_int8(*a)]
+        graphs.append((g, outs))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for i in (0, 1, 1, 0):
+        graphs[i][0].replay()
+        there = ql.qlinear_int8(*sets[1 - i], stream=side)
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, alone[i]) for o in graphs[i][1]) and torch.equal(there, alone[1 - i])
+
+
+def test_refusals(ql):
+    xq, xs, w, ws = [torch.from_numpy(a).cuda() for a in make(3, 32, 64)]
+    y = torch.empty(3, 32, dtype=torch.bfloat16, device="cuda")
+    for args, kw in [((xq.cpu(), xs, w, ws), {}), ((xq, xs.cpu(), w, ws), {}), ((xq, xs, w.cpu(), ws), {}),
+                     ((xq, xs, w, ws.cpu()), {}), ((xq.to(torch.uint8), xs, w, ws), {}), ((xq, xs.double(), w, ws), {}),
+                     ((xq, xs[:2], w, ws), {}), ((xq, xs, w, ws[:31]), {}), ((xq[:, :48], xs, w, ws), {}),
+                     ((xq[:, :40], xs, w[:, :40], ws), {}), ((xq.t(), xs, w, ws), {}), ((xq[:0], xs[:0], w, ws), {}),
+                     ((xq, xs, w, ws, y[0].float()[:32]), {}), ((xq, xs, w, ws), dict(out_dtype=torch.float64)),
+                     ((xq, xs, w, ws), dict(out=y[:, :31])), ((xq, xs, w, ws), dict(out=y.int())),
+                     ((xq, xs, w, ws), dict(out=y.cpu()))]:
+        with pytest.raises((TypeError, ValueError, ql.QLError)):
+            ql.qlinear_int8(*args, **kw)
+    x = torch.randn(3, 64).to(torch.bfloat16).cuda()
+    for args, kw in [((x.cpu(),), {}), ((x.float(),), {}), ((x[:, :60],), {}), ((x.t(),), {}), ((x[:0],), {}),
+                     ((x,), dict(out=torch.empty(3, 48, dtype=torch.int8, device="cuda"))),
+                     ((x,), dict(out_scale=torch.empty(4, device="cuda")))]:
+        with pytest.raises((TypeError, ValueError, ql.QLError)):
+            ql.quantize_int8(*args, **kw)

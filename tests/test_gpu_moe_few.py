@@ -196,31 +196,33 @@ def test_ties_and_extreme_logits(ql):
     check(layer, x, layer(ql, x, router_logits=logits, topk=6, debug=True), logits=logits, topk=6)
 
 
+@pytest.mark.parametrize("M", [1, 9, 20])
 @pytest.mark.parametrize("fmt", ["bf16", "int8", "int4"])
-def test_a_token_with_nan_leaves_the_others(ql, fmt):
+def test_a_token_with_nan_leaves_the_others(ql, fmt, M):
     layer = Layer(fmt, 6, 160, 96, seed=2)
-    x = tokens(9, 160, seed=6, fmt=fmt)
-    logits = torch.randn(9, 6, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).cuda()
+    x = tokens(M, 160, seed=6, fmt=fmt)
+    at = M // 2
+    logits = torch.randn(M, 6, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).cuda()
     clean = layer(ql, x, router_logits=logits, topk=3)
     for bad in (float("nan"), float("inf")):
         dirty = x.clone()
-        dirty[4, 77] = bad
+        dirty[at, 77] = bad
         y = layer(ql, dirty, router_logits=logits, topk=3)
-        assert torch.equal(torch.cat((y[:4], y[5:])), torch.cat((clean[:4], clean[5:])))
-        assert y[4].isnan().all()
+        assert torch.equal(torch.cat((y[:at], y[at + 1:])), torch.cat((clean[:at], clean[at + 1:])))
+        assert y[at].isnan().all()
     zero = x.clone()
-    zero[4] = 0
-    assert not layer(ql, zero, router_logits=logits, topk=3)[4].any()
+    zero[at] = 0
+    assert not layer(ql, zero, router_logits=logits, topk=3)[at].any()
 
 
 @pytest.mark.parametrize("fmt", ["bf16", "int8", "int4"])
 def test_workspace_is_left_zero_and_results_repeat(ql, fmt):
     layer = Layer(fmt, 32, 1024, 320, seed=11)
     ws = ql.Workspace("cuda")
-    logits = torch.randn(12, 32, generator=torch.Generator().manual_seed(2)).to(torch.bfloat16).cuda()
-    x = tokens(12, 1024, seed=7, fmt=fmt)
+    logits = torch.randn(40, 32, generator=torch.Generator().manual_seed(2)).to(torch.bfloat16).cuda()
+    x = tokens(40, 1024, seed=7, fmt=fmt)
     first = {}
-    for M in (12, 1, 7, 12, 1, 7):
+    for M in (12, 1, 7, 40, 12, 1, 7, 40):
         y = layer(ql, x[:M], router_logits=logits[:M], topk=4, workspace=ws)
         assert not ws.buf[:256 + (1 << 20)].any()
         assert torch.equal(first.setdefault(M, y), y)
@@ -235,3 +237,95 @@ def test_full_size_layers(ql):
         x = tokens(M, H, seed=9, fmt=fmt)
         got = layer(ql, x, topk_ids=torch.from_numpy(ids).cuda(), topk_weights=torch.from_numpy(w).cuda(), debug=True)
         check(layer, x, got, ids=ids, weights=w.astype(np.float64))
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "int8", "int4"])
+@pytest.mark.parametrize("M,E,topk,H,I", [(16, 3, 2, 4096, 64), (8, 3, 2, 8224, 32), (12, 2, 2, 96, 8224)])
+def test_rows_too_long_for_shared_memory(ql, fmt, M, E, topk, H, I):
+    layer = Layer(fmt, E, H, I, seed=M, group=64)
+    x = tokens(M, H, seed=M, fmt=fmt)
+    logits = torch.randn(M, E, generator=torch.Generator().manual_seed(M)).to(torch.bfloat16).cuda()
+    check(layer, x, layer(ql, x, router_logits=logits, topk=topk, debug=True), logits=logits, topk=topk)
+
+
+@pytest.mark.parametrize("M", [1, 6, 24])
+@pytest.mark.parametrize("fmt", ["bf16", "int8", "int4"])
+def test_graphs_streams_and_threads(ql, fmt, M):
+    """Captured graphs replayed in any order and against eager calls, a call on a given stream, and host
+    threads on one stream give what one call gives."""
+    import threading
+    layers = [Layer(fmt, 16, 288, 160, seed=s) for s in (1, 2)]
+    x = tokens(M, 288, seed=8, fmt=fmt)
+    logits = torch.randn(M, 16, generator=torch.Generator().manual_seed(3)).to(torch.bfloat16).cuda()
+    run = [lambda l=l, **kw: l(ql, x, router_logits=logits, topk=4, **kw) for l in layers]
+    want = [r() for r in run]
+    graphs = []
+    for r in run:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            first = r()
+            out = (first, r(debug=True))
+        graphs.append((g, out))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for order in ((0, 1), (1, 0), (1, 1, 0)):
+        for i in order:
+            graphs[i][0].replay()
+            there = run[1 - i](stream=side)
+            torch.cuda.synchronize()
+            assert torch.equal(graphs[i][1][0], want[i]) and torch.equal(graphs[i][1][1][0], want[i])
+            assert torch.equal(there, want[1 - i])
+    with torch.cuda.stream(side):  # two graphs at once, each with memory of its own
+        graphs[0][0].replay()
+    graphs[1][0].replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(g[1][0], w) for g, w in zip(graphs, want))
+    bad = []
+
+    def thread(i):
+        for _ in range(20):
+            if not torch.equal(run[i % 2](), want[i % 2]):
+                bad.append(i)
+
+    threads = [threading.Thread(target=thread, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
+
+
+def test_outputs_and_refusals(ql):
+    layer = Layer("int8", 4, 64, 32, seed=5)
+    x = tokens(3, 64, fmt="int8")
+    logits = torch.randn(3, 4, generator=torch.Generator().manual_seed(4)).to(torch.bfloat16).cuda()
+    want = layer(ql, x, router_logits=logits, topk=2)
+    wide = torch.full((5, 96), 3.0, dtype=torch.bfloat16, device="cuda")
+    layer(ql, x, router_logits=logits, topk=2, out=wide[1:4, 16:80])
+    assert torch.equal(wide[1:4, 16:80], want)
+    wide[1:4, 16:80] = 3.0
+    assert (wide == 3.0).all()
+    w13, s13, w2, s2 = layer.args
+    ids, wt = torch.zeros(3, 2, dtype=torch.int32).cuda(), torch.ones(3, 2).cuda()
+    for args, kw in [((x.cpu(), w13, s13, w2, s2), dict(router_logits=logits, topk=2)),
+                     ((x, w13.cpu(), s13, w2, s2), dict(router_logits=logits, topk=2)),
+                     ((x, w13, s13.cpu(), w2, s2), dict(router_logits=logits, topk=2)),
+                     ((x, w13, s13, w2, s2), dict(router_logits=logits.cpu(), topk=2)),
+                     ((x, w13, s13, w2, s2), dict(router_logits=logits.float(), topk=2)),
+                     ((x, w13, s13, w2, s2), dict(topk=2)),
+                     ((x, w13, s13, w2, s2), dict(router_logits=logits, topk_ids=ids, topk_weights=wt)),
+                     ((x, w13, s13, w2, s2), dict(topk_ids=ids)),
+                     ((x, w13, s13, w2, s2), dict(topk_ids=ids.long(), topk_weights=wt)),
+                     ((x, w13, s13, w2, s2), dict(topk_ids=ids[:2], topk_weights=wt)),
+                     ((x, w13[:, :63], s13, w2, s2), dict(router_logits=logits, topk=2)),
+                     ((x, w13, s13[:, :60], w2, s2), dict(router_logits=logits, topk=2)),
+                     ((x, w13, s13, w2[:3], s2), dict(router_logits=logits, topk=2)),
+                     ((x, w13, s13, w2, s2), dict(router_logits=logits, topk=5)),
+                     ((x, w13, s13, w2, s2), dict(router_logits=logits, topk=0)),
+                     ((x, w13, s13, w2, s2), dict(router_logits=logits, topk=2, swiglu_limit=-1.0)),
+                     ((x.t(), w13, s13, w2, s2), dict(router_logits=logits, topk=2)),
+                     ((x[:0], w13, s13, w2, s2), dict(router_logits=logits[:0], topk=2)),
+                     ((x.repeat(22, 1), w13, s13, w2, s2), dict(router_logits=logits.repeat(22, 1), topk=2)),
+                     ((x, w13, s13, w2, s2), dict(router_logits=logits, topk=2, out=wide[:3, :63]))]:
+        with pytest.raises((TypeError, ValueError, ql.QLError)):
+            ql.moe_int8(*args, **kw)
