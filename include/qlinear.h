@@ -507,12 +507,12 @@ QL_API ql_status qlinear_int8(const int8_t* x_q, int64_t M, int64_t K, int64_t l
  *   h = bf16( silu(alpha * min(g, limit)) * clamp(u, -limit, limit) ),  y = bf16( sum_j weight_j W2[e_j] h_j )
  *   moe_bf16: w13 bf16 [E, 2I, H], w2 bf16 [E, H, I]; fp32 sums.
  *   moe_int8: w13 int8 [E, 2I, H] and s13 fp32 [E, 2I], w2 int8 [E, H, I] and s2 fp32 [E, H] (dense);
- *     x is quantised per token and h per pair: scale = max|v| / 127, code = v (127 / max|v|) rounded
- *     half to even in fp32 (within 2^-13 of a tie it may be the other neighbour); exact int32 sums.
- *     A row with an infinity or a NaN gives NaN throughout.
+ *     x is quantised per token and h per pair by quantize_int8's rule (a row whose largest magnitude is
+ *     below 2^-110 counts as zeros); exact int32 sums.  A row with an infinity or a NaN gives NaN
+ *     throughout.
  *   moe_int4: w13 packed codes [E, 2I, ldw13], w2 [E, H, ldw2] with scales and zero points stored as
  *     qlinear_int4's: s13 [E, 2I, lds13], s2 [E, H, lds2], z13, z2 likewise (each NULL: 8).  No weight
- *     is rounded; x and h stay bf16.
+ *     is rounded; x and h stay bf16; values of x of 2^63 and more count as infinite.
  * Experts, rows and scale rows are ld / stride elements apart (packed codes: bytes): w_estride13 is the distance
  * of two experts of w13, and so on.  x: bf16 [M, ldx]; y: bf16 [M, ldy].
  * Requires 1 <= M <= 64, 1 <= topk <= min(E, 16), E <= 1024, H and I at most 32768 and multiples of 8

@@ -4,7 +4,8 @@ and of the linear on 8-bit codes.  numpy only; shares no code with the GPU path.
   pair (m, j) with expert e = ids[m, j] (left out if e is outside [0, E)):
     g = W13[e][:I] x_m, u = W13[e][I:] x_m, h = silu(a min(g, L)) * clamp(u, -L, L)
     y_m = sum_j weights[m, j] W2[e] h_(m, j)
-  codes: scale = max|v| / 127, code = v / scale rounded half to even
+  codes: scale = max|v| / 127, code = v / scale rounded half to even, in fp32 (a quotient of two fp32 values
+  that is rounded to 64 bits first rounds to fp32 as if at once: 53 >= 2 * 24 + 2)
 """
 from __future__ import annotations
 
@@ -14,10 +15,10 @@ from .ffn_oracle import sigmoid
 
 
 def codes(v):
-    """(codes, scale, distance of every v / scale from the nearest tie) of the rows of v."""
-    scale = np.abs(v).max(axis=-1, keepdims=True) / 127.0
-    q = v / np.where(scale > 0, scale, 1.0)
-    return np.rint(q), scale, np.abs(q - np.floor(q) - 0.5)
+    """(codes, scale) of the rows of bf16 values: scale and quotient are fp32, rounded once each."""
+    scale = (np.abs(v).max(axis=-1, keepdims=True) / 127.0).astype(np.float32)
+    q = (v / np.where(scale > 0, scale, 1.0).astype(np.float64)).astype(np.float32)
+    return np.where(scale > 0, np.clip(np.rint(q.astype(np.float64)), -127, 127), 0.0), scale.astype(np.float64)
 
 
 def gate_up(x, w13, ids):

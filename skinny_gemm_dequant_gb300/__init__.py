@@ -802,7 +802,7 @@ def moe_int8(x, w13, s13, w2, s2, *, router_logits=None, topk_ids=None, topk_wei
              swiglu_alpha=1.0, swiglu_limit=None, debug=False, out=None, workspace=None, stream=None):
     """moe_bf16's layer on 8-bit codes: w13 int8 [E, 2I, H] with s13 fp32 [E, 2I], w2 int8 [E, H, I]
     with s2 fp32 [E, H]; H and I multiples of 16.  x is quantised per token and h per (token, expert)
-    inside, scale = max|v| / 127; the sums are exact."""
+    inside, by quantize_int8's rule; the sums are exact."""
     def mats(E, I, H, dev):
         return (*_experts(w13, "w13", E, 2 * I, H, torch.int8, dev), _dense(s13, "s13", (E, 2 * I), torch.float32, dev),
                 *_experts(w2, "w2", E, H, I, torch.int8, dev), _dense(s2, "s2", (E, H), torch.float32, dev))
@@ -818,8 +818,8 @@ def moe_int4(x, w13, s13, w2, s2, z13=None, z2=None, *, group=128, router_logits
              workspace=None, stream=None):
     """moe_bf16's layer on 4-bit weights stored as qlinear_int4's: w13 uint8 [E, 2I, >=H/2], w2 uint8
     [E, H, >=I/2], scales bf16 or fp16 [E, rows, >=ceil(columns/group)], zero points uint8 of the same
-    shape or None: 8; H and I multiples of 32, group a power of two >= 32.  Values of x or h of 2^63 and more
-    count as infinite."""
+    shape or None: 8; H and I multiples of 32, group a power of two >= 32.  Values of x of 2^63 and more count
+    as infinite."""
     def mats(E, I, H, dev):
         scale, u8 = s13.dtype, torch.uint8
         fmt = _SCALE_FORMATS.get(scale)

@@ -5,7 +5,7 @@
 //   DOWN     y_m = bf16( sum_j w_(m,j) W2[e] h_(m,j) )
 //
 // 8-bit weights: tokens (GATE_UP) and h (DOWN) are quantised here, scale = max|v| / 127 over the
-// row, code = v (127 / max|v|) rounded half to even; products of codes are exact in fp32, sums of
+// row, code = v / scale rounded half to even; products of codes are exact in fp32, sums of
 // 1024 k too.  4-bit weights: no weight is rounded, a group's fp32 sum is multiplied by its scale once.
 //
 // Both kernels are persistent, one CTA per SM, and stream every chosen expert's weights once through
@@ -182,6 +182,7 @@ __global__ void __launch_bounds__(kGuWarps * 32, 1)
   l.heads = reinterpret_cast<Entry*>(ring_base);  // the rings are filled later
   l.keys = reinterpret_cast<int*>(l.heads + P);
   __shared__ unsigned s_top[16];
+  __shared__ float s_inv[16];
   __shared__ int s_one, s_next;
 
   if (I8 && threadIdx.x < 16) s_top[threadIdx.x] = 0u;
@@ -216,7 +217,7 @@ __global__ void __launch_bounds__(kGuWarps * 32, 1)
         const int m = on ? i / vecs : 0, v = i - m * vecs, b = v / (XK / 8), c = v % (XK / 8);
         uint4 x = x2[q];
         if constexpr (I8) {
-          const float top = __uint_as_float(s_top[m]), inv = top == 0.f ? 0.f : __fdiv_rn(127.f, top);
+          const float inv = s_inv[m];
           x = make_uint4(quant2(x.x, inv), quant2(x.y, inv), quant2(x.z, inv), quant2(x.w, inv));
         }
         if constexpr (I4) {
@@ -269,6 +270,14 @@ __global__ void __launch_bounds__(kGuWarps * 32, 1)
   }
   if constexpr (!I8) stage_x();
   __syncthreads();
+  if constexpr (I8) {
+    if (threadIdx.x < p.M) {
+      const float top = __uint_as_float(s_top[threadIdx.x]);
+      s_xs[threadIdx.x] = __fdiv_rn(top, 127.f);
+      s_inv[threadIdx.x] = code_factor(top);
+    }
+    __syncthreads();
+  }
   ne = p.M == 1 ? s_one : dispatch<kGuWarps>(p, l, kPerEntry, most);
 
   const int otiles = p.N / 8, total = ne * otiles;
@@ -307,7 +316,6 @@ __global__ void __launch_bounds__(kGuWarps * 32, 1)
 
   if constexpr (I8) {  // (the weights are on their way)
     stage_x();
-    if (threadIdx.x < p.M) s_xs[threadIdx.x] = __fdiv_rn(__uint_as_float(s_top[threadIdx.x]), 127.f);
     __syncthreads();
   }
   Handed& to_down = *reinterpret_cast<Handed*>(p.handed);
@@ -537,7 +545,7 @@ __global__ void __launch_bounds__(dn_warps(FMT) * 32, 1)
     if constexpr (I8) {
       const float top = __uint_as_float(p.amax[i]);
       wt *= __fdiv_rn(top, 127.f);
-      s_inv[i] = top == 0.f ? 0.f : __fdiv_rn(127.f, top);
+      s_inv[i] = code_factor(top);
     }
     s_wt[i] = wt;
   }

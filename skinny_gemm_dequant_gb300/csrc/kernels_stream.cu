@@ -7,7 +7,7 @@
 //   LINEAR   y = (acc x_s) w_s, acc = sum_k x_q w_q  (+ bias after the cast)
 //
 // 8-bit weights: tokens (GATE_UP) and h (DOWN) are quantised here, scale = max|v| / 127 over the
-// row, code = v (127 / max|v|) rounded half to even; products of codes are exact in fp32, sums
+// row, code = v / scale rounded half to even; products of codes are exact in fp32, sums
 // below 2^24 too, and every 1024 k they move to int32: sums are exact.  4-bit weights: q - z is
 // exact in bf16, a group's fp32 sum is multiplied by its scale once.
 #include <cuda_fp16.h>
@@ -139,7 +139,7 @@ __global__ void __launch_bounds__((compute_warps(FMT, NT) + 1) * 32, 1)
         for (int o = 16; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
         if (lane == 0) {
           s_xs[m] = __fdiv_rn(top, 127.f);
-          s_inv[m] = top == 0.f ? 0.f : __fdiv_rn(127.f, top);
+          s_inv[m] = code_factor(top);
         }
       }
     }
@@ -372,7 +372,7 @@ __global__ void __launch_bounds__((compute_warps(FMT, NT) + 1) * 32, 1)
         for (int i = threadIdx.x; i < P; i += W * 32) {
           const float top = __uint_as_float(__ldcg(p.amax + i));
           s_xs[i] = __fdiv_rn(top, 127.f);
-          s_inv[i] = top == 0.f ? 0.f : __fdiv_rn(127.f, top);
+          s_inv[i] = code_factor(top);
         }
         __syncthreads();
         // every CTA has read the maxima once all have counted in: they are zero for the next call

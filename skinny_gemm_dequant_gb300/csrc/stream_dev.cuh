@@ -64,14 +64,26 @@ __device__ __forceinline__ uint4 pair_up(uint4 x) {
   return make_uint4(__byte_perm(x.x, x.z, 0x5410), __byte_perm(x.x, x.z, 0x7632), __byte_perm(x.y, x.w, 0x5410),
                     __byte_perm(x.y, x.w, 0x7632));
 }
-// two bf16 values as whole f16 numbers: v inv + 1536 rounded to a whole number by the conversion
-// (f16 has steps of 1 there), less 1536
-__device__ __forceinline__ uint32_t quant2(uint32_t w, float inv) {
-  const float lo = fmaf(__uint_as_float(w << 16), inv, 1536.f);
-  const float hi = fmaf(__uint_as_float(w & 0xFFFF0000u), inv, 1536.f);
-  uint32_t r;
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(pack_f16x2(lo, hi)), "r"(0x66006600u));
-  return r;
+// 8-bit codes of a row of bf16 values whose largest magnitude is `top`: scale = top / 127, code =
+// v / scale rounded half to even, both IEEE fp32 divisions.  Rounding v f, f = 127 / top, gives the same
+// codes but for ties: with 8-bit mantissas v / top = a / (b 2^s), so v 127 / top is a tie only where b =
+// 254, when all is exact, or v = top / 2, and it is never nearer than 1 / (255 2^s) to a tie otherwise,
+// far more than the error of f.  Which way the quotient of top / 2 falls is asked once, and f moved to
+// the side of 127 / top that falls the same way.
+__device__ __forceinline__ float code_factor(float top) {
+  if (top < 7.7037197775489436e-34f) return 0.f;  // 2^-110: zeros
+  float f = __fdiv_rn(127.f, top);
+  const float off = __fmaf_rn(f, top, -127.f);  // its sign is exact
+  const bool down = __fdiv_rn(0.5f * top, __fdiv_rn(top, 127.f)) < 63.5f;
+  if (down && off >= 0.f) f = __uint_as_float(__float_as_uint(f) - 1u);
+  if (!down && off < 0.f) f = __uint_as_float(__float_as_uint(f) + 1u);
+  return f;  // an infinite row: 0, which its infinities turn into NaN; a NaN stays
+}
+// two bf16 values as whole f16 numbers: v f + 1.5 2^23 is rounded once, to a whole number
+__device__ __forceinline__ uint32_t quant2(uint32_t w, float f) {
+  const float lo = fmaf(__uint_as_float(w << 16), f, 12582912.f) - 12582912.f;
+  const float hi = fmaf(__uint_as_float(w & 0xFFFF0000u), f, 12582912.f) - 12582912.f;
+  return pack_f16x2(lo, hi);
 }
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   uint32_t r;

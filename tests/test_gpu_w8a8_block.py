@@ -55,12 +55,12 @@ def test_block(ql, weights, M):
     assert np.array_equal(ids.cpu().numpy(), rid)
     # the layer on the block's own activations, in 64 bits: 8-bit h is 0.4 % of its row's largest a step, of
     # which rounding moves half at most; 2 % of y's norm is far above that and far below a wrong expert
-    qm, sm, _ = MO.codes(mixed.double().cpu().numpy())
+    qm, sm = MO.codes(mixed.double().cpu().numpy())
     w13 = w["w13"].double().cpu().numpy() * s["w13"].double().cpu().numpy()[..., None]
     w2 = w["w2"].double().cpu().numpy() * s["w2"].double().cpu().numpy()[..., None]
     g, u, G, U = MO.gate_up(qm * sm, w13, rid)
     h, _ = MO.activation(g, u, 0 * G, 0 * U)
-    hq, hs, _ = MO.codes(h)
+    hq, hs = MO.codes(h)
     ref, _ = MO.down(hq * hs, w2, rid, rw)
     assert np.linalg.norm(y.double().cpu().numpy() - ref) < 0.02 * np.linalg.norm(ref)
     graph = torch.cuda.CUDAGraph()

@@ -7,11 +7,10 @@ from oracle import moe_few_oracle as MO
 
 
 def test_codes_by_hand():
-    q, s, tie = MO.codes(np.array([[12.7, -6.35, 0.05, 0.0], [0.0, 0.0, 0.0, 0.0], [254.0, 1.0, 3.0, -5.0]]))
+    q, s = MO.codes(np.array([[12.7, -6.35, 0.05, 0.0], [0.0, 0.0, 0.0, 0.0], [254.0, 1.0, 3.0, -5.0]]))
     assert np.allclose(s[:, 0], [0.1, 0.0, 2.0])
     assert np.array_equal(q[1], [0, 0, 0, 0])
     assert np.array_equal(q[2], [127, 0, 2, -2])  # .5, 1.5, -2.5: to even
-    assert np.array_equal(tie[2], [0.5, 0, 0, 0])
     assert q[0, 0] == 127 and q[0, 3] == 0
 
 
