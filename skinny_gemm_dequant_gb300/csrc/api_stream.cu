@@ -117,10 +117,12 @@ ql_status moe_run(int fmt, const Moe& a, const Matrix& w13, const Matrix& w2, St
   dn.N = (int)a.H;
   dn.y = a.y;
   dn.ldy = a.ldy;
-  const bool few = moe_few_takes(fmt, gu);
-  cudaError_t e = few ? launch_moe_few(fmt, STREAM_GATE_UP, gu, st) : launch_stream(fmt, STREAM_GATE_UP, gu, st);
+  auto launch = [&](int mode, const StreamArgs& args) {
+    return moe_few_takes(fmt, mode, gu) ? launch_moe_few(fmt, mode, args, st) : launch_stream(fmt, mode, args, st);
+  };
+  cudaError_t e = launch(STREAM_GATE_UP, gu);
   if (e != cudaSuccess) return cuda_status(e);
-  e = few ? launch_moe_few(fmt, STREAM_DOWN, dn, st) : launch_stream(fmt, STREAM_DOWN, dn, st);
+  e = launch(STREAM_DOWN, dn);
   if (e != cudaSuccess) {
     // the maxima that GATE_UP left are not taken back: what is zero between calls is made so
     cudaMemsetAsync(gu.amax, 0, (size_t)a.M * a.topk * 4, st);

@@ -26,13 +26,16 @@ namespace ql {
 namespace {
 
 constexpr int kGuWarps = 16;
-constexpr int kMaxTokens = 16, kMaxPairs = kMaxTokens * kMoeMaxTopk;
+constexpr int kMaxTokens = 16, kMaxPairs = kMaxTokens * kMoeMaxTopk;  // of DOWN
 constexpr int kPerEntry = 8;  // pairs: one token tile of GATE_UP
 constexpr int R = kStreamRows;
 constexpr int kPitch = R + 4;  // of a column of sums: lanes (g, t) write 8 t + g, all banks once
 constexpr int kSmem = 226 * 1024;
 constexpr int kStage = 16 * 128, kDepth = 4;  // a ring of GATE_UP: bytes of a stage, stages
-constexpr int kMaxX = kSmem - kGuWarps * kDepth * kStage - 4352;  // for the tokens of GATE_UP; the lists take 4 KB
+// shared memory of GATE_UP for lists; the tokens have the rest
+__host__ __device__ constexpr int gu_list_bytes(int pairs) {
+  return (pairs * 16 + kMoeMaxTokens * 4 + 127) & ~127;  // entries, ids, sorted pairs and tokens; scales
+}
 
 __host__ __device__ constexpr int dn_warps(int fmt) { return fmt == STREAM_INT4 ? 12 : 8; }
 __host__ __device__ constexpr int gu_k(int fmt) { return fmt == STREAM_INT4 ? 256 : fmt == STREAM_INT8 ? 128 : 64; }
@@ -47,19 +50,18 @@ struct Lists {
   int* keys;       // scratch
 };
 
-// what GATE_UP hands to DOWN beside h: the lists and the weights
+// what GATE_UP hands to DOWN beside h: the weights by pair and, up to kMaxTokens, the lists
 struct Handed {
+  float weight[kMoeMaxTokens * kMoeMaxTopk];
   int entries, most, pad[2];
   Entry entry[kMaxPairs];
   uint16_t pair[kMaxPairs], tok[kMaxPairs];
-  float weight[kMaxPairs];  // by pair
 };
 
-template <int WARPS>
-__device__ __forceinline__ void route(const StreamArgs& p, const Lists& l) {
+__device__ __forceinline__ void route(const StreamArgs& p, const Lists& l, int warps) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 #pragma unroll 1
-  for (int m = warp; m < p.M; m += WARPS) {
+  for (int m = warp; m < p.M; m += warps) {
     int id = -1;
     float wt;
     if (p.logits)
@@ -109,13 +111,21 @@ __device__ __forceinline__ int dispatch(const StreamArgs& p, const Lists& l, int
   for (int i = threadIdx.x; i < P; i += WARPS * 32) {
     const int key = l.keys[i];
     int before = 0, rank = 0, all = 0;
-#pragma unroll 4
-    for (int j = 0; j < P; ++j) {
-      const int o = l.keys[j];
+    auto meet = [&](int o, int j) {
       before += o < key;
       all += o == key;
       rank += o == key && j < i;
+    };
+    int j = 0;
+#pragma unroll 2
+    for (; j + 4 <= P; j += 4) {
+      const int4 o = *reinterpret_cast<const int4*>(l.keys + j);
+      meet(o.x, j);
+      meet(o.y, j + 1);
+      meet(o.z, j + 2);
+      meet(o.w, j + 3);
     }
+    for (; j < P; ++j) meet(l.keys[j], j);
     l.pair[before + rank] = (uint16_t)i;
     l.tok[before + rank] = (uint16_t)(i / p.topk);
     const bool head = key != kNone && rank % per_entry == 0;
@@ -177,22 +187,22 @@ __global__ void __launch_bounds__(kGuWarps * 32, 1)
   l.entries = reinterpret_cast<Entry*>(smem + x_bytes);
   l.ids = reinterpret_cast<int*>(l.entries + P);
   float* s_xs = reinterpret_cast<float*>(l.ids + P);
-  l.pair = reinterpret_cast<uint16_t*>(s_xs + 16);
+  l.pair = reinterpret_cast<uint16_t*>(s_xs + kMoeMaxTokens);
   l.tok = l.pair + P;
-  l.heads = reinterpret_cast<Entry*>(ring_base);  // the rings are filled later
-  l.keys = reinterpret_cast<int*>(l.heads + P);
-  __shared__ unsigned s_top[16];
-  __shared__ float s_inv[16];
+  l.keys = reinterpret_cast<int*>(ring_base);  // the rings are filled later
+  l.heads = reinterpret_cast<Entry*>(l.keys + (P + 3) / 4 * 4);
+  __shared__ unsigned s_top[kMoeMaxTokens];
+  __shared__ float s_inv[kMoeMaxTokens];
   __shared__ int s_one, s_next;
 
-  if (I8 && threadIdx.x < 16) s_top[threadIdx.x] = 0u;
+  if (I8 && threadIdx.x < kMoeMaxTokens) s_top[threadIdx.x] = 0u;
   if (threadIdx.x == 0) s_next = 0;
   __syncthreads();
   pdl_wait();
   pdl_launch_dependents();
 
   // the first warps route, the others take x meanwhile
-  const int routing = min(p.M, kGuWarps / 2), vecs = nxb * (XK / 8);
+  const int routing = p.M <= kGuWarps ? min(p.M, kGuWarps / 2) : kGuWarps, vecs = nxb * (XK / 8);
   const int chunks = (vecs * p.M + 63) / 64;
   auto stage_x = [&]() {
     // a warp takes the next 64 pieces, so that those that route join in later; pieces of a token are
@@ -264,9 +274,13 @@ __global__ void __launch_bounds__(kGuWarps * 32, 1)
     if (p.M == 1)
       s_one = route_one(p, l);
     else
-      route<kGuWarps / 2>(p, l);
-  } else if constexpr (I8) {
-    top_x(threadIdx.x - routing * 32, (kGuWarps - routing) * 32);
+      route(p, l, routing);
+  }
+  if constexpr (I8) {
+    if (routing == kGuWarps)
+      top_x(threadIdx.x, kGuWarps * 32);
+    else if (warp >= routing)
+      top_x(threadIdx.x - routing * 32, (kGuWarps - routing) * 32);
   }
   if constexpr (!I8) stage_x();
   __syncthreads();
@@ -319,7 +333,7 @@ __global__ void __launch_bounds__(kGuWarps * 32, 1)
     __syncthreads();
   }
   Handed& to_down = *reinterpret_cast<Handed*>(p.handed);
-  if (blockIdx.x == gridDim.x - 1 && warp == kGuWarps - 2) {
+  if (p.M <= kMaxTokens && blockIdx.x == gridDim.x - 1 && warp == kGuWarps - 2) {
     if (lane == 0) {
       to_down.entries = ne;
       to_down.most = most;
@@ -556,9 +570,7 @@ __global__ void __launch_bounds__(dn_warps(FMT) * 32, 1)
       reinterpret_cast<uint16_t*>(p.y)[(int64_t)(i / p.N) * p.ldy + i % p.N] = 0;
     return;
   }
-  // equal shares; a short tile stays in one CTA, which is cheaper than joining its parts
-  int share = (total + gridDim.x - 1) / gridDim.x;
-  if (share < whole && whole <= 2 * W) share = whole;
+  const int share = unit_share(total, whole, W);
   const int u0 = min(total, (int)blockIdx.x * share), u1 = min(total, u0 + share);
   auto bound = [&](int w) { return u0 + (u1 - u0) * w / W; };  // (at most 2^26 units a CTA)
   const int v0 = bound(warp), v1 = bound(warp + 1);
@@ -987,15 +999,13 @@ __global__ void __launch_bounds__(dn_warps(FMT) * 32, 1)
   }
   if (!s_last[0] && !s_last[1]) return;
   __threadfence();  // the other parts were fenced before their counts
+  const int quads = p.M * (R / 4);  // four rows of a token each
 #pragma unroll 1
-  for (int i = threadIdx.x; i < 2 * p.M * R; i += THREADS) {
-    const int which = i >= p.M * R, at = i - which * p.M * R;
+  for (int i = threadIdx.x; i < 2 * quads; i += THREADS) {
+    const int which = i >= quads, at = i - which * quads;
     if (!s_last[which]) continue;
-    const int tile = which ? tile1 : tile0, c0 = tile * whole / share, c1 = ((tile + 1) * whole - 1) / share;
-    float v = 0.f;
-#pragma unroll 4
-    for (int q = c0; q <= c1; ++q) v += __ldcg(slot_of(q, q == c0) + at);
-    put(tile, at, v);
+    const int tile = which ? tile1 : tile0;
+    put4(p, tile, at, add_parts(slot_of, tile * whole / share, ((tile + 1) * whole - 1) / share, at));
   }
 }
 
@@ -1005,7 +1015,7 @@ cudaError_t launch_gu(const StreamArgs& a, int x_bytes, cudaStream_t st) {
   static OncePerDevice once;
   if (const cudaError_t e = raise_smem_limit(kfn, once); e != cudaSuccess) return e;
   const int P = a.M * a.topk;
-  const int lists = (P * (int)(sizeof(Entry) + 4 + 4) + 64 + 127) & ~127;
+  const int lists = gu_list_bytes(P);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(kNumSMs, 1, 1);
   cfg.blockDim = dim3(kGuWarps * 32, 1, 1);
@@ -1060,8 +1070,10 @@ int64_t gu_x_bytes(int fmt, const StreamArgs& a) {
 
 static_assert(sizeof(Handed) <= kMoeHandedBytes, "workspace");
 
-bool moe_few_takes(int fmt, const StreamArgs& gate_up) {
-  return gate_up.M <= kMaxTokens && gu_x_bytes(fmt, gate_up) <= kMaxX;
+bool moe_few_takes(int fmt, int mode, const StreamArgs& gate_up) {
+  const int P = gate_up.M * gate_up.topk;
+  if (mode == STREAM_DOWN && gate_up.M > kMaxTokens) return false;
+  return gu_x_bytes(fmt, gate_up) + gu_list_bytes(P) + kGuWarps * kDepth * kStage <= kSmem;
 }
 
 cudaError_t launch_moe_few(int fmt, int mode, const StreamArgs& a, cudaStream_t st) {

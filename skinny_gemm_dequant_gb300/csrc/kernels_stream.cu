@@ -193,9 +193,7 @@ __global__ void __launch_bounds__((compute_warps(FMT, NT) + 1) * 32, 1)
   const int tiles = (p.N + OUT - 1) / OUT;
   const int whole = (DN ? ne : 1) * nblk;  // units whose sums meet before the epilogue
   const int total = tiles * ne * nblk;
-  // equal shares; a short item stays in one CTA, which is cheaper than joining its parts
-  int share = (total + gridDim.x - 1) / gridDim.x;
-  if (share < whole && whole <= 2 * W) share = whole;
+  const int share = unit_share(total, whole, W);
   const int u0 = min(total, (int)blockIdx.x * share), u1 = min(total, u0 + share);
 
   auto entry = [&](int a) {
@@ -625,7 +623,8 @@ __global__ void __launch_bounds__((compute_warps(FMT, NT) + 1) * 32, 1)
       const auto en = entry(c.a);
       const int b = (it - item0) % buffers;
       bar_sync<kFull, THREADS>(b);
-      const int ua = max(u0, it * nblk), units = min(min(u1, (it + 1) * nblk) - ua, W), w0 = (ua - u0) % W;
+      const int ua = max(u0, it * nblk);
+      int units = min(min(u1, (it + 1) * nblk) - ua, W), w0 = (ua - u0) % W;
       const Sum* sums = reinterpret_cast<const Sum*>(smem + lay.lists + b * buffer) + lane;
       auto own = [&](int k, Sum (&v)[2]) {  // the sums of this CTA's warps
         v[0] = v[1] = 0;
@@ -651,6 +650,30 @@ __global__ void __launch_bounds__((compute_warps(FMT, NT) + 1) * 32, 1)
           __stcg(mine + k * R + 32, v[1]);
         }
         ready = last_part(it * nblk, (it + 1) * nblk);
+        if (ready) {
+          // the sums go where the first warp left its own
+          const int c0 = it * nblk / share, c1 = ((it + 1) * nblk - 1) / share;
+          Sum v[TT][2] = {};
+#pragma unroll 1
+          for (int q = c0; q <= c1; ++q) {
+            const Sum* s = reinterpret_cast<const Sum*>(slot_of(q, q == c0)) + lane;
+#pragma unroll
+            for (int k = 0; k < TT; ++k)
+              if (k < en.count) {
+                v[k][0] += __ldcg(s + k * R);
+                v[k][1] += __ldcg(s + k * R + 32);
+              }
+          }
+          Sum* to = const_cast<Sum*>(sums);
+#pragma unroll
+          for (int k = 0; k < TT; ++k)
+            if (k < en.count) {
+              to[k * kPitch] = v[k][0];
+              to[k * kPitch + 32] = v[k][1];
+            }
+          units = 1;
+          w0 = 0;
+        }
       }
       const int n = c.tile * OUT + lane;
       float ws[2] = {1.f, 1.f}, bias[2] = {};
@@ -667,18 +690,7 @@ __global__ void __launch_bounds__((compute_warps(FMT, NT) + 1) * 32, 1)
 #pragma unroll 1
       for (int k = 0; k < en.count && ready; ++k) {
         Sum v[2];
-        if (parts) {
-          const int c0 = it * nblk / share, c1 = ((it + 1) * nblk - 1) / share;
-          v[0] = v[1] = 0;
-#pragma unroll 4
-          for (int q = c0; q <= c1; ++q) {
-            const Sum* s = reinterpret_cast<const Sum*>(slot_of(q, q == c0)) + k * R + lane;
-            v[0] += __ldcg(s);
-            v[1] += __ldcg(s + 32);
-          }
-        } else {
-          own(k, v);
-        }
+        own(k, v);
         float f[2] = {(float)v[0], (float)v[1]};
         if constexpr (GU) {
           const int pair = s_pair[en.first + k];
@@ -730,47 +742,56 @@ __global__ void __launch_bounds__((compute_warps(FMT, NT) + 1) * 32, 1)
       if (it + buffers <= item1) bar_arrive<kEmpty, THREADS>(b);
       if (DN && (it == item1 || c.a == ne - 1)) {
         // the end of this CTA's part of the tile
-        const int a = c.tile * whole, z = a + whole;
-        const bool shared = a < u0 || z > u1;
-        const int c0 = a / share, c1 = (z - 1) / share;
+        const int a = c.tile * whole;
+        const bool shared = a < u0 || a + whole > u1;
         float4* y4 = reinterpret_cast<float4*>(s_y);
-        bool write = true;
-        if (shared) {
-          float4* mine = reinterpret_cast<float4*>(slot_of(blockIdx.x, a >= u0));
-          __syncwarp();
-          for (int i = lane; i < p.M * (R / 4); i += 32) __stcg(mine + i, y4[i]);
-          write = last_part(a, z);
-        }
-        if (write) {
-          // four rows of a token a lane; the parts' loads go out together
-#pragma unroll 1
-          for (int i = lane; i < p.M * (R / 4); i += 32) {
-            float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (shared) {
-#pragma unroll 4
-              for (int q = c0; q <= c1; ++q) {
-                const float4 v = __ldcg(reinterpret_cast<const float4*>(slot_of(q, q == c0)) + i);
-                y = make_float4(y.x + v.x, y.y + v.y, y.z + v.z, y.w + v.w);
-              }
-            } else {
-              y = y4[i];
-            }
-            const int row = c.tile * R + i % (R / 4) * 4;
-            uint16_t* dst = reinterpret_cast<uint16_t*>(p.y) + (int64_t)(i / (R / 4)) * p.ldy + row;
-            const float v[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              if (row + j < p.N) dst[j] = f32_to_bf16_rn(v[j]);
-          }
-        }
         __syncwarp();
-        for (int i = lane; i < p.M * (R / 4); i += 32) y4[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i = lane; i < p.M * (R / 4); i += 32) {
+          if (shared)
+            __stcg(reinterpret_cast<float4*>(slot_of(blockIdx.x, a >= u0)) + i, y4[i]);
+          else
+            put4(p, c.tile, i, y4[i]);
+          y4[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
         __syncwarp();
       }
       c.next(nblk, nblk, ne);
     }
   }
+  if constexpr (DN) {
+    // At most two tiles, the first and the last, have parts in other CTAs: the last CTA of each adds the
+    // parts in the order of K
+    __shared__ int s_last[2];
+    auto slot_of = [&](int cta, int tail) { return p.slots + ((int64_t)cta * 2 + tail) * (p.M * R); };
+    const int tile0 = u0 / whole, tile1 = u1 > u0 ? (u1 - 1) / whole : tile0 - 1;
+    const bool cut0 = tile0 <= tile1 && (tile0 * whole < u0 || (tile0 + 1) * whole > u1);
+    const bool cut1 = tile1 > tile0 && (tile1 + 1) * whole > u1;
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x < 64 && lane == 0) {
+      const int tile = warp ? tile1 : tile0;
+      bool last = false;
+      if (warp ? cut1 : cut0) {
+        const int c0 = tile * whole / share, c1 = ((tile + 1) * whole - 1) / share;
+        last = atomicAdd(p.tickets + c0, 1u) == (unsigned)(c1 - c0);
+        if (last) p.tickets[c0] = 0u;
+      }
+      s_last[warp] = last;
+    }
+    __syncthreads();
+    if (!s_last[0] && !s_last[1]) return;
+    __threadfence();  // the other parts were fenced before their counts
+    const int quads = p.M * (R / 4);
+#pragma unroll 1
+    for (int i = threadIdx.x; i < 2 * quads; i += THREADS) {
+      const int which = i >= quads, at = i - which * quads;
+      if (!s_last[which]) continue;
+      const int tile = which ? tile1 : tile0;
+      put4(p, tile, at, add_parts(slot_of, tile * whole / share, ((tile + 1) * whole - 1) / share, at));
+    }
+  }
 }
+
 
 template <int FMT, int MODE, int NT, bool FINE, bool ZP>
 cudaError_t launch(const StreamArgs& a, cudaStream_t st) {

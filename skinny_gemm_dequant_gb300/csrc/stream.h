@@ -53,8 +53,9 @@ struct StreamArgs {
 };
 
 cudaError_t launch_stream(int fmt, int mode, const StreamArgs& a, cudaStream_t st);
-// the launches for up to 16 tokens (kernels_moe_few.cu), where they take a call's GATE_UP
-bool moe_few_takes(int fmt, const StreamArgs& gate_up);
+// the launches of kernels_moe_few.cu, where they take a call: GATE_UP while the tokens fit in shared memory,
+// DOWN up to 16 of these tokens
+bool moe_few_takes(int fmt, int mode, const StreamArgs& gate_up);
 cudaError_t launch_moe_few(int fmt, int mode, const StreamArgs& a, cudaStream_t st);
 size_t stream_slot_bytes(int64_t M);
 // of QL_OP_INT8_CODES and QL_OP_MOE_FEW (api_stream.cu)

@@ -4,6 +4,7 @@
 #include <cuda_fp16.h>
 
 #include "common.cuh"
+#include "stream.h"
 
 namespace ql {
 
@@ -96,6 +97,37 @@ __device__ __forceinline__ void mma_first(float (&d)[4], uint32_t a0, uint32_t a
   asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+// Units of a CTA, of `total` that are cut into equal shares; `whole` units' sums meet before a result.  A
+// share has a unit for each of the CTA's warps, which take them at once (fewer would only make more parts
+// to join), and whole results where those are short.
+__device__ __forceinline__ int unit_share(int total, int whole, int warps) {
+  if (total == 0) return 1;
+  int share = max((total + (int)gridDim.x - 1) / (int)gridDim.x, min(warps, whole));
+  if (whole <= 2 * warps) share = (share + whole - 1) / whole * whole;
+  return share;
+}
+
+// the parts c0..c1 of a DOWN tile, in the order of K: quad `at` (four rows of a token)
+template <class Slot>
+__device__ __forceinline__ float4 add_parts(Slot slot_of, int c0, int c1, int at) {
+  float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+  for (int q = c0; q <= c1; ++q) {
+    const float4 v = __ldcg(reinterpret_cast<const float4*>(slot_of(q, q == c0)) + at);
+    y = make_float4(y.x + v.x, y.y + v.y, y.z + v.z, y.w + v.w);
+  }
+  return y;
+}
+__device__ __forceinline__ void put4(const StreamArgs& p, int tile, int at, float4 y) {
+  constexpr int Q = kStreamRows / 4;
+  const int row = tile * kStreamRows + at % Q * 4;
+  uint16_t* dst = reinterpret_cast<uint16_t*>(p.y) + (int64_t)(at / Q) * p.ldy + row;
+  const float v[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (row + j < p.N) dst[j] = f32_to_bf16_rn(v[j]);
 }
 
 }  // namespace ql
