@@ -252,14 +252,17 @@ __global__ void __launch_bounds__(kGuWarps * 32, 1)
       }
     }
   };
-  auto top_x = [&](int first, int step) {
+  auto top_x = [&](int first, int warps) {
+    // a warp takes a token, or where they are few a segment of one
+    const int segments = max(1, warps / p.M), vecs_row = p.K / 8;
 #pragma unroll 1
-    for (int m = 0; m < p.M; ++m) {
+    for (int i = first; i < p.M * segments; i += warps) {
+      const int m = i / segments, s = i - m * segments;
       float top = 0.f;
-#pragma unroll 2
-      for (int i = first; i < p.K / 8; i += step) {
-        const uint4 v = *reinterpret_cast<const uint4*>(p.x + m * p.ldx + i * 16);
-        const uint32_t q[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll 4
+      for (int v = vecs_row * s / segments + lane; v < vecs_row * (s + 1) / segments; v += 32) {
+        const uint4 x = *reinterpret_cast<const uint4*>(p.x + m * p.ldx + v * 16);
+        const uint32_t q[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           top = max_nan(max_nan(top, fabsf(__uint_as_float(q[j] << 16))), fabsf(__uint_as_float(q[j] & 0xFFFF0000u)));
@@ -278,9 +281,9 @@ __global__ void __launch_bounds__(kGuWarps * 32, 1)
   }
   if constexpr (I8) {
     if (routing == kGuWarps)
-      top_x(threadIdx.x, kGuWarps * 32);
+      top_x(warp, kGuWarps);
     else if (warp >= routing)
-      top_x(threadIdx.x - routing * 32, (kGuWarps - routing) * 32);
+      top_x(warp - routing, kGuWarps - routing);
   }
   if constexpr (!I8) stage_x();
   __syncthreads();
