@@ -169,7 +169,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   // have finished, the stage and its A buffer are free
   __shared__ uint64_t full_w[kStages], full_x[kStages], empty[kStages], ready[kABufs], dfull[2], dempty[2], done;
   __shared__ uint32_t s_tmem;
-  __shared__ int s_abort, s_issued, s_last;
+  __shared__ int s_abort, s_issued, s_ahead, s_last;
   __shared__ float s_xs[kMaxWidth];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -210,7 +210,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   __syncthreads();
   cluster_sync_all();
   tc_fence_after();
-  pdl_wait();
+  // What the launch before (codes_f16_kernel, which has waited for everything earlier) writes is the
+  // tokens alone: only their loads wait for it
   pdl_launch_dependents();
   const uint32_t tmem = s_tmem;
   auto fail = [&]() {
@@ -224,10 +225,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (warp == 0) {
       // ---------------------------------------------------------- producer
       const bool leader = elect_one();
-      int s = 0, issued = 0;
-      uint32_t ph = 1;  // the first pass over the stages finds them empty
+      int s = 0, issued = 0, ahead = 0;  // ahead: stages whose weights are under way
+      uint32_t ph = 1;                   // the first pass over the stages finds them empty
       bool ok = true;
       int t, k0, k1;
+      auto stage_at = [&](int i) { return smem_raw + (base - smem_u32(smem_raw)) + (size_t)i * kStageBytes; };
+      auto load_w = [&](int i, int kt, int rw) {
+        mbar_arrive_expect_tx(&full_w[i], kWBytes);
+        tma_load_2d(stage_at(i), &tmW, kt * kStageK, rw, &full_w[i]);
+      };
+      for (Walk w(p, pair); ahead < kStages && w.next(p, t, k0, k1);) {
+        int tn, tm;
+        tile_at(p, t, tn, tm);
+        for (int kt = k0; kt < k1 && ahead < kStages; ++kt, ++ahead)
+          if (leader) load_w(ahead, kt, tn * 256 + (int)rank * 128);
+      }
+      __syncwarp();
+      pdl_wait();
       for (Walk w(p, pair); ok && w.next(p, t, k0, k1);) {
         int tn, tm;
         tile_at(p, t, tn, tm);
@@ -239,13 +253,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             break;
           }
           if (leader) {
-            const uint32_t bar = in_cta(smem_u32(&full_x[s]), 0);
-            uint8_t* at = smem_raw + (base - smem_u32(smem_raw)) + (size_t)s * kStageBytes;
-            mbar_arrive_expect_tx(&full_w[s], kWBytes);
+            const uint32_t bar = in_cta(smem_u32(&full_x[s]), 0), at = smem_u32(stage_at(s));
+            if (issued >= ahead) load_w(s, kt, rw);
             if (rank == 0) mbar_arrive_expect_tx(&full_x[s], 4 * x_bytes);
-            tma_load_2d(at, &tmW, kt * kStageK, rw, &full_w[s]);
-            load_pair(smem_u32(at) + kWBytes, &tmX, kt * kStageK, rx, bar);
-            load_pair(smem_u32(at) + kWBytes + kXTile, &tmX, kt * kStageK + 64, rx, bar);
+            load_pair(at + kWBytes, &tmX, kt * kStageK, rx, bar);
+            load_pair(at + kWBytes + kXTile, &tmX, kt * kStageK + 64, rx, bar);
           }
           __syncwarp();
           ++issued;
@@ -265,7 +277,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       }
       if (ok && !wait2_warp(&done, 0, lim, abort) && leader) fail();
-      if (leader) s_issued = issued;
+      if (leader) {
+        s_issued = issued;
+        s_ahead = ahead;
+      }
     } else if (warp == 1 && rank == 0) {
       // ---------------------------------------------------------- MMA issue
       const bool leader = elect_one();
@@ -333,6 +348,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else if (warp < 12) {
     // ------------------------------------------------------------ int32 sums, results
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSums) : "memory");
+    pdl_wait();  // scales are read, results written
     const int q = warp & 3, half = (warp - 4) >> 2;  // tensor-memory lane quadrant, column half
     const int r = 32 * q + lane;                     // row of this CTA's 128
     const int cols = p.width / 2;                    // of a thread
@@ -518,7 +534,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // half's arrival or bytes are supplied here
     if (threadIdx.x == 0) {
       wait2(&done, 0, kDrainLimit, nullptr);  // no product is reading them
-      const int mine = s_issued;
+      const int mine = s_issued > s_ahead ? s_issued : s_ahead;
       for (int i = mine > kStages ? mine - kStages : 0; i < mine; ++i)
         wait2(&full_w[i % kStages], (uint32_t)(i / kStages) & 1, kDrainLimit, nullptr);
     }
