@@ -470,7 +470,8 @@ QL_API ql_status gated_ffn_int4(const uint16_t* x, int64_t M, int64_t H, int64_t
 /*
  * 8-bit codes of tokens, by the rule of qlinear_int8_w8a8, for projections that share them:
  *   scale[m] = max_k |x[m,k]| / 127,  codes[m,k] = clamp(round_half_even(x[m,k] / scale[m]), -127, 127)
- * (IEEE fp32 divisions; an all-zero token has scale 0 and codes 0.)  x: bf16 [M, ldx]; codes: int8
+ * (IEEE fp32 divisions; an all-zero token has scale 0 and codes 0; one with an infinity or a NaN has
+ * that for its scale, and codes of no meaning.)  x: bf16 [M, ldx]; codes: int8
  * [M, K] dense; scale: fp32 [M].
  * Requires 1 <= M <= 2^22, K >= 8, K % 8 == 0, K <= 2^20, ldx >= K, ldx % 8 == 0, 16-byte aligned x
  * and codes.

@@ -158,8 +158,7 @@ ql_status quantize_int8(const uint16_t* x, int64_t M, int64_t K, int64_t ldx, in
   if (!x || !codes || !scale || M < 1 || K < 1 || ldx < K) return QL_ERR_INVALID_ARG;
   if (M > (1 << 22) || K > (1 << 20) || K % 8 != 0) return QL_ERR_UNSUPPORTED;
   if (!aligned<16>(x) || !aligned<16>(codes) || !aligned<4>(scale) || ldx % 8 != 0) return QL_ERR_ALIGNMENT;
-  return cuda_status(
-      launch_quant_int8(x, (int)M, (int)K, ldx, codes, scale, nullptr, nullptr, (cudaStream_t)stream));
+  return cuda_status(launch_token_codes(x, M, K, ldx, codes, scale, (cudaStream_t)stream));
 }
 
 ql_status qlinear_int8(const int8_t* x_q, int64_t M, int64_t K, int64_t ldx, const float* x_scale, const int8_t* w,

@@ -52,6 +52,9 @@ struct StreamArgs {
   const float* x_scale;  // LINEAR: [M]
 };
 
+// codes and scales of tokens (kernels_codes.cu)
+cudaError_t launch_token_codes(const uint16_t* x, int64_t M, int64_t K, int64_t ldx, int8_t* codes, float* scale,
+                               cudaStream_t st);
 cudaError_t launch_stream(int fmt, int mode, const StreamArgs& a, cudaStream_t st);
 // the launches of kernels_moe_few.cu, where they take a call: GATE_UP while the tokens fit in shared memory,
 // DOWN up to 16 of these tokens

@@ -92,6 +92,31 @@ def test_quantize(ql, M, K):
     assert np.array_equal(q.cpu().numpy(), codes)
 
 
+@pytest.mark.parametrize("K", [2048, 4104, 9000, 20000])
+def test_quantize_ties_and_small_rows(ql, K):
+    """Every mantissa as the row's largest: halves of it are ties, and for some all odd mantissas are; rows
+    down to the smallest numbers."""
+    g = torch.Generator().manual_seed(K)
+    x = torch.randn(300, K, generator=g).clamp(-2, 2).to(torch.bfloat16)
+    top = torch.arange(128, 256).repeat(3)[:300].to(torch.float32) / 64
+    x[:, 5] = top.to(torch.bfloat16)
+    x[:, 6::11] = (top / 2).to(torch.bfloat16)[:, None]
+    x[:, 7::11] = -(top / 2).to(torch.bfloat16)[:, None]
+    x[260:] = (x[260:].double() * 2.0 ** -torch.arange(90, 130)[:, None]).to(torch.bfloat16)
+    q, s = ql.quantize_int8(x.cuda())
+    v = x.float().numpy()
+    scale = np.abs(v).max(axis=1) / np.float32(127)
+    assert np.array_equal(s.cpu().numpy(), scale)
+    assert np.array_equal(q.cpu().numpy(), np.clip(np.rint(v / scale[:, None]), -127, 127).astype(np.int8))
+
+
+def test_quantize_tells_of_nan_and_infinity(ql):
+    x = torch.ones(3, 64, dtype=torch.bfloat16)
+    x[0, 9], x[2, 63] = float("nan"), -float("inf")
+    s = ql.quantize_int8(x.cuda())[1].cpu()
+    assert s[0].isnan() and s[1] == np.float32(1) / np.float32(127) and s[2].isinf()
+
+
 @pytest.mark.parametrize("M", [1, 5, 16, 30, 260])
 def test_same_as_the_linear_that_quantises_itself(ql, M):
     g = torch.Generator().manual_seed(M)
