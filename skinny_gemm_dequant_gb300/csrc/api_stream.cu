@@ -14,7 +14,6 @@ namespace {
 
 constexpr size_t kTicketOff = 256;          // the zero region of every workspace: tickets,
 constexpr size_t kAmaxOff = 256 + 4096;     // then the rows' maxima of moe_int8
-static_assert(kMoeMaxTokens * kMoeMaxTopk * 4 <= kMoeHandedBytes, "weights");
 static_assert((kNumSMs + 1) * 4 <= 4096 && kMoeMaxTokens * kMoeMaxTopk * 4 <= (1 << 20) - 4096, "zero region");
 
 template <int N>
@@ -91,7 +90,8 @@ StreamArgs moe_args(const Moe& a) {
   s.amax = at<unsigned>(a.ws, kAmaxOff);
   s.slots = at<float>(a.ws, workspace_zero_bytes());
   s.handed = at<uint8_t>(a.ws, workspace_zero_bytes() + al256(stream_slot_bytes(a.M)));
-  s.h = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(s.handed) + kMoeHandedBytes);
+  s.heads = reinterpret_cast<float*>(static_cast<uint8_t*>(s.handed) + kMoeHandedBytes);
+  s.h = reinterpret_cast<uint16_t*>(reinterpret_cast<uint8_t*>(s.heads) + al256(down_head_bytes(a.M)));
   s.ldh = cdiv(a.I, 8) * 8;
   return s;
 }
@@ -117,12 +117,9 @@ ql_status moe_run(int fmt, const Moe& a, const Matrix& w13, const Matrix& w2, St
   dn.N = (int)a.H;
   dn.y = a.y;
   dn.ldy = a.ldy;
-  auto launch = [&](int mode, const StreamArgs& args) {
-    return moe_few_takes(fmt, mode, gu) ? launch_moe_few(fmt, mode, args, st) : launch_stream(fmt, mode, args, st);
-  };
-  cudaError_t e = launch(STREAM_GATE_UP, gu);
+  cudaError_t e = gate_up_few_takes(fmt, gu) ? launch_gate_up_few(fmt, gu, st) : launch_gate_up(fmt, gu, st);
   if (e != cudaSuccess) return cuda_status(e);
-  e = launch(STREAM_DOWN, dn);
+  e = launch_down(fmt, dn, st);
   if (e != cudaSuccess) {
     // the maxima that GATE_UP left are not taken back: what is zero between calls is made so
     cudaMemsetAsync(gu.amax, 0, (size_t)a.M * a.topk * 4, st);
@@ -147,7 +144,7 @@ size_t stream_workspace_bytes(int op, int64_t M, int64_t N, int64_t K, int E, in
   if (E <= 0 || topk <= 0) return 0;
   if (M > kMoeMaxTokens || topk > kMoeMaxTopk || K > 32768) return workspace_zero_bytes();  // refused
   return workspace_zero_bytes() + al256(stream_slot_bytes(M)) +
-         kMoeHandedBytes + (size_t)M * topk * cdiv(K, 8) * 8 * 2;
+         kMoeHandedBytes + al256(down_head_bytes(M)) + (size_t)M * topk * cdiv(K, 8) * 8 * 2;
 }
 }  // namespace ql
 
@@ -218,7 +215,7 @@ ql_status qlinear_int8(const int8_t* x_q, int64_t M, int64_t K, int64_t ldx, con
   s.ldy = ldy;
   s.tickets = at<unsigned>(workspace, kTicketOff);
   s.slots = at<float>(workspace, workspace_zero_bytes());
-  const cudaError_t e = launch_stream(STREAM_INT8, STREAM_LINEAR, s, (cudaStream_t)stream);
+  const cudaError_t e = launch_linear(s, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_status(e);
   if (path_out) *path_out = QL_PATH_INT8_CODES_SKINNY;
   return QL_OK;

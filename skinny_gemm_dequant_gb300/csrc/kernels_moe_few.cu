@@ -17,7 +17,7 @@
 // are all its experts' K in a row; they are cut evenly over the warps of all CTAs.
 #include "common.cuh"
 #include "ffn_act.cuh"
-#include "route.cuh"
+#include "moe_dispatch.cuh"
 #include "stream.h"
 #include "stream_dev.cuh"
 
@@ -26,8 +26,6 @@ namespace ql {
 namespace {
 
 constexpr int kGuWarps = 16;
-constexpr int kMaxTokens = 16, kMaxPairs = kMaxTokens * kMoeMaxTopk;  // of DOWN
-constexpr int kPerEntry = 8;  // pairs: one token tile of GATE_UP
 constexpr int R = kStreamRows;
 constexpr int kPitch = R + 4;  // of a column of sums: lanes (g, t) write 8 t + g, all banks once
 constexpr int kSmem = 226 * 1024;
@@ -37,121 +35,7 @@ __host__ __device__ constexpr int gu_list_bytes(int pairs) {
   return (pairs * 16 + kMoeMaxTokens * 4 + 127) & ~127;  // entries, ids, sorted pairs and tokens; scales
 }
 
-__host__ __device__ constexpr int dn_warps(int fmt) { return fmt == STREAM_INT4 ? 12 : 8; }
 __host__ __device__ constexpr int gu_k(int fmt) { return fmt == STREAM_INT4 ? 256 : fmt == STREAM_INT8 ? 128 : 64; }
-
-// Routing and dispatch, by every CTA for itself: pairs sorted by (expert, how often the token had it
-// before), entries of up to `most` pairs.  Scratch: P keys.
-struct Lists {
-  Entry* entries;
-  int* ids;        // by pair
-  uint16_t *pair, *tok;  // sorted
-  Entry* heads;    // scratch
-  int* keys;       // scratch
-};
-
-// what GATE_UP hands to DOWN beside h: the weights by pair and, up to kMaxTokens, the lists
-struct Handed {
-  float weight[kMoeMaxTokens * kMoeMaxTopk];
-  int entries, most, pad[2];
-  Entry entry[kMaxPairs];
-  uint16_t pair[kMaxPairs], tok[kMaxPairs];
-};
-
-__device__ __forceinline__ void route(const StreamArgs& p, const Lists& l, int warps) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-#pragma unroll 1
-  for (int m = warp; m < p.M; m += warps) {
-    int id = -1;
-    float wt;
-    if (p.logits)
-      route_token_warp<false>(p.logits + (int64_t)m * p.E, p.E, p.topk, false, id, wt);
-    else if (lane < p.topk)
-      id = p.ids[m * p.topk + lane];
-    if (id < 0 || id >= p.E) id = kNone;  // padding: not dispatched
-    if (lane < p.topk) l.ids[m * p.topk + lane] = id;
-  }
-}
-
-// One token, by one warp: an entry for each pair.  Returns their number.
-__device__ __forceinline__ int route_one(const StreamArgs& p, const Lists& l) {
-  const int lane = threadIdx.x & 31;
-  int id = -1;
-  float wt;
-  if (p.logits)
-    route_token_warp<false>(p.logits, p.E, p.topk, false, id, wt);
-  else if (lane < p.topk)
-    id = p.ids[lane];
-  const bool on = lane < p.topk && id >= 0 && id < p.E;
-  const unsigned all = __ballot_sync(0xffffffffu, on);
-  if (lane < p.topk) l.ids[lane] = on ? id : kNone;
-  if (on) {
-    const int n = __popc(all & ((1u << lane) - 1));
-    l.entries[n] = {(uint16_t)id, (uint16_t)n, 1};
-    l.pair[n] = (uint16_t)lane;
-    l.tok[n] = 0;
-  }
-  return __popc(all);
-}
-
-// after a barrier; ends with one.  Returns the number of entries, and the most pairs of one
-template <int WARPS>
-__device__ __forceinline__ int dispatch(const StreamArgs& p, const Lists& l, int per_entry, int& most_out) {
-  __shared__ int s_entries, s_most;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, P = p.M * p.topk;
-#pragma unroll 1
-  for (int i = threadIdx.x; i < P; i += WARPS * 32) {
-    int repeats = 0;
-    if (!p.logits)
-      for (int j = i - i % p.topk; j < i; ++j) repeats += l.ids[j] == l.ids[i];
-    l.keys[i] = l.ids[i] == kNone ? kNone : l.ids[i] * kMoeMaxTopk + repeats;
-  }
-  __syncthreads();
-#pragma unroll 1
-  for (int i = threadIdx.x; i < P; i += WARPS * 32) {
-    const int key = l.keys[i];
-    int before = 0, rank = 0, all = 0;
-    auto meet = [&](int o, int j) {
-      before += o < key;
-      all += o == key;
-      rank += o == key && j < i;
-    };
-    int j = 0;
-#pragma unroll 2
-    for (; j + 4 <= P; j += 4) {
-      const int4 o = *reinterpret_cast<const int4*>(l.keys + j);
-      meet(o.x, j);
-      meet(o.y, j + 1);
-      meet(o.z, j + 2);
-      meet(o.w, j + 3);
-    }
-    for (; j < P; ++j) meet(l.keys[j], j);
-    l.pair[before + rank] = (uint16_t)i;
-    l.tok[before + rank] = (uint16_t)(i / p.topk);
-    const bool head = key != kNone && rank % per_entry == 0;
-    l.heads[before + rank] = {(uint16_t)l.ids[i], (uint16_t)(before + rank), head ? min(per_entry, all - rank) : 0};
-  }
-  __syncthreads();
-  if (warp == 0) {
-    int n = 0, most = 1;
-#pragma unroll 1
-    for (int i0 = 0; i0 < P; i0 += 32) {
-      const int count = i0 + lane < P ? l.heads[i0 + lane].count : 0;
-      const unsigned all = __ballot_sync(0xffffffffu, count > 0);
-      most = max(most, count);
-      if (count > 0) l.entries[n + __popc(all & ((1u << lane) - 1))] = l.heads[i0 + lane];
-      n += __popc(all);
-    }
-    most = __reduce_max_sync(0xffffffffu, most);
-    if (lane == 0) {
-      s_entries = n;
-      s_most = most;
-    }
-  }
-  __syncthreads();
-  most_out = s_most;
-  return s_entries;
-}
 
 // slot of 16-byte piece c of row m of MMA operands of BYTES a row, for the reads below
 template <int FMT, bool FINE>
@@ -335,34 +219,9 @@ __global__ void __launch_bounds__(kGuWarps * 32, 1)
     stage_x();
     __syncthreads();
   }
-  Handed& to_down = *reinterpret_cast<Handed*>(p.handed);
-  if (p.M <= kMaxTokens && blockIdx.x == gridDim.x - 1 && warp == kGuWarps - 2) {
-    if (lane == 0) {
-      to_down.entries = ne;
-      to_down.most = most;
-    }
-    for (int i = lane; i < P; i += 32) {
-      if (i < ne) to_down.entry[i] = l.entries[i];
-      to_down.pair[i] = l.pair[i];
-      to_down.tok[i] = l.tok[i];
-    }
-  }
-  if (gridDim.x - 1 - blockIdx.x < p.M && warp == kGuWarps - 1) {
-    // the weights of a token, for the next launch: by the warps that have the fewest tiles
-    const int m = gridDim.x - 1 - blockIdx.x;
-    int id = 0;
-    float wt = 0.f;
-    if (p.logits)
-      route_token_warp(p.logits + (int64_t)m * p.E, p.E, p.topk, p.renorm != 0, id, wt);
-    else if (lane < p.topk)
-      wt = p.wts[m * p.topk + lane];
-    if (lane < p.topk) {
-      const int i = m * p.topk + lane;
-      to_down.weight[i] = wt;
-      if (p.wts_out) p.wts_out[i] = wt;
-      if (p.ids_out) p.ids_out[i] = l.ids[i] == kNone ? -1 : l.ids[i];
-    }
-  }
+  // for the next launch, by the warps that have the fewest tiles
+  if (blockIdx.x == gridDim.x - 1 && warp == kGuWarps - 2) hand_lists(p, l, ne, most);
+  if (gridDim.x - 1 - blockIdx.x < p.M && warp == kGuWarps - 1) hand_weights(p, l, gridDim.x - 1 - blockIdx.x);
 
   uint32_t slot = 0;  // byte offset of the stage in the ring
   const uint32_t w0_at = ring + (uint32_t)(g * 128 + wslot(t, g) * 16), w1_at = w0_at ^ 64u;  // pieces t, 4 + t
@@ -526,38 +385,37 @@ __global__ void __launch_bounds__(kGuWarps * 32, 1)
 }
 
 // ------------------------------------------------------------------ DOWN
-// NT: token columns / 8
-template <int FMT, int NT, bool FINE, bool ZP>
-__global__ void __launch_bounds__(dn_warps(FMT) * 32, 1)
-    down_kernel(const __grid_constant__ StreamArgs p, int lists) {
+// W: warps
+template <int FMT, int W, bool FINE, bool ZP>
+__global__ void __launch_bounds__(W * 32, 1) down_kernel(const __grid_constant__ StreamArgs p, int lists) {
   constexpr bool I8 = FMT == STREAM_INT8, I4 = FMT == STREAM_INT4;
-  constexpr int W = dn_warps(FMT), THREADS = W * 32, MT = R / 16;
+  constexpr int THREADS = W * 32, MT = R / 16;
   constexpr int KU = FMT == STREAM_BF16 ? 64 : 128, WB = I4 ? 64 : 128, XB = FMT == STREAM_BF16 ? 128 : 256;
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int P = p.M * p.topk;
+  const int P = p.M * p.topk, ysize = p.M * kPitch;
 
-  // shared memory: sums that a warp leaves of the tile it begins in [W][M][kPitch], lists, rings
-  float* s_head = reinterpret_cast<float*>(smem);
-  Lists l;
-  l.entries = reinterpret_cast<Entry*>(s_head + W * p.M * kPitch);
-  l.ids = reinterpret_cast<int*>(l.entries + P);
-  float* s_wt = reinterpret_cast<float*>(l.ids + P);  // by pair; 8-bit: times the scale of h
+  // shared memory: the warps' results of the tile they are in [W][M][kPitch], lists, rings
+  float* s_y = reinterpret_cast<float*>(smem);
+  Entry* entries = reinterpret_cast<Entry*>(s_y + W * ysize);
+  float* s_wt = reinterpret_cast<float*>(entries + P);  // by pair; 8-bit: times the scale of h
   float* s_inv = s_wt + P;
-  l.pair = reinterpret_cast<uint16_t*>(s_inv + P);
-  l.tok = l.pair + P;
+  uint16_t* s_pair = reinterpret_cast<uint16_t*>(s_inv + P);
+  uint16_t* s_tok = s_pair + P;
   uint8_t* rings = smem + lists;
   __shared__ int s_last[3];
 
+  float* y = s_y + warp * ysize;
+  for (int i = lane; i < ysize; i += 32) y[i] = 0.f;
   pdl_wait();
   pdl_launch_dependents();
   const Handed& from_gu = *reinterpret_cast<const Handed*>(p.handed);
   const int ne = from_gu.entries, xt = from_gu.most;
 #pragma unroll 1
   for (int i = threadIdx.x; i < P; i += THREADS) {
-    if (i < ne) l.entries[i] = from_gu.entry[i];
-    l.pair[i] = from_gu.pair[i];
-    l.tok[i] = from_gu.tok[i];
+    if (i < ne) entries[i] = from_gu.entry[i];
+    s_pair[i] = from_gu.pair[i];
+    s_tok[i] = from_gu.tok[i];
     float wt = from_gu.weight[i];
     if constexpr (I8) {
       const float top = __uint_as_float(p.amax[i]);
@@ -567,6 +425,7 @@ __global__ void __launch_bounds__(dn_warps(FMT) * 32, 1)
     s_wt[i] = wt;
   }
   __syncthreads();
+
   const int nblk = (p.K + KU - 1) / KU, tiles = (p.N + R - 1) / R, whole = ne * nblk, total = tiles * whole;
   if (total == 0) {  // nothing was dispatched
     for (int i = blockIdx.x * THREADS + threadIdx.x; i < p.M * p.N; i += gridDim.x * THREADS)
@@ -614,13 +473,17 @@ __global__ void __launch_bounds__(dn_warps(FMT) * 32, 1)
   const uint8_t* f_w = nullptr;
   const int64_t wstep = (int64_t)RPI * p.ldw;
   auto target = [&]() {
-    const Entry en = l.entries[f.a];
+    const Entry en = entries[f.a];
     f_valid = p.N - f.tile * R - cr;
     f_toks = en.count;
     f_first = en.first;
     f_w = p.w + en.expert * p.w_estride + (int64_t)(f.tile * R + cr) * p.ldw + cc * 16;
   };
-  auto fetch_w = [&](uint32_t at) {
+  auto fetch = [&](uint32_t at) {
+    const int kx = f.kb * XB + tc * 16;
+#pragma unroll 1
+    for (int m = tr; m < f_toks; m += TPI)
+      cp16(at + R * WB + m * XB + xslot<FMT, FINE>(tc, m) * 16, p.x + s_pair[f_first + m] * p.ldx + kx, kx < p.K * 2);
     const int k = f.kb * WB + cc * 16;
     const int valid = k < (I4 ? p.K / 2 : I8 ? p.K : p.K * 2) ? f_valid : -R;
     const uint8_t* src = f_w + (int64_t)f.kb * WB;
@@ -631,22 +494,16 @@ __global__ void __launch_bounds__(dn_warps(FMT) * 32, 1)
       src += wstep;
     }
   };
-  auto fetch_x = [&](uint32_t at) {
-    const int k = f.kb * XB + tc * 16;
-#pragma unroll 1
-    for (int m = tr; m < f_toks; m += TPI)
-      cp16(at + R * WB + m * XB + xslot<FMT, FINE>(tc, m) * 16, p.x + l.pair[f_first + m] * p.ldx + k, k < p.K * 2);
-  };
 
   // scales of a unit (4-bit) or of an entry (8-bit): a lane reads those of rows lane and lane + 32
   constexpr int NS = FINE ? 4 : 1;
-  uint16_t s_next[2][NS];
+  uint16_t s_next[2][NS];  // as loaded: turning them into numbers here would wait for them
   uint8_t z_next[2][NS];
   const uint16_t* sp[2] = {};
   const uint8_t* zp[2] = {};
   auto scale_rows = [&](const At& w) {
     if constexpr (I4) {
-      const int e = l.entries[w.a].expert;
+      const int e = entries[w.a].expert;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int64_t row = min(w.tile * R + lane + 32 * h, p.N - 1);
@@ -670,21 +527,18 @@ __global__ void __launch_bounds__(dn_warps(FMT) * 32, 1)
     }
   };
 
-  float y[MT][NT][4], part[MT][NT][4];
+  float part[MT][4];
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) y[mt][nt][i] = part[mt][nt][i] = 0.f;
+    for (int i = 0; i < 4; ++i) part[mt][i] = 0.f;
 
   const int pre = depth - 1;
 #pragma unroll 1
   for (int d = 0; d < pre; ++d) {
     if (f.u < v1) {
       if (d == 0 || f.kb == 0) target();
-      fetch_x(ring + d * stage);
-      fetch_w(ring + d * stage);
+      fetch(ring + d * stage);
     }
     cp_commit();
     next(f);
@@ -693,94 +547,68 @@ __global__ void __launch_bounds__(dn_warps(FMT) * 32, 1)
   At c = set(v0);
   int first_u = v0;  // of the tile's units that this warp has added
   uint32_t slot = 0, to_slot = pre;
-  // what the entry's tokens are to this lane: its B columns' rows of x and factors; its sums' weights
-  int row[NT];
-  float inv[NT], wc[NT][2];
-  bool here[NT][2], any[NT];
+  int count = 0, row = 0, first = 0;  // the entry's pairs; this lane's B column among them
+  float inv = 0.f;
   float ws[2] = {1.f, 1.f};
   auto enter = [&]() {
-    const Entry en = l.entries[c.a];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      row[nt] = 0;
-      here[nt][0] = here[nt][1] = any[nt] = false;
-      wc[nt][0] = wc[nt][1] = inv[nt] = 0.f;
-    }
-#pragma unroll 1
-    for (int i = 0; i < en.count; ++i) {
-      const int m = l.tok[en.first + i], pair = l.pair[en.first + i];
-      const float wt = s_wt[pair];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        if (m == nt * 8 + g) {
-          row[nt] = i;
-          if (I8) inv[nt] = s_inv[pair];
-        }
-        any[nt] = any[nt] || (m >> 3) == nt;
-#pragma unroll
-        for (int q = 0; q < 2; ++q)
-          if (m == nt * 8 + 2 * t + q) {
-            here[nt][q] = true;
-            wc[nt][q] = wt;
-          }
-      }
-    }
+    const Entry en = entries[c.a];
+    count = en.count;
+    first = en.first;
+    row = min(g, count - 1);
     if constexpr (I8) {
+      inv = s_inv[s_pair[first + row]];
       const float* s = reinterpret_cast<const float*>(p.scale) + en.expert * p.s_estride + c.tile * R + lane;
 #pragma unroll
       for (int h = 0; h < 2; ++h) ws[h] = c.tile * R + lane + 32 * h < p.N ? s[32 * h] : 0.f;
     }
   };
-  // an entry's sums, times the token's weight, into the tile's
+  // an entry's sums, times the tokens' weights, into the tile's results: a lane has its own rows of columns
+  // 2t and 2t + 1, whose tokens differ
   auto fold = [&]() {
+    float sc[MT][2];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float s = I8 ? __shfl_sync(0xffffffffu, ws[mt / 2], mt % 2 * 16 + h * 8 + g) : I4 ? 64.f : 1.f;
+      for (int h = 0; h < 2; ++h)
+        sc[mt][h] = I8 ? __shfl_sync(0xffffffffu, ws[mt / 2], mt % 2 * 16 + h * 8 + g) : I4 ? 64.f : 1.f;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+    for (int q = 0; q < 2; ++q)
+      if (2 * t + q < count) {
+        const int at = first + 2 * t + q;
+        const float wt = s_wt[s_pair[at]];
+        float* to = y + s_tok[at] * kPitch + g;
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            float& d = part[mt][nt][2 * h + q];
-            if (here[nt][q]) y[mt][nt][2 * h + q] = fmaf(wc[nt][q], s * d, y[mt][nt][2 * h + q]);
-            d = 0.f;
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float& v = to[mt * 16 + 8 * h];
+            v = fmaf(wt, sc[mt][h] * part[mt][2 * h + q], v);
           }
       }
-  };
-  auto leave = [&](float* to) {  // [M][kPitch]
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int m = nt * 8 + 2 * t + (i & 1);
-          if (m < p.M) to[m * kPitch + mt * 16 + g + 8 * (i >> 1)] = y[mt][nt][i];
-          y[mt][nt][i] = 0.f;
-        }
+      for (int i = 0; i < 4; ++i) part[mt][i] = 0.f;
   };
-  // the end of this warp's part [first_u, end) of a tile
-  auto finish = [&](int tile, int end) {
-    if (first_u > tile * whole) {
-      leave(s_head + warp * p.M * kPitch);
-    } else if (end == (tile + 1) * whole) {  // all of it
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int m = nt * 8 + 2 * t + (i & 1), n = tile * R + mt * 16 + g + 8 * (i >> 1);
-            if (m < p.M && n < p.N)
-              reinterpret_cast<uint16_t*>(p.y)[(int64_t)m * p.ldy + n] = f32_to_bf16_rn(y[mt][nt][i]);
-            y[mt][nt][i] = 0.f;
-          }
-    } else {  // the last of this warp's units: its ring is free
-      asm volatile("cp.async.wait_group 0;" ::: "memory");
-      __syncwarp();
-      leave(reinterpret_cast<float*>(rings + (size_t)warp * depth * stage));
+  auto put = [&](int tile, int i, float v) {  // element i of [M][R]
+    const int n = tile * R + i % R;
+    if (n < p.N) reinterpret_cast<uint16_t*>(p.y)[(int64_t)(i / R) * p.ldy + n] = f32_to_bf16_rn(v);
+  };
+  // results of the tile that a warp begins in, where it goes on to another one: [CTA][W][M][R]
+  auto head_of = [&](int w) { return p.heads + ((int64_t)blockIdx.x * W + w) * (p.M * R); };
+  // the end of this warp's part [first_u, end) of a tile, which is not its last: written, or left
+  auto finish = [&](int tile) {
+    const bool all = first_u == tile * whole;
+    __syncwarp();
+    for (int i = lane; i < p.M * R; i += 32) {
+      float& v = y[i / R * kPitch + i % R];
+      if (all)
+        put(tile, i, v);
+      else
+        __stcg(head_of(warp) + i, v);
+      v = 0.f;
     }
+    __syncwarp();
   };
 
   int folded = 0;
@@ -795,13 +623,12 @@ __global__ void __launch_bounds__(dn_warps(FMT) * 32, 1)
     __syncwarp();  // every lane's copies of this unit have landed, and the unit before is read
     if (f.u < v1) {
       if (f.kb == 0) target();
-      fetch_x(ring + to_slot * stage);
-      fetch_w(ring + to_slot * stage);
+      fetch(ring + to_slot * stage);
     }
     cp_commit();
     next(f);
     if (++to_slot == (uint32_t)depth) to_slot = 0;
-    const uint32_t wat = ring + slot * stage + g * WB, xat = ring + slot * stage + R * WB;
+    const uint32_t wat = ring + slot * stage + g * WB, xat = ring + slot * stage + R * WB + row * XB;
     if (++slot == (uint32_t)depth) slot = 0;
     float scl[2][NS];  // scale and zero point (as bf16x2 of -z / 64) of this lane's rows
     uint32_t nzl[2][NS];
@@ -823,23 +650,19 @@ __global__ void __launch_bounds__(dn_warps(FMT) * 32, 1)
     }
 
     if constexpr (I4) {
-      uint4 bx[NT][4];
+      uint4 bx[4];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-        if (NT == 1 || any[nt]) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            bx[nt][j] = pair_up(lds16(xat + row[nt] * XB + xslot<FMT, FINE>(FINE ? j * 4 + t : t * 4 + j, row[nt]) * 16));
-        }
+      for (int j = 0; j < 4; ++j) bx[j] = pair_up(lds16(xat + xslot<FMT, FINE>(FINE ? j * 4 + t : t * 4 + j, row) * 16));
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
         // rows g, g + 8 of the row tile
         uint32_t wv[2][4], negz[2];
-        float sc[2], grp[NT][4];
+        float sc[2], grp[4];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const uint32_t at = wat + (mt * 16 + h * 8) * WB;
           if constexpr (FINE) {
+            // word t of every 32-k piece, so that an MMA stays inside one group
 #pragma unroll
             for (int j = 0; j < 4; ++j) wv[h][j] = lds4(at + swz(j, g) * 16 + t * 4);
           } else {
@@ -862,45 +685,37 @@ __global__ void __launch_bounds__(dn_warps(FMT) * 32, 1)
           uint32_t q0[4], q1[4];
           codes_to_bf16(wv[0][j], negz[0], q0);
           codes_to_bf16(wv[1][j], negz[1], q1);
+          if (j == 0 || FINE)
+            mma_first(grp, q0[0], q1[0], q0[1], q1[1], bx[j].x, bx[j].y);
+          else
+            mma_bf16_16816(grp, q0[0], q1[0], q0[1], q1[1], bx[j].x, bx[j].y);
+          mma_bf16_16816(grp, q0[2], q1[2], q0[3], q1[3], bx[j].z, bx[j].w);
+          if (FINE || j == 3) {
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            if (NT == 1 || any[nt]) {
-              if (j == 0 || FINE)
-                mma_first(grp[nt], q0[0], q1[0], q0[1], q1[1], bx[nt][j].x, bx[nt][j].y);
-              else
-                mma_bf16_16816(grp[nt], q0[0], q1[0], q0[1], q1[1], bx[nt][j].x, bx[nt][j].y);
-              mma_bf16_16816(grp[nt], q0[2], q1[2], q0[3], q1[3], bx[nt][j].z, bx[nt][j].w);
-              if (FINE || j == 3) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) part[mt][nt][i] = fmaf(sc[i >> 1], grp[nt][i], part[mt][nt][i]);
-              }
-            }
+            for (int i = 0; i < 4; ++i) part[mt][i] = fmaf(sc[i >> 1], grp[i], part[mt][i]);
+          }
         }
       }
     } else {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        uint32_t b[NT][8];
+        uint32_t b[8];
+        if constexpr (I8) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-          if (NT == 1 || any[nt]) {
-            if constexpr (I8) {
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                const uint4 v = lds16(xat + row[nt] * XB + xslot<FMT, FINE>(8 * j + 2 * t + i, row[nt]) * 16);
-                b[nt][4 * i] = quant2(v.x, inv[nt]);
-                b[nt][4 * i + 1] = quant2(v.y, inv[nt]);
-                b[nt][4 * i + 2] = quant2(v.z, inv[nt]);
-                b[nt][4 * i + 3] = quant2(v.w, inv[nt]);
-              }
-            } else {
-              const uint4 v = lds16(xat + row[nt] * XB + xslot<FMT, FINE>(4 * j + t, row[nt]) * 16);
-              b[nt][0] = v.x;
-              b[nt][1] = v.y;
-              b[nt][2] = v.z;
-              b[nt][3] = v.w;
-            }
+          for (int i = 0; i < 2; ++i) {
+            const uint4 v = lds16(xat + xslot<FMT, FINE>(8 * j + 2 * t + i, row) * 16);
+            b[4 * i] = quant2(v.x, inv);
+            b[4 * i + 1] = quant2(v.y, inv);
+            b[4 * i + 2] = quant2(v.z, inv);
+            b[4 * i + 3] = quant2(v.w, inv);
           }
+        } else {
+          const uint4 v = lds16(xat + xslot<FMT, FINE>(4 * j + t, row) * 16);
+          b[0] = v.x;
+          b[1] = v.y;
+          b[2] = v.z;
+          b[3] = v.w;
+        }
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
           const uint4 w0 = lds16(wat + (mt * 16) * WB + swz(4 * j + t, g) * 16);
@@ -912,17 +727,11 @@ __global__ void __launch_bounds__(dn_warps(FMT) * 32, 1)
               uint32_t a0, a1, a2, a3;
               s8x4_to_f16x2x2(lo[i], a0, a2);
               s8x4_to_f16x2x2(hi[i], a1, a3);
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-                if (NT == 1 || any[nt]) mma_f16_16816(part[mt][nt], a0, a1, a2, a3, b[nt][2 * i], b[nt][2 * i + 1]);
+              mma_f16_16816(part[mt], a0, a1, a2, a3, b[2 * i], b[2 * i + 1]);
             }
           } else {
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              if (NT == 1 || any[nt]) {
-                mma_bf16_16816(part[mt][nt], w0.x, w1.x, w0.y, w1.y, b[nt][0], b[nt][1]);
-                mma_bf16_16816(part[mt][nt], w0.z, w1.z, w0.w, w1.w, b[nt][2], b[nt][3]);
-              }
+            mma_bf16_16816(part[mt], w0.x, w1.x, w0.y, w1.y, b[0], b[1]);
+            mma_bf16_16816(part[mt], w0.z, w1.z, w0.w, w1.w, b[2], b[3]);
           }
         }
       }
@@ -931,8 +740,8 @@ __global__ void __launch_bounds__(dn_warps(FMT) * 32, 1)
     if (last || n.kb == 0 || (I8 && ++folded == 8)) {  // 8-bit: at most 1024 k, sums of at most 2^24
       fold();
       folded = 0;
-      if (last || (n.kb == 0 && n.a == 0)) {
-        finish(c.tile, n.u);
+      if (!last && n.kb == 0 && n.a == 0) {
+        finish(c.tile);
         first_u = n.u;
       }
       c = n;
@@ -943,13 +752,8 @@ __global__ void __launch_bounds__(dn_warps(FMT) * 32, 1)
   __syncthreads();
 
   // ---------------------------------------------------------------- tiles that warps or CTAs share
-  const int slot_floats = p.M * R;
   // 0: the part of a tile that began in an earlier CTA, 1: of one that ends in a later CTA
-  auto slot_of = [&](int cta, int tail) { return p.slots + ((int64_t)cta * 2 + tail) * slot_floats; };
-  auto put = [&](int tile, int i, float v) {
-    const int n = tile * R + i % R;
-    if (n < p.N) reinterpret_cast<uint16_t*>(p.y)[(int64_t)(i / R) * p.ldy + n] = f32_to_bf16_rn(v);
-  };
+  auto slot_of = [&](int cta, int tail) { return p.slots + ((int64_t)cta * 2 + tail) * (p.M * R); };
   const int tile0 = u0 / whole, tile1 = u1 > u0 ? (u1 - 1) / whole : tile0 - 1;
 #pragma unroll 1
   for (int tile = tile0; tile <= tile1; ++tile) {
@@ -958,16 +762,15 @@ __global__ void __launch_bounds__(dn_warps(FMT) * 32, 1)
     int lo = 0, hi = W - 1;
     while (bound(lo + 1) <= a) ++lo;
     while (bound(hi) >= b) --hi;
-    if (lo == hi && a == s && b == e) continue;  // written
+    if (lo == hi && a == s && b < bound(lo + 1)) continue;  // written: whole, and not the warp's last
 #pragma unroll 1
     for (int i = threadIdx.x; i < p.M * R; i += THREADS) {
       float v = 0.f;
 #pragma unroll 1
       for (int w = lo; w <= hi; ++w) {
-        if (bound(w) == bound(w + 1)) continue;
-        const float* from = bound(w) > s ? s_head + w * p.M * kPitch
-                                         : reinterpret_cast<const float*>(rings + (size_t)w * depth * stage);
-        v += from[i / R * kPitch + i % R];
+        const int end = bound(w + 1);
+        if (bound(w) == end) continue;
+        v += end <= e ? s_y[w * ysize + i / R * kPitch + i % R] : __ldcg(head_of(w) + i);
       }
       if (a > s || b < e)
         __stcg(slot_of(blockIdx.x, a == s) + i, v);
@@ -981,15 +784,15 @@ __global__ void __launch_bounds__(dn_warps(FMT) * 32, 1)
   const bool cut1 = tile1 > tile0 && (tile1 + 1) * whole > u1;
   __threadfence();
   __syncthreads();
-  if (threadIdx.x < 64 && (threadIdx.x & 31) == 0) {
-    const int which = threadIdx.x >> 5, tile = which ? tile1 : tile0;
+  if (threadIdx.x < 64 && lane == 0) {
+    const int tile = warp ? tile1 : tile0;
     bool last = false;
-    if (which ? cut1 : cut0) {
+    if (warp ? cut1 : cut0) {
       const int c0 = tile * whole / share, c1 = ((tile + 1) * whole - 1) / share;
       last = atomicAdd(p.tickets + c0, 1u) == (unsigned)(c1 - c0);
       if (last) p.tickets[c0] = 0u;
     }
-    s_last[which] = last;
+    s_last[warp] = last;
   }
   if (I8 && threadIdx.x == 64) {
     // every CTA has read h's maxima before its first product: the last one here leaves them zero
@@ -1032,16 +835,16 @@ cudaError_t launch_gu(const StreamArgs& a, int x_bytes, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, kfn, a, x_bytes, lists);
 }
 
-template <int FMT, int NT, bool FINE, bool ZP>
+template <int FMT, int W, bool FINE, bool ZP>
 cudaError_t launch_dn(const StreamArgs& a, cudaStream_t st) {
-  auto* kfn = down_kernel<FMT, NT, FINE, ZP>;
+  auto* kfn = down_kernel<FMT, W, FINE, ZP>;
   static OncePerDevice once;
   if (const cudaError_t e = raise_smem_limit(kfn, once); e != cudaSuccess) return e;
   const int P = a.M * a.topk;
-  const int lists = (dn_warps(FMT) * a.M * kPitch * 4 + P * (int)(sizeof(Entry) + 3 * 4 + 4) + 127) & ~127;
+  const int lists = (W * a.M * kPitch * 4 + P * (int)(sizeof(Entry) + 2 * 4 + 2 * 2) + 127) & ~127;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(kNumSMs, 1, 1);
-  cfg.blockDim = dim3(dn_warps(FMT) * 32, 1, 1);
+  cfg.blockDim = dim3(W * 32, 1, 1);
   cfg.dynamicSmemBytes = (size_t)kSmem;
   cfg.stream = st;
   cudaLaunchAttribute at[1];
@@ -1052,13 +855,28 @@ cudaError_t launch_dn(const StreamArgs& a, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, kfn, a, lists);
 }
 
-template <int NT>
-cudaError_t launch_dn_nt(int fmt, const StreamArgs& a, cudaStream_t st) {
-  if (fmt == STREAM_BF16) return launch_dn<STREAM_BF16, NT, false, false>(a, st);
-  if (fmt == STREAM_INT8) return launch_dn<STREAM_INT8, NT, false, false>(a, st);
-  if (a.group_shift < 7)
-    return a.zero ? launch_dn<STREAM_INT4, NT, true, true>(a, st) : launch_dn<STREAM_INT4, NT, true, false>(a, st);
-  return a.zero ? launch_dn<STREAM_INT4, NT, false, true>(a, st) : launch_dn<STREAM_INT4, NT, false, false>(a, st);
+// Warps of DOWN: what leaves each a ring of two stages with 8 tokens beside the results of all tokens
+template <int FMT>
+__host__ __device__ constexpr int dn_warps(int tokens) {
+  constexpr bool I4 = FMT == STREAM_INT4;
+  return tokens <= 4 && I4 ? 16 : tokens <= 20 ? (I4 ? 12 : 8) : tokens <= 40 ? (I4 ? 9 : 6) : I4 ? 7 : 5;
+}
+template <int FMT>
+constexpr bool dn_fits(int tokens) {
+  const int stage = R * (FMT == STREAM_INT4 ? 64 : 128) + (tokens < 8 ? tokens : 8) * (FMT == STREAM_BF16 ? 128 : 256);
+  return dn_warps<FMT>(tokens) * (tokens * kPitch * 4 + 2 * stage) + tokens * kMoeMaxTopk * 20 + 128 <= kSmem;
+}
+static_assert(dn_fits<STREAM_INT4>(4) && dn_fits<STREAM_INT4>(20) && dn_fits<STREAM_INT4>(40) &&
+                  dn_fits<STREAM_INT4>(64) && dn_fits<STREAM_INT8>(20) && dn_fits<STREAM_INT8>(40) &&
+                  dn_fits<STREAM_INT8>(64),
+              "two stages for every warp");
+
+template <int FMT, bool FINE, bool ZP>
+cudaError_t launch_dn_warps(const StreamArgs& a, cudaStream_t st) {
+  if (FMT == STREAM_INT4 && a.M <= 4) return launch_dn<FMT, dn_warps<FMT>(4), FINE, ZP>(a, st);
+  if (a.M <= 20) return launch_dn<FMT, dn_warps<FMT>(20), FINE, ZP>(a, st);
+  if (a.M <= 40) return launch_dn<FMT, dn_warps<FMT>(40), FINE, ZP>(a, st);
+  return launch_dn<FMT, dn_warps<FMT>(64), FINE, ZP>(a, st);
 }
 
 // bytes of GATE_UP's tokens in shared memory
@@ -1071,24 +889,29 @@ int64_t gu_x_bytes(int fmt, const StreamArgs& a) {
 
 }  // namespace
 
-static_assert(sizeof(Handed) <= kMoeHandedBytes, "workspace");
-
-bool moe_few_takes(int fmt, int mode, const StreamArgs& gate_up) {
-  const int P = gate_up.M * gate_up.topk;
-  if (mode == STREAM_DOWN && gate_up.M > kMaxTokens) return false;
-  return gu_x_bytes(fmt, gate_up) + gu_list_bytes(P) + kGuWarps * kDepth * kStage <= kSmem;
+bool gate_up_few_takes(int fmt, const StreamArgs& a) {
+  return gu_x_bytes(fmt, a) + gu_list_bytes(a.M * a.topk) + kGuWarps * kDepth * kStage <= kSmem;
 }
 
-cudaError_t launch_moe_few(int fmt, int mode, const StreamArgs& a, cudaStream_t st) {
-  const bool fine = a.group_shift < 7;
-  if (mode == STREAM_GATE_UP) {
-    const int x = (int)gu_x_bytes(fmt, a);
-    if (fmt == STREAM_BF16) return launch_gu<STREAM_BF16, false, false>(a, x, st);
-    if (fmt == STREAM_INT8) return launch_gu<STREAM_INT8, false, false>(a, x, st);
-    if (fine) return a.zero ? launch_gu<STREAM_INT4, true, true>(a, x, st) : launch_gu<STREAM_INT4, true, false>(a, x, st);
-    return a.zero ? launch_gu<STREAM_INT4, false, true>(a, x, st) : launch_gu<STREAM_INT4, false, false>(a, x, st);
-  }
-  return a.M <= 8 ? launch_dn_nt<1>(fmt, a, st) : launch_dn_nt<2>(fmt, a, st);
+cudaError_t launch_gate_up_few(int fmt, const StreamArgs& a, cudaStream_t st) {
+  const int x = (int)gu_x_bytes(fmt, a);
+  if (fmt == STREAM_BF16) return launch_gu<STREAM_BF16, false, false>(a, x, st);
+  if (fmt == STREAM_INT8) return launch_gu<STREAM_INT8, false, false>(a, x, st);
+  if (a.group_shift < 7)
+    return a.zero ? launch_gu<STREAM_INT4, true, true>(a, x, st) : launch_gu<STREAM_INT4, true, false>(a, x, st);
+  return a.zero ? launch_gu<STREAM_INT4, false, true>(a, x, st) : launch_gu<STREAM_INT4, false, false>(a, x, st);
+}
+
+cudaError_t launch_down(int fmt, const StreamArgs& a, cudaStream_t st) {
+  if (fmt == STREAM_BF16) return launch_dn_warps<STREAM_BF16, false, false>(a, st);
+  if (fmt == STREAM_INT8) return launch_dn_warps<STREAM_INT8, false, false>(a, st);
+  if (a.group_shift < 7)
+    return a.zero ? launch_dn_warps<STREAM_INT4, true, true>(a, st) : launch_dn_warps<STREAM_INT4, true, false>(a, st);
+  return a.zero ? launch_dn_warps<STREAM_INT4, false, true>(a, st) : launch_dn_warps<STREAM_INT4, false, false>(a, st);
+}
+
+size_t down_head_bytes(int64_t M) {
+  return (size_t)kNumSMs * dn_warps<STREAM_INT4>((int)M) * M * R * 4;  // (the most of all types)
 }
 
 }  // namespace ql

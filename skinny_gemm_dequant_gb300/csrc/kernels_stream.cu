@@ -14,7 +14,7 @@
 
 #include "common.cuh"
 #include "ffn_act.cuh"
-#include "route.cuh"
+#include "moe_dispatch.cuh"
 #include "stream.h"
 #include "stream_dev.cuh"
 
@@ -77,7 +77,7 @@ __global__ void __launch_bounds__((compute_warps(FMT, NT) + 1) * 32, 1)
     stream_kernel(const __grid_constant__ StreamArgs p, const __grid_constant__ Layout lay) {
   constexpr int W = compute_warps(FMT, NT), THREADS = (W + 1) * 32;
   constexpr int TT = NT * 8, KU = unit_k(FMT), WB = row_bytes(FMT), XB = token_bytes(FMT, MODE);
-  constexpr bool GU = MODE == STREAM_GATE_UP, DN = MODE == STREAM_DOWN, LIN = MODE == STREAM_LINEAR;
+  constexpr bool GU = MODE == STREAM_GATE_UP, LIN = MODE == STREAM_LINEAR;
   constexpr bool I8 = FMT == STREAM_INT8, I4 = FMT == STREAM_INT4;
   constexpr int kFull = 1, kEmpty = 1 + kBuffers;  // named barriers: a buffer of sums is written, is read
   constexpr int OUT = GU ? R / 2 : R;   // outputs of a tile: half gate rows, half up rows
@@ -86,43 +86,27 @@ __global__ void __launch_bounds__((compute_warps(FMT, NT) + 1) * 32, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int P = LIN ? 0 : p.M * p.topk;
 
-  // lists: results of the tile, entries, ids and weights by pair, (INT8) factor and scale by row of x, sorted pairs
-  float* s_y = reinterpret_cast<float*>(smem);  // DOWN: [M][R]
-  Entry* entries = reinterpret_cast<Entry*>(s_y + (DN ? p.M * R : 0));
-  Entry* heads = reinterpret_cast<Entry*>(smem + lay.lists);  // of passes, by place; read before the rings are filled
-  int* s_id = reinterpret_cast<int*>(entries + P);
-  float* s_wt = reinterpret_cast<float*>(s_id + P);
-  float* s_inv = s_wt + (DN ? P : 0);
-  float* s_xs = s_inv + (I8 ? P : 0);
-  uint16_t* s_pair = reinterpret_cast<uint16_t*>(s_xs + (I8 ? P : 0));  // sorted by expert
-  uint16_t* s_tok = s_pair + P;                                         // their tokens
-  const uint16_t* s_row = GU ? s_tok : s_pair;                          // their rows of x
-  __shared__ int s_entries, s_most;
+  // lists: entries, ids by pair, (INT8) factor and scale by token, sorted pairs and their tokens
+  Lists l;
+  l.entries = reinterpret_cast<Entry*>(smem);
+  l.ids = reinterpret_cast<int*>(l.entries + P);
+  float* s_inv = reinterpret_cast<float*>(l.ids + P);
+  float* s_xs = s_inv + (I8 ? kMoeMaxTokens : 0);
+  l.pair = reinterpret_cast<uint16_t*>(s_xs + (I8 ? kMoeMaxTokens : 0));
+  l.tok = l.pair + P;
+  l.keys = reinterpret_cast<int*>(smem + lay.lists);  // the rings are filled later
+  l.heads = reinterpret_cast<Entry*>(l.keys + (P + 3) / 4 * 4);
 
-  if (!DN) {
-    pdl_wait();
-    pdl_launch_dependents();
-  }
+  pdl_wait();
+  pdl_launch_dependents();
   int ne, xt;  // entries, most tokens of one
   if constexpr (LIN) {
     ne = (p.M + TT - 1) / TT;
     xt = min(p.M, TT);
   } else {
-    // ---------------------------------------------------------------- routing and dispatch
-    // Every CTA chooses for itself.  DOWN does so before its wait: the launch before, GATE_UP, has
-    // waited for what wrote the logits.  The weights are computed later, by one CTA for each token.
-#pragma unroll 1
-    for (int m = warp; m < p.M; m += W + 1) {
-      int id = -1;
-      float wt;
-      if (p.logits)
-        route_token_warp<false>(p.logits + (int64_t)m * p.E, p.E, p.topk, false, id, wt);
-      else if (lane < p.topk)
-        id = p.ids[m * p.topk + lane];
-      if (id < 0 || id >= p.E) id = kNone;  // padding: not dispatched
-      if (lane < p.topk) s_id[m * p.topk + lane] = id;
-    }
-    if (GU && I8) {
+    static_assert(TT == kPerEntry, "a token tile for each entry");
+    route(p, l, W + 1);
+    if (I8) {
 #pragma unroll 1
       for (int m = W - warp; m < p.M; m += W + 1) {  // (from the last warp on: the first ones route)
         const uint4* row = reinterpret_cast<const uint4*>(p.x + m * p.ldx);
@@ -144,45 +128,10 @@ __global__ void __launch_bounds__((compute_warps(FMT, NT) + 1) * 32, 1)
       }
     }
     __syncthreads();
-    // a pair's place is the number of pairs before it by (expert, pair); every TT pairs of an expert
-    // begin a pass over its weights
-#pragma unroll 1
-    for (int i = threadIdx.x; i < P; i += THREADS) {
-      const int e = s_id[i];
-      int before = 0, rank = 0, all = 0;
-#pragma unroll 4
-      for (int j = 0; j < P; ++j) {
-        const int o = s_id[j];
-        before += o < e;
-        all += o == e;
-        rank += o == e && j < i;
-      }
-      s_pair[before + rank] = (uint16_t)i;
-      s_tok[before + rank] = (uint16_t)(i / p.topk);
-      const bool head = e != kNone && rank % TT == 0;
-      heads[before + rank] = {(uint16_t)e, (uint16_t)(before + rank), head ? min(TT, all - rank) : 0};
-    }
-    __syncthreads();
-    if (warp == 0) {
-      int n = 0, most = 1;
-#pragma unroll 1
-      for (int i0 = 0; i0 < P; i0 += 32) {
-        const int count = i0 + lane < P ? heads[i0 + lane].count : 0;
-        const bool head = count > 0;
-        most = max(most, count);
-        const unsigned all = __ballot_sync(0xffffffffu, head);
-        if (head) entries[n + __popc(all & ((1u << lane) - 1))] = heads[i0 + lane];
-        n += __popc(all);
-      }
-      most = __reduce_max_sync(0xffffffffu, most);
-      if (lane == 0) {
-        s_entries = n;
-        s_most = most;
-      }
-    }
-    __syncthreads();
-    ne = s_entries;
-    xt = s_most;
+    ne = dispatch<W + 1>(p, l, kPerEntry, xt);
+    // for the next launch
+    if (blockIdx.x == gridDim.x - 1 && warp == W) hand_lists(p, l, ne, xt);
+    if (blockIdx.x < p.M && warp == W) hand_weights(p, l, blockIdx.x);
   }
   const int buffer = W * xt * kPitch * 4, buffers = max(1, min(kBuffers, 24 * 1024 / buffer));
   const int rings = (lay.lists + buffers * buffer + 127) & ~127, stage = R * WB + xt * XB;
@@ -191,9 +140,8 @@ __global__ void __launch_bounds__((compute_warps(FMT, NT) + 1) * 32, 1)
   // ------------------------------------------------------------------ this CTA's units
   const int nblk = (p.K + KU - 1) / KU;
   const int tiles = (p.N + OUT - 1) / OUT;
-  const int whole = (DN ? ne : 1) * nblk;  // units whose sums meet before the epilogue
   const int total = tiles * ne * nblk;
-  const int share = unit_share(total, whole, W);
+  const int share = unit_share(total, nblk, W);
   const int u0 = min(total, (int)blockIdx.x * share), u1 = min(total, u0 + share);
 
   auto entry = [&](int a) {
@@ -203,35 +151,12 @@ __global__ void __launch_bounds__((compute_warps(FMT, NT) + 1) * 32, 1)
     if constexpr (LIN) {
       en.count = min(TT, en.count);
     } else {
-      const Entry q = entries[a];
+      const Entry q = l.entries[a];
       en = {q.expert, q.first, q.count};
     }
     return en;
   };
-  if (GU && warp == W && blockIdx.x < p.M) {
-    // the weights of a token, for the next launch
-    const int m = blockIdx.x;
-    int id = 0;
-    float wt = 0.f;
-    if (p.logits)
-      route_token_warp(p.logits + (int64_t)m * p.E, p.E, p.topk, p.renorm != 0, id, wt);
-    else if (lane < p.topk)
-      wt = p.wts[m * p.topk + lane];
-    if (lane < p.topk) {
-      const int i = m * p.topk + lane;
-      reinterpret_cast<float*>(p.handed)[i] = wt;
-      if (p.wts_out) p.wts_out[i] = wt;
-      if (p.ids_out) p.ids_out[i] = s_id[i] == kNone ? -1 : s_id[i];
-    }
-  }
-  if (total == 0) {  // nothing was dispatched
-    if (DN) {
-      pdl_wait();
-      for (int i = blockIdx.x * THREADS + threadIdx.x; i < p.M * p.N; i += gridDim.x * THREADS)
-        reinterpret_cast<uint16_t*>(p.y)[(int64_t)(i / p.N) * p.ldy + i % p.N] = 0;
-    }
-    return;
-  }
+  if (total == 0) return;  // nothing was dispatched
 
   if (warp < W) {
     // ---------------------------------------------------------------- streaming and products
@@ -269,7 +194,7 @@ __global__ void __launch_bounds__((compute_warps(FMT, NT) + 1) * 32, 1)
       for (int i = 0; i < XCOPIES; ++i) {
         if (i * TPI >= en.count) break;
         const int r = en.first + min(i * TPI + tr, en.count - 1);
-        f_x[i] = p.x + (LIN ? r : s_row[r]) * p.ldx + tc * 16;
+        f_x[i] = p.x + (LIN ? r : l.tok[r]) * p.ldx + tc * 16;
       }
     };
     const int64_t wstep = (int64_t)RPI * p.ldw, to_up = ((int64_t)p.N - OUT) * p.ldw;
@@ -357,34 +282,17 @@ __global__ void __launch_bounds__((compute_warps(FMT, NT) + 1) * 32, 1)
       }
     };
 
-    // DOWN: weights do not depend on the launch before, activations (h) do.  So the first steps of the
-    // loop below only copy: weights, then, after the wait, what meets them
     const int pre = depth - 1;
-    int warm = DN ? 2 * pre : pre;
-    const Walk first = f;
-    auto after_wait = [&]() {
-      pdl_wait();
-      pdl_launch_dependents();
-      if constexpr (I8) {
 #pragma unroll 1
-        for (int i = threadIdx.x; i < P; i += W * 32) {
-          const float top = __uint_as_float(__ldcg(p.amax + i));
-          s_xs[i] = __fdiv_rn(top, 127.f);
-          s_inv[i] = code_factor(top);
-        }
-        __syncthreads();
-        // every CTA has read the maxima once all have counted in: they are zero for the next call
-        if (threadIdx.x == 0) {
-          __threadfence();
-          s_entries = atomicAdd(p.tickets + gridDim.x, 1u) == gridDim.x - 1;
-        }
-        __syncthreads();
-        if (s_entries) {
-          for (int i = threadIdx.x; i < P; i += W * 32) p.amax[i] = 0u;
-          if (threadIdx.x == 0) p.tickets[gridDim.x] = 0u;
-        }
+    for (int d = 0; d < pre; ++d) {
+      if (f.u < u1) {
+        target();
+        fetch_w(ring + d * stage);
+        fetch_x(ring + d * stage);
       }
-    };
+      cp_commit();
+      f.next(W, nblk, ne);
+    }
 
     Walk c, n;  // the unit to compute, and the one after it
     c.set(u0 + warp, nblk, ne);
@@ -393,66 +301,54 @@ __global__ void __launch_bounds__((compute_warps(FMT, NT) + 1) * 32, 1)
     int done = item0, c_item = -1;
     bool mine = false;  // a unit of item `done` has been added
     float inv[NT] = {};
-    uint32_t slot = 0;
+    uint32_t slot = 0, to_slot = pre;
     const int cap_t = xt - 1;
     if (c.u < u1) scales(c);
-    uint32_t to_slot = 0;
 #pragma unroll 1
     for (;;) {
-      if (warm == 0) {
-        const int to = c.u < u1 ? c.item : item1 + 1;
+      const int to = c.u < u1 ? c.item : item1 + 1;
 #pragma unroll 1
-        for (; done < to; ++done) {
-          // leave the sums of item `done` to the last warp
-          const int b = (done - item0) % buffers;
-          if (done - item0 >= buffers) bar_sync<kEmpty, THREADS>(b);
-          if (mine) {
-            fold();
-            Sum* s = reinterpret_cast<Sum*>(smem + lay.lists + b * buffer) + warp * xt * kPitch;
+      for (; done < to; ++done) {
+        // leave the sums of item `done` to the last warp
+        const int b = (done - item0) % buffers;
+        if (done - item0 >= buffers) bar_sync<kEmpty, THREADS>(b);
+        if (mine) {
+          fold();
+          Sum* s = reinterpret_cast<Sum*>(smem + lay.lists + b * buffer) + warp * xt * kPitch;
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
+          for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  if (nt * 8 + 2 * t + (i & 1) < xt)
-                    s[(nt * 8 + 2 * t + (i & 1)) * kPitch + mt * 16 + g + 8 * (i >> 1)] = acc[mt][nt][i];
-                  acc[mt][nt][i] = 0;
-                }
-            mine = false;
-          }
-          bar_arrive<kFull, THREADS>(b);
+              for (int i = 0; i < 4; ++i) {
+                if (nt * 8 + 2 * t + (i & 1) < xt)
+                  s[(nt * 8 + 2 * t + (i & 1)) * kPitch + mt * 16 + g + 8 * (i >> 1)] = acc[mt][nt][i];
+                acc[mt][nt][i] = 0;
+              }
+          mine = false;
         }
-        if (c.u >= u1) break;
-        mine = true;
-        if (I8 && !LIN && c.item != c_item) {
-          c_item = c.item;
-          const auto en = entry(c.a);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            inv[nt] = s_inv[s_row[en.first + min(nt * 8 + g, en.count - 1)]];
-          }
-        }
-        cp_wait(pre - 1);
-        __syncwarp();  // every lane's copies of this unit have landed, and the unit before is read
-      } else if (DN && warm == pre) {
-        after_wait();
-        f = first;
-        to_slot = 0;
+        bar_arrive<kFull, THREADS>(b);
       }
+      if (c.u >= u1) break;
+      mine = true;
+      if (I8 && !LIN && c.item != c_item) {
+        c_item = c.item;
+        const auto en = entry(c.a);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          inv[nt] = s_inv[l.tok[en.first + min(nt * 8 + g, en.count - 1)]];
+        }
+      }
+      cp_wait(pre - 1);
+      __syncwarp();  // every lane's copies of this unit have landed, and the unit before is read
       if (f.u < u1) {
         target();
-        const uint32_t at = ring + to_slot * stage;
-        if (!DN || warm == 0 || warm > pre) fetch_w(at);
-        if (!DN || warm <= pre) fetch_x(at);
+        fetch_w(ring + to_slot * stage);
+        fetch_x(ring + to_slot * stage);
       }
-      if (!DN || warm <= pre) cp_commit();
-      if (++to_slot == (uint32_t)depth) to_slot = 0;
+      cp_commit();
       f.next(W, nblk, ne);
-      if (warm > 0) {
-        --warm;
-        continue;
-      }
+      if (++to_slot == (uint32_t)depth) to_slot = 0;
       const uint32_t wat = ring + slot * stage + g * WB, xat = ring + slot * stage + R * WB;
       if (++slot == (uint32_t)depth) slot = 0;
       uint32_t sz[2][NS];  // a scale leaves the low bits of its fp32 image free for the zero point
@@ -587,18 +483,8 @@ __global__ void __launch_bounds__((compute_warps(FMT, NT) + 1) * 32, 1)
     }
   } else {
     // ---------------------------------------------------------------- sums and results: rows lane, lane + 32
-    if (DN) {
-      pdl_wait();
-      for (int i = lane; i < P; i += 32) s_wt[i] = reinterpret_cast<const float*>(p.handed)[i];
-      __syncwarp();
-      if (I8) {
-        __syncthreads();
-        __syncthreads();
-      }
-    }
-    const int slot_floats = (DN ? p.M : TT) * R;
     // 0: the part of an item that began in an earlier CTA, 1: of one that ends in a later CTA
-    auto slot_of = [&](int cta, int tail) { return p.slots + ((int64_t)cta * 2 + tail) * slot_floats; };
+    auto slot_of = [&](int cta, int tail) { return p.slots + ((int64_t)cta * 2 + tail) * (TT * R); };
     // counts a part of the item of units [a, b) in; true for the last one, which finds all parts stored
     auto last_part = [&](int a, int b) {
       const int c0 = a / share, c1 = (b - 1) / share;
@@ -616,8 +502,6 @@ __global__ void __launch_bounds__((compute_warps(FMT, NT) + 1) * 32, 1)
     const int item0 = u0 / nblk, item1 = u1 > u0 ? (u1 - 1) / nblk : item0 - 1;
     Walk c;
     c.set(item0 * nblk, nblk, ne);
-    if (DN)
-      for (int i = lane; i < p.M * R; i += 32) s_y[i] = 0.f;
 #pragma unroll 1
     for (int it = item0; it <= item1; ++it) {
       const auto en = entry(c.a);
@@ -638,7 +522,7 @@ __global__ void __launch_bounds__((compute_warps(FMT, NT) + 1) * 32, 1)
         }
       };
       // an item that is shared with other CTAs: the last of them adds the parts in the order of K
-      const bool parts = !DN && (it * nblk < u0 || (it + 1) * nblk > u1);
+      const bool parts = it * nblk < u0 || (it + 1) * nblk > u1;
       bool ready = true;
       if (parts) {
         Sum* mine = reinterpret_cast<Sum*>(slot_of(blockIdx.x, it * nblk >= u0)) + lane;
@@ -693,9 +577,9 @@ __global__ void __launch_bounds__((compute_warps(FMT, NT) + 1) * 32, 1)
         own(k, v);
         float f[2] = {(float)v[0], (float)v[1]};
         if constexpr (GU) {
-          const int pair = s_pair[en.first + k];
+          const int pair = l.pair[en.first + k];
           if constexpr (I8) {
-            const float xs = s_xs[s_tok[en.first + k]];
+            const float xs = s_xs[l.tok[en.first + k]];
             f[0] = f[0] * xs * ws[0];
             f[1] = f[1] * xs * ws[1];
           }
@@ -705,17 +589,6 @@ __global__ void __launch_bounds__((compute_warps(FMT, NT) + 1) * 32, 1)
             const unsigned top = __reduce_max_sync(0xffffffffu, n < p.N ? (unsigned)(hb & 0x7FFF) << 16 : 0u);
             if (lane == 0) atomicMax(p.amax + pair, top);
           }
-        } else if constexpr (DN) {
-          const int pair = s_pair[en.first + k];
-          const float wt = s_wt[pair];
-          float* y = s_y + s_tok[en.first + k] * R + lane;
-          if constexpr (I8) {
-            const float xs = s_xs[pair];
-            f[0] = f[0] * xs * ws[0];
-            f[1] = f[1] * xs * ws[1];
-          }
-          y[0] += wt * f[0];
-          y[32] += wt * f[1];
         } else {
           const int m = en.first + k;
           const float xs = p.x_scale[m];
@@ -740,58 +613,10 @@ __global__ void __launch_bounds__((compute_warps(FMT, NT) + 1) * 32, 1)
       }
       __syncwarp();
       if (it + buffers <= item1) bar_arrive<kEmpty, THREADS>(b);
-      if (DN && (it == item1 || c.a == ne - 1)) {
-        // the end of this CTA's part of the tile
-        const int a = c.tile * whole;
-        const bool shared = a < u0 || a + whole > u1;
-        float4* y4 = reinterpret_cast<float4*>(s_y);
-        __syncwarp();
-        for (int i = lane; i < p.M * (R / 4); i += 32) {
-          if (shared)
-            __stcg(reinterpret_cast<float4*>(slot_of(blockIdx.x, a >= u0)) + i, y4[i]);
-          else
-            put4(p, c.tile, i, y4[i]);
-          y4[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-        __syncwarp();
-      }
       c.next(nblk, nblk, ne);
     }
   }
-  if constexpr (DN) {
-    // At most two tiles, the first and the last, have parts in other CTAs: the last CTA of each adds the
-    // parts in the order of K
-    __shared__ int s_last[2];
-    auto slot_of = [&](int cta, int tail) { return p.slots + ((int64_t)cta * 2 + tail) * (p.M * R); };
-    const int tile0 = u0 / whole, tile1 = u1 > u0 ? (u1 - 1) / whole : tile0 - 1;
-    const bool cut0 = tile0 <= tile1 && (tile0 * whole < u0 || (tile0 + 1) * whole > u1);
-    const bool cut1 = tile1 > tile0 && (tile1 + 1) * whole > u1;
-    __threadfence();
-    __syncthreads();
-    if (threadIdx.x < 64 && lane == 0) {
-      const int tile = warp ? tile1 : tile0;
-      bool last = false;
-      if (warp ? cut1 : cut0) {
-        const int c0 = tile * whole / share, c1 = ((tile + 1) * whole - 1) / share;
-        last = atomicAdd(p.tickets + c0, 1u) == (unsigned)(c1 - c0);
-        if (last) p.tickets[c0] = 0u;
-      }
-      s_last[warp] = last;
-    }
-    __syncthreads();
-    if (!s_last[0] && !s_last[1]) return;
-    __threadfence();  // the other parts were fenced before their counts
-    const int quads = p.M * (R / 4);
-#pragma unroll 1
-    for (int i = threadIdx.x; i < 2 * quads; i += THREADS) {
-      const int which = i >= quads, at = i - which * quads;
-      if (!s_last[which]) continue;
-      const int tile = which ? tile1 : tile0;
-      put4(p, tile, at, add_parts(slot_of, tile * whole / share, ((tile + 1) * whole - 1) / share, at));
-    }
-  }
 }
-
 
 template <int FMT, int MODE, int NT, bool FINE, bool ZP>
 cudaError_t launch(const StreamArgs& a, cudaStream_t st) {
@@ -801,9 +626,7 @@ cudaError_t launch(const StreamArgs& a, cudaStream_t st) {
   if (const cudaError_t e = raise_smem_limit(kfn, once); e != cudaSuccess) return e;
   const int P = MODE == STREAM_LINEAR ? 0 : a.M * a.topk;
   Layout l = {};
-  l.lists = P * (int)(sizeof(Entry) + 4 + 2 * 2 + (MODE == STREAM_DOWN ? 4 : 0) + (FMT == STREAM_INT8 ? 8 : 0)) +
-            (MODE == STREAM_DOWN ? a.M * R * 4 : 0);
-  l.lists = (l.lists + 127) & ~127;
+  l.lists = (P * (int)(sizeof(Entry) + 4 + 2 * 2) + (FMT == STREAM_INT8 ? kMoeMaxTokens * 8 : 0) + 127) & ~127;
   l.total = 227 * 1024 - 1024;
   // two stages with the most tokens an entry can have (64 tokens, 16 experts each: 2.05)
   if ((l.total - l.lists - W * TT * kPitch * 4 - 128) / (W * (R * row_bytes(FMT) + TT * token_bytes(FMT, MODE))) < 2)
@@ -821,15 +644,6 @@ cudaError_t launch(const StreamArgs& a, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, kfn, a, l);
 }
 
-template <int MODE>
-cudaError_t launch_moe(int fmt, const StreamArgs& a, cudaStream_t st) {
-  if (fmt == STREAM_BF16) return launch<STREAM_BF16, MODE, 1, false, false>(a, st);
-  if (fmt == STREAM_INT8) return launch<STREAM_INT8, MODE, 1, false, false>(a, st);
-  if (a.group_shift < 7)
-    return a.zero ? launch<STREAM_INT4, MODE, 1, true, true>(a, st) : launch<STREAM_INT4, MODE, 1, true, false>(a, st);
-  return a.zero ? launch<STREAM_INT4, MODE, 1, false, true>(a, st) : launch<STREAM_INT4, MODE, 1, false, false>(a, st);
-}
-
 }  // namespace
 
 size_t stream_slot_bytes(int64_t M) {
@@ -837,9 +651,16 @@ size_t stream_slot_bytes(int64_t M) {
   return (size_t)kNumSMs * 2 * columns * R * 4;
 }
 
-cudaError_t launch_stream(int fmt, int mode, const StreamArgs& a, cudaStream_t st) {
-  if (mode == STREAM_GATE_UP) return launch_moe<STREAM_GATE_UP>(fmt, a, st);
-  if (mode == STREAM_DOWN) return launch_moe<STREAM_DOWN>(fmt, a, st);
+cudaError_t launch_gate_up(int fmt, const StreamArgs& a, cudaStream_t st) {
+  constexpr int GU = STREAM_GATE_UP;
+  if (fmt == STREAM_BF16) return launch<STREAM_BF16, GU, 1, false, false>(a, st);
+  if (fmt == STREAM_INT8) return launch<STREAM_INT8, GU, 1, false, false>(a, st);
+  if (a.group_shift < 7)
+    return a.zero ? launch<STREAM_INT4, GU, 1, true, true>(a, st) : launch<STREAM_INT4, GU, 1, true, false>(a, st);
+  return a.zero ? launch<STREAM_INT4, GU, 1, false, true>(a, st) : launch<STREAM_INT4, GU, 1, false, false>(a, st);
+}
+
+cudaError_t launch_linear(const StreamArgs& a, cudaStream_t st) {
   if (a.M <= 8) return launch<STREAM_INT8, STREAM_LINEAR, 1, false, false>(a, st);
   return launch<STREAM_INT8, STREAM_LINEAR, 2, false, false>(a, st);
 }

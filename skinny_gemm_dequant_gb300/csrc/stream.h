@@ -9,12 +9,12 @@
 namespace ql {
 
 enum { STREAM_BF16 = 0, STREAM_INT8 = 1, STREAM_INT4 = 2 };
-enum { STREAM_GATE_UP = 0, STREAM_DOWN = 1, STREAM_LINEAR = 2 };
+enum { STREAM_GATE_UP = 0, STREAM_LINEAR = 1 };
 
 constexpr int kStreamRows = 64;       // weight rows of a tile
 constexpr int kMoeMaxTokens = 64;     // of a mixture-of-experts call
 constexpr int kMoeMaxTopk = 16;
-constexpr int kMoeHandedBytes = 8192;
+constexpr int kMoeHandedBytes = 16640;
 constexpr int kStreamMaxTokens = 16;  // of a linear call
 
 struct StreamArgs {
@@ -40,7 +40,8 @@ struct StreamArgs {
   float alpha, limit;
   uint16_t* h;  // GATE_UP writes bf16 [M topk, ldh]
   int64_t ldh;
-  void* handed;       // kMoeHandedBytes that GATE_UP writes for DOWN: weights by pair, up to 16 tokens lists too
+  void* handed;       // kMoeHandedBytes that GATE_UP writes for DOWN (moe_dispatch.cuh)
+  float* heads;       // DOWN: down_head_bytes
   unsigned* amax;     // INT8: [M topk] bits of max|h|, zero between calls
   unsigned* tickets;  // zero between calls
   float* slots;       // sums of tiles that CTAs share
@@ -55,11 +56,14 @@ struct StreamArgs {
 // codes and scales of tokens (kernels_codes.cu)
 cudaError_t launch_token_codes(const uint16_t* x, int64_t M, int64_t K, int64_t ldx, int8_t* codes, float* scale,
                                cudaStream_t st);
-cudaError_t launch_stream(int fmt, int mode, const StreamArgs& a, cudaStream_t st);
-// the launches of kernels_moe_few.cu, where they take a call: GATE_UP while the tokens fit in shared memory,
-// DOWN up to 16 of these tokens
-bool moe_few_takes(int fmt, int mode, const StreamArgs& gate_up);
-cudaError_t launch_moe_few(int fmt, int mode, const StreamArgs& a, cudaStream_t st);
+// kernels_stream.cu: GATE_UP of any call, LINEAR of up to kStreamMaxTokens
+cudaError_t launch_gate_up(int fmt, const StreamArgs& a, cudaStream_t st);
+cudaError_t launch_linear(const StreamArgs& a, cudaStream_t st);
+// kernels_moe_few.cu: GATE_UP while the tokens fit in shared memory, DOWN
+bool gate_up_few_takes(int fmt, const StreamArgs& a);
+cudaError_t launch_gate_up_few(int fmt, const StreamArgs& a, cudaStream_t st);
+cudaError_t launch_down(int fmt, const StreamArgs& a, cudaStream_t st);
+size_t down_head_bytes(int64_t M);
 size_t stream_slot_bytes(int64_t M);
 // of QL_OP_INT8_CODES and QL_OP_MOE_FEW (api_stream.cu)
 size_t stream_workspace_bytes(int op, int64_t M, int64_t N, int64_t K, int E, int topk);
