@@ -26,8 +26,7 @@ namespace ql {
 namespace {
 
 constexpr int kGuWarps = 16;
-constexpr int R = kStreamRows;
-constexpr int kPitch = R + 4;  // of a column of sums: lanes (g, t) write 8 t + g, all banks once
+constexpr int kDnRows = 32, kDnFew = 20;  // DOWN: rows of a tile; tokens that leave 4-bit weights 16 warps
 constexpr int kSmem = 226 * 1024;
 constexpr int kStage = 16 * 128, kDepth = 4;  // a ring of GATE_UP: bytes of a stage, stages
 // shared memory of GATE_UP for lists; the tokens have the rest
@@ -389,7 +388,7 @@ __global__ void __launch_bounds__(kGuWarps * 32, 1)
 template <int FMT, int W, bool FINE, bool ZP>
 __global__ void __launch_bounds__(W * 32, 1) down_kernel(const __grid_constant__ StreamArgs p, int lists) {
   constexpr bool I8 = FMT == STREAM_INT8, I4 = FMT == STREAM_INT4;
-  constexpr int THREADS = W * 32, MT = R / 16;
+  constexpr int R = kDnRows, THREADS = W * 32, MT = R / 16, kPitch = R + 4;
   constexpr int KU = FMT == STREAM_BF16 ? 64 : 128, WB = I4 ? 64 : 128, XB = FMT == STREAM_BF16 ? 128 : 256;
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -495,21 +494,19 @@ __global__ void __launch_bounds__(W * 32, 1) down_kernel(const __grid_constant__
     }
   };
 
-  // scales of a unit (4-bit) or of an entry (8-bit): a lane reads those of rows lane and lane + 32
+  // scales of a unit (4-bit) or of an entry (8-bit): a lane reads those of row `lane` of the tile
+  static_assert(R == 32, "a row for each lane");
   constexpr int NS = FINE ? 4 : 1;
-  uint16_t s_next[2][NS];  // as loaded: turning them into numbers here would wait for them
-  uint8_t z_next[2][NS];
-  const uint16_t* sp[2] = {};
-  const uint8_t* zp[2] = {};
+  uint16_t s_next[NS];  // as loaded: turning them into numbers here would wait for them
+  uint8_t z_next[NS];
+  const uint16_t* sp = nullptr;
+  const uint8_t* zp = nullptr;
   auto scale_rows = [&](const At& w) {
     if constexpr (I4) {
       const int e = entries[w.a].expert;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int64_t row = min(w.tile * R + lane + 32 * h, p.N - 1);
-        sp[h] = reinterpret_cast<const uint16_t*>(p.scale) + e * p.s_estride + row * p.lds;
-        if (ZP) zp[h] = p.zero + e * p.z_estride + row * p.ldz;
-      }
+      const int64_t n = min(w.tile * R + lane, p.N - 1);
+      sp = reinterpret_cast<const uint16_t*>(p.scale) + e * p.s_estride + n * p.lds;
+      if (ZP) zp = p.zero + e * p.z_estride + n * p.ldz;
     }
   };
   auto scales = [&](int kb) {
@@ -518,11 +515,8 @@ __global__ void __launch_bounds__(W * 32, 1) down_kernel(const __grid_constant__
       for (int j = 0; j < NS; ++j) {
         const int k = kb * KU + j * 32;
         const int gi = min(k, p.K - 1) >> p.group_shift;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          s_next[h][j] = k < p.K ? sp[h][gi] : (uint16_t)0;  // past the end: sums of zeros
-          if (ZP) z_next[h][j] = zp[h][gi];
-        }
+        s_next[j] = k < p.K ? sp[gi] : (uint16_t)0;  // past the end: sums of zeros
+        if (ZP) z_next[j] = zp[gi];
       }
     }
   };
@@ -549,7 +543,7 @@ __global__ void __launch_bounds__(W * 32, 1) down_kernel(const __grid_constant__
   uint32_t slot = 0, to_slot = pre;
   int count = 0, row = 0, first = 0;  // the entry's pairs; this lane's B column among them
   float inv = 0.f;
-  float ws[2] = {1.f, 1.f};
+  float ws = 0.f;
   auto enter = [&]() {
     const Entry en = entries[c.a];
     count = en.count;
@@ -557,9 +551,8 @@ __global__ void __launch_bounds__(W * 32, 1) down_kernel(const __grid_constant__
     row = min(g, count - 1);
     if constexpr (I8) {
       inv = s_inv[s_pair[first + row]];
-      const float* s = reinterpret_cast<const float*>(p.scale) + en.expert * p.s_estride + c.tile * R + lane;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) ws[h] = c.tile * R + lane + 32 * h < p.N ? s[32 * h] : 0.f;
+      const int n = c.tile * R + lane;
+      ws = n < p.N ? reinterpret_cast<const float*>(p.scale)[en.expert * p.s_estride + n] : 0.f;
     }
   };
   // an entry's sums, times the tokens' weights, into the tile's results: a lane has its own rows of columns
@@ -570,7 +563,7 @@ __global__ void __launch_bounds__(W * 32, 1) down_kernel(const __grid_constant__
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
       for (int h = 0; h < 2; ++h)
-        sc[mt][h] = I8 ? __shfl_sync(0xffffffffu, ws[mt / 2], mt % 2 * 16 + h * 8 + g) : I4 ? 64.f : 1.f;
+        sc[mt][h] = I8 ? __shfl_sync(0xffffffffu, ws, mt * 16 + h * 8 + g) : I4 ? 64.f : 1.f;
 #pragma unroll
     for (int q = 0; q < 2; ++q)
       if (2 * t + q < count) {
@@ -630,19 +623,17 @@ __global__ void __launch_bounds__(W * 32, 1) down_kernel(const __grid_constant__
     if (++to_slot == (uint32_t)depth) to_slot = 0;
     const uint32_t wat = ring + slot * stage + g * WB, xat = ring + slot * stage + R * WB + row * XB;
     if (++slot == (uint32_t)depth) slot = 0;
-    float scl[2][NS];  // scale and zero point (as bf16x2 of -z / 64) of this lane's rows
-    uint32_t nzl[2][NS];
+    float scl[NS];  // scale and zero point (as bf16x2 of -z / 64) of this lane's rows
+    uint32_t nzl[NS];
     At n = c;
     next(n);
     if constexpr (I4) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int j = 0; j < NS; ++j) {
-          scl[h][j] = p.scale_fp16 ? __half2float(__ushort_as_half(s_next[h][j])) : bf16_bits_to_f32(s_next[h][j]);
-          // z's pattern stands for z 2^-133, times -2^127
-          if (ZP) nzl[h][j] = fma_bf16x2(z_next[h][j] * 0x10001u, 0xFF00FF00u, 0u);
-        }
+      for (int j = 0; j < NS; ++j) {
+        scl[j] = p.scale_fp16 ? __half2float(__ushort_as_half(s_next[j])) : bf16_bits_to_f32(s_next[j]);
+        // z's pattern stands for z 2^-133, times -2^127
+        if (ZP) nzl[j] = fma_bf16x2(z_next[j] * 0x10001u, 0xFF00FF00u, 0u);
+      }
       if (n.u < v1) {
         if (n.kb == 0) scale_rows(n);
         scales(n.kb);
@@ -678,8 +669,8 @@ __global__ void __launch_bounds__(W * 32, 1) down_kernel(const __grid_constant__
           if (j == 0 || FINE) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              sc[h] = __shfl_sync(0xffffffffu, scl[mt / 2][FINE ? j : 0], mt % 2 * 16 + h * 8 + g);
-              negz[h] = ZP ? __shfl_sync(0xffffffffu, nzl[mt / 2][FINE ? j : 0], mt % 2 * 16 + h * 8 + g) : 0xBE00BE00u;
+              sc[h] = __shfl_sync(0xffffffffu, scl[FINE ? j : 0], mt * 16 + h * 8 + g);
+              negz[h] = ZP ? __shfl_sync(0xffffffffu, nzl[FINE ? j : 0], mt * 16 + h * 8 + g) : 0xBE00BE00u;
             }
           }
           uint32_t q0[4], q1[4];
@@ -811,7 +802,7 @@ __global__ void __launch_bounds__(W * 32, 1) down_kernel(const __grid_constant__
     const int which = i >= quads, at = i - which * quads;
     if (!s_last[which]) continue;
     const int tile = which ? tile1 : tile0;
-    put4(p, tile, at, add_parts(slot_of, tile * whole / share, ((tile + 1) * whole - 1) / share, at));
+    put4<R>(p, tile, at, add_parts(slot_of, tile * whole / share, ((tile + 1) * whole - 1) / share, at));
   }
 }
 
@@ -841,7 +832,7 @@ cudaError_t launch_dn(const StreamArgs& a, cudaStream_t st) {
   static OncePerDevice once;
   if (const cudaError_t e = raise_smem_limit(kfn, once); e != cudaSuccess) return e;
   const int P = a.M * a.topk;
-  const int lists = (W * a.M * kPitch * 4 + P * (int)(sizeof(Entry) + 2 * 4 + 2 * 2) + 127) & ~127;
+  const int lists = (W * a.M * (kDnRows + 4) * 4 + P * (int)(sizeof(Entry) + 2 * 4 + 2 * 2) + 127) & ~127;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(kNumSMs, 1, 1);
   cfg.blockDim = dim3(W * 32, 1, 1);
@@ -855,28 +846,24 @@ cudaError_t launch_dn(const StreamArgs& a, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, kfn, a, lists);
 }
 
-// Warps of DOWN: what leaves each a ring of two stages with 8 tokens beside the results of all tokens
+// Warps of DOWN: what leaves each a ring of two stages with 8 tokens beside the results of all
 template <int FMT>
 __host__ __device__ constexpr int dn_warps(int tokens) {
-  constexpr bool I4 = FMT == STREAM_INT4;
-  return tokens <= 4 && I4 ? 16 : tokens <= 20 ? (I4 ? 12 : 8) : tokens <= 40 ? (I4 ? 9 : 6) : I4 ? 7 : 5;
+  return FMT != STREAM_INT4 ? 8 : tokens <= kDnFew ? 16 : 12;
 }
 template <int FMT>
 constexpr bool dn_fits(int tokens) {
-  const int stage = R * (FMT == STREAM_INT4 ? 64 : 128) + (tokens < 8 ? tokens : 8) * (FMT == STREAM_BF16 ? 128 : 256);
-  return dn_warps<FMT>(tokens) * (tokens * kPitch * 4 + 2 * stage) + tokens * kMoeMaxTopk * 20 + 128 <= kSmem;
+  constexpr int WB = FMT == STREAM_INT4 ? 64 : 128, XB = FMT == STREAM_BF16 ? 128 : 256;
+  const int stage = kDnRows * WB + 8 * XB;
+  return dn_warps<FMT>(tokens) * (tokens * (kDnRows + 4) * 4 + 2 * stage) + tokens * kMoeMaxTopk * 20 + 128 <= kSmem;
 }
-static_assert(dn_fits<STREAM_INT4>(4) && dn_fits<STREAM_INT4>(20) && dn_fits<STREAM_INT4>(40) &&
-                  dn_fits<STREAM_INT4>(64) && dn_fits<STREAM_INT8>(20) && dn_fits<STREAM_INT8>(40) &&
-                  dn_fits<STREAM_INT8>(64),
+static_assert(dn_fits<STREAM_INT4>(kDnFew) && dn_fits<STREAM_INT4>(kMoeMaxTokens) && dn_fits<STREAM_INT8>(kMoeMaxTokens),
               "two stages for every warp");
 
 template <int FMT, bool FINE, bool ZP>
 cudaError_t launch_dn_warps(const StreamArgs& a, cudaStream_t st) {
-  if (FMT == STREAM_INT4 && a.M <= 4) return launch_dn<FMT, dn_warps<FMT>(4), FINE, ZP>(a, st);
-  if (a.M <= 20) return launch_dn<FMT, dn_warps<FMT>(20), FINE, ZP>(a, st);
-  if (a.M <= 40) return launch_dn<FMT, dn_warps<FMT>(40), FINE, ZP>(a, st);
-  return launch_dn<FMT, dn_warps<FMT>(64), FINE, ZP>(a, st);
+  if (FMT == STREAM_INT4 && a.M <= kDnFew) return launch_dn<FMT, dn_warps<FMT>(kDnFew), FINE, ZP>(a, st);
+  return launch_dn<FMT, dn_warps<FMT>(kMoeMaxTokens), FINE, ZP>(a, st);
 }
 
 // bytes of GATE_UP's tokens in shared memory
@@ -911,7 +898,7 @@ cudaError_t launch_down(int fmt, const StreamArgs& a, cudaStream_t st) {
 }
 
 size_t down_head_bytes(int64_t M) {
-  return (size_t)kNumSMs * dn_warps<STREAM_INT4>((int)M) * M * R * 4;  // (the most of all types)
+  return (size_t)kNumSMs * dn_warps<STREAM_INT4>((int)M) * M * kDnRows * 4;  // the most of all types
 }
 
 }  // namespace ql

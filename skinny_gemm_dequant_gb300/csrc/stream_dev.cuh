@@ -120,9 +120,10 @@ __device__ __forceinline__ float4 add_parts(Slot slot_of, int c0, int c1, int at
   }
   return y;
 }
+template <int R>
 __device__ __forceinline__ void put4(const StreamArgs& p, int tile, int at, float4 y) {
-  constexpr int Q = kStreamRows / 4;
-  const int row = tile * kStreamRows + at % Q * 4;
+  constexpr int Q = R / 4;
+  const int row = tile * R + at % Q * 4;
   uint16_t* dst = reinterpret_cast<uint16_t*>(p.y) + (int64_t)(at / Q) * p.ldy + row;
   const float v[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
