@@ -15,6 +15,8 @@
 // DOWN: tokens are the columns whatever expert they meet, so a warp adds experts one after the other
 // into the same registers: w_(m,j) is applied where the expert changes.  The units of a 64-row tile
 // are all its experts' K in a row; they are cut evenly over the warps of all CTAs.
+#include <algorithm>
+
 #include "common.cuh"
 #include "ffn_act.cuh"
 #include "moe_dispatch.cuh"
@@ -28,7 +30,7 @@ namespace {
 constexpr int kGuWarps = 16;
 constexpr int kDnRows = 32, kDnFew = 20;  // DOWN: rows of a tile; tokens that leave 4-bit weights 16 warps
 constexpr int kSmem = 226 * 1024;
-constexpr int kStage = 16 * 128, kDepth = 4;  // a ring of GATE_UP: bytes of a stage, stages
+constexpr int kStage = 16 * 128, kGuDepth = 4;  // GATE_UP's rings: bytes of a stage, stages at most
 // shared memory of GATE_UP for lists; the tokens have the rest
 __host__ __device__ constexpr int gu_list_bytes(int pairs) {
   return (pairs * 16 + kMoeMaxTokens * 4 + 127) & ~127;  // entries, ids, sorted pairs and tokens; scales
@@ -52,9 +54,10 @@ constexpr float kDown69 = 1.6940658945086007e-21f;                       // 2^-6
 constexpr float kUp69 = 590295810358705651712.f;                         // 2^69
 
 // ------------------------------------------------------------------ GATE_UP
-template <int FMT, bool FINE, bool ZP>
+// DEPTH: stages of a ring, or 0: as the argument says
+template <int FMT, int DEPTH, bool FINE, bool ZP>
 __global__ void __launch_bounds__(kGuWarps * 32, 1)
-    gate_up_kernel(const __grid_constant__ StreamArgs p, int x_bytes, int lists) {
+    gate_up_kernel(const __grid_constant__ StreamArgs p, int x_bytes, int lists, int depth_arg) {
   constexpr bool I8 = FMT == STREAM_INT8, I4 = FMT == STREAM_INT4;
   constexpr int KS = gu_k(FMT), XB = FMT == STREAM_BF16 ? 128 : 256;  // k of a stage; bytes of a token's x block
   constexpr int XK = FMT == STREAM_BF16 ? 64 : 128, SB = KS / XK;     // k of an x block; blocks of a stage
@@ -180,9 +183,10 @@ __global__ void __launch_bounds__(kGuWarps * 32, 1)
   }
   ne = p.M == 1 ? s_one : dispatch<kGuWarps>(p, l, kPerEntry, most);
 
+  const int depth = DEPTH > 0 ? DEPTH : depth_arg;
   const int otiles = p.N / 8, total = ne * otiles;
   const int step = (int)gridDim.x * kGuWarps;
-  const uint32_t ring = smem_addr(ring_base) + (uint32_t)(warp * kDepth * kStage);
+  const uint32_t ring = smem_addr(ring_base) + (uint32_t)(warp * depth * kStage);
 
   // a lane copies 16-byte piece cc of rows cr and cr + 4, gate and up
   const int cr = lane >> 3, cc = lane & 7;
@@ -212,7 +216,7 @@ __global__ void __launch_bounds__(kGuWarps * 32, 1)
     cp_commit();
   };
 #pragma unroll 1
-  for (int d = 0; d < kDepth - 1; ++d) fetch(ring + d * kStage);
+  for (int d = 0; d < depth - 1; ++d) fetch(ring + d * kStage);
 
   if constexpr (I8) {  // (the weights are on their way)
     stage_x();
@@ -222,6 +226,7 @@ __global__ void __launch_bounds__(kGuWarps * 32, 1)
   if (blockIdx.x == gridDim.x - 1 && warp == kGuWarps - 2) hand_lists(p, l, ne, most);
   if (gridDim.x - 1 - blockIdx.x < p.M && warp == kGuWarps - 1) hand_weights(p, l, gridDim.x - 1 - blockIdx.x);
 
+  const uint32_t end = (uint32_t)(depth * kStage);
   uint32_t slot = 0;  // byte offset of the stage in the ring
   const uint32_t w0_at = ring + (uint32_t)(g * 128 + wslot(t, g) * 16), w1_at = w0_at ^ 64u;  // pieces t, 4 + t
 #pragma unroll 1
@@ -267,12 +272,12 @@ __global__ void __launch_bounds__(kGuWarps * 32, 1)
     int whole[4] = {};
 #pragma unroll 1
     for (int s = 0; s < nstage; ++s) {
-      asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 2) : "memory");
+      cp_wait(depth - 2);
       __syncwarp();  // every lane's copies of this stage have landed, and the stage before is read
-      fetch(ring + ((slot - kStage) & (kDepth * kStage - 1)));
+      fetch(ring + (slot == 0 ? end : slot) - kStage);
       const uint32_t wa[2] = {w0_at + slot, w1_at + slot};
       const uint32_t wf = ring + slot + g * 128 + t * 4, wx = wslot(0, g) * 16;  // FINE: word t of piece c at c * 16 ^ wx
-      slot = (slot + kStage) & (kDepth * kStage - 1);
+      slot = slot + kStage == end ? 0u : slot + kStage;
       float sc[NS], sz[NS];  // scale, scale times zero point: of this lane's row and block
       if constexpr (I4) {
 #pragma unroll
@@ -806,9 +811,9 @@ __global__ void __launch_bounds__(W * 32, 1) down_kernel(const __grid_constant__
   }
 }
 
-template <int FMT, bool FINE, bool ZP>
-cudaError_t launch_gu(const StreamArgs& a, int x_bytes, cudaStream_t st) {
-  auto* kfn = gate_up_kernel<FMT, FINE, ZP>;
+template <int FMT, int DEPTH, bool FINE, bool ZP>
+cudaError_t launch_gu(const StreamArgs& a, int x_bytes, int depth, cudaStream_t st) {
+  auto* kfn = gate_up_kernel<FMT, DEPTH, FINE, ZP>;
   static OncePerDevice once;
   if (const cudaError_t e = raise_smem_limit(kfn, once); e != cudaSuccess) return e;
   const int P = a.M * a.topk;
@@ -816,14 +821,14 @@ cudaError_t launch_gu(const StreamArgs& a, int x_bytes, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(kNumSMs, 1, 1);
   cfg.blockDim = dim3(kGuWarps * 32, 1, 1);
-  cfg.dynamicSmemBytes = (size_t)(x_bytes + lists + kGuWarps * kDepth * kStage);
+  cfg.dynamicSmemBytes = (size_t)(x_bytes + lists + kGuWarps * depth * kStage);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kfn, a, x_bytes, lists);
+  return cudaLaunchKernelEx(&cfg, kfn, a, x_bytes, lists, depth);
 }
 
 template <int FMT, int W, bool FINE, bool ZP>
@@ -874,19 +879,32 @@ int64_t gu_x_bytes(int fmt, const StreamArgs& a) {
   return (b + 127) & ~int64_t(127);
 }
 
-}  // namespace
-
-bool gate_up_few_takes(int fmt, const StreamArgs& a) {
-  return gu_x_bytes(fmt, a) + gu_list_bytes(a.M * a.topk) + kGuWarps * kDepth * kStage <= kSmem;
+// stages of GATE_UP's rings beside the tokens
+int gu_depth(int fmt, const StreamArgs& a) {
+  const int64_t left = kSmem - gu_x_bytes(fmt, a) - gu_list_bytes(a.M * a.topk);
+  return left < 0 ? 0 : (int)std::min<int64_t>(kGuDepth, left / (kGuWarps * kStage));
 }
 
+template <bool FINE, bool ZP>
+cudaError_t launch_gu_int4(const StreamArgs& a, int x, int depth, cudaStream_t st) {
+  if (depth == kGuDepth) return launch_gu<STREAM_INT4, kGuDepth, FINE, ZP>(a, x, depth, st);
+  return launch_gu<STREAM_INT4, 0, FINE, ZP>(a, x, depth, st);
+}
+
+}  // namespace
+
+// 4-bit weights: rings of two or three stages too.  8 of 256 experts of 2048x4096, this kernel and
+// stream_kernel: 12 tokens (3 stages) 207 and 280 us, 18 tokens (2 stages) 297 and 373 us; bf16: 15
+// tokens (3) 747 and 707 us, 18 tokens (2) 984 and 801 us; 8-bit: 18 tokens (2) 522 and 459 us.
+bool gate_up_few_takes(int fmt, const StreamArgs& a) { return gu_depth(fmt, a) >= (fmt == STREAM_INT4 ? 2 : kGuDepth); }
+
 cudaError_t launch_gate_up_few(int fmt, const StreamArgs& a, cudaStream_t st) {
-  const int x = (int)gu_x_bytes(fmt, a);
-  if (fmt == STREAM_BF16) return launch_gu<STREAM_BF16, false, false>(a, x, st);
-  if (fmt == STREAM_INT8) return launch_gu<STREAM_INT8, false, false>(a, x, st);
+  const int x = (int)gu_x_bytes(fmt, a), d = gu_depth(fmt, a);
+  if (fmt == STREAM_BF16) return launch_gu<STREAM_BF16, kGuDepth, false, false>(a, x, d, st);
+  if (fmt == STREAM_INT8) return launch_gu<STREAM_INT8, kGuDepth, false, false>(a, x, d, st);
   if (a.group_shift < 7)
-    return a.zero ? launch_gu<STREAM_INT4, true, true>(a, x, st) : launch_gu<STREAM_INT4, true, false>(a, x, st);
-  return a.zero ? launch_gu<STREAM_INT4, false, true>(a, x, st) : launch_gu<STREAM_INT4, false, false>(a, x, st);
+    return a.zero ? launch_gu_int4<true, true>(a, x, d, st) : launch_gu_int4<true, false>(a, x, d, st);
+  return a.zero ? launch_gu_int4<false, true>(a, x, d, st) : launch_gu_int4<false, false>(a, x, d, st);
 }
 
 cudaError_t launch_down(int fmt, const StreamArgs& a, cudaStream_t st) {

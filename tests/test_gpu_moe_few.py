@@ -242,6 +242,25 @@ def test_rows_too_long_for_shared_memory(ql, fmt, M, E, topk, H, I):
     check(layer, x, layer(ql, x, router_logits=logits, topk=topk, debug=True), logits=logits, topk=topk)
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "int8", "int4"])
+@pytest.mark.parametrize("M,E,topk,H,I", [(4, 2, 1, 32768, 32), (4, 2, 2, 32768, 32), (3, 3, 2, 32736, 416), (21, 3, 3, 24608, 160)])
+def test_wide_outputs(ql, fmt, M, E, topk, H, I):
+    """Down: warps that hold whole tiles, parts of two, and both."""
+    layer = Layer(fmt, E, H, I, seed=M, group=128)
+    x = tokens(M, H, seed=M, fmt=fmt)
+    logits = torch.randn(M, E, generator=torch.Generator().manual_seed(M)).to(torch.bfloat16).cuda()
+    check(layer, x, layer(ql, x, router_logits=logits, topk=topk, debug=True), logits=logits, topk=topk)
+
+
+@pytest.mark.parametrize("M,H", [(12, 4096), (18, 4096), (24, 2080), (20, 2080)])
+@pytest.mark.parametrize("group,zeros", [(32, True), (32, False), (128, True), (128, False)])
+def test_int4_many_tokens_in_shared_memory(ql, M, H, group, zeros):
+    layer = Layer("int4", 4, H, 96, seed=M, group=group, zeros=zeros)
+    x = tokens(M, H, seed=M)
+    logits = torch.randn(M, 4, generator=torch.Generator().manual_seed(M)).to(torch.bfloat16).cuda()
+    check(layer, x, layer(ql, x, router_logits=logits, topk=2, debug=True), logits=logits, topk=2)
+
+
 @pytest.mark.parametrize("M", [1, 6, 24])
 @pytest.mark.parametrize("fmt", ["bf16", "int8", "int4"])
 def test_graphs_streams_and_threads(ql, fmt, M):
