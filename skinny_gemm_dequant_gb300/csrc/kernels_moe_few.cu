@@ -1,4 +1,4 @@
-// The two launches of a mixture-of-experts layer for up to 16 tokens (bf16, 8-bit and 4-bit weights).
+// The two launches of a mixture-of-experts layer for up to 64 tokens (bf16, 8-bit and 4-bit weights).
 //
 //   GATE_UP  g = W13[e][0:I] x_m, u = W13[e][I:2I] x_m for every routed pair (m, j) with expert e,
 //            h = bf16( silu(a min(g, L)) clamp(u, -L, L) )
@@ -7,14 +7,31 @@
 // 8-bit weights: tokens (GATE_UP) and h (DOWN) are quantised here, scale = max|v| / 127 over the
 // row, code = v / scale rounded half to even; products of codes are exact in fp32, sums of
 // 1024 k too.  4-bit weights: no weight is rounded, a group's fp32 sum is multiplied by its scale once.
+// h is rounded to bf16 once (the products' operand); all sums are fp32 or whole numbers.
 //
-// Both kernels are persistent, one CTA per SM, and stream every chosen expert's weights once through
-// rings of the warps' own (cp.async), the weights as the warp MMA's A operand and tokens as its columns.
-// GATE_UP: all tokens stay in shared memory as MMA operands; a warp takes 8 gate rows and the 8 up rows
-// of the same outputs over the whole K, so that nothing is joined and h is made in its registers.
-// DOWN: tokens are the columns whatever expert they meet, so a warp adds experts one after the other
-// into the same registers: w_(m,j) is applied where the expert changes.  The units of a 64-row tile
-// are all its experts' K in a row; they are cut evenly over the warps of all CTAs.
+// Both kernels are persistent, one CTA per SM, and stream a chosen expert's weights once for 8 of its
+// tokens through rings of the warps' own (cp.async: no warp waits for another), the weights as the warp
+// MMA's A operand and tokens as its columns.  At these counts of tokens the tensor cores idle either way
+// and what counts is the bytes in flight.
+// GATE_UP: all tokens stay in shared memory as MMA operands (where they do not fit, the launch of
+// kernels_stream.cu takes over: gate_up_few_takes); a warp takes 8 gate rows and the 8 up rows of the same
+// outputs over the whole K, so that nothing is joined and h is made in its registers.  K cut over
+// warps and joined through shared memory took 40 us where this takes 35 in both launches (4-bit, one
+// token, 8 experts of 2048x4096), 55 and 46 with 8-bit weights.
+// DOWN: the units (32 rows by 64 or 128 k) of a tile are all its experts' K in a row; they are cut evenly
+// over the warps of all CTAs.  A warp adds an expert's products into registers and, where the expert
+// changes, w_(m,j) times them into its results of the tile, [tokens][32] in shared memory.  64-row tiles
+// leave fewer warps room beside 64 tokens' results: bf16 1801 and 1685 us, 4-bit 806 and 787 us (8 of
+// 256 experts), 78 and 105 us (bf16, 16 experts of 1032x2056); up to 16 tokens they are even.
+// GATE_UP hands DOWN the routing, so that it is worked out once (39 to 36 us with one token).
+//
+// Measured, both launches of 8 experts of 2048x4096 a token on one of 256 (bytes: chosen experts'
+// weights): bf16 one token 70 us (5.7 TB/s), 24 tokens 982 us (7.0 TB/s); 8-bit one token 46 us
+// (4.4 TB/s), 16 tokens 410 us (6.3 TB/s); 4-bit one token 35 us (2.9 TB/s), 12 tokens 203 us
+// (5.2 TB/s).  Many tokens are bound by HBM.  One token: 10 of the microseconds are two launches' starts,
+// routing, the tokens' way into shared memory and the joining of tiles; 4-bit weights are bound by
+// instructions beside that (the nibbles' masks and shifts, scales by shuffles; groups below 128 take
+// twice the scale work).
 #include <algorithm>
 
 #include "common.cuh"
@@ -36,6 +53,7 @@ __host__ __device__ constexpr int gu_list_bytes(int pairs) {
   return (pairs * 16 + kMoeMaxTokens * 4 + 127) & ~127;  // entries, ids, sorted pairs and tokens; scales
 }
 
+// k of a stage
 __host__ __device__ constexpr int gu_k(int fmt) { return fmt == STREAM_INT4 ? 256 : fmt == STREAM_INT8 ? 128 : 64; }
 
 // slot of 16-byte piece c of row m of MMA operands of BYTES a row, for the reads below
@@ -851,7 +869,9 @@ cudaError_t launch_dn(const StreamArgs& a, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, kfn, a, lists);
 }
 
-// Warps of DOWN: what leaves each a ring of two stages with 8 tokens beside the results of all
+// Warps of DOWN: what leaves each a ring of two stages with 8 tokens beside the results of all.  4-bit
+// weights are bound by instructions and take more: 16 and 12 warps 96 and 96 us at 12 tokens, 13.4
+// and 14.4 us on 8 experts of 512x1024 (60 experts of 1376x2080 and those).
 template <int FMT>
 __host__ __device__ constexpr int dn_warps(int tokens) {
   return FMT != STREAM_INT4 ? 8 : tokens <= kDnFew ? 16 : 12;

@@ -1,15 +1,28 @@
-// Weight-streaming kernels for few tokens: the two launches of a mixture-of-experts layer (bf16,
-// 8-bit and 4-bit weights) and the linear on 8-bit codes.
+// Weight-streaming kernel for few tokens: gate and up of a mixture-of-experts layer whose tokens do not
+// fit in shared memory (bf16, 8-bit and 4-bit weights), and the linear on 8-bit codes of up to 16 tokens.
 //
 //   GATE_UP  g = W13[e][0:I] x_m, u = W13[e][I:2I] x_m for every routed pair (m, j) with expert e,
 //            h = bf16( silu(a min(g, L)) clamp(u, -L, L) )
-//   DOWN     y_m = bf16( sum_j w_(m,j) W2[e] h_(m,j) )
 //   LINEAR   y = (acc x_s) w_s, acc = sum_k x_q w_q  (+ bias after the cast)
 //
-// 8-bit weights: tokens (GATE_UP) and h (DOWN) are quantised here, scale = max|v| / 127 over the
+// 8-bit weights: GATE_UP's tokens are quantised here, scale = max|v| / 127 over the
 // row, code = v / scale rounded half to even; products of codes are exact in fp32, sums
 // below 2^24 too, and every 1024 k they move to int32: sums are exact.  4-bit weights: q - z is
 // exact in bf16, a group's fp32 sum is multiplied by its scale once.
+//
+// Persistent, one CTA per SM.  Units of 64 weight rows (32 gate, 32 up) by 64 or 128 k are cut evenly
+// over the CTAs and dealt to their warps in turn; a unit's weights and its tokens' part of x come through
+// the warp's own ring (cp.async), weights as the warp MMA's A operand.  At the end of an item (a tile for
+// one entry of 8 tokens) the warps leave their sums in a buffer, and one more warp adds them, makes the
+// results and joins items that CTAs share: the last of them finds all parts in the workspace and adds
+// them in the order of K.  Nobody waits for another CTA.
+//
+// Bound by HBM where units are many: LINEAR 1x17408x5120 19.2 us (4.6 TB/s; 5 us of start, first
+// loads and last join), GATE_UP of 24 tokens, 8 of 256 experts of 2048x4096, with DOWN: bf16 982 us
+// (7.0 TB/s), 8-bit 559 us (6.2 TB/s).  4-bit weights are bound by instructions (475 us, 3.7 TB/s).
+// Tiles of 32 rows took 66 us where 64 take 55 (8-bit, one token): half the copies of x.  LINEAR for 17
+// to 64 tokens in passes of 16 would take 50 to 90 us at 17408x5120, where the tensor-core GEMM takes 34
+// to 36; up to 16 tokens this one is ahead (kStreamMaxTokens).
 #include <cuda_fp16.h>
 
 #include "common.cuh"
@@ -145,16 +158,10 @@ __global__ void __launch_bounds__((compute_warps(FMT, NT) + 1) * 32, 1)
   const int u0 = min(total, (int)blockIdx.x * share), u1 = min(total, u0 + share);
 
   auto entry = [&](int a) {
-    struct {
-      int expert, first, count;
-    } en = {0, a * TT, p.M - a * TT};
-    if constexpr (LIN) {
-      en.count = min(TT, en.count);
-    } else {
-      const Entry q = l.entries[a];
-      en = {q.expert, q.first, q.count};
-    }
-    return en;
+    if constexpr (LIN)
+      return Entry{0, (uint16_t)(a * TT), min(TT, p.M - a * TT)};
+    else
+      return l.entries[a];
   };
   if (total == 0) return;  // nothing was dispatched
 
