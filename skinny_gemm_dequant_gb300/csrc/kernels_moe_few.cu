@@ -870,8 +870,9 @@ cudaError_t launch_dn(const StreamArgs& a, cudaStream_t st) {
 }
 
 // Warps of DOWN: what leaves each a ring of two stages with 8 tokens beside the results of all.  4-bit
-// weights are bound by instructions and take more: 16 and 12 warps 96 and 96 us at 12 tokens, 13.4
-// and 14.4 us on 8 experts of 512x1024 (60 experts of 1376x2080 and those).
+// weights are bound by instructions and take more: at 12 tokens 16 and 12 warps take 13.4 and 14.4 us on 8
+// experts of 512x1024 and are even on 60 of 1376x2080.  Of bf16 and 8-bit weights 16 warps make
+// nothing of one to 8 tokens faster (47.7 and 48.2 us, 485.9 and 488.2 us, 36.9 and 35.9 us).
 template <int FMT>
 __host__ __device__ constexpr int dn_warps(int tokens) {
   return FMT != STREAM_INT4 ? 8 : tokens <= kDnFew ? 16 : 12;
