@@ -40,7 +40,7 @@ constexpr int MT = R / 16;
 constexpr int kPitch = R + 4;  // of a column of sums: lanes (g, t) write 8 t + g, all banks once
 constexpr int kBuffers = 4;  // of sums, at most
 
-__host__ __device__ constexpr int compute_warps(int fmt, int nt) { return fmt == STREAM_INT4 ? 11 : nt > 1 ? 6 : 8; }
+__host__ __device__ constexpr int compute_warps(int fmt) { return fmt == STREAM_INT4 ? 11 : 8; }
 __host__ __device__ constexpr int unit_k(int fmt) { return fmt == STREAM_BF16 ? 64 : 128; }
 __host__ __device__ constexpr int row_bytes(int fmt) { return fmt == STREAM_INT4 ? 64 : 128; }
 __host__ __device__ constexpr int token_bytes(int fmt, int mode) {
@@ -86,9 +86,9 @@ struct Walk {
 };
 
 template <int FMT, int MODE, int NT, bool FINE, bool ZP>
-__global__ void __launch_bounds__((compute_warps(FMT, NT) + 1) * 32, 1)
+__global__ void __launch_bounds__((compute_warps(FMT) + 1) * 32, 1)
     stream_kernel(const __grid_constant__ StreamArgs p, const __grid_constant__ Layout lay) {
-  constexpr int W = compute_warps(FMT, NT), THREADS = (W + 1) * 32;
+  constexpr int W = compute_warps(FMT), THREADS = (W + 1) * 32;
   constexpr int TT = NT * 8, KU = unit_k(FMT), WB = row_bytes(FMT), XB = token_bytes(FMT, MODE);
   constexpr bool GU = MODE == STREAM_GATE_UP, LIN = MODE == STREAM_LINEAR;
   constexpr bool I8 = FMT == STREAM_INT8, I4 = FMT == STREAM_INT4;
@@ -163,7 +163,8 @@ __global__ void __launch_bounds__((compute_warps(FMT, NT) + 1) * 32, 1)
     else
       return l.entries[a];
   };
-  if (total == 0) return;  // nothing was dispatched
+  if (u0 >= u1) return;  // nothing was dispatched, or nothing is left
+  const int item0 = u0 / nblk, item1 = (u1 - 1) / nblk;
 
   if (warp < W) {
     // ---------------------------------------------------------------- streaming and products
@@ -304,7 +305,6 @@ __global__ void __launch_bounds__((compute_warps(FMT, NT) + 1) * 32, 1)
     Walk c, n;  // the unit to compute, and the one after it
     c.set(u0 + warp, nblk, ne);
     n = c;
-    const int item0 = u0 / nblk, item1 = u1 > u0 ? (u1 - 1) / nblk : item0 - 1;
     int done = item0, c_item = -1;
     bool mine = false;  // a unit of item `done` has been added
     float inv[NT] = {};
@@ -334,7 +334,7 @@ __global__ void __launch_bounds__((compute_warps(FMT, NT) + 1) * 32, 1)
               }
           mine = false;
         }
-        bar_arrive<kFull, THREADS>(b);
+        if (done < item1) bar_arrive<kFull, THREADS>(b);
       }
       if (c.u >= u1) break;
       mine = true;
@@ -488,146 +488,187 @@ __global__ void __launch_bounds__((compute_warps(FMT, NT) + 1) * 32, 1)
       }
       c = n;
     }
-  } else {
-    // ---------------------------------------------------------------- sums and results: rows lane, lane + 32
-    // 0: the part of an item that began in an earlier CTA, 1: of one that ends in a later CTA
-    auto slot_of = [&](int cta, int tail) { return p.slots + ((int64_t)cta * 2 + tail) * (TT * R); };
-    // counts a part of the item of units [a, b) in; true for the last one, which finds all parts stored
-    auto last_part = [&](int a, int b) {
-      const int c0 = a / share, c1 = (b - 1) / share;
-      __threadfence();
-      __syncwarp();
-      unsigned before = 0;
-      if (lane == 0) {
-        before = atomicAdd(p.tickets + c0, 1u);
-        if (before == (unsigned)(c1 - c0)) p.tickets[c0] = 0u;
+  }
+
+  // ------------------------------------------------------------------ sums and results: rows lane, lane + 32
+  // 0: the part of an item that began in an earlier CTA, 1: of one that ends in a later CTA
+  auto slot_of = [&](int cta, int tail) {
+    return reinterpret_cast<Sum*>(p.slots + ((int64_t)cta * 2 + tail) * (TT * R)) + lane;
+  };
+  struct Item {
+    int it, units, w0, n;  // its units here, the warp that has the first; row of a lane
+    const Sum* sums;
+    bool cut;
+    float ws[2], bias[2];
+  };
+  auto item_of = [&](int it, const Walk& c, int expert) {
+    Item m;
+    const int ua = max(u0, it * nblk);
+    m.it = it;
+    m.units = min(min(u1, (it + 1) * nblk) - ua, W);
+    m.w0 = (ua - u0) % W;
+    m.sums = reinterpret_cast<const Sum*>(smem + lay.lists + (it - item0) % buffers * buffer) + lane;
+    m.cut = it * nblk < u0 || (it + 1) * nblk > u1;
+    m.n = c.tile * OUT + lane;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      m.ws[h] = 1.f;
+      m.bias[h] = 0.f;
+      const int row = GU ? m.n : m.n + 32 * h;
+      if (row < p.N) {
+        if (I8)
+          m.ws[h] = reinterpret_cast<const float*>(p.scale)[LIN ? (p.lds ? row : 0)
+                                                                : expert * p.s_estride + (GU && h ? p.N : 0) + row];
+        if (LIN && p.bias) m.bias[h] = bf16_bits_to_f32(p.bias[row]);
       }
-      before = __shfl_sync(0xffffffffu, before, 0);
-      __threadfence();
-      return before == (unsigned)(c1 - c0);
-    };
-    const int item0 = u0 / nblk, item1 = u1 > u0 ? (u1 - 1) / nblk : item0 - 1;
+    }
+    return m;
+  };
+  auto own = [&](const Item& m, int k, Sum (&v)[2]) {  // the sums of this CTA's warps
+    v[0] = v[1] = 0;
+    int w = m.w0;
+#pragma unroll 4
+    for (int i = 0; i < m.units; ++i) {
+      const Sum* q = m.sums + (w * xt + k) * kPitch;
+      v[0] += q[0];
+      v[1] += q[32];
+      if (++w == W) w = 0;
+    }
+  };
+  auto leave = [&](const Item& m, int k) {
+    Sum v[2], *to = slot_of(blockIdx.x, m.it * nblk >= u0) + k * R;
+    own(m, k, v);
+    __stcg(to, v[0]);
+    __stcg(to + 32, v[1]);
+  };
+  // by one thread: counts a part of item `it` in; true for the last one, which finds all parts stored
+  auto last_part = [&](int it) {
+    const int c0 = it * nblk / share, c1 = ((it + 1) * nblk - 1) / share;
+    const unsigned before = atomicAdd(p.tickets + c0, 1u);
+    if (before == (unsigned)(c1 - c0)) p.tickets[c0] = 0u;
+    return before == (unsigned)(c1 - c0);
+  };
+  auto joined = [&](const Item& m, int k, Sum (&v)[2]) {  // all parts in the order of K
+    const int c0 = m.it * nblk / share, c1 = ((m.it + 1) * nblk - 1) / share;
+    v[0] = v[1] = 0;
+#pragma unroll 4
+    for (int q = c0; q <= c1; ++q) {
+      const Sum* from = slot_of(q, q == c0) + k * R;
+      v[0] += __ldcg(from);
+      v[1] += __ldcg(from + 32);
+    }
+  };
+  auto result = [&](const Item& m, int place, const Sum (&v)[2]) {  // of pair or token `place`
+    float f[2] = {(float)v[0], (float)v[1]};
+    if constexpr (GU) {
+      const int pair = l.pair[place];
+      if constexpr (I8) {
+        const float xs = s_xs[l.tok[place]];
+        f[0] = f[0] * xs * m.ws[0];
+        f[1] = f[1] * xs * m.ws[1];
+      }
+      const uint16_t hb = f32_to_bf16_rn(gated_act(f[0], f[1], p.alpha, p.limit));
+      if (m.n < p.N) p.h[pair * p.ldh + m.n] = hb;
+      if (I8) {
+        const unsigned top = __reduce_max_sync(0xffffffffu, m.n < p.N ? (unsigned)(hb & 0x7FFF) << 16 : 0u);
+        if (lane == 0) atomicMax(p.amax + pair, top);
+      }
+    } else {
+      const float xs = p.x_scale[place];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (m.n + 32 * h >= p.N) continue;
+        const float o32 = __fmul_rn(__fmul_rn(f[h], xs), m.ws[h]);
+        const int64_t at = (int64_t)place * p.ldy + m.n + 32 * h;
+        if (p.out_type == QL_OUT_FP32) {
+          reinterpret_cast<float*>(p.y)[at] = p.bias ? o32 + m.bias[h] : o32;
+        } else if (p.out_type == QL_OUT_FP16) {
+          __half o = __float2half_rn(o32);
+          if (p.bias) o = __float2half_rn(__half2float(o) + m.bias[h]);
+          reinterpret_cast<__half*>(p.y)[at] = o;
+        } else {
+          uint16_t o = f32_to_bf16_rn(o32);
+          if (p.bias) o = f32_to_bf16_rn(bf16_bits_to_f32(o) + m.bias[h]);
+          reinterpret_cast<uint16_t*>(p.y)[at] = o;
+        }
+      }
+    }
+  };
+
+  // All items but the last by the last warp, while the others go on.  Only the first can be shared with other
+  // CTAs; it is joined at the end, by all warps
+  __shared__ bool s_join[2];  // this CTA has the last part of its first, its last item
+  if (warp == W) {
+    if (lane == 0) s_join[0] = false;
     Walk c;
     c.set(item0 * nblk, nblk, ne);
 #pragma unroll 1
-    for (int it = item0; it <= item1; ++it) {
+    for (int it = item0; it < item1; ++it) {
       const auto en = entry(c.a);
       const int b = (it - item0) % buffers;
+      const Item m = item_of(it, c, en.expert);
       bar_sync<kFull, THREADS>(b);
-      const int ua = max(u0, it * nblk);
-      int units = min(min(u1, (it + 1) * nblk) - ua, W), w0 = (ua - u0) % W;
-      const Sum* sums = reinterpret_cast<const Sum*>(smem + lay.lists + b * buffer) + lane;
-      auto own = [&](int k, Sum (&v)[2]) {  // the sums of this CTA's warps
-        v[0] = v[1] = 0;
-        int w = w0;
-#pragma unroll 4
-        for (int i = 0; i < units; ++i) {
-          const Sum* s = sums + (w * xt + k) * kPitch;
-          v[0] += s[0];
-          v[1] += s[32];
-          if (++w == W) w = 0;
-        }
-      };
-      // an item that is shared with other CTAs: the last of them adds the parts in the order of K
-      const bool parts = it * nblk < u0 || (it + 1) * nblk > u1;
-      bool ready = true;
-      if (parts) {
-        Sum* mine = reinterpret_cast<Sum*>(slot_of(blockIdx.x, it * nblk >= u0)) + lane;
 #pragma unroll 1
-        for (int k = 0; k < en.count; ++k) {
-          Sum v[2];
-          own(k, v);
-          __stcg(mine + k * R, v[0]);
-          __stcg(mine + k * R + 32, v[1]);
+      for (int k = 0; k < en.count; ++k) {
+        if (m.cut) {
+          leave(m, k);
+          continue;
         }
-        ready = last_part(it * nblk, (it + 1) * nblk);
-        if (ready) {
-          // the sums go where the first warp left its own
-          const int c0 = it * nblk / share, c1 = ((it + 1) * nblk - 1) / share;
-          Sum v[TT][2] = {};
-#pragma unroll 1
-          for (int q = c0; q <= c1; ++q) {
-            const Sum* s = reinterpret_cast<const Sum*>(slot_of(q, q == c0)) + lane;
-#pragma unroll
-            for (int k = 0; k < TT; ++k)
-              if (k < en.count) {
-                v[k][0] += __ldcg(s + k * R);
-                v[k][1] += __ldcg(s + k * R + 32);
-              }
-          }
-          Sum* to = const_cast<Sum*>(sums);
-#pragma unroll
-          for (int k = 0; k < TT; ++k)
-            if (k < en.count) {
-              to[k * kPitch] = v[k][0];
-              to[k * kPitch + 32] = v[k][1];
-            }
-          units = 1;
-          w0 = 0;
-        }
-      }
-      const int n = c.tile * OUT + lane;
-      float ws[2] = {1.f, 1.f}, bias[2] = {};
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int row = GU ? n : n + 32 * h;
-        if (row < p.N) {
-          if (I8)
-            ws[h] = reinterpret_cast<const float*>(p.scale)[LIN ? (p.lds ? row : 0)
-                                                                : en.expert * p.s_estride + (GU && h ? p.N : 0) + row];
-          if (LIN && p.bias) bias[h] = bf16_bits_to_f32(p.bias[row]);
-        }
-      }
-#pragma unroll 1
-      for (int k = 0; k < en.count && ready; ++k) {
         Sum v[2];
-        own(k, v);
-        float f[2] = {(float)v[0], (float)v[1]};
-        if constexpr (GU) {
-          const int pair = l.pair[en.first + k];
-          if constexpr (I8) {
-            const float xs = s_xs[l.tok[en.first + k]];
-            f[0] = f[0] * xs * ws[0];
-            f[1] = f[1] * xs * ws[1];
-          }
-          const uint16_t hb = f32_to_bf16_rn(gated_act(f[0], f[1], p.alpha, p.limit));
-          if (n < p.N) p.h[pair * p.ldh + n] = hb;
-          if (I8) {
-            const unsigned top = __reduce_max_sync(0xffffffffu, n < p.N ? (unsigned)(hb & 0x7FFF) << 16 : 0u);
-            if (lane == 0) atomicMax(p.amax + pair, top);
-          }
-        } else {
-          const int m = en.first + k;
-          const float xs = p.x_scale[m];
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if (n + 32 * h >= p.N) continue;
-            const float o32 = __fmul_rn(__fmul_rn(f[h], xs), ws[h]);
-            const int64_t at = (int64_t)m * p.ldy + n + 32 * h;
-            if (p.out_type == QL_OUT_FP32) {
-              reinterpret_cast<float*>(p.y)[at] = p.bias ? o32 + bias[h] : o32;
-            } else if (p.out_type == QL_OUT_FP16) {
-              __half o = __float2half_rn(o32);
-              if (p.bias) o = __float2half_rn(__half2float(o) + bias[h]);
-              reinterpret_cast<__half*>(p.y)[at] = o;
-            } else {
-              uint16_t o = f32_to_bf16_rn(o32);
-              if (p.bias) o = f32_to_bf16_rn(bf16_bits_to_f32(o) + bias[h]);
-              reinterpret_cast<uint16_t*>(p.y)[at] = o;
-            }
-          }
-        }
+        own(m, k, v);
+        result(m, en.first + k, v);
       }
       __syncwarp();
       if (it + buffers <= item1) bar_arrive<kEmpty, THREADS>(b);
+      if (m.cut) {
+        __threadfence();
+        __syncwarp();
+        if (lane == 0) s_join[0] = last_part(it);
+      }
       c.next(nblk, nblk, ne);
+    }
+  }
+  __syncthreads();
+  // the last item by all warps, a token each
+  Walk c;
+  c.set(item1 * nblk, nblk, ne);
+  const auto en = entry(c.a);
+  const Item m = item_of(item1, c, en.expert);
+  if (m.cut) {
+#pragma unroll 1
+    for (int k = warp; k < en.count; k += W + 1) leave(m, k);
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) s_join[1] = last_part(item1);
+    __syncthreads();
+  } else {
+#pragma unroll 1
+    for (int k = warp; k < en.count; k += W + 1) {
+      Sum v[2];
+      own(m, k, v);
+      result(m, en.first + k, v);
+    }
+  }
+  __threadfence();  // the other parts were fenced before their counts
+#pragma unroll 1
+  for (int which = 0; which < 2; ++which) {
+    if (which ? !m.cut || !s_join[1] : !s_join[0]) continue;
+    const int it = which ? item1 : item0;
+    c.set(it * nblk, nblk, ne);
+    const auto of = entry(c.a);
+    const Item j = item_of(it, c, of.expert);
+#pragma unroll 1
+    for (int k = warp; k < of.count; k += W + 1) {
+      Sum v[2];
+      joined(j, k, v);
+      result(j, of.first + k, v);
     }
   }
 }
 
 template <int FMT, int MODE, int NT, bool FINE, bool ZP>
 cudaError_t launch(const StreamArgs& a, cudaStream_t st) {
-  constexpr int W = compute_warps(FMT, NT), TT = NT * 8;
+  constexpr int W = compute_warps(FMT), TT = NT * 8;
   auto* kfn = stream_kernel<FMT, MODE, NT, FINE, ZP>;
   static OncePerDevice once;
   if (const cudaError_t e = raise_smem_limit(kfn, once); e != cudaSuccess) return e;
