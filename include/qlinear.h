@@ -486,9 +486,10 @@ QL_API ql_status quantize_int8(const uint16_t* x, int64_t M, int64_t K, int64_t 
  * qlinear_int8_w8a8's y bit for bit.  x_q: int8 [M, ldx]; x_scale: fp32 [M]; w: int8 [N, ldw], both of
  * any value, -128 too; w_scale: fp32 [N] or [1] (w_scale_len); bias: nullable bf16 [N]; y: [M, ldy] of
  * out_type QL_OUT_*.
- * Paths: M <= 16: one launch that streams the weights once; else a launch that widens the tokens'
- *        codes to f16 and one tcgen05 GEMM that widens the weights on the way (sm_103a has no integer
- *        tcgen05 MMA; fp32 sums are exact below 2^24 and move to int32 every 1024 k).
+ * Paths: M <= 16, or up to 1024 tokens on weights small enough: one launch that streams the weights once per
+ *        16 tokens; else a launch that widens the tokens' codes to f16 and one tcgen05 GEMM that widens
+ *        the weights on the way (sm_103a has no integer tcgen05 MMA; fp32 sums are exact below 2^24 and
+ *        move to int32 every 1024 k).  The result is the same.
  * Requires 1 <= M <= 2^22, 1 <= N <= 2^24, K >= 16, K % 16 == 0, K <= 131056 (|acc| < 2^31), ldx >= K,
  * ldw >= K, both multiples of 16, 16-byte aligned x_q and w, 4-byte aligned scales, y aligned to its
  * type, ldy >= N.  workspace: ql_workspace_bytes(QL_OP_INT8_CODES, M, N, K, 0, 0) bytes, zeroed once.

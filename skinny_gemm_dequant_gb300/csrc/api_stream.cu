@@ -139,7 +139,7 @@ namespace ql {
 size_t stream_workspace_bytes(int op, int64_t M, int64_t N, int64_t K, int E, int topk) {
   if (op == QL_OP_INT8_CODES) {
     if (M > (1 << 22) || N > (1 << 24) || K > 131056 || M < 1 || N < 1 || K < 1) return workspace_zero_bytes();  // refused
-    return workspace_zero_bytes() + (M > kStreamMaxTokens ? tc::codes_gemm_bytes(M, N, K) : stream_slot_bytes(1));
+    return workspace_zero_bytes() + (linear_streams(M, N, K) ? stream_slot_bytes(1) : tc::codes_gemm_bytes(M, N, K));
   }
   if (E <= 0 || topk <= 0) return 0;
   if (M > kMoeMaxTokens || topk > kMoeMaxTopk || K > 32768) return workspace_zero_bytes();  // refused
@@ -173,7 +173,7 @@ ql_status qlinear_int8(const int8_t* x_q, int64_t M, int64_t K, int64_t ldx, con
     return QL_ERR_ALIGNMENT;
   if (!workspace || workspace_bytes < ql_workspace_bytes(QL_OP_INT8_CODES, M, N, K, 0, 0)) return QL_ERR_WORKSPACE;
   if (!aligned<16>(workspace)) return QL_ERR_ALIGNMENT;
-  if (M > kStreamMaxTokens) {
+  if (!linear_streams(M, N, K)) {
     tc::CodesGemm g = {};
     g.x = x_q;
     g.M = M;

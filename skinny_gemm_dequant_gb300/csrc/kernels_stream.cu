@@ -1,5 +1,5 @@
 // Weight-streaming kernel for few tokens: gate and up of a mixture-of-experts layer whose tokens do not
-// fit in shared memory (bf16, 8-bit and 4-bit weights), and the linear on 8-bit codes of up to 16 tokens.
+// fit in shared memory (bf16, 8-bit and 4-bit weights), and the linear on 8-bit codes of few tokens.
 //
 //   GATE_UP  g = W13[e][0:I] x_m, u = W13[e][I:2I] x_m for every routed pair (m, j) with expert e,
 //            h = bf16( silu(a min(g, L)) clamp(u, -L, L) )
@@ -13,16 +13,16 @@
 // Persistent, one CTA per SM.  Units of 64 weight rows (32 gate, 32 up) by 64 or 128 k are cut evenly
 // over the CTAs and dealt to their warps in turn; a unit's weights and its tokens' part of x come through
 // the warp's own ring (cp.async), weights as the warp MMA's A operand.  At the end of an item (a tile for
-// one entry of 8 tokens) the warps leave their sums in a buffer, and one more warp adds them, makes the
-// results and joins items that CTAs share: the last of them finds all parts in the workspace and adds
-// them in the order of K.  Nobody waits for another CTA.
+// one entry of 8 tokens) the warps leave their sums in a buffer, and one more warp adds them and
+// makes the results, of a CTA's last item all warps.  Items that CTAs share are joined by the last of
+// them, which finds all parts in the workspace and adds them in the order of K, all warps at once (by one warp
+// 16 tokens of 2048x4096 took 25 us, now 8).  Nobody waits for another CTA.
 //
 // Bound by HBM where units are many: LINEAR 1x17408x5120 19.2 us (4.6 TB/s; 5 us of start, first
-// loads and last join), GATE_UP of 24 tokens, 8 of 256 experts of 2048x4096, with DOWN: bf16 982 us
+// loads and last join), 16 tokens 28 us, GATE_UP of 24 tokens, 8 of 256 experts of 2048x4096, with DOWN: bf16 982 us
 // (7.0 TB/s), 8-bit 559 us (6.2 TB/s).  4-bit weights are bound by instructions (475 us, 3.7 TB/s).
-// Tiles of 32 rows took 66 us where 64 take 55 (8-bit, one token): half the copies of x.  LINEAR for 17
-// to 64 tokens in passes of 16 would take 50 to 90 us at 17408x5120, where the tensor-core GEMM takes 34
-// to 36; up to 16 tokens this one is ahead (kStreamMaxTokens).
+// Tiles of 32 rows took 66 us where 64 take 55 (8-bit, one token): half the copies of x.  LINEAR's passes
+// of 16 tokens over a tile follow each other in one CTA, so that only the first reads HBM (linear_streams).
 #include <cuda_fp16.h>
 
 #include "common.cuh"
@@ -695,7 +695,7 @@ cudaError_t launch(const StreamArgs& a, cudaStream_t st) {
 }  // namespace
 
 size_t stream_slot_bytes(int64_t M) {
-  const int64_t columns = M < kStreamMaxTokens ? kStreamMaxTokens : M;
+  const int64_t columns = M < kLinearTokens ? kLinearTokens : M;
   return (size_t)kNumSMs * 2 * columns * R * 4;
 }
 

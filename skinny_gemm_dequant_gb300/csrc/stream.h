@@ -15,7 +15,18 @@ constexpr int kStreamRows = 64;       // weight rows of a tile
 constexpr int kMoeMaxTokens = 64;     // of a mixture-of-experts call
 constexpr int kMoeMaxTopk = 16;
 constexpr int kMoeHandedBytes = 16640;
-constexpr int kStreamMaxTokens = 16;  // of a linear call
+constexpr int kLinearTokens = 16;     // of a pass of LINEAR over the weights
+
+// LINEAR's launch or, for more tokens and larger matrices, the GEMM's (gemm_codes.h).  LINEAR takes 5 us and a
+// time that grows with passes, rows and (K + 3300); the GEMM hardly grows with few tokens.  Both sides in
+// us: 17408x5120, 16 tokens 28 and 32, 32 tokens 42 and 33; 5120x5120, 32 tokens 20 and 22, 64 tokens 29
+// and 25; 2048x4096, 64 tokens 16 and 21, 128 tokens 22 and 25, 192 tokens 30 and 24; 5120x512, 32 tokens
+// 9 and 11, 64 tokens 14 and 12; 512x1024, 256 tokens 5 and 15.
+inline bool linear_streams(int64_t M, int64_t N, int64_t K) {
+  if (M <= kLinearTokens) return true;
+  const int64_t rows = (M + kLinearTokens - 1) / kLinearTokens * N;
+  return M <= 1024 && rows * (K + 3300) <= 24500 * (K < 3100 ? K + 2100 : 5200);
+}
 
 struct StreamArgs {
   const uint8_t* x;  // activations: bf16 rows (tokens; DOWN: h by pair), LINEAR: 8-bit codes
@@ -56,7 +67,7 @@ struct StreamArgs {
 // codes and scales of tokens (kernels_codes.cu)
 cudaError_t launch_token_codes(const uint16_t* x, int64_t M, int64_t K, int64_t ldx, int8_t* codes, float* scale,
                                cudaStream_t st);
-// kernels_stream.cu: GATE_UP of any call, LINEAR of up to kStreamMaxTokens
+// kernels_stream.cu: GATE_UP of any call, LINEAR of what linear_streams says
 cudaError_t launch_gate_up(int fmt, const StreamArgs& a, cudaStream_t st);
 cudaError_t launch_linear(const StreamArgs& a, cudaStream_t st);
 // kernels_moe_few.cu: GATE_UP while the tokens fit in shared memory, DOWN

@@ -37,7 +37,8 @@ def call(ql, xq, xs, w, ws, K, **kw):
 
 SIZES = [(1, 512, 1024), (1, 1, 16), (2, 33, 48), (3, 5120, 272), (8, 100, 2080), (9, 31, 1040), (16, 257, 528),
          (17, 64, 2048), (32, 130, 1600), (33, 513, 144), (100, 256, 1024), (192, 300, 2064), (193, 1000, 5136),
-         (400, 2056, 400), (1000, 777, 1040), (200, 17408, 272), (161, 40, 8192)]
+         (400, 2056, 400), (1000, 777, 1040), (200, 17408, 272), (161, 40, 8192),
+         (17, 12800, 1040), (33, 6001, 4112), (100, 2056, 8208), (1025, 33, 48), (1100, 300, 2064), (1024, 9, 16)]
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
@@ -47,7 +48,9 @@ def test_exact(ql, M, N, K, dtype):
     acc = MO.linear_codes(xq[:, :K], xs, w[:, :K], ws)[0]
     bias = torch.randn(N, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16) if M % 2 else None
     y, path = call(ql, xq, xs, w, ws, K, bias=None if bias is None else bias.cuda(), out_dtype=dtype, debug=True)
-    assert path == ("int8_codes_skinny" if M <= 16 else "int8_codes_tcgen05")
+    rows = -(-M // 16) * N  # of 16 tokens
+    few = M <= 16 or M <= 1024 and rows * (K + 3300) <= 24500 * min(K + 2100, 5200)
+    assert path == ("int8_codes_skinny" if few else "int8_codes_tcgen05")
     assert torch.equal(y.cpu(), want(acc, xs, ws, dtype, bias))
     one = call(ql, xq, xs, w, ws[:1], K, out_dtype=dtype)
     assert torch.equal(one.cpu(), want(acc, xs, np.repeat(ws[:1], N), dtype))
@@ -55,17 +58,17 @@ def test_exact(ql, M, N, K, dtype):
 
 def test_sums_of_one_sign_are_exact(ql):
     """Codes of -128 over a long K: every partial sum is a power of two, the last one 2^14 K."""
-    for M, K in ((2, 17408), (24, 131056)):
-        xq, w = np.full((M, K), -128, np.int8), np.full((40, K), -128, np.int8)
+    for M, N, K in ((2, 40, 17408), (24, 40, 131056), (24, 1000, 131056)):
+        xq, w = np.full((M, K), -128, np.int8), np.full((N, K), -128, np.int8)
         w[1] = 127
         xq[1, ::2] = 1
-        one = np.ones(max(M, 40), np.float32)
-        y = call(ql, xq, one[:M], w, one[:40], K, out_dtype=torch.float32)
-        acc = MO.linear_codes(xq, one[:M], w, one[:40])[0]
+        one = np.ones(max(M, N), np.float32)
+        y = call(ql, xq, one[:M], w, one[:N], K, out_dtype=torch.float32)
+        acc = MO.linear_codes(xq, one[:M], w, one[:N])[0]
         assert np.array_equal(y.cpu().numpy(), acc.astype(np.float32))
 
 
-@pytest.mark.parametrize("M", [1, 7, 16, 32, 200])
+@pytest.mark.parametrize("M", [1, 7, 16, 32, 200, 1040])
 def test_output_rows_beyond_the_call_stay(ql, M):
     xq, xs, w, ws = make(M, 45, 160, seed=3)
     wide = torch.full((M + 2, 64), 5.0, dtype=torch.bfloat16, device="cuda")
@@ -117,7 +120,7 @@ def test_quantize_tells_of_nan_and_infinity(ql):
     assert s[0].isnan() and s[1] == np.float32(1) / np.float32(127) and s[2].isinf()
 
 
-@pytest.mark.parametrize("M", [1, 5, 16, 30, 260])
+@pytest.mark.parametrize("M", [1, 5, 16, 30, 260, 1050])
 def test_same_as_the_linear_that_quantises_itself(ql, M):
     g = torch.Generator().manual_seed(M)
     x = torch.randn(M, 1280, generator=g).to(torch.bfloat16).cuda()
@@ -128,7 +131,7 @@ def test_same_as_the_linear_that_quantises_itself(ql, M):
     assert torch.equal(ql.qlinear_int8(codes, scale, w, ws, bias), ql.qlinear_int8_w8a8(x, w, ws, bias))
 
 
-GEMM = [(20, 300, 8192), (161, 5000, 1040), (400, 700, 4112)]  # tiles of the rest alone; whole tiles too
+GEMM = [(20, 12000, 1040), (161, 5000, 1040), (400, 700, 4112)]  # tiles of the rest alone; whole tiles too
 
 
 @pytest.mark.parametrize("M,N,K", GEMM)
@@ -154,7 +157,7 @@ def test_nothing_is_left_behind_by_waits_that_run_out(ql, M, N, K):
     assert seen
 
 
-@pytest.mark.parametrize("M", [1, 12, 40, 300])
+@pytest.mark.parametrize("M", [1, 12, 40, 300, 1030])
 def test_graphs_and_streams(ql, M):
     sets = [[torch.from_numpy(a).cuda() for a in make(M, 600, 2064, seed=s)] for s in (1, 2)]
     alone = [ql.qlinear_int8(*a) for a in sets]
