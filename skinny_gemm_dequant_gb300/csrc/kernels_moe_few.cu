@@ -6,7 +6,8 @@
 //
 // 8-bit weights: tokens (GATE_UP) and h (DOWN) are quantised here, scale = max|v| / 127 over the
 // row, code = v / scale rounded half to even; products of codes are exact in fp32, sums of
-// 1024 k too.  4-bit weights: no weight is rounded, a group's fp32 sum is multiplied by its scale once.
+// 1024 k too.  4-bit weights: no weight is rounded, a group's fp32 sum is multiplied by its scale once;
+// GATE_UP takes the zero point out of it by the group's sum of x, sum (q - z) x = sum q x - z sum x.
 // h is rounded to bf16 once (the products' operand); all sums are fp32 or whole numbers.
 //
 // Both kernels are persistent, one CTA per SM, and stream a chosen expert's weights once for 8 of its

@@ -1,5 +1,6 @@
-// Host-side declarations of the weight-streaming kernels for few tokens (kernels_stream.cu): the
-// mixture-of-experts layers on bf16, 8-bit and 4-bit weights and the linear on 8-bit codes.
+// Host-side declarations of the weight-streaming kernels for few tokens (kernels_stream.cu,
+// kernels_moe_few.cu): the mixture-of-experts layers on bf16, 8-bit and 4-bit weights and the linear on
+// 8-bit codes.
 #pragma once
 #include <cstdint>
 #include <cuda_runtime.h>
