@@ -505,7 +505,7 @@ QL_API ql_status qlinear_int8(const int8_t* x_q, int64_t M, int64_t K, int64_t l
  * and debug outputs) in two launches that stream every chosen expert's weights once per 8 of its
  * tokens.
  * Expert ids outside [0, E) are padding: the pair is left out, and a token without any expert gets
- * zeros (topk_ids_out reports -1).
+ * zeros (topk_ids_out reports -1, topk_w_out the weight as given, and the pair's row of h_out is zeros).
  *   h = bf16( silu(alpha * min(g, limit)) * clamp(u, -limit, limit) ),  y = bf16( sum_j weight_j W2[e_j] h_j )
  *   moe_bf16: w13 bf16 [E, 2I, H], w2 bf16 [E, H, I]; fp32 sums.
  *   moe_int8: w13 int8 [E, 2I, H] and s13 fp32 [E, 2I], w2 int8 [E, H, I] and s2 fp32 [E, H] (dense);

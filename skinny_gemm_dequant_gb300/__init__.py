@@ -792,7 +792,8 @@ def moe_bf16(x, w13, w2, *, router_logits=None, topk_ids=None, topk_weights=None
     """Mixture-of-experts layer for 1 to 64 tokens on bf16 weights, in two launches.  x: bf16 [M, H];
     w13: bf16 [E, 2I, H] (gate rows, then up rows), w2: bf16 [E, H, I]; H and I multiples of 8.  Routing,
     activation and debug=True's (y, ids, weights, h, path) are moe_mxfp4_grouped's; an id outside
-    [0, E) is padding, and a token without an expert gets zeros.  Workspaces as qlinear_int8's."""
+    [0, E) is padding (debug=True: id -1 and a row of zeros in h), and a token without an expert gets
+    zeros.  Workspaces as qlinear_int8's."""
     def mats(E, I, H, dev):
         return (*_experts(w13, "w13", E, 2 * I, H, torch.bfloat16, dev), *_experts(w2, "w2", E, H, I, torch.bfloat16, dev))
     return _moe(lib.moe_bf16, x, w13, mats, router_logits, topk_ids, topk_weights, topk, renormalize, swiglu_alpha,

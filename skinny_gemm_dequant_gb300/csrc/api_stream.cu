@@ -117,7 +117,12 @@ ql_status moe_run(int fmt, const Moe& a, const Matrix& w13, const Matrix& w2, St
   dn.N = (int)a.H;
   dn.y = a.y;
   dn.ldy = a.ldy;
-  cudaError_t e = gate_up_few_takes(fmt, gu) ? launch_gate_up_few(fmt, gu, st) : launch_gate_up(fmt, gu, st);
+  cudaError_t e = cudaSuccess;
+  if (a.h_out) {  // GATE_UP writes no row of a padding pair: the caller gets zeros there, not an earlier call's h
+    e = cudaMemsetAsync(gu.h, 0, (size_t)a.M * a.topk * gu.ldh * 2, st);
+    if (e != cudaSuccess) return cuda_status(e);
+  }
+  e = gate_up_few_takes(fmt, gu) ? launch_gate_up_few(fmt, gu, st) : launch_gate_up(fmt, gu, st);
   if (e != cudaSuccess) return cuda_status(e);
   e = launch_down(fmt, dn, st);
   if (e != cudaSuccess) {
