@@ -514,8 +514,7 @@ QL_API ql_status qlinear_int8(const int8_t* x_q, int64_t M, int64_t K, int64_t l
  *     throughout.
  *   moe_int4: w13 packed codes [E, 2I, ldw13], w2 [E, H, ldw2] with scales and zero points stored as
  *     qlinear_int4's: s13 [E, 2I, lds13], s2 [E, H, lds2], z13, z2 likewise (each NULL: 8).  No weight
- *     is rounded; x and h stay bf16; gate and up sums are fp32, rounded relative to scale * sum (q + z) |x|;
- *     values of x of 2^63 and more may count as infinite, and parts of a sum below 2^-80 as zero.
+ *     is rounded; x and h stay bf16; a group's sum of (q - z) x is fp32 and meets its scale once.
  * Experts, rows and scale rows are ld / stride elements apart (packed codes: bytes): w_estride13 is the distance
  * of two experts of w13, and so on.  x: bf16 [M, ldx]; y: bf16 [M, ldy].
  * Requires 1 <= M <= 64, 1 <= topk <= min(E, 16), E <= 1024, H and I at most 32768 and multiples of 8

@@ -820,8 +820,7 @@ def moe_int4(x, w13, s13, w2, s2, z13=None, z2=None, *, group=128, router_logits
              workspace=None, stream=None):
     """moe_bf16's layer on 4-bit weights stored as qlinear_int4's: w13 uint8 [E, 2I, >=H/2], w2 uint8
     [E, H, >=I/2], scales bf16 or fp16 [E, rows, >=ceil(columns/group)], zero points uint8 of the same
-    shape or None: 8; H and I multiples of 32, group a power of two >= 32.  Values of x of 2^63 and more may
-    count as infinite."""
+    shape or None: 8; H and I multiples of 32, group a power of two >= 32."""
     def mats(E, I, H, dev):
         scale, u8 = s13.dtype, torch.uint8
         fmt = _SCALE_FORMATS.get(scale)

@@ -6,8 +6,7 @@
 //
 // 8-bit weights: tokens (GATE_UP) and h (DOWN) are quantised here, scale = max|v| / 127 over the
 // row, code = v / scale rounded half to even; products of codes are exact in fp32, sums of
-// 1024 k too.  4-bit weights: no weight is rounded, a group's fp32 sum is multiplied by its scale once;
-// GATE_UP takes the zero point out of it by the group's sum of x, sum (q - z) x = sum q x - z sum x.
+// 1024 k too.  4-bit weights: q - z is exact in bf16, a group's fp32 sum is multiplied by its scale once.
 // h is rounded to bf16 once (the products' operand); all sums are fp32 or whole numbers.
 //
 // Both kernels are persistent, one CTA per SM, and stream a chosen expert's weights once for 8 of its
@@ -25,11 +24,15 @@
 // leave fewer warps room beside 64 tokens' results: bf16 1801 and 1685 us, 4-bit 806 and 787 us (8 of
 // 256 experts), 78 and 105 us (bf16, 16 experts of 1032x2056); up to 16 tokens they are even.
 // GATE_UP hands DOWN the routing, so that it is worked out once (39 to 36 us with one token).
+// 4-bit weights become (q - z) / 64 by a multiply-add a pair.  Raw nibbles as bf16 numbers q 2^-133, x times 2^64
+// and the zero point taken out by sums of x a group save those, but x of 2^63 and more overflows and the sum
+// is off relative to (q + z) |x|; measured: 35.0 and 35.9 us (one token, groups of 128 without zero points),
+// 38.8 and 37.5 with them, 68.0 and 65.8 in groups of 32, 98 and 94 (13 tokens, 60 experts of 1376x2080).
 //
 // Measured, both launches of 8 experts of 2048x4096 a token on one of 256 (bytes: chosen experts'
 // weights): bf16 one token 70 us (5.7 TB/s), 24 tokens 982 us (7.0 TB/s); 8-bit one token 46 us
-// (4.4 TB/s), 16 tokens 410 us (6.3 TB/s); 4-bit one token 35 us (2.9 TB/s), 12 tokens 203 us
-// (5.2 TB/s).  Many tokens are bound by HBM.  One token: 10 of the microseconds are two launches' starts,
+// (4.4 TB/s), 16 tokens 410 us (6.3 TB/s); 4-bit one token 36 us (2.9 TB/s), 12 tokens 208 us
+// (5.1 TB/s).  Many tokens are bound by HBM.  One token: 10 of the microseconds are two launches' starts,
 // routing, the tokens' way into shared memory and the joining of tiles; 4-bit weights are bound by
 // instructions beside that (the nibbles' masks and shifts, scales by shuffles; groups below 128 take
 // twice the scale work).
@@ -66,12 +69,6 @@ __device__ __forceinline__ int xslot(int c, int m) {
 }
 __device__ __forceinline__ int wslot(int c, int r) { return c ^ (((r & 1) << 2) | ((r >> 1) & 3)); }
 
-// x of a 4-bit product: nibbles stay where they are in their half words, as bf16 numbers q 2^-133 (low
-// nibble) and q 2^-129, so activations carry 2^64 and 2^60 and a sum is 2^-69 of the true one
-constexpr uint32_t kLowScale = 0x5F805F80u, kHighScale = 0x5D805D80u;  // bf16x2 of 2^64, 2^60
-constexpr float kDown69 = 1.6940658945086007e-21f;                       // 2^-69
-constexpr float kUp69 = 590295810358705651712.f;                         // 2^69
-
 // ------------------------------------------------------------------ GATE_UP
 // DEPTH: stages of a ring, or 0: as the argument says
 template <int FMT, int DEPTH, bool FINE, bool ZP>
@@ -85,9 +82,8 @@ __global__ void __launch_bounds__(kGuWarps * 32, 1)
   const int P = p.M * p.topk;
   const int nstage = (p.K + KS - 1) / KS, nxb = nstage * SB;  // x is zero past K
 
-  // shared memory: x blocks [nxb][M], 4-bit: sums of x [nxb or 4 nxb][M], lists, rings
+  // shared memory: x blocks [nxb][M], lists, rings
   uint8_t* ring_base = smem + x_bytes + lists;
-  float* s_sum = reinterpret_cast<float*>(smem + (size_t)nxb * p.M * XB);
   Lists l;
   l.entries = reinterpret_cast<Entry*>(smem + x_bytes);
   l.ids = reinterpret_cast<int*>(l.entries + P);
@@ -128,31 +124,14 @@ __global__ void __launch_bounds__(kGuWarps * 32, 1)
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         const int i = next * 64 + q * 32 + lane;
-        const bool on = i < vecs * p.M;  // (whole groups of 16 lanes)
+        const bool on = i < vecs * p.M;
         const int m = on ? i / vecs : 0, v = i - m * vecs, b = v / (XK / 8), c = v % (XK / 8);
         uint4 x = x2[q];
         if constexpr (I8) {
           const float inv = s_inv[m];
           x = make_uint4(quant2(x.x, inv), quant2(x.y, inv), quant2(x.z, inv), quant2(x.w, inv));
         }
-        if constexpr (I4) {
-          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-          float s = 0.f;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) s += __uint_as_float(w[j] << 16) + __uint_as_float(w[j] & 0xFFFF0000u);
-          s += __shfl_xor_sync(0xffffffffu, s, 1);
-          s += __shfl_xor_sync(0xffffffffu, s, 2);
-          if constexpr (FINE) {
-            if (on && (c & 3) == 0) s_sum[(b * 4 + (c >> 2)) * p.M + m] = s * kDown69;
-          } else {
-            s += __shfl_xor_sync(0xffffffffu, s, 4);
-            s += __shfl_xor_sync(0xffffffffu, s, 8);
-            if (on && c == 0) s_sum[b * p.M + m] = s * kDown69;
-          }
-          x = pair_up(x);
-          x = make_uint4(mul_bf16x2(x.x, kLowScale), mul_bf16x2(x.y, kHighScale), mul_bf16x2(x.z, kLowScale),
-                         mul_bf16x2(x.w, kHighScale));
-        }
+        if constexpr (I4) x = pair_up(x);
         if (on) *reinterpret_cast<uint4*>(smem + (size_t)(b * p.M + m) * XB + xslot<FMT, FINE>(c, m) * 16) = x;
       }
     }
@@ -297,13 +276,14 @@ __global__ void __launch_bounds__(kGuWarps * 32, 1)
       const uint32_t wa[2] = {w0_at + slot, w1_at + slot};
       const uint32_t wf = ring + slot + g * 128 + t * 4, wx = wslot(0, g) * 16;  // FINE: word t of piece c at c * 16 ^ wx
       slot = slot + kStage == end ? 0u : slot + kStage;
-      float sc[NS], sz[NS];  // scale, scale times zero point: of this lane's row and block
+      float sc[NS];  // scale and zero point (as bf16x2 of -z / 64) of this lane's row and block
+      uint32_t nz[NS];
       if constexpr (I4) {
 #pragma unroll
         for (int j = 0; j < NS; ++j) {
           sc[j] = p.scale_fp16 ? __half2float(__ushort_as_half(s_next[j])) : bf16_bits_to_f32(s_next[j]);
-          // the zero point as a number: 2^23 + z, less 2^23
-          sz[j] = -sc[j] * (ZP ? __uint_as_float(0x4B000000u | z_next[j]) - 8388608.f : 8.f);
+          // z's pattern stands for z 2^-133, times -2^127
+          if (ZP) nz[j] = fma_bf16x2(z_next[j] * 0x10001u, 0xFF00FF00u, 0u);
         }
         if (s + 1 < nstage) scales(s + 1);
       }
@@ -325,26 +305,29 @@ __global__ void __launch_bounds__(kGuWarps * 32, 1)
               wv[h][3] = v.w;
             }
           }
-          float grp[4];
+          float grp[4], f[2];
+          uint32_t negz[2];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const uint4 bx = lds16(xb + xslot<FMT, FINE>(FINE ? 4 * j + t : 4 * t + j, xg) * 16);
-            const uint32_t w0 = wv[0][j], w1 = wv[1][j], v0 = w0 >> 8, v1 = w1 >> 8;
-            if (j == 0 || FINE)
-              mma_first(grp, w0 & 0x000F000Fu, w1 & 0x000F000Fu, w0 & 0x00F000F0u, w1 & 0x00F000F0u, bx.x, bx.y);
-            else
-              mma_bf16_16816(grp, w0 & 0x000F000Fu, w1 & 0x000F000Fu, w0 & 0x00F000F0u, w1 & 0x00F000F0u, bx.x, bx.y);
-            mma_bf16_16816(grp, v0 & 0x000F000Fu, v1 & 0x000F000Fu, v0 & 0x00F000F0u, v1 & 0x00F000F0u, bx.z, bx.w);
-            if (FINE || j == 3) {
-              const float* sx = s_sum + (FINE ? (s * SB + sb) * 4 + j : s * SB + sb) * p.M;
-              const float x0 = sx[c0], x1 = sx[c1];
+            if (j == 0 || FINE) {
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
-                const float f = __shfl_sync(0xffffffffu, sc[FINE ? j : 0], g * 4 + h * 2 + sb);
-                const float z = ZP ? __shfl_sync(0xffffffffu, sz[FINE ? j : 0], g * 4 + h * 2 + sb) : -8.f * f;
-                acc[2 * h] = fmaf(z, x0, fmaf(f, grp[2 * h], acc[2 * h]));
-                acc[2 * h + 1] = fmaf(z, x1, fmaf(f, grp[2 * h + 1], acc[2 * h + 1]));
+                f[h] = __shfl_sync(0xffffffffu, sc[FINE ? j : 0], g * 4 + h * 2 + sb);
+                negz[h] = ZP ? __shfl_sync(0xffffffffu, nz[FINE ? j : 0], g * 4 + h * 2 + sb) : 0xBE00BE00u;
               }
+            }
+            uint32_t q0[4], q1[4];
+            codes_to_bf16(wv[0][j], negz[0], q0);
+            codes_to_bf16(wv[1][j], negz[1], q1);
+            if (j == 0 || FINE)
+              mma_first(grp, q0[0], q1[0], q0[1], q1[1], bx.x, bx.y);
+            else
+              mma_bf16_16816(grp, q0[0], q1[0], q0[1], q1[1], bx.x, bx.y);
+            mma_bf16_16816(grp, q0[2], q1[2], q0[3], q1[3], bx.z, bx.w);
+            if (FINE || j == 3) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) acc[i] = fmaf(f[i >> 1], grp[i], acc[i]);
             }
           }
         } else {
@@ -391,8 +374,8 @@ __global__ void __launch_bounds__(kGuWarps * 32, 1)
         uv = (float)whole[2 + i] * xs * ws[1];
       }
       if constexpr (I4) {
-        gv *= kUp69;
-        uv *= kUp69;
+        gv *= 64.f;
+        uv *= 64.f;
       }
       const uint16_t hb = f32_to_bf16_rn(gated_act(gv, uv, p.alpha, p.limit));
       const int pair = l.pair[en.first + min(2 * t + i, en.count - 1)];
@@ -896,9 +879,7 @@ cudaError_t launch_dn_warps(const StreamArgs& a, cudaStream_t st) {
 // bytes of GATE_UP's tokens in shared memory
 int64_t gu_x_bytes(int fmt, const StreamArgs& a) {
   const int64_t ks = gu_k(fmt), stages = (a.K + ks - 1) / ks;
-  int64_t b = stages * ks * 2 * a.M;
-  if (fmt == STREAM_INT4) b += stages * 2 * (a.group_shift < 7 ? 4 : 1) * a.M * 4;
-  return (b + 127) & ~int64_t(127);
+  return (stages * ks * 2 * a.M + 127) & ~int64_t(127);
 }
 
 // stages of GATE_UP's rings beside the tokens
@@ -916,7 +897,7 @@ cudaError_t launch_gu_int4(const StreamArgs& a, int x, int depth, cudaStream_t s
 }  // namespace
 
 // 4-bit weights: rings of two or three stages too.  8 of 256 experts of 2048x4096, this kernel and
-// stream_kernel: 12 tokens (3 stages) 207 and 280 us, 18 tokens (2 stages) 297 and 373 us; bf16: 15
+// stream_kernel: 12 tokens (3 stages) 208 and 280 us, 18 tokens (2 stages) 299 and 373 us; bf16: 15
 // tokens (3) 747 and 707 us, 18 tokens (2) 984 and 801 us; 8-bit: 18 tokens (2) 522 and 459 us.
 bool gate_up_few_takes(int fmt, const StreamArgs& a) { return gu_depth(fmt, a) >= (fmt == STREAM_INT4 ? 2 : kGuDepth); }
 

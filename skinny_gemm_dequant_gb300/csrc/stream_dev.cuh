@@ -86,11 +86,6 @@ __device__ __forceinline__ uint32_t quant2(uint32_t w, float f) {
   const float hi = fmaf(__uint_as_float(w & 0xFFFF0000u), f, 12582912.f) - 12582912.f;
   return pack_f16x2(lo, hi);
 }
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
 // the first MMA of a group's sum: no accumulator to clear
 __device__ __forceinline__ void mma_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                           uint32_t b0, uint32_t b1) {

@@ -1,10 +1,11 @@
-"""Edges of the mixture-of-experts layers for a few tokens: what the debug output holds for padding."""
+"""Edges of the mixture-of-experts layers for a few tokens: what the debug output holds for padding, and
+4-bit layers on tokens of any magnitude (tolerances are those of test_gpu_moe_few)."""
 import numpy as np
 import pytest
 import torch
 
 from _util import gpu_lib
-from test_gpu_moe_few import Layer, check, tokens
+from test_gpu_moe_few import Layer, check, rebuild, tokens
 
 pytestmark = pytest.mark.gpu
 
@@ -39,3 +40,41 @@ def test_debug_h_of_padding_is_zero(ql, fmt, M):
     ws.buf[256 + (1 << 20):] = 0xFF  # every 16-bit number a NaN
     none = layer(ql, x, topk_ids=torch.full((M, topk), -1, dtype=torch.int32).cuda(), **how)
     assert not none[3].any() and not none[0].any()
+
+
+@pytest.mark.parametrize("M,H", [(1, 256), (6, 288), (24, 4096)])
+@pytest.mark.parametrize("group,zeros,limit", [(32, True, 1.5), (64, False, None), (128, True, None), (128, False, 1.5)])
+@pytest.mark.parametrize("power", [100, 62, -78])
+def test_int4_tokens_of_any_magnitude(ql, M, H, group, zeros, limit, power):
+    """x far from one and weights as far on the other side: sums of ordinary size.  Beside large tokens half
+    stay ordinary, and their sums, 2^-power of the others', count like any."""
+    layer = Layer("int4", 4, H, 64, seed=M + group, group=group, zeros=True)
+    s13 = layer.args[1]
+    if not zeros:
+        for z in layer.zero_args:
+            z.fill_(8)
+    layer.args[1] = (s13.double() * 2.0 ** -power).to(torch.bfloat16)
+    rebuild(layer)
+    if not zeros:
+        layer.zero_args = [None, None]
+    x = (tokens(M, H, seed=M).double() * 2.0 ** power).to(torch.bfloat16)
+    if power > 0:  # (with weights of 2^78 ordinary tokens' h is infinite by the definition)
+        x[1::2] = tokens(M, H, seed=M + 1)[1::2]
+    logits = torch.randn(M, 4, generator=torch.Generator().manual_seed(M)).to(torch.bfloat16).cuda()
+    got = layer(ql, x, router_logits=logits, topk=2, swiglu_limit=limit, debug=True)
+    assert got[3].view(M, 2, 64)[::2].any(dim=2).all()
+    check(layer, x, got, logits=logits, topk=2, limit=limit or np.inf)
+
+
+@pytest.mark.parametrize("M,H", [(1, 256), (6, 288), (24, 4096)])
+@pytest.mark.parametrize("group", [32, 128])
+def test_int4_codes_at_their_zero_point_are_nothing(ql, M, H, group):
+    """Rows whose codes all equal their zero points give zero exactly, however large x."""
+    layer = Layer("int4", 3, H, 64, seed=M, group=group)
+    layer.args[0][:, 64:] = 0x55  # the up rows
+    layer.zero_args[0][:, 64:] = 5
+    rebuild(layer)
+    x = tokens(M, H, seed=M) * 100
+    logits = torch.randn(M, 3, generator=torch.Generator().manual_seed(M)).to(torch.bfloat16).cuda()
+    y, _, _, h, _ = layer(ql, x, router_logits=logits, topk=2, debug=True)
+    assert not h.any() and not y.any()
