@@ -510,8 +510,10 @@ QL_API ql_status qlinear_int8(const int8_t* x_q, int64_t M, int64_t K, int64_t l
  *   moe_bf16: w13 bf16 [E, 2I, H], w2 bf16 [E, H, I]; fp32 sums.
  *   moe_int8: w13 int8 [E, 2I, H] and s13 fp32 [E, 2I], w2 int8 [E, H, I] and s2 fp32 [E, H] (dense);
  *     x is quantised per token and h per pair by quantize_int8's rule (a row whose largest magnitude is
- *     below 2^-110 counts as zeros); exact int32 sums.  A row with an infinity or a NaN gives NaN
- *     throughout.
+ *     below 2^-110 counts as zeros).  Gate and up are exact int32 sums.  Down is exact over runs of one expert's
+ *     k, at most 1024 of them; a run is scaled and added to the token's sum in fp32, and where runs end
+ *     (multiples of 128 k) depends on the call's sizes and routing.  A row with an infinity or a NaN gives
+ *     NaN throughout.
  *   moe_int4: w13 packed codes [E, 2I, ldw13], w2 [E, H, ldw2] with scales and zero points stored as
  *     qlinear_int4's: s13 [E, 2I, lds13], s2 [E, H, lds2], z13, z2 likewise (each NULL: 8).  No weight
  *     is rounded; x and h stay bf16; a group's sum of (q - z) x is fp32 and meets its scale once.

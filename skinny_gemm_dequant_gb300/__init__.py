@@ -804,7 +804,8 @@ def moe_int8(x, w13, s13, w2, s2, *, router_logits=None, topk_ids=None, topk_wei
              swiglu_alpha=1.0, swiglu_limit=None, debug=False, out=None, workspace=None, stream=None):
     """moe_bf16's layer on 8-bit codes: w13 int8 [E, 2I, H] with s13 fp32 [E, 2I], w2 int8 [E, H, I]
     with s2 fp32 [E, H]; H and I multiples of 16.  x is quantised per token and h per (token, expert)
-    inside, by quantize_int8's rule; the sums are exact."""
+    inside, by quantize_int8's rule.  Sums of gate and up are exact, those of down over runs of at most
+    1024 k of an expert, which are scaled and added in fp32."""
     def mats(E, I, H, dev):
         return (*_experts(w13, "w13", E, 2 * I, H, torch.int8, dev), _dense(s13, "s13", (E, 2 * I), torch.float32, dev),
                 *_experts(w2, "w2", E, H, I, torch.int8, dev), _dense(s2, "s2", (E, H), torch.float32, dev))

@@ -7,7 +7,8 @@
 // 8-bit weights: tokens (GATE_UP) and h (DOWN) are quantised here, scale = max|v| / 127 over the
 // row, code = v / scale rounded half to even; products of codes are exact in fp32, sums of
 // 1024 k too.  4-bit weights: q - z is exact in bf16, a group's fp32 sum is multiplied by its scale once.
-// h is rounded to bf16 once (the products' operand); all sums are fp32 or whole numbers.
+// h is rounded to bf16 once (the products' operand).  GATE_UP's 8-bit sums are whole numbers; all others are
+// fp32, in DOWN of 8-bit weights over runs of at most 1024 k whose own sums are exact.
 //
 // Both kernels are persistent, one CTA per SM, and stream a chosen expert's weights once for 8 of its
 // tokens through rings of the warps' own (cp.async: no warp waits for another), the weights as the warp

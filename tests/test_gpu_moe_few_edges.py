@@ -1,10 +1,13 @@
-"""Edges of the mixture-of-experts layers for a few tokens: what the debug output holds for padding, and
-4-bit layers on tokens of any magnitude (tolerances are those of test_gpu_moe_few)."""
+"""Edges of the mixture-of-experts layers for a few tokens: what the debug output holds for padding,
+4-bit layers on tokens of any magnitude (tolerances are those of test_gpu_moe_few), and what is rounded in the
+8-bit layer's down."""
 import numpy as np
 import pytest
 import torch
 
-from _util import gpu_lib
+from _util import bits_of, gpu_lib
+from oracle import formats as F
+from oracle import moe_few_oracle as MO
 from test_gpu_moe_few import Layer, check, rebuild, tokens
 
 pytestmark = pytest.mark.gpu
@@ -78,3 +81,57 @@ def test_int4_codes_at_their_zero_point_are_nothing(ql, M, H, group):
     logits = torch.randn(M, 3, generator=torch.Generator().manual_seed(M)).to(torch.bfloat16).cuda()
     y, _, _, h, _ = layer(ql, x, router_logits=logits, topk=2, debug=True)
     assert not h.any() and not y.any()
+
+
+def int8_down(layer, h, ids, weights):
+    """(y, how far fp32 may be off) of moe_int8's down on the kernel's own h.
+
+    An expert's whole-number sums over units of 128 k are exact, and so are those of the runs of units that a
+    warp adds (at most 1024 k).  A run's sum meets the channel's scale (one rounding) and the weight times the
+    scale of h (one rounding to make it, one by the multiply-add that adds it).  A token has U = topk *
+    ceil(I / 128) units, so no more than U runs, U parts of warps and U parts of CTAs that are not zero: 3 U
+    additions and 2 roundings of a term, each by 2^-24 of the units' magnitudes."""
+    q, s = MO.codes(h)
+    M, topk = ids.shape
+    w2, s2 = layer.values[1], layer.scales[1]
+    y, a = np.zeros((M, layer.H)), np.zeros((M, layer.H))
+    for p, e in enumerate(ids.reshape(-1)):
+        if 0 <= e < layer.E:
+            f = weights.reshape(-1)[p] * s[p] * s2[e]
+            for k in range(0, layer.I, 128):
+                unit = w2[e][:, k:k + 128] @ q[p, k:k + 128]
+                y[p // topk] += f * unit
+                a[p // topk] += np.abs(f * unit)
+    return y, (3 * topk * -(-layer.I // 128) + 2) * 2.0 ** -24 * a
+
+
+@pytest.mark.parametrize("M,E,topk,H,I", [(1, 8, 2, 256, 128), (1, 6, 6, 1024, 2080), (7, 5, 3, 544, 1056),
+                                          (24, 4, 2, 288, 4096), (64, 3, 3, 96, 608)])
+def test_int8_down_rounds_runs_not_products(ql, M, E, topk, H, I):
+    layer = Layer("int8", E, H, I, seed=I)
+    x = tokens(M, H, seed=I, fmt="int8")
+    g = np.random.default_rng(I)
+    ids = np.stack([g.permutation(E)[:topk] for _ in range(M)]).astype(np.int32)
+    w = g.standard_normal((M, topk)).astype(np.float32)
+    y, _, _, h, _ = layer(ql, x, topk_ids=torch.from_numpy(ids).cuda(), topk_weights=torch.from_numpy(w).cuda(), debug=True)
+    ref, off = int8_down(layer, F.bf16_to_f64(bits_of(h)), ids, w.astype(np.float64))
+    assert (np.abs(F.bf16_to_f64(bits_of(y)) - ref) <= off + F.bf16_ulp(np.abs(ref) + off) / 2).all()
+
+
+@pytest.mark.parametrize("M,H,I", [(1, 512, 2080), (9, 256, 1056), (40, 160, 608)])
+def test_int8_down_of_opposite_weights(ql, M, H, I):
+    """Two experts of equal weights, w and -w: what is left are the roundings of runs, and no bf16 rounding
+    of a larger result hides them."""
+    layer = Layer("int8", 4, H, I, seed=I)
+    for a in (*layer.args, *layer.values, *layer.scales):
+        a[2:] = a[:2]
+    x = tokens(M, H, seed=I, fmt="int8")
+    ids = np.tile(np.array([[0, 2, 3, 1]], np.int32), (M, 1))
+    w = np.random.default_rng(1).random((M, 2)).astype(np.float32)
+    w = np.stack((w[:, 0], -w[:, 0], w[:, 1], -w[:, 1]), axis=1)
+    y, _, _, h, _ = layer(ql, x, topk_ids=torch.from_numpy(ids).cuda(), topk_weights=torch.from_numpy(w).cuda(), debug=True)
+    hv = h.view(M, 4, I)
+    assert torch.equal(hv[:, 0], hv[:, 1]) and torch.equal(hv[:, 2], hv[:, 3])
+    ref, off = int8_down(layer, F.bf16_to_f64(bits_of(h)), ids, w.astype(np.float64))
+    assert (np.abs(ref) <= 2.0 ** -40 * off / 2.0 ** -24).all()
+    assert (np.abs(F.bf16_to_f64(bits_of(y))) <= off * (1 + 2.0 ** -8)).all()
