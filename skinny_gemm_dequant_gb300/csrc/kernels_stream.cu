@@ -52,6 +52,15 @@ __host__ __device__ constexpr int token_bytes(int fmt, int mode) {
 struct Layout {
   int lists, total;  // bytes
 };
+constexpr int kSmem = 227 * 1024 - 1024;
+__host__ __device__ constexpr int list_bytes(int fmt, int pairs) {
+  return (pairs * (int)(sizeof(Entry) + 4 + 2 * 2) + (fmt == STREAM_INT8 ? kMoeMaxTokens * 8 : 0) + 127) & ~127;
+}
+// stages of a warp's ring beside one buffer of sums, with `tokens` of an entry
+constexpr int ring_stages(int fmt, int mode, int pairs, int tokens) {
+  return (kSmem - list_bytes(fmt, pairs) - compute_warps(fmt) * tokens * kPitch * 4 - 128) /
+         (compute_warps(fmt) * (R * row_bytes(fmt) + tokens * token_bytes(fmt, mode)));
+}
 
 template <int ID0, int THREADS>
 __device__ __forceinline__ void bar_sync(int b) {
@@ -92,6 +101,7 @@ __global__ void __launch_bounds__((compute_warps(FMT) + 1) * 32, 1)
   constexpr int TT = NT * 8, KU = unit_k(FMT), WB = row_bytes(FMT), XB = token_bytes(FMT, MODE);
   constexpr bool GU = MODE == STREAM_GATE_UP, LIN = MODE == STREAM_LINEAR;
   constexpr bool I8 = FMT == STREAM_INT8, I4 = FMT == STREAM_INT4;
+  static_assert(GU || I8, "the linear is on 8-bit codes");
   constexpr int kFull = 1, kEmpty = 1 + kBuffers;  // named barriers: a buffer of sums is written, is read
   constexpr int OUT = GU ? R / 2 : R;   // outputs of a tile: half gate rows, half up rows
   using Sum = typename std::conditional<I8, int, float>::type;
@@ -148,7 +158,7 @@ __global__ void __launch_bounds__((compute_warps(FMT) + 1) * 32, 1)
   }
   const int buffer = W * xt * kPitch * 4, buffers = max(1, min(kBuffers, 24 * 1024 / buffer));
   const int rings = (lay.lists + buffers * buffer + 127) & ~127, stage = R * WB + xt * XB;
-  const int depth = min(6, (lay.total - rings) / (W * stage));  // of a warp's ring; 2 at least, as the host made sure
+  const int depth = min(6, (lay.total - rings) / (W * stage));  // of a warp's ring; 2 at least (ring_stages)
 
   // ------------------------------------------------------------------ this CTA's units
   const int nblk = (p.K + KU - 1) / KU;
@@ -242,7 +252,7 @@ __global__ void __launch_bounds__((compute_warps(FMT) + 1) * 32, 1)
           const int e = entry(w.a).expert, n0 = w.tile * OUT + lane;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const int64_t row = GU ? (int64_t)(h ? p.N : 0) + min(n0, p.N - 1) : min(n0 + 32 * h, p.N - 1);
+            const int64_t row = (int64_t)(h ? p.N : 0) + min(n0, p.N - 1);
             sp[h] = reinterpret_cast<const uint16_t*>(p.scale) + e * p.s_estride + row * p.lds;
             if (ZP) zp[h] = p.zero + e * p.z_estride + row * p.ldz;
           }
@@ -668,17 +678,14 @@ __global__ void __launch_bounds__((compute_warps(FMT) + 1) * 32, 1)
 
 template <int FMT, int MODE, int NT, bool FINE, bool ZP>
 cudaError_t launch(const StreamArgs& a, cudaStream_t st) {
-  constexpr int W = compute_warps(FMT), TT = NT * 8;
+  constexpr int W = compute_warps(FMT);
   auto* kfn = stream_kernel<FMT, MODE, NT, FINE, ZP>;
   static OncePerDevice once;
   if (const cudaError_t e = raise_smem_limit(kfn, once); e != cudaSuccess) return e;
   const int P = MODE == STREAM_LINEAR ? 0 : a.M * a.topk;
-  Layout l = {};
-  l.lists = (P * (int)(sizeof(Entry) + 4 + 2 * 2) + (FMT == STREAM_INT8 ? kMoeMaxTokens * 8 : 0) + 127) & ~127;
-  l.total = 227 * 1024 - 1024;
-  // two stages with the most tokens an entry can have (64 tokens, 16 experts each: 2.05)
-  if ((l.total - l.lists - W * TT * kPitch * 4 - 128) / (W * (R * row_bytes(FMT) + TT * token_bytes(FMT, MODE))) < 2)
-    return cudaErrorInvalidConfiguration;
+  const Layout l = {list_bytes(FMT, P), kSmem};
+  static_assert(ring_stages(FMT, MODE, MODE == STREAM_LINEAR ? 0 : kMoeMaxTokens * kMoeMaxTopk, NT * 8) >= 2,
+                "two stages with the most pairs, and the most tokens of an entry");
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(kNumSMs, 1, 1);
   cfg.blockDim = dim3((W + 1) * 32, 1, 1);
