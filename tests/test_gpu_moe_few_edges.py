@@ -1,6 +1,7 @@
 """Edges of the mixture-of-experts layers for a few tokens: what the debug output holds for padding,
-4-bit layers on tokens of any magnitude (tolerances are those of test_gpu_moe_few), and what is rounded in the
-8-bit layer's down."""
+4-bit layers on tokens of any magnitude, what is rounded in the 8-bit layer's down, up to 1024 experts, experts
+of many tokens.  Tolerances are those of test_gpu_moe_few where no others are derived.  One workspace for
+these calls and the library's other ones: test_gpu_workspace_sharing_more.py."""
 import numpy as np
 import pytest
 import torch
@@ -135,3 +136,46 @@ def test_int8_down_of_opposite_weights(ql, M, H, I):
     ref, off = int8_down(layer, F.bf16_to_f64(bits_of(h)), ids, w.astype(np.float64))
     assert (np.abs(ref) <= 2.0 ** -40 * off / 2.0 ** -24).all()
     assert (np.abs(F.bf16_to_f64(bits_of(y))) <= off * (1 + 2.0 ** -8)).all()
+
+
+@pytest.mark.parametrize("E", [257, 512, 513, 1024])
+@pytest.mark.parametrize("M,topk", [(1, 8), (1, 16), (5, 3), (33, 16)])
+@pytest.mark.parametrize("fmt", ["bf16", "int8", "int4"])
+def test_many_experts(ql, fmt, E, M, topk):
+    """Every form of the router, with tied logits; a wrong pairing of ids and weights would show in y."""
+    layer = Layer(fmt, E, 64, 32, seed=E)
+    x = tokens(M, 64, seed=E, fmt=fmt)
+    g = torch.Generator().manual_seed(E + M)
+    logits = (torch.randint(-9, 10, (M, E), generator=g) / 4).to(torch.bfloat16).cuda()
+    logits[0, E - 1] = 3.0
+    check(layer, x, layer(ql, x, router_logits=logits, topk=topk, renormalize=E % 2 == 1, debug=True), logits=logits,
+          topk=topk, renorm=E % 2 == 1)
+
+
+@pytest.mark.parametrize("M", [1, 4, 20])
+@pytest.mark.parametrize("fmt", ["bf16", "int8", "int4"])
+def test_given_ids_of_the_last_experts_that_repeat(ql, fmt, M):
+    E = 1024
+    layer = Layer(fmt, E, 64, 32, seed=3)
+    x = tokens(M, 64, seed=4, fmt=fmt)
+    g = np.random.default_rng(M)
+    ids = g.choice([E - 1, E - 2, E - 17, 0, -1, E], (M, 16), p=[0.4, 0.2, 0.1, 0.1, 0.1, 0.1]).astype(np.int32)
+    ids[0] = E - 1
+    w = g.standard_normal((M, 16)).astype(np.float32)
+    got = layer(ql, x, topk_ids=torch.from_numpy(ids).cuda(), topk_weights=torch.from_numpy(w).cuda(), debug=True)
+    check(layer, x, got, ids=ids, weights=w.astype(np.float64))
+
+
+@pytest.mark.parametrize("M,H,I", [(40, 2080, 96), (64, 1056, 1056), (24, 4096, 160), (17, 96, 2080)])
+@pytest.mark.parametrize("fmt", ["bf16", "int8", "int4"])
+def test_experts_of_many_tokens_on_cut_sums(ql, fmt, M, H, I):
+    """Two of three experts and ids that repeat: an expert has up to 64 tokens two times each, and both launches cut
+    its K over several warps and CTAs."""
+    layer = Layer(fmt, 3, H, I, seed=M, group=64)
+    x = tokens(M, H, seed=M, fmt=fmt)
+    g = np.random.default_rng(M)
+    ids = g.integers(0, 2, (M, 3)).astype(np.int32)
+    ids[::5, 1] = -1
+    w = g.standard_normal((M, 3)).astype(np.float32)
+    got = layer(ql, x, topk_ids=torch.from_numpy(ids).cuda(), topk_weights=torch.from_numpy(w).cuda(), debug=True)
+    check(layer, x, got, ids=ids, weights=w.astype(np.float64))
