@@ -482,8 +482,9 @@ QL_API ql_status quantize_int8(const uint16_t* x, int64_t M, int64_t K, int64_t 
 /*
  * Linear layer on 8-bit codes on both sides, their scales given:
  *   acc[m,n] = sum_k x_q[m,k] * w[n,k]  (exact int32),  y[m,n] = out((acc * x_scale[m]) * w_scale[n])
- * then, if bias, y = out(y + bias[n]).  With quantize_int8's codes and scales and QL_OUT_BF16 it is
- * qlinear_int8_w8a8's y bit for bit.  x_q: int8 [M, ldx]; x_scale: fp32 [M]; w: int8 [N, ldw], both of
+ * then, if bias, y = out(y + bias[n]).  With quantize_int8's codes and scales of finite tokens and
+ * QL_OUT_BF16 it is qlinear_int8_w8a8's y bit for bit (a token with a NaN: NaN throughout here, left out of
+ * the largest magnitude there).  x_q: int8 [M, ldx]; x_scale: fp32 [M]; w: int8 [N, ldw], both of
  * any value, -128 too; w_scale: fp32 [N] or [1] (w_scale_len); bias: nullable bf16 [N]; y: [M, ldy] of
  * out_type QL_OUT_*.
  * Paths: M <= 16, or up to 1024 tokens on weights small enough: one launch that streams the weights once per
