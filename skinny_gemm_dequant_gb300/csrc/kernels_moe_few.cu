@@ -17,7 +17,7 @@
 // GATE_UP: all tokens stay in shared memory as MMA operands (where they do not fit, the launch of
 // kernels_stream.cu takes over: gate_up_few_takes); a warp takes 8 gate rows and the 8 up rows of the same
 // outputs over the whole K, so that nothing is joined and h is made in its registers.  K cut over
-// warps and joined through shared memory took 40 us where this takes 35 in both launches (4-bit, one
+// warps and joined through shared memory took 40 us where this took 35 in both launches (4-bit, one
 // token, 8 experts of 2048x4096), 55 and 46 with 8-bit weights.
 // DOWN: the units (32 rows by 64 or 128 k) of a tile are all its experts' K in a row; they are cut evenly
 // over the warps of all CTAs.  A warp adds an expert's products into registers and, where the expert
@@ -34,9 +34,11 @@
 // weights): bf16 one token 70 us (5.7 TB/s), 24 tokens 982 us (7.0 TB/s); 8-bit one token 46 us
 // (4.4 TB/s), 16 tokens 410 us (6.3 TB/s); 4-bit one token 36 us (2.9 TB/s), 12 tokens 208 us
 // (5.1 TB/s).  Many tokens are bound by HBM.  One token: 10 of the microseconds are two launches' starts,
-// routing, the tokens' way into shared memory and the joining of tiles; 4-bit weights are bound by
-// instructions beside that (the nibbles' masks and shifts, scales by shuffles; groups below 128 take
-// twice the scale work).
+// routing, the tokens' way into shared memory and the joining of tiles.  4-bit weights are bound by latency
+// beside that: four warps a scheduler, each alone in its chain of loads, nibbles, scales by shuffles and
+// products, issue 1.3 to 1.6 instructions a cycle an SM with DRAM at 12 to 39 % and the tensor pipe at 6 to 18 %
+// (groups below 128 take twice the scale work).  An expert's tokens beyond 8 read its weights again, in DOWN nearly
+// always from HBM: the rows that all warps go through between two passes are larger than L2.
 #include <algorithm>
 
 #include "common.cuh"

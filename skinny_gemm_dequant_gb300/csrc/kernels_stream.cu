@@ -20,7 +20,8 @@
 //
 // Bound by HBM where units are many: LINEAR 1x17408x5120 19.2 us (4.6 TB/s; 5 us of start, first
 // loads and last join), 16 tokens 28 us, GATE_UP of 24 tokens, 8 of 256 experts of 2048x4096, with DOWN: bf16 982 us
-// (7.0 TB/s), 8-bit 559 us (6.2 TB/s).  4-bit weights are bound by instructions (475 us, 3.7 TB/s).
+// (7.0 TB/s), 8-bit 559 us (6.2 TB/s).  4-bit weights 475 us (3.7 TB/s): the chain of a unit's loads, nibbles,
+// scales and products, three warps a scheduler.
 // Tiles of 32 rows took 66 us where 64 take 55 (8-bit, one token): half the copies of x.  LINEAR's passes
 // of 16 tokens over a tile follow each other in one CTA, so that only the first reads HBM (linear_streams).
 #include <cuda_fp16.h>
