@@ -69,8 +69,8 @@ __device__ __forceinline__ uint4 pair_up(uint4 x) {
 // v / scale rounded half to even, both IEEE fp32 divisions.  Rounding v f, f = 127 / top, gives the same
 // codes but for ties: with 8-bit mantissas v / top = a / (b 2^s), so v 127 / top is a tie only where b =
 // 254, when all is exact, or v = top / 2, and it is never nearer than 1 / (510 2^s) to a tie otherwise
-// (a = 254, b = 255: 126.50196), far more than what v f is off by, 2^-14 / 2^s.  Which way the quotient of top / 2 falls is asked once, and f moved to
-// the side of 127 / top that falls the same way.
+// (a = 254, b = 255: 126.50196), far more than what v f is off by, 2^-14 / 2^s.  Which way the quotient of
+// top / 2 falls is asked once, and f moved to the side of 127 / top that falls the same way.
 __device__ __forceinline__ float code_factor(float top) {
   if (top < 7.7037197775489436e-34f) return 0.f;  // 2^-110: zeros
   float f = __fdiv_rn(127.f, top);

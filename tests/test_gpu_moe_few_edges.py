@@ -84,6 +84,15 @@ def test_int4_codes_at_their_zero_point_are_nothing(ql, M, H, group):
     assert not h.any() and not y.any()
 
 
+@pytest.mark.parametrize("M,H", [(1, 32768), (2, 32768), (3, 32736), (19, 4096), (20, 4096)])
+@pytest.mark.parametrize("group,zeros", [(32, True), (64, False), (128, True), (256, False)])
+def test_int4_tokens_that_just_fit_in_shared_memory(ql, M, H, group, zeros):
+    layer = Layer("int4", 2, H, 32, seed=M, group=group, zeros=zeros, pad=1)
+    x = tokens(M, H, seed=M, pad=1)
+    logits = torch.randn(M, 2, generator=torch.Generator().manual_seed(M)).to(torch.bfloat16).cuda()
+    check(layer, x, layer(ql, x, router_logits=logits, topk=2, debug=True), logits=logits, topk=2)
+
+
 def int8_down(layer, h, ids, weights):
     """(y, how far fp32 may be off) of moe_int8's down on the kernel's own h.
 
